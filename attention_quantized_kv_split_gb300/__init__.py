@@ -5,6 +5,7 @@ only marshals torch tensors (device memory and streams) into that ABI, under the
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional, Sequence
 
@@ -194,6 +195,128 @@ def qdecode_qgemv(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tenso
     return y
 
 
+def _on(t: torch.Tensor, stream):
+    """The device a paged call runs on (its first tensor's, made current) and its stream's handle."""
+    if not t.is_cuda:
+        raise ValueError("paged calls take CUDA tensors")
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext(), _stream(stream)
+    return torch.cuda.device(t.device), torch.cuda.current_stream(t.device).cuda_stream if stream is None else _stream(stream)
+
+
+def _same(device, dtype, **tensors):
+    """Every tensor given: contiguous, on `device` and (dtype not None) of that dtype."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != device or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+            raise ValueError(f"{name}: expected a contiguous {dtype or 'tensor'} on {device}, got {t.dtype} on "
+                             f"{t.device}, strides {t.stride()}")
+
+
+def _pool(k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits):
+    """num_pages, Hkv and page of a pool's six arrays, their shapes checked."""
+    pages, Hkv, page, W = k_packed.shape
+    if GS < 1 or W * 32 != D * bits or v_packed.shape != k_packed.shape:
+        raise ValueError(f"packed arrays {tuple(k_packed.shape)}, {tuple(v_packed.shape)} do not hold {bits}-bit rows of {D}")
+    for t in (k_scales, k_biases, v_scales, v_biases):
+        if t.shape != (pages, Hkv, page, D // GS) or t.dtype != k_scales.dtype:
+            raise ValueError(f"scales and biases must be [{pages}, {Hkv}, {page}, {D // GS}] of one dtype, got "
+                             f"{tuple(t.shape)} {t.dtype}")
+    _same(k_packed.device, None, k_packed=k_packed, k_scales=k_scales, k_biases=k_biases, v_packed=v_packed,
+          v_scales=v_scales, v_biases=v_biases)
+    if k_packed.element_size() != 4 or v_packed.element_size() != 4:
+        raise ValueError("packed arrays are 32-bit words")
+    return pages, Hkv, page
+
+
+def qdecode_paged_map(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                      page: int, q_start: torch.Tensor, kv_len: torch.Tensor, slots: torch.Tensor,
+                      positions: Optional[torch.Tensor], used: torch.Tensor, stream=None) -> None:
+    """One step's tables on the GPU (all int32): from ``old_len``, ``new_len [B]`` and ``free_pages [n_free]`` writes
+    ``q_start [B + 1]``, ``kv_len [B]``, the new pages' entries of ``block_table [B, max_pages]``, ``slots`` and
+    ``positions [max_tokens]`` (-1 behind the last token) and ``used [1]``, the pages that the step takes."""
+    _same(old_len.device, torch.int32, old_len=old_len, new_len=new_len, block_table=block_table, free_pages=free_pages,
+          q_start=q_start, kv_len=kv_len, slots=slots, positions=positions, used=used)
+    B, max_pages = block_table.shape
+    if not (old_len.numel() == new_len.numel() == kv_len.numel() == B and q_start.numel() == B + 1 and used.numel() >= 1):
+        raise ValueError("old_len, new_len and kv_len hold B values, q_start B + 1")
+    if positions is not None and positions.numel() < slots.numel():
+        raise ValueError("positions holds fewer tokens than slots")
+    device, st = _on(old_len, stream)
+    with device:
+        st = lib().qdecode_paged_map(_ptr(old_len), _ptr(new_len), _ptr(block_table), _ptr(free_pages), _ptr(q_start),
+                                     _ptr(kv_len), _ptr(slots), _ptr(positions), _ptr(used), B, max_pages,
+                                     free_pages.numel(), page, slots.numel(), st)
+    _lib.check(st, "qdecode_paged_map")
+
+
+def qdecode_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_packed: torch.Tensor,
+                         k_scales: torch.Tensor, k_biases: torch.Tensor, v_packed: torch.Tensor, v_scales: torch.Tensor,
+                         v_biases: torch.Tensor, GS: int, bits: int, k_held: Optional[torch.Tensor] = None,
+                         v_held: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantize new rows ``k``, ``v [T, Hkv, D]`` (bf16, fp16 or fp32; last dimension contiguous, other strides free)
+    into the pool at ``slots [T]`` (int32; negative: skipped). ``k_held``, ``v_held [T, Hkv, D]`` in the cache dtype
+    receive the values the cache now stands for."""
+    T, Hkv, D = k.shape
+    pages, heads, page = _pool(k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits)
+    if v.shape != k.shape or v.dtype != k.dtype or heads != Hkv or slots.numel() != T:
+        raise ValueError(f"k {tuple(k.shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype}, {slots.numel()} slots and a pool "
+                         f"of {heads} heads do not belong together")
+    if T and (k.stride(2) != 1 or v.stride(2) != 1):
+        raise ValueError("rows of k and v must be contiguous")
+    if k.device != k_packed.device or v.device != k_packed.device:
+        raise ValueError("k, v and the pool must be on one device")
+    _same(k.device, torch.int32, slots=slots)
+    _same(k.device, k_scales.dtype, k_held=k_held, v_held=v_held)
+    for t in (k_held, v_held):
+        if t is not None and t.shape != k.shape:
+            raise ValueError(f"k_held and v_held must be {tuple(k.shape)}")
+    device, st = _on(k, stream)
+    with device:
+        st = lib().qdecode_paged_append(_ptr(k), _ptr(v), k.stride(0), k.stride(1), v.stride(0), v.stride(1), _ptr(slots),
+                                        _ptr(k_packed), _ptr(k_scales), _ptr(k_biases), _ptr(v_packed), _ptr(v_scales),
+                                        _ptr(v_biases), _ptr(k_held), _ptr(v_held), T, Hkv, pages, page, D, GS, bits,
+                                        dtype_code(k_scales.dtype, k.dtype), st)
+    _lib.check(st, "qdecode_paged_append")
+
+
+def qdecode_paged_attn(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.Tensor, k_biases: torch.Tensor,
+                       v_packed: torch.Tensor, v_scales: torch.Tensor, v_biases: torch.Tensor, out: torch.Tensor,
+                       q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor, max_q: int, GS: int,
+                       bits: int, causal: bool = True, stream=None) -> torch.Tensor:
+    """Attention of every sequence's new tokens over its pages: q ``[total_q, H, D]`` (rows contiguous), out the same
+    shape, contiguous; ``q_start [B + 1]``, ``kv_len [B]``, ``block_table [B, max_pages]`` int32 on the GPU. ``max_q``
+    bounds the new tokens of a sequence (it only chooses the kernel). ``causal=False`` is cross attention."""
+    T, H, D = q.shape
+    pages, Hkv, page = _pool(k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits)
+    B, max_pages = block_table.shape
+    if q.dtype != k_scales.dtype or out.shape != q.shape or kv_len.numel() != B or q_start.numel() != B + 1:
+        raise ValueError(f"q {tuple(q.shape)} {q.dtype}, out {tuple(out.shape)}, {kv_len.numel()} lengths and "
+                         f"{q_start.numel()} starts do not fit a {k_scales.dtype} cache of {B} sequences")
+    if T and q.stride(2) != 1:
+        raise ValueError("rows of q must be contiguous")
+    if q.device != k_packed.device:
+        raise ValueError("q and the pool must be on one device")
+    _same(q.device, q.dtype, out=out)
+    _same(q.device, torch.int32, q_start=q_start, kv_len=kv_len, block_table=block_table)
+    device, st = _on(q, stream)
+    with device:
+        st = lib().qdecode_paged_attn(_ptr(q), q.stride(0), q.stride(1), _ptr(k_packed), _ptr(k_scales), _ptr(k_biases),
+                                      _ptr(v_packed), _ptr(v_scales), _ptr(v_biases), _ptr(out), _ptr(q_start),
+                                      _ptr(kv_len), _ptr(block_table), T, max_q, B, H, Hkv, pages, page, max_pages,
+                                      int(causal), D, GS, bits, dtype_code(q.dtype), st)
+    _lib.check(st, "qdecode_paged_attn")
+    return out
+
+
+def qdecode_paged_attn_workspace_bytes(B: int, H: int, Hkv: int, max_q: int, D: int, GS: int, bits: int) -> int:
+    out = ctypes.c_size_t()
+    st = lib().qdecode_paged_attn_workspace_bytes(B, H, Hkv, max_q, D, GS, bits, ctypes.byref(out))
+    _lib.check(st, "qdecode_paged_attn_workspace_bytes")
+    return out.value
+
+
 def qdecode_attn_device_status() -> int:
     flags = ctypes.c_uint()
     _lib.check(lib().qdecode_attn_device_status(ctypes.byref(flags)), "qdecode_attn_device_status")
@@ -274,3 +397,40 @@ def decode_attention(q: torch.Tensor, cache: QuantizedKV, out_dtype: Optional[to
         out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
     return qdecode_attn(q, cache.kp, cache.ks, cache.kb, cache.vp, cache.vs, cache.vb, out, cache.N, cache.Hkv,
                         cache.GS, cache.bits, stream)
+
+
+class PagedKV:
+    """A pool of pages in the library's layout, and the paged calls on it. Tables, lengths and the free list are the
+    caller's (int32 tensors on the GPU); ``step_tables`` allocates one step's and fills them with qdecode_paged_map."""
+
+    def __init__(self, num_pages, Hkv, page, D, GS, bits, dtype, device="cuda"):
+        self.num_pages, self.Hkv, self.page, self.D, self.GS, self.bits = num_pages, Hkv, page, D, GS, bits
+        mk = lambda last, dt: torch.zeros((num_pages, Hkv, page, last), dtype=dt, device=device)  # noqa: E731
+        W, NG = D * bits // 32, D // GS
+        self.kp, self.ks, self.kb = mk(W, torch.int32), mk(NG, dtype), mk(NG, dtype)
+        self.vp, self.vs, self.vb = mk(W, torch.int32), mk(NG, dtype), mk(NG, dtype)
+
+    @property
+    def dtype(self):
+        return self.ks.dtype
+
+    def arrays(self):
+        return self.kp, self.ks, self.kb, self.vp, self.vs, self.vb
+
+    def step_tables(self, old_len, new_len, block_table, free_pages, max_tokens, stream=None) -> dict:
+        """q_start, kv_len, slots, positions and used of a step (qdecode_paged_map; block_table is extended in place)."""
+        B = block_table.shape[0]
+        mk = lambda n: torch.empty(n, dtype=torch.int32, device=block_table.device)  # noqa: E731
+        t = {"q_start": mk(B + 1), "kv_len": mk(B), "slots": mk(max_tokens), "positions": mk(max_tokens), "used": mk(1)}
+        qdecode_paged_map(old_len, new_len, block_table, free_pages, self.page, **t, stream=stream)
+        return t
+
+    def append(self, k, v, slots, k_held=None, v_held=None, stream=None) -> None:
+        qdecode_paged_append(k, v, slots, *self.arrays(), self.GS, self.bits, k_held, v_held, stream)
+
+    def attend(self, q, q_start, kv_len, block_table, max_q, causal=True, out=None, stream=None) -> torch.Tensor:
+        """Allocating wrapper of qdecode_paged_attn (rows of q behind q_start[B] leave theirs unwritten)."""
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        return qdecode_paged_attn(q, *self.arrays(), out, q_start, kv_len, block_table, max_q, self.GS, self.bits, causal,
+                                  stream)

@@ -21,6 +21,7 @@ QDA_MAX_B = 512
 QDA_MAX_NREP = 64
 QDA_MAX_L = 8
 QDA_QGEMV_MAX_T = 4
+QDA_PAGE_MIN, QDA_PAGE_MAX = 16, 256
 
 
 class QdaPlan(ctypes.Structure):
@@ -61,6 +62,10 @@ SIGNATURES = {
     "qdecode_qgemv": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "qdecode_cache_append": (_I, [_P] * 14 + [_I, _I, _PI32, _I, _I, _I, _I, _I, _P]),
     "qdecode_quantize": (_I, [_P, _LL, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "qdecode_paged_map": (_I, [_P] * 9 + [_I] * 5 + [_P]),
+    "qdecode_paged_append": (_I, [_P, _P, _LL, _LL, _LL, _LL] + [_P] * 9 + [_I] * 8 + [_P]),
+    "qdecode_paged_attn": (_I, [_P, _LL, _LL] + [_P] * 10 + [_I] * 13 + [_P]),
+    "qdecode_paged_attn_workspace_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_SZ)]),
     "qdecode_attn_strerror": (ctypes.c_char_p, [_I]),
     "qdecode_attn_last_cuda_error": (_I, []),
     "qdecode_attn_device_status": (_I, [ctypes.POINTER(ctypes.c_uint)]),

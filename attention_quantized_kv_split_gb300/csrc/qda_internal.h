@@ -208,6 +208,10 @@ cudaError_t qda_occupancy_split2s_b8_x1(int D, int nh, int ng, size_t smem, int*
 // Records a CUDA runtime error for qdecode_attn_last_cuda_error() (this host thread) and returns QDA_ERR_CUDA.
 int qda_cuda_fail(cudaError_t e);
 
+// The current device's SM count and error word; a call's workspace of `need` bytes (installed or the library's own).
+int qda_device(int* num_sms, unsigned int** err);
+int qda_workspace(size_t need, void** ws);
+
 // slices: CTAs per (b, l, h), each combining D / slices values of the head dimension; num_sms: the device's SMs (a
 // merge of few CTAs takes 1024 threads per CTA).
 cudaError_t qda_launch_merge(const QdaParams& p, void* out, int out_dtype, bool pdl, int slices, int num_sms,

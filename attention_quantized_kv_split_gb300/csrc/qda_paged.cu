@@ -1,0 +1,465 @@
+// The paged cache (sm_103a): the step's tables, the append into pages, and the host side of the paged calls.
+#include <algorithm>
+#include <cstring>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qda_paged.h"
+#include "qda_ptx.cuh"
+
+namespace qda {
+
+// ----------------------------------------------------------------------------------------------------- tables
+
+constexpr int kMapThreads = 512;   // one thread per sequence in the scan (QDA_MAX_B)
+static_assert(kMapThreads >= QDA_MAX_B, "one thread per sequence");
+
+// Inclusive scan of a pair over the CTA's threads: shuffles in the warp, the warps' totals through shared memory.
+__device__ __forceinline__ longlong2 block_scan2(longlong2 v, longlong2* tot) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, v.x, o), y = __shfl_up_sync(0xffffffffu, v.y, o);
+    if (lane >= o) {
+      v.x += x;
+      v.y += y;
+    }
+  }
+  if (lane == 31) tot[warp] = v;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) {
+    v.x += tot[w].x;
+    v.y += tot[w].y;
+  }
+  return v;
+}
+
+// Largest b < n with first[b] <= x (first ascending, first[0] <= x).
+__device__ __forceinline__ int seq_of(const int* first, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Every CTA scans the B lengths for itself (at most QDA_MAX_B values, all in L2) and then writes its share of the
+// tokens' slots and of the new pages: one launch, no CTA waits for another. A token on a new page takes its page id from the free
+// list and not from the table, which another CTA may be writing. Bound by the latency of two dependent loads and the scan.
+__global__ void __launch_bounds__(kMapThreads)
+    qda_paged_map_kernel(const int* __restrict__ old_len, const int* __restrict__ new_len, int* __restrict__ table,
+                         const int* __restrict__ free_pages, int* __restrict__ q_start, int* __restrict__ kv_len,
+                         int* __restrict__ slots, int* __restrict__ positions, int* __restrict__ used, int B,
+                         int max_pages, int n_free, int page_shift, int max_tokens, unsigned int* err) {
+  __shared__ longlong2 tot[kMapThreads / 32];
+  __shared__ int s_start[QDA_MAX_B + 1], s_take[QDA_MAX_B + 1], s_old[QDA_MAX_B];
+  const int tid = threadIdx.x;
+  const int pmask = (1 << page_shift) - 1;
+  int o = 0, n = 0;
+  bool bad = false;
+  if (tid < B) {
+    o = old_len[tid];
+    n = new_len[tid];
+    bad = o < 0 || n < 0;
+    o = max(o, 0);
+    n = max(n, 0);
+    if ((long long)o + n > 0x7fffffffLL) {
+      bad = true;
+      n = 0x7fffffff - o;
+    }
+  }
+  const int had = (int)(((long long)o + pmask) >> page_shift), has = (int)(((long long)o + n + pmask) >> page_shift);
+  const longlong2 in = block_scan2(make_longlong2(n, has - had), tot);
+  constexpr long long kTop = 0x7fffffffLL;
+  if (tid < B) {
+    s_start[tid] = (int)min(in.x - n, kTop);
+    s_take[tid] = (int)min(in.y - (has - had), kTop);
+    s_old[tid] = o;
+    if (tid == B - 1) {
+      s_start[B] = (int)min(in.x, kTop);
+      s_take[B] = (int)min(in.y, kTop);
+      bad = bad || in.x > max_tokens;
+    }
+    if (blockIdx.x == 0) {
+      q_start[tid] = (int)min(in.x - n, kTop);
+      kv_len[tid] = o + n;
+      if (tid == B - 1) {
+        q_start[B] = (int)min(in.x, kTop);
+        used[0] = (int)min(in.y, kTop);
+      }
+    }
+  }
+  __syncthreads();
+  const int first = blockIdx.x * kMapThreads + tid, step = gridDim.x * kMapThreads;
+  // the new pages, in the order of sequences and columns
+  const int pages = s_take[B];
+  for (long long i = first; i < pages; i += step) {
+    const int b = seq_of(s_take, B, (int)i);
+    const long long col = (((long long)s_old[b] + pmask) >> page_shift) + (i - s_take[b]);
+    if (col >= max_pages) {
+      bad = true;
+      continue;
+    }
+    const bool have = i < n_free;
+    bad = bad || !have;
+    table[(size_t)b * max_pages + col] = have ? free_pages[i] : -1;
+  }
+  const int total = s_start[B];
+  for (long long t = first; t < max_tokens; t += step) {
+    int slot = -1, pos = -1;
+    if (t < total) {
+      const int b = seq_of(s_start, B, (int)t);
+      const int ob = s_old[b];
+      const long long at = (long long)ob + (t - s_start[b]);
+      const long long col = at >> page_shift, old_cols = ((long long)ob + pmask) >> page_shift;
+      pos = (int)at;
+      int pg = -1;
+      if (col < max_pages) {
+        const long long nth = s_take[b] + (col - old_cols);
+        if (col < old_cols) pg = table[(size_t)b * max_pages + col];
+        else if (nth < n_free) pg = free_pages[nth];
+      }
+      if (pg >= 0) slot = (pg << page_shift) | ((int)at & pmask);
+      else bad = true;
+    }
+    slots[t] = slot;
+    if (positions) positions[t] = pos;
+  }
+  if (bad) atomicOr(err, QDA_ERR_BIT_PAGED);
+}
+
+// ----------------------------------------------------------------------------------------------------- append
+
+template <bool F16>
+__device__ __forceinline__ uint32_t to_bits16(float x) {
+  if constexpr (F16) return __half_as_ushort(__float2half_rn(x));
+  else return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t to_bits16x2(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+struct AppendParams {
+  const void *k, *v;
+  long long kt, kh, vt, vh;      // strides of k and v in elements
+  const int* slots;
+  uint32_t *kp, *vp;
+  uint16_t *ks, *kb, *vs, *vb, *k_held, *v_held;
+  long long rows;                // T * Hkv
+  int Hkv, pool_slots, page_shift, GS;
+  unsigned int* err;
+};
+
+// A row of D values takes D / E lanes of E consecutive values (E = 8, 16 at D = 512): 16 bytes or more per load of the
+// 16-bit types and whole words of codes per lane. A group spans GS / E lanes (minimum and maximum by shuffles). The arithmetic is the quantizer's,
+// in IEEE fp32. K and V of a row go to the same lanes, both loads in flight together. Bound by HBM.
+template <int BITS, int E, int LANES, bool F16, int SRC>
+__global__ void __launch_bounds__(256) qda_paged_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int D = LANES * E, PER = 32 / BITS, W = D / PER, WL = E / PER;
+  constexpr float QMAX = (float)((1 << BITS) - 1);
+  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES;
+  const bool live = row < p.rows;   // a warp may hold several rows: all its lanes stay for the shuffles
+  const int lane = threadIdx.x % LANES;
+  const long long rr = live ? row : p.rows - 1;
+  const long long t = rr / p.Hkv;
+  const int h = (int)(rr - t * p.Hkv);
+  const int slot = p.slots[t];
+  float x[2][E];
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    const long long at = w == 0 ? t * p.kt + h * p.kh : t * p.vt + h * p.vh;
+    const void* src = w == 0 ? p.k : p.v;
+    if constexpr (SRC == QDA_FP32) {
+      const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at + lane * E);
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        const float4 a = __ldcs(s + i);
+        x[w][4 * i] = a.x;
+        x[w][4 * i + 1] = a.y;
+        x[w][4 * i + 2] = a.z;
+        x[w][4 * i + 3] = a.w;
+      }
+    } else {
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + at + lane * E);
+#pragma unroll
+      for (int i = 0; i < E / 8; ++i) {
+        const uint4 a = __ldcs(s + i);
+        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[w][8 * i + 2 * j] = half_bits_to_float<SRC == QDA_FP16>(u[j] & 0xffffu);
+          x[w][8 * i + 2 * j + 1] = half_bits_to_float<SRC == QDA_FP16>(u[j] >> 16);
+        }
+      }
+    }
+  }
+  if (live && slot >= p.pool_slots && lane == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);
+  const bool put = live && slot >= 0 && slot < p.pool_slots;
+  const long long orow = qda_pool_row(slot >> p.page_shift, h, slot & ((1 << p.page_shift) - 1), p.Hkv, p.page_shift);
+  const int lpg = p.GS / E, NG = D / p.GS;
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    float lo = x[w][0], hi = x[w][0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) {
+      lo = fminf(lo, x[w][e]);
+      hi = fmaxf(hi, x[w][e]);
+    }
+    for (int off = 1; off < lpg; off <<= 1) {
+      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    }
+    const uint32_t sb = to_bits16<F16>(__fdiv_rn(__fsub_rn(hi, lo), QMAX)), bb = to_bits16<F16>(lo);
+    const float s = half_bits_to_float<F16>(sb), b = half_bits_to_float<F16>(bb);
+    float c[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float r = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[w][e], b), s)), 0.f), QMAX);
+      c[e] = s == 0.f ? 0.f : r;
+    }
+    if (put) {
+      uint32_t word[WL];
+#pragma unroll
+      for (int i = 0; i < WL; ++i) {
+        word[i] = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) word[i] |= (uint32_t)c[i * PER + j] << (BITS * j);
+      }
+      uint32_t* dst = (w == 0 ? p.kp : p.vp) + orow * W + lane * WL;
+      if constexpr (WL == 1) {
+        dst[0] = word[0];
+      } else if constexpr (WL == 2) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(word[0], word[1]);
+      } else {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(word[0], word[1], word[2], word[3]);
+      }
+      if (lane % lpg == 0) {
+        (w == 0 ? p.ks : p.vs)[orow * NG + lane / lpg] = (uint16_t)sb;
+        (w == 0 ? p.kb : p.vb)[orow * NG + lane / lpg] = (uint16_t)bb;
+      }
+    }
+    if (live && p.k_held != nullptr) {
+      uint4* dst = reinterpret_cast<uint4*>((w == 0 ? p.k_held : p.v_held) + rr * D + lane * E);
+#pragma unroll
+      for (int i = 0; i < E / 8; ++i) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          u[j] = to_bits16x2<F16>(fmaf(s, c[8 * i + 2 * j], b), fmaf(s, c[8 * i + 2 * j + 1], b));
+        __stcs(dst + i, make_uint4(u[0], u[1], u[2], u[3]));
+      }
+    }
+  }
+}
+
+template <int BITS, bool F16, int SRC>
+cudaError_t launch_append(const AppendParams& p, int D, cudaStream_t s) {
+  const int lanes = D == 512 ? 32 : D / 8;
+  const unsigned grid = (unsigned)((p.rows * lanes + 255) / 256);
+  switch (D) {
+    case 64: qda_paged_append_kernel<BITS, 8, 8, F16, SRC><<<grid, 256, 0, s>>>(p); break;
+    case 128: qda_paged_append_kernel<BITS, 8, 16, F16, SRC><<<grid, 256, 0, s>>>(p); break;
+    case 256: qda_paged_append_kernel<BITS, 8, 32, F16, SRC><<<grid, 256, 0, s>>>(p); break;
+    default: qda_paged_append_kernel<BITS, 16, 32, F16, SRC><<<grid, 256, 0, s>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+template <int BITS>
+cudaError_t launch_append_types(const AppendParams& p, int D, bool f16, int src, cudaStream_t s) {
+  if (f16)
+    return src == QDA_BF16   ? launch_append<BITS, true, QDA_BF16>(p, D, s)
+           : src == QDA_FP16 ? launch_append<BITS, true, QDA_FP16>(p, D, s)
+                             : launch_append<BITS, true, QDA_FP32>(p, D, s);
+  return src == QDA_BF16   ? launch_append<BITS, false, QDA_BF16>(p, D, s)
+         : src == QDA_FP16 ? launch_append<BITS, false, QDA_FP16>(p, D, s)
+                           : launch_append<BITS, false, QDA_FP32>(p, D, s);
+}
+
+bool good_page(int page) { return page >= QDA_PAGE_MIN && page <= QDA_PAGE_MAX && (page & (page - 1)) == 0; }
+
+int page_shift_of(int page) {
+  int s = 0;
+  while ((1 << s) < page) ++s;
+  return s;
+}
+
+// bits, GS and D of every paged call: the quantizer's
+int check_codec(int D, int GS, int bits) {
+  if (D < 1 || GS < 1) return QDA_ERR_INVALID;
+  if (bits != 4 && bits != 8) return QDA_ERR_UNSUPPORTED;
+  if (GS != 32 && GS != 64 && GS != 128) return QDA_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128 && D != 256 && D != 512) return QDA_ERR_UNSUPPORTED;
+  if (D % GS != 0) return QDA_ERR_UNSUPPORTED;
+  return QDA_OK;
+}
+
+int check_pool(int num_pages, int page) {
+  if (num_pages < 1 || page < 1) return QDA_ERR_INVALID;
+  if (!good_page(page) || (long long)num_pages * page > 0x7fffffffLL) return QDA_ERR_UNSUPPORTED;
+  return QDA_OK;
+}
+
+bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+}  // namespace qda
+
+extern "C" int qdecode_paged_map(const int32_t* old_len, const int32_t* new_len, int32_t* block_table,
+                                 const int32_t* free_pages, int32_t* q_start, int32_t* kv_len, int32_t* slots,
+                                 int32_t* positions, int32_t* used, int B, int max_pages, int n_free, int page,
+                                 int max_tokens, void* stream) {
+  using namespace qda;
+  if (!old_len || !new_len || !block_table || !q_start || !kv_len || !used) return QDA_ERR_INVALID;
+  if (B < 1 || max_pages < 1 || n_free < 0 || page < 1 || max_tokens < 0) return QDA_ERR_INVALID;
+  if ((n_free > 0 && !free_pages) || (max_tokens > 0 && !slots)) return QDA_ERR_INVALID;
+  if (kv_len == old_len || kv_len == new_len) return QDA_ERR_INVALID;
+  if (!good_page(page) || B > QDA_MAX_B) return QDA_ERR_UNSUPPORTED;
+  const void* ptrs[9] = {old_len, new_len, block_table, free_pages, q_start, kv_len, slots, positions, used};
+  for (const void* p : ptrs)
+    if (off4(p)) return QDA_ERR_ALIGN;
+  int sms;
+  unsigned int* err;
+  const int st = qda_device(&sms, &err);
+  if (st != QDA_OK) return st;
+  const int grid = (int)std::min<long long>(sms, std::max(1LL, ((long long)max_tokens + kMapThreads - 1) / kMapThreads));
+  qda_paged_map_kernel<<<grid, kMapThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+      old_len, new_len, block_table, free_pages, q_start, kv_len, slots, positions, used, B, max_pages, n_free,
+      page_shift_of(page), max_tokens, err);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
+}
+
+extern "C" int qdecode_paged_append(const void* k, const void* v, long long k_tstride, long long k_hstride,
+                                    long long v_tstride, long long v_hstride, const int32_t* slots, uint32_t* k_packed,
+                                    void* k_scales, void* k_biases, uint32_t* v_packed, void* v_scales, void* v_biases,
+                                    void* k_held, void* v_held, int T, int Hkv, int num_pages, int page, int D, int GS,
+                                    int bits, int dtype, void* stream) {
+  using namespace qda;
+  if (!k_packed || !k_scales || !k_biases || !v_packed || !v_scales || !v_biases) return QDA_ERR_INVALID;
+  if (T < 0 || Hkv < 1 || (k_held == nullptr) != (v_held == nullptr)) return QDA_ERR_INVALID;
+  if (T > 0 && (!k || !v || !slots)) return QDA_ERR_INVALID;
+  const int cache = dtype & 0xff, src_byte = (dtype >> 8) & 0xff;
+  if ((dtype >> 16) != 0 || (cache != QDA_BF16 && cache != QDA_FP16)) return QDA_ERR_INVALID;
+  if (src_byte != 0 && src_byte != QDA_BF16 && src_byte != QDA_FP16 && src_byte != QDA_FP32) return QDA_ERR_INVALID;
+  int st = check_codec(D, GS, bits);
+  if (st == QDA_OK) st = check_pool(num_pages, page);
+  if (st != QDA_OK) return st;
+  const int src = src_byte == 0 ? cache : src_byte;
+  const long long unit = src == QDA_FP32 ? 4 : 8;   // elements in 16 bytes
+  const void* ptrs[10] = {k, v, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, k_held, v_held};
+  for (const void* p : ptrs)
+    if (off16(p)) return QDA_ERR_ALIGN;
+  if (off4(slots) || k_tstride % unit || k_hstride % unit || v_tstride % unit || v_hstride % unit) return QDA_ERR_ALIGN;
+  if (T == 0) return QDA_OK;
+  AppendParams p;
+  std::memset(&p, 0, sizeof(p));
+  int sms;
+  st = qda_device(&sms, &p.err);
+  if (st != QDA_OK) return st;
+  p.k = k;
+  p.v = v;
+  p.kt = k_tstride;
+  p.kh = k_hstride;
+  p.vt = v_tstride;
+  p.vh = v_hstride;
+  p.slots = slots;
+  p.kp = k_packed;
+  p.vp = v_packed;
+  p.ks = static_cast<uint16_t*>(k_scales);
+  p.kb = static_cast<uint16_t*>(k_biases);
+  p.vs = static_cast<uint16_t*>(v_scales);
+  p.vb = static_cast<uint16_t*>(v_biases);
+  p.k_held = static_cast<uint16_t*>(k_held);
+  p.v_held = static_cast<uint16_t*>(v_held);
+  p.rows = (long long)T * Hkv;
+  p.Hkv = Hkv;
+  p.pool_slots = num_pages * page;
+  p.page_shift = page_shift_of(page);
+  p.GS = GS;
+  if ((p.rows * (D / 8) + 255) / 256 > 0x7fffffffLL) return QDA_ERR_UNSUPPORTED;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = bits == 4 ? launch_append_types<4>(p, D, cache == QDA_FP16, src, s)
+                                  : launch_append_types<8>(p, D, cache == QDA_FP16, src, s);
+  return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
+}
+
+extern "C" int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max_q, int D, int GS, int bits,
+                                                  size_t* bytes) {
+  using namespace qda;
+  if (bytes == nullptr || B < 1 || H < 1 || Hkv < 1 || max_q < 1 || H % Hkv != 0) return QDA_ERR_INVALID;
+  const int st = check_codec(D, GS, bits);
+  if (st != QDA_OK) return st;
+  if (B > QDA_MAX_B || H / Hkv > QDA_MAX_NREP) return QDA_ERR_UNSUPPORTED;
+  *bytes = 0;
+  return QDA_OK;
+}
+
+extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
+                                  const void* k_scales, const void* k_biases, const uint32_t* v_packed,
+                                  const void* v_scales, const void* v_biases, void* out, const int32_t* q_start,
+                                  const int32_t* kv_len, const int32_t* block_table, int total_q, int max_q, int B,
+                                  int H, int Hkv, int num_pages, int page, int max_pages, int causal, int D, int GS,
+                                  int bits, int dtype, void* stream) {
+  using namespace qda;
+  if (!k_packed || !k_scales || !k_biases || !v_packed || !v_scales || !v_biases || !q_start || !kv_len ||
+      !block_table)
+    return QDA_ERR_INVALID;
+  if (total_q < 0 || max_q < 1 || B < 1 || H < 1 || Hkv < 1 || max_pages < 1 || H % Hkv != 0) return QDA_ERR_INVALID;
+  if (total_q > 0 && (!q || !out)) return QDA_ERR_INVALID;
+  if (dtype != QDA_BF16 && dtype != QDA_FP16) return QDA_ERR_INVALID;
+  int st = check_codec(D, GS, bits);
+  if (st == QDA_OK) st = check_pool(num_pages, page);
+  if (st != QDA_OK) return st;
+  if (B > QDA_MAX_B || H / Hkv > QDA_MAX_NREP) return QDA_ERR_UNSUPPORTED;
+  const void* ptrs[8] = {q, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, out};
+  for (const void* p : ptrs)
+    if (off16(p)) return QDA_ERR_ALIGN;
+  if (off4(q_start) || off4(kv_len) || off4(block_table) || q_tstride % 8 || q_hstride % 8) return QDA_ERR_ALIGN;
+  if (total_q == 0) return QDA_OK;
+  QdaPagedParams p;
+  std::memset(&p, 0, sizeof(p));
+  int sms;
+  st = qda_device(&sms, &p.err);
+  if (st != QDA_OK) return st;
+  p.q = static_cast<const uint16_t*>(q);
+  p.kp = k_packed;
+  p.ks = static_cast<const uint16_t*>(k_scales);
+  p.kb = static_cast<const uint16_t*>(k_biases);
+  p.vp = v_packed;
+  p.vs = static_cast<const uint16_t*>(v_scales);
+  p.vb = static_cast<const uint16_t*>(v_biases);
+  p.out = static_cast<uint16_t*>(out);
+  p.q_start = q_start;
+  p.kv_len = kv_len;
+  p.table = block_table;
+  p.q_tstride = q_tstride;
+  p.q_hstride = q_hstride;
+  p.total_q = total_q;
+  p.B = B;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.nrep = H / Hkv;
+  p.num_pages = num_pages;
+  p.page_shift = page_shift_of(page);
+  p.max_pages = max_pages;
+  p.causal = causal != 0;
+  p.D = D;
+  p.GS = GS;
+  p.NG = D / GS;
+  p.W = D * bits / 32;
+  p.f16 = dtype == QDA_FP16;
+  p.qscale = 1.4426950408889634f / sqrtf((float)D);
+  const cudaError_t e = qda_launch_paged_simple(p, bits, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
+}

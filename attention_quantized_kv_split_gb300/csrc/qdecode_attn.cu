@@ -173,6 +173,29 @@ cudaError_t split_launch(int bits, bool exact, const QdaParams& p, const Variant
                : qda_launch_split2_b8_x0(p, p.D, v.nh, v.NG, grid, v.smem, s);
 }
 
+// A call's scratch: the installed workspace if there is one, else the library's own, grown when it is too small.
+int workspace_for(DeviceState& d, size_t need, void** ws) {
+  std::lock_guard<std::mutex> lock(d.mu);
+  if (d.user_ws != nullptr) {
+    if (d.user_ws_bytes < need) return QDA_ERR_WORKSPACE;
+    *ws = d.user_ws;
+    return QDA_OK;
+  }
+  if (d.ws_bytes < need) {
+    // grow (at least doubling); the smaller buffer is retired, not freed: a CUDA graph captured earlier or a
+    // launch another thread is about to make may still write to it
+    const size_t want = std::max({need, 2 * d.ws_bytes, (size_t)1 << 20});
+    void* grown = nullptr;
+    cudaError_t e = cudaMalloc(&grown, want);
+    if (e != cudaSuccess) return cuda_fail(e);
+    if (d.ws != nullptr) d.retired.push_back(d.ws);
+    d.ws = grown;
+    d.ws_bytes = want;
+  }
+  *ws = d.ws;
+  return QDA_OK;
+}
+
 // The plan: one contiguous, equal share of the flattened rows per CTA, as many CTAs as fit on the GPU at once
 // (one wave), but no fewer than kMinRowsPerCta rows each. Deterministic in (shape, SM count, occupancy).
 void make_plan(int B, int Hkv, const int32_t* N, int D, int num_sms, int ctas_per_sm, const Variant& v,
@@ -354,24 +377,8 @@ int run_call(const void* q, const uint32_t* k_packed, const void* k_scales, cons
     }
     ws = g_static_scratch_addr[dev];
   } else {
-    std::lock_guard<std::mutex> lock(d->mu);
-    if (d->user_ws != nullptr) {
-      if (d->user_ws_bytes < plan.workspace_bytes) return QDA_ERR_WORKSPACE;
-      ws = d->user_ws;
-    } else {
-      if (d->ws_bytes < plan.workspace_bytes) {
-        // grow (at least doubling); the smaller buffer is retired, not freed: a CUDA graph captured earlier or a
-        // launch another thread is about to make may still write to it
-        const size_t want = std::max({plan.workspace_bytes, 2 * d->ws_bytes, (size_t)1 << 20});
-        void* grown = nullptr;
-        cudaError_t e = cudaMalloc(&grown, want);
-        if (e != cudaSuccess) return cuda_fail(e);
-        if (d->ws != nullptr) d->retired.push_back(d->ws);
-        d->ws = grown;
-        d->ws_bytes = want;
-      }
-      ws = d->ws;
-    }
+    st = workspace_for(*d, plan.workspace_bytes, &ws);
+    if (st != QDA_OK) return st;
   }
 
   QdaParams p;
@@ -461,6 +468,22 @@ int run_call(const void* q, const uint32_t* k_packed, const void* k_scales, cons
 }  // namespace
 
 int qda_cuda_fail(cudaError_t e) { return cuda_fail(e); }
+
+int qda_device(int* num_sms, unsigned int** err) {
+  int dev;
+  DeviceState* d = device_state(&dev);
+  if (d == nullptr) return QDA_ERR_CUDA;
+  *num_sms = d->num_sms;
+  *err = d->err;
+  return QDA_OK;
+}
+
+int qda_workspace(size_t need, void** ws) {
+  int dev;
+  DeviceState* d = device_state(&dev);
+  if (d == nullptr) return QDA_ERR_CUDA;
+  return workspace_for(*d, need, ws);
+}
 
 extern "C" {
 

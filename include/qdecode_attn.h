@@ -259,6 +259,74 @@ int qdecode_cache_append(const uint32_t* k_packed, const void* k_scales, const v
                          uint32_t* v_packed_out, void* v_scales_out, void* v_biases_out, int B, int Hkv,
                          const int32_t* N, int T, int D, int GS, int bits, int dtype, void* stream);
 
+/*
+ * The paged cache. Pages of `page` tokens in a pool; a sequence's token n lives in row n % page of the page that its row
+ * of the block table names at column n / page. Each page is laid out like one sequence of the cache above, so the
+ * pool's arrays are
+ *     k_packed, v_packed  [num_pages, Hkv, page, D * bits / 32]  uint32
+ *     k_scales, k_biases, v_scales, v_biases  [num_pages, Hkv, page, D / GS]  input dtype
+ * and a slot is page_id * page + row. (The pages this library follows hold one contiguous cache per step, maya-mac
+ * mlx_kernels.py, _ATTEND; they have no counterpart of this section.) Lengths, tables and slots are int32 DEVICE
+ * arrays, read by the kernels only: a step can be captured once in a CUDA graph and replayed as they change.
+ * page is a power of two from 16 to 256; num_pages * page < 2^31. What the host cannot check is checked on the device:
+ * an entry of the table or of slots outside the pool is skipped and sets bit 8 of qdecode_attn_device_status().
+ */
+#define QDA_PAGE_MIN 16
+#define QDA_PAGE_MAX 256
+
+/*
+ * qdecode_paged_map: the tables of one step, built on the GPU from the request lengths. Sequence b (b < B <= QDA_MAX_B)
+ * holds old_len[b] tokens and receives new_len[b] more (each >= 0). With need(n) = ceil(n / page) it writes
+ *     q_start[B + 1]   exclusive sums of new_len: sequence b's new tokens are rows q_start[b] .. q_start[b + 1] - 1
+ *     kv_len[B]        old_len + new_len
+ *     block_table      [B, max_pages]: columns need(old_len[b]) .. need(kv_len[b]) - 1 of row b take the next pages of
+ *                      free_pages[n_free], sequences in order; every other entry stays as it is
+ *     used[1]          pages needed in all; above n_free, the pool is exhausted
+ *     slots, positions [max_tokens]: slot and position in its sequence of every new token; -1 behind the last one
+ * A token or a table entry that has no page (free list exhausted, row too short) gets -1 and sets bit 8 of the device
+ * status; so does a negative length (taken as 0) and a step of more than max_tokens tokens. kv_len must not be old_len
+ * or new_len. positions may be NULL; slots may be NULL if max_tokens is 0. Asynchronous on stream, no workspace.
+ */
+int qdecode_paged_map(const int32_t* old_len, const int32_t* new_len, int32_t* block_table, const int32_t* free_pages,
+                      int32_t* q_start, int32_t* kv_len, int32_t* slots, int32_t* positions, int32_t* used, int B,
+                      int max_pages, int n_free, int page, int max_tokens, void* stream);
+
+/*
+ * qdecode_paged_append: quantize T new tokens' rows k, v [T, Hkv, D] into the pool, token t at slots[t] (its scale, bias
+ * and codes exactly as qdecode_quantize gives them). A negative slot is skipped. slots must be distinct. The rows are
+ * read with strides (in elements: k_tstride from token to token, k_hstride from head to head; rows themselves are
+ * contiguous), so views of a fused projection need no copy. k_held, v_held (contiguous [T, Hkv, D] in the cache dtype, or
+ * both NULL) receive scale * code + bias, the values that the cache holds from then on. dtype: the cache dtype in the low byte, the
+ * dtype of k and v (bf16, fp16 or fp32; 0 = the cache dtype) in the next. T = 0 does nothing. Data pointers 16-byte
+ * aligned, strides multiples of 16 bytes. Asynchronous on stream, no workspace.
+ */
+int qdecode_paged_append(const void* k, const void* v, long long k_tstride, long long k_hstride, long long v_tstride,
+                         long long v_hstride, const int32_t* slots, uint32_t* k_packed, void* k_scales, void* k_biases,
+                         uint32_t* v_packed, void* v_scales, void* v_biases, void* k_held, void* v_held, int T, int Hkv,
+                         int num_pages, int page, int D, int GS, int bits, int dtype, void* stream);
+
+/*
+ * qdecode_paged_attn: attention of each sequence's new tokens over its pages: one token per sequence, chunks of prompts,
+ * or any mix in one call. Row t = q_start[b] + i of q [total_q, H, D] is new token i < L_b = q_start[b + 1] - q_start[b]
+ * of sequence b and sees keys n < kv_len[b], with causal != 0 only n <= kv_len[b] - L_b + i (the new tokens are the
+ * sequence's last, already appended):
+ *     out[t, h, :] = sum_n softmax_n( q[t, h, :] . k_hat[n] / sqrt(D) ) v_hat[n]
+ * causal = 0 is cross attention to states of another length (an encoder's, appended once). A token that sees no key
+ * gives zeros. Rows of out at and behind q_start[B] stay as they are. max_q (>= 1) is the host's bound on the L_b and
+ * only chooses the kernel: results are right for any value. q has strides q_tstride, q_hstride in elements; out is
+ * contiguous [total_q, H, D] in q's dtype. dtype is the input dtype alone (q, scales, biases and out). Supported: the bits, GS and D of qdecode_attn,
+ * H / Hkv <= QDA_MAX_NREP, B <= QDA_MAX_B. Uses the workspace as qdecode_attn does, of
+ * qdecode_paged_attn_workspace_bytes() bytes.
+ */
+int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
+                       const void* k_scales, const void* k_biases, const uint32_t* v_packed, const void* v_scales,
+                       const void* v_biases, void* out, const int32_t* q_start, const int32_t* kv_len,
+                       const int32_t* block_table, int total_q, int max_q, int B, int H, int Hkv, int num_pages,
+                       int page, int max_pages, int causal, int D, int GS, int bits, int dtype, void* stream);
+
+/* Workspace in bytes that qdecode_paged_attn needs for these arguments on the current device, whatever the lengths. */
+int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max_q, int D, int GS, int bits, size_t* bytes);
+
 /* Human-readable text for a status code (static storage). */
 const char* qdecode_attn_strerror(int status);
 
@@ -269,7 +337,8 @@ int qdecode_attn_last_cuda_error(void);
  * Device-side status: copies (synchronously) and clears the current device's error word. Bits: 1 = a pipeline
  * wait in the split kernel gave up after its time limit (the output of that call is invalid); 2 = waiting for the
  * CTA's own copies to land before it exits gave up; 4 = an index check failed (only a library built with
- * QDA_BOUNDS_CHECK checks, and it skips the access). 0 = clean.
+ * QDA_BOUNDS_CHECK checks, and it skips the access); 8 = a paged call met a page, slot or length outside its pool or
+ * table. 0 = clean.
  */
 int qdecode_attn_device_status(unsigned int* flags);
 
