@@ -1,11 +1,12 @@
 // The paged cache (sm_103a): the step's tables, the append into pages, and the host side of the paged calls.
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "qda_paged.h"
+#include "qda_paged_sched.cuh"
 #include "qda_ptx.cuh"
 
 namespace qda {
@@ -286,6 +287,129 @@ cudaError_t launch_append_types(const AppendParams& p, int D, bool f16, int src,
                            : launch_append<BITS, false, QDA_FP32>(p, D, s);
 }
 
+// ------------------------------------------------------------------------------------------- merge of split tiles
+
+// out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M) over the CTAs c that share a tile, in CTA order. CTA (x, y) looks at the tile that starts in
+// piece x and goes on behind it, and takes 8 / WPR of its rows, WPR warps to a row: each folds every WPR-th part, then
+// the warps' sums meet in shared memory. Launched with programmatic dependent launch: the scan of the lengths overlaps
+// the kernel before it, whose parts it then waits for.
+template <int D, int WPR>
+__global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_constant__ QdaPagedParams p, int MT, int KB) {
+  constexpr int E = D / 64;   // pairs of values per lane
+  __shared__ PagedLine line;
+  __shared__ PagedTile s_t;
+  __shared__ float2 s_o[8][D / 2];
+  __shared__ float2 s_ml[8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
+  paged_line(p, MT, line);
+  const long long total = line.at[p.B];
+  const int ctas = total == 0 ? 0 : paged_ctas(total, p.ctas, p.min_keys);
+  bool work = c + 1 < ctas;
+  if (work) {
+    if (tid == 0) s_t = paged_tile_at(p, line, MT, paged_border(total, ctas, c + 1));
+    __syncthreads();
+  }
+  const PagedTile& t = s_t;
+  int nblk = 0, last = c;   // the last CTA that shares the tile
+  if (work) {
+    nblk = (paged_tile_keys(p, t, MT) + KB - 1) / KB;
+    work = t.lo >= paged_border(total, ctas, c) && t.lo < paged_border(total, ctas, c + 1) && nblk > 0;
+  }
+  if (work) {   // a CTA that had every block wrote the tile itself
+    bool whole = false;
+    for (int k = c + tid; k < ctas; k += 256) {
+      const long long a = paged_border(total, ctas, k), b = paged_border(total, ctas, k + 1);
+      if (a >= t.hi) break;
+      whole = whole || (paged_block_at(t, nblk, a) == 0 && paged_block_at(t, nblk, b) == nblk);
+    }
+    work = !__syncthreads_or(whole);
+    // the CTA that holds the tile's end
+    int lo = c, hi = ctas;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (paged_border(total, ctas, mid) < t.hi) lo = mid; else hi = mid;
+    }
+    last = lo;
+  }
+  pdl_wait();
+  if (!work) return;
+  const int r = blockIdx.y * (8 / WPR) + warp / WPR, part = warp % WPR;
+  const bool live = t.i * MT + r < t.s.rows;
+  float m = -INFINITY, l = 0.f;
+  float2 o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = make_float2(0.f, 0.f);
+  if (live) {
+#pragma unroll 2
+    for (int k = c + part; k <= last; k += WPR) {
+      const int j0 = paged_block_at(t, nblk, paged_border(total, ctas, k));
+      const int j1 = paged_block_at(t, nblk, paged_border(total, ctas, k + 1));
+      if (j0 >= j1) continue;   // wrote nothing
+      const size_t at = (size_t)(2 * k + (k == c)) * MT + r;
+      const float2 ml = p.part_ml[at];
+      const float2* po = reinterpret_cast<const float2*>(p.part_o + at * D);
+      float2 v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = po[e * 32 + lane];
+      const float mn = fmaxf(m, ml.x);
+      const float a = m == -INFINITY ? 0.f : exp2f(m - mn), w = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
+      m = mn;
+      l = fmaf(l, a, ml.y * w);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        o[e].x = fmaf(o[e].x, a, v[e].x * w);
+        o[e].y = fmaf(o[e].y, a, v[e].y * w);
+      }
+    }
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][e * 32 + lane] = o[e];
+    if (lane == 0) s_ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (part != 0 || !live) return;
+    for (int w = 1; w < WPR; ++w) {
+      const float2 ml = s_ml[warp + w];
+      if (ml.x == -INFINITY) continue;
+      const float mn = fmaxf(m, ml.x);
+      const float a = m == -INFINITY ? 0.f : exp2f(m - mn), x = exp2f(ml.x - mn);
+      m = mn;
+      l = fmaf(l, a, ml.y * x);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float2 v = s_o[warp + w][e * 32 + lane];
+        o[e].x = fmaf(o[e].x, a, v.x * x);
+        o[e].y = fmaf(o[e].y, a, v.y * x);
+      }
+    }
+  }
+  if (!live) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int row = t.i * MT + r, tok = row / p.nrep;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(
+      p.out + ((long long)(t.s.first + tok) * p.H + t.kvh * p.nrep + (row - tok * p.nrep)) * D);
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    dst[e * 32 + lane] = p.f16 ? to_bits16x2<true>(o[e].x * inv, o[e].y * inv) : to_bits16x2<false>(o[e].x * inv, o[e].y * inv);
+}
+
+template <int D>
+cudaError_t launch_merge(const QdaPagedParams& p, int rows, int kb, cudaStream_t s) {
+  // few rows per tile: a tile may be shared by many CTAs, so eight warps fold one row; many rows: a warp each
+  const bool few = rows <= 16;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)(few ? rows : rows / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return few ? cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 8>, p, rows, kb)
+             : cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 1>, p, rows, kb);
+}
+
 bool good_page(int page) { return page >= QDA_PAGE_MIN && page <= QDA_PAGE_MAX && (page & (page - 1)) == 0; }
 
 int page_shift_of(int page) {
@@ -310,10 +434,55 @@ int check_pool(int num_pages, int page) {
   return QDA_OK;
 }
 
+// The kernel a call takes, from what the host knows: the shape and the bound on a sequence's new tokens.
+struct PagedPlan {
+  int rows, kb, ctas, min_keys;
+  size_t o_bytes, bytes;   // workspace: partial outputs, and with the (reference, sum) pairs
+};
+
+using SplitFn = cudaError_t (*)(const QdaPagedParams*, int, int, int, int*, cudaStream_t);
+SplitFn split_fn(int bits, bool f16) {
+  return bits == 4 ? (f16 ? qda_paged_split_b4_f1 : qda_paged_split_b4_f0)
+                   : (f16 ? qda_paged_split_b8_f1 : qda_paged_split_b8_f0);
+}
+
+int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int sms, PagedPlan* plan) {
+  plan->rows = max_q * nrep > 8 && D <= 256 ? 16 : 8;
+  plan->kb = D * bits / 8 <= 64 ? 32 : 16;
+  plan->min_keys = 256;
+  int dev = 0;
+  const cudaError_t de = cudaGetDevice(&dev);
+  if (de != cudaSuccess || dev < 0 || dev >= 64) return qda_cuda_fail(de == cudaSuccess ? cudaErrorInvalidDevice : de);
+  static std::atomic<int> cache[64][2][2][4][3][2] = {};   // resident CTAs per SM of an instance, 0 = not asked yet
+  const int di = D == 64 ? 0 : D == 128 ? 1 : D == 256 ? 2 : 3, gi = GS == 32 ? 0 : GS == 64 ? 1 : 2;
+  std::atomic<int>& slot = cache[dev][bits == 8][f16][di][gi][plan->rows == 16];
+  int occ = slot.load();
+  if (occ == 0) {
+    const cudaError_t e = split_fn(bits, f16)(nullptr, D, GS, plan->rows, &occ, nullptr);
+    if (e != cudaSuccess) return qda_cuda_fail(e);
+    occ = std::max(occ, 1);
+    slot.store(occ);
+  }
+  plan->ctas = sms * occ;
+  const size_t rows = (size_t)2 * plan->ctas * plan->rows;
+  plan->o_bytes = (rows * D * 4 + 255) & ~(size_t)255;
+  plan->bytes = plan->o_bytes + rows * sizeof(float2);
+  return QDA_OK;
+}
+
 bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 }  // namespace qda
+
+cudaError_t qda_launch_paged_merge(const QdaPagedParams& p, int rows, int kb, cudaStream_t s) {
+  switch (p.D) {
+    case 64: return qda::launch_merge<64>(p, rows, kb, s);
+    case 128: return qda::launch_merge<128>(p, rows, kb, s);
+    case 256: return qda::launch_merge<256>(p, rows, kb, s);
+    default: return qda::launch_merge<512>(p, rows, kb, s);
+  }
+}
 
 extern "C" int qdecode_paged_map(const int32_t* old_len, const int32_t* new_len, int32_t* block_table,
                                  const int32_t* free_pages, int32_t* q_start, int32_t* kv_len, int32_t* slots,
@@ -401,7 +570,21 @@ extern "C" int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max
   const int st = check_codec(D, GS, bits);
   if (st != QDA_OK) return st;
   if (B > QDA_MAX_B || H / Hkv > QDA_MAX_NREP) return QDA_ERR_UNSUPPORTED;
-  *bytes = 0;
+  int sms;
+  unsigned int* err;
+  int got = qda_device(&sms, &err);
+  if (got != QDA_OK) return got;
+  // a call may state a smaller max_q than this one, and either dtype
+  size_t most = 0;
+  for (int f16 = 0; f16 < 2; ++f16) {
+    for (long long m : {1LL, (long long)max_q}) {
+      PagedPlan plan;
+      got = paged_plan(H / Hkv, m, D, GS, bits, f16 != 0, sms, &plan);
+      if (got != QDA_OK) return got;
+      most = std::max(most, plan.bytes);
+    }
+  }
+  *bytes = most;
   return QDA_OK;
 }
 
@@ -460,6 +643,18 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   p.W = D * bits / 32;
   p.f16 = dtype == QDA_FP16;
   p.qscale = 1.4426950408889634f / sqrtf((float)D);
-  const cudaError_t e = qda_launch_paged_simple(p, bits, static_cast<cudaStream_t>(stream));
+  PagedPlan plan;
+  st = paged_plan(p.nrep, max_q, D, GS, bits, p.f16 != 0, sms, &plan);
+  if (st != QDA_OK) return st;
+  void* ws = nullptr;
+  st = qda_workspace(plan.bytes, &ws);
+  if (st != QDA_OK) return st;
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + plan.o_bytes);
+  p.ctas = plan.ctas;
+  p.min_keys = plan.min_keys;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = split_fn(bits, p.f16 != 0)(&p, D, GS, plan.rows, nullptr, s);
+  if (e == cudaSuccess) e = qda_launch_paged_merge(p, plan.rows, plan.kb, s);
   return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
 }

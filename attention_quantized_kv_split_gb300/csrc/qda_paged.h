@@ -22,6 +22,10 @@ struct QdaPagedParams {
   long long q_tstride, q_hstride;
   int total_q, B, H, Hkv, nrep, num_pages, page_shift, max_pages, causal, D, GS, NG, W, f16;
   float qscale;               // log2(e) / sqrt(D)
+  // how the call is shared among CTAs (qda_paged_sched.cuh)
+  int ctas, min_keys;         // CTAs launched; fewest keys of a CTA's piece
+  float* part_o;              // [2 * ctas, MT, D] unnormalised partial outputs of split tiles
+  float2* part_ml;            // [2 * ctas, MT] (reference in log2 units, sum of weights)
 };
 
 // Row of the pool arrays that holds row `r` of page `pg` of KV head `kvh`.
@@ -29,4 +33,12 @@ __host__ __device__ inline long long qda_pool_row(int pg, int kvh, int r, int Hk
   return ((((long long)pg * Hkv) + kvh) << page_shift) + r;
 }
 
-cudaError_t qda_launch_paged_simple(const QdaPagedParams& p, int bits, cudaStream_t s);
+// The split kernel (qda_paged_split.cuh), translation units per (bits, fp16): its instance for (D, GS, rows per tile).
+// With ctas_per_sm the instance's resident CTAs per SM are stored there and nothing is launched; else p.ctas CTAs are.
+cudaError_t qda_paged_split_b4_f0(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_split_b4_f1(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_split_b8_f0(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_split_b8_f1(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+
+// Merge of the split tiles' partial results, behind a kernel of `rows` rows per tile and key blocks of kb keys.
+cudaError_t qda_launch_paged_merge(const QdaPagedParams& p, int rows, int kb, cudaStream_t s);

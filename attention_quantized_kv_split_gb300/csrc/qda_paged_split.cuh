@@ -1,0 +1,743 @@
+// Paged attention for few query rows per KV head (sm_103a): single tokens, a few tokens per sequence, and every shape the
+// chunk kernel does not take. Bound by HBM (the cache is read once per tile of 8 or 16 rows) and next to it by issue slots.
+//
+// Matrix instructions work on the codes themselves. A warp takes 16 keys at a time; the codes, straight from shared memory, become the 16-bit
+// A operand of m16n8k16 products with fp32 sums (a few query rows are far too thin for the 128-row tiles of tcgen05, and its operands would have to be written back
+// to shared or tensor memory first; here they never leave the registers):
+//   scores   rows = keys, k = head dimension, columns = query rows. A code c is the fp16 value 1024 + c (one AND/OR for two), or
+//            1024 + 16 c where a nibble is left unshifted, with q / 16 on the other side. q goes in as fp16 after an
+//            exact scaling of each row by a power of two (bf16 has fewer significant bits and a wider range). The sums start at -1024 sum(q), so the product
+//            is sum(c q), and per group s_g sum(c q) + b_g sum(q) is formed in fp32. Codes and q are exact: so are the scores, to fp32.
+//   values   rows = head dimension, k = keys, columns = query rows: the weight w = p s_g of each group is the B operand,
+//            rounded to bf16 (for fp16 caches as a pair hi + lo of bf16: 16 significant bits; a bf16 result takes one). Codes are bf16 128 + c; an
+//            8-bit code is 128 + low nibble plus 2048 + 16 * high nibble, in two products. sum(w) of a group, for the offset and to centre the codes on the middle of
+//            their range (so that the rounding of w meets values no larger than half a group's range), comes from one more product
+//            with A = 1, or with many groups the offset is taken off the codes; the rest, sum(p (b_g + mid s_g)), stays in fp32.
+// Keys and query rows change places between the two products: one movmatrix per 8 x 8 weights.
+//
+// Memory: each warp fills its own ring of shared-memory stages with 16-byte asynchronous copies (no warp waits for another), the 16-byte
+// pieces of a row XORed over the banks so that both operand reads are free of conflicts. The online softmax keeps a
+// reference per query row that moves only when a score passes it by more than 8 (log2 units): one vote per 16 keys.
+// Hidden keys (behind the sequence, in a token's future, on a page outside the pool) get the weight 0 by selection, so that what
+// their rows hold, NaN included, reaches nothing.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "qda_paged_sched.cuh"
+
+namespace qda {
+
+constexpr int kPsWarps = 4;
+
+template <int BITS, int D, int GS, int NT>
+struct PsGeom {
+  static constexpr int MT = 8 * NT;
+  static constexpr int NG = D / GS;
+  static constexpr int RB = D * BITS / 8;                 // bytes of codes per row
+  static constexpr int KPS = RB <= 64 ? 32 : 16;          // keys per stage: at least 2 KB of codes of each kind
+  static constexpr int CODE = KPS * RB;                   // bytes of K (or V) codes per stage
+  static constexpr int SC = KPS * NG * 2;                 // bytes of one scale or bias array per stage
+  static constexpr int STAGE = 2 * CODE + 4 * SC;
+  static constexpr int STAGES = 3;
+  static constexpr bool QSMEM = D * NT > 256;             // q operands in shared memory (else in registers)
+  static constexpr bool SSMEM = NG * NT > 4;              // sums of q in shared memory
+  static constexpr bool ONES = NG <= 4;                   // sum(w) by a product with A = 1 (else offset-free codes)
+  static constexpr int QF = QSMEM ? (D / 16) * NT * 256 : 0;
+  static constexpr int QS = SSMEM ? NG * MT * 8 : 0;
+  static constexpr int ROWS = QF + QS;
+  static constexpr int RING = kPsWarps * STAGES * STAGE;
+  static constexpr int COMB = kPsWarps * 8 * D * 4;   // the warps' results of 8 query rows
+  static constexpr int SMEM = ROWS + (RING > COMB ? RING : COMB);
+  static constexpr int OREGS = D / 4 * NT;
+  static constexpr int MINB = OREGS <= 32 ? 4 : OREGS <= 64 ? 3 : 2;
+};
+
+__device__ __forceinline__ void ps_cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void ps_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void ps_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <bool F16>
+__device__ __forceinline__ void ps_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1, float c0, float c1, float c2, float c3) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
+        "%12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
+        "%12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+__device__ __forceinline__ uint32_t ps_trans(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ float ps_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t ps_bf2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// (a & mask) | magic in one operation
+__device__ __forceinline__ uint32_t ps_or(uint32_t a, uint32_t mask, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(magic));
+  return d;
+}
+
+// Byte offset of byte `at` of key row `row` within a stage's codes: 16-byte pieces XORed so that the operand reads (8 rows
+// at one column, and 4 rows two apart at neighbouring columns) fall on distinct banks.
+template <int RB>
+__device__ __forceinline__ uint32_t ps_code_at(int row, int at) {
+  const uint32_t lin = row * RB + at;
+  if constexpr (RB < 128) {
+    return lin ^ (((lin >> 7) & 3u) << 5);
+  } else {
+    return lin ^ ((((uint32_t)row & 3u) ^ (((uint32_t)row >> 2) & 1u)) << 5);
+  }
+}
+
+// N 16-bit values of a row's scales (or biases) from shared memory
+template <int N>
+__device__ __forceinline__ void ps_halves(uint32_t addr, uint32_t (&w)[(N + 1) / 2]) {
+  if constexpr (N == 1) {
+    unsigned short h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr));
+    w[0] = h;
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  } else if constexpr (N == 4) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(addr + 16 * i));
+  }
+}
+template <bool F16>
+__device__ __forceinline__ float ps_half(const uint32_t* w, int g) {
+  const uint32_t x = w[g >> 1];
+  if constexpr (F16) {
+    return __half2float(__ushort_as_half((unsigned short)((g & 1) ? x >> 16 : x & 0xffffu)));
+  } else {
+    return __uint_as_float((g & 1) ? x & 0xffff0000u : x << 16);
+  }
+}
+
+// NW words of codes (NW = 0: half a word) from shared memory
+template <int NW>
+__device__ __forceinline__ void ps_words(uint32_t addr, uint32_t* w) {
+  if constexpr (NW == 0) {
+    unsigned short h;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(addr));
+    w[0] = h;
+  } else if constexpr (NW == 1) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+  } else if constexpr (NW == 2) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  } else {
+#pragma unroll
+    for (int i = 0; i < NW / 4; ++i)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "r"(addr + 16 * i));
+  }
+}
+
+// One output pair (two neighbouring values of the head dimension).
+template <bool F16>
+__device__ __forceinline__ uint32_t ps_out2(float a, float b) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return ps_bf2(a, b);
+  }
+}
+
+template <int BITS, int D, int GS, int NT, bool F16>
+__global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
+    qda_paged_split_kernel(const __grid_constant__ QdaPagedParams p) {
+  using G = PsGeom<BITS, D, GS, NT>;
+  constexpr int NG = G::NG, MT = G::MT, KPS = G::KPS, RB = G::RB, STAGES = G::STAGES;
+  constexpr int KS = GS / 16;                 // products per group and key tile, on either side
+  constexpr float MID = BITS == 4 ? 8.f : 128.f;
+  constexpr float VOFF = BITS == 4 ? 128.f : 2176.f;
+  constexpr float VADD = G::ONES ? VOFF + MID : 0.f;
+  extern __shared__ __align__(128) unsigned char ps_smem[];
+  __shared__ PagedLine line;
+  __shared__ float s_ml[NT][kPsWarps][2][8];   // per 8 query rows and warp: reference, sum
+  __shared__ PagedTile t;   // the tile at hand, and this CTA's piece of the line
+  __shared__ long long s_x[2];
+  __shared__ int s_more;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r8 = lane >> 2, c4 = lane & 3;
+  uint2* s_qf = reinterpret_cast<uint2*>(ps_smem);
+  float2* s_qs = reinterpret_cast<float2*>(ps_smem + G::QF);   // [NG][MT] (-offset sum, sum) of q
+  const uint32_t ring = smem_addr(ps_smem + G::ROWS) + warp * STAGES * G::STAGE;
+  float* comb = reinterpret_cast<float*>(ps_smem + G::ROWS);
+
+  pdl_launch_dependents();
+  paged_line(p, MT, line);
+  const long long total = line.at[p.B];
+  if (total == 0) return;
+  const int ctas = paged_ctas(total, p.ctas, p.min_keys);
+  const int cta = blockIdx.x;
+  if (cta >= ctas) return;
+  if (tid == 0) {
+    s_x[0] = paged_border(total, ctas, cta);
+    s_x[1] = paged_border(total, ctas, cta + 1);
+    t = paged_tile_at(p, line, MT, s_x[0]);
+  }
+  __syncthreads();
+  const int pmask = (1 << p.page_shift) - 1;
+
+  for (;;) {
+    const int keys = paged_tile_keys(p, t, MT);
+    const int nblk = (keys + KPS - 1) / KPS;
+    const int j0 = paged_block_at(t, nblk, s_x[0]), j1 = paged_block_at(t, nblk, s_x[1]);
+    const bool mine = s_x[0] <= t.lo;   // the CTA that starts the tile
+    if (j0 < j1 || (nblk == 0 && mine)) {
+      const int row0 = t.i * MT;
+      // ---- the tile's query rows: B operands, sums per group, and how far each sees
+      uint2 qf[G::QSMEM ? 1 : D / 16 * NT];
+      float qoff[G::SSMEM ? 1 : NG * NT][2], qsum[G::SSMEM ? 1 : NG * NT][2];
+      float qmul[NT][2];
+      int seen[NT][2];
+      int least = 0x7fffffff;   // keys that every row of the tile sees
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = row0 + nt * 8 + r8;
+        const bool real = r < t.s.rows;
+        const int tok = r / p.nrep;
+        const uint16_t* qp = p.q + (long long)(t.s.first + tok) * p.q_tstride +
+                             (long long)(t.kvh * p.nrep + (r - tok * p.nrep)) * p.q_hstride;
+        // lane c4 holds dimensions g GS + c4 GS / 4 ... of every group of row r8
+        uint32_t raw[D / 8];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+#pragma unroll
+          for (int i = 0; i < GS / 32; ++i) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (real) v = *reinterpret_cast<const uint4*>(qp + g * GS + c4 * (GS / 4) + 8 * i);
+            raw[g * (GS / 8) + 4 * i] = v.x;
+            raw[g * (GS / 8) + 4 * i + 1] = v.y;
+            raw[g * (GS / 8) + 4 * i + 2] = v.z;
+            raw[g * (GS / 8) + 4 * i + 3] = v.w;
+          }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          top = fmaxf(top, fmaxf(fabsf(ps_half<F16>(&raw[i], 0)), fabsf(ps_half<F16>(&raw[i], 1))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // largest value of the row to [2^8, 2^9): every product stays far inside fp32, values down to 2^-22 of it are normal in fp16
+        const int fe = min(262 - (int)((__float_as_uint(top) >> 23) & 255u), 253);
+        const float up = __uint_as_float((uint32_t)fe << 23), down = __uint_as_float((uint32_t)(254 - fe) << 23);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          float off = 0.f, sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < GS / 32; ++i) {
+            // eight values of the row: 4-bit: two products (codes 0 4 | 1 5, and 2 6 | 3 7), 8-bit: (0 2 | 1 3, 4 6 | 5 7)
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = ps_half<F16>(&raw[g * (GS / 8) + 4 * i], e) * up;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float lo0 = BITS == 4 ? v[2 * h] : v[4 * h], lo1 = BITS == 4 ? v[2 * h + 4] : v[4 * h + 2];
+              const float hi0 = BITS == 4 ? v[2 * h + 1] * 0.0625f : v[4 * h + 1];
+              const float hi1 = BITS == 4 ? v[2 * h + 5] * 0.0625f : v[4 * h + 3];
+              const __half2 a = __floats2half2_rn(lo0, lo1), b = __floats2half2_rn(hi0, hi1);
+              const float2 af = __half22float2(a), bf = __half22float2(b);
+              off += af.x + af.y + bf.x + bf.y;   // what the offset 1024 of every code adds up to
+              const uint2 f = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+              const int ks = (g * (GS / 32) + i) * 2 + h;
+              if constexpr (G::QSMEM) {
+                if (warp == 0) s_qf[(ks * NT + nt) * 32 + lane] = f;
+              } else {
+                qf[ks * NT + nt] = f;
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += v[e];
+          }
+          // over the four lanes of the row
+          off += __shfl_xor_sync(0xffffffffu, off, 1);
+          off += __shfl_xor_sync(0xffffffffu, off, 2);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          off *= -1024.f;
+          if constexpr (G::SSMEM) {
+            if (warp == 0 && c4 == 0) s_qs[g * MT + nt * 8 + r8] = make_float2(off, sum);
+          } else {
+            // scores hold query rows 2 c4, 2 c4 + 1 in this lane
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              qoff[g * NT + nt][j] = __shfl_sync(0xffffffffu, off, (2 * c4 + j) * 4);
+              qsum[g * NT + nt][j] = __shfl_sync(0xffffffffu, sum, (2 * c4 + j) * 4);
+            }
+          }
+        }
+        const int sr = real ? paged_seen(p, t.s, r) : keys;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          qmul[nt][j] = __shfl_sync(0xffffffffu, down, (2 * c4 + j) * 4) * p.qscale;
+          seen[nt][j] = __shfl_sync(0xffffffffu, sr, (2 * c4 + j) * 4);
+          least = min(least, seen[nt][j]);
+        }
+      }
+      least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
+      least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
+      if constexpr (G::QSMEM || G::SSMEM) __syncthreads();
+
+      // ---- this warp's key blocks j0 + warp, + kPsWarps, ... through its ring
+      const int mine_n = j1 - j0 > warp ? (j1 - j0 - warp + kPsWarps - 1) / kPsWarps : 0;
+      const int* tab = p.table + (size_t)t.b * p.max_pages;
+      // the pages of a block's two 16-key halves (one half where a block is 16 keys), looked up one block ahead
+      int pg[KPS / 16];
+      auto look = [&](int k) {
+#pragma unroll
+        for (int h = 0; h < KPS / 16; ++h) {
+          const int n = (j0 + warp + k * kPsWarps) * KPS + 16 * h;
+          pg[h] = k < mine_n && n < keys ? __ldg(tab + (n >> p.page_shift)) : 0;
+        }
+      };
+      bool saw_absent = false;
+      uint32_t absent = 0;   // bit (stage * 2 + half): that half's page is outside the pool
+      auto issue = [&](int k) {
+        if (k < mine_n) {
+          const int st = k % STAGES;
+          const uint32_t base = ring + st * G::STAGE;
+          const int n0 = (j0 + warp + k * kPsWarps) * KPS;
+          long long row[KPS / 16];
+#pragma unroll
+          for (int h = 0; h < KPS / 16; ++h) {
+            const bool ok = (unsigned)pg[h] < (unsigned)p.num_pages;
+            const uint32_t bit = 1u << (st * 2 + h);
+            absent = ok ? absent & ~bit : absent | bit;
+            saw_absent = saw_absent || !ok;
+            row[h] = qda_pool_row(ok ? pg[h] : 0, t.kvh, (n0 + 16 * h) & pmask, p.Hkv, p.page_shift);
+          }
+#pragma unroll
+          for (int i = 0; i < G::CODE / 512; ++i) {
+            const int at = (i * 32 + lane) * 16, key = at / RB, col = at % RB;
+            const long long src = (row[KPS == 32 ? (i * 512 / RB) / 16 : 0] + (key & 15)) * RB + col;
+            const uint32_t dst = base + ps_code_at<RB>(key, col);
+            ps_cp16(dst, reinterpret_cast<const char*>(p.kp) + src);
+            ps_cp16(dst + G::CODE, reinterpret_cast<const char*>(p.vp) + src);
+          }
+          // scales and biases: 16 keys' are contiguous, NG * 2 pieces of 16 bytes per array and half
+          constexpr int PC = KPS / 16 * NG * 2;   // pieces per array
+#pragma unroll
+          for (int i = 0; i < (4 * PC + 31) / 32; ++i) {
+            const int id = i * 32 + lane, a = id / PC, k16 = id % PC;
+            if (id < 4 * PC) {
+              const uint16_t* arr = a == 0 ? p.ks : a == 1 ? p.kb : a == 2 ? p.vs : p.vb;
+              const int h = KPS == 32 ? k16 / (NG * 2) : 0;
+              const long long src = row[h] * (NG * 2) + (k16 - h * NG * 2) * 16;
+              ps_cp16(base + 2 * G::CODE + a * G::SC + k16 * 16, reinterpret_cast<const char*>(arr) + src);
+            }
+          }
+          look(k + 1);
+        }
+        ps_commit();
+      };
+
+      float o[NG * KS * NT][4], wsum[G::ONES ? NG * NT : 1][4], vb[NG * NT][2], l[NT][2], m[NT][2];
+#pragma unroll
+      for (int i = 0; i < NG * KS * NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      if constexpr (G::ONES) {
+#pragma unroll
+        for (int i = 0; i < NG * NT; ++i) wsum[i][0] = wsum[i][1] = wsum[i][2] = wsum[i][3] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < NG * NT; ++i) vb[i][0] = vb[i][1] = 0.f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        l[nt][0] = l[nt][1] = 0.f;
+        m[nt][0] = m[nt][1] = -INFINITY;
+      }
+
+      look(0);
+#pragma unroll
+      for (int k = 0; k < STAGES - 1; ++k) issue(k);
+      for (int k = 0; k < mine_n; ++k) {
+        issue(k + STAGES - 1);   // into the stage read one block ago
+        ps_wait<STAGES - 1>();
+        __syncwarp();   // every lane's pieces of the stage are in
+        const int st = k % STAGES;
+        const uint32_t base = ring + st * G::STAGE;
+#pragma unroll 1
+        for (int h = 0; h < KPS / 16; ++h) {
+          const int n0 = (j0 + warp + k * kPsWarps) * KPS + 16 * h;
+          if (n0 >= keys) break;
+          const bool gone = (absent >> (st * 2 + h)) & 1u;
+          const bool edge = gone || n0 + 16 > least;
+          const uint32_t kcode = base, vcode = base + G::CODE;
+          const uint32_t sc = base + 2 * G::CODE + (16 * h + r8) * NG * 2;   // this lane's key rows: r8 and r8 + 8
+          // ---- scores
+          float s[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+          {
+            uint32_t sw[2][(NG + 1) / 2], bw[2][(NG + 1) / 2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              ps_halves<NG>(sc + x * 8 * NG * 2, sw[x]);
+              ps_halves<NG>(sc + G::SC + x * 8 * NG * 2, bw[x]);
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              constexpr int KW = GS * BITS / 128;   // words per lane, group and row
+              uint32_t w0[KW], w1[KW];
+              const int col = (g * GS + c4 * (GS / 4)) * BITS / 8;
+              ps_words<KW>(kcode + ps_code_at<RB>(16 * h + r8, col), w0);
+              ps_words<KW>(kcode + ps_code_at<RB>(16 * h + r8 + 8, col), w1);
+              float acc[NT][4];
+#pragma unroll
+              for (int j = 0; j < KS; ++j) {
+                uint32_t a0, a1, a2, a3;
+                if constexpr (BITS == 4) {
+                  const uint32_t u = (j & 1) ? w0[j / 2] >> 8 : w0[j / 2], v = (j & 1) ? w1[j / 2] >> 8 : w1[j / 2];
+                  a0 = ps_or(u, 0x000F000Fu, 0x64006400u);
+                  a1 = ps_or(v, 0x000F000Fu, 0x64006400u);
+                  a2 = ps_or(u, 0x00F000F0u, 0x64006400u);
+                  a3 = ps_or(v, 0x00F000F0u, 0x64006400u);
+                } else {
+                  a0 = ps_or(w0[j], 0x00FF00FFu, 0x64006400u);
+                  a1 = ps_or(w1[j], 0x00FF00FFu, 0x64006400u);
+                  a2 = ps_or(w0[j] >> 8, 0x00FF00FFu, 0x64006400u);
+                  a3 = ps_or(w1[j] >> 8, 0x00FF00FFu, 0x64006400u);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  uint2 f;
+                  if constexpr (G::QSMEM) f = s_qf[((g * KS + j) * NT + nt) * 32 + lane];
+                  else f = qf[(g * KS + j) * NT + nt];
+                  if (j == 0) {
+                    float o0, o1;
+                    if constexpr (G::SSMEM) {
+                      o0 = s_qs[g * MT + nt * 8 + 2 * c4].x;
+                      o1 = s_qs[g * MT + nt * 8 + 2 * c4 + 1].x;
+                    } else {
+                      o0 = qoff[g * NT + nt][0];
+                      o1 = qoff[g * NT + nt][1];
+                    }
+                    ps_mma<true>(acc[nt], a0, a1, a2, a3, f.x, f.y, o0, o1, o0, o1);
+                  } else {
+                    ps_mma<true>(acc[nt], a0, a1, a2, a3, f.x, f.y, acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+                  }
+                }
+              }
+              const float s0 = ps_half<F16>(sw[0], g), s1 = ps_half<F16>(sw[1], g);
+              const float b0 = ps_half<F16>(bw[0], g), b1 = ps_half<F16>(bw[1], g);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float q0, q1;
+                if constexpr (G::SSMEM) {
+                  q0 = s_qs[g * MT + nt * 8 + 2 * c4].y;
+                  q1 = s_qs[g * MT + nt * 8 + 2 * c4 + 1].y;
+                } else {
+                  q0 = qsum[g * NT + nt][0];
+                  q1 = qsum[g * NT + nt][1];
+                }
+                s[nt][0] = fmaf(b0, q0, fmaf(s0, acc[nt][0], s[nt][0]));
+                s[nt][1] = fmaf(b0, q1, fmaf(s0, acc[nt][1], s[nt][1]));
+                s[nt][2] = fmaf(b1, q0, fmaf(s1, acc[nt][2], s[nt][2]));
+                s[nt][3] = fmaf(b1, q1, fmaf(s1, acc[nt][3], s[nt][3]));
+              }
+            }
+          }
+          // ---- weights
+          bool rise = false;
+          uint32_t hidden = 0;   // bit 4 nt + j: score j of query rows nt is hidden
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[nt][j] *= qmul[nt][j & 1];
+            if (edge) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (gone || n0 + r8 + (j >> 1) * 8 >= seen[nt][j & 1]) {
+                  s[nt][j] = -INFINITY;
+                  hidden |= 1u << (4 * nt + j);
+                }
+            }
+            rise = rise || fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + 8.f || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + 8.f;
+          }
+          if (__any_sync(0xffffffffu, rise)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float x = fmaxf(s[nt][j], s[nt][j + 2]);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                const float mn = fmaxf(m[nt][j], x);
+                const float f = mn == -INFINITY ? 1.f : ps_ex2(m[nt][j] - mn);   // 0 at the first visible key
+                m[nt][j] = mn;
+                l[nt][j] *= f;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                  vb[g * NT + nt][j] *= f;
+                  if constexpr (G::ONES) {
+                    wsum[g * NT + nt][j] *= f;
+                    wsum[g * NT + nt][j + 2] *= f;
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < NG * KS; ++i) {
+                  o[i * NT + nt][j] *= f;
+                  o[i * NT + nt][j + 2] *= f;
+                }
+              }
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+            s[nt][0] = ps_ex2(s[nt][0] - m0);
+            s[nt][1] = ps_ex2(s[nt][1] - m1);
+            s[nt][2] = ps_ex2(s[nt][2] - m0);
+            s[nt][3] = ps_ex2(s[nt][3] - m1);
+            l[nt][0] += s[nt][0] + s[nt][2];
+            l[nt][1] += s[nt][1] + s[nt][3];
+          }
+          // ---- values
+          uint32_t sw[2][(NG + 1) / 2], bw[2][(NG + 1) / 2];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            ps_halves<NG>(sc + 2 * G::SC + x * 8 * NG * 2, sw[x]);
+            ps_halves<NG>(sc + 3 * G::SC + x * 8 * NG * 2, bw[x]);
+          }
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const float s0 = ps_half<F16>(sw[0], g), s1 = ps_half<F16>(sw[1], g);
+            const float c0 = fmaf(MID, s0, ps_half<F16>(bw[0], g)), c1 = fmaf(MID, s1, ps_half<F16>(bw[1], g));
+            uint32_t hi[NT][2], lo[F16 ? NT : 1][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              float w[4] = {s[nt][0] * s0, s[nt][1] * s0, s[nt][2] * s1, s[nt][3] * s1};
+              float e[4] = {s[nt][0] * c0, s[nt][1] * c0, s[nt][2] * c1, s[nt][3] * c1};
+              if (edge) {   // a hidden key's scale and bias may be anything
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const bool no = (hidden >> (4 * nt + j)) & 1u;
+                  w[j] = no ? 0.f : w[j];
+                  e[j] = no ? 0.f : e[j];
+                }
+              }
+              vb[g * NT + nt][0] += e[0] + e[2];
+              vb[g * NT + nt][1] += e[1] + e[3];
+              const uint32_t h0 = ps_bf2(w[0], w[1]), h1 = ps_bf2(w[2], w[3]);
+              hi[nt][0] = ps_trans(h0);
+              hi[nt][1] = ps_trans(h1);
+              if constexpr (F16) {
+                lo[nt][0] = ps_trans(ps_bf2(w[0] - __uint_as_float(h0 << 16), w[1] - __uint_as_float(h0 & 0xffff0000u)));
+                lo[nt][1] = ps_trans(ps_bf2(w[2] - __uint_as_float(h1 << 16), w[3] - __uint_as_float(h1 & 0xffff0000u)));
+              }
+            }
+            auto mul = [&](float (&acc)[4], int nt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+              ps_mma<false>(acc, a0, a1, a2, a3, hi[nt][0], hi[nt][1], acc[0], acc[1], acc[2], acc[3]);
+              if constexpr (F16)
+                ps_mma<false>(acc, a0, a1, a2, a3, lo[nt][0], lo[nt][1], acc[0], acc[1], acc[2], acc[3]);
+            };
+            if constexpr (G::ONES) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mul(wsum[g * NT + nt], nt, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+            }
+            // this lane's codes: dimensions g GS + r8 GS / 8 ..., of keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
+            constexpr int VW = GS * BITS / 256;   // words per lane, group and key (0: half a word)
+            uint32_t kw[4][VW ? VW : 1];
+            const int col = (g * GS + r8 * (GS / 8)) * BITS / 8;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              ps_words<VW>(vcode + ps_code_at<RB>(16 * h + 2 * c4 + (x & 1) + (x >> 1) * 8, col), kw[x]);
+            // pairs of keys: 16 bits of codes of either
+            constexpr int PW = VW ? 2 * VW : 1;
+            uint32_t pa[PW], pb[PW];   // keys (2 c4, 2 c4 + 1) and those 8 behind
+#pragma unroll
+            for (int i = 0; i < PW; ++i) {
+              const uint32_t sel = VW && (i & 1) ? 0x7632u : 0x5410u;
+              pa[i] = __byte_perm(kw[0][i / 2], kw[1][i / 2], sel);
+              pb[i] = __byte_perm(kw[2][i / 2], kw[3][i / 2], sel);
+            }
+            // product j of the group: dimensions r8 GS / 8 + 2 j (rows 0-7) and + 2 j + 1 (rows 8-15)
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+              if constexpr (BITS == 4) {
+                const int i = j / 2, sh = 8 * (j & 1);
+                uint32_t a[4] = {pa[i] >> sh, pa[i] >> (sh + 4), pb[i] >> sh, pb[i] >> (sh + 4)};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  a[x] = ps_or(a[x], 0x000F000Fu, 0x43004300u);
+                  if constexpr (!G::ONES) {
+                    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[x]),
+                                                     __floats2bfloat162_rn(136.f, 136.f));
+                    a[x] = *reinterpret_cast<const uint32_t*>(&v);
+                  }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mul(o[(g * KS + j) * NT + nt], nt, a[0], a[1], a[2], a[3]);
+              } else {
+                // one pair word holds two dimensions: low byte 2 j, high byte 2 j + 1; nibbles in two products
+                uint32_t a[4] = {pa[j], pa[j] >> 8, pb[j], pb[j] >> 8}, b[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  b[x] = ps_or(a[x] >> 4, 0x000F000Fu, 0x45004500u);   // 2048 + 16 * high nibble
+                  a[x] = ps_or(a[x], 0x000F000Fu, 0x43004300u);        // 128 + low nibble
+                  if constexpr (!G::ONES) {
+                    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b[x]),
+                                                     __floats2bfloat162_rn(2176.f, 2176.f));
+                    b[x] = *reinterpret_cast<const uint32_t*>(&v);
+                    const __nv_bfloat162 u = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[x]),
+                                                     __floats2bfloat162_rn(128.f, 128.f));
+                    a[x] = *reinterpret_cast<const uint32_t*>(&u);
+                  }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  mul(o[(g * KS + j) * NT + nt], nt, a[0], a[1], a[2], a[3]);
+                  mul(o[(g * KS + j) * NT + nt], nt, b[0], b[1], b[2], b[3]);
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();   // the stage is read before it is filled again
+      }
+      ps_wait<0>();
+
+      // ---- the warps' results, 8 query rows at a time, through shared memory (the rings are empty now)
+      const bool whole = j0 == 0 && j1 == nblk;
+      const int slot = 2 * cta + (mine ? 1 : 0);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int sh = 4; sh <= 16; sh <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], sh);
+          if (r8 == 0) {
+            s_ml[nt][warp][0][2 * c4 + j] = m[nt][j];
+            s_ml[nt][warp][1][2 * c4 + j] = l[nt][j];
+          }
+        }
+        __syncthreads();   // also: every warp is through with its ring (or with the last 8 rows)
+        float f[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float M = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kPsWarps; ++w) M = fmaxf(M, s_ml[nt][w][0][2 * c4 + j]);
+          f[j] = m[nt][j] == -INFINITY ? 0.f : ps_ex2(m[nt][j] - M);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float e = vb[g * NT + nt][j];
+#pragma unroll
+            for (int sh = 4; sh <= 16; sh <<= 1) e += __shfl_xor_sync(0xffffffffu, e, sh);
+            if constexpr (G::ONES) e = fmaf(-VADD, wsum[g * NT + nt][j], e);
+            e *= f[j];
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+              float* dst = comb + (warp * 8 + 2 * c4 + j) * D + g * GS + r8 * (GS / 8) + 2 * i;
+              const float* oo = o[(g * KS + i) * NT + nt];
+              *reinterpret_cast<float2*>(dst) = make_float2(fmaf(oo[j], f[j], e), fmaf(oo[j + 2], f[j], e));
+            }
+          }
+        }
+        __syncthreads();
+        // one warp per query row in turn: sum over the warps in order, lanes along the head dimension
+        for (int q = warp; q < 8; q += kPsWarps) {
+          const int r = nt * 8 + q;
+          if (row0 + r >= t.s.rows) break;
+          float M = -INFINITY, L = 0.f;
+#pragma unroll
+          for (int w = 0; w < kPsWarps; ++w) M = fmaxf(M, s_ml[nt][w][0][q]);
+#pragma unroll
+          for (int w = 0; w < kPsWarps; ++w)
+            L += s_ml[nt][w][0][q] == -INFINITY ? 0.f : s_ml[nt][w][1][q] * ps_ex2(s_ml[nt][w][0][q] - M);
+          const int tok = (row0 + r) / p.nrep;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(
+              p.out + ((long long)(t.s.first + tok) * p.H + t.kvh * p.nrep + (row0 + r - tok * p.nrep)) * D);
+          float* po = p.part_o + ((size_t)slot * MT + r) * D;
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+          for (int d = 0; d < D; d += 64) {
+            float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kPsWarps; ++w) {
+              const float2 x = *reinterpret_cast<const float2*>(comb + (w * 8 + q) * D + d + 2 * lane);
+              v.x += x.x;
+              v.y += x.y;
+            }
+            if (whole) dst[(d >> 1) + lane] = ps_out2<F16>(v.x * inv, v.y * inv);
+            else *reinterpret_cast<float2*>(po + d + 2 * lane) = v;
+          }
+          if (!whole && lane == 0) p.part_ml[(size_t)slot * MT + r] = make_float2(M, L);
+        }
+      }
+      if (saw_absent && lane == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);
+    }
+    __syncthreads();   // the tile and the combine area are read before the next tile overwrites them
+    if (tid == 0) s_more = s_x[1] > t.hi && paged_tile_next(p, line, MT, t);
+    __syncthreads();
+    if (!s_more) break;
+  }
+}
+
+template <int BITS, int D, int GS, int NT, bool F16>
+cudaError_t ps_run(const QdaPagedParams* p, int* ctas_per_sm, cudaStream_t s) {
+  using G = PsGeom<BITS, D, GS, NT>;
+  auto kern = qda_paged_split_kernel<BITS, D, GS, NT, F16>;
+  if (ctas_per_sm != nullptr) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, kern, kPsWarps * 32, G::SMEM);
+    return e;
+  }
+  kern<<<p->ctas, kPsWarps * 32, G::SMEM, s>>>(*p);
+  return cudaGetLastError();
+}
+
+template <int BITS, bool F16>
+cudaError_t ps_pick(const QdaPagedParams* p, int D, int GS, int rows, int* occ, cudaStream_t s) {
+#define QDA_PS(d, gs)                                                                   \
+  if (D == d && GS == gs) {                                                             \
+    if constexpr (d <= 256) {                                                           \
+      if (rows > 8) return ps_run<BITS, d, gs, 2, F16>(p, occ, s);                      \
+    }                                                                                   \
+    return ps_run<BITS, d, gs, 1, F16>(p, occ, s);                                      \
+  }
+  QDA_PS(64, 32) QDA_PS(64, 64)
+  QDA_PS(128, 32) QDA_PS(128, 64) QDA_PS(128, 128)
+  QDA_PS(256, 32) QDA_PS(256, 64) QDA_PS(256, 128)
+  QDA_PS(512, 32) QDA_PS(512, 64) QDA_PS(512, 128)
+#undef QDA_PS
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace qda
