@@ -387,7 +387,8 @@ __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_const
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int row = t.i * MT + r, tok = row / p.nrep;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
-      p.out + ((long long)(t.s.first + tok) * p.H + t.kvh * p.nrep + (row - tok * p.nrep)) * D);
+      p.out + ((long long)(t.s.first + tok) * p.H + (t.unit / p.parts) * p.nrep + (row - tok * p.nrep)) * p.D +
+      (t.unit % p.parts) * D);
 #pragma unroll
   for (int e = 0; e < E; ++e)
     dst[e * 32 + lane] = p.f16 ? to_bits16x2<true>(o[e].x * inv, o[e].y * inv) : to_bits16x2<false>(o[e].x * inv, o[e].y * inv);
@@ -436,7 +437,8 @@ int check_pool(int num_pages, int page) {
 
 // The kernel a call takes, from what the host knows: the shape and the bound on a sequence's new tokens.
 struct PagedPlan {
-  int rows, kb, ctas, min_keys;
+  bool chunk;              // the chunk kernel (else the split kernel)
+  int rows, kb, ctas, min_keys, parts;
   size_t o_bytes, bytes;   // workspace: partial outputs, and with the (reference, sum) pairs
 };
 
@@ -446,27 +448,52 @@ SplitFn split_fn(int bits, bool f16) {
                    : (f16 ? qda_paged_split_b8_f1 : qda_paged_split_b8_f0);
 }
 
+// Rows (new tokens times query heads of a KV head) up to which the split kernel takes a call.
+constexpr long long kSplitRows = 16;
+
+cudaError_t chunk_run(const QdaPagedParams* p, int D, int bits, int rows, bool prepare, cudaStream_t s) {
+  return bits == 4 ? qda_paged_chunk_b4(p, D, rows / 128, prepare, s) : qda_paged_chunk_b8(p, D, rows / 128, prepare, s);
+}
+
 int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int sms, PagedPlan* plan) {
-  plan->rows = max_q * nrep > 8 && D <= 256 ? 16 : 8;
-  plan->kb = D * bits / 8 <= 64 ? 32 : 16;
-  plan->min_keys = 256;
+  const long long rows = max_q * nrep;
   int dev = 0;
   const cudaError_t de = cudaGetDevice(&dev);
   if (de != cudaSuccess || dev < 0 || dev >= 64) return qda_cuda_fail(de == cudaSuccess ? cudaErrorInvalidDevice : de);
-  static std::atomic<int> cache[64][2][2][4][3][2] = {};   // resident CTAs per SM of an instance, 0 = not asked yet
   const int di = D == 64 ? 0 : D == 128 ? 1 : D == 256 ? 2 : 3, gi = GS == 32 ? 0 : GS == 64 ? 1 : 2;
-  std::atomic<int>& slot = cache[dev][bits == 8][f16][di][gi][plan->rows == 16];
-  int occ = slot.load();
-  if (occ == 0) {
-    const cudaError_t e = split_fn(bits, f16)(nullptr, D, GS, plan->rows, &occ, nullptr);
-    if (e != cudaSuccess) return qda_cuda_fail(e);
-    occ = std::max(occ, 1);
-    slot.store(occ);
+  plan->chunk = rows > kSplitRows;
+  if (plan->chunk) {
+    plan->rows = rows > 128 && D <= 128 ? 256 : 128;
+    plan->kb = 128;
+    plan->min_keys = 512;
+    plan->parts = D == 512 ? 2 : 1;
+    plan->ctas = sms;
+    static std::atomic<bool> ready[64][2][4][2] = {};
+    std::atomic<bool>& r = ready[dev][bits == 8][di][plan->rows == 256];
+    if (!r.load()) {
+      const cudaError_t e = chunk_run(nullptr, D, bits, plan->rows, true, nullptr);
+      if (e != cudaSuccess) return qda_cuda_fail(e);
+      r.store(true);
+    }
+  } else {
+    plan->rows = rows > 8 && D <= 256 ? 16 : 8;
+    plan->kb = D * bits / 8 <= 64 ? 32 : 16;
+    plan->min_keys = 256;
+    plan->parts = 1;
+    static std::atomic<int> cache[64][2][2][4][3][2] = {};   // resident CTAs per SM of an instance, 0 = not asked yet
+    std::atomic<int>& slot = cache[dev][bits == 8][f16][di][gi][plan->rows == 16];
+    int occ = slot.load();
+    if (occ == 0) {
+      const cudaError_t e = split_fn(bits, f16)(nullptr, D, GS, plan->rows, &occ, nullptr);
+      if (e != cudaSuccess) return qda_cuda_fail(e);
+      occ = std::max(occ, 1);
+      slot.store(occ);
+    }
+    plan->ctas = sms * occ;
   }
-  plan->ctas = sms * occ;
-  const size_t rows = (size_t)2 * plan->ctas * plan->rows;
-  plan->o_bytes = (rows * D * 4 + 255) & ~(size_t)255;
-  plan->bytes = plan->o_bytes + rows * sizeof(float2);
+  const size_t n = (size_t)2 * plan->ctas * plan->rows;
+  plan->o_bytes = (n * (D / plan->parts) * 4 + 255) & ~(size_t)255;
+  plan->bytes = plan->o_bytes + n * sizeof(float2);
   return QDA_OK;
 }
 
@@ -476,7 +503,7 @@ bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 }  // namespace qda
 
 cudaError_t qda_launch_paged_merge(const QdaPagedParams& p, int rows, int kb, cudaStream_t s) {
-  switch (p.D) {
+  switch (p.D / p.parts) {
     case 64: return qda::launch_merge<64>(p, rows, kb, s);
     case 128: return qda::launch_merge<128>(p, rows, kb, s);
     case 256: return qda::launch_merge<256>(p, rows, kb, s);
@@ -577,7 +604,8 @@ extern "C" int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max
   // a call may state a smaller max_q than this one, and either dtype
   size_t most = 0;
   for (int f16 = 0; f16 < 2; ++f16) {
-    for (long long m : {1LL, (long long)max_q}) {
+    for (long long m : {1LL, kSplitRows / (H / Hkv), 128LL / (H / Hkv), (long long)max_q}) {
+      m = std::max(1LL, std::min(m, (long long)max_q));
       PagedPlan plan;
       got = paged_plan(H / Hkv, m, D, GS, bits, f16 != 0, sms, &plan);
       if (got != QDA_OK) return got;
@@ -652,9 +680,12 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + plan.o_bytes);
   p.ctas = plan.ctas;
+  p.parts = plan.parts;
+  p.units = Hkv * plan.parts;
   p.min_keys = plan.min_keys;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = split_fn(bits, p.f16 != 0)(&p, D, GS, plan.rows, nullptr, s);
+  cudaError_t e = plan.chunk ? chunk_run(&p, D, bits, plan.rows, false, s)
+                             : split_fn(bits, p.f16 != 0)(&p, D, GS, plan.rows, nullptr, s);
   if (e == cudaSuccess) e = qda_launch_paged_merge(p, plan.rows, plan.kb, s);
   return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
 }

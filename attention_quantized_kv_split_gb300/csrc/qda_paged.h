@@ -24,7 +24,8 @@ struct QdaPagedParams {
   float qscale;               // log2(e) / sqrt(D)
   // how the call is shared among CTAs (qda_paged_sched.cuh)
   int ctas, min_keys;         // CTAs launched; fewest keys of a CTA's piece
-  float* part_o;              // [2 * ctas, MT, D] unnormalised partial outputs of split tiles
+  int units, parts;           // units of a sequence: Hkv * parts, unit u holds part u % parts of KV head u / parts's values
+  float* part_o;              // [2 * ctas, MT, D / parts] unnormalised partial outputs of split tiles
   float2* part_ml;            // [2 * ctas, MT] (reference in log2 units, sum of weights)
 };
 
@@ -39,6 +40,11 @@ cudaError_t qda_paged_split_b4_f0(const QdaPagedParams* p, int D, int GS, int ro
 cudaError_t qda_paged_split_b4_f1(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 cudaError_t qda_paged_split_b8_f0(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 cudaError_t qda_paged_split_b8_f1(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+
+// The chunk kernel (qda_paged_chunk.cuh): 128 * tiles query rows per tile (tiles 1 or 2; 1 for D > 128), one CTA per SM.
+// prepare sets the instance's shared memory limit on the current device and launches nothing.
+cudaError_t qda_paged_chunk_b4(const QdaPagedParams* p, int D, int tiles, bool prepare, cudaStream_t s);
+cudaError_t qda_paged_chunk_b8(const QdaPagedParams* p, int D, int tiles, bool prepare, cudaStream_t s);
 
 // Merge of the split tiles' partial results, behind a kernel of `rows` rows per tile and key blocks of kb keys.
 cudaError_t qda_launch_paged_merge(const QdaPagedParams& p, int rows, int kb, cudaStream_t s);

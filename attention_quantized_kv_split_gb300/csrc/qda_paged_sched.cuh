@@ -1,7 +1,8 @@
 // How a paged attention call is shared among its CTAs (sm_103a), from lengths that only the device knows.
 //
 // The rows of a sequence under one KV head, r = i * nrep + j for new token i and the head's query head j, are cut into
-// tiles of MT rows; a tile walks the keys that its last row sees. All (sequence, KV head, tile) triples in that order
+// tiles of MT rows; a tile walks the keys that its last row sees. All (sequence, unit, tile) triples in that order (a unit is a KV head, or
+// for a kernel that cannot hold a head's values at once, a KV head and a part of its values)
 // form one line, each with a length in keys: exact for cross attention, linear in the tile's index for causal attention (plus a constant for a
 // tile's fixed work). CTA c takes the c-th of `ctas` equal pieces of the line, so ragged lengths, chunks and single
 // tokens are balanced alike, whatever they are. A piece border inside a tile falls on the border of a key block in proportion; the tile's partial
@@ -42,7 +43,7 @@ __device__ __forceinline__ int paged_seen(const QdaPagedParams& p, const PagedSe
   return p.causal ? max(0, min(s.n_all, s.base + r / p.nrep + 1)) : s.n_all;
 }
 
-// Length of the sequence's first i tiles (of one KV head) on the line.
+// Length of the sequence's first i tiles (of one unit) on the line.
 __device__ __forceinline__ long long paged_prefix(const QdaPagedParams& p, const PagedSeq& s, long long i) {
   return i * (kTileCost + max(s.base, 0)) + s.step2 * (i * (i + 1) / 2) / p.nrep;
 }
@@ -63,7 +64,7 @@ __device__ __forceinline__ void paged_line(const QdaPagedParams& p, int MT, Page
     long long v = 0;
     if (b < p.B) {
       const PagedSeq s = paged_seq(p, b, MT);
-      v = p.Hkv * paged_prefix(p, s, s.tiles);
+      v = p.units * paged_prefix(p, s, s.tiles);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -92,16 +93,10 @@ __device__ __forceinline__ long long paged_border(long long total, int ctas, int
 
 // A tile on the line.
 struct PagedTile {
-  int b, kvh, i;        // sequence, KV head, tile of the sequence
+  int b, unit, i;       // sequence, unit (KV head, or a part of its values), tile of the sequence
   long long lo, hi;     // its place on the line
   PagedSeq s;
 };
-
-__device__ __forceinline__ void paged_tile_place(const QdaPagedParams& p, const PagedLine& line, PagedTile& t) {
-  const long long head = line.at[t.b] + t.kvh * paged_prefix(p, t.s, t.s.tiles);
-  t.lo = head + paged_prefix(p, t.s, t.i);
-  t.hi = head + paged_prefix(p, t.s, t.i + 1);
-}
 
 // The tile that holds place x of the line (0 <= x < line.at[B]).
 __device__ __forceinline__ PagedTile paged_tile_at(const QdaPagedParams& p, const PagedLine& line, int MT, long long x) {
@@ -115,31 +110,34 @@ __device__ __forceinline__ PagedTile paged_tile_at(const QdaPagedParams& p, cons
   t.s = paged_seq(p, lo, MT);
   const long long head = paged_prefix(p, t.s, t.s.tiles);
   const long long y = x - line.at[lo];
-  t.kvh = (int)(y / head);
-  const long long z = y - t.kvh * head;
+  t.unit = (int)(y / head);
+  const long long z = y - t.unit * head;
   int a = 0, e = t.s.tiles;
   while (e - a > 1) {
     const int mid = (a + e) >> 1;
     if (paged_prefix(p, t.s, mid) <= z) a = mid; else e = mid;
   }
   t.i = a;
-  paged_tile_place(p, line, t);
+  const long long at = line.at[lo] + t.unit * head;
+  t.lo = at + paged_prefix(p, t.s, t.i);
+  t.hi = at + paged_prefix(p, t.s, t.i + 1);
   return t;
 }
 
-// The next tile on the line; false behind the last.
-__device__ __forceinline__ bool paged_tile_next(const QdaPagedParams& p, const PagedLine& line, int MT, PagedTile& t) {
+// The next tile on the line; false behind the last. Tiles are contiguous on the line, so it starts where this one ends.
+__device__ __forceinline__ bool paged_tile_next(const QdaPagedParams& p, int MT, PagedTile& t) {
   if (++t.i >= t.s.tiles) {
     t.i = 0;
-    if (++t.kvh >= p.Hkv) {
-      t.kvh = 0;
+    if (++t.unit >= p.units) {
+      t.unit = 0;
       do {
         if (++t.b >= p.B) return false;
-      } while (line.at[t.b + 1] == line.at[t.b]);
-      t.s = paged_seq(p, t.b, MT);
+        t.s = paged_seq(p, t.b, MT);
+      } while (t.s.tiles == 0);
     }
   }
-  paged_tile_place(p, line, t);
+  t.lo = t.hi;
+  t.hi = t.lo + paged_prefix(p, t.s, t.i + 1) - paged_prefix(p, t.s, t.i);
   return true;
 }
 

@@ -50,6 +50,7 @@ struct PsGeom {
   static constexpr int RING = kPsWarps * STAGES * STAGE;
   static constexpr int COMB = kPsWarps * 8 * D * 4;   // the warps' results of 8 query rows
   static constexpr int SMEM = ROWS + (RING > COMB ? RING : COMB);
+  static_assert(SMEM - ROWS >= (int)sizeof(PagedLine), "the line lies in the ring");
   static constexpr int OREGS = D / 4 * NT;
   static constexpr int MINB = OREGS <= 32 ? 4 : OREGS <= 64 ? 3 : 2;
 };
@@ -184,7 +185,6 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
   constexpr float VOFF = BITS == 4 ? 128.f : 2176.f;
   constexpr float VADD = G::ONES ? VOFF + MID : 0.f;
   extern __shared__ __align__(128) unsigned char ps_smem[];
-  __shared__ PagedLine line;
   __shared__ float s_ml[NT][kPsWarps][2][8];   // per 8 query rows and warp: reference, sum
   __shared__ PagedTile t;   // the tile at hand, and this CTA's piece of the line
   __shared__ long long s_x[2];
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
   float* comb = reinterpret_cast<float*>(ps_smem + G::ROWS);
 
   pdl_launch_dependents();
+  PagedLine& line = *reinterpret_cast<PagedLine*>(comb);   // before the first copy lands there
   paged_line(p, MT, line);
   const long long total = line.at[p.B];
   if (total == 0) return;
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
         const bool real = r < t.s.rows;
         const int tok = r / p.nrep;
         const uint16_t* qp = p.q + (long long)(t.s.first + tok) * p.q_tstride +
-                             (long long)(t.kvh * p.nrep + (r - tok * p.nrep)) * p.q_hstride;
+                             (long long)(t.unit * p.nrep + (r - tok * p.nrep)) * p.q_hstride;
         // lane c4 holds dimensions g GS + c4 GS / 4 ... of every group of row r8
         uint32_t raw[D / 8];
 #pragma unroll
@@ -336,7 +337,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             const uint32_t bit = 1u << (st * 2 + h);
             absent = ok ? absent & ~bit : absent | bit;
             saw_absent = saw_absent || !ok;
-            row[h] = qda_pool_row(ok ? pg[h] : 0, t.kvh, (n0 + 16 * h) & pmask, p.Hkv, p.page_shift);
+            row[h] = qda_pool_row(ok ? pg[h] : 0, t.unit, (n0 + 16 * h) & pmask, p.Hkv, p.page_shift);
           }
 #pragma unroll
           for (int i = 0; i < G::CODE / 512; ++i) {
@@ -683,7 +684,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             L += s_ml[nt][w][0][q] == -INFINITY ? 0.f : s_ml[nt][w][1][q] * ps_ex2(s_ml[nt][w][0][q] - M);
           const int tok = (row0 + r) / p.nrep;
           uint32_t* dst = reinterpret_cast<uint32_t*>(
-              p.out + ((long long)(t.s.first + tok) * p.H + t.kvh * p.nrep + (row0 + r - tok * p.nrep)) * D);
+              p.out + ((long long)(t.s.first + tok) * p.H + t.unit * p.nrep + (row0 + r - tok * p.nrep)) * D);
           float* po = p.part_o + ((size_t)slot * MT + r) * D;
           const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
@@ -704,7 +705,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       if (saw_absent && lane == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);
     }
     __syncthreads();   // the tile and the combine area are read before the next tile overwrites them
-    if (tid == 0) s_more = s_x[1] > t.hi && paged_tile_next(p, line, MT, t);
+    if (tid == 0) s_more = s_x[1] > t.hi && paged_tile_next(p, MT, t);
     __syncthreads();
     if (!s_more) break;
   }

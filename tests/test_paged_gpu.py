@@ -197,6 +197,30 @@ def test_long_sequences_are_split(q_len, kv, D):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("D,GS,bits", [(64, 32, 8), (128, 64, 4), (256, 32, 8), (256, 128, 4), (512, 64, 8)])
+@pytest.mark.parametrize("q_len", [60, 130])
+def test_many_tiles_and_blocks_per_cta(D, GS, bits, q_len):
+    # more work than CTAs: every CTA walks several tiles of a few dozen key blocks, with and without split ones
+    B = {64: 24, 128: 12, 256: 8, 512: 4}[D]
+    kv = [2400 + 301 * (i % 5) for i in range(B)]
+    c = Case([q_len] * B, kv, 16, 8, D, bits, GS, "bf16", 32, seed=D + q_len)
+    ref = None
+    for _ in range(3):
+        got = c.run()
+        ref = got.clone() if ref is None else ref
+        assert torch.equal(got, ref)
+    assert qda.qdecode_attn_device_status() == 0
+    rows = [b for b in range(B) if b % max(1, B // 3) == 0]   # a few sequences in 64 bits
+    sub = Case.__new__(Case)
+    sub.__dict__.update(c.__dict__)
+    sub.q_lens, sub.kv_lens, sub.total = [q_len] * len(rows), [kv[b] for b in rows], q_len * len(rows)
+    sub.K, sub.V, sub.A = ([x[b] for b in rows] for x in (c.K, c.V, c.A))
+    sub.start = np.arange(len(rows) + 1) * q_len
+    pick = np.concatenate([np.arange(b * q_len, (b + 1) * q_len) for b in rows])
+    sub.q64 = c.q64[pick]
+    sub.check(got[torch.from_numpy(pick).cuda()])
+
+
 @pytest.mark.parametrize("q_lens", [[1, 1], [90, 140]])
 def test_more_queries_than_keys(q_lens):
     # cross attention to fewer states than tokens; with a causal mask the first tokens see nothing and give zeros
