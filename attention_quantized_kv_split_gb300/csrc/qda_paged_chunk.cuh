@@ -7,7 +7,7 @@
 //   softmax warps        one thread per query row: reads its row of S from tensor memory, writes P (fp16) over it;
 //   MMA warp             one thread issues every product. With two tiles the products of one run while the softmax of the other does;
 //                        with one tile S has two buffers and the next block's scores run during this block's softmax;
-//   info warp            one block ahead: the block's pages, and how large its keys and values can be.
+//   info warps           blocks ahead: a block's pages, and how large its keys and values can be.
 // Every link is an mbarrier; every wait is bounded and sets the device error word.
 //
 // Operands are fp16 for both input types (11 significant bits; for bf16 caches the operands then add almost nothing to the one
@@ -23,6 +23,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "qda_paged_sched.cuh"
 
 namespace qda {
@@ -30,12 +32,14 @@ namespace qda {
 constexpr int kPcKeys = 128;     // keys per block
 constexpr int kPcDeq = 8;        // dequantising warps
 constexpr int kPcInfo = 8;       // blocks of info in flight
+constexpr int kPcTiles = 4;      // tiles in flight
+constexpr int kPcInfoWarps = 3;  // info warps, taking blocks in turn (they fill up the last group of four warps)
 
 struct PcInfo {
   int pg[8];              // page of each 16 keys (-1: none or absent)
   float kmul;             // what undoes the keys' scale
-  float kfac, vfac;       // the keys' and values' scale
-  int kv;                 // values' scale is 2^-kv
+  float kfac;             // the keys' scale
+  int kv;                 // 2^-kv scales this block's values so; the walk takes the largest kv up to here
   uint32_t flags;         // any bit of gone or bad
   uint32_t gone[4];       // keys on absent pages
   uint32_t bad[4];        // keys or values that are not finite
@@ -53,21 +57,37 @@ struct PcGeom {
   static constexpr int SLOTS0 = (226 * 1024 - 1024 - QB) / SLOT;
   static constexpr int SLOTS = SLOTS0 > 6 ? 6 : SLOTS0;
   static constexpr int SOFT = 4 * NQ;                   // softmax warps
-  static constexpr int WARPS = SOFT + kPcDeq + 2;
+  static constexpr int WARPS = SOFT + kPcDeq + 1 + kPcInfoWarps;
+  // registers a thread: the launch's 96 (20 warps) or 128 (16 warps), dealt out anew among the warpgroups
+  static constexpr int R_SOFT = NQ == 2 ? 128 : 176, R_DEQ = NQ == 2 ? 88 : 120, R_LAST = NQ == 2 ? 48 : 80;
+  static_assert(SOFT * R_SOFT + kPcDeq * R_DEQ + 4 * R_LAST <= WARPS * (NQ == 2 ? 96 : 128), "registers of the launch");
+  static constexpr int AHEAD = BITS == 8 && NQ == 2 ? 1 : 2;   // items of codes under way: what the registers hold
   static constexpr int O_COL = 256;                     // O behind two S buffers of 128 columns
   static_assert(NQ == 1 || D <= 128, "two tiles need room for two O");
   static_assert(SLOTS >= 3 && O_COL + NQ * DV <= 512, "shared or tensor memory");
 };
 
+// A tile of this CTA's piece, and its part of the tile's key blocks.
+struct PcTile {
+  int n, j0;              // blocks j0 .. j0 + n - 1 (n = 0: a tile without keys, whose rows are zeros; -1: behind the last tile)
+  int keys;               // keys that the tile walks
+  int whole, mine;        // all of the tile's blocks; the tile starts in this CTA's piece
+  int row0, kvh, part, b;
+  PagedSeq s;
+};
+
 struct PcShared {
   PcInfo info[kPcInfo];
-  uint64_t info_full[kPcInfo], info_empty[kPcInfo], full[6], empty[6], q_full, s_full[2], p_full[2], drain;
-  uint64_t pv_done[2];   // one tile: values of even and odd blocks (a parity tells only neighbouring phases apart, and no more than two blocks are open)
+  PcTile tile[kPcTiles];
+  uint64_t info_full[kPcInfo], info_empty[kPcInfo], tile_full[kPcTiles], tile_empty[kPcTiles], full[6], empty[6], q_full,
+      s_full[2], p_full[2], drain;
+  uint64_t pv_done[2];    // two tiles: a tile's last values; one: values of even and odd blocks
   PagedTile t;
   long long x[2];
   uint32_t tmem;
   int abort, more;
 };
+// (A wait on a phase's parity tells neighbouring phases apart only: no barrier runs two phases ahead of a waiting role.)
 
 template <int D, int BITS, int NQ>
 constexpr int pc_smem() {
@@ -88,38 +108,43 @@ __device__ __forceinline__ uint64_t pc_desc(uint32_t saddr, uint32_t lbo) {
          (1ull << 46) | (2ull << 61);
 }
 
-__device__ __forceinline__ void pc_mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// One lane of the warp, the same one every time. The products below are issued by that lane while the whole warp walks through the code: addresses and
+// descriptors then stay in uniform registers, where the instruction wants them.
+__device__ __forceinline__ uint32_t pc_elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
+// D (tensor memory) (+)= A (shared memory) * B (shared memory)
+__device__ __forceinline__ void pc_mma_ss(uint32_t one, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
       : "memory");
 }
-
-__device__ __forceinline__ void pc_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
+// D (tensor memory) (+)= A (tensor memory) * B (shared memory)
+__device__ __forceinline__ void pc_mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void pc_commit(uint32_t one, uint64_t* bar) {
+  if (one) mma_commit(bar);
+}
+
+__device__ __forceinline__ void pc_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void pc_st32(uint32_t taddr, const float (&v)[32]) {
-  uint32_t a[16], b[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    a[i] = __float_as_uint(v[i]);
-    b[i] = __float_as_uint(v[16 + i]);
-  }
-  tmem_st16(taddr, a);
-  tmem_st16(taddr + 16, b);
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 __device__ __forceinline__ uint32_t pc_h2(float lo, float hi) {
@@ -140,20 +165,30 @@ __host__ __device__ constexpr int pc_dim(int i) {
   return BITS == 4 ? (i >> 1) + 4 * (i & 1) : (i & 4) + ((i & 3) >> 1) + 2 * (i & 1);
 }
 
+// Register count of the calling warpgroup from here on (the sums over the warpgroups stay within the launch's).
+template <int N>
+__device__ __forceinline__ void pc_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void pc_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int D, int BITS, int NQ>
 __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     qda_paged_chunk_kernel(const __grid_constant__ QdaPagedParams p) {
   using G = PcGeom<D, BITS, NQ>;
   constexpr int MT = G::MT, SD = G::SD, DV = G::DV, KSL = G::KSL, VSL = G::VSL, SLOTS = G::SLOTS;
   constexpr float QMAX = (float)((1 << BITS) - 1);
-  constexpr float FINITE = 1.329228e36f;   // 2^120: what is larger counts as not finite
+  constexpr float FINITE = 1.2980742e33f;   // 2^110: a scale or bias this large counts as not finite
   extern __shared__ __align__(1024) unsigned char pc_smem_raw[];
   unsigned char* base = pc_smem_raw + ((1024u - (smem_addr(pc_smem_raw) & 1023u)) & 1023u);
   unsigned char* q_s = base;
   unsigned char* ring = base + G::QB;
   PcShared& sh = *reinterpret_cast<PcShared*>(ring + SLOTS * G::SLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int W_DEQ = G::SOFT, W_MMA = G::SOFT + kPcDeq;   // and the info warp behind
+  constexpr int W_DEQ = G::SOFT, W_MMA = G::SOFT + kPcDeq;   // the info warps behind
   volatile int* abort = &sh.abort;
 
   pdl_launch_dependents();
@@ -165,6 +200,11 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&sh.full[i], kPcDeq);
       mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < kPcTiles; ++i) {
+      mbar_init(&sh.tile_full[i], 1);
+      mbar_init(&sh.tile_empty[i], G::WARPS - 1);
+      sh.tile[i].n = -1;
     }
     mbar_init(&sh.q_full, G::SOFT);
     for (int i = 0; i < 2; ++i) {
@@ -193,492 +233,665 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const int pmask = (1 << p.page_shift) - 1, Hkv = p.units / G::PARTS;
-  uint32_t bc = 0, ic = 0, sc = 0, tc = 0;   // blocks, slots, s_full phases (two tiles) and tiles so far
+  // blocks, slots and tiles with blocks so far: every role counts them for itself
+  uint32_t bc = 0, ic = 0, tc = 0;
+  auto wait = [&](uint64_t* bar, uint32_t phase) { mbar_wait_bounded(bar, phase & 1u, abort, p.err, 1u); };
+  // tile k of this CTA's piece (null behind the last); every warp hands it back with tile_done
+  auto tile_at = [&](int k) -> const PcTile* {
+    wait(&sh.tile_full[k % kPcTiles], k / kPcTiles);
+    if (__any_sync(0xffffffffu, *abort != 0)) return nullptr;   // a wait gave up somewhere: every role ends
+    const PcTile* t = &sh.tile[k % kPcTiles];
+    return t->n < 0 ? nullptr : t;
+  };
+  auto tile_done = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.tile_empty[k % kPcTiles]);
+  };
+  // slots of a tile of n blocks in the order of use: K(0), then K(j + 1), V(j)
+  auto it_k = [&](int j) { return ic + (j == 0 ? 0 : KSL + (j - 1) * (KSL + VSL)); };
+  auto it_v = [&](int j, int n) { return ic + KSL + j * (KSL + VSL) + (j + 1 < n ? KSL : 0); };
 
-  for (;;) {
-    const PagedTile& t = sh.t;
-    const int keys = paged_tile_keys(p, t, MT);
-    const int nblk = (keys + kPcKeys - 1) / kPcKeys;
-    const int j0 = paged_block_at(t, nblk, sh.x[0]), j1 = paged_block_at(t, nblk, sh.x[1]), n = j1 - j0;
-    const bool mine = sh.x[0] <= t.lo;
-    const int row0 = t.i * MT, kvh = t.unit / G::PARTS, part = t.unit % G::PARTS;
-    // slots in the order of use: K(0), then K(j + 1), V(j)
-    auto it_k = [&](int j) { return ic + (j == 0 ? 0 : KSL + (j - 1) * (KSL + VSL)); };
-    auto it_v = [&](int j) { return ic + KSL + j * (KSL + VSL) + (j + 1 < n ? KSL : 0); };
-
-    if (n > 0 || (nblk == 0 && mine)) {
-      if (warp < G::SOFT) {
-        // ================================================================================= softmax: a thread per row
-        const int tq = warp >> 2;
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const int rt = tq * 128 + 32 * (warp & 3) + lane;   // row of the tile
-        const int r = row0 + rt;
-        const bool real = r < t.s.rows;
-        const int tok = r / p.nrep, head = kvh * p.nrep + (r - tok * p.nrep);
-        const int seen = real ? paged_seen(p, t.s, r) : keys;
-        float qmul = p.qscale;
-        if (n > 0) {
-          const uint4* qp = reinterpret_cast<const uint4*>(p.q + (long long)(t.s.first + tok) * p.q_tstride +
-                                                           (long long)head * p.q_hstride);
-          float top = 0.f;
-          if (real) {
-#pragma unroll 4
-            for (int i = 0; i < D / 8; ++i) {
-              const uint4 a = qp[i];
-              const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+  if (warp < G::SOFT) {
+    // =================================================================================== softmax: a thread per row
+    pc_regs_up<G::R_SOFT>();
+    const int tq = warp >> 2;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const int rt = tq * 128 + 32 * (warp & 3) + lane;   // row of the tile
+    const uint32_t o_t = tmem + lanes + G::O_COL + tq * DV;
+    // the row's query into shared memory, in the codes' unpacked order; returns what undoes its scale, times the softmax scale
+    auto load_q = [&](const PcTile& t) {
+      const int r = t.row0 + rt;
+      const bool real = r < t.s.rows;
+      const int tok = r / p.nrep;
+      const uint4* qp = reinterpret_cast<const uint4*>(p.q + (long long)(t.s.first + tok) * p.q_tstride +
+                                                       (long long)(t.kvh * p.nrep + (r - tok * p.nrep)) * p.q_hstride);
+      constexpr int C = D / 8, H = C < 16 ? C : 16;   // 16-byte pieces; held in registers at a time
+      uint4 a[H];
+      float top = 0.f;
+      auto get = [&](int c0) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 f = half2_bits_to_float2_rt(u[k], p.f16);
-                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
-            }
-          }
-          const int fe = min(262 - (int)((__float_as_uint(top) >> 23) & 255u), 253);
-          const float up = __uint_as_float((uint32_t)fe << 23);
-          qmul *= __uint_as_float((uint32_t)(254 - fe) << 23);
-          unsigned char* dst = q_s + tq * 128 * D * 2 + (rt & 127) * 128;
-#pragma unroll 4
-          for (int i = 0; i < D / 8; ++i) {
-            uint4 a = make_uint4(0, 0, 0, 0);
-            if (real) a = qp[i];
-            const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-            float v[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = half2_bits_to_float2_rt(u[k], p.f16);
-              v[2 * k] = f.x * up;
-              v[2 * k + 1] = f.y * up;
-            }
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = pc_h2(v[pc_dim<BITS>(2 * k)], v[pc_dim<BITS>(2 * k + 1)]);
-            *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (rt & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.q_full);
-        }
-        float m = -INFINITY, l = 0.f;
-        int kv = 0;
-        bool poison = false;
-        const uint32_t o_t = tmem + lanes + G::O_COL + tq * DV;
-        for (int j = 0; j < n; ++j) {
-          const uint32_t g = bc + j;
-          const PcInfo& f = sh.info[g % kPcInfo];
-          const int sb = NQ == 2 ? tq : (int)(g & 1);
-          const uint32_t s_t = tmem + lanes + 128 * sb;
-          mbar_wait_bounded(&sh.info_full[g % kPcInfo], (g / kPcInfo) & 1, abort, p.err, 1u);
-          mbar_wait_bounded(&sh.s_full[sb], NQ == 2 ? (sc + j) & 1 : (g >> 1) & 1, abort, p.err, 1u);
-          tc_fence_after();
-          const float mult = qmul * f.kmul;
-          const int kv_new = f.kv;
-          const uint32_t flags = f.flags;
-          const int key0 = (j0 + j) * kPcKeys;
-          const bool edge = flags || __any_sync(0xffffffffu, key0 + kPcKeys > seen);
-          float v[32];
-          // a score that the row does not see becomes -inf
-          auto mask = [&](int c) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (key0 + 32 * c + i >= seen) v[i] = -INFINITY;
-            if (flags) {
-              const uint32_t gone = f.gone[c], bad = f.bad[c];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if ((gone >> i) & 1u) v[i] = -INFINITY;
-                else if (((bad >> i) & 1u) && key0 + 32 * c + i < seen) poison = true;
-              }
-            }
-          };
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            pc_ld32(s_t + 32 * c, v);
-            tmem_wait_ld();
-            if (edge) mask(c);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) top = fmaxf(top, fmaxf(v[i], v[i + 1]));
-          }
-          top *= mult;   // mult > 0
-          if (j == 0) kv = kv_new;
-          if (__any_sync(0xffffffffu, top > m + 8.f) || kv_new != kv) {
-            const float mn = fmaxf(m, top);
-            const float a = mn == -INFINITY ? 1.f : pc_ex2(m - mn);
-            m = mn;
-            l *= a;
-            if (j > 0) {
-              if (NQ == 1) {   // the last block's values are in O (with two tiles the scores' barrier says so)
-                mbar_wait_bounded(&sh.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort, p.err, 1u);
-                tc_fence_after();
-              }
-              const float x = a * pc_ex2((float)(kv - kv_new));
+        for (int i = 0; i < H; ++i) a[i] = real ? __ldg(qp + c0 + i) : make_uint4(0, 0, 0, 0);
+      };
 #pragma unroll 1
-              for (int c = 0; c < DV / 32; ++c) {
-                pc_ld32(o_t + 32 * c, v);
-                tmem_wait_ld();
+      for (int c0 = 0; c0 < C; c0 += H) {
+        get(c0);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= x;
-                pc_st32(o_t + 32 * c, v);
-              }
-            }
-            kv = kv_new;
+        for (int i = 0; i < H; ++i) {
+          const uint32_t u[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = half2_bits_to_float2_rt(u[k], p.f16);
+            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
-          const float mm = m == -INFINITY ? 0.f : -m;
-          float2 sum = make_float2(0.f, 0.f);
+        }
+      }
+      const int fe = min(262 - (int)((__float_as_uint(top) >> 23) & 255u), 253);
+      const float up = __uint_as_float((uint32_t)fe << 23);
+      unsigned char* dst = q_s + tq * 128 * D * 2 + (rt & 127) * 128;
+#pragma unroll 1
+      for (int c0 = 0; c0 < C; c0 += H) {
+        if (C > H) get(c0);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            pc_ld32(s_t + 32 * c, v);
-            tmem_wait_ld();
-            if (edge) mask(c);
-            uint32_t w[16];
+        for (int i = 0; i < H; ++i) {
+          const uint32_t u[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = half2_bits_to_float2_rt(u[k], p.f16);
+            v[2 * k] = f.x * up;
+            v[2 * k + 1] = f.y * up;
+          }
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = pc_h2(v[pc_dim<BITS>(2 * k)], v[pc_dim<BITS>(2 * k + 1)]);
+          const int c = c0 + i;
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (rt & 7)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_full);
+      return p.qscale * __uint_as_float((uint32_t)(254 - fe) << 23);
+    };
+
+    const PcTile* t = tile_at(0);
+    float qmul_next = t != nullptr && t->n > 0 ? load_q(*t) : 0.f;
+    for (int k = 0; t != nullptr; ++k) {
+      const float qmul = qmul_next;
+      const int n = t->n, r = t->row0 + rt;
+      const bool real = r < t->s.rows;
+      const int seen = real ? paged_seen(p, t->s, r) : t->keys;
+      float m = -INFINITY, l = 0.f;
+      int kv = 0;
+      bool poison = false;
+      for (int j = 0; j < n; ++j) {
+        const uint32_t g = bc + j;
+        const PcInfo& f = sh.info[g % kPcInfo];
+        const int sb = NQ == 2 ? tq : (int)(g & 1);
+        const uint32_t s_t = tmem + lanes + 128 * sb;
+        wait(&sh.info_full[g % kPcInfo], g / kPcInfo);
+        wait(&sh.s_full[sb], NQ == 2 ? g : g >> 1);
+        tc_fence_after();
+        const float mult = qmul * f.kmul;
+        const int kv_new = j == 0 ? f.kv : max(kv, f.kv);
+        const uint32_t flags = f.flags;
+        const int left = seen - (t->j0 + j) * kPcKeys;   // keys of the block that the row sees
+        const bool edge = flags || __any_sync(0xffffffffu, left < kPcKeys);
+        // a score that the row does not see becomes -inf
+        auto mask = [&](float (&v)[16], int c) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (16 * c + i >= left) v[i] = -INFINITY;
+          if (flags) {
+            const uint32_t gone = f.gone[c >> 1] >> (16 * (c & 1)), bad = f.bad[c >> 1] >> (16 * (c & 1));
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 e = __ffma2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(mult, mult), make_float2(mm, mm));
-              const float2 x = make_float2(pc_ex2(e.x), pc_ex2(e.y));
-              sum = __fadd2_rn(sum, x);
-              w[i] = pc_h2(x.x, x.y);
+              if ((gone >> i) & 1u) v[i] = -INFINITY;
+              else if (((bad >> i) & 1u) && 16 * c + i < left) poison = true;
             }
-            tmem_st16(s_t + 16 * c, w);   // over scores that this thread has already read
           }
-          l += sum.x + sum.y;
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sh.p_full[sb]);
-            mbar_arrive(&sh.info_empty[g % kPcInfo]);
-          }
-        }
-        // ---- the row's result
-        const bool whole = j0 == 0 && j1 == nblk;
-        float scale = 0.f;
-        if (n > 0) {
-          if (NQ == 2) {
-            mbar_wait_bounded(&sh.s_full[tq], (sc + n) & 1, abort, p.err, 1u);
-          } else {
-            const uint32_t g = bc + n - 1;
-            mbar_wait_bounded(&sh.pv_done[g & 1], (g >> 1) & 1, abort, p.err, 1u);
-          }
-          tc_fence_after();
-          if (poison) l = __uint_as_float(0x7fc00000u);
-          scale = pc_ex2((float)kv) * (whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
-        }
-        const size_t slot = (size_t)(2 * cta + (mine ? 1 : 0)) * MT + rt;
-        uint4* out = reinterpret_cast<uint4*>(p.out + ((long long)(t.s.first + tok) * p.H + head) * D + part * DV);
-        float4* po = reinterpret_cast<float4*>(p.part_o + slot * DV);
-#pragma unroll 1
-        for (int c = 0; c < DV / 32; ++c) {
-          float v[32];
-          if (n > 0) {
-            pc_ld32(o_t + 32 * c, v);
+        };
+        // largest visible score of the row, times its scale (which is positive)
+        auto scan = [&](auto edged) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 8; c += 2) {
+            float v[2][16];
+            pc_ld16(s_t + 16 * c, v[0]);
+            pc_ld16(s_t + 16 * c + 16, v[1]);
             tmem_wait_ld();
-          } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          }
-          float o[32];
+            for (int x = 0; x < 2; ++x) {
+              if constexpr (decltype(edged)::value) mask(v[x], c + x);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float x = v[i];
-            o[(i & ~7) + pc_dim<BITS>(i & 7)] = m == -INFINITY && !poison ? 0.f : x * scale;
-          }
-          if (!real) continue;
-          if (whole) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float a = o[8 * k + 2 * i], b = o[8 * k + 2 * i + 1];
-                if (p.f16) {
-                  w[i] = pc_h2(a, b);
-                } else {
-                  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-                  w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-              }
-              out[4 * c + k] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int i = 0; i < 16; i += 2) top = fmaxf(top, fmaxf(v[x][i], v[x][i + 1]));
             }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) po[8 * c + k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           }
-        }
-        if (real && !whole) p.part_ml[slot] = make_float2(m, l);
-        tc_fence_before();
-      } else if (warp < W_MMA) {
-        // ======================================================================= codes -> fp16 tiles in shared memory
-        constexpr int CPR = SD * BITS / 128;       // 16-byte pieces of codes per row of a slot
-        constexpr int NCH = 128 * CPR / (kPcDeq * 32);
-        constexpr int DPC = 128 / BITS;            // dimensions per piece
-        constexpr int W = D * BITS / 32;
-        const int id = tid - W_DEQ * 32;
-        uint4 code[NCH];
-        uint32_t sbv[NCH];                         // scale | bias << 16; both 0 where the key counts as zero
-        int gshift = 31 - __clz(p.GS);
-        const int items = n * (KSL + VSL);
-        // item x of the walk: block, keys or values, slice of the dimensions
-        auto what = [&](int x, int& j, bool& val, int& sl) {
-          if (x < KSL) {
-            j = 0;
-            val = false;
-            sl = x;
-            return;
-          }
-          const int y = x - KSL, per = KSL + VSL;
-          j = y / per;
-          int z = y - j * per;
-          if (j + 1 < n) {
-            val = z >= KSL;
-            sl = val ? z - KSL : z;
-            if (!val) ++j;
-          } else {
-            val = true;
-            sl = z;
-          }
+          return top * mult;
         };
-        auto load = [&](int x) {
-          int j, sl;
-          bool val;
-          what(x, j, val, sl);
-          const uint32_t g = bc + j;
-          mbar_wait_bounded(&sh.info_full[g % kPcInfo], (g / kPcInfo) & 1, abort, p.err, 1u);
-          const PcInfo& f = sh.info[g % kPcInfo];
-          const uint32_t* src = val ? p.vp : p.kp;
-          const uint16_t *ss = val ? p.vs : p.ks, *bs = val ? p.vb : p.kb;
-          const int d0 = val ? part * DV + sl * SD : sl * SD;
-#pragma unroll
-          for (int i = 0; i < NCH; ++i) {
-            const int at = i * (kPcDeq * 32) + id, row = at / CPR, q = at % CPR;
-            const int key = (j0 + j) * kPcKeys + row, pg = f.pg[row >> 4];
-            const bool ok = pg >= 0 && key < keys;
-            const long long pr = qda_pool_row(ok ? pg : 0, kvh, ok ? key & pmask : 0, Hkv, p.page_shift);
-            code[i] = __ldg(reinterpret_cast<const uint4*>(src + pr * W + d0 / (32 / BITS)) + q);
-            const long long si = pr * p.NG + ((d0 + q * DPC) >> gshift);
-            const uint32_t s = __ldg(ss + si), b = __ldg(bs + si);
-            sbv[i] = ok ? s | b << 16 : 0u;
-          }
-        };
-        if (items > 0) load(0);
-        for (int x = 0; x < items; ++x) {
-          int j, sl;
-          bool val;
-          what(x, j, val, sl);
-          const uint32_t it = ic + x, slot = it % SLOTS, use = it / SLOTS;
-          const float fac = val ? sh.info[(bc + j) % kPcInfo].vfac : sh.info[(bc + j) % kPcInfo].kfac;
-          mbar_wait_bounded(&sh.empty[slot], (use & 1) ^ 1, abort, p.err, 1u);
-          const uint32_t dst = smem_addr(ring) + slot * G::SLOT;
-#pragma unroll
-          for (int i = 0; i < NCH; ++i) {
-            const int at = i * (kPcDeq * 32) + id, row = at / CPR, q = at % CPR;
-            float s = pc_half(sbv[i], p.f16), b = pc_half(sbv[i] >> 16, p.f16);
-            if (!(fmaf(fabsf(s), QMAX, fabsf(b)) < FINITE)) s = b = 0.f;
-            const float s24 = s * fac * 16777216.f, bf = b * fac;
-            const uint32_t s1 = pc_h2(s24, s24), s16 = pc_h2(s24 * 0.0625f, s24 * 0.0625f), b2 = pc_h2(bf, bf);
-            const uint32_t cw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-            constexpr int PP = DPC / 8;   // 16-byte pieces of operand values
-            // the order of the pieces differs between the halves of a row, so that eight lanes' stores meet all banks
-            const int turn = SD == 128 ? (BITS == 4 ? (q >= 2 ? 2 : 0) : (q >= 4 ? 1 : 0)) : 0;
-#pragma unroll
-            for (int k = 0; k < PP; ++k) {
-              uint32_t y[4];
-              if constexpr (BITS == 4) {
-                const uint32_t w = turn ? cw[k ^ 2] : cw[k];
-                const uint32_t w8 = w >> 8;
-                y[0] = pc_fma2(w & 0x000F000Fu, s1, b2);
-                y[1] = pc_fma2(w & 0x00F000F0u, s16, b2);
-                y[2] = pc_fma2(w8 & 0x000F000Fu, s1, b2);
-                y[3] = pc_fma2(w8 & 0x00F000F0u, s16, b2);
-              } else {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t w = turn ? cw[2 * (k ^ 1) + h] : cw[2 * k + h];
-                  y[2 * h] = pc_fma2(w & 0x00FF00FFu, s1, b2);
-                  y[2 * h + 1] = pc_fma2((w >> 8) & 0x00FF00FFu, s1, b2);
-                }
-              }
-              const int piece = q * PP + (k ^ turn);
-              const uint32_t a = dst + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                           : "memory");
-            }
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sh.full[slot]);
-            if (val && sl == VSL - 1) mbar_arrive(&sh.info_empty[(bc + j) % kPcInfo]);
-          }
-          if (x + 1 < items) load(x + 1);
-        }
-      } else if (warp == W_MMA) {
-        // ============================================================================== one thread issues the products
-        if (lane == 0 && n > 0) {
-          const uint32_t id_qk = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | (8u << 24);                // M 128, N 128
-          const uint32_t id_pv = (1u << 4) | (1u << 16) | ((uint32_t)(SD >> 3) << 17) | (8u << 24);   // M 128, N SD, B along N
-          const uint32_t ring_a = smem_addr(ring), q_a = smem_addr(q_s);
-          auto wait_slot = [&](uint32_t it) {
-            mbar_wait_bounded(&sh.full[it % SLOTS], (it / SLOTS) & 1, abort, p.err, 1u);
-            tc_fence_after();
-          };
-          // scores of tile tq from key slice sl in slot it
-          auto qk = [&](int tq, int sl, uint32_t it, uint32_t d) {
-#pragma unroll
-            for (int k = 0; k < SD / 16; ++k) {
-              const uint32_t off = (k >> 2) * 16384 + (k & 3) * 32;
-              pc_mma_ss(d, pc_desc(q_a + tq * 128 * D * 2 + sl * 2 * 16384 + off, 16),
-                        pc_desc(ring_a + (it % SLOTS) * G::SLOT + off, 16), id_qk, sl > 0 || k > 0);
-            }
-          };
-          // O (+)= P V for value slice sl in slot it
-          auto pv = [&](int sl, uint32_t it, uint32_t pt, uint32_t d, bool acc) {
-#pragma unroll
-            for (int k = 0; k < kPcKeys / 16; ++k)
-              mma_f16_ts(d + sl * SD, pt + 8 * k, pc_desc(ring_a + (it % SLOTS) * G::SLOT + k * 2048, 16384), id_pv,
-                         acc || k > 0);
-          };
-          mbar_wait_bounded(&sh.q_full, tc & 1, abort, p.err, 1u);
-          tc_fence_after();
-          if constexpr (NQ == 2) {
-            wait_slot(it_k(0));
-            for (int tq = 0; tq < 2; ++tq) {
-              qk(tq, 0, it_k(0), tmem + 128 * tq);
-              if (tq == 1) mma_commit(&sh.empty[it_k(0) % SLOTS]);
-              mma_commit(&sh.s_full[tq]);
-            }
-            for (int j = 0; j < n; ++j) {
-              for (int tq = 0; tq < 2; ++tq) {
-                if (tq == 0) wait_slot(it_v(j));
-                mbar_wait_bounded(&sh.p_full[tq], (bc + j) & 1, abort, p.err, 1u);
-                tc_fence_after();
-                pv(0, it_v(j), tmem + 128 * tq, tmem + G::O_COL + tq * DV, j > 0);
-                if (tq == 1) mma_commit(&sh.empty[it_v(j) % SLOTS]);
-                if (j + 1 < n) {
-                  if (tq == 0) wait_slot(it_k(j + 1));
-                  qk(tq, 0, it_k(j + 1), tmem + 128 * tq);
-                  if (tq == 1) mma_commit(&sh.empty[it_k(j + 1) % SLOTS]);
-                }
-                mma_commit(&sh.s_full[tq]);   // the next scores are there, and this block's values in O
-              }
-            }
-          } else {
-            auto scores = [&](int j) {
-              const uint32_t sb = (bc + j) & 1;
-              for (int sl = 0; sl < KSL; ++sl) {
-                wait_slot(it_k(j) + sl);
-                qk(0, sl, it_k(j) + sl, tmem + 128 * sb);
-                mma_commit(&sh.empty[(it_k(j) + sl) % SLOTS]);
-              }
-              mma_commit(&sh.s_full[sb]);
-            };
-            scores(0);
-            for (int j = 0; j < n; ++j) {
-              const uint32_t g = bc + j;
-              if (j + 1 < n) scores(j + 1);
-              mbar_wait_bounded(&sh.p_full[g & 1], (g >> 1) & 1, abort, p.err, 1u);
+        // a new reference (and unit) for the row's sums: O is rescaled with them
+        auto rescale = [&](float top) {
+          const float mn = fmaxf(m, top);
+          const float a = mn == -INFINITY ? 1.f : pc_ex2(m - mn);
+          m = mn;
+          l *= a;
+          if (j > 0) {
+            if (NQ == 1) {   // the last block's values are in O (with two tiles the scores' barrier says so)
+              wait(&sh.pv_done[(g - 1) & 1], (g - 1) >> 1);
               tc_fence_after();
-              for (int sl = 0; sl < VSL; ++sl) {
-                wait_slot(it_v(j) + sl);
-                pv(sl, it_v(j) + sl, tmem + 128 * (g & 1), tmem + G::O_COL, j > 0);
-                mma_commit(&sh.empty[(it_v(j) + sl) % SLOTS]);
-              }
-              mma_commit(&sh.pv_done[g & 1]);
+            }
+            const float x = a * pc_ex2((float)(kv - kv_new));
+#pragma unroll 1
+            for (int c = 0; c < DV / 16; ++c) {
+              float v[16];
+              pc_ld16(o_t + 16 * c, v);
+              tmem_wait_ld();
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * x);
+              tmem_st16(o_t + 16 * c, w);
             }
           }
-        }
-        __syncwarp();
-      } else {
-        // ========================================================== pages and magnitudes of the blocks, a block ahead
-        const int* tab = p.table + (size_t)t.b * p.max_pages;
-        auto page_of = [&](int j) {   // lanes 0-7: the page of 16 keys
-          const int k = (j0 + j) * kPcKeys + 16 * lane;
-          return lane < 8 && j < n && k < keys ? __ldg(tab + (k >> p.page_shift)) : -1;
+          kv = kv_new;
         };
-        int next = n > 0 ? page_of(0) : -1;
-        int kv_run = -126;
-        const int nvec = 16 * p.NG;   // 16-byte pieces per array
-        for (int j = 0; j < n; ++j) {
-          const uint32_t g = bc + j;
-          PcInfo& f = sh.info[g % kPcInfo];
-          const int key0 = (j0 + j) * kPcKeys;
-          int pg = next;
-          next = page_of(j + 1);
-          const bool asked = lane < 8 && key0 + 16 * lane < keys;
-          const bool gone = asked && (unsigned)pg >= (unsigned)p.num_pages;
-          if (gone) pg = -1;
-          const uint32_t gone8 = __ballot_sync(0xffffffffu, gone);
-          if (gone8 && lane == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);
-          mbar_wait_bounded(&sh.info_empty[g % kPcInfo], ((g / kPcInfo) & 1) ^ 1, abort, p.err, 1u);
-          if (lane < 8) f.pg[lane] = pg;
-          if (lane < 4) {
-            f.gone[lane] = ((gone8 >> (2 * lane)) & 1u ? 0xffffu : 0u) | ((gone8 >> (2 * lane + 1)) & 1u ? 0xffff0000u : 0u);
-            f.bad[lane] = 0u;
+        uint32_t w[64];   // the row's weights, stored only when they are final: they lie over its scores
+        float sum = 0.f;
+        // weights against the present reference; returns the largest score as scan does
+        auto weigh = [&](auto edged) {
+          const float mm = m == -INFINITY ? 0.f : -m;
+          float2 s2 = make_float2(0.f, 0.f);
+          float top = -INFINITY;
+          float v[2][16];
+          pc_ld16(s_t, v[0]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            tmem_wait_ld();
+            if (c + 1 < 8) pc_ld16(s_t + 16 * (c + 1), v[(c + 1) & 1]);
+            float (&u)[16] = v[c & 1];
+            if constexpr (decltype(edged)::value) mask(u, c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              top = fmaxf(top, fmaxf(u[2 * i], u[2 * i + 1]));
+              const float2 e = __ffma2_rn(make_float2(u[2 * i], u[2 * i + 1]), make_float2(mult, mult), make_float2(mm, mm));
+              const float2 x = make_float2(pc_ex2(e.x), pc_ex2(e.y));
+              s2 = __fadd2_rn(s2, x);
+              w[8 * c + i] = pc_h2(x.x, x.y);
+            }
+          }
+          sum = s2.x + s2.y;
+          return top * mult;
+        };
+        if (edge) {
+          if (j == 0 || kv_new != kv) {
+            if (j == 0) kv = kv_new;
+            rescale(scan(std::true_type{}));
+          }
+          const float top = weigh(std::true_type{});
+          if (__any_sync(0xffffffffu, top > m + 8.f)) {
+            rescale(top);
+            weigh(std::true_type{});
+          }
+        } else {
+          if (j == 0 || kv_new != kv) {
+            if (j == 0) kv = kv_new;
+            rescale(scan(std::false_type{}));
+          }
+          const float top = weigh(std::false_type{});
+          if (__any_sync(0xffffffffu, top > m + 8.f)) {
+            rescale(top);
+            weigh(std::false_type{});
+          }
+        }
+        l += sum;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t x[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = w[16 * c + i];
+          tmem_st16(s_t + 16 * c, x);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.p_full[sb]);
+          mbar_arrive(&sh.info_empty[g % kPcInfo]);
+        }
+      }
+      // the next tile's queries, while the last values are summed: every score of this tile is done
+      const PcTile* next = tile_at(k + 1);
+      qmul_next = next != nullptr && next->n > 0 ? load_q(*next) : 0.f;
+      // ---- the row's result
+      float scale = 0.f;
+      if (n > 0) {
+        const uint32_t g = bc + n - 1;
+        if (NQ == 2) wait(&sh.pv_done[tq], tc);
+        else wait(&sh.pv_done[g & 1], g >> 1);
+        tc_fence_after();
+        if (poison) l = __uint_as_float(0x7fc00000u);
+        scale = pc_ex2((float)kv) * (t->whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
+      }
+      const bool whole = t->whole;
+      const bool none = m == -INFINITY && !poison;   // the row saw no key
+      const int tok = r / p.nrep;
+      const size_t slot = (size_t)(2 * cta + t->mine) * MT + rt;
+      uint4* out = reinterpret_cast<uint4*>(
+          p.out + ((long long)(t->s.first + tok) * p.H + t->kvh * p.nrep + (r - tok * p.nrep)) * D + t->part * DV);
+      float4* po = reinterpret_cast<float4*>(p.part_o + slot * DV);
+#pragma unroll 1
+      for (int c = 0; c < DV / 32; ++c) {
+        float v[2][16];
+        if (n > 0) {
+          pc_ld16(o_t + 32 * c, v[0]);
+          pc_ld16(o_t + 32 * c + 16, v[1]);
+          tmem_wait_ld();
+        }
+        float o[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[(i & ~7) + pc_dim<BITS>(i & 7)] = none ? 0.f : v[i >> 4][i & 15] * scale;
+        if (!real) continue;
+        if (whole) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = o[8 * x + 2 * i], b = o[8 * x + 2 * i + 1];
+              if (p.f16) {
+                y[i] = pc_h2(a, b);
+              } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+                y[i] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+            }
+            out[4 * c + x] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) po[8 * c + x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        }
+      }
+      if (real && !whole) p.part_ml[slot] = make_float2(m, l);
+      tc_fence_before();
+      bc += n;
+      tc += n > 0;
+      tile_done(k);
+      t = next;
+    }
+  } else if (warp < W_MMA) {
+    // ========================================================================= codes -> fp16 tiles in shared memory
+    pc_regs_down<G::R_DEQ>();
+    constexpr int CPR = SD * BITS / 128;       // 16-byte pieces of codes per row of a slot
+    constexpr int NCH = 128 * CPR / (kPcDeq * 32);
+    constexpr int DPC = 128 / BITS;            // dimensions per piece
+    constexpr int W = D * BITS / 32;
+    constexpr int AHEAD = G::AHEAD;            // items whose codes are under way
+    const int id = tid - W_DEQ * 32;
+    const int gshift = 31 - __clz(p.GS);
+    struct Item {
+      uint4 code[NCH];
+      uint32_t sb[NCH];                        // scale | bias << 16; both 0 where the key counts as zero
+    };
+    Item reg[AHEAD + 1];
+    for (int k = 0;; ++k) {
+      const PcTile* t = tile_at(k);
+      if (t == nullptr) break;
+      const int n = t->n, items = n * (KSL + VSL);
+      int kv_run = -126;
+      // item x of the walk: block, keys or values, slice of the dimensions
+      auto what = [&](int x, int& j, bool& val, int& sl) {
+        const int y = x - KSL;
+        if (y < 0) {
+          j = 0;
+          val = false;
+          sl = x;
+          return;
+        }
+        j = y / (KSL + VSL);
+        const int z = y - j * (KSL + VSL);
+        if (j + 1 < n) {
+          val = z >= KSL;
+          sl = val ? z - KSL : z;
+          if (!val) ++j;
+        } else {
+          val = true;
+          sl = z;
+        }
+      };
+      auto load = [&](int x, Item& to) {
+        int j, sl;
+        bool val;
+        what(x, j, val, sl);
+        const uint32_t g = bc + j;
+        wait(&sh.info_full[g % kPcInfo], g / kPcInfo);
+        const PcInfo& f = sh.info[g % kPcInfo];
+        const uint32_t* src = val ? p.vp : p.kp;
+        const uint16_t *ss = val ? p.vs : p.ks, *bs = val ? p.vb : p.kb;
+        const int d0 = val ? t->part * DV + sl * SD : sl * SD;
+        const int key0 = (t->j0 + j) * kPcKeys;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          const int at = i * (kPcDeq * 32) + id, row = at / CPR, q = at % CPR;
+          const int pg = f.pg[row >> 4];
+          const bool ok = pg >= 0 && key0 + row < t->keys;
+          const long long pr = qda_pool_row(ok ? pg : 0, t->kvh, ok ? (key0 + row) & pmask : 0, Hkv, p.page_shift);
+          to.code[i] = __ldg(reinterpret_cast<const uint4*>(src + pr * W + d0 / (32 / BITS)) + q);
+          const long long si = pr * p.NG + ((d0 + q * DPC) >> gshift);
+          to.sb[i] = ok ? (uint32_t)__ldg(ss + si) | (uint32_t)__ldg(bs + si) << 16 : 0u;
+        }
+      };
+      auto convert = [&](int x, const Item& it) {
+        int j, sl;
+        bool val;
+        what(x, j, val, sl);
+        const uint32_t at0 = ic + x, slot = at0 % SLOTS;
+        if (val) kv_run = max(kv_run, sh.info[(bc + j) % kPcInfo].kv);
+        const float fac = val ? __uint_as_float((uint32_t)(127 - kv_run) << 23) : sh.info[(bc + j) % kPcInfo].kfac;
+        wait(&sh.empty[slot], at0 / SLOTS + 1);
+        const uint32_t dst = smem_addr(ring) + slot * G::SLOT;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          const int at = i * (kPcDeq * 32) + id, row = at / CPR, q = at % CPR;
+          float s = pc_half(it.sb[i], p.f16), b = pc_half(it.sb[i] >> 16, p.f16);
+          if (!(fmaxf(fabsf(s), fabsf(b)) < FINITE)) s = b = 0.f;   // not finite (the info's flags say so)
+          const float s24 = s * fac * 16777216.f, bf = b * fac;
+          const uint32_t s1 = pc_h2(s24, s24), s16 = pc_h2(s24 * 0.0625f, s24 * 0.0625f), b2 = pc_h2(bf, bf);
+          const uint32_t cw[4] = {it.code[i].x, it.code[i].y, it.code[i].z, it.code[i].w};
+          constexpr int PP = DPC / 8;   // 16-byte pieces of operand values
+          // the order of the pieces differs between the halves of a row, so that eight lanes' stores meet all banks
+          const int turn = SD == 128 ? (BITS == 4 ? (q >= 2 ? 2 : 0) : (q >= 4 ? 1 : 0)) : 0;
+#pragma unroll
+          for (int u = 0; u < PP; ++u) {
+            uint32_t y[4];
+            if constexpr (BITS == 4) {
+              const uint32_t w = turn ? cw[u ^ 2] : cw[u];
+              const uint32_t w8 = w >> 8;
+              y[0] = pc_fma2(w & 0x000F000Fu, s1, b2);
+              y[1] = pc_fma2(w & 0x00F000F0u, s16, b2);
+              y[2] = pc_fma2(w8 & 0x000F000Fu, s1, b2);
+              y[3] = pc_fma2(w8 & 0x00F000F0u, s16, b2);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t w = turn ? cw[2 * (u ^ 1) + h] : cw[2 * u + h];
+                y[2 * h] = pc_fma2(w & 0x00FF00FFu, s1, b2);
+                y[2 * h + 1] = pc_fma2((w >> 8) & 0x00FF00FFu, s1, b2);
+              }
+            }
+            const int piece = q * PP + (u ^ turn);
+            const uint32_t a = dst + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                         : "memory");
+          }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.full[slot]);
+          if (val && sl == VSL - 1) mbar_arrive(&sh.info_empty[(bc + j) % kPcInfo]);
+        }
+      };
+#pragma unroll
+      for (int x = 0; x < AHEAD; ++x)
+        if (x < items) load(x, reg[x]);
+      for (int x0 = 0; x0 < items; x0 += AHEAD + 1) {
+#pragma unroll
+        for (int u = 0; u <= AHEAD; ++u) {
+          const int x = x0 + u;
+          if (x < items) {
+            if (x + AHEAD < items) load(x + AHEAD, reg[(u + AHEAD) % (AHEAD + 1)]);
+            convert(x, reg[u]);
+          }
+        }
+      }
+      bc += n;
+      ic += items;
+      tile_done(k);
+    }
+  } else {
+   pc_regs_down<G::R_LAST>();
+   if (warp == W_MMA) {
+    // ================================================================================ one thread issues the products
+    constexpr uint32_t ID_QK = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | (8u << 24);               // M 128, N 128
+    constexpr uint32_t ID_PV = (1u << 4) | (1u << 16) | ((uint32_t)(SD >> 3) << 17) | (8u << 24);   // M 128, N SD, B along N
+    const uint32_t one = pc_elect();
+    const uint32_t ring_a = smem_addr(ring), q_a = smem_addr(q_s);
+    for (int k = 0;; ++k) {
+      const PcTile* t = tile_at(k);
+      if (t == nullptr) break;
+      const int n = t->n;
+      if (n > 0) {
+        auto wait_slot = [&](uint32_t it) {
+          wait(&sh.full[it % SLOTS], it / SLOTS);
+          tc_fence_after();
+        };
+        // scores of tile tq from key slice sl in slot it: 32 bytes of K per product, 64 values per 128-byte row
+        auto qk = [&](int tq, int sl, uint32_t it, uint32_t d) {
+          const uint64_t a = pc_desc(q_a + tq * 128 * D * 2 + sl * 2 * 16384, 16);
+          const uint64_t b = pc_desc(ring_a + (it % SLOTS) * G::SLOT, 16);
+#pragma unroll
+          for (int x = 0; x < SD / 16; ++x) {
+            const uint32_t off = ((x >> 2) * 16384 + (x & 3) * 32) >> 4;
+            pc_mma_ss(one, d, a + off, b + off, ID_QK, sl > 0 || x > 0);
+          }
+        };
+        // O (+)= P V for value slice sl in slot it: 16 keys per product
+        auto pv = [&](int sl, uint32_t it, uint32_t pt, uint32_t d, bool acc) {
+          const uint64_t b = pc_desc(ring_a + (it % SLOTS) * G::SLOT, 16384);
+#pragma unroll
+          for (int x = 0; x < kPcKeys / 16; ++x) pc_mma_ts(one, d + sl * SD, pt + 8 * x, b + x * (2048 >> 4), ID_PV, acc || x > 0);
+        };
+        wait(&sh.q_full, tc);
+        tc_fence_after();
+        if constexpr (NQ == 2) {
+          wait_slot(it_k(0));
+          for (int tq = 0; tq < 2; ++tq) {
+            qk(tq, 0, it_k(0), tmem + 128 * tq);
+            if (tq == 1) pc_commit(one, &sh.empty[it_k(0) % SLOTS]);
+            pc_commit(one, &sh.s_full[tq]);
+          }
+          for (int j = 0; j < n; ++j) {
+#pragma unroll
+            for (int tq = 0; tq < 2; ++tq) {
+              if (tq == 0) wait_slot(it_v(j, n));
+              wait(&sh.p_full[tq], bc + j);
+              tc_fence_after();
+              pv(0, it_v(j, n), tmem + 128 * tq, tmem + G::O_COL + tq * DV, j > 0);
+              if (tq == 1) pc_commit(one, &sh.empty[it_v(j, n) % SLOTS]);
+              if (j + 1 < n) {
+                if (tq == 0) wait_slot(it_k(j + 1));
+                qk(tq, 0, it_k(j + 1), tmem + 128 * tq);
+                if (tq == 1) pc_commit(one, &sh.empty[it_k(j + 1) % SLOTS]);
+                pc_commit(one, &sh.s_full[tq]);   // the next scores are there, and this block's values in O
+              } else {
+                pc_commit(one, &sh.pv_done[tq]);
+              }
+            }
+          }
+        } else {
+          auto scores = [&](int j) {
+            const uint32_t g = bc + j;
+            for (int sl = 0; sl < KSL; ++sl) {
+              wait_slot(it_k(j) + sl);
+              qk(0, sl, it_k(j) + sl, tmem + 128 * (g & 1));
+              pc_commit(one, &sh.empty[(it_k(j) + sl) % SLOTS]);
+            }
+            pc_commit(one, &sh.s_full[g & 1]);
+          };
+          scores(0);
+          for (int j = 0; j < n; ++j) {
+            const uint32_t g = bc + j;
+            if (j + 1 < n) scores(j + 1);
+            wait(&sh.p_full[g & 1], g >> 1);
+            tc_fence_after();
+            for (int sl = 0; sl < VSL; ++sl) {
+              wait_slot(it_v(j, n) + sl);
+              pv(sl, it_v(j, n) + sl, tmem + 128 * (g & 1), tmem + G::O_COL, j > 0);
+              pc_commit(one, &sh.empty[(it_v(j, n) + sl) % SLOTS]);
+            }
+            pc_commit(one, &sh.pv_done[g & 1]);
+          }
+        }
+      }
+      __syncwarp();
+      bc += n;
+      ic += n * (KSL + VSL);
+      tc += n > 0;
+      tile_done(k);
+    }
+   } else {
+    // ================================================ the piece's tiles, and pages and magnitudes of the blocks, ahead
+    const int first = warp - W_MMA - 1;
+    const int nvec = 16 * p.NG;   // 16-byte pieces per array
+    bool more = true;             // first info warp: sh.t is a tile of this piece
+    for (int k = 0;; ++k) {
+      if (first == 0) {
+        // the next tile with work for this CTA
+        wait(&sh.tile_empty[k % kPcTiles], k / kPcTiles + 1);
+        PcTile& e = sh.tile[k % kPcTiles];
+        int n = -1;
+        while (more && n < 0) {
+          const PagedTile& t = sh.t;
+          const int keys = paged_tile_keys(p, t, MT);
+          const int nblk = (keys + kPcKeys - 1) / kPcKeys;
+          const int j0 = paged_block_at(t, nblk, sh.x[0]), j1 = paged_block_at(t, nblk, sh.x[1]);
+          const bool mine = sh.x[0] <= t.lo;   // the CTA that starts the tile writes it if it has no keys
+          if (j1 > j0 || (nblk == 0 && mine)) {
+            n = j1 - j0;
+            if (lane == 0) {
+              e.n = n;
+              e.j0 = j0;
+              e.keys = keys;
+              e.whole = j0 == 0 && j1 == nblk;
+              e.mine = mine;
+              e.row0 = t.i * MT;
+              e.kvh = t.unit / G::PARTS;
+              e.part = t.unit % G::PARTS;
+              e.b = t.b;
+              e.s = t.s;
+            }
           }
           __syncwarp();
-          float top[2] = {0.f, 0.f};
-          bool any_bad = false;
-#pragma unroll 2
+          if (lane == 0) sh.more = sh.x[1] > sh.t.hi && paged_tile_next(p, MT, sh.t);
+          __syncwarp();
+          more = sh.more != 0;
+          __syncwarp();
+        }
+        if (n < 0 && lane == 0) e.n = -1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.tile_full[k % kPcTiles]);
+      }
+      const PcTile* t = tile_at(k);
+      if (t == nullptr) break;
+      const int n = t->n, j0 = t->j0, keys = t->keys, kvh = t->kvh;
+      const int* tab = p.table + (size_t)t->b * p.max_pages;
+      auto page_of = [&](int j) {   // lanes 0-7: the page of 16 keys
+        const int key = (j0 + j) * kPcKeys + 16 * lane;
+        return lane < 8 && j < n && key < keys ? __ldg(tab + (key >> p.page_shift)) : -1;
+      };
+      int next = page_of(first);
+      for (int j = first; j < n; j += kPcInfoWarps) {
+        const uint32_t g = bc + j;
+        PcInfo& f = sh.info[g % kPcInfo];
+        const int key0 = (j0 + j) * kPcKeys;
+        int pg = next;
+        next = page_of(j + kPcInfoWarps);
+        const bool asked = lane < 8 && key0 + 16 * lane < keys;
+        const bool gone = asked && (unsigned)pg >= (unsigned)p.num_pages;
+        if (gone) pg = -1;
+        const uint32_t gone8 = __ballot_sync(0xffffffffu, gone);
+        if (gone8 && lane == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);
+        // largest 16-bit patterns of |scale| and |bias| of the block's keys and of its values: halves of a word each
+        uint32_t top[4] = {0u, 0u, 0u, 0u};
+        const bool cut = key0 + kPcKeys > keys;   // rows behind the sequence may hold anything
+        const uint32_t limit = p.f16 ? 0x7C00u : 0x7680u;   // fp16 infinity; 2^110 in bf16
+        bool odd = false;
+        auto visit = [&](auto&& each) {
           for (int v0 = 0; v0 < nvec; v0 += 32) {
             const int v = v0 + lane, g16 = min(v / (2 * p.NG), 7);
             const int pv = __shfl_sync(0xffffffffu, pg, g16);
             if (v < nvec && pv >= 0) {
-              const int piece = v - g16 * 2 * p.NG;
               const long long row = qda_pool_row(pv, kvh, (key0 + 16 * g16) & pmask, Hkv, p.page_shift);
+              const int piece = v - g16 * 2 * p.NG;
               const long long at = row * p.NG / 8 + piece;
               const uint4 a[4] = {__ldg(reinterpret_cast<const uint4*>(p.ks) + at), __ldg(reinterpret_cast<const uint4*>(p.kb) + at),
                                   __ldg(reinterpret_cast<const uint4*>(p.vs) + at), __ldg(reinterpret_cast<const uint4*>(p.vb) + at)};
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                const uint32_t su[4] = {a[2 * x].x, a[2 * x].y, a[2 * x].z, a[2 * x].w};
-                const uint32_t bu[4] = {a[2 * x + 1].x, a[2 * x + 1].y, a[2 * x + 1].z, a[2 * x + 1].w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int key = 16 * g16 + (piece * 8 + e) / p.NG;   // of the block
-                  const float s = pc_half(su[e >> 1] >> (16 * (e & 1)), p.f16), b = pc_half(bu[e >> 1] >> (16 * (e & 1)), p.f16);
-                  const float big = fmaf(fabsf(s), QMAX, fabsf(b));
-                  if (key0 + key >= keys) continue;
-                  if (big < FINITE) {
-                    top[x] = fmaxf(top[x], big);
-                  } else {
-                    atomicOr(&f.bad[key >> 5], 1u << (key & 31));
-                    any_bad = true;
-                  }
-                }
-              }
+              each(a, 16 * g16, piece);
             }
           }
-          const uint32_t tk = __reduce_max_sync(0xffffffffu, __float_as_uint(top[0]));
-          const uint32_t tv = __reduce_max_sync(0xffffffffu, __float_as_uint(top[1]));
-          any_bad = __any_sync(0xffffffffu, any_bad);
-          // largest magnitude to [2^T, 2^(T + 1)): the scale times 2^24 stays below 2^16
-          constexpr int T = BITS == 4 ? -6 : -3;
-          const int fk = max(1, min(254 + T - (int)(tk >> 23), 253)), fv = max(1, min(254 + T - (int)(tv >> 23), 253));
-          kv_run = max(kv_run, 127 - fv);
-          if (lane == 0) {
-            f.kfac = __uint_as_float((uint32_t)fk << 23);
-            f.kmul = __uint_as_float((uint32_t)(254 - fk) << 23);
-            f.kv = kv_run;
-            f.vfac = __uint_as_float((uint32_t)(127 - kv_run) << 23);
-            f.flags = (gone8 != 0) | (any_bad ? 2u : 0u);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.info_full[g % kPcInfo]);
+        };
+        visit([&](const uint4 (&a)[4], int key, int piece) {
+          if (cut) odd = odd || key0 + key + (piece * 8 + 7) / p.NG >= keys;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            top[x] = __vmaxu2(top[x], __vmaxu2(__vmaxu2(a[x].x & 0x7fff7fffu, a[x].y & 0x7fff7fffu),
+                                               __vmaxu2(a[x].z & 0x7fff7fffu, a[x].w & 0x7fff7fffu)));
+        });
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          top[x] = max(top[x] & 0xffffu, top[x] >> 16);
+          odd = odd || top[x] >= limit;
         }
+        uint32_t bad[4] = {0u, 0u, 0u, 0u};   // this lane's keys that are not finite
+        if (__any_sync(0xffffffffu, odd)) {    // one value at a time, without rows behind the sequence
+          top[0] = top[1] = top[2] = top[3] = 0u;
+          visit([&](const uint4 (&a)[4], int key, int piece) {
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+              const int at = key + (piece * 8 + e) / p.NG;
+              if (key0 + at >= keys) continue;
+              uint32_t u[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const uint32_t w = (e >> 1) == 0 ? a[x].x : (e >> 1) == 1 ? a[x].y : (e >> 1) == 2 ? a[x].z : a[x].w;
+                u[x] = (w >> (16 * (e & 1))) & 0x7fffu;
+              }
+              if (max(max(u[0], u[1]), max(u[2], u[3])) >= limit) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                  if ((at >> 5) == x) bad[x] |= 1u << (at & 31);
+              } else {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) top[x] = max(top[x], u[x]);
+              }
+            }
+          });
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          top[x] = __reduce_max_sync(0xffffffffu, top[x]);
+          bad[x] = __reduce_or_sync(0xffffffffu, bad[x]);
+        }
+        // no key (value) of the block is larger than scale * QMAX + bias of the largest ones: to [2^T, 2^(T + 1)), where
+        // a scale times 2^24 stays below 2^16
+        constexpr int T = BITS == 4 ? -6 : -3;
+        const uint32_t tk = __float_as_uint(fmaf(pc_half(top[0], p.f16), QMAX, pc_half(top[1], p.f16)));
+        const uint32_t tv = __float_as_uint(fmaf(pc_half(top[2], p.f16), QMAX, pc_half(top[3], p.f16)));
+        const int fk = max(1, min(254 + T - (int)(tk >> 23), 253)), fv = max(1, min(254 + T - (int)(tv >> 23), 253));
+        wait(&sh.info_empty[g % kPcInfo], g / kPcInfo + 1);
+        if (lane < 8) f.pg[lane] = pg;
+        if (lane < 4) {
+          f.gone[lane] = ((gone8 >> (2 * lane)) & 1u ? 0xffffu : 0u) | ((gone8 >> (2 * lane + 1)) & 1u ? 0xffff0000u : 0u);
+          f.bad[lane] = lane == 0 ? bad[0] : lane == 1 ? bad[1] : lane == 2 ? bad[2] : bad[3];
+        }
+        if (lane == 0) {
+          f.kfac = __uint_as_float((uint32_t)fk << 23);
+          f.kmul = __uint_as_float((uint32_t)(254 - fk) << 23);
+          f.kv = 127 - fv;
+          f.flags = (gone8 != 0) | ((bad[0] | bad[1] | bad[2] | bad[3]) ? 2u : 0u);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.info_full[g % kPcInfo]);
       }
-    }
-    if (n > 0) {
       bc += n;
-      ic += n * (KSL + VSL);
-      sc += n + 1;
-      ++tc;
+      if (first != 0) tile_done(k);
     }
-    __syncthreads();   // every warp is through with the tile
-    if (tid == 0) sh.more = sh.x[1] > sh.t.hi && paged_tile_next(p, MT, sh.t);
-    tc_fence_after();
-    __syncthreads();
-    if (!sh.more) break;
+   }
   }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   if (warp == W_MMA) {
     if (lane == 0) {   // no product is under way when the tensor memory goes back (after a wait that gave up some may be)
       volatile int none = 0;
