@@ -633,6 +633,7 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   if (st == QDA_OK) st = check_pool(num_pages, page);
   if (st != QDA_OK) return st;
   if (B > QDA_MAX_B || H / Hkv > QDA_MAX_NREP) return QDA_ERR_UNSUPPORTED;
+  if ((long long)num_pages * page * Hkv >= 0xffffffffLL) return QDA_ERR_UNSUPPORTED;   // pool rows are 32-bit
   const void* ptrs[8] = {q, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, out};
   for (const void* p : ptrs)
     if (off16(p)) return QDA_ERR_ALIGN;

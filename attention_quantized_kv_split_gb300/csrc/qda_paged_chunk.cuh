@@ -30,13 +30,14 @@
 namespace qda {
 
 constexpr int kPcKeys = 128;     // keys per block
-constexpr int kPcDeq = 8;        // dequantising warps
 constexpr int kPcInfo = 8;       // blocks of info in flight
 constexpr int kPcTiles = 4;      // tiles in flight
 constexpr int kPcInfoWarps = 3;  // info warps, taking blocks in turn (they fill up the last group of four warps)
 
+constexpr uint32_t kPcNoRow = 0xffffffffu;
+
 struct PcInfo {
-  int pg[8];              // page of each 16 keys (-1: none or absent)
+  uint32_t row[8];        // pool row of each 16 keys (kPcNoRow: behind the sequence or on an absent page)
   float kmul;             // what undoes the keys' scale
   float kfac;             // the keys' scale
   int kv;                 // 2^-kv scales this block's values so; the walk takes the largest kv up to here
@@ -57,11 +58,13 @@ struct PcGeom {
   static constexpr int SLOTS0 = (226 * 1024 - 1024 - QB) / SLOT;
   static constexpr int SLOTS = SLOTS0 > 6 ? 6 : SLOTS0;
   static constexpr int SOFT = 4 * NQ;                   // softmax warps
-  static constexpr int WARPS = SOFT + kPcDeq + 1 + kPcInfoWarps;
+  static constexpr int DEQ = 8;                         // dequantising warps
+  static constexpr int WARPS = SOFT + DEQ + 1 + kPcInfoWarps;
   // registers a thread: the launch's 96 (20 warps) or 128 (16 warps), dealt out anew among the warpgroups
-  static constexpr int R_SOFT = NQ == 2 ? 128 : 176, R_DEQ = NQ == 2 ? 88 : 120, R_LAST = NQ == 2 ? 48 : 80;
-  static_assert(SOFT * R_SOFT + kPcDeq * R_DEQ + 4 * R_LAST <= WARPS * (NQ == 2 ? 96 : 128), "registers of the launch");
-  static constexpr int AHEAD = BITS == 8 && NQ == 2 ? 1 : 2;   // items of codes under way: what the registers hold
+  static constexpr int R_ALL = NQ == 2 ? 96 : 128;
+  static constexpr int R_SOFT = NQ == 2 ? 152 : 168, R_DEQ = NQ == 2 ? 64 : 128, R_LAST = NQ == 2 ? 48 : 80;
+  static_assert(SOFT * R_SOFT + DEQ * R_DEQ + 4 * R_LAST <= WARPS * R_ALL, "registers of the launch");
+  static constexpr int AHEAD = NQ == 2 ? 1 : (BITS == 4 ? 3 : 2);   // items of codes under way: what the registers hold
   static constexpr int O_COL = 256;                     // O behind two S buffers of 128 columns
   static_assert(NQ == 1 || D <= 128, "two tiles need room for two O");
   static_assert(SLOTS >= 3 && O_COL + NQ * DV <= 512, "shared or tensor memory");
@@ -135,6 +138,21 @@ __device__ __forceinline__ void pc_commit(uint32_t one, uint64_t* bar) {
   if (one) mma_commit(bar);
 }
 
+__device__ __forceinline__ void pc_ld32(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 __device__ __forceinline__ void pc_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(
@@ -145,6 +163,21 @@ __device__ __forceinline__ void pc_ld16(uint32_t taddr, float (&v)[16]) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 8 columns of this thread's lane times x (rare; few registers, since the scores are being held)
+__device__ __forceinline__ void pc_scale8(uint32_t taddr, float x) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * x);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t pc_h2(float lo, float hi) {
@@ -166,19 +199,17 @@ __host__ __device__ constexpr int pc_dim(int i) {
 }
 
 // Register count of the calling warpgroup from here on (the sums over the warpgroups stay within the launch's).
-template <int N>
-__device__ __forceinline__ void pc_regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void pc_regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+template <int N, int LAUNCH>
+__device__ __forceinline__ void pc_regs() {
+  if constexpr (N > LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N < LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int D, int BITS, int NQ>
 __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     qda_paged_chunk_kernel(const __grid_constant__ QdaPagedParams p) {
   using G = PcGeom<D, BITS, NQ>;
+  constexpr int DEQ = G::DEQ;
   constexpr int MT = G::MT, SD = G::SD, DV = G::DV, KSL = G::KSL, VSL = G::VSL, SLOTS = G::SLOTS;
   constexpr float QMAX = (float)((1 << BITS) - 1);
   constexpr float FINITE = 1.2980742e33f;   // 2^110: a scale or bias this large counts as not finite
@@ -188,17 +219,17 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
   unsigned char* ring = base + G::QB;
   PcShared& sh = *reinterpret_cast<PcShared*>(ring + SLOTS * G::SLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int W_DEQ = G::SOFT, W_MMA = G::SOFT + kPcDeq;   // the info warps behind
+  constexpr int W_DEQ = G::SOFT, W_MMA = G::SOFT + DEQ;   // the info warps behind
   volatile int* abort = &sh.abort;
 
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < kPcInfo; ++i) {
       mbar_init(&sh.info_full[i], 1);
-      mbar_init(&sh.info_empty[i], G::SOFT + kPcDeq);
+      mbar_init(&sh.info_empty[i], G::SOFT + DEQ);
     }
     for (int i = 0; i < SLOTS; ++i) {
-      mbar_init(&sh.full[i], kPcDeq);
+      mbar_init(&sh.full[i], DEQ);
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < kPcTiles; ++i) {
@@ -253,7 +284,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
 
   if (warp < G::SOFT) {
     // =================================================================================== softmax: a thread per row
-    pc_regs_up<G::R_SOFT>();
+    pc_regs<G::R_SOFT, G::R_ALL>();
     const int tq = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int rt = tq * 128 + 32 * (warp & 3) + lane;   // row of the tile
@@ -337,39 +368,25 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         const int kv_new = j == 0 ? f.kv : max(kv, f.kv);
         const uint32_t flags = f.flags;
         const int left = seen - (t->j0 + j) * kPcKeys;   // keys of the block that the row sees
-        const bool edge = flags || __any_sync(0xffffffffu, left < kPcKeys);
-        // a score that the row does not see becomes -inf
-        auto mask = [&](float (&v)[16], int c) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (16 * c + i >= left) v[i] = -INFINITY;
-          if (flags) {
+        const bool edge = __any_sync(0xffffffffu, left < kPcKeys);
+        if (flags) {   // rare: keys on absent pages are hidden; who sees a key that is not finite becomes NaN
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
             const uint32_t gone = f.gone[c >> 1] >> (16 * (c & 1)), bad = f.bad[c >> 1] >> (16 * (c & 1));
+            float v[16];
+            pc_ld16(s_t + 16 * c, v);
+            tmem_wait_ld();
+            uint32_t y[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              if ((gone >> i) & 1u) v[i] = -INFINITY;
-              else if (((bad >> i) & 1u) && 16 * c + i < left) poison = true;
+              const bool no = (gone >> i) & 1u;
+              if (!no && ((bad >> i) & 1u) && 16 * c + i < left) poison = true;
+              y[i] = no ? 0xff800000u : __float_as_uint(v[i]);
             }
+            tmem_st16(s_t + 16 * c, y);
           }
-        };
-        // largest visible score of the row, times its scale (which is positive)
-        auto scan = [&](auto edged) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 8; c += 2) {
-            float v[2][16];
-            pc_ld16(s_t + 16 * c, v[0]);
-            pc_ld16(s_t + 16 * c + 16, v[1]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if constexpr (decltype(edged)::value) mask(v[x], c + x);
-#pragma unroll
-              for (int i = 0; i < 16; i += 2) top = fmaxf(top, fmaxf(v[x][i], v[x][i + 1]));
-            }
-          }
-          return top * mult;
-        };
+          tmem_wait_st();
+        }
         // a new reference (and unit) for the row's sums: O is rescaled with them
         auto rescale = [&](float top) {
           const float mn = fmaxf(m, top);
@@ -383,74 +400,45 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
             }
             const float x = a * pc_ex2((float)(kv - kv_new));
 #pragma unroll 1
-            for (int c = 0; c < DV / 16; ++c) {
-              float v[16];
-              pc_ld16(o_t + 16 * c, v);
-              tmem_wait_ld();
-              uint32_t w[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i] * x);
-              tmem_st16(o_t + 16 * c, w);
-            }
+            for (int c = 0; c < DV / 8; ++c) pc_scale8(o_t + 8 * c, x);
           }
           kv = kv_new;
         };
-        uint32_t w[64];   // the row's weights, stored only when they are final: they lie over its scores
-        float sum = 0.f;
-        // weights against the present reference; returns the largest score as scan does
-        auto weigh = [&](auto edged) {
-          const float mm = m == -INFINITY ? 0.f : -m;
-          float2 s2 = make_float2(0.f, 0.f);
-          float top = -INFINITY;
-          float v[2][16];
-          pc_ld16(s_t, v[0]);
+        float v[4][32];   // the row's scores
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            tmem_wait_ld();
-            if (c + 1 < 8) pc_ld16(s_t + 16 * (c + 1), v[(c + 1) & 1]);
-            float (&u)[16] = v[c & 1];
-            if constexpr (decltype(edged)::value) mask(u, c);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              top = fmaxf(top, fmaxf(u[2 * i], u[2 * i + 1]));
-              const float2 e = __ffma2_rn(make_float2(u[2 * i], u[2 * i + 1]), make_float2(mult, mult), make_float2(mm, mm));
-              const float2 x = make_float2(pc_ex2(e.x), pc_ex2(e.y));
-              s2 = __fadd2_rn(s2, x);
-              w[8 * c + i] = pc_h2(x.x, x.y);
-            }
-          }
-          sum = s2.x + s2.y;
-          return top * mult;
-        };
+        for (int c = 0; c < 4; ++c) pc_ld32(s_t + 32 * c, v[c]);
+        tmem_wait_ld();
         if (edge) {
-          if (j == 0 || kv_new != kv) {
-            if (j == 0) kv = kv_new;
-            rescale(scan(std::true_type{}));
-          }
-          const float top = weigh(std::true_type{});
-          if (__any_sync(0xffffffffu, top > m + 8.f)) {
-            rescale(top);
-            weigh(std::true_type{});
-          }
-        } else {
-          if (j == 0 || kv_new != kv) {
-            if (j == 0) kv = kv_new;
-            rescale(scan(std::false_type{}));
-          }
-          const float top = weigh(std::false_type{});
-          if (__any_sync(0xffffffffu, top > m + 8.f)) {
-            rescale(top);
-            weigh(std::false_type{});
-          }
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= left) v[i >> 5][i & 31] = -INFINITY;
         }
-        l += sum;
+        float top4[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          uint32_t x[16];
+          top4[c] = v[c][0];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = w[16 * c + i];
-          tmem_st16(s_t + 16 * c, x);
+          for (int i = 1; i < 31; i += 2) top4[c] = fmaxf(top4[c], fmaxf(v[c][i], v[c][i + 1]));
+          top4[c] = fmaxf(top4[c], v[c][31]);
         }
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * mult;   // mult > 0
+        if (j == 0) kv = kv_new;
+        if (__any_sync(0xffffffffu, top > m + 8.f) || kv_new != kv) rescale(top);
+        const float mm = m == -INFINITY ? 0.f : -m;
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = __ffma2_rn(make_float2(v[c][2 * i], v[c][2 * i + 1]), make_float2(mult, mult), make_float2(mm, mm));
+            const float2 x = make_float2(pc_ex2(e.x), pc_ex2(e.y));
+            sum[i & 1] = __fadd2_rn(sum[i & 1], x);
+            w[i] = pc_h2(x.x, x.y);
+          }
+          tmem_st16(s_t + 16 * c, w);   // over the scores, which are in registers
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -521,17 +509,29 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     }
   } else if (warp < W_MMA) {
     // ========================================================================= codes -> fp16 tiles in shared memory
-    pc_regs_down<G::R_DEQ>();
-    constexpr int CPR = SD * BITS / 128;       // 16-byte pieces of codes per row of a slot
-    constexpr int NCH = 128 * CPR / (kPcDeq * 32);
-    constexpr int DPC = 128 / BITS;            // dimensions per piece
-    constexpr int W = D * BITS / 32;
+    pc_regs<G::R_DEQ, G::R_ALL>();
+    constexpr int UPR = SD / 32;               // units of 32 codes (which share a scale) per row of a slot
+    constexpr int NU = 128 * UPR / (DEQ * 32);
+    constexpr int UW = BITS;                   // words of codes per unit
+    constexpr int ROWB = D * BITS / 8;         // bytes of codes per row
     constexpr int AHEAD = G::AHEAD;            // items whose codes are under way
     const int id = tid - W_DEQ * 32;
+    const int row = id / UPR, q = id % UPR;    // this thread's units: unit q of rows row, row + threads / UPR, ...
     const int gshift = 31 - __clz(p.GS);
+    const uint32_t sstride = p.NG * 2;
+    // where a unit's four 16-byte pieces of operand go in a slot: rows of 64 values, pieces XORed by the row. The order of the
+    // pieces differs between the halves of a row, so that eight lanes' stores meet all banks
+    const int turn = UPR == 4 && q >= 2 ? 2 : 0;
+    uint32_t to[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int piece = q * 4 + (u ^ turn);
+      to[u] = (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+    }
     struct Item {
-      uint4 code[NCH];
-      uint32_t sb[NCH];                        // scale | bias << 16; both 0 where the key counts as zero
+      uint32_t code[NU][UW];
+      uint32_t s[NU], b[NU];                   // as they are in memory: nothing waits for a load before its item's turn
+      uint32_t ok;                             // bit per unit: the key counts (else it is zero)
     };
     Item reg[AHEAD + 1];
     for (int k = 0;; ++k) {
@@ -559,26 +559,37 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           sl = z;
         }
       };
-      auto load = [&](int x, Item& to) {
+      auto load = [&](int x, Item& it) {
         int j, sl;
         bool val;
         what(x, j, val, sl);
         const uint32_t g = bc + j;
         wait(&sh.info_full[g % kPcInfo], g / kPcInfo);
         const PcInfo& f = sh.info[g % kPcInfo];
-        const uint32_t* src = val ? p.vp : p.kp;
-        const uint16_t *ss = val ? p.vs : p.ks, *bs = val ? p.vb : p.kb;
-        const int d0 = val ? t->part * DV + sl * SD : sl * SD;
-        const int key0 = (t->j0 + j) * kPcKeys;
+        const int d0 = (val ? t->part * DV : 0) + sl * SD + 32 * q;
+        const char* src = reinterpret_cast<const char*>(val ? p.vp : p.kp) + d0 * BITS / 8;
+        const char* ss = reinterpret_cast<const char*>(val ? p.vs : p.ks) + (d0 >> gshift) * 2;
+        const char* bs = reinterpret_cast<const char*>(val ? p.vb : p.kb) + (d0 >> gshift) * 2;
+        const int left = t->keys - (t->j0 + j) * kPcKeys;
+        it.ok = 0;
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          const int at = i * (kPcDeq * 32) + id, row = at / CPR, q = at % CPR;
-          const int pg = f.pg[row >> 4];
-          const bool ok = pg >= 0 && key0 + row < t->keys;
-          const long long pr = qda_pool_row(ok ? pg : 0, t->kvh, ok ? (key0 + row) & pmask : 0, Hkv, p.page_shift);
-          to.code[i] = __ldg(reinterpret_cast<const uint4*>(src + pr * W + d0 / (32 / BITS)) + q);
-          const long long si = pr * p.NG + ((d0 + q * DPC) >> gshift);
-          to.sb[i] = ok ? (uint32_t)__ldg(ss + si) | (uint32_t)__ldg(bs + si) << 16 : 0u;
+        for (int i = 0; i < NU; ++i) {
+          const int r = row + i * ((DEQ * 32 / UPR));
+          const uint32_t base = f.row[r >> 4];
+          const bool ok = base != kPcNoRow && r < left;
+          const uint32_t pr = ok ? base + (r & 15) : 0u;
+          const uint4* c = reinterpret_cast<const uint4*>(src + (uint64_t)pr * ROWB);
+#pragma unroll
+          for (int u = 0; u < UW / 4; ++u) {
+            const uint4 v = __ldg(c + u);
+            it.code[i][4 * u] = v.x;
+            it.code[i][4 * u + 1] = v.y;
+            it.code[i][4 * u + 2] = v.z;
+            it.code[i][4 * u + 3] = v.w;
+          }
+          it.s[i] = __ldg(reinterpret_cast<const uint16_t*>(ss + (uint64_t)pr * sstride));
+          it.b[i] = __ldg(reinterpret_cast<const uint16_t*>(bs + (uint64_t)pr * sstride));
+          it.ok |= (uint32_t)ok << i;
         }
       };
       auto convert = [&](int x, const Item& it) {
@@ -586,26 +597,31 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         bool val;
         what(x, j, val, sl);
         const uint32_t at0 = ic + x, slot = at0 % SLOTS;
-        if (val) kv_run = max(kv_run, sh.info[(bc + j) % kPcInfo].kv);
-        const float fac = val ? __uint_as_float((uint32_t)(127 - kv_run) << 23) : sh.info[(bc + j) % kPcInfo].kfac;
+        const PcInfo& f = sh.info[(bc + j) % kPcInfo];
+        if (val) kv_run = max(kv_run, f.kv);
+        const float fac = val ? __uint_as_float((uint32_t)(127 - kv_run) << 23) : f.kfac;
+        const bool odd = f.flags & 2u;
         wait(&sh.empty[slot], at0 / SLOTS + 1);
         const uint32_t dst = smem_addr(ring) + slot * G::SLOT;
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          const int at = i * (kPcDeq * 32) + id, row = at / CPR, q = at % CPR;
-          float s = pc_half(it.sb[i], p.f16), b = pc_half(it.sb[i] >> 16, p.f16);
-          if (!(fmaxf(fabsf(s), fabsf(b)) < FINITE)) s = b = 0.f;   // not finite (the info's flags say so)
-          const float s24 = s * fac * 16777216.f, bf = b * fac;
-          const uint32_t s1 = pc_h2(s24, s24), s16 = pc_h2(s24 * 0.0625f, s24 * 0.0625f), b2 = pc_h2(bf, bf);
-          const uint32_t cw[4] = {it.code[i].x, it.code[i].y, it.code[i].z, it.code[i].w};
-          constexpr int PP = DPC / 8;   // 16-byte pieces of operand values
-          // the order of the pieces differs between the halves of a row, so that eight lanes' stores meet all banks
-          const int turn = SD == 128 ? (BITS == 4 ? (q >= 2 ? 2 : 0) : (q >= 4 ? 1 : 0)) : 0;
+        for (int i = 0; i < NU; ++i) {
+          float s, b;
+          if (p.f16) {
+            s = fp16_bits_to_float(it.s[i]);
+            b = fp16_bits_to_float(it.b[i]);
+          } else {
+            s = __uint_as_float(it.s[i] << 16);
+            b = __uint_as_float(it.b[i] << 16);
+          }
+          if (!((it.ok >> i) & 1u) || (odd && !(fmaxf(fabsf(s), fabsf(b)) < FINITE))) s = b = 0.f;
+          s *= fac;
+          b *= fac;
+          const uint32_t s1 = pc_h2(s * 16777216.f, s * 16777216.f), s16 = pc_h2(s * 1048576.f, s * 1048576.f), b2 = pc_h2(b, b);
 #pragma unroll
-          for (int u = 0; u < PP; ++u) {
+          for (int u = 0; u < 4; ++u) {
             uint32_t y[4];
             if constexpr (BITS == 4) {
-              const uint32_t w = turn ? cw[u ^ 2] : cw[u];
+              const uint32_t w = turn ? it.code[i][u ^ 2] : it.code[i][u];
               const uint32_t w8 = w >> 8;
               y[0] = pc_fma2(w & 0x000F000Fu, s1, b2);
               y[1] = pc_fma2(w & 0x00F000F0u, s16, b2);
@@ -614,14 +630,13 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
             } else {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t w = turn ? cw[2 * (u ^ 1) + h] : cw[2 * u + h];
+                const uint32_t w = turn ? it.code[i][2 * (u ^ 2) + h] : it.code[i][2 * u + h];
                 y[2 * h] = pc_fma2(w & 0x00FF00FFu, s1, b2);
                 y[2 * h + 1] = pc_fma2((w >> 8) & 0x00FF00FFu, s1, b2);
               }
             }
-            const int piece = q * PP + (u ^ turn);
-            const uint32_t a = dst + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + to[u] + i * ((DEQ * 32 / UPR)) * 128), "r"(y[0]),
+                         "r"(y[1]), "r"(y[2]), "r"(y[3])
                          : "memory");
           }
         }
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
       tile_done(k);
     }
   } else {
-   pc_regs_down<G::R_LAST>();
+   pc_regs<G::R_LAST, G::R_ALL>();
    if (warp == W_MMA) {
     // ================================================================================ one thread issues the products
     constexpr uint32_t ID_QK = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | (8u << 24);               // M 128, N 128
@@ -870,7 +885,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         const uint32_t tv = __float_as_uint(fmaf(pc_half(top[2], p.f16), QMAX, pc_half(top[3], p.f16)));
         const int fk = max(1, min(254 + T - (int)(tk >> 23), 253)), fv = max(1, min(254 + T - (int)(tv >> 23), 253));
         wait(&sh.info_empty[g % kPcInfo], g / kPcInfo + 1);
-        if (lane < 8) f.pg[lane] = pg;
+        if (lane < 8)
+          f.row[lane] = pg < 0 ? kPcNoRow : (uint32_t)qda_pool_row(pg, kvh, (key0 + 16 * lane) & pmask, Hkv, p.page_shift);
         if (lane < 4) {
           f.gone[lane] = ((gone8 >> (2 * lane)) & 1u ? 0xffffu : 0u) | ((gone8 >> (2 * lane + 1)) & 1u ? 0xffff0000u : 0u);
           f.bad[lane] = lane == 0 ? bad[0] : lane == 1 ? bad[1] : lane == 2 ? bad[2] : bad[3];

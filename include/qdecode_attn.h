@@ -268,7 +268,7 @@ int qdecode_cache_append(const uint32_t* k_packed, const void* k_scales, const v
  * and a slot is page_id * page + row. (The pages this library follows hold one contiguous cache per step, maya-mac
  * mlx_kernels.py, _ATTEND; they have no counterpart of this section.) Lengths, tables and slots are int32 DEVICE
  * arrays, read by the kernels only: a step can be captured once in a CUDA graph and replayed as they change.
- * page is a power of two from 16 to 256; num_pages * page < 2^31. What the host cannot check is checked on the device:
+ * page is a power of two from 16 to 256; num_pages * page < 2^31, num_pages * page * Hkv < 2^32 - 1. What the host cannot check is checked on the device:
  * an entry of the table or of slots outside the pool is skipped and sets bit 8 of qdecode_attn_device_status().
  */
 #define QDA_PAGE_MIN 16
