@@ -64,7 +64,8 @@ struct PcGeom {
   static constexpr int R_ALL = NQ == 2 ? 96 : 128;
   static constexpr int R_SOFT = NQ == 2 ? 152 : 168, R_DEQ = NQ == 2 ? 64 : 128, R_LAST = NQ == 2 ? 48 : 80;
   static_assert(SOFT * R_SOFT + DEQ * R_DEQ + 4 * R_LAST <= WARPS * R_ALL, "registers of the launch");
-  static constexpr int AHEAD = NQ == 2 ? 1 : (BITS == 4 ? 3 : 2);   // items of codes under way: what the registers hold
+  // items of codes under way: what the registers hold, and a divisor of a block's items less one
+  static constexpr int AHEAD = D <= 128 ? 1 : D == 256 ? 3 : BITS == 4 ? 5 : 2;
   static constexpr int O_COL = 256;                     // O behind two S buffers of 128 columns
   static_assert(NQ == 1 || D <= 128, "two tiles need room for two O");
   static_assert(SLOTS >= 3 && O_COL + NQ * DV <= 512, "shared or tensor memory");
@@ -203,6 +204,15 @@ template <int N, int LAUNCH>
 __device__ __forceinline__ void pc_regs() {
   if constexpr (N > LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
   if constexpr (N < LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// f(integral_constant<0>), ..., f(integral_constant<N - 1>)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void pc_each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    pc_each<N, I + 1>(f);
+  }
 }
 
 template <int D, int BITS, int NQ>
@@ -533,51 +543,60 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
       uint32_t s[NU], b[NU];                   // as they are in memory: nothing waits for a load before its item's turn
       uint32_t ok;                             // bit per unit: the key counts (else it is zero)
     };
+    // The slots of a tile come in groups g = -1 ... n - 1 of KSL + VSL items: the keys of block g + 1, the values of block g
+    // (where there are such). Items are loaded AHEAD items before they are converted.
+    constexpr int P = KSL + VSL;
+    static_assert(P % (AHEAD + 1) == 0, "an item's registers are known at compile time");
     Item reg[AHEAD + 1];
     for (int k = 0;; ++k) {
       const PcTile* t = tile_at(k);
       if (t == nullptr) break;
-      const int n = t->n, items = n * (KSL + VSL);
+      const int n = t->n, left0 = t->keys - t->j0 * kPcKeys;
+      const int vd0 = t->part * DV + 32 * q;
+      const char* ksrc = reinterpret_cast<const char*>(p.kp) + 4 * BITS * q;
+      const char* vsrc = reinterpret_cast<const char*>(p.vp) + vd0 * BITS / 8;
+      uint32_t prk[NU], prv[NU], okk = 0, okv = 0;   // pool rows of the block whose keys were loaded last, and of the one before
+#pragma unroll
+      for (int i = 0; i < NU; ++i) prk[i] = prv[i] = 0;
       int kv_run = -126;
-      // item x of the walk: block, keys or values, slice of the dimensions
-      auto what = [&](int x, int& j, bool& val, int& sl) {
-        const int y = x - KSL;
-        if (y < 0) {
-          j = 0;
-          val = false;
-          sl = x;
-          return;
+      uint32_t at = ic;                              // slots so far
+      auto load = [&](auto item, int g) {
+        constexpr int X = decltype(item)::value;
+        constexpr bool VAL = X >= KSL;
+        constexpr int SL = VAL ? X - KSL : X;
+        if (VAL ? g < 0 : g + 1 >= n) return;
+        Item& it = reg[X % (AHEAD + 1)];
+        if constexpr (X == 0) {
+          const uint32_t x = bc + g + 1;
+          const PcInfo& f = sh.info[x % kPcInfo];
+          wait(&sh.info_full[x % kPcInfo], x / kPcInfo);
+          const int left = left0 - (g + 1) * kPcKeys;
+          okv = okk;
+          okk = 0;
+#pragma unroll
+          for (int i = 0; i < NU; ++i) {
+            const int r = row + i * (DEQ * 32 / UPR);
+            const uint32_t base = f.row[r >> 4];
+            const bool ok = base != kPcNoRow && r < left;
+            prv[i] = prk[i];
+            prk[i] = ok ? base + (r & 15) : 0u;
+            okk |= (uint32_t)ok << i;
+          }
+        } else if constexpr (X == KSL) {
+          if (g + 1 >= n) {   // the last group has no keys: its values are of the block whose keys came last
+            okv = okk;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) prv[i] = prk[i];
+          }
         }
-        j = y / (KSL + VSL);
-        const int z = y - j * (KSL + VSL);
-        if (j + 1 < n) {
-          val = z >= KSL;
-          sl = val ? z - KSL : z;
-          if (!val) ++j;
-        } else {
-          val = true;
-          sl = z;
-        }
-      };
-      auto load = [&](int x, Item& it) {
-        int j, sl;
-        bool val;
-        what(x, j, val, sl);
-        const uint32_t g = bc + j;
-        wait(&sh.info_full[g % kPcInfo], g / kPcInfo);
-        const PcInfo& f = sh.info[g % kPcInfo];
-        const int d0 = (val ? t->part * DV : 0) + sl * SD + 32 * q;
-        const char* src = reinterpret_cast<const char*>(val ? p.vp : p.kp) + d0 * BITS / 8;
-        const char* ss = reinterpret_cast<const char*>(val ? p.vs : p.ks) + (d0 >> gshift) * 2;
-        const char* bs = reinterpret_cast<const char*>(val ? p.vb : p.kb) + (d0 >> gshift) * 2;
-        const int left = t->keys - (t->j0 + j) * kPcKeys;
-        it.ok = 0;
+        const uint32_t goff = (((VAL ? vd0 : 32 * q) + SL * SD) >> gshift) * 2;
+        const char* src = (VAL ? vsrc : ksrc) + SL * SD * BITS / 8;
+        const char* ss = reinterpret_cast<const char*>(VAL ? p.vs : p.ks) + goff;
+        const char* bs = reinterpret_cast<const char*>(VAL ? p.vb : p.kb) + goff;
+        it.ok = VAL ? okv : okk;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-          const int r = row + i * ((DEQ * 32 / UPR));
-          const uint32_t base = f.row[r >> 4];
-          const bool ok = base != kPcNoRow && r < left;
-          const uint32_t pr = ok ? base + (r & 15) : 0u;
+          const uint32_t pr = VAL ? prv[i] : prk[i];
           const uint4* c = reinterpret_cast<const uint4*>(src + (uint64_t)pr * ROWB);
 #pragma unroll
           for (int u = 0; u < UW / 4; ++u) {
@@ -589,19 +608,21 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           }
           it.s[i] = __ldg(reinterpret_cast<const uint16_t*>(ss + (uint64_t)pr * sstride));
           it.b[i] = __ldg(reinterpret_cast<const uint16_t*>(bs + (uint64_t)pr * sstride));
-          it.ok |= (uint32_t)ok << i;
         }
       };
-      auto convert = [&](int x, const Item& it) {
-        int j, sl;
-        bool val;
-        what(x, j, val, sl);
-        const uint32_t at0 = ic + x, slot = at0 % SLOTS;
-        const PcInfo& f = sh.info[(bc + j) % kPcInfo];
-        if (val) kv_run = max(kv_run, f.kv);
-        const float fac = val ? __uint_as_float((uint32_t)(127 - kv_run) << 23) : f.kfac;
+      auto convert = [&](auto item, int g) {
+        constexpr int X = decltype(item)::value;
+        constexpr bool VAL = X >= KSL;
+        constexpr int SL = VAL ? X - KSL : X;
+        if (VAL ? g < 0 : g + 1 >= n) return;
+        const Item& it = reg[X % (AHEAD + 1)];
+        const PcInfo& f = sh.info[(bc + g + (VAL ? 0 : 1)) % kPcInfo];
+        if constexpr (VAL && SL == 0) kv_run = max(kv_run, f.kv);
+        const float fac = VAL ? __uint_as_float((uint32_t)(127 - kv_run) << 23) : f.kfac;
         const bool odd = f.flags & 2u;
-        wait(&sh.empty[slot], at0 / SLOTS + 1);
+        const uint32_t slot = at % SLOTS;
+        wait(&sh.empty[slot], at / SLOTS + 1);
+        ++at;
         const uint32_t dst = smem_addr(ring) + slot * G::SLOT;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
@@ -635,8 +656,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
                 y[2 * h + 1] = pc_fma2((w >> 8) & 0x00FF00FFu, s1, b2);
               }
             }
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + to[u] + i * ((DEQ * 32 / UPR)) * 128), "r"(y[0]),
-                         "r"(y[1]), "r"(y[2]), "r"(y[3])
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + to[u] + i * (DEQ * 32 / UPR) * 128),
+                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                          : "memory");
           }
         }
@@ -644,24 +665,20 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sh.full[slot]);
-          if (val && sl == VSL - 1) mbar_arrive(&sh.info_empty[(bc + j) % kPcInfo]);
+          if (VAL && SL == VSL - 1) mbar_arrive(&sh.info_empty[(bc + g) % kPcInfo]);
         }
       };
-#pragma unroll
-      for (int x = 0; x < AHEAD; ++x)
-        if (x < items) load(x, reg[x]);
-      for (int x0 = 0; x0 < items; x0 += AHEAD + 1) {
-#pragma unroll
-        for (int u = 0; u <= AHEAD; ++u) {
-          const int x = x0 + u;
-          if (x < items) {
-            if (x + AHEAD < items) load(x + AHEAD, reg[(u + AHEAD) % (AHEAD + 1)]);
-            convert(x, reg[u]);
-          }
-        }
+      if (n > 0) {
+        pc_each<AHEAD>([&](auto item) { load(item, -1); });
+        for (int g = -1; g < n; ++g)
+          pc_each<P>([&](auto item) {
+            constexpr int NEXT = decltype(item)::value + AHEAD;
+            load(std::integral_constant<int, NEXT % P>{}, g + NEXT / P);
+            convert(item, g);
+          });
       }
       bc += n;
-      ic += items;
+      ic += n * P;
       tile_done(k);
     }
   } else {
