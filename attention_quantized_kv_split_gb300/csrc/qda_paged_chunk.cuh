@@ -62,7 +62,7 @@ struct PcGeom {
   static constexpr int WARPS = SOFT + DEQ + 1 + kPcInfoWarps;
   // registers a thread: the launch's 96 (20 warps) or 128 (16 warps), dealt out anew among the warpgroups
   static constexpr int R_ALL = NQ == 2 ? 96 : 128;
-  static constexpr int R_SOFT = NQ == 2 ? 152 : 168, R_DEQ = NQ == 2 ? 64 : 128, R_LAST = NQ == 2 ? 48 : 80;
+  static constexpr int R_SOFT = NQ == 2 ? 128 : 136, R_DEQ = NQ == 2 ? 80 : 136, R_LAST = NQ == 2 ? 64 : 96;
   static_assert(SOFT * R_SOFT + DEQ * R_DEQ + 4 * R_LAST <= WARPS * R_ALL, "registers of the launch");
   // items of codes under way: what the registers hold, and a divisor of a block's items less one
   static constexpr int AHEAD = D <= 128 ? 1 : D == 256 ? 3 : BITS == 4 ? 5 : 2;
@@ -179,6 +179,12 @@ __device__ __forceinline__ void pc_scale8(uint32_t taddr, float x) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+__device__ __forceinline__ float pc_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t pc_h2(float lo, float hi) {
@@ -414,40 +420,64 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           }
           kv = kv_new;
         };
-        float v[4][32];   // the row's scores
+        // The row's 128 scores do not fit the registers next to everything else: the second half is read for its maximum, the
+        // first is read and kept, and the second read again as the first's registers come free. Weights lie over the
+        // first half's scores.
+        float u[2][32];
+        auto get = [&](float (&x)[32], int c) { pc_ld32(s_t + 32 * c, x); };
+        auto hide = [&](float (&x)[32], int c) {
+          if (edge) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) pc_ld32(s_t + 32 * c, v[c]);
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= left) x[i] = -INFINITY;
+          }
+        };
+        auto largest = [&](const float (&x)[32]) {
+          float a = pc_max3(x[0], x[1], x[2]), b = pc_max3(x[3], x[4], x[5]);
+#pragma unroll
+          for (int i = 6; i < 30; i += 4) {
+            a = pc_max3(a, x[i], x[i + 1]);
+            b = pc_max3(b, x[i + 2], x[i + 3]);
+          }
+          return fmaxf(pc_max3(a, b, x[30]), x[31]);
+        };
+        get(u[0], 2);
+        get(u[1], 3);
         tmem_wait_ld();
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= left) v[i >> 5][i & 31] = -INFINITY;
-        }
-        float top4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          top4[c] = v[c][0];
-#pragma unroll
-          for (int i = 1; i < 31; i += 2) top4[c] = fmaxf(top4[c], fmaxf(v[c][i], v[c][i + 1]));
-          top4[c] = fmaxf(top4[c], v[c][31]);
-        }
-        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * mult;   // mult > 0
+        hide(u[0], 2);
+        hide(u[1], 3);
+        float top = fmaxf(largest(u[0]), largest(u[1]));
+        get(u[0], 0);
+        get(u[1], 1);
+        tmem_wait_ld();
+        hide(u[0], 0);
+        hide(u[1], 1);
+        top = pc_max3(top, largest(u[0]), largest(u[1])) * mult;   // mult > 0
         if (j == 0) kv = kv_new;
         if (__any_sync(0xffffffffu, top > m + 8.f) || kv_new != kv) rescale(top);
         const float mm = m == -INFINITY ? 0.f : -m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        auto weigh = [&](const float (&x)[32], int c) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float2 e = __ffma2_rn(make_float2(v[c][2 * i], v[c][2 * i + 1]), make_float2(mult, mult), make_float2(mm, mm));
-            const float2 x = make_float2(pc_ex2(e.x), pc_ex2(e.y));
-            sum[i & 1] = __fadd2_rn(sum[i & 1], x);
-            w[i] = pc_h2(x.x, x.y);
+            const float2 e = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(mult, mult), make_float2(mm, mm));
+            const float2 y = make_float2(pc_ex2(e.x), pc_ex2(e.y));
+            sum[i & 1] = __fadd2_rn(sum[i & 1], y);
+            w[i] = pc_h2(y.x, y.y);
           }
-          tmem_st16(s_t + 16 * c, w);   // over the scores, which are in registers
-        }
+          tmem_st16(s_t + 16 * c, w);
+        };
+        weigh(u[0], 0);
+        get(u[0], 2);
+        weigh(u[1], 1);
+        tmem_wait_ld();
+        get(u[1], 3);
+        hide(u[0], 2);
+        weigh(u[0], 2);
+        tmem_wait_ld();
+        hide(u[1], 3);
+        weigh(u[1], 3);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
