@@ -62,7 +62,7 @@ struct PcGeom {
   static constexpr int WARPS = SOFT + DEQ + 1 + kPcInfoWarps;
   // registers a thread: the launch's 96 (20 warps) or 128 (16 warps), dealt out anew among the warpgroups
   static constexpr int R_ALL = NQ == 2 ? 96 : 128;
-  static constexpr int R_SOFT = NQ == 2 ? 128 : 136, R_DEQ = NQ == 2 ? 80 : 136, R_LAST = NQ == 2 ? 64 : 96;
+  static constexpr int R_SOFT = NQ == 2 ? 136 : 136, R_DEQ = NQ == 2 ? 72 : 136, R_LAST = NQ == 2 ? 64 : 96;
   static_assert(SOFT * R_SOFT + DEQ * R_DEQ + 4 * R_LAST <= WARPS * R_ALL, "registers of the launch");
   // items of codes under way: what the registers hold, and a divisor of a block's items less one
   static constexpr int AHEAD = D <= 128 ? 1 : D == 256 ? 3 : BITS == 4 ? 5 : 2;
