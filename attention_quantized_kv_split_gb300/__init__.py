@@ -5,8 +5,8 @@ only marshals torch tensors (device memory and streams) into that ABI, under the
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -195,39 +195,48 @@ def qdecode_qgemv(x: torch.Tensor, w_packed: torch.Tensor, w_scales: torch.Tenso
     return y
 
 
-def _on(t: torch.Tensor, stream):
-    """The device a paged call runs on (its first tensor's, made current) and its stream's handle."""
-    if not t.is_cuda:
-        raise ValueError("paged calls take CUDA tensors")
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext(), _stream(stream)
-    return torch.cuda.device(t.device), torch.cuda.current_stream(t.device).cuda_stream if stream is None else _stream(stream)
+def _paged_call(op: int, name: str, pack, dev: int, stream, args) -> None:
+    """One paged call on device ``dev``: the arguments packed (one foreign-call argument instead of thirty), the stream
+    given or the device's current one."""
+    if dev < 0:
+        raise ValueError(f"{name} takes CUDA tensors")
+    if dev == torch.cuda.current_device():
+        st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+        st = lib().qdecode_paged_packed(op, pack(*args, st))
+    else:
+        with torch.cuda.device(dev):
+            st = torch.cuda.current_stream().cuda_stream if stream is None else _stream(stream)
+            st = lib().qdecode_paged_packed(op, pack(*args, st))
+    if st:
+        raise _lib.QdaError(st, name)
 
 
-def _same(device, dtype, **tensors):
-    """Every tensor given: contiguous, on `device` and (dtype not None) of that dtype."""
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device != device or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-            raise ValueError(f"{name}: expected a contiguous {dtype or 'tensor'} on {device}, got {t.dtype} on "
-                             f"{t.device}, strides {t.stride()}")
+def _ints(dev: int, names: str, *tensors) -> None:
+    """Every tensor given: int32, contiguous, on device ``dev``."""
+    for i, t in enumerate(tensors):
+        if t is not None and not (t.dtype is torch.int32 and t.is_contiguous() and t.get_device() == dev):
+            raise ValueError(f"{names.split()[i]}: expected contiguous int32 on device {dev}, got {t.dtype} on {t.device}, "
+                             f"strides {t.stride()}")
 
 
-def _pool(k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits):
-    """num_pages, Hkv and page of a pool's six arrays, their shapes checked."""
-    pages, Hkv, page, W = k_packed.shape
-    if GS < 1 or W * 32 != D * bits or v_packed.shape != k_packed.shape:
-        raise ValueError(f"packed arrays {tuple(k_packed.shape)}, {tuple(v_packed.shape)} do not hold {bits}-bit rows of {D}")
-    for t in (k_scales, k_biases, v_scales, v_biases):
-        if t.shape != (pages, Hkv, page, D // GS) or t.dtype != k_scales.dtype:
-            raise ValueError(f"scales and biases must be [{pages}, {Hkv}, {page}, {D // GS}] of one dtype, got "
-                             f"{tuple(t.shape)} {t.dtype}")
-    _same(k_packed.device, None, k_packed=k_packed, k_scales=k_scales, k_biases=k_biases, v_packed=v_packed,
-          v_scales=v_scales, v_biases=v_biases)
-    if k_packed.element_size() != 4 or v_packed.element_size() != 4:
-        raise ValueError("packed arrays are 32-bit words")
-    return pages, Hkv, page
+def _pool(dev, kp, ks, kb, vp, vs, vb, D, GS, bits):
+    """num_pages, Hkv, page and dtype of a pool's six arrays: shapes, dtypes, device and contiguity checked."""
+    shape, groups, dt = kp.shape, ks.shape, ks.dtype
+    pages, Hkv, page, W = shape
+    if GS < 1 or W * 32 != D * bits or vp.shape != shape or kp.element_size() != 4 or vp.element_size() != 4:
+        raise ValueError(f"packed arrays {tuple(shape)} {kp.dtype}, {tuple(vp.shape)} {vp.dtype} do not hold {bits}-bit "
+                         f"rows of {D} in 32-bit words")
+    if not (groups == (pages, Hkv, page, D // GS) == kb.shape == vs.shape == vb.shape and kb.dtype is dt
+            and vs.dtype is dt and vb.dtype is dt):
+        raise ValueError(f"scales and biases must be [{pages}, {Hkv}, {page}, {D // GS}] of one dtype, got "
+                         f"{[(tuple(t.shape), t.dtype) for t in (ks, kb, vs, vb)]}")
+    for t in (kp, ks, kb, vp, vs, vb):
+        if not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"the pool's arrays must be contiguous and on device {dev}")
+    return pages, Hkv, page, dt
+
+
+_PACK_MAP, _PACK_APPEND, _PACK_ATTN = (struct.Struct(f"={n}q").pack for n in (15, 24, 27))
 
 
 def qdecode_paged_map(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -236,19 +245,19 @@ def qdecode_paged_map(old_len: torch.Tensor, new_len: torch.Tensor, block_table:
     """One step's tables on the GPU (all int32): from ``old_len``, ``new_len [B]`` and ``free_pages [n_free]`` writes
     ``q_start [B + 1]``, ``kv_len [B]``, the new pages' entries of ``block_table [B, max_pages]``, ``slots`` and
     ``positions [max_tokens]`` (-1 behind the last token) and ``used [1]``, the pages that the step takes."""
-    _same(old_len.device, torch.int32, old_len=old_len, new_len=new_len, block_table=block_table, free_pages=free_pages,
-          q_start=q_start, kv_len=kv_len, slots=slots, positions=positions, used=used)
+    dev = old_len.get_device()
+    _ints(dev, "old_len new_len block_table free_pages q_start kv_len slots positions used", old_len, new_len, block_table,
+          free_pages, q_start, kv_len, slots, positions, used)
     B, max_pages = block_table.shape
+    n = slots.numel()
     if not (old_len.numel() == new_len.numel() == kv_len.numel() == B and q_start.numel() == B + 1 and used.numel() >= 1):
         raise ValueError("old_len, new_len and kv_len hold B values, q_start B + 1")
-    if positions is not None and positions.numel() < slots.numel():
+    if positions is not None and positions.numel() < n:
         raise ValueError("positions holds fewer tokens than slots")
-    device, st = _on(old_len, stream)
-    with device:
-        st = lib().qdecode_paged_map(_ptr(old_len), _ptr(new_len), _ptr(block_table), _ptr(free_pages), _ptr(q_start),
-                                     _ptr(kv_len), _ptr(slots), _ptr(positions), _ptr(used), B, max_pages,
-                                     free_pages.numel(), page, slots.numel(), st)
-    _lib.check(st, "qdecode_paged_map")
+    _paged_call(0, "qdecode_paged_map", _PACK_MAP, dev, stream,
+                (old_len.data_ptr(), new_len.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), q_start.data_ptr(),
+                 kv_len.data_ptr(), slots.data_ptr(), 0 if positions is None else positions.data_ptr(), used.data_ptr(), B,
+                 max_pages, free_pages.numel(), page, n))
 
 
 def qdecode_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_packed: torch.Tensor,
@@ -258,27 +267,24 @@ def qdecode_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, 
     """Quantize new rows ``k``, ``v [T, Hkv, D]`` (bf16, fp16 or fp32; last dimension contiguous, other strides free)
     into the pool at ``slots [T]`` (int32; negative: skipped). ``k_held``, ``v_held [T, Hkv, D]`` in the cache dtype
     receive the values the cache now stands for."""
-    T, Hkv, D = k.shape
-    pages, heads, page = _pool(k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits)
-    if v.shape != k.shape or v.dtype != k.dtype or heads != Hkv or slots.numel() != T:
-        raise ValueError(f"k {tuple(k.shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype}, {slots.numel()} slots and a pool "
-                         f"of {heads} heads do not belong together")
-    if T and (k.stride(2) != 1 or v.stride(2) != 1):
+    shape, dev = k.shape, k.get_device()
+    T, Hkv, D = shape
+    pages, heads, page, dt = _pool(dev, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits)
+    if v.shape != shape or v.dtype is not k.dtype or v.get_device() != dev or heads != Hkv or slots.numel() != T:
+        raise ValueError(f"k {tuple(shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype} on {v.device}, {slots.numel()} slots "
+                         f"and a pool of {heads} heads do not belong together")
+    (kt, kh, kd), (vt, vh, vd) = k.stride(), v.stride()
+    if T and (kd != 1 or vd != 1):
         raise ValueError("rows of k and v must be contiguous")
-    if k.device != k_packed.device or v.device != k_packed.device:
-        raise ValueError("k, v and the pool must be on one device")
-    _same(k.device, torch.int32, slots=slots)
-    _same(k.device, k_scales.dtype, k_held=k_held, v_held=v_held)
+    _ints(dev, "slots", slots)
     for t in (k_held, v_held):
-        if t is not None and t.shape != k.shape:
-            raise ValueError(f"k_held and v_held must be {tuple(k.shape)}")
-    device, st = _on(k, stream)
-    with device:
-        st = lib().qdecode_paged_append(_ptr(k), _ptr(v), k.stride(0), k.stride(1), v.stride(0), v.stride(1), _ptr(slots),
-                                        _ptr(k_packed), _ptr(k_scales), _ptr(k_biases), _ptr(v_packed), _ptr(v_scales),
-                                        _ptr(v_biases), _ptr(k_held), _ptr(v_held), T, Hkv, pages, page, D, GS, bits,
-                                        dtype_code(k_scales.dtype, k.dtype), st)
-    _lib.check(st, "qdecode_paged_append")
+        if t is not None and not (t.shape == shape and t.dtype is dt and t.is_contiguous() and t.get_device() == dev):
+            raise ValueError(f"k_held and v_held must be contiguous {tuple(shape)} {dt} on the pool's device")
+    _paged_call(1, "qdecode_paged_append", _PACK_APPEND, dev, stream,
+                (k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, slots.data_ptr(), k_packed.data_ptr(), k_scales.data_ptr(),
+                 k_biases.data_ptr(), v_packed.data_ptr(), v_scales.data_ptr(), v_biases.data_ptr(),
+                 0 if k_held is None else k_held.data_ptr(), 0 if v_held is None else v_held.data_ptr(), T, Hkv, pages,
+                 page, D, GS, bits, _DT_CODE[dt] | _DT_CODE[k.dtype] << 8))
 
 
 def qdecode_paged_attn(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.Tensor, k_biases: torch.Tensor,
@@ -288,25 +294,23 @@ def qdecode_paged_attn(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.
     """Attention of every sequence's new tokens over its pages: q ``[total_q, H, D]`` (rows contiguous), out the same
     shape, contiguous; ``q_start [B + 1]``, ``kv_len [B]``, ``block_table [B, max_pages]`` int32 on the GPU. ``max_q``
     bounds the new tokens of a sequence (it only chooses the kernel). ``causal=False`` is cross attention."""
-    T, H, D = q.shape
-    pages, Hkv, page = _pool(k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits)
+    shape, dev = q.shape, q.get_device()
+    T, H, D = shape
+    pages, Hkv, page, dt = _pool(dev, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits)
     B, max_pages = block_table.shape
-    if q.dtype != k_scales.dtype or out.shape != q.shape or kv_len.numel() != B or q_start.numel() != B + 1:
-        raise ValueError(f"q {tuple(q.shape)} {q.dtype}, out {tuple(out.shape)}, {kv_len.numel()} lengths and "
-                         f"{q_start.numel()} starts do not fit a {k_scales.dtype} cache of {B} sequences")
-    if T and q.stride(2) != 1:
+    if not (q.dtype is dt and out.dtype is dt and out.shape == shape and out.is_contiguous() and out.get_device() == dev
+            and kv_len.numel() == B and q_start.numel() == B + 1):
+        raise ValueError(f"q {tuple(shape)} {q.dtype}, out {tuple(out.shape)} {out.dtype} on {out.device} (contiguous), "
+                         f"{kv_len.numel()} lengths and {q_start.numel()} starts do not fit a {dt} cache of {B} sequences")
+    qt, qh, qd = q.stride()
+    if T and qd != 1:
         raise ValueError("rows of q must be contiguous")
-    if q.device != k_packed.device:
-        raise ValueError("q and the pool must be on one device")
-    _same(q.device, q.dtype, out=out)
-    _same(q.device, torch.int32, q_start=q_start, kv_len=kv_len, block_table=block_table)
-    device, st = _on(q, stream)
-    with device:
-        st = lib().qdecode_paged_attn(_ptr(q), q.stride(0), q.stride(1), _ptr(k_packed), _ptr(k_scales), _ptr(k_biases),
-                                      _ptr(v_packed), _ptr(v_scales), _ptr(v_biases), _ptr(out), _ptr(q_start),
-                                      _ptr(kv_len), _ptr(block_table), T, max_q, B, H, Hkv, pages, page, max_pages,
-                                      int(causal), D, GS, bits, dtype_code(q.dtype), st)
-    _lib.check(st, "qdecode_paged_attn")
+    _ints(dev, "q_start kv_len block_table", q_start, kv_len, block_table)
+    _paged_call(2, "qdecode_paged_attn", _PACK_ATTN, dev, stream,
+                (q.data_ptr(), qt, qh, k_packed.data_ptr(), k_scales.data_ptr(), k_biases.data_ptr(), v_packed.data_ptr(),
+                 v_scales.data_ptr(), v_biases.data_ptr(), out.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                 block_table.data_ptr(), T, max_q, B, H, Hkv, pages, page, max_pages, 1 if causal else 0, D, GS, bits,
+                 _DT_CODE[dt]))
     return out
 
 

@@ -65,6 +65,7 @@ SIGNATURES = {
     "qdecode_paged_map": (_I, [_P] * 9 + [_I] * 5 + [_P]),
     "qdecode_paged_append": (_I, [_P, _P, _LL, _LL, _LL, _LL] + [_P] * 9 + [_I] * 8 + [_P]),
     "qdecode_paged_attn": (_I, [_P, _LL, _LL] + [_P] * 10 + [_I] * 13 + [_P]),
+    "qdecode_paged_packed": (_I, [_I, ctypes.c_char_p]),
     "qdecode_paged_attn_workspace_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_SZ)]),
     "qdecode_attn_strerror": (ctypes.c_char_p, [_I]),
     "qdecode_attn_last_cuda_error": (_I, []),

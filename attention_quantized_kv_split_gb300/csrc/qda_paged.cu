@@ -690,3 +690,25 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   if (e == cudaSuccess) e = qda_launch_paged_merge(p, plan.rows, plan.kb, s);
   return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
 }
+
+extern "C" int qdecode_paged_packed(int op, const int64_t* args) {
+  static const int counts[3] = {15, 24, 27}, first_int[3] = {9, 15, 13};   // arguments; the first of the 32-bit ones
+  if (args == nullptr || op < 0 || op > 2) return QDA_ERR_INVALID;
+  int64_t a[27];
+  std::memcpy(a, args, sizeof(int64_t) * counts[op]);   // args may have any alignment
+  for (int i = first_int[op]; i < counts[op] - 1; ++i)
+    if (a[i] < INT32_MIN || a[i] > INT32_MAX) return QDA_ERR_INVALID;
+  auto ptr = [&](int i) { return reinterpret_cast<void*>(static_cast<intptr_t>(a[i])); };
+  auto i32 = [&](int i) { return static_cast<int32_t*>(ptr(i)); };
+  auto u32 = [&](int i) { return static_cast<uint32_t*>(ptr(i)); };
+  auto n = [&](int i) { return static_cast<int>(a[i]); };
+  if (op == 0)
+    return qdecode_paged_map(i32(0), i32(1), i32(2), i32(3), i32(4), i32(5), i32(6), i32(7), i32(8), n(9), n(10), n(11),
+                             n(12), n(13), ptr(14));
+  if (op == 1)
+    return qdecode_paged_append(ptr(0), ptr(1), a[2], a[3], a[4], a[5], i32(6), u32(7), ptr(8), ptr(9), u32(10), ptr(11),
+                                ptr(12), ptr(13), ptr(14), n(15), n(16), n(17), n(18), n(19), n(20), n(21), n(22), ptr(23));
+  return qdecode_paged_attn(ptr(0), a[1], a[2], u32(3), ptr(4), ptr(5), u32(6), ptr(7), ptr(8), ptr(9), i32(10), i32(11),
+                            i32(12), n(13), n(14), n(15), n(16), n(17), n(18), n(19), n(20), n(21), n(22), n(23), n(24),
+                            n(25), ptr(26));
+}

@@ -4,15 +4,15 @@
 // Matrix instructions work on the codes themselves. A warp takes 16 keys at a time; the codes, straight from shared memory, become the 16-bit
 // A operand of m16n8k16 products with fp32 sums (a few query rows are far too thin for the 128-row tiles of tcgen05, and its operands would have to be written back
 // to shared or tensor memory first; here they never leave the registers):
-//   scores   rows = keys, k = head dimension, columns = query rows. A code c is the fp16 value 1024 + c (one AND/OR for two), or
-//            1024 + 16 c where a nibble is left unshifted, with q / 16 on the other side. q goes in as fp16 after an
-//            exact scaling of each row by a power of two (bf16 has fewer significant bits and a wider range). The sums start at -1024 sum(q), so the product
-//            is sum(c q), and per group s_g sum(c q) + b_g sum(q) is formed in fp32. Codes and q are exact: so are the scores, to fp32.
+//   scores   rows = keys, k = head dimension, columns = query rows. A code's bits as they are, masked out of the packed word, are the fp16
+//            subnormal c 2^-24 (16 c 2^-24 where a nibble is left unshifted, with q / 16 on the other side): one AND makes two
+//            operand values, exact. q goes in as fp16 after an exact scaling of each row by a power of two (bf16 has fewer significant
+//            bits and a wider range). Per group, s_g sum(c q) + b_g sum(q) is formed in fp32: the scores are right to fp32.
 //   values   rows = head dimension, k = keys, columns = query rows: the weight w = p s_g of each group is the B operand,
-//            rounded to bf16 (for fp16 caches as a pair hi + lo of bf16: 16 significant bits; a bf16 result takes one). Codes are bf16 128 + c; an
-//            8-bit code is 128 + low nibble plus 2048 + 16 * high nibble, in two products. sum(w) of a group, for the offset and to centre the codes on the middle of
-//            their range (so that the rounding of w meets values no larger than half a group's range), comes from one more product
-//            with A = 1, or with many groups the offset is taken off the codes; the rest, sum(p (b_g + mid s_g)), stays in fp32.
+//            rounded to fp16 (11 significant bits: next to nothing beside a bf16 result, as much as the one rounding of an fp16 one); a power of two that
+//            follows the largest scale met keeps it in range. To centre the codes on the middle of their range (so that the rounding of w meets
+//            values no larger than half a group's range), sum(w) of a group comes from one more product with A = the middle, or with
+//            many groups the middle is taken off the codes; the rest, sum(p (b_g + mid s_g)), stays in fp32.
 // Keys and query rows change places between the two products: one movmatrix per 8 x 8 weights.
 //
 // Memory: each warp fills its own ring of shared-memory stages with 16-byte asynchronous copies (no warp waits for another), the 16-byte
@@ -43,16 +43,16 @@ struct PsGeom {
   static constexpr int STAGES = 3;
   static constexpr bool QSMEM = D * NT > 256;             // q operands in shared memory (else in registers)
   static constexpr bool SSMEM = NG * NT > 4;              // sums of q in shared memory
-  static constexpr bool ONES = NG <= 4;                   // sum(w) by a product with A = 1 (else offset-free codes)
+  static constexpr bool ONES = NG <= 4;                   // codes centred by a product with A = middle (else one by one)
   static constexpr int QF = QSMEM ? (D / 16) * NT * 256 : 0;
-  static constexpr int QS = SSMEM ? NG * MT * 8 : 0;
+  static constexpr int QS = SSMEM ? NG * MT * 4 : 0;
   static constexpr int ROWS = QF + QS;
   static constexpr int RING = kPsWarps * STAGES * STAGE;
   static constexpr int COMB = kPsWarps * 8 * D * 4;   // the warps' results of 8 query rows
   static constexpr int SMEM = ROWS + (RING > COMB ? RING : COMB);
   static_assert(SMEM - ROWS >= (int)sizeof(PagedLine), "the line lies in the ring");
   static constexpr int OREGS = D / 4 * NT;
-  static constexpr int MINB = OREGS <= 32 ? 4 : OREGS <= 64 ? 3 : 2;
+  static constexpr int MINB = OREGS <= 32 ? (NG * NT > 2 ? 3 : 4) : OREGS <= 64 ? (NT == 2 ? 2 : 3) : 2;   // spills else
 };
 
 __device__ __forceinline__ void ps_cp16(uint32_t dst, const void* src) {
@@ -64,19 +64,12 @@ __device__ __forceinline__ void ps_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-template <bool F16>
 __device__ __forceinline__ void ps_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                        uint32_t b1, float c0, float c1, float c2, float c3) {
-  if constexpr (F16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
-        "%12, %13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
-        "%12, %13};"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
+      "%12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 __device__ __forceinline__ uint32_t ps_trans(uint32_t a) {
@@ -96,10 +89,13 @@ __device__ __forceinline__ uint32_t ps_bf2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// (a & mask) | magic in one operation
-__device__ __forceinline__ uint32_t ps_or(uint32_t a, uint32_t mask, uint32_t magic) {
+__device__ __forceinline__ uint32_t ps_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t ps_sub2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(magic));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
@@ -182,8 +178,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
   constexpr int NG = G::NG, MT = G::MT, KPS = G::KPS, RB = G::RB, STAGES = G::STAGES;
   constexpr int KS = GS / 16;                 // products per group and key tile, on either side
   constexpr float MID = BITS == 4 ? 8.f : 128.f;
-  constexpr float VOFF = BITS == 4 ? 128.f : 2176.f;
-  constexpr float VADD = G::ONES ? VOFF + MID : 0.f;
+  constexpr uint32_t MID_LO = BITS == 4 ? 0x00080008u : 0x00800080u, MID_HI = 0x00800080u;   // middle codes as operands
+  constexpr float TINY = 5.9604644775390625e-8f, GREAT = 16777216.f;                         // 2^-24, 2^24
   extern __shared__ __align__(128) unsigned char ps_smem[];
   __shared__ float s_ml[NT][kPsWarps][2][8];   // per 8 query rows and warp: reference, sum
   __shared__ PagedTile t;   // the tile at hand, and this CTA's piece of the line
@@ -191,7 +187,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
   __shared__ int s_more;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, r8 = lane >> 2, c4 = lane & 3;
   uint2* s_qf = reinterpret_cast<uint2*>(ps_smem);
-  float2* s_qs = reinterpret_cast<float2*>(ps_smem + G::QF);   // [NG][MT] (-offset sum, sum) of q
+  float* s_qs = reinterpret_cast<float*>(ps_smem + G::QF);   // [NG][MT] sums of q, times 2^-24
   const uint32_t ring = smem_addr(ps_smem + G::ROWS) + warp * STAGES * G::STAGE;
   float* comb = reinterpret_cast<float*>(ps_smem + G::ROWS);
 
@@ -220,7 +216,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       const int row0 = t.i * MT;
       // ---- the tile's query rows: B operands, sums per group, and how far each sees
       uint2 qf[G::QSMEM ? 1 : D / 16 * NT];
-      float qoff[G::SSMEM ? 1 : NG * NT][2], qsum[G::SSMEM ? 1 : NG * NT][2];
+      float qsum[G::SSMEM ? 1 : NG * NT][2];
       float qmul[NT][2];
       int seen[NT][2];
       int least = 0x7fffffff;   // keys that every row of the tile sees
@@ -256,7 +252,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
         const float up = __uint_as_float((uint32_t)fe << 23), down = __uint_as_float((uint32_t)(254 - fe) << 23);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-          float off = 0.f, sum = 0.f;
+          float sum = 0.f;
 #pragma unroll
           for (int i = 0; i < GS / 32; ++i) {
             // eight values of the row: 4-bit: two products (codes 0 4 | 1 5, and 2 6 | 3 7), 8-bit: (0 2 | 1 3, 4 6 | 5 7)
@@ -269,8 +265,6 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
               const float hi0 = BITS == 4 ? v[2 * h + 1] * 0.0625f : v[4 * h + 1];
               const float hi1 = BITS == 4 ? v[2 * h + 5] * 0.0625f : v[4 * h + 3];
               const __half2 a = __floats2half2_rn(lo0, lo1), b = __floats2half2_rn(hi0, hi1);
-              const float2 af = __half22float2(a), bf = __half22float2(b);
-              off += af.x + af.y + bf.x + bf.y;   // what the offset 1024 of every code adds up to
               const uint2 f = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
               const int ks = (g * (GS / 32) + i) * 2 + h;
               if constexpr (G::QSMEM) {
@@ -283,26 +277,21 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             for (int e = 0; e < 8; ++e) sum += v[e];
           }
           // over the four lanes of the row
-          off += __shfl_xor_sync(0xffffffffu, off, 1);
-          off += __shfl_xor_sync(0xffffffffu, off, 2);
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          off *= -1024.f;
+          sum *= TINY;
           if constexpr (G::SSMEM) {
-            if (warp == 0 && c4 == 0) s_qs[g * MT + nt * 8 + r8] = make_float2(off, sum);
+            if (warp == 0 && c4 == 0) s_qs[g * MT + nt * 8 + r8] = sum;
           } else {
             // scores hold query rows 2 c4, 2 c4 + 1 in this lane
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              qoff[g * NT + nt][j] = __shfl_sync(0xffffffffu, off, (2 * c4 + j) * 4);
-              qsum[g * NT + nt][j] = __shfl_sync(0xffffffffu, sum, (2 * c4 + j) * 4);
-            }
+            for (int j = 0; j < 2; ++j) qsum[g * NT + nt][j] = __shfl_sync(0xffffffffu, sum, (2 * c4 + j) * 4);
           }
         }
         const int sr = real ? paged_seen(p, t.s, r) : keys;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          qmul[nt][j] = __shfl_sync(0xffffffffu, down, (2 * c4 + j) * 4) * p.qscale;
+          qmul[nt][j] = __shfl_sync(0xffffffffu, down, (2 * c4 + j) * 4) * p.qscale * GREAT;
           seen[nt][j] = __shfl_sync(0xffffffffu, sr, (2 * c4 + j) * 4);
           least = min(least, seen[nt][j]);
         }
@@ -379,6 +368,9 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
         m[nt][0] = m[nt][1] = -INFINITY;
       }
 
+      uint32_t most = 0;        // 16-bit pattern of the largest value scale that the weights' unit allows
+      int vexp = 0;             // weights are taken times 2^vexp
+
       look(0);
 #pragma unroll
       for (int k = 0; k < STAGES - 1; ++k) issue(k);
@@ -420,15 +412,15 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
                 uint32_t a0, a1, a2, a3;
                 if constexpr (BITS == 4) {
                   const uint32_t u = (j & 1) ? w0[j / 2] >> 8 : w0[j / 2], v = (j & 1) ? w1[j / 2] >> 8 : w1[j / 2];
-                  a0 = ps_or(u, 0x000F000Fu, 0x64006400u);
-                  a1 = ps_or(v, 0x000F000Fu, 0x64006400u);
-                  a2 = ps_or(u, 0x00F000F0u, 0x64006400u);
-                  a3 = ps_or(v, 0x00F000F0u, 0x64006400u);
+                  a0 = u & 0x000F000Fu;
+                  a1 = v & 0x000F000Fu;
+                  a2 = u & 0x00F000F0u;
+                  a3 = v & 0x00F000F0u;
                 } else {
-                  a0 = ps_or(w0[j], 0x00FF00FFu, 0x64006400u);
-                  a1 = ps_or(w1[j], 0x00FF00FFu, 0x64006400u);
-                  a2 = ps_or(w0[j] >> 8, 0x00FF00FFu, 0x64006400u);
-                  a3 = ps_or(w1[j] >> 8, 0x00FF00FFu, 0x64006400u);
+                  a0 = w0[j] & 0x00FF00FFu;
+                  a1 = w1[j] & 0x00FF00FFu;
+                  a2 = (w0[j] >> 8) & 0x00FF00FFu;
+                  a3 = (w1[j] >> 8) & 0x00FF00FFu;
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -436,17 +428,9 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
                   if constexpr (G::QSMEM) f = s_qf[((g * KS + j) * NT + nt) * 32 + lane];
                   else f = qf[(g * KS + j) * NT + nt];
                   if (j == 0) {
-                    float o0, o1;
-                    if constexpr (G::SSMEM) {
-                      o0 = s_qs[g * MT + nt * 8 + 2 * c4].x;
-                      o1 = s_qs[g * MT + nt * 8 + 2 * c4 + 1].x;
-                    } else {
-                      o0 = qoff[g * NT + nt][0];
-                      o1 = qoff[g * NT + nt][1];
-                    }
-                    ps_mma<true>(acc[nt], a0, a1, a2, a3, f.x, f.y, o0, o1, o0, o1);
+                    ps_mma(acc[nt], a0, a1, a2, a3, f.x, f.y, 0.f, 0.f, 0.f, 0.f);
                   } else {
-                    ps_mma<true>(acc[nt], a0, a1, a2, a3, f.x, f.y, acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
+                    ps_mma(acc[nt], a0, a1, a2, a3, f.x, f.y, acc[nt][0], acc[nt][1], acc[nt][2], acc[nt][3]);
                   }
                 }
               }
@@ -456,8 +440,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
               for (int nt = 0; nt < NT; ++nt) {
                 float q0, q1;
                 if constexpr (G::SSMEM) {
-                  q0 = s_qs[g * MT + nt * 8 + 2 * c4].y;
-                  q1 = s_qs[g * MT + nt * 8 + 2 * c4 + 1].y;
+                  q0 = s_qs[g * MT + nt * 8 + 2 * c4];
+                  q1 = s_qs[g * MT + nt * 8 + 2 * c4 + 1];
                 } else {
                   q0 = qsum[g * NT + nt][0];
                   q1 = qsum[g * NT + nt][1];
@@ -470,7 +454,23 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             }
           }
           // ---- weights
-          bool rise = false;
+          uint32_t sw[2][(NG + 1) / 2], bw[2][(NG + 1) / 2];   // the values' scales and biases
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            ps_halves<NG>(sc + 2 * G::SC + x * 8 * NG * 2, sw[x]);
+            ps_halves<NG>(sc + 3 * G::SC + x * 8 * NG * 2, bw[x]);
+          }
+          uint32_t big = 0;   // largest scale of this lane's keys (a pattern per half word)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t y = sw[x][0] & 0x7fff7fffu;
+#pragma unroll
+            for (int i = 1; i < (NG + 1) / 2; ++i) y = __vmaxu2(y, sw[x][i] & 0x7fff7fffu);
+            if (edge && (gone || n0 + r8 + 8 * x >= keys)) y = 0;   // rows behind the sequence may hold anything
+            big = __vmaxu2(big, y);
+          }
+          big = max(big & 0xffffu, big >> 16);
+          bool rise = big > most;
           uint32_t hidden = 0;   // bit 4 nt + j: score j of query rows nt is hidden
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -487,6 +487,18 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             rise = rise || fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + 8.f || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + 8.f;
           }
           if (__any_sync(0xffffffffu, rise)) {
+            // the weights' unit: the largest finite scale to [2^2, 2^3), good for scales up to 16 times that (w stays below 2^15)
+            constexpr uint32_t INF = F16 ? 0x7C00u : 0x7F80u, SHIFT = F16 ? 10 : 7;
+            big = __reduce_max_sync(0xffffffffu, big < INF ? big : 0u);
+            float fo = 1.f;
+            if (big > most) {
+              most = min(big + (4u << SHIFT), INF - 1);
+              const uint32_t w = big;
+              const int e = (int)(__float_as_uint(ps_half<F16>(&w, 0)) >> 23) - 127;
+              const int ve = max(-126, min(2 - e, 126));
+              fo = ps_ex2((float)(ve - vexp));
+              vexp = ve;
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -496,25 +508,28 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                 const float mn = fmaxf(m[nt][j], x);
-                const float f = mn == -INFINITY ? 1.f : ps_ex2(m[nt][j] - mn);   // 0 at the first visible key
+                // 0 at the first visible key (where the sums are 0, and the change of unit may be infinite)
+                const float f = mn == -INFINITY ? 1.f : ps_ex2(m[nt][j] - mn);
+                const float g1 = f == 0.f || m[nt][j] == -INFINITY ? 0.f : f * fo;
                 m[nt][j] = mn;
                 l[nt][j] *= f;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                   vb[g * NT + nt][j] *= f;
                   if constexpr (G::ONES) {
-                    wsum[g * NT + nt][j] *= f;
-                    wsum[g * NT + nt][j + 2] *= f;
+                    wsum[g * NT + nt][j] *= g1;
+                    wsum[g * NT + nt][j + 2] *= g1;
                   }
                 }
 #pragma unroll
                 for (int i = 0; i < NG * KS; ++i) {
-                  o[i * NT + nt][j] *= f;
-                  o[i * NT + nt][j + 2] *= f;
+                  o[i * NT + nt][j] *= g1;
+                  o[i * NT + nt][j + 2] *= g1;
                 }
               }
             }
           }
+          const float vfac = __uint_as_float((uint32_t)(127 + vexp) << 23);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
@@ -526,20 +541,14 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             l[nt][1] += s[nt][1] + s[nt][3];
           }
           // ---- values
-          uint32_t sw[2][(NG + 1) / 2], bw[2][(NG + 1) / 2];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            ps_halves<NG>(sc + 2 * G::SC + x * 8 * NG * 2, sw[x]);
-            ps_halves<NG>(sc + 3 * G::SC + x * 8 * NG * 2, bw[x]);
-          }
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             const float s0 = ps_half<F16>(sw[0], g), s1 = ps_half<F16>(sw[1], g);
             const float c0 = fmaf(MID, s0, ps_half<F16>(bw[0], g)), c1 = fmaf(MID, s1, ps_half<F16>(bw[1], g));
-            uint32_t hi[NT][2], lo[F16 ? NT : 1][2];
+            uint32_t wt[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float w[4] = {s[nt][0] * s0, s[nt][1] * s0, s[nt][2] * s1, s[nt][3] * s1};
+              float w[4] = {s[nt][0] * vfac * s0, s[nt][1] * vfac * s0, s[nt][2] * vfac * s1, s[nt][3] * vfac * s1};
               float e[4] = {s[nt][0] * c0, s[nt][1] * c0, s[nt][2] * c1, s[nt][3] * c1};
               if (edge) {   // a hidden key's scale and bias may be anything
 #pragma unroll
@@ -551,23 +560,15 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
               }
               vb[g * NT + nt][0] += e[0] + e[2];
               vb[g * NT + nt][1] += e[1] + e[3];
-              const uint32_t h0 = ps_bf2(w[0], w[1]), h1 = ps_bf2(w[2], w[3]);
-              hi[nt][0] = ps_trans(h0);
-              hi[nt][1] = ps_trans(h1);
-              if constexpr (F16) {
-                lo[nt][0] = ps_trans(ps_bf2(w[0] - __uint_as_float(h0 << 16), w[1] - __uint_as_float(h0 & 0xffff0000u)));
-                lo[nt][1] = ps_trans(ps_bf2(w[2] - __uint_as_float(h1 << 16), w[3] - __uint_as_float(h1 & 0xffff0000u)));
-              }
+              wt[nt][0] = ps_trans(ps_h2(w[0], w[1]));
+              wt[nt][1] = ps_trans(ps_h2(w[2], w[3]));
             }
             auto mul = [&](float (&acc)[4], int nt, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
-              ps_mma<false>(acc, a0, a1, a2, a3, hi[nt][0], hi[nt][1], acc[0], acc[1], acc[2], acc[3]);
-              if constexpr (F16)
-                ps_mma<false>(acc, a0, a1, a2, a3, lo[nt][0], lo[nt][1], acc[0], acc[1], acc[2], acc[3]);
+              ps_mma(acc, a0, a1, a2, a3, wt[nt][0], wt[nt][1], acc[0], acc[1], acc[2], acc[3]);
             };
             if constexpr (G::ONES) {
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mul(wsum[g * NT + nt], nt, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+              for (int nt = 0; nt < NT; ++nt) mul(wsum[g * NT + nt], nt, MID_LO, MID_HI, MID_LO, MID_HI);
             }
             // this lane's codes: dimensions g GS + r8 GS / 8 ..., of keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
             constexpr int VW = GS * BITS / 256;   // words per lane, group and key (0: half a word)
@@ -588,42 +589,27 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             // product j of the group: dimensions r8 GS / 8 + 2 j (rows 0-7) and + 2 j + 1 (rows 8-15)
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
+              // 4-bit: a pair word holds four dimensions, two of them after a shift by 8; the odd ones count 16-fold (rows 8-15
+              // are a dimension of their own: divided at the end). 8-bit: two dimensions
+              uint32_t a[4];
               if constexpr (BITS == 4) {
-                const int i = j / 2, sh = 8 * (j & 1);
-                uint32_t a[4] = {pa[i] >> sh, pa[i] >> (sh + 4), pb[i] >> sh, pb[i] >> (sh + 4)};
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  a[x] = ps_or(a[x], 0x000F000Fu, 0x43004300u);
-                  if constexpr (!G::ONES) {
-                    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[x]),
-                                                     __floats2bfloat162_rn(136.f, 136.f));
-                    a[x] = *reinterpret_cast<const uint32_t*>(&v);
-                  }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mul(o[(g * KS + j) * NT + nt], nt, a[0], a[1], a[2], a[3]);
+                const uint32_t u = (j & 1) ? pa[j / 2] >> 8 : pa[j / 2], v = (j & 1) ? pb[j / 2] >> 8 : pb[j / 2];
+                a[0] = u & 0x000F000Fu;
+                a[1] = u & 0x00F000F0u;
+                a[2] = v & 0x000F000Fu;
+                a[3] = v & 0x00F000F0u;
               } else {
-                // one pair word holds two dimensions: low byte 2 j, high byte 2 j + 1; nibbles in two products
-                uint32_t a[4] = {pa[j], pa[j] >> 8, pb[j], pb[j] >> 8}, b[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                  b[x] = ps_or(a[x] >> 4, 0x000F000Fu, 0x45004500u);   // 2048 + 16 * high nibble
-                  a[x] = ps_or(a[x], 0x000F000Fu, 0x43004300u);        // 128 + low nibble
-                  if constexpr (!G::ONES) {
-                    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b[x]),
-                                                     __floats2bfloat162_rn(2176.f, 2176.f));
-                    b[x] = *reinterpret_cast<const uint32_t*>(&v);
-                    const __nv_bfloat162 u = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a[x]),
-                                                     __floats2bfloat162_rn(128.f, 128.f));
-                    a[x] = *reinterpret_cast<const uint32_t*>(&u);
-                  }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  mul(o[(g * KS + j) * NT + nt], nt, a[0], a[1], a[2], a[3]);
-                  mul(o[(g * KS + j) * NT + nt], nt, b[0], b[1], b[2], b[3]);
-                }
+                a[0] = pa[j] & 0x00FF00FFu;
+                a[1] = (pa[j] >> 8) & 0x00FF00FFu;
+                a[2] = pb[j] & 0x00FF00FFu;
+                a[3] = (pb[j] >> 8) & 0x00FF00FFu;
               }
+              if constexpr (!G::ONES) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) a[x] = ps_sub2(a[x], (x & 1) ? MID_HI : MID_LO);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mul(o[(g * KS + j) * NT + nt], nt, a[0], a[1], a[2], a[3]);
             }
           }
         }
@@ -634,6 +620,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       // ---- the warps' results, 8 query rows at a time, through shared memory (the rings are empty now)
       const bool whole = j0 == 0 && j1 == nblk;
       const int slot = 2 * cta + (mine ? 1 : 0);
+      const float back = __uint_as_float((uint32_t)(127 - vexp) << 23);   // from the weights' unit
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -661,13 +648,17 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             float e = vb[g * NT + nt][j];
 #pragma unroll
             for (int sh = 4; sh <= 16; sh <<= 1) e += __shfl_xor_sync(0xffffffffu, e, sh);
-            if constexpr (G::ONES) e = fmaf(-VADD, wsum[g * NT + nt][j], e);
             e *= f[j];
+            const float f0 = f[j] * GREAT, f1 = BITS == 4 ? f0 * 0.0625f : f0;
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
               float* dst = comb + (warp * 8 + 2 * c4 + j) * D + g * GS + r8 * (GS / 8) + 2 * i;
-              const float* oo = o[(g * KS + i) * NT + nt];
-              *reinterpret_cast<float2*>(dst) = make_float2(fmaf(oo[j], f[j], e), fmaf(oo[j + 2], f[j], e));
+              float x = o[(g * KS + i) * NT + nt][j], y = o[(g * KS + i) * NT + nt][j + 2];
+              if constexpr (G::ONES) {
+                x -= wsum[g * NT + nt][j];
+                y -= wsum[g * NT + nt][j + 2];
+              }
+              *reinterpret_cast<float2*>(dst) = make_float2(fmaf(x * f0, back, e), fmaf(y * f1, back, e));
             }
           }
         }

@@ -327,6 +327,14 @@ int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, 
 /* Workspace in bytes that qdecode_paged_attn needs for these arguments on the current device, whatever the lengths. */
 int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max_q, int D, int GS, int bits, size_t* bytes);
 
+/*
+ * qdecode_paged_packed: the calls above for bindings whose foreign calls cost by the argument: op 0 = qdecode_paged_map, 1 =
+ * qdecode_paged_append, 2 = qdecode_paged_attn; args holds that call's arguments in order, each widened to 64 bits
+ * (pointers as integers, the stream last). QDA_ERR_INVALID for another op, null args or a value beyond its parameter's
+ * range.
+ */
+int qdecode_paged_packed(int op, const int64_t* args);
+
 /* Human-readable text for a status code (static storage). */
 const char* qdecode_attn_strerror(int status);
 

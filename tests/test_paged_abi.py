@@ -125,3 +125,22 @@ def test_attn_workspace_arguments(L, args, status):
     n = ctypes.c_size_t()
     assert L.qdecode_paged_attn_workspace_bytes(*args, ctypes.byref(n)) == status
     assert L.qdecode_paged_attn_workspace_bytes(*args, None) == INVALID
+
+
+def test_packed_calls(L):
+    """The packed form makes the same calls: the same answers, and refusals of its own."""
+    import struct
+    P = lambda *a: struct.pack(f"={len(a)}q", *a)  # noqa: E731
+    m = [*ptrs(9), 4, 8, 5, 16, 9, 0]
+    a = [*ptrs(2), 1024, 128, 1024, 128, *ptrs(9), 3, 8, 4, 16, 128, 64, 4, 1, 0]
+    t = [FAKE, 1024, 128, *ptrs(10), 5, 2, 2, 8, 2, 9, 16, 4, 1, 128, 64, 4, 1, 0]
+    call = L.qdecode_paged_packed
+    assert call(3, P(*m)) == call(-1, P(*m)) == call(0, None) == INVALID
+    for op, args, i, v, status in [(0, m, 9, 0, INVALID), (0, m, 12, 24, UNSUPPORTED), (0, m, 0, 0, INVALID),
+                                   (0, m, 13, 1 << 31, INVALID), (0, m, 6, FAKE + 2, ALIGN), (1, a, 7, 0, INVALID),
+                                   (1, a, 2, 1028, ALIGN), (1, a, 15, 0, 0), (1, a, 21, 3, UNSUPPORTED),
+                                   (2, t, 14, 0, INVALID), (2, t, 13, 0, 0), (2, t, 2, 4, ALIGN), (2, t, 24, 7, UNSUPPORTED),
+                                   (2, t, 17, 3, INVALID), (2, t, 20, -(1 << 40), INVALID)]:
+        x = list(args)
+        x[i] = v
+        assert call(op, P(*x)) == status, (op, i, v)
