@@ -6,7 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "qda_paged_sched.cuh"
+#include "qda_paged.h"
 #include "qda_ptx.cuh"
 
 namespace qda {
@@ -289,62 +289,30 @@ cudaError_t launch_append_types(const AppendParams& p, int D, bool f16, int src,
 
 // ------------------------------------------------------------------------------------------- merge of split tiles
 
-// out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M) over the CTAs c that share a tile, in CTA order. CTA (x, y) looks at the tile that starts in
-// piece x and goes on behind it, and takes 8 / WPR of its rows, WPR warps to a row: each folds every WPR-th part, then
-// the warps' sums meet in shared memory. Launched with programmatic dependent launch: the scan of the lengths overlaps
-// the kernel before it, whose parts it then waits for.
+// out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M) over the CTAs c that share a tile, in CTA order. CTA (x, y) takes the tile that starts in
+// piece x and goes on behind it (most CTAs find none and end), and 8 / WPR of its rows, WPR warps to a row: each folds every WPR-th part, then
+// the warps' sums meet in shared memory. Launched with programmatic dependent launch, ahead of the end of the kernel before it.
 template <int D, int WPR>
-__global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_constant__ QdaPagedParams p, int MT, int KB) {
+__global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_constant__ QdaPagedParams p, int MT) {
   constexpr int E = D / 64;   // pairs of values per lane
-  __shared__ PagedLine line;
-  __shared__ PagedTile s_t;
-  __shared__ float2 s_o[8][D / 2];
+  __shared__ float2 s_o[WPR > 1 ? 8 : 1][D / 2];
   __shared__ float2 s_ml[8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
-  paged_line(p, MT, line);
-  const long long total = line.at[p.B];
-  const int ctas = total == 0 ? 0 : paged_ctas(total, p.ctas, p.min_keys);
-  bool work = c + 1 < ctas;
-  if (work) {
-    if (tid == 0) s_t = paged_tile_at(p, line, MT, paged_border(total, ctas, c + 1));
-    __syncthreads();
-  }
-  const PagedTile& t = s_t;
-  int nblk = 0, last = c;   // the last CTA that shares the tile
-  if (work) {
-    nblk = (paged_tile_keys(p, t, MT) + KB - 1) / KB;
-    work = t.lo >= paged_border(total, ctas, c) && t.lo < paged_border(total, ctas, c + 1) && nblk > 0;
-  }
-  if (work) {   // a CTA that had every block wrote the tile itself
-    bool whole = false;
-    for (int k = c + tid; k < ctas; k += 256) {
-      const long long a = paged_border(total, ctas, k), b = paged_border(total, ctas, k + 1);
-      if (a >= t.hi) break;
-      whole = whole || (paged_block_at(t, nblk, a) == 0 && paged_block_at(t, nblk, b) == nblk);
-    }
-    work = !__syncthreads_or(whole);
-    // the CTA that holds the tile's end
-    int lo = c, hi = ctas;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (paged_border(total, ctas, mid) < t.hi) lo = mid; else hi = mid;
-    }
-    last = lo;
-  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
   pdl_wait();
-  if (!work) return;
+  const QdaPagedSplitTile t = p.split[c];
+  if (!t.go || (int)blockIdx.y * (8 / WPR) >= t.rows) return;
+  const int last = t.last;
   const int r = blockIdx.y * (8 / WPR) + warp / WPR, part = warp % WPR;
-  const bool live = t.i * MT + r < t.s.rows;
+  const bool live = r < t.rows;
   float m = -INFINITY, l = 0.f;
   float2 o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = make_float2(0.f, 0.f);
   if (live) {
-#pragma unroll 2
+#pragma unroll 4
     for (int k = c + part; k <= last; k += WPR) {
-      const int j0 = paged_block_at(t, nblk, paged_border(total, ctas, k));
-      const int j1 = paged_block_at(t, nblk, paged_border(total, ctas, k + 1));
-      if (j0 >= j1) continue;   // wrote nothing
+      const QdaPagedSplitTile& rk = p.split[k];
+      if (!(k == c ? rk.last_filled : rk.first_filled)) continue;
       const size_t at = (size_t)(2 * k + (k == c)) * MT + r;
       const float2 ml = p.part_ml[at];
       const float2* po = reinterpret_cast<const float2*>(p.part_o + at * D);
@@ -385,9 +353,9 @@ __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_const
   }
   if (!live) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int row = t.i * MT + r, tok = row / p.nrep;
+  const int row = t.row0 + r, tok = row / p.nrep;
   uint32_t* dst = reinterpret_cast<uint32_t*>(
-      p.out + ((long long)(t.s.first + tok) * p.H + (t.unit / p.parts) * p.nrep + (row - tok * p.nrep)) * p.D +
+      p.out + ((long long)(t.token0 + tok) * p.H + (t.unit / p.parts) * p.nrep + (row - tok * p.nrep)) * p.D +
       (t.unit % p.parts) * D);
 #pragma unroll
   for (int e = 0; e < E; ++e)
@@ -395,7 +363,7 @@ __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_const
 }
 
 template <int D>
-cudaError_t launch_merge(const QdaPagedParams& p, int rows, int kb, cudaStream_t s) {
+cudaError_t launch_merge(const QdaPagedParams& p, int rows, cudaStream_t s) {
   // few rows per tile: a tile may be shared by many CTAs, so eight warps fold one row; many rows: a warp each
   const bool few = rows <= 16;
   cudaLaunchConfig_t cfg = {};
@@ -407,8 +375,8 @@ cudaError_t launch_merge(const QdaPagedParams& p, int rows, int kb, cudaStream_t
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 8>, p, rows, kb)
-             : cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 1>, p, rows, kb);
+  return few ? cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 8>, p, rows)
+             : cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 1>, p, rows);
 }
 
 bool good_page(int page) { return page >= QDA_PAGE_MIN && page <= QDA_PAGE_MAX && (page & (page - 1)) == 0; }
@@ -438,8 +406,8 @@ int check_pool(int num_pages, int page) {
 // The kernel a call takes, from what the host knows: the shape and the bound on a sequence's new tokens.
 struct PagedPlan {
   bool chunk;              // the chunk kernel (else the split kernel)
-  int rows, kb, ctas, min_keys, parts;
-  size_t o_bytes, bytes;   // workspace: partial outputs, and with the (reference, sum) pairs
+  int rows, ctas, min_keys, parts;
+  size_t o_bytes, ml_bytes, bytes;   // workspace: partial outputs, (reference, sum) pairs, all with the split tiles
 };
 
 using SplitFn = cudaError_t (*)(const QdaPagedParams*, int, int, int, int*, cudaStream_t);
@@ -464,7 +432,6 @@ int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int
   plan->chunk = rows > kSplitRows;
   if (plan->chunk) {
     plan->rows = rows > 128 && D <= 128 ? 256 : 128;
-    plan->kb = 128;
     plan->min_keys = 512;
     plan->parts = D == 512 ? 2 : 1;
     plan->ctas = sms;
@@ -477,8 +444,7 @@ int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int
     }
   } else {
     plan->rows = rows > 8 && D <= 256 ? 16 : 8;
-    plan->kb = D * bits / 8 <= 64 ? 32 : 16;
-    plan->min_keys = 256;
+    plan->min_keys = 128;
     plan->parts = 1;
     static std::atomic<int> cache[64][2][2][4][3][2] = {};   // resident CTAs per SM of an instance, 0 = not asked yet
     std::atomic<int>& slot = cache[dev][bits == 8][f16][di][gi][plan->rows == 16];
@@ -493,7 +459,8 @@ int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int
   }
   const size_t n = (size_t)2 * plan->ctas * plan->rows;
   plan->o_bytes = (n * (D / plan->parts) * 4 + 255) & ~(size_t)255;
-  plan->bytes = plan->o_bytes + n * sizeof(float2);
+  plan->ml_bytes = (n * sizeof(float2) + 255) & ~(size_t)255;
+  plan->bytes = plan->o_bytes + plan->ml_bytes + plan->ctas * sizeof(QdaPagedSplitTile);
   return QDA_OK;
 }
 
@@ -502,12 +469,12 @@ bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 }  // namespace qda
 
-cudaError_t qda_launch_paged_merge(const QdaPagedParams& p, int rows, int kb, cudaStream_t s) {
+cudaError_t qda_launch_paged_merge(const QdaPagedParams& p, int rows, cudaStream_t s) {
   switch (p.D / p.parts) {
-    case 64: return qda::launch_merge<64>(p, rows, kb, s);
-    case 128: return qda::launch_merge<128>(p, rows, kb, s);
-    case 256: return qda::launch_merge<256>(p, rows, kb, s);
-    default: return qda::launch_merge<512>(p, rows, kb, s);
+    case 64: return qda::launch_merge<64>(p, rows, s);
+    case 128: return qda::launch_merge<128>(p, rows, s);
+    case 256: return qda::launch_merge<256>(p, rows, s);
+    default: return qda::launch_merge<512>(p, rows, s);
   }
 }
 
@@ -680,6 +647,7 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   if (st != QDA_OK) return st;
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + plan.o_bytes);
+  p.split = reinterpret_cast<QdaPagedSplitTile*>(static_cast<char*>(ws) + plan.o_bytes + plan.ml_bytes);
   p.ctas = plan.ctas;
   p.parts = plan.parts;
   p.units = Hkv * plan.parts;
@@ -687,7 +655,7 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = plan.chunk ? chunk_run(&p, D, bits, plan.rows, false, s)
                              : split_fn(bits, p.f16 != 0)(&p, D, GS, plan.rows, nullptr, s);
-  if (e == cudaSuccess) e = qda_launch_paged_merge(p, plan.rows, plan.kb, s);
+  if (e == cudaSuccess) e = qda_launch_paged_merge(p, plan.rows, s);
   return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
 }
 

@@ -5,6 +5,14 @@
 
 #define QDA_ERR_BIT_PAGED 8u   // device status: a page, slot or length outside its pool or table
 
+// What a CTA of the attention kernels leaves for the merge: the tile that starts in its piece of the work and goes on behind it, and which of its
+// two slots (a tile that started before its piece, and one that starts in it) hold a part.
+struct QdaPagedSplitTile {
+  int go, last;                     // there is such a tile; the last CTA that shares it
+  int row0, rows, token0, unit;     // its query rows, the sequence's first token, the unit
+  int first_filled, last_filled;
+};
+
 // Launch parameters of the paged attention kernels (passed by value as a __grid_constant__).
 struct QdaPagedParams {
   const uint16_t* q;          // row t, head h at t * q_tstride + h * q_hstride
@@ -25,6 +33,7 @@ struct QdaPagedParams {
   // how the call is shared among CTAs (qda_paged_sched.cuh)
   int ctas, min_keys;         // CTAs launched; fewest keys of a CTA's piece
   int units, parts;           // units of a sequence: Hkv * parts, unit u holds part u % parts of KV head u / parts's values
+  QdaPagedSplitTile* split;   // [ctas]
   float* part_o;              // [2 * ctas, MT, D / parts] unnormalised partial outputs of split tiles
   float2* part_ml;            // [2 * ctas, MT] (reference in log2 units, sum of weights)
 };
@@ -46,5 +55,5 @@ cudaError_t qda_paged_split_b8_f1(const QdaPagedParams* p, int D, int GS, int ro
 cudaError_t qda_paged_chunk_b4(const QdaPagedParams* p, int D, int tiles, bool prepare, cudaStream_t s);
 cudaError_t qda_paged_chunk_b8(const QdaPagedParams* p, int D, int tiles, bool prepare, cudaStream_t s);
 
-// Merge of the split tiles' partial results, behind a kernel of `rows` rows per tile and key blocks of kb keys.
-cudaError_t qda_launch_paged_merge(const QdaPagedParams& p, int rows, int kb, cudaStream_t s);
+// Merge of the split tiles' partial results, behind a kernel of `rows` rows per tile.
+cudaError_t qda_launch_paged_merge(const QdaPagedParams& p, int rows, cudaStream_t s);

@@ -265,14 +265,14 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
   }
   PagedLine& line = *reinterpret_cast<PagedLine*>(ring);   // before the first slot is filled
   paged_line(p, MT, line);
-  const long long total = line.at[p.B];
-  if (total == 0) return;
-  const int ctas = paged_ctas(total, p.ctas, p.min_keys), cta = blockIdx.x;
-  if (cta >= ctas) return;
+  const int cta = blockIdx.x;
+  const PagedPieces pieces = paged_pieces(p, line.at[p.B]);
+  if (tid == 0) p.split[cta] = QdaPagedSplitTile{};
+  if (cta >= pieces.ctas) return;
   if (warp == W_MMA) tmem_alloc(&sh.tmem, 512);
   if (tid == 0) {
-    sh.x[0] = paged_border(total, ctas, cta);
-    sh.x[1] = paged_border(total, ctas, cta + 1);
+    sh.x[0] = paged_border(pieces, cta);
+    sh.x[1] = paged_border(pieces, cta + 1);
     sh.t = paged_tile_at(p, line, MT, sh.x[0]);
   }
   tc_fence_before();
@@ -835,6 +835,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
             }
           }
           __syncwarp();
+          if (lane == 0 && (t.lo < sh.x[0] || t.hi > sh.x[1])) paged_record(p, pieces, t, MT, nblk, j0, j1, cta);
           if (lane == 0) sh.more = sh.x[1] > sh.t.hi && paged_tile_next(p, MT, sh.t);
           __syncwarp();
           more = sh.more != 0;

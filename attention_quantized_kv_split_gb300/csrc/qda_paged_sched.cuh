@@ -15,27 +15,28 @@
 
 namespace qda {
 
-// Keys of a tile's fixed work (its query rows, its epilogue) on the line.
+// A tile's fixed work (its query rows, its epilogue), in keys.
 constexpr int kTileCost = 64;
 
 struct PagedSeq {
   int rows, tiles, n_all, first;   // query rows and tiles, keys, first token's row in q
   int base;                        // causal: keys before the first new token (may be negative); cross: keys
-  long long step2;                 // causal: MT (keys grow by step2 / nrep a tile); cross: 0
 };
 
-__device__ __forceinline__ PagedSeq paged_seq(const QdaPagedParams& p, int b, int MT) {
+// Sequence b from its first token's row, the next sequence's and its number of keys.
+__device__ __forceinline__ PagedSeq paged_seq(const QdaPagedParams& p, int start, int end, int n, int MT) {
   PagedSeq s;
-  const int q0 = min(max(p.q_start[b], 0), p.total_q), q1 = min(max(p.q_start[b + 1], q0), p.total_q);
-  const long long cap = (long long)p.max_pages << p.page_shift;
-  const int n = max(p.kv_len[b], 0);
+  const int q0 = min(max(start, 0), p.total_q), q1 = min(max(end, q0), p.total_q);
+  n = max(n, 0);
   s.first = q0;
   s.rows = (q1 - q0) * p.nrep;
   s.tiles = (s.rows + MT - 1) / MT;
-  s.n_all = (int)min((long long)n, cap);
+  s.n_all = (int)min((long long)n, (long long)p.max_pages << p.page_shift);
   s.base = p.causal ? n - (q1 - q0) : s.n_all;
-  s.step2 = p.causal ? MT : 0;
   return s;
+}
+__device__ __forceinline__ PagedSeq paged_seq(const QdaPagedParams& p, int b, int MT) {
+  return paged_seq(p, p.q_start[b], p.q_start[b + 1], p.kv_len[b], MT);
 }
 
 // Keys that row r of the sequence sees.
@@ -43,14 +44,22 @@ __device__ __forceinline__ int paged_seen(const QdaPagedParams& p, const PagedSe
   return p.causal ? max(0, min(s.n_all, s.base + r / p.nrep + 1)) : s.n_all;
 }
 
-// Length of the sequence's first i tiles (of one unit) on the line.
-__device__ __forceinline__ long long paged_prefix(const QdaPagedParams& p, const PagedSeq& s, long long i) {
-  return i * (kTileCost + max(s.base, 0)) + s.step2 * (i * (i + 1) / 2) / p.nrep;
+// Length of the sequence's first i tiles (of one unit) on the line, in keys times nrep: no division.
+__device__ __forceinline__ long long paged_prefix(const QdaPagedParams& p, const PagedSeq& s, int MT, int i) {
+  const long long flat = (long long)i * ((kTileCost + max(s.base, 0)) * (long long)p.nrep);
+  return p.causal ? flat + (long long)MT * ((long long)i * (i + 1) / 2) : flat;
 }
 
-// The line's per-sequence starts, in shared memory: line[b] for b <= B.
+// a / b for a >= 0, b > 0; 64-bit division only where it is needed.
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  if (((unsigned long long)a | (unsigned long long)b) >> 32) return a / b;
+  return (uint32_t)a / (uint32_t)b;
+}
+
+// The line's per-sequence starts and the sequences' lengths, in shared memory.
 struct PagedLine {
   long long at[QDA_MAX_B + 1];
+  int start[QDA_MAX_B + 1], n[QDA_MAX_B];
   long long warp_tot[32];
 };
 
@@ -63,20 +72,27 @@ __device__ __forceinline__ void paged_line(const QdaPagedParams& p, int MT, Page
     const int b = b0 + tid;
     long long v = 0;
     if (b < p.B) {
-      const PagedSeq s = paged_seq(p, b, MT);
-      v = p.units * paged_prefix(p, s, s.tiles);
+      const int q0 = p.q_start[b], q1 = p.q_start[b + 1], n = p.kv_len[b];
+      line.start[b] = q0;
+      if (b + 1 == p.B) line.start[p.B] = q1;
+      line.n[b] = n;
+      const PagedSeq s = paged_seq(p, q0, q1, n, MT);
+      v = p.units * paged_prefix(p, s, MT, s.tiles);
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long x = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += x;
     }
-    if (lane == 31) line.warp_tot[warp] = v;
-    __syncthreads();
+    const bool one = p.B - b0 <= 32;   // the first warp holds all there is
+    if (!one && lane == 31) line.warp_tot[warp] = v;
+    if (!one) __syncthreads();
     long long before = carry, all = carry;
-    for (int w = 0; w < (nt + 31) / 32; ++w) {
-      if (w < warp) before += line.warp_tot[w];
-      all += line.warp_tot[w];
+    if (!one) {
+      for (int w = 0; w < nt / 32; ++w) {
+        if (w < warp) before += line.warp_tot[w];
+        all += line.warp_tot[w];
+      }
     }
     if (b < p.B) line.at[b + 1] = before + v;
     carry = all;
@@ -84,12 +100,19 @@ __device__ __forceinline__ void paged_line(const QdaPagedParams& p, int MT, Page
   }
 }
 
-// CTAs that share the line: as many as there are, but no piece shorter than min_keys.
-__device__ __forceinline__ int paged_ctas(long long total, int ctas, int min_keys) {
-  return (int)max(1LL, min((long long)ctas, total / min_keys));
+// The pieces of the line: equal, but none shorter than min_keys.
+struct PagedPieces {
+  long long total, piece;
+  int ctas;   // pieces that there are
+};
+__device__ __forceinline__ PagedPieces paged_pieces(const QdaPagedParams& p, long long total) {
+  PagedPieces c;
+  c.total = total;
+  c.piece = max(paged_div(total + p.ctas - 1, p.ctas), (long long)p.min_keys * p.nrep);
+  c.ctas = (int)paged_div(total + c.piece - 1, c.piece);
+  return c;
 }
-
-__device__ __forceinline__ long long paged_border(long long total, int ctas, int c) { return total / ctas * c + total % ctas * c / ctas; }
+__device__ __forceinline__ long long paged_border(const PagedPieces& c, int k) { return min(c.total, k * c.piece); }
 
 // A tile on the line.
 struct PagedTile {
@@ -107,20 +130,20 @@ __device__ __forceinline__ PagedTile paged_tile_at(const QdaPagedParams& p, cons
     if (line.at[mid] <= x) lo = mid; else hi = mid;
   }
   t.b = lo;
-  t.s = paged_seq(p, lo, MT);
-  const long long head = paged_prefix(p, t.s, t.s.tiles);
+  t.s = paged_seq(p, line.start[lo], line.start[lo + 1], line.n[lo], MT);
+  const long long head = paged_prefix(p, t.s, MT, t.s.tiles);
   const long long y = x - line.at[lo];
-  t.unit = (int)(y / head);
+  t.unit = (int)paged_div(y, head);
   const long long z = y - t.unit * head;
   int a = 0, e = t.s.tiles;
   while (e - a > 1) {
     const int mid = (a + e) >> 1;
-    if (paged_prefix(p, t.s, mid) <= z) a = mid; else e = mid;
+    if (paged_prefix(p, t.s, MT, mid) <= z) a = mid; else e = mid;
   }
   t.i = a;
   const long long at = line.at[lo] + t.unit * head;
-  t.lo = at + paged_prefix(p, t.s, t.i);
-  t.hi = at + paged_prefix(p, t.s, t.i + 1);
+  t.lo = at + paged_prefix(p, t.s, MT, t.i);
+  t.hi = at + paged_prefix(p, t.s, MT, t.i + 1);
   return t;
 }
 
@@ -137,7 +160,7 @@ __device__ __forceinline__ bool paged_tile_next(const QdaPagedParams& p, int MT,
     }
   }
   t.lo = t.hi;
-  t.hi = t.lo + paged_prefix(p, t.s, t.i + 1) - paged_prefix(p, t.s, t.i);
+  t.hi = t.lo + paged_prefix(p, t.s, MT, t.i + 1) - paged_prefix(p, t.s, MT, t.i);
   return true;
 }
 
@@ -150,7 +173,35 @@ __device__ __forceinline__ int paged_tile_keys(const QdaPagedParams& p, const Pa
 __device__ __forceinline__ int paged_block_at(const PagedTile& t, int nblk, long long x) {
   if (x <= t.lo) return 0;
   if (x >= t.hi) return nblk;
-  return (int)((x - t.lo) * nblk / (t.hi - t.lo));
+  return (int)paged_div((x - t.lo) * nblk, t.hi - t.lo);
+}
+
+// Behind CTA k's part [j0, j1) of tile t (one thread): what the merge has to know of the tile, if it starts in piece k and goes on behind it, and
+// which of the CTA's two slots it has filled.
+__device__ __forceinline__ void paged_record(const QdaPagedParams& p, const PagedPieces& c, const PagedTile& t, int MT,
+                                             int nblk, int j0, int j1, int k) {
+  QdaPagedSplitTile& r = p.split[k];
+  const bool mine = paged_border(c, k) <= t.lo;
+  const bool filled = j0 < j1 && !(j0 == 0 && j1 == nblk);
+  if (!mine) {
+    r.first_filled = filled;
+    return;
+  }
+  bool go = t.hi > paged_border(c, k + 1) && nblk > 0 && j1 < nblk;
+  // a CTA behind this one may have had every block (and written the tile itself)
+  for (int x = k + 1; go && x < c.ctas && paged_border(c, x) < t.hi; ++x) {
+    const int e = paged_block_at(t, nblk, paged_border(c, x + 1));
+    if (j1 == 0 && e == nblk) go = false;
+    if (e > 0) break;
+  }
+  r.last_filled = filled;
+  if (!go) return;
+  r.go = 1;
+  r.last = min((int)paged_div(t.hi - 1, c.piece), c.ctas - 1);
+  r.row0 = t.i * MT;
+  r.rows = min(MT, t.s.rows - t.i * MT);
+  r.token0 = t.s.first;
+  r.unit = t.unit;
 }
 
 }  // namespace qda

@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
   PagedLine& line = *reinterpret_cast<PagedLine*>(comb);   // before the first copy lands there
   paged_line(p, MT, line);
   const long long total = line.at[p.B];
-  if (total == 0) return;
-  const int ctas = paged_ctas(total, p.ctas, p.min_keys);
   const int cta = blockIdx.x;
-  if (cta >= ctas) return;
+  const PagedPieces pieces = paged_pieces(p, total);
+  if (tid == 0) p.split[cta] = QdaPagedSplitTile{};
+  if (cta >= pieces.ctas) return;
   if (tid == 0) {
-    s_x[0] = paged_border(total, ctas, cta);
-    s_x[1] = paged_border(total, ctas, cta + 1);
+    s_x[0] = paged_border(pieces, cta);
+    s_x[1] = paged_border(pieces, cta + 1);
     t = paged_tile_at(p, line, MT, s_x[0]);
   }
   __syncthreads();
@@ -696,6 +696,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       if (saw_absent && lane == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);
     }
     __syncthreads();   // the tile and the combine area are read before the next tile overwrites them
+    if (tid == 0 && (t.lo < s_x[0] || t.hi > s_x[1])) paged_record(p, pieces, t, MT, nblk, j0, j1, cta);
     if (tid == 0) s_more = s_x[1] > t.hi && paged_tile_next(p, MT, t);
     __syncthreads();
     if (!s_more) break;
