@@ -9,8 +9,8 @@
 //            operand values, exact. q goes in as fp16 after an exact scaling of each row by a power of two (bf16 has fewer significant
 //            bits and a wider range). Per group, s_g sum(c q) + b_g sum(q) is formed in fp32: the scores are right to fp32.
 //   values   rows = head dimension, k = keys, columns = query rows: the weight w = p s_g of each group is the B operand,
-//            rounded to fp16 (11 significant bits: next to nothing beside a bf16 result, as much as the one rounding of an fp16 one); a power of two that
-//            follows the largest scale met keeps it in range. To centre the codes on the middle of their range (so that the rounding of w meets
+//            rounded to fp16 (11 significant bits: next to nothing beside a bf16 result, as much as the one rounding of an fp16 one); all sums
+//            are taken in a unit 2^-vexp that follows the largest scale met and keeps w in range. To centre the codes on the middle of their range (so that the rounding of w meets
 //            values no larger than half a group's range), sum(w) of a group comes from one more product with A = the middle, or with
 //            many groups the middle is taken off the codes; the rest, sum(p (b_g + mid s_g)), stays in fp32.
 // Keys and query rows change places between the two products: one movmatrix per 8 x 8 weights.
@@ -99,16 +99,11 @@ __device__ __forceinline__ uint32_t ps_sub2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Byte offset of byte `at` of key row `row` within a stage's codes: 16-byte pieces XORed so that the operand reads (8 rows
-// at one column, and 4 rows two apart at neighbouring columns) fall on distinct banks.
+// What a key row's bytes are XORed with within a stage's codes: 32-byte pieces move over the banks so that the operand reads (8 rows at
+// one column, and 4 rows two apart at neighbouring columns) fall on distinct ones.
 template <int RB>
-__device__ __forceinline__ uint32_t ps_code_at(int row, int at) {
-  const uint32_t lin = row * RB + at;
-  if constexpr (RB < 128) {
-    return lin ^ (((lin >> 7) & 3u) << 5);
-  } else {
-    return lin ^ ((((uint32_t)row & 3u) ^ (((uint32_t)row >> 2) & 1u)) << 5);
-  }
+__host__ __device__ constexpr uint32_t ps_turn(int row) {
+  return (RB < 128 ? ((row * RB) >> 7) & 3 : (row & 3) ^ ((row >> 2) & 1)) << 5;
 }
 
 // N 16-bit values of a row's scales (or biases) from shared memory
@@ -176,6 +171,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
     qda_paged_split_kernel(const __grid_constant__ QdaPagedParams p) {
   using G = PsGeom<BITS, D, GS, NT>;
   constexpr int NG = G::NG, MT = G::MT, KPS = G::KPS, RB = G::RB, STAGES = G::STAGES;
+  constexpr int GSB = GS * BITS / 8;          // bytes of a group's codes
   constexpr int KS = GS / 16;                 // products per group and key tile, on either side
   constexpr float MID = BITS == 4 ? 8.f : 128.f;
   constexpr uint32_t MID_LO = BITS == 4 ? 0x00080008u : 0x00800080u, MID_HI = 0x00800080u;   // middle codes as operands
@@ -190,6 +186,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
   float* s_qs = reinterpret_cast<float*>(ps_smem + G::QF);   // [NG][MT] sums of q, times 2^-24
   const uint32_t ring = smem_addr(ps_smem + G::ROWS) + warp * STAGES * G::STAGE;
   float* comb = reinterpret_cast<float*>(ps_smem + G::ROWS);
+
+  const uint32_t koff = (r8 * RB + c4 * (GSB / 4)) ^ ps_turn<RB>(r8), voff = (2 * c4 * RB + r8 * (GSB / 8)) ^ ps_turn<RB>(2 * c4);
 
   pdl_launch_dependents();
   PagedLine& line = *reinterpret_cast<PagedLine*>(comb);   // before the first copy lands there
@@ -332,7 +330,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           for (int i = 0; i < G::CODE / 512; ++i) {
             const int at = (i * 32 + lane) * 16, key = at / RB, col = at % RB;
             const long long src = (row[KPS == 32 ? (i * 512 / RB) / 16 : 0] + (key & 15)) * RB + col;
-            const uint32_t dst = base + ps_code_at<RB>(key, col);
+            const uint32_t dst = base + ((key * RB + col) ^ ps_turn<RB>(key));
             ps_cp16(dst, reinterpret_cast<const char*>(p.kp) + src);
             ps_cp16(dst + G::CODE, reinterpret_cast<const char*>(p.vp) + src);
           }
@@ -369,7 +367,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       }
 
       uint32_t most = 0;        // 16-bit pattern of the largest value scale that the weights' unit allows
-      int vexp = 0;             // weights are taken times 2^vexp
+      float vexp = 0.f;         // everything that is summed is taken times 2^vexp, an integer
 
       look(0);
 #pragma unroll
@@ -386,7 +384,10 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           if (n0 >= keys) break;
           const bool gone = (absent >> (st * 2 + h)) & 1u;
           const bool edge = gone || n0 + 16 > least;
-          const uint32_t kcode = base, vcode = base + G::CODE;
+          // codes: key row r8 (and r8 + 8) at this lane's quarter of a group; key rows 2 c4, 2 c4 + 1 (and 8 behind) at its
+          // eighth. Stages lie on 128-byte borders: what moves within 128 bytes is an XOR, the rest a sum
+          const uint32_t kat = base + 16 * h * RB + koff, vat = base + G::CODE + 16 * h * RB + voff;
+          constexpr uint32_t UP8 = RB == 32 ? 64 : 0, ODD = RB >= 128 ? 32 : RB, ODD_UP = RB >= 128 ? RB : 0;
           const uint32_t sc = base + 2 * G::CODE + (16 * h + r8) * NG * 2;   // this lane's key rows: r8 and r8 + 8
           // ---- scores
           float s[NT][4];
@@ -403,9 +404,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             for (int g = 0; g < NG; ++g) {
               constexpr int KW = GS * BITS / 128;   // words per lane, group and row
               uint32_t w0[KW], w1[KW];
-              const int col = (g * GS + c4 * (GS / 4)) * BITS / 8;
-              ps_words<KW>(kcode + ps_code_at<RB>(16 * h + r8, col), w0);
-              ps_words<KW>(kcode + ps_code_at<RB>(16 * h + r8 + 8, col), w1);
+              ps_words<KW>((kat ^ (g * GSB & 127)) + (g * GSB & ~127), w0);
+              ps_words<KW>((kat ^ (g * GSB & 127) ^ UP8) + (g * GSB & ~127) + 8 * RB, w1);
               float acc[NT][4];
 #pragma unroll
               for (int j = 0; j < KS; ++j) {
@@ -495,8 +495,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
               most = min(big + (4u << SHIFT), INF - 1);
               const uint32_t w = big;
               const int e = (int)(__float_as_uint(ps_half<F16>(&w, 0)) >> 23) - 127;
-              const int ve = max(-126, min(2 - e, 126));
-              fo = ps_ex2((float)(ve - vexp));
+              const float ve = (float)max(-60, min(2 - e, 60));
+              fo = ps_ex2(ve - vexp);
               vexp = ve;
             }
 #pragma unroll
@@ -508,31 +508,28 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                 const float mn = fmaxf(m[nt][j], x);
-                // 0 at the first visible key (where the sums are 0, and the change of unit may be infinite)
-                const float f = mn == -INFINITY ? 1.f : ps_ex2(m[nt][j] - mn);
-                const float g1 = f == 0.f || m[nt][j] == -INFINITY ? 0.f : f * fo;
+                const float f = m[nt][j] == -INFINITY ? 0.f : ps_ex2(m[nt][j] - mn) * fo;   // no key was visible before: sums are 0
                 m[nt][j] = mn;
                 l[nt][j] *= f;
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                   vb[g * NT + nt][j] *= f;
                   if constexpr (G::ONES) {
-                    wsum[g * NT + nt][j] *= g1;
-                    wsum[g * NT + nt][j + 2] *= g1;
+                    wsum[g * NT + nt][j] *= f;
+                    wsum[g * NT + nt][j + 2] *= f;
                   }
                 }
 #pragma unroll
                 for (int i = 0; i < NG * KS; ++i) {
-                  o[i * NT + nt][j] *= g1;
-                  o[i * NT + nt][j + 2] *= g1;
+                  o[i * NT + nt][j] *= f;
+                  o[i * NT + nt][j + 2] *= f;
                 }
               }
             }
           }
-          const float vfac = __uint_as_float((uint32_t)(127 + vexp) << 23);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+            const float m0 = (m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - vexp, m1 = (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - vexp;
             s[nt][0] = ps_ex2(s[nt][0] - m0);
             s[nt][1] = ps_ex2(s[nt][1] - m1);
             s[nt][2] = ps_ex2(s[nt][2] - m0);
@@ -548,18 +545,18 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             uint32_t wt[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float w[4] = {s[nt][0] * vfac * s0, s[nt][1] * vfac * s0, s[nt][2] * vfac * s1, s[nt][3] * vfac * s1};
-              float e[4] = {s[nt][0] * c0, s[nt][1] * c0, s[nt][2] * c1, s[nt][3] * c1};
-              if (edge) {   // a hidden key's scale and bias may be anything
+              float w[4] = {s[nt][0] * s0, s[nt][1] * s0, s[nt][2] * s1, s[nt][3] * s1};
+              if (!edge) {
+                vb[g * NT + nt][0] = fmaf(s[nt][0], c0, fmaf(s[nt][2], c1, vb[g * NT + nt][0]));
+                vb[g * NT + nt][1] = fmaf(s[nt][1], c0, fmaf(s[nt][3], c1, vb[g * NT + nt][1]));
+              } else {   // a hidden key's scale and bias may be anything
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                   const bool no = (hidden >> (4 * nt + j)) & 1u;
                   w[j] = no ? 0.f : w[j];
-                  e[j] = no ? 0.f : e[j];
+                  vb[g * NT + nt][j & 1] += no ? 0.f : s[nt][j] * (j < 2 ? c0 : c1);
                 }
               }
-              vb[g * NT + nt][0] += e[0] + e[2];
-              vb[g * NT + nt][1] += e[1] + e[3];
               wt[nt][0] = ps_trans(ps_h2(w[0], w[1]));
               wt[nt][1] = ps_trans(ps_h2(w[2], w[3]));
             }
@@ -573,10 +570,10 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             // this lane's codes: dimensions g GS + r8 GS / 8 ..., of keys 2 c4, 2 c4 + 1, 2 c4 + 8, 2 c4 + 9
             constexpr int VW = GS * BITS / 256;   // words per lane, group and key (0: half a word)
             uint32_t kw[4][VW ? VW : 1];
-            const int col = (g * GS + r8 * (GS / 8)) * BITS / 8;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              ps_words<VW>(vcode + ps_code_at<RB>(16 * h + 2 * c4 + (x & 1) + (x >> 1) * 8, col), kw[x]);
+              ps_words<VW>((vat ^ (g * GSB & 127) ^ ((x & 1) ? ODD : 0u) ^ ((x >> 1) ? UP8 : 0u)) + (g * GSB & ~127) +
+                               (x & 1) * ODD_UP + (x >> 1) * 8 * RB, kw[x]);
             // pairs of keys: 16 bits of codes of either
             constexpr int PW = VW ? 2 * VW : 1;
             uint32_t pa[PW], pb[PW];   // keys (2 c4, 2 c4 + 1) and those 8 behind
@@ -620,7 +617,6 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       // ---- the warps' results, 8 query rows at a time, through shared memory (the rings are empty now)
       const bool whole = j0 == 0 && j1 == nblk;
       const int slot = 2 * cta + (mine ? 1 : 0);
-      const float back = __uint_as_float((uint32_t)(127 - vexp) << 23);   // from the weights' unit
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -629,7 +625,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           for (int sh = 4; sh <= 16; sh <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], sh);
           if (r8 == 0) {
             s_ml[nt][warp][0][2 * c4 + j] = m[nt][j];
-            s_ml[nt][warp][1][2 * c4 + j] = l[nt][j];
+            s_ml[nt][warp][1][2 * c4 + j] = l[nt][j] * ps_ex2(-vexp);
           }
         }
         __syncthreads();   // also: every warp is through with its ring (or with the last 8 rows)
@@ -639,7 +635,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           float M = -INFINITY;
 #pragma unroll
           for (int w = 0; w < kPsWarps; ++w) M = fmaxf(M, s_ml[nt][w][0][2 * c4 + j]);
-          f[j] = m[nt][j] == -INFINITY ? 0.f : ps_ex2(m[nt][j] - M);
+          f[j] = m[nt][j] == -INFINITY ? 0.f : ps_ex2(m[nt][j] - M - vexp);
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -658,7 +654,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
                 x -= wsum[g * NT + nt][j];
                 y -= wsum[g * NT + nt][j + 2];
               }
-              *reinterpret_cast<float2*>(dst) = make_float2(fmaf(x * f0, back, e), fmaf(y * f1, back, e));
+              *reinterpret_cast<float2*>(dst) = make_float2(fmaf(x, f0, e), fmaf(y, f1, e));
             }
           }
         }
