@@ -150,35 +150,39 @@ __device__ __forceinline__ uint32_t to_bits16x2(float lo, float hi) {
   }
 }
 
+// The quantizer's code of x.
+__device__ __forceinline__ float exact_code(float x, float b, float s, float qmax) {
+  return s == 0.f ? 0.f : fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, b), s)), 0.f), qmax);
+}
+
 struct AppendParams {
   const void *k, *v;
   long long kt, kh, vt, vh;      // strides of k and v in elements
   const int* slots;
   uint32_t *kp, *vp;
   uint16_t *ks, *kb, *vs, *vb, *k_held, *v_held;
-  long long rows;                // T * Hkv
+  uint32_t rows;                 // T * Hkv
   int Hkv, pool_slots, page_shift, GS;
   unsigned int* err;
 };
 
-// A row of D values takes D / E lanes of E consecutive values (E = 8, 16 at D = 512): 16 bytes or more per load of the
-// 16-bit types and whole words of codes per lane. A group spans GS / E lanes (minimum and maximum by shuffles). The arithmetic is the quantizer's,
+// A row of D values takes D / E lanes of E = 8 consecutive values (two warps at D = 512; 16 values a lane measured 5 % slower there: fewer warps
+// fit): 16 bytes or more per load and whole words of codes per lane. A group spans GS / E lanes of one warp (minimum and maximum by shuffles). The arithmetic is the quantizer's,
 // in IEEE fp32. K and V of a row go to the same lanes, both loads in flight together. Bound by HBM.
 template <int BITS, int E, int LANES, bool F16, int SRC>
 __global__ void __launch_bounds__(256) qda_paged_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int D = LANES * E, PER = 32 / BITS, W = D / PER, WL = E / PER;
   constexpr float QMAX = (float)((1 << BITS) - 1);
-  const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / LANES;
+  const uint32_t row = blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
   const bool live = row < p.rows;   // a warp may hold several rows: all its lanes stay for the shuffles
   const int lane = threadIdx.x % LANES;
-  const long long rr = live ? row : p.rows - 1;
-  const long long t = rr / p.Hkv;
-  const int h = (int)(rr - t * p.Hkv);
+  const uint32_t rr = live ? row : p.rows - 1, t = rr / (uint32_t)p.Hkv;
+  const int h = (int)(rr - t * (uint32_t)p.Hkv);
   const int slot = p.slots[t];
   float x[2][E];
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
-    const long long at = w == 0 ? t * p.kt + h * p.kh : t * p.vt + h * p.vh;
+    const long long at = w == 0 ? (long long)t * p.kt + h * p.kh : (long long)t * p.vt + h * p.vh;
     const void* src = w == 0 ? p.k : p.v;
     if constexpr (SRC == QDA_FP32) {
       const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at + lane * E);
@@ -222,11 +226,40 @@ __global__ void __launch_bounds__(256) qda_paged_append_kernel(const __grid_cons
     }
     const uint32_t sb = to_bits16<F16>(__fdiv_rn(__fsub_rn(hi, lo), QMAX)), bb = to_bits16<F16>(lo);
     const float s = half_bits_to_float<F16>(sb), b = half_bits_to_float<F16>(bb);
-    float c[E];
+    // code = clamp(rint(RN((x - b) / s))), without the division: the product with 1 / s is off by less than 2^-14 in the codes' range
+    // (q 2^-23 and the quotient's own rounding, q < 258). Adding 1.5 * 2^23 rounds to the nearest integer, ties to even, and leaves it in the
+    // low bits. A value within 2^-14 of the middle m between two codes (common: the inputs are coarse) is decided by the remainder d - m s, whose
+    // sign a fused multiply-add gives exactly: |d - m s| up to s times half a step of m means that the quotient rounds to m itself
+    // (it never lies halfway between two floats), a tie.
+    constexpr float ROUND = 12582912.f, NEAR = 0.5f - 6.2e-5f;
+    const bool plain = s >= 1e-30f && s <= 1e30f && fabsf(b) <= 1e30f;
+    const float inv = plain ? __frcp_rn(s) : 0.f;
+    float r[E];   // code + ROUND
+    float off = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float r = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[w][e], b), s)), 0.f), QMAX);
-      c[e] = s == 0.f ? 0.f : r;
+      const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[w][e], b), inv), 0.f), QMAX);
+      r[e] = __fadd_rn(q, ROUND);
+      off = fmaxf(off, fabsf(__fsub_rn(q, __fsub_rn(r[e], ROUND))));
+    }
+    if (off > NEAR) {
+      const float s24 = s * 5.9604644775390625e-8f;   // s 2^-24
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float d = __fsub_rn(x[w][e], b);
+        const float q = fminf(fmaxf(__fmul_rn(d, inv), 0.f), QMAX), c = __fsub_rn(r[e], ROUND);
+        const uint32_t side = __float_as_uint(__fsub_rn(q, c)) & 0x80000000u;
+        const float m = c + __uint_as_float(0x3f000000u | side);                           // the nearest middle
+        const float rest = __uint_as_float(__float_as_uint(__fmaf_rn(-m, s, d)) ^ side);   // > 0: beyond it
+        const float step = s24 * __uint_as_float(__float_as_uint(m) & 0x7f800000u);
+        // beyond by more than step: the next code; within: the even one of the two
+        const float edge = __float_as_uint(r[e]) & 1u ? -step : step;
+        if (rest > edge) r[e] = fminf(__fadd_rn(r[e], __uint_as_float(0x3f800000u | side)), ROUND + QMAX);
+      }
+    }
+    if (!plain) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) r[e] = __fadd_rn(exact_code(x[w][e], b, s, QMAX), ROUND);
     }
     if (put) {
       uint32_t word[WL];
@@ -234,7 +267,7 @@ __global__ void __launch_bounds__(256) qda_paged_append_kernel(const __grid_cons
       for (int i = 0; i < WL; ++i) {
         word[i] = 0;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) word[i] |= (uint32_t)c[i * PER + j] << (BITS * j);
+        for (int j = 0; j < PER; ++j) word[i] |= (__float_as_uint(r[i * PER + j]) & 0xffu) << (BITS * j);
       }
       uint32_t* dst = (w == 0 ? p.kp : p.vp) + orow * W + lane * WL;
       if constexpr (WL == 1) {
@@ -250,13 +283,13 @@ __global__ void __launch_bounds__(256) qda_paged_append_kernel(const __grid_cons
       }
     }
     if (live && p.k_held != nullptr) {
-      uint4* dst = reinterpret_cast<uint4*>((w == 0 ? p.k_held : p.v_held) + rr * D + lane * E);
+      uint4* dst = reinterpret_cast<uint4*>((w == 0 ? p.k_held : p.v_held) + (size_t)rr * D + lane * E);
 #pragma unroll
       for (int i = 0; i < E / 8; ++i) {
         uint32_t u[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          u[j] = to_bits16x2<F16>(fmaf(s, c[8 * i + 2 * j], b), fmaf(s, c[8 * i + 2 * j + 1], b));
+          u[j] = to_bits16x2<F16>(fmaf(s, r[8 * i + 2 * j] - ROUND, b), fmaf(s, r[8 * i + 2 * j + 1] - ROUND, b));
         __stcs(dst + i, make_uint4(u[0], u[1], u[2], u[3]));
       }
     }
@@ -265,13 +298,13 @@ __global__ void __launch_bounds__(256) qda_paged_append_kernel(const __grid_cons
 
 template <int BITS, bool F16, int SRC>
 cudaError_t launch_append(const AppendParams& p, int D, cudaStream_t s) {
-  const int lanes = D == 512 ? 32 : D / 8;
-  const unsigned grid = (unsigned)((p.rows * lanes + 255) / 256);
+  const int lanes = D / 8;
+  const unsigned grid = (unsigned)(((long long)p.rows * lanes + 255) / 256);
   switch (D) {
     case 64: qda_paged_append_kernel<BITS, 8, 8, F16, SRC><<<grid, 256, 0, s>>>(p); break;
     case 128: qda_paged_append_kernel<BITS, 8, 16, F16, SRC><<<grid, 256, 0, s>>>(p); break;
     case 256: qda_paged_append_kernel<BITS, 8, 32, F16, SRC><<<grid, 256, 0, s>>>(p); break;
-    default: qda_paged_append_kernel<BITS, 16, 32, F16, SRC><<<grid, 256, 0, s>>>(p); break;
+    default: qda_paged_append_kernel<BITS, 8, 64, F16, SRC><<<grid, 256, 0, s>>>(p); break;
   }
   return cudaGetLastError();
 }
@@ -545,12 +578,12 @@ extern "C" int qdecode_paged_append(const void* k, const void* v, long long k_ts
   p.vb = static_cast<uint16_t*>(v_biases);
   p.k_held = static_cast<uint16_t*>(k_held);
   p.v_held = static_cast<uint16_t*>(v_held);
-  p.rows = (long long)T * Hkv;
+  if ((long long)T * Hkv * (D / 8) > 0x7fffffffLL * 256) return QDA_ERR_UNSUPPORTED;   // more than any GPU holds
+  p.rows = (uint32_t)((long long)T * Hkv);
   p.Hkv = Hkv;
   p.pool_slots = num_pages * page;
   p.page_shift = page_shift_of(page);
   p.GS = GS;
-  if ((p.rows * (D / 8) + 255) / 256 > 0x7fffffffLL) return QDA_ERR_UNSUPPORTED;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = bits == 4 ? launch_append_types<4>(p, D, cache == QDA_FP16, src, s)
                                   : launch_append_types<8>(p, D, cache == QDA_FP16, src, s);

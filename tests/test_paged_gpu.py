@@ -133,6 +133,36 @@ def test_append_bit_exact(D, GS, bits, cache, src, T, Hkv, page):
     assert qda.qdecode_attn_device_status() == 0
 
 
+@pytest.mark.parametrize("bits,cache", [(4, "bf16"), (8, "bf16"), (4, "fp16"), (8, "fp16")])
+def test_append_values_between_two_codes(bits, cache):
+    """Rows whose values lie on and next to the middle between two codes, tiny and huge groups, groups of one value, and
+    infinities and NaN: the codes are the quantizer's to the bit."""
+    D, GS, top = 128, 64, 2 ** bits - 1
+    rng = np.random.default_rng(bits)
+    rows = []
+    for scale in (1.0, 0.375, 2.0 ** -9, 3e-5, 1e-38, 3e4 if cache == "fp16" else 1e35):
+        x = (rng.integers(0, 2 * top, (8, D)) * 0.5 - 3) * scale / top     # whole and half codes
+        x[:, 0::GS], x[:, 1::GS] = -3 * scale / top, (top - 3) * scale / top
+        rows += [x, np.nextafter(x.astype(np.float32), np.float32(np.inf)), np.nextafter(x.astype(np.float32), -np.float32(np.inf))]
+    rows.append(rng.standard_normal((300, D)) * np.exp(rng.standard_normal((300, 1)) * 4))
+    odd = rng.standard_normal((6, D))
+    odd[0, 3], odd[1, 5], odd[2, 7], odd[3, :GS], odd[4, 9], odd[4, 10], odd[5] = np.nan, np.inf, -np.inf, np.nan, np.inf, -np.inf, 0
+    x = torch.from_numpy(np.concatenate(rows + [odd]).astype(np.float32)).cuda()
+    T = x.shape[0]
+    pages = -(-T // 16)
+    arr = pool_arrays(pages, 1, 16, D, GS, bits, DT[cache])
+    qda.qdecode_paged_append(x[:, None], x[:, None], i32(np.arange(T)), *arr, GS, bits)
+    packed = torch.empty(T, D * bits // 32, dtype=torch.int32, device="cuda")
+    sc, bi = (torch.empty(T, D // GS, dtype=DT[cache], device="cuda") for _ in range(2))
+    qda.qdecode_quantize(x, GS, bits, DT[cache], packed, sc, bi)
+    torch.cuda.synchronize()
+    for a in (0, 3):
+        for got, ref in zip(arr[a: a + 3], (packed, sc, bi)):
+            g = got.reshape(pages * 16, -1)[:T]
+            view = torch.int32 if g.dtype == torch.int32 else torch.int16
+            assert torch.equal(g.view(view), ref.view(view))
+
+
 def test_append_slots_outside_the_pool_are_skipped():
     T, Hkv, D = 6, 2, 128
     x = torch.randn(T, Hkv, D, device="cuda", dtype=torch.bfloat16)
