@@ -3,7 +3,7 @@
 // One CTA per SM takes a tile of 128 query rows of a KV head, or two of them side by side (D <= 128), and walks the tile's keys in blocks
 // of 128: S = Q K^T and O += P V on tcgen05 (fp16 operands, fp32 sums in tensor memory), an online softmax in between. Rows are (token, query head)
 // pairs, so all query heads of a KV head share a block's keys and values, which are turned from codes into operands once per block:
-//   dequantising warps   codes -> fp16 tiles in shared memory (a ring of slots of 128 keys x 128 dimensions), next slot's codes in flight in registers;
+//   dequantising warps   codes -> fp16 tiles in shared memory (a ring of slots of 128 keys x 128 dimensions, 64 at D = 64 and 512);
 //   softmax warps        one thread per query row: reads its row of S from tensor memory, writes P (fp16) over it;
 //   MMA warp             one thread issues every product. With two tiles the products of one run while the softmax of the other does;
 //                        with one tile S has two buffers and the next block's scores run during this block's softmax;
@@ -22,8 +22,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-
-#include <type_traits>
 
 #include "qda_paged_sched.cuh"
 
@@ -49,23 +47,25 @@ struct PcInfo {
 template <int D, int BITS, int NQ>
 struct PcGeom {
   static constexpr int MT = 128 * NQ;
-  static constexpr int SD = D < 128 ? D : 128;          // dimensions per slot
+  static constexpr int SD = D == 128 || D == 256 ? 128 : 64;   // dimensions per slot (D = 512: what fits beside its queries)
   static constexpr int DV = D < 256 ? D : 256;          // values' dimensions of a unit (TMEM holds O of no more)
   static constexpr int PARTS = D / DV;
   static constexpr int KSL = D / SD, VSL = DV / SD;     // slots of a block's keys and of its values
   static constexpr int SLOT = kPcKeys * SD * 2;
   static constexpr int QB = MT * D * 2;
-  static constexpr int SLOTS0 = (226 * 1024 - 1024 - QB) / SLOT;
-  static constexpr int SLOTS = SLOTS0 > 6 ? 6 : SLOTS0;
   static constexpr int SOFT = 4 * NQ;                   // softmax warps
   static constexpr int DEQ = 8;                         // dequantising warps
   static constexpr int WARPS = SOFT + DEQ + 1 + kPcInfoWarps;
+  static constexpr int NU = 128 * (SD / 32) / (DEQ * 32);   // units of 32 codes per dequantising thread and slot
+  static constexpr int STAGE = DEQ * 32 * NU * (4 * BITS + 8);   // a slot's codes, scales and biases as they are in memory
+  // stages of codes under way and slots of operands: what shared memory holds
+  static constexpr int STAGES = D == 128 && BITS == 4 && NQ == 2 ? 2 : 3;
+  static constexpr int SLOTS0 = (226 * 1024 - 1024 - QB - STAGES * STAGE) / SLOT;
+  static constexpr int SLOTS = SLOTS0 > 6 ? 6 : SLOTS0;
   // registers a thread: the launch's 96 (20 warps) or 128 (16 warps), dealt out anew among the warpgroups
   static constexpr int R_ALL = NQ == 2 ? 96 : 128;
-  static constexpr int R_SOFT = NQ == 2 ? 136 : 136, R_DEQ = NQ == 2 ? 72 : 136, R_LAST = NQ == 2 ? 64 : 96;
+  static constexpr int R_SOFT = NQ == 2 ? 136 : 136, R_DEQ = NQ == 2 ? 72 : 128, R_LAST = NQ == 2 ? 64 : 96;
   static_assert(SOFT * R_SOFT + DEQ * R_DEQ + 4 * R_LAST <= WARPS * R_ALL, "registers of the launch");
-  // items of codes under way: what the registers hold, and a divisor of a block's items less one
-  static constexpr int AHEAD = D <= 128 ? 1 : D == 256 ? 3 : BITS == 4 ? 5 : 2;
   static constexpr int O_COL = 256;                     // O behind two S buffers of 128 columns
   static_assert(NQ == 1 || D <= 128, "two tiles need room for two O");
   static_assert(SLOTS >= 3 && O_COL + NQ * DV <= 512, "shared or tensor memory");
@@ -96,7 +96,7 @@ struct PcShared {
 template <int D, int BITS, int NQ>
 constexpr int pc_smem() {
   using G = PcGeom<D, BITS, NQ>;
-  return 1024 + G::QB + G::SLOTS * G::SLOT + (int)sizeof(PcShared);
+  return 1024 + G::QB + G::SLOTS * G::SLOT + G::STAGES * G::STAGE + (int)sizeof(PcShared);
 }
 
 __device__ __forceinline__ float pc_ex2(float x) {
@@ -212,15 +212,6 @@ __device__ __forceinline__ void pc_regs() {
   if constexpr (N < LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// f(integral_constant<0>), ..., f(integral_constant<N - 1>)
-template <int N, int I = 0, typename F>
-__device__ __forceinline__ void pc_each(F&& f) {
-  if constexpr (I < N) {
-    f(std::integral_constant<int, I>{});
-    pc_each<N, I + 1>(f);
-  }
-}
-
 template <int D, int BITS, int NQ>
 __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     qda_paged_chunk_kernel(const __grid_constant__ QdaPagedParams p) {
@@ -233,7 +224,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
   unsigned char* base = pc_smem_raw + ((1024u - (smem_addr(pc_smem_raw) & 1023u)) & 1023u);
   unsigned char* q_s = base;
   unsigned char* ring = base + G::QB;
-  PcShared& sh = *reinterpret_cast<PcShared*>(ring + SLOTS * G::SLOT);
+  unsigned char* staged = ring + SLOTS * G::SLOT;
+  PcShared& sh = *reinterpret_cast<PcShared*>(staged + G::STAGES * G::STAGE);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int W_DEQ = G::SOFT, W_MMA = G::SOFT + DEQ;   // the info warps behind
   volatile int* abort = &sh.abort;
@@ -551,12 +543,12 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     // ========================================================================= codes -> fp16 tiles in shared memory
     pc_regs<G::R_DEQ, G::R_ALL>();
     constexpr int UPR = SD / 32;               // units of 32 codes (which share a scale) per row of a slot
-    constexpr int NU = 128 * UPR / (DEQ * 32);
-    constexpr int UW = BITS;                   // words of codes per unit
+    constexpr int NU = G::NU, STAGES = G::STAGES;
     constexpr int ROWB = D * BITS / 8;         // bytes of codes per row
-    constexpr int AHEAD = G::AHEAD;            // items whose codes are under way
+    constexpr int RSTEP = DEQ * 32 / UPR;      // rows between a thread's units
+    constexpr int P = KSL + VSL;
     const int id = tid - W_DEQ * 32;
-    const int row = id / UPR, q = id % UPR;    // this thread's units: unit q of rows row, row + threads / UPR, ...
+    const int row = id / UPR, q = id % UPR;    // this thread's units: unit q of rows row, row + RSTEP, ...
     const int gshift = 31 - __clz(p.GS);
     const uint32_t sstride = p.NG * 2;
     // where a unit's four 16-byte pieces of operand go in a slot: rows of 64 values, pieces XORed by the row. The order of the
@@ -568,103 +560,102 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
       const int piece = q * 4 + (u ^ turn);
       to[u] = (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
     }
-    struct Item {
-      uint32_t code[NU][UW];
-      uint32_t s[NU], b[NU];                   // as they are in memory: nothing waits for a load before its item's turn
-      uint32_t ok;                             // bit per unit: the key counts (else it is zero)
-    };
-    // The slots of a tile come in groups g = -1 ... n - 1 of KSL + VSL items: the keys of block g + 1, the values of block g
-    // (where there are such). Items are loaded AHEAD items before they are converted.
-    constexpr int P = KSL + VSL;
-    static_assert(P % (AHEAD + 1) == 0, "an item's registers are known at compile time");
-    Item reg[AHEAD + 1];
+    // Codes go through stages that a thread fills and reads by itself, 16 bytes a lane (no bank conflicts, nobody else to wait
+    // for): asynchronous copies hold no registers, and the loop is one body for keys and values (bodies for each kind
+    // of item, with the codes in registers, ran out of instruction cache).
+    constexpr int CU = BITS / 4;               // 16-byte pieces of codes per unit
+    const uint32_t stage0 = smem_addr(staged) + id * 16, scale0 = smem_addr(staged) + DEQ * 32 * NU * 4 * BITS + id * 8;
+    uint32_t filled = 0, taken = 0;            // stages filled and read so far
     for (int k = 0;; ++k) {
       const PcTile* t = tile_at(k);
       if (t == nullptr) break;
-      const int n = t->n, left0 = t->keys - t->j0 * kPcKeys;
-      const int vd0 = t->part * DV + 32 * q;
-      const char* ksrc = reinterpret_cast<const char*>(p.kp) + 4 * BITS * q;
-      const char* vsrc = reinterpret_cast<const char*>(p.vp) + vd0 * BITS / 8;
-      uint32_t prk[NU], prv[NU], okk = 0, okv = 0;   // pool rows of the block whose keys were loaded last, and of the one before
-#pragma unroll
-      for (int i = 0; i < NU; ++i) prk[i] = prv[i] = 0;
-      int kv_run = -126;
-      uint32_t at = ic;                              // slots so far
-      auto load = [&](auto item, int g) {
-        constexpr int X = decltype(item)::value;
-        constexpr bool VAL = X >= KSL;
-        constexpr int SL = VAL ? X - KSL : X;
-        if (VAL ? g < 0 : g + 1 >= n) return;
-        Item& it = reg[X % (AHEAD + 1)];
-        if constexpr (X == 0) {
-          const uint32_t x = bc + g + 1;
-          const PcInfo& f = sh.info[x % kPcInfo];
-          wait(&sh.info_full[x % kPcInfo], x / kPcInfo);
-          const int left = left0 - (g + 1) * kPcKeys;
-          okv = okk;
-          okk = 0;
-#pragma unroll
-          for (int i = 0; i < NU; ++i) {
-            const int r = row + i * (DEQ * 32 / UPR);
-            const uint32_t base = f.row[r >> 4];
-            const bool ok = base != kPcNoRow && r < left;
-            prv[i] = prk[i];
-            prk[i] = ok ? base + (r & 15) : 0u;
-            okk |= (uint32_t)ok << i;
-          }
-        } else if constexpr (X == KSL) {
-          if (g + 1 >= n) {   // the last group has no keys: its values are of the block whose keys came last
-            okv = okk;
-#pragma unroll
-            for (int i = 0; i < NU; ++i) prv[i] = prk[i];
-          }
-        }
-        const uint32_t goff = (((VAL ? vd0 : 32 * q) + SL * SD) >> gshift) * 2;
-        const char* src = (VAL ? vsrc : ksrc) + SL * SD * BITS / 8;
-        const char* ss = reinterpret_cast<const char*>(VAL ? p.vs : p.ks) + goff;
-        const char* bs = reinterpret_cast<const char*>(VAL ? p.vb : p.kb) + goff;
-        it.ok = VAL ? okv : okk;
-#pragma unroll
-        for (int i = 0; i < NU; ++i) {
-          const uint32_t pr = VAL ? prv[i] : prk[i];
-          const uint4* c = reinterpret_cast<const uint4*>(src + (uint64_t)pr * ROWB);
-#pragma unroll
-          for (int u = 0; u < UW / 4; ++u) {
-            const uint4 v = __ldg(c + u);
-            it.code[i][4 * u] = v.x;
-            it.code[i][4 * u + 1] = v.y;
-            it.code[i][4 * u + 2] = v.z;
-            it.code[i][4 * u + 3] = v.w;
-          }
-          it.s[i] = __ldg(reinterpret_cast<const uint16_t*>(ss + (uint64_t)pr * sstride));
-          it.b[i] = __ldg(reinterpret_cast<const uint16_t*>(bs + (uint64_t)pr * sstride));
+      const int n = t->n, left0 = t->keys - t->j0 * kPcKeys, vd0 = t->part * DV;
+      // The slots of a tile come in groups g = -1 ... n - 1 of P items: the slices of the keys of block g + 1, then of the values of block
+      // g (where there are such). Two cursors walk them: codes are sent for STAGES - 1 items before they are converted.
+      auto step = [&](int& g, int& z) {
+        if (++z == (g < 0 ? KSL : P)) {
+          ++g;
+          z = g + 1 < n ? 0 : KSL;
         }
       };
-      auto convert = [&](auto item, int g) {
-        constexpr int X = decltype(item)::value;
-        constexpr bool VAL = X >= KSL;
-        constexpr int SL = VAL ? X - KSL : X;
-        if (VAL ? g < 0 : g + 1 >= n) return;
-        const Item& it = reg[X % (AHEAD + 1)];
-        const PcInfo& f = sh.info[(bc + g + (VAL ? 0 : 1)) % kPcInfo];
-        if constexpr (VAL && SL == 0) kv_run = max(kv_run, f.kv);
-        const float fac = VAL ? __uint_as_float((uint32_t)(127 - kv_run) << 23) : f.kfac;
+      int ig = n > 0 ? -1 : n, iz = 0;
+      auto issue = [&]() {
+        if (ig < n) {
+          const bool val = iz >= KSL;
+          const int sl = val ? iz - KSL : iz, j = val ? ig : ig + 1;
+          const uint32_t x = bc + j;
+          if (iz == 0) wait(&sh.info_full[x % kPcInfo], x / kPcInfo);
+          const PcInfo& f = sh.info[x % kPcInfo];
+          const int d0 = (val ? vd0 : 0) + sl * SD + 32 * q;
+          const char* src = reinterpret_cast<const char*>(val ? p.vp : p.kp) + d0 * BITS / 8;
+          const uint32_t goff = (d0 >> gshift) * 2;
+          const char* ss = reinterpret_cast<const char*>(val ? p.vs : p.ks);
+          const char* bs = reinterpret_cast<const char*>(val ? p.vb : p.kb);
+          const uint32_t st = (filled % STAGES) * G::STAGE;
+#pragma unroll
+          for (int i = 0; i < NU; ++i) {
+            const int r = row + i * RSTEP;
+            const uint32_t base = f.row[r >> 4], pr = base == kPcNoRow ? 0u : base + (r & 15);
+            const char* c = src + (uint64_t)pr * ROWB;
+#pragma unroll
+            for (int u = 0; u < CU; ++u)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(stage0 + st + (i * CU + u) * DEQ * 512),
+                           "l"(c + 16 * u)
+                           : "memory");
+            const uint64_t at = ((uint64_t)pr * sstride + goff) & ~(uint64_t)3;   // the word that holds the 16 bits
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scale0 + st + i * DEQ * 256), "l"(ss + at) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scale0 + st + i * DEQ * 256 + 4), "l"(bs + at)
+                         : "memory");
+          }
+          ++filled;
+          step(ig, iz);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");   // an empty group keeps the count
+      };
+#pragma unroll
+      for (int x = 0; x < STAGES - 1; ++x) issue();
+      int kv_run = -126;
+      uint32_t at = ic;                              // slots so far
+      for (int g = n > 0 ? -1 : n, z = 0; g < n; step(g, z)) {
+        issue();
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+        const bool val = z >= KSL;
+        const int sl = val ? z - KSL : z, j = val ? g : g + 1;
+        const PcInfo& f = sh.info[(bc + j) % kPcInfo];
+        if (val) kv_run = max(kv_run, f.kv);
+        const float fac = val ? __uint_as_float((uint32_t)(127 - kv_run) << 23) : f.kfac;
         const bool odd = f.flags & 2u;
-        const uint32_t slot = at % SLOTS;
+        const int left = left0 - j * kPcKeys;
+        const uint32_t gsel = (((val ? vd0 : 0) + sl * SD + 32 * q) >> gshift) * 2;
+        const uint32_t slot = at % SLOTS, st = (taken % STAGES) * G::STAGE;
         wait(&sh.empty[slot], at / SLOTS + 1);
         ++at;
+        ++taken;
         const uint32_t dst = smem_addr(ring) + slot * G::SLOT;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
+          const int r = row + i * RSTEP;
+          const uint32_t base = f.row[r >> 4];
+          const bool ok = base != kPcNoRow && r < left;
+          uint32_t code[BITS], sw, bw;
+#pragma unroll
+          for (int u = 0; u < CU; ++u)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(code[4 * u]), "=r"(code[4 * u + 1]), "=r"(code[4 * u + 2]), "=r"(code[4 * u + 3])
+                         : "r"(stage0 + st + (i * CU + u) * DEQ * 512));
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(sw), "=r"(bw) : "r"(scale0 + st + i * DEQ * 256));
+          const uint32_t sh16 = ((base + (r & 15)) * sstride + gsel) & 2u ? 16 : 0;
+          sw >>= sh16;
+          bw >>= sh16;
           float s, b;
           if (p.f16) {
-            s = fp16_bits_to_float(it.s[i]);
-            b = fp16_bits_to_float(it.b[i]);
+            s = fp16_bits_to_float(sw & 0xffffu);
+            b = fp16_bits_to_float(bw & 0xffffu);
           } else {
-            s = __uint_as_float(it.s[i] << 16);
-            b = __uint_as_float(it.b[i] << 16);
+            s = __uint_as_float(sw << 16);
+            b = __uint_as_float(bw << 16);
           }
-          if (!((it.ok >> i) & 1u) || (odd && !(fmaxf(fabsf(s), fabsf(b)) < FINITE))) s = b = 0.f;
+          if (!ok || (odd && !(fmaxf(fabsf(s), fabsf(b)) < FINITE))) s = b = 0.f;
           s *= fac;
           b *= fac;
           const uint32_t s1 = pc_h2(s * 16777216.f, s * 16777216.f), s16 = pc_h2(s * 1048576.f, s * 1048576.f), b2 = pc_h2(b, b);
@@ -672,7 +663,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           for (int u = 0; u < 4; ++u) {
             uint32_t y[4];
             if constexpr (BITS == 4) {
-              const uint32_t w = turn ? it.code[i][u ^ 2] : it.code[i][u];
+              const uint32_t w = turn ? code[u ^ 2] : code[u];
               const uint32_t w8 = w >> 8;
               y[0] = pc_fma2(w & 0x000F000Fu, s1, b2);
               y[1] = pc_fma2(w & 0x00F000F0u, s16, b2);
@@ -681,13 +672,13 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
             } else {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t w = turn ? it.code[i][2 * (u ^ 2) + h] : it.code[i][2 * u + h];
+                const uint32_t w = turn ? code[2 * (u ^ 2) + h] : code[2 * u + h];
                 y[2 * h] = pc_fma2(w & 0x00FF00FFu, s1, b2);
                 y[2 * h + 1] = pc_fma2((w >> 8) & 0x00FF00FFu, s1, b2);
               }
             }
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + to[u] + i * (DEQ * 32 / UPR) * 128),
-                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + to[u] + i * RSTEP * 128), "r"(y[0]),
+                         "r"(y[1]), "r"(y[2]), "r"(y[3])
                          : "memory");
           }
         }
@@ -695,22 +686,14 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sh.full[slot]);
-          if (VAL && SL == VSL - 1) mbar_arrive(&sh.info_empty[(bc + g) % kPcInfo]);
+          if (val && sl == VSL - 1) mbar_arrive(&sh.info_empty[(bc + j) % kPcInfo]);
         }
-      };
-      if (n > 0) {
-        pc_each<AHEAD>([&](auto item) { load(item, -1); });
-        for (int g = -1; g < n; ++g)
-          pc_each<P>([&](auto item) {
-            constexpr int NEXT = decltype(item)::value + AHEAD;
-            load(std::integral_constant<int, NEXT % P>{}, g + NEXT / P);
-            convert(item, g);
-          });
       }
       bc += n;
       ic += n * P;
       tile_done(k);
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
    pc_regs<G::R_LAST, G::R_ALL>();
    if (warp == W_MMA) {
@@ -730,7 +713,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         };
         // scores of tile tq from key slice sl in slot it: 32 bytes of K per product, 64 values per 128-byte row
         auto qk = [&](int tq, int sl, uint32_t it, uint32_t d) {
-          const uint64_t a = pc_desc(q_a + tq * 128 * D * 2 + sl * 2 * 16384, 16);
+          const uint64_t a = pc_desc(q_a + tq * 128 * D * 2 + sl * (SD / 64) * 16384, 16);
           const uint64_t b = pc_desc(ring_a + (it % SLOTS) * G::SLOT, 16);
 #pragma unroll
           for (int x = 0; x < SD / 16; ++x) {
