@@ -3,7 +3,7 @@
 // One CTA per SM takes a tile of 128 query rows of a KV head, or two of them side by side (D <= 128), and walks the tile's keys in blocks
 // of 128: S = Q K^T and O += P V on tcgen05 (fp16 operands, fp32 sums in tensor memory), an online softmax in between. Rows are (token, query head)
 // pairs, so all query heads of a KV head share a block's keys and values, which are turned from codes into operands once per block:
-//   dequantising warps   codes -> fp16 tiles in shared memory (a ring of slots of 128 keys x 128 dimensions, 64 at D = 64 and 512);
+//   dequantising warps   codes -> fp16 tiles in shared memory (a ring of slots of 128 keys x 128 dimensions), next slot's codes in flight in registers;
 //   softmax warps        one thread per query row: reads its row of S from tensor memory, writes P (fp16) over it;
 //   MMA warp             one thread issues every product. With two tiles the products of one run while the softmax of the other does;
 //                        with one tile S has two buffers and the next block's scores run during this block's softmax;
@@ -22,6 +22,8 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "qda_paged_sched.cuh"
 
@@ -47,25 +49,23 @@ struct PcInfo {
 template <int D, int BITS, int NQ>
 struct PcGeom {
   static constexpr int MT = 128 * NQ;
-  static constexpr int SD = D == 128 || D == 256 ? 128 : 64;   // dimensions per slot (D = 512: what fits beside its queries)
+  static constexpr int SD = D < 128 ? D : 128;          // dimensions per slot
   static constexpr int DV = D < 256 ? D : 256;          // values' dimensions of a unit (TMEM holds O of no more)
   static constexpr int PARTS = D / DV;
   static constexpr int KSL = D / SD, VSL = DV / SD;     // slots of a block's keys and of its values
   static constexpr int SLOT = kPcKeys * SD * 2;
   static constexpr int QB = MT * D * 2;
+  static constexpr int SLOTS0 = (226 * 1024 - 1024 - QB) / SLOT;
+  static constexpr int SLOTS = SLOTS0 > 6 ? 6 : SLOTS0;
   static constexpr int SOFT = 4 * NQ;                   // softmax warps
   static constexpr int DEQ = 8;                         // dequantising warps
   static constexpr int WARPS = SOFT + DEQ + 1 + kPcInfoWarps;
-  static constexpr int NU = 128 * (SD / 32) / (DEQ * 32);   // units of 32 codes per dequantising thread and slot
-  static constexpr int STAGE = DEQ * 32 * NU * (4 * BITS + 8);   // a slot's codes, scales and biases as they are in memory
-  // stages of codes under way and slots of operands: what shared memory holds
-  static constexpr int STAGES = D == 128 && BITS == 4 && NQ == 2 ? 2 : 3;
-  static constexpr int SLOTS0 = (226 * 1024 - 1024 - QB - STAGES * STAGE) / SLOT;
-  static constexpr int SLOTS = SLOTS0 > 6 ? 6 : SLOTS0;
   // registers a thread: the launch's 96 (20 warps) or 128 (16 warps), dealt out anew among the warpgroups
   static constexpr int R_ALL = NQ == 2 ? 96 : 128;
-  static constexpr int R_SOFT = NQ == 2 ? 136 : 136, R_DEQ = NQ == 2 ? 72 : 128, R_LAST = NQ == 2 ? 64 : 96;
+  static constexpr int R_SOFT = NQ == 2 ? 136 : 136, R_DEQ = NQ == 2 ? 72 : 136, R_LAST = NQ == 2 ? 64 : 96;
   static_assert(SOFT * R_SOFT + DEQ * R_DEQ + 4 * R_LAST <= WARPS * R_ALL, "registers of the launch");
+  // items of codes under way: what the registers hold, and a divisor of a block's items less one
+  static constexpr int AHEAD = D <= 128 ? 1 : D == 256 ? 3 : BITS == 4 ? 5 : 2;
   static constexpr int O_COL = 256;                     // O behind two S buffers of 128 columns
   static_assert(NQ == 1 || D <= 128, "two tiles need room for two O");
   static_assert(SLOTS >= 3 && O_COL + NQ * DV <= 512, "shared or tensor memory");
@@ -96,7 +96,7 @@ struct PcShared {
 template <int D, int BITS, int NQ>
 constexpr int pc_smem() {
   using G = PcGeom<D, BITS, NQ>;
-  return 1024 + G::QB + G::SLOTS * G::SLOT + G::STAGES * G::STAGE + (int)sizeof(PcShared);
+  return 1024 + G::QB + G::SLOTS * G::SLOT + (int)sizeof(PcShared);
 }
 
 __device__ __forceinline__ float pc_ex2(float x) {
@@ -212,6 +212,15 @@ __device__ __forceinline__ void pc_regs() {
   if constexpr (N < LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// f(integral_constant<0>), ..., f(integral_constant<N - 1>)
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void pc_each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    pc_each<N, I + 1>(f);
+  }
+}
+
 template <int D, int BITS, int NQ>
 __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     qda_paged_chunk_kernel(const __grid_constant__ QdaPagedParams p) {
@@ -224,8 +233,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
   unsigned char* base = pc_smem_raw + ((1024u - (smem_addr(pc_smem_raw) & 1023u)) & 1023u);
   unsigned char* q_s = base;
   unsigned char* ring = base + G::QB;
-  unsigned char* staged = ring + SLOTS * G::SLOT;
-  PcShared& sh = *reinterpret_cast<PcShared*>(staged + G::STAGES * G::STAGE);
+  PcShared& sh = *reinterpret_cast<PcShared*>(ring + SLOTS * G::SLOT);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int W_DEQ = G::SOFT, W_MMA = G::SOFT + DEQ;   // the info warps behind
   volatile int* abort = &sh.abort;
@@ -297,25 +305,49 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int rt = tq * 128 + 32 * (warp & 3) + lane;   // row of the tile
     const uint32_t o_t = tmem + lanes + G::O_COL + tq * DV;
-    // the row's query into shared memory, in the codes' unpacked order; returns what undoes its scale, times the softmax scale
+    // The warp's 32 query rows into shared memory, in the codes' unpacked order, each row scaled by a power of two; returns what undoes this thread's
+    // row's scale, times the softmax scale. With one tile a row is read by lanes side by side; with two tiles (D <= 128) a thread reads its own
+    // row, which is slower by itself, but the other form costs the softmax loop registers there (ragged chunks at D = 256: 574 against 624 us for
+    // the first form; chunk over 32768 keys at D = 128: 869 us with the second, 887 with the first).
     auto load_q = [&](const PcTile& t) {
-      const int r = t.row0 + rt;
-      const bool real = r < t.s.rows;
-      const int tok = r / p.nrep;
-      const uint4* qp = reinterpret_cast<const uint4*>(p.q + (long long)(t.s.first + tok) * p.q_tstride +
-                                                       (long long)(t.kvh * p.nrep + (r - tok * p.nrep)) * p.q_hstride);
-      constexpr int C = D / 8, H = C < 16 ? C : 16;   // 16-byte pieces; held in registers at a time
-      uint4 a[H];
-      float top = 0.f;
-      auto get = [&](int c0) {
+      float mul = 0.f;
+      // 8 values: their largest magnitude; and with `up` 16 bytes of operand
+      auto values = [&](const uint4& a, float (&v)[8]) {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < H; ++i) a[i] = real ? __ldg(qp + c0 + i) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = half2_bits_to_float2_rt(w[k], p.f16);
+          v[2 * k] = f.x;
+          v[2 * k + 1] = f.y;
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+        return top;
       };
-#pragma unroll 1
-      for (int c0 = 0; c0 < C; c0 += H) {
-        get(c0);
+      auto store = [&](const float (&v)[8], float up, int row, int piece) {
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
+        for (int k = 0; k < 4; ++k) w[k] = pc_h2(v[pc_dim<BITS>(2 * k)] * up, v[pc_dim<BITS>(2 * k + 1)] * up);
+        *reinterpret_cast<uint4*>(q_s + tq * 128 * D * 2 + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      };
+      // exponent field of the power of two that brings `top` to [2^8, 2^9)
+      auto scale_of = [](float top) { return min(262 - (int)((__float_as_uint(top) >> 23) & 255u), 253); };
+      auto row_at = [&](int r) {
+        const int tok = r / p.nrep;
+        return reinterpret_cast<const uint4*>(p.q + (long long)(t.s.first + tok) * p.q_tstride +
+                                              (long long)(t.kvh * p.nrep + (r - tok * p.nrep)) * p.q_hstride);
+      };
+      if constexpr (NQ == 2) {
+        const int r = t.row0 + rt;
+        const bool real = r < t.s.rows;
+        const uint4* qp = row_at(r);
+        uint4 a[D / 8];
+        float top = 0.f, v[8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) a[i] = real ? __ldg(qp + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
           const uint32_t u[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -323,35 +355,50 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
             top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
           }
         }
-      }
-      const int fe = min(262 - (int)((__float_as_uint(top) >> 23) & 255u), 253);
-      const float up = __uint_as_float((uint32_t)fe << 23);
-      unsigned char* dst = q_s + tq * 128 * D * 2 + (rt & 127) * 128;
+        const int fe = scale_of(top);
+        const float up = __uint_as_float((uint32_t)fe << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          values(a[i], v);
+          store(v, up, rt & 127, i);
+        }
+        mul = __uint_as_float((uint32_t)(254 - fe) << 23);
+      } else {
+        constexpr int LPR = D < 256 ? D / 8 : 32;   // lanes per row, 16 bytes each
+        constexpr int RPI = 32 / LPR;               // rows at a time
+        constexpr int C = D / 8 / LPR;              // pieces per lane
+        constexpr int U = 4;                        // row groups in flight
+        const int sub = lane / LPR, l = lane % LPR;
 #pragma unroll 1
-      for (int c0 = 0; c0 < C; c0 += H) {
-        if (C > H) get(c0);
+        for (int g0 = 0; g0 < 32 / RPI; g0 += U) {
+          uint4 a[U][C];
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-          const uint32_t u[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
-          float v[8];
+          for (int u = 0; u < U; ++u) {
+            const int r = t.row0 + 32 * warp + (g0 + u) * RPI + sub;
+            const uint4* qp = row_at(r);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = half2_bits_to_float2_rt(u[k], p.f16);
-            v[2 * k] = f.x * up;
-            v[2 * k + 1] = f.y * up;
+            for (int c = 0; c < C; ++c) a[u][c] = r < t.s.rows ? __ldg(qp + l + 32 * c) : make_uint4(0, 0, 0, 0);
           }
-          uint32_t w[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = pc_h2(v[pc_dim<BITS>(2 * k)], v[pc_dim<BITS>(2 * k + 1)]);
-          const int c = c0 + i;
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * 16384 + (((c & 7) ^ (rt & 7)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          for (int u = 0; u < U; ++u) {
+            float v[C][8], top = 0.f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) top = fmaxf(top, values(a[u][c], v[c]));
+#pragma unroll
+            for (int o = LPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int fe = scale_of(top);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+              store(v[c], __uint_as_float((uint32_t)fe << 23), 32 * warp + (g0 + u) * RPI + sub, l + 32 * c);
+            const float mine = __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(254 - fe) << 23), (lane % RPI) * LPR);
+            if (lane / RPI == g0 + u) mul = mine;   // this thread's row is among these
+          }
         }
       }
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_full);
-      return p.qscale * __uint_as_float((uint32_t)(254 - fe) << 23);
+      return p.qscale * mul;
     };
 
     const PcTile* t = tile_at(0);
@@ -543,12 +590,12 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     // ========================================================================= codes -> fp16 tiles in shared memory
     pc_regs<G::R_DEQ, G::R_ALL>();
     constexpr int UPR = SD / 32;               // units of 32 codes (which share a scale) per row of a slot
-    constexpr int NU = G::NU, STAGES = G::STAGES;
+    constexpr int NU = 128 * UPR / (DEQ * 32);
+    constexpr int UW = BITS;                   // words of codes per unit
     constexpr int ROWB = D * BITS / 8;         // bytes of codes per row
-    constexpr int RSTEP = DEQ * 32 / UPR;      // rows between a thread's units
-    constexpr int P = KSL + VSL;
+    constexpr int AHEAD = G::AHEAD;            // items whose codes are under way
     const int id = tid - W_DEQ * 32;
-    const int row = id / UPR, q = id % UPR;    // this thread's units: unit q of rows row, row + RSTEP, ...
+    const int row = id / UPR, q = id % UPR;    // this thread's units: unit q of rows row, row + threads / UPR, ...
     const int gshift = 31 - __clz(p.GS);
     const uint32_t sstride = p.NG * 2;
     // where a unit's four 16-byte pieces of operand go in a slot: rows of 64 values, pieces XORed by the row. The order of the
@@ -560,102 +607,103 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
       const int piece = q * 4 + (u ^ turn);
       to[u] = (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
     }
-    // Codes go through stages that a thread fills and reads by itself, 16 bytes a lane (no bank conflicts, nobody else to wait
-    // for): asynchronous copies hold no registers, and the loop is one body for keys and values (bodies for each kind
-    // of item, with the codes in registers, ran out of instruction cache).
-    constexpr int CU = BITS / 4;               // 16-byte pieces of codes per unit
-    const uint32_t stage0 = smem_addr(staged) + id * 16, scale0 = smem_addr(staged) + DEQ * 32 * NU * 4 * BITS + id * 8;
-    uint32_t filled = 0, taken = 0;            // stages filled and read so far
+    struct Item {
+      uint32_t code[NU][UW];
+      uint32_t s[NU], b[NU];                   // as they are in memory: nothing waits for a load before its item's turn
+      uint32_t ok;                             // bit per unit: the key counts (else it is zero)
+    };
+    // The slots of a tile come in groups g = -1 ... n - 1 of KSL + VSL items: the keys of block g + 1, the values of block g
+    // (where there are such). Items are loaded AHEAD items before they are converted.
+    constexpr int P = KSL + VSL;
+    static_assert(P % (AHEAD + 1) == 0, "an item's registers are known at compile time");
+    Item reg[AHEAD + 1];
     for (int k = 0;; ++k) {
       const PcTile* t = tile_at(k);
       if (t == nullptr) break;
-      const int n = t->n, left0 = t->keys - t->j0 * kPcKeys, vd0 = t->part * DV;
-      // The slots of a tile come in groups g = -1 ... n - 1 of P items: the slices of the keys of block g + 1, then of the values of block
-      // g (where there are such). Two cursors walk them: codes are sent for STAGES - 1 items before they are converted.
-      auto step = [&](int& g, int& z) {
-        if (++z == (g < 0 ? KSL : P)) {
-          ++g;
-          z = g + 1 < n ? 0 : KSL;
-        }
-      };
-      int ig = n > 0 ? -1 : n, iz = 0;
-      auto issue = [&]() {
-        if (ig < n) {
-          const bool val = iz >= KSL;
-          const int sl = val ? iz - KSL : iz, j = val ? ig : ig + 1;
-          const uint32_t x = bc + j;
-          if (iz == 0) wait(&sh.info_full[x % kPcInfo], x / kPcInfo);
-          const PcInfo& f = sh.info[x % kPcInfo];
-          const int d0 = (val ? vd0 : 0) + sl * SD + 32 * q;
-          const char* src = reinterpret_cast<const char*>(val ? p.vp : p.kp) + d0 * BITS / 8;
-          const uint32_t goff = (d0 >> gshift) * 2;
-          const char* ss = reinterpret_cast<const char*>(val ? p.vs : p.ks);
-          const char* bs = reinterpret_cast<const char*>(val ? p.vb : p.kb);
-          const uint32_t st = (filled % STAGES) * G::STAGE;
+      const int n = t->n, left0 = t->keys - t->j0 * kPcKeys;
+      const int vd0 = t->part * DV + 32 * q;
+      const char* ksrc = reinterpret_cast<const char*>(p.kp) + 4 * BITS * q;
+      const char* vsrc = reinterpret_cast<const char*>(p.vp) + vd0 * BITS / 8;
+      uint32_t prk[NU], prv[NU], okk = 0, okv = 0;   // pool rows of the block whose keys were loaded last, and of the one before
 #pragma unroll
-          for (int i = 0; i < NU; ++i) {
-            const int r = row + i * RSTEP;
-            const uint32_t base = f.row[r >> 4], pr = base == kPcNoRow ? 0u : base + (r & 15);
-            const char* c = src + (uint64_t)pr * ROWB;
-#pragma unroll
-            for (int u = 0; u < CU; ++u)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(stage0 + st + (i * CU + u) * DEQ * 512),
-                           "l"(c + 16 * u)
-                           : "memory");
-            const uint64_t at = ((uint64_t)pr * sstride + goff) & ~(uint64_t)3;   // the word that holds the 16 bits
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scale0 + st + i * DEQ * 256), "l"(ss + at) : "memory");
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(scale0 + st + i * DEQ * 256 + 4), "l"(bs + at)
-                         : "memory");
-          }
-          ++filled;
-          step(ig, iz);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");   // an empty group keeps the count
-      };
-#pragma unroll
-      for (int x = 0; x < STAGES - 1; ++x) issue();
+      for (int i = 0; i < NU; ++i) prk[i] = prv[i] = 0;
       int kv_run = -126;
       uint32_t at = ic;                              // slots so far
-      for (int g = n > 0 ? -1 : n, z = 0; g < n; step(g, z)) {
-        issue();
-        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-        const bool val = z >= KSL;
-        const int sl = val ? z - KSL : z, j = val ? g : g + 1;
-        const PcInfo& f = sh.info[(bc + j) % kPcInfo];
-        if (val) kv_run = max(kv_run, f.kv);
-        const float fac = val ? __uint_as_float((uint32_t)(127 - kv_run) << 23) : f.kfac;
+      auto load = [&](auto item, int g) {
+        constexpr int X = decltype(item)::value;
+        constexpr bool VAL = X >= KSL;
+        constexpr int SL = VAL ? X - KSL : X;
+        if (VAL ? g < 0 : g + 1 >= n) return;
+        Item& it = reg[X % (AHEAD + 1)];
+        if constexpr (X == 0) {
+          const uint32_t x = bc + g + 1;
+          const PcInfo& f = sh.info[x % kPcInfo];
+          wait(&sh.info_full[x % kPcInfo], x / kPcInfo);
+          const int left = left0 - (g + 1) * kPcKeys;
+          okv = okk;
+          okk = 0;
+#pragma unroll
+          for (int i = 0; i < NU; ++i) {
+            const int r = row + i * (DEQ * 32 / UPR);
+            const uint32_t base = f.row[r >> 4];
+            const bool ok = base != kPcNoRow && r < left;
+            prv[i] = prk[i];
+            prk[i] = ok ? base + (r & 15) : 0u;
+            okk |= (uint32_t)ok << i;
+          }
+        } else if constexpr (X == KSL) {
+          if (g + 1 >= n) {   // the last group has no keys: its values are of the block whose keys came last
+            okv = okk;
+#pragma unroll
+            for (int i = 0; i < NU; ++i) prv[i] = prk[i];
+          }
+        }
+        const uint32_t goff = (((VAL ? vd0 : 32 * q) + SL * SD) >> gshift) * 2;
+        const char* src = (VAL ? vsrc : ksrc) + SL * SD * BITS / 8;
+        const char* ss = reinterpret_cast<const char*>(VAL ? p.vs : p.ks) + goff;
+        const char* bs = reinterpret_cast<const char*>(VAL ? p.vb : p.kb) + goff;
+        it.ok = VAL ? okv : okk;
+#pragma unroll
+        for (int i = 0; i < NU; ++i) {
+          const uint32_t pr = VAL ? prv[i] : prk[i];
+          const uint4* c = reinterpret_cast<const uint4*>(src + (uint64_t)pr * ROWB);
+#pragma unroll
+          for (int u = 0; u < UW / 4; ++u) {
+            const uint4 v = __ldg(c + u);
+            it.code[i][4 * u] = v.x;
+            it.code[i][4 * u + 1] = v.y;
+            it.code[i][4 * u + 2] = v.z;
+            it.code[i][4 * u + 3] = v.w;
+          }
+          it.s[i] = __ldg(reinterpret_cast<const uint16_t*>(ss + (uint64_t)pr * sstride));
+          it.b[i] = __ldg(reinterpret_cast<const uint16_t*>(bs + (uint64_t)pr * sstride));
+        }
+      };
+      auto convert = [&](auto item, int g) {
+        constexpr int X = decltype(item)::value;
+        constexpr bool VAL = X >= KSL;
+        constexpr int SL = VAL ? X - KSL : X;
+        if (VAL ? g < 0 : g + 1 >= n) return;
+        const Item& it = reg[X % (AHEAD + 1)];
+        const PcInfo& f = sh.info[(bc + g + (VAL ? 0 : 1)) % kPcInfo];
+        if constexpr (VAL && SL == 0) kv_run = max(kv_run, f.kv);
+        const float fac = VAL ? __uint_as_float((uint32_t)(127 - kv_run) << 23) : f.kfac;
         const bool odd = f.flags & 2u;
-        const int left = left0 - j * kPcKeys;
-        const uint32_t gsel = (((val ? vd0 : 0) + sl * SD + 32 * q) >> gshift) * 2;
-        const uint32_t slot = at % SLOTS, st = (taken % STAGES) * G::STAGE;
+        const uint32_t slot = at % SLOTS;
         wait(&sh.empty[slot], at / SLOTS + 1);
         ++at;
-        ++taken;
         const uint32_t dst = smem_addr(ring) + slot * G::SLOT;
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-          const int r = row + i * RSTEP;
-          const uint32_t base = f.row[r >> 4];
-          const bool ok = base != kPcNoRow && r < left;
-          uint32_t code[BITS], sw, bw;
-#pragma unroll
-          for (int u = 0; u < CU; ++u)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(code[4 * u]), "=r"(code[4 * u + 1]), "=r"(code[4 * u + 2]), "=r"(code[4 * u + 3])
-                         : "r"(stage0 + st + (i * CU + u) * DEQ * 512));
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(sw), "=r"(bw) : "r"(scale0 + st + i * DEQ * 256));
-          const uint32_t sh16 = ((base + (r & 15)) * sstride + gsel) & 2u ? 16 : 0;
-          sw >>= sh16;
-          bw >>= sh16;
           float s, b;
           if (p.f16) {
-            s = fp16_bits_to_float(sw & 0xffffu);
-            b = fp16_bits_to_float(bw & 0xffffu);
+            s = fp16_bits_to_float(it.s[i]);
+            b = fp16_bits_to_float(it.b[i]);
           } else {
-            s = __uint_as_float(sw << 16);
-            b = __uint_as_float(bw << 16);
+            s = __uint_as_float(it.s[i] << 16);
+            b = __uint_as_float(it.b[i] << 16);
           }
-          if (!ok || (odd && !(fmaxf(fabsf(s), fabsf(b)) < FINITE))) s = b = 0.f;
+          if (!((it.ok >> i) & 1u) || (odd && !(fmaxf(fabsf(s), fabsf(b)) < FINITE))) s = b = 0.f;
           s *= fac;
           b *= fac;
           const uint32_t s1 = pc_h2(s * 16777216.f, s * 16777216.f), s16 = pc_h2(s * 1048576.f, s * 1048576.f), b2 = pc_h2(b, b);
@@ -663,7 +711,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           for (int u = 0; u < 4; ++u) {
             uint32_t y[4];
             if constexpr (BITS == 4) {
-              const uint32_t w = turn ? code[u ^ 2] : code[u];
+              const uint32_t w = turn ? it.code[i][u ^ 2] : it.code[i][u];
               const uint32_t w8 = w >> 8;
               y[0] = pc_fma2(w & 0x000F000Fu, s1, b2);
               y[1] = pc_fma2(w & 0x00F000F0u, s16, b2);
@@ -672,13 +720,13 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
             } else {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t w = turn ? code[2 * (u ^ 2) + h] : code[2 * u + h];
+                const uint32_t w = turn ? it.code[i][2 * (u ^ 2) + h] : it.code[i][2 * u + h];
                 y[2 * h] = pc_fma2(w & 0x00FF00FFu, s1, b2);
                 y[2 * h + 1] = pc_fma2((w >> 8) & 0x00FF00FFu, s1, b2);
               }
             }
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + to[u] + i * RSTEP * 128), "r"(y[0]),
-                         "r"(y[1]), "r"(y[2]), "r"(y[3])
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + to[u] + i * (DEQ * 32 / UPR) * 128),
+                         "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
                          : "memory");
           }
         }
@@ -686,14 +734,22 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sh.full[slot]);
-          if (val && sl == VSL - 1) mbar_arrive(&sh.info_empty[(bc + j) % kPcInfo]);
+          if (VAL && SL == VSL - 1) mbar_arrive(&sh.info_empty[(bc + g) % kPcInfo]);
         }
+      };
+      if (n > 0) {
+        pc_each<AHEAD>([&](auto item) { load(item, -1); });
+        for (int g = -1; g < n; ++g)
+          pc_each<P>([&](auto item) {
+            constexpr int NEXT = decltype(item)::value + AHEAD;
+            load(std::integral_constant<int, NEXT % P>{}, g + NEXT / P);
+            convert(item, g);
+          });
       }
       bc += n;
       ic += n * P;
       tile_done(k);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
    pc_regs<G::R_LAST, G::R_ALL>();
    if (warp == W_MMA) {
@@ -713,7 +769,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         };
         // scores of tile tq from key slice sl in slot it: 32 bytes of K per product, 64 values per 128-byte row
         auto qk = [&](int tq, int sl, uint32_t it, uint32_t d) {
-          const uint64_t a = pc_desc(q_a + tq * 128 * D * 2 + sl * (SD / 64) * 16384, 16);
+          const uint64_t a = pc_desc(q_a + tq * 128 * D * 2 + sl * 2 * 16384, 16);
           const uint64_t b = pc_desc(ring_a + (it % SLOTS) * G::SLOT, 16);
 #pragma unroll
           for (int x = 0; x < SD / 16; ++x) {
