@@ -449,8 +449,10 @@ SplitFn split_fn(int bits, bool f16) {
                    : (f16 ? qda_paged_split_b8_f1 : qda_paged_split_b8_f0);
 }
 
-// Rows (new tokens times query heads of a KV head) up to which the split kernel takes a call.
-constexpr long long kSplitRows = 16;
+// Rows (new tokens times query heads of a KV head) up to which the split kernel takes a call. Its time grows with every 16 rows (8 at
+// D = 512), the chunk kernel's stays the same up to 128. Split against chunk kernel at 32 rows: D 64 (32 sequences, 8-bit) 79 / 85 us, D 128 (16
+// sequences, 4-bit) 101 / 99, one sequence of 32768 keys 43 / 47, D 512 80 / 104 (48 rows: 107 / 110); D 256 (8-bit) 91 / 67, and at 16 rows 60 / 64.
+constexpr long long split_rows(int D) { return D == 512 ? 48 : D == 256 ? 16 : 32; }
 
 cudaError_t chunk_run(const QdaPagedParams* p, int D, int bits, int rows, bool prepare, cudaStream_t s) {
   return bits == 4 ? qda_paged_chunk_b4(p, D, rows / 128, prepare, s) : qda_paged_chunk_b8(p, D, rows / 128, prepare, s);
@@ -462,7 +464,7 @@ int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int
   const cudaError_t de = cudaGetDevice(&dev);
   if (de != cudaSuccess || dev < 0 || dev >= 64) return qda_cuda_fail(de == cudaSuccess ? cudaErrorInvalidDevice : de);
   const int di = D == 64 ? 0 : D == 128 ? 1 : D == 256 ? 2 : 3, gi = GS == 32 ? 0 : GS == 64 ? 1 : 2;
-  plan->chunk = rows > kSplitRows;
+  plan->chunk = rows > split_rows(D);
   if (plan->chunk) {
     plan->rows = rows > 128 && D <= 128 ? 256 : 128;
     plan->min_keys = 512;
@@ -604,7 +606,7 @@ extern "C" int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max
   // a call may state a smaller max_q than this one, and either dtype
   size_t most = 0;
   for (int f16 = 0; f16 < 2; ++f16) {
-    for (long long m : {1LL, kSplitRows / (H / Hkv), 128LL / (H / Hkv), (long long)max_q}) {
+    for (long long m : {1LL, split_rows(D) / (H / Hkv), 128LL / (H / Hkv), (long long)max_q}) {
       m = std::max(1LL, std::min(m, (long long)max_q));
       PagedPlan plan;
       got = paged_plan(H / Hkv, m, D, GS, bits, f16 != 0, sms, &plan);

@@ -52,7 +52,7 @@ struct PsGeom {
   static constexpr int SMEM = ROWS + (RING > COMB ? RING : COMB);
   static_assert(SMEM - ROWS >= (int)sizeof(PagedLine), "the line lies in the ring");
   static constexpr int OREGS = D / 4 * NT;
-  static constexpr int MINB = OREGS <= 32 ? (NG * NT > 2 ? 3 : 4) : OREGS <= 64 ? (NT == 2 ? 2 : 3) : 2;   // spills else
+  static constexpr int MINB = OREGS <= 32 ? (NG * NT > 2 ? 3 : 4) : 2;   // spills else
 };
 
 __device__ __forceinline__ void ps_cp16(uint32_t dst, const void* src) {
@@ -212,6 +212,63 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
     const bool mine = s_x[0] <= t.lo;   // the CTA that starts the tile
     if (j0 < j1 || (nblk == 0 && mine)) {
       const int row0 = t.i * MT;
+      // ---- this warp's key blocks j0 + warp, + kPsWarps, ... through its ring
+      const int mine_n = j1 - j0 > warp ? (j1 - j0 - warp + kPsWarps - 1) / kPsWarps : 0;
+      const int* tab = p.table + (size_t)t.b * p.max_pages;
+      // the pages of a block's two 16-key halves (one half where a block is 16 keys), looked up one block ahead
+      int pg[KPS / 16];
+      auto look = [&](int k) {
+#pragma unroll
+        for (int h = 0; h < KPS / 16; ++h) {
+          const int n = (j0 + warp + k * kPsWarps) * KPS + 16 * h;
+          pg[h] = k < mine_n && n < keys ? __ldg(tab + (n >> p.page_shift)) : 0;
+        }
+      };
+      bool saw_absent = false;
+      uint32_t absent = 0;   // bit (stage * 2 + half): that half's page is outside the pool
+      auto issue = [&](int k) {
+        if (k < mine_n) {
+          const int st = k % STAGES;
+          const uint32_t base = ring + st * G::STAGE;
+          const int n0 = (j0 + warp + k * kPsWarps) * KPS;
+          long long row[KPS / 16];
+#pragma unroll
+          for (int h = 0; h < KPS / 16; ++h) {
+            const bool ok = (unsigned)pg[h] < (unsigned)p.num_pages;
+            const uint32_t bit = 1u << (st * 2 + h);
+            absent = ok ? absent & ~bit : absent | bit;
+            saw_absent = saw_absent || !ok;
+            row[h] = qda_pool_row(ok ? pg[h] : 0, t.unit, (n0 + 16 * h) & pmask, p.Hkv, p.page_shift);
+          }
+#pragma unroll
+          for (int i = 0; i < G::CODE / 512; ++i) {
+            const int at = (i * 32 + lane) * 16, key = at / RB, col = at % RB;
+            const long long src = (row[KPS == 32 ? (i * 512 / RB) / 16 : 0] + (key & 15)) * RB + col;
+            const uint32_t dst = base + ((key * RB + col) ^ ps_turn<RB>(key));
+            ps_cp16(dst, reinterpret_cast<const char*>(p.kp) + src);
+            ps_cp16(dst + G::CODE, reinterpret_cast<const char*>(p.vp) + src);
+          }
+          // scales and biases: 16 keys' are contiguous, NG * 2 pieces of 16 bytes per array and half
+          constexpr int PC = KPS / 16 * NG * 2;   // pieces per array
+#pragma unroll
+          for (int i = 0; i < (4 * PC + 31) / 32; ++i) {
+            const int id = i * 32 + lane, a = id / PC, k16 = id % PC;
+            if (id < 4 * PC) {
+              const uint16_t* arr = a == 0 ? p.ks : a == 1 ? p.kb : a == 2 ? p.vs : p.vb;
+              const int h = KPS == 32 ? k16 / (NG * 2) : 0;
+              const long long src = row[h] * (NG * 2) + (k16 - h * NG * 2) * 16;
+              ps_cp16(base + 2 * G::CODE + a * G::SC + k16 * 16, reinterpret_cast<const char*>(arr) + src);
+            }
+          }
+          look(k + 1);
+        }
+        ps_commit();
+      };
+
+      look(0);
+#pragma unroll
+      for (int k = 0; k < STAGES - 1; ++k) issue(k);   // under way while the queries are prepared
+
       // ---- the tile's query rows: B operands, sums per group, and how far each sees
       uint2 qf[G::QSMEM ? 1 : D / 16 * NT];
       float qsum[G::SSMEM ? 1 : NG * NT][2];
@@ -298,59 +355,6 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
       if constexpr (G::QSMEM || G::SSMEM) __syncthreads();
 
-      // ---- this warp's key blocks j0 + warp, + kPsWarps, ... through its ring
-      const int mine_n = j1 - j0 > warp ? (j1 - j0 - warp + kPsWarps - 1) / kPsWarps : 0;
-      const int* tab = p.table + (size_t)t.b * p.max_pages;
-      // the pages of a block's two 16-key halves (one half where a block is 16 keys), looked up one block ahead
-      int pg[KPS / 16];
-      auto look = [&](int k) {
-#pragma unroll
-        for (int h = 0; h < KPS / 16; ++h) {
-          const int n = (j0 + warp + k * kPsWarps) * KPS + 16 * h;
-          pg[h] = k < mine_n && n < keys ? __ldg(tab + (n >> p.page_shift)) : 0;
-        }
-      };
-      bool saw_absent = false;
-      uint32_t absent = 0;   // bit (stage * 2 + half): that half's page is outside the pool
-      auto issue = [&](int k) {
-        if (k < mine_n) {
-          const int st = k % STAGES;
-          const uint32_t base = ring + st * G::STAGE;
-          const int n0 = (j0 + warp + k * kPsWarps) * KPS;
-          long long row[KPS / 16];
-#pragma unroll
-          for (int h = 0; h < KPS / 16; ++h) {
-            const bool ok = (unsigned)pg[h] < (unsigned)p.num_pages;
-            const uint32_t bit = 1u << (st * 2 + h);
-            absent = ok ? absent & ~bit : absent | bit;
-            saw_absent = saw_absent || !ok;
-            row[h] = qda_pool_row(ok ? pg[h] : 0, t.unit, (n0 + 16 * h) & pmask, p.Hkv, p.page_shift);
-          }
-#pragma unroll
-          for (int i = 0; i < G::CODE / 512; ++i) {
-            const int at = (i * 32 + lane) * 16, key = at / RB, col = at % RB;
-            const long long src = (row[KPS == 32 ? (i * 512 / RB) / 16 : 0] + (key & 15)) * RB + col;
-            const uint32_t dst = base + ((key * RB + col) ^ ps_turn<RB>(key));
-            ps_cp16(dst, reinterpret_cast<const char*>(p.kp) + src);
-            ps_cp16(dst + G::CODE, reinterpret_cast<const char*>(p.vp) + src);
-          }
-          // scales and biases: 16 keys' are contiguous, NG * 2 pieces of 16 bytes per array and half
-          constexpr int PC = KPS / 16 * NG * 2;   // pieces per array
-#pragma unroll
-          for (int i = 0; i < (4 * PC + 31) / 32; ++i) {
-            const int id = i * 32 + lane, a = id / PC, k16 = id % PC;
-            if (id < 4 * PC) {
-              const uint16_t* arr = a == 0 ? p.ks : a == 1 ? p.kb : a == 2 ? p.vs : p.vb;
-              const int h = KPS == 32 ? k16 / (NG * 2) : 0;
-              const long long src = row[h] * (NG * 2) + (k16 - h * NG * 2) * 16;
-              ps_cp16(base + 2 * G::CODE + a * G::SC + k16 * 16, reinterpret_cast<const char*>(arr) + src);
-            }
-          }
-          look(k + 1);
-        }
-        ps_commit();
-      };
-
       float o[NG * KS * NT][4], wsum[G::ONES ? NG * NT : 1][4], vb[NG * NT][2], l[NT][2], m[NT][2];
 #pragma unroll
       for (int i = 0; i < NG * KS * NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -369,9 +373,6 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       uint32_t most = 0;        // 16-bit pattern of the largest value scale that the weights' unit allows
       float vexp = 0.f;         // everything that is summed is taken times 2^vexp, an integer
 
-      look(0);
-#pragma unroll
-      for (int k = 0; k < STAGES - 1; ++k) issue(k);
       for (int k = 0; k < mine_n; ++k) {
         issue(k + STAGES - 1);   // into the stage read one block ago
         ps_wait<STAGES - 1>();
