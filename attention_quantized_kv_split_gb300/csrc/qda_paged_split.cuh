@@ -215,59 +215,70 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       // ---- this warp's key blocks j0 + warp, + kPsWarps, ... through its ring
       const int mine_n = j1 - j0 > warp ? (j1 - j0 - warp + kPsWarps - 1) / kPsWarps : 0;
       const int* tab = p.table + (size_t)t.b * p.max_pages;
-      // the pages of a block's two 16-key halves (one half where a block is 16 keys), looked up one block ahead
-      int pg[KPS / 16];
-      auto look = [&](int k) {
+      // the pages of a block's two 16-key halves (one half where a block is 16 keys), looked up one block ahead of the copies
+      constexpr int HALVES = KPS / 16, STEP = kPsWarps * KPS;
+      int pg[HALVES];
+      int fill_n = (j0 + warp) * KPS, fill_left = mine_n, fill_stage = 0;   // next block to copy, blocks to copy, its stage
+      auto look = [&]() {
 #pragma unroll
-        for (int h = 0; h < KPS / 16; ++h) {
-          const int n = (j0 + warp + k * kPsWarps) * KPS + 16 * h;
-          pg[h] = k < mine_n && n < keys ? __ldg(tab + (n >> p.page_shift)) : 0;
+        for (int h = 0; h < HALVES; ++h) {
+          const int n = fill_n + 16 * h;
+          pg[h] = fill_left > 0 && n < keys ? __ldg(tab + (n >> p.page_shift)) : 0;
         }
       };
       bool saw_absent = false;
       uint32_t absent = 0;   // bit (stage * 2 + half): that half's page is outside the pool
-      auto issue = [&](int k) {
-        if (k < mine_n) {
-          const int st = k % STAGES;
-          const uint32_t base = ring + st * G::STAGE;
-          const int n0 = (j0 + warp + k * kPsWarps) * KPS;
-          long long row[KPS / 16];
+      // this lane's 16 bytes of a block's scales and biases: NG * 2 pieces per array and half
+      constexpr int PC = HALVES * NG * 2, SI = (4 * PC + 31) / 32;
+      auto issue = [&]() {
+        if (fill_left > 0) {
+          const uint32_t base = ring + fill_stage * G::STAGE;
+          uint32_t row[HALVES], gone = 0;   // pool rows (32 bits: the host checks)
 #pragma unroll
-          for (int h = 0; h < KPS / 16; ++h) {
+          for (int h = 0; h < HALVES; ++h) {
             const bool ok = (unsigned)pg[h] < (unsigned)p.num_pages;
-            const uint32_t bit = 1u << (st * 2 + h);
-            absent = ok ? absent & ~bit : absent | bit;
-            saw_absent = saw_absent || !ok;
-            row[h] = qda_pool_row(ok ? pg[h] : 0, t.unit, (n0 + 16 * h) & pmask, p.Hkv, p.page_shift);
+            gone |= ok ? 0u : 1u << h;
+            row[h] = ((((uint32_t)(ok ? pg[h] : 0) * p.Hkv) + t.unit) << p.page_shift) + ((fill_n + 16 * h) & pmask);
+          }
+          if (gone | absent) {   // rare
+            absent = (absent & ~(3u << (2 * fill_stage))) | gone << (2 * fill_stage);
+            saw_absent = saw_absent || gone;
+          }
+          constexpr int PER = 16 * RB / 512;   // copies of 32 lanes per half
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            const char* ksrc = reinterpret_cast<const char*>(p.kp) + (uint64_t)row[h] * RB + lane * 16;
+            const char* vsrc = reinterpret_cast<const char*>(p.vp) + (uint64_t)row[h] * RB + lane * 16;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+              const int at = ((h * PER + i) * 32 + lane) * 16, key = at / RB;
+              const uint32_t dst = base + (at ^ ps_turn<RB>(key));
+              ps_cp16(dst, ksrc + i * 512);
+              ps_cp16(dst + G::CODE, vsrc + i * 512);
+            }
           }
 #pragma unroll
-          for (int i = 0; i < G::CODE / 512; ++i) {
-            const int at = (i * 32 + lane) * 16, key = at / RB, col = at % RB;
-            const long long src = (row[KPS == 32 ? (i * 512 / RB) / 16 : 0] + (key & 15)) * RB + col;
-            const uint32_t dst = base + ((key * RB + col) ^ ps_turn<RB>(key));
-            ps_cp16(dst, reinterpret_cast<const char*>(p.kp) + src);
-            ps_cp16(dst + G::CODE, reinterpret_cast<const char*>(p.vp) + src);
-          }
-          // scales and biases: 16 keys' are contiguous, NG * 2 pieces of 16 bytes per array and half
-          constexpr int PC = KPS / 16 * NG * 2;   // pieces per array
-#pragma unroll
-          for (int i = 0; i < (4 * PC + 31) / 32; ++i) {
+          for (int i = 0; i < SI; ++i) {
             const int id = i * 32 + lane, a = id / PC, k16 = id % PC;
             if (id < 4 * PC) {
               const uint16_t* arr = a == 0 ? p.ks : a == 1 ? p.kb : a == 2 ? p.vs : p.vb;
-              const int h = KPS == 32 ? k16 / (NG * 2) : 0;
-              const long long src = row[h] * (NG * 2) + (k16 - h * NG * 2) * 16;
-              ps_cp16(base + 2 * G::CODE + a * G::SC + k16 * 16, reinterpret_cast<const char*>(arr) + src);
+              const int h = HALVES == 2 ? k16 / (NG * 2) : 0;
+              const char* src = reinterpret_cast<const char*>(arr) + (k16 - h * NG * 2) * 16 +
+                                (uint64_t)(HALVES == 2 && h ? row[HALVES - 1] : row[0]) * (NG * 2);
+              ps_cp16(base + 2 * G::CODE + a * G::SC + k16 * 16, src);
             }
           }
-          look(k + 1);
+          fill_stage = fill_stage + 1 == STAGES ? 0 : fill_stage + 1;
+          fill_n += STEP;
+          --fill_left;
+          look();
         }
         ps_commit();
       };
 
-      look(0);
+      look();
 #pragma unroll
-      for (int k = 0; k < STAGES - 1; ++k) issue(k);   // under way while the queries are prepared
+      for (int k = 0; k < STAGES - 1; ++k) issue();   // under way while the queries are prepared
 
       // ---- the tile's query rows: B operands, sums per group, and how far each sees
       uint2 qf[G::QSMEM ? 1 : D / 16 * NT];
@@ -373,15 +384,15 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
       uint32_t most = 0;        // 16-bit pattern of the largest value scale that the weights' unit allows
       float vexp = 0.f;         // everything that is summed is taken times 2^vexp, an integer
 
+      int st = 0, first = (j0 + warp) * KPS;   // the block's stage and first key
       for (int k = 0; k < mine_n; ++k) {
-        issue(k + STAGES - 1);   // into the stage read one block ago
+        issue();   // into the stage read one block ago
         ps_wait<STAGES - 1>();
         __syncwarp();   // every lane's pieces of the stage are in
-        const int st = k % STAGES;
         const uint32_t base = ring + st * G::STAGE;
 #pragma unroll 1
         for (int h = 0; h < KPS / 16; ++h) {
-          const int n0 = (j0 + warp + k * kPsWarps) * KPS + 16 * h;
+          const int n0 = first + 16 * h;
           if (n0 >= keys) break;
           const bool gone = (absent >> (st * 2 + h)) & 1u;
           const bool edge = gone || n0 + 16 > least;
@@ -612,6 +623,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           }
         }
         __syncwarp();   // the stage is read before it is filled again
+        st = st + 1 == STAGES ? 0 : st + 1;
+        first += STEP;
       }
       ps_wait<0>();
 
