@@ -479,7 +479,7 @@ int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int
     }
   } else {
     plan->rows = rows > 8 && D <= 256 ? 16 : 8;
-    plan->min_keys = 128;
+    plan->min_keys = 176;
     plan->parts = 1;
     static std::atomic<int> cache[64][2][2][4][3][2] = {};   // resident CTAs per SM of an instance, 0 = not asked yet
     std::atomic<int>& slot = cache[dev][bits == 8][f16][di][gi][plan->rows == 16];

@@ -58,14 +58,17 @@ struct PcGeom {
   static constexpr int SLOTS0 = (226 * 1024 - 1024 - QB) / SLOT;
   static constexpr int SLOTS = SLOTS0 > 6 ? 6 : SLOTS0;
   static constexpr int SOFT = 4 * NQ;                   // softmax warps
-  static constexpr int DEQ = 8;                         // dequantising warps
+  // dequantising warps. Sixteen with half the work and the registers each hide more latency than eight that fetch three items
+  // ahead (ragged chunks at D = 256: 550 against 576 us; D = 512: 104 against 109); two tiles leave no registers for them
+  static constexpr bool MANY = NQ == 1 && D >= 128;
+  static constexpr int DEQ = MANY ? 16 : 8;
   static constexpr int WARPS = SOFT + DEQ + 1 + kPcInfoWarps;
-  // registers a thread: the launch's 96 (20 warps) or 128 (16 warps), dealt out anew among the warpgroups
-  static constexpr int R_ALL = NQ == 2 ? 96 : 128;
-  static constexpr int R_SOFT = NQ == 2 ? 136 : 136, R_DEQ = NQ == 2 ? 72 : 136, R_LAST = NQ == 2 ? 64 : 96;
+  // registers a thread: the launch's 80 (24 warps), 96 (20) or 128 (16), dealt out anew among the warpgroups
+  static constexpr int R_ALL = MANY ? 80 : NQ == 2 ? 96 : 128;
+  static constexpr int R_SOFT = 136, R_DEQ = MANY ? 64 : NQ == 2 ? 72 : 136, R_LAST = MANY || NQ == 2 ? 64 : 96;
   static_assert(SOFT * R_SOFT + DEQ * R_DEQ + 4 * R_LAST <= WARPS * R_ALL, "registers of the launch");
   // items of codes under way: what the registers hold, and a divisor of a block's items less one
-  static constexpr int AHEAD = D <= 128 ? 1 : D == 256 ? 3 : BITS == 4 ? 5 : 2;
+  static constexpr int AHEAD = D == 512 && BITS == 4 ? 2 : 1;
   static constexpr int O_COL = 256;                     // O behind two S buffers of 128 columns
   static_assert(NQ == 1 || D <= 128, "two tiles need room for two O");
   static_assert(SLOTS >= 3 && O_COL + NQ * DV <= 512, "shared or tensor memory");
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         constexpr int LPR = D < 256 ? D / 8 : 32;   // lanes per row, 16 bytes each
         constexpr int RPI = 32 / LPR;               // rows at a time
         constexpr int C = D / 8 / LPR;              // pieces per lane
-        constexpr int U = 4;                        // row groups in flight
+        constexpr int U = 8 / C;                    // row groups in flight
         const int sub = lane / LPR, l = lane % LPR;
 #pragma unroll 1
         for (int g0 = 0; g0 < 32 / RPI; g0 += U) {
@@ -871,6 +874,14 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
               e.part = t.unit % G::PARTS;
               e.b = t.b;
               e.s = t.s;
+            }
+            // the softmax warps read the tile's queries when they are done with the tile before: on their way to L2 until then
+            for (int x = lane; NQ == 1 && x < MT; x += 32) {
+              const int r = t.i * MT + x, tok = r / p.nrep;
+              if (r >= t.s.rows) break;
+              const uint16_t* row = p.q + (long long)(t.s.first + tok) * p.q_tstride +
+                                    (long long)(t.unit / G::PARTS * p.nrep + (r - tok * p.nrep)) * p.q_hstride;
+              for (int i = 0; i < D / 64; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + 64 * i));
             }
           }
           __syncwarp();

@@ -268,8 +268,9 @@ int qdecode_cache_append(const uint32_t* k_packed, const void* k_scales, const v
  * and a slot is page_id * page + row. (The pages this library follows hold one contiguous cache per step, maya-mac
  * mlx_kernels.py, _ATTEND; they have no counterpart of this section.) Lengths, tables and slots are int32 DEVICE
  * arrays, read by the kernels only: a step can be captured once in a CUDA graph and replayed as they change.
- * page is a power of two from 16 to 256; num_pages * page < 2^31, num_pages * page * Hkv < 2^32 - 1. What the host cannot check is checked on the device:
- * an entry of the table or of slots outside the pool is skipped and sets bit 8 of qdecode_attn_device_status().
+ * page is a power of two from 16 to 256; num_pages * page < 2^31, num_pages * page * Hkv < 2^32 - 1. What the host
+ * cannot check is checked on the device: an entry of the table or of slots outside the pool is skipped and sets bit 8
+ * of qdecode_attn_device_status().
  */
 #define QDA_PAGE_MIN 16
 #define QDA_PAGE_MAX 256
@@ -312,10 +313,19 @@ int qdecode_paged_append(const void* k, const void* v, long long k_tstride, long
  * sequence's last, already appended):
  *     out[t, h, :] = sum_n softmax_n( q[t, h, :] . k_hat[n] / sqrt(D) ) v_hat[n]
  * causal = 0 is cross attention to states of another length (an encoder's, appended once). A token that sees no key
- * gives zeros. Rows of out at and behind q_start[B] stay as they are. max_q (>= 1) is the host's bound on the L_b and
- * only chooses the kernel: results are right for any value. q has strides q_tstride, q_hstride in elements; out is
- * contiguous [total_q, H, D] in q's dtype. dtype is the input dtype alone (q, scales, biases and out). Supported: the bits, GS and D of qdecode_attn,
- * H / Hkv <= QDA_MAX_NREP, B <= QDA_MAX_B. Uses the workspace as qdecode_attn does, of
+ * gives zeros. Keys that a token does not see, rows of pages behind kv_len[b] among them, reach nothing, whatever they
+ * hold. Rows of out at and behind q_start[B] stay as they are. max_q (>= 1) is the host's bound on the L_b and only
+ * chooses the kernel: results are right for any value. Calls of up to 32 rows per KV head (max_q * H / Hkv; 16 at D =
+ * 256, 48 at D = 512) take a kernel that reads the codes into matrix instructions as they are, with scores right to
+ * fp32 and weights rounded to 11 significant bits; larger ones a kernel that turns the codes into fp16 operands (keys,
+ * values and weights rounded to 11 significant bits). All sums and the softmax are fp32 in both. Scales and biases are
+ * meant to be finite and below 2^64 in magnitude: a token that sees a key with others may become infinite or NaN (in
+ * the second kernel NaN from 2^110 on), tokens that do not see it do not. In the second kernel a block of 128 keys
+ * shares a power of two, and so do all values up to a block: rows 2^10 times smaller than the largest there keep their
+ * 11 bits, smaller ones lose a bit with every further factor of two. q has strides q_tstride, q_hstride in elements;
+ * out is contiguous [total_q, H, D] in q's dtype. dtype is the input dtype alone (q, scales, biases and out).
+ * Supported: the bits, GS and D of qdecode_attn, H / Hkv <= QDA_MAX_NREP, B <= QDA_MAX_B. Uses the workspace as
+ * qdecode_attn does, of
  * qdecode_paged_attn_workspace_bytes() bytes.
  */
 int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
@@ -343,10 +353,10 @@ int qdecode_attn_last_cuda_error(void);
 
 /*
  * Device-side status: copies (synchronously) and clears the current device's error word. Bits: 1 = a pipeline
- * wait in the split kernel gave up after its time limit (the output of that call is invalid); 2 = waiting for the
- * CTA's own copies to land before it exits gave up; 4 = an index check failed (only a library built with
- * QDA_BOUNDS_CHECK checks, and it skips the access); 8 = a paged call met a page, slot or length outside its pool or
- * table. 0 = clean.
+ * wait in a split kernel or in the paged calls' chunk kernel gave up after its time limit (the output of that call is
+ * invalid); 2 = waiting for the CTA's own copies or products to land before it exits gave up; 4 = an index check failed
+ * (only a library built with QDA_BOUNDS_CHECK checks, and it skips the access); 8 = a paged call met a page, slot or
+ * length outside its pool or table. 0 = clean.
  */
 int qdecode_attn_device_status(unsigned int* flags);
 
