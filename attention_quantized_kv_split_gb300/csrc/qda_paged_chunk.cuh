@@ -57,18 +57,14 @@ struct PcGeom {
   static constexpr int QB = MT * D * 2;
   static constexpr int SLOTS0 = (226 * 1024 - 1024 - QB) / SLOT;
   static constexpr int SLOTS = SLOTS0 > 6 ? 6 : SLOTS0;
-  static constexpr int SOFT = 4 * NQ;                   // softmax warps
-  // dequantising warps. Sixteen with half the work and the registers each hide more latency than eight that fetch three items
-  // ahead (ragged chunks at D = 256: 550 against 576 us; D = 512: 104 against 109); two tiles leave no registers for them
-  static constexpr bool MANY = NQ == 1 && D >= 128;
-  static constexpr int DEQ = MANY ? 16 : 8;
+  static constexpr int SOFT = 8;                        // softmax warps
+  static constexpr int DEQ = 8;                         // dequantising warps
   static constexpr int WARPS = SOFT + DEQ + 1 + kPcInfoWarps;
-  // registers a thread: the launch's 80 (24 warps), 96 (20) or 128 (16), dealt out anew among the warpgroups
-  static constexpr int R_ALL = MANY ? 80 : NQ == 2 ? 96 : 128;
-  static constexpr int R_SOFT = 136, R_DEQ = MANY ? 64 : NQ == 2 ? 72 : 136, R_LAST = MANY || NQ == 2 ? 64 : 96;
+  // registers a thread: the launch's 96, dealt out anew among the warpgroups
+  static constexpr int R_ALL = 96, R_SOFT = 136, R_DEQ = 72, R_LAST = 64;
   static_assert(SOFT * R_SOFT + DEQ * R_DEQ + 4 * R_LAST <= WARPS * R_ALL, "registers of the launch");
   // items of codes under way: what the registers hold, and a divisor of a block's items less one
-  static constexpr int AHEAD = D == 512 && BITS == 4 ? 2 : 1;
+  static constexpr int AHEAD = 1;
   static constexpr int O_COL = 256;                     // O behind two S buffers of 128 columns
   static_assert(NQ == 1 || D <= 128, "two tiles need room for two O");
   static_assert(SLOTS >= 3 && O_COL + NQ * DV <= 512, "shared or tensor memory");
@@ -89,6 +85,9 @@ struct PcShared {
   uint64_t info_full[kPcInfo], info_empty[kPcInfo], tile_full[kPcTiles], tile_empty[kPcTiles], full[6], empty[6], q_full,
       s_full[2], p_full[2], drain;
   uint64_t pv_done[2];    // two tiles: a tile's last values; one: values of even and odd blocks
+  uint64_t pair[4];       // one tile: the two warps that share 32 rows
+  float row[128];         // what they tell each other
+  int rise[2][8];
   PagedTile t;
   long long x[2];
   uint32_t tmem;
@@ -259,9 +258,10 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     mbar_init(&sh.q_full, G::SOFT);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 4);
+      mbar_init(&sh.p_full[i], 8 / NQ);
       mbar_init(&sh.pv_done[i], 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.pair[i], 2);
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
     fence_barrier_init();
@@ -302,13 +302,29 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
   auto it_v = [&](int j, int n) { return ic + KSL + j * (KSL + VSL) + (j + 1 < n ? KSL : 0); };
 
   if (warp < G::SOFT) {
-    // =================================================================================== softmax: a thread per row
+    // =================================================================================== softmax: one or two threads per row
     pc_regs<G::R_SOFT, G::R_ALL>();
-    const int tq = warp >> 2;
+    // two tiles: a warpgroup each, a thread per row. One: two threads per row, in warps w and w + 4; each takes half of the
+    // block's keys and half of the row's values
+    const int tq = NQ == 2 ? warp >> 2 : 0, half = NQ == 2 ? 0 : warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
     const int rt = tq * 128 + 32 * (warp & 3) + lane;   // row of the tile
     const uint32_t o_t = tmem + lanes + G::O_COL + tq * DV;
-    // The warp's 32 query rows into shared memory, in the codes' unpacked order, each row scaled by a power of two; returns what undoes this thread's
+    uint32_t pairs = 0;
+    auto pair_sync = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pair[warp & 3]);
+      wait(&sh.pair[warp & 3], pairs++);
+    };
+    // both threads of a row get f(the first one's x, the second one's)
+    auto both = [&](float x, auto f) {
+      if (half == 0) sh.row[rt] = x;
+      pair_sync();
+      if (half == 1) sh.row[rt] = x = f(sh.row[rt], x);
+      pair_sync();
+      return half == 0 ? sh.row[rt] : x;
+    };
+    // The warp's query rows into shared memory, in the codes' unpacked order, each row scaled by a power of two; returns what undoes this thread's
     // row's scale, times the softmax scale. With one tile a row is read by lanes side by side; with two tiles (D <= 128) a thread reads its own
     // row, which is slower by itself, but the other form costs the softmax loop registers there (ragged chunks at D = 256: 574 against 624 us for
     // the first form; chunk over 32768 keys at D = 128: 869 us with the second, 887 with the first).
@@ -370,14 +386,16 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         constexpr int LPR = D < 256 ? D / 8 : 32;   // lanes per row, 16 bytes each
         constexpr int RPI = 32 / LPR;               // rows at a time
         constexpr int C = D / 8 / LPR;              // pieces per lane
-        constexpr int U = 8 / C;                    // row groups in flight
+        constexpr int U = 8 / C < 16 / RPI ? 8 / C : 16 / RPI;   // row groups in flight
+        const int row0 = 32 * (warp & 3) + 16 * half;            // the warp's 16 rows
         const int sub = lane / LPR, l = lane % LPR;
+        pair_sync();                                // the other warp has read what `both` left in sh.row
 #pragma unroll 1
-        for (int g0 = 0; g0 < 32 / RPI; g0 += U) {
+        for (int g0 = 0; g0 < 16 / RPI; g0 += U) {
           uint4 a[U][C];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int r = t.row0 + 32 * warp + (g0 + u) * RPI + sub;
+            const int r = t.row0 + row0 + (g0 + u) * RPI + sub;
             const uint4* qp = row_at(r);
 #pragma unroll
             for (int c = 0; c < C; ++c) a[u][c] = r < t.s.rows ? __ldg(qp + l + 32 * c) : make_uint4(0, 0, 0, 0);
@@ -392,11 +410,13 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
             const int fe = scale_of(top);
 #pragma unroll
             for (int c = 0; c < C; ++c)
-              store(v[c], __uint_as_float((uint32_t)fe << 23), 32 * warp + (g0 + u) * RPI + sub, l + 32 * c);
-            const float mine = __shfl_sync(0xffffffffu, __uint_as_float((uint32_t)(254 - fe) << 23), (lane % RPI) * LPR);
-            if (lane / RPI == g0 + u) mul = mine;   // this thread's row is among these
+              store(v[c], __uint_as_float((uint32_t)fe << 23), row0 + (g0 + u) * RPI + sub, l + 32 * c);
+            if (l == 0) sh.row[row0 + (g0 + u) * RPI + sub] = __uint_as_float((uint32_t)(254 - fe) << 23);
           }
         }
+        pair_sync();
+        mul = sh.row[rt];
+        pair_sync();
       }
       fence_proxy_async();
       __syncwarp();
@@ -429,7 +449,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         const bool edge = __any_sync(0xffffffffu, left < kPcKeys);
         if (flags) {   // rare: keys on absent pages are hidden; who sees a key that is not finite becomes NaN
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
+          for (int c = 4 * half; c < (NQ == 2 ? 8 : 4 * half + 4); ++c) {
             const uint32_t gone = f.gone[c >> 1] >> (16 * (c & 1)), bad = f.bad[c >> 1] >> (16 * (c & 1));
             float v[16];
             pc_ld16(s_t + 16 * c, v);
@@ -458,20 +478,20 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
             }
             const float x = a * pc_ex2((float)(kv - kv_new));
 #pragma unroll 1
-            for (int c = 0; c < DV / 8; ++c) pc_scale8(o_t + 8 * c, x);
+            for (int c = half * (DV / 16); c < (NQ == 2 ? DV / 8 : (half + 1) * (DV / 16)); ++c) pc_scale8(o_t + 8 * c, x);
           }
           kv = kv_new;
         };
-        // The row's 128 scores do not fit the registers next to everything else: the second half is read for its maximum, the
+        // Two tiles: the row's 128 scores do not fit the registers next to everything else: the second half is read for its maximum, the
         // first is read and kept, and the second read again as the first's registers come free. Weights lie over the
         // first half's scores.
         float u[2][32];
-        auto get = [&](float (&x)[32], int c) { pc_ld32(s_t + 32 * c, x); };
+        auto get = [&](float (&x)[32], int c) { pc_ld32(s_t + 64 * half + 32 * c, x); };
         auto hide = [&](float (&x)[32], int c) {
           if (edge) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= left) x[i] = -INFINITY;
+              if (32 * c + i >= left - 64 * half) x[i] = -INFINITY;
           }
         };
         auto largest = [&](const float (&x)[32]) {
@@ -483,12 +503,15 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           }
           return fmaxf(pc_max3(a, b, x[30]), x[31]);
         };
-        get(u[0], 2);
-        get(u[1], 3);
-        tmem_wait_ld();
-        hide(u[0], 2);
-        hide(u[1], 3);
-        float top = fmaxf(largest(u[0]), largest(u[1]));
+        float top = -INFINITY;
+        if constexpr (NQ == 2) {
+          get(u[0], 2);
+          get(u[1], 3);
+          tmem_wait_ld();
+          hide(u[0], 2);
+          hide(u[1], 3);
+          top = fmaxf(largest(u[0]), largest(u[1]));
+        }
         get(u[0], 0);
         get(u[1], 1);
         tmem_wait_ld();
@@ -496,7 +519,17 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         hide(u[1], 1);
         top = pc_max3(top, largest(u[0]), largest(u[1])) * mult;   // mult > 0
         if (j == 0) kv = kv_new;
-        if (__any_sync(0xffffffffu, top > m + 8.f) || kv_new != kv) rescale(top);
+        bool rise = __any_sync(0xffffffffu, top > m + 8.f || kv_new != kv);
+        if constexpr (NQ == 1) {
+          // does the other half of any row rise? Behind this both halves hold their scores in registers and weights may lie over them
+          tc_fence_before();
+          if (lane == 0) sh.rise[g & 1][warp] = rise;
+          pair_sync();
+          tc_fence_after();
+          rise = rise || sh.rise[g & 1][warp ^ 4] != 0;
+          if (rise) top = both(top, [](float x, float y) { return fmaxf(x, y); });
+        }
+        if (rise) rescale(top);
         const float mm = m == -INFINITY ? 0.f : -m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         auto weigh = [&](const float (&x)[32], int c) {
@@ -508,18 +541,20 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
             sum[i & 1] = __fadd2_rn(sum[i & 1], y);
             w[i] = pc_h2(y.x, y.y);
           }
-          tmem_st16(s_t + 16 * c, w);
+          tmem_st16(s_t + 32 * half + 16 * c, w);
         };
         weigh(u[0], 0);
-        get(u[0], 2);
+        if (NQ == 2) get(u[0], 2);
         weigh(u[1], 1);
-        tmem_wait_ld();
-        get(u[1], 3);
-        hide(u[0], 2);
-        weigh(u[0], 2);
-        tmem_wait_ld();
-        hide(u[1], 3);
-        weigh(u[1], 3);
+        if constexpr (NQ == 2) {
+          tmem_wait_ld();
+          get(u[1], 3);
+          hide(u[0], 2);
+          weigh(u[0], 2);
+          tmem_wait_ld();
+          hide(u[1], 3);
+          weigh(u[1], 3);
+        }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
@@ -540,17 +575,18 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         else wait(&sh.pv_done[g & 1], g >> 1);
         tc_fence_after();
         if (poison) l = __uint_as_float(0x7fc00000u);
+        if (NQ == 1) l = both(l, [](float x, float y) { return x + y; });
         scale = pc_ex2((float)kv) * (t->whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f);
       }
       const bool whole = t->whole;
-      const bool none = m == -INFINITY && !poison;   // the row saw no key
+      const bool none = m == -INFINITY && l == l;   // the row saw no key
       const int tok = r / p.nrep;
       const size_t slot = (size_t)(2 * cta + t->mine) * MT + rt;
       uint4* out = reinterpret_cast<uint4*>(
           p.out + ((long long)(t->s.first + tok) * p.H + t->kvh * p.nrep + (r - tok * p.nrep)) * D + t->part * DV);
       float4* po = reinterpret_cast<float4*>(p.part_o + slot * DV);
 #pragma unroll 1
-      for (int c = 0; c < DV / 32; ++c) {
+      for (int c = half * (DV / 64); c < (NQ == 2 ? DV / 32 : (half + 1) * (DV / 64)); ++c) {
         float v[2][16];
         if (n > 0) {
           pc_ld16(o_t + 32 * c, v[0]);
@@ -582,7 +618,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           for (int x = 0; x < 8; ++x) po[8 * c + x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
         }
       }
-      if (real && !whole) p.part_ml[slot] = make_float2(m, l);
+      if (real && !whole && half == 0) p.part_ml[slot] = make_float2(m, l);
       tc_fence_before();
       bc += n;
       tc += n > 0;
