@@ -450,9 +450,10 @@ SplitFn split_fn(int bits, bool f16) {
 }
 
 // Rows (new tokens times query heads of a KV head) up to which the split kernel takes a call. Its time grows with every 16 rows (8 at
-// D = 512), the chunk kernel's stays the same up to 128. Split against chunk kernel at 32 rows: D 64 (32 sequences, 8-bit) 79 / 85 us, D 128 (16
-// sequences, 4-bit) 101 / 99, one sequence of 32768 keys 43 / 47, D 512 80 / 104 (48 rows: 107 / 110); D 256 (8-bit) 91 / 67, and at 16 rows 60 / 64.
-constexpr long long split_rows(int D) { return D == 512 ? 48 : D == 256 ? 16 : 32; }
+// D = 512), the chunk kernel's stays the same up to 128. Split against chunk kernel, 8 KV heads and about 90000 keys in all: D 64, 8-bit, 32 rows
+// 84 / 85 us (64 rows 100 / 97), D 128, 4-bit, 16 rows 65 / 99, 32 rows 107 / 100 (one sequence alone 82 / 86), D 256, 4-bit, 16 rows
+// 98 / 130 (32 rows of 4 sequences' tokens 91 / 67), D 512, 4-bit, 16 rows 240 / 339, 32 rows 455 / 338 (of one short sequence 80 / 95).
+constexpr long long split_rows(int D) { return D == 512 ? 24 : D == 256 ? 16 : 32; }
 
 cudaError_t chunk_run(const QdaPagedParams* p, int D, int bits, int rows, bool prepare, cudaStream_t s) {
   return bits == 4 ? qda_paged_chunk_b4(p, D, rows / 128, prepare, s) : qda_paged_chunk_b8(p, D, rows / 128, prepare, s);

@@ -3,10 +3,12 @@
 // One CTA per SM takes a tile of 128 query rows of a KV head, or two of them side by side (D <= 128), and walks the tile's keys in blocks
 // of 128: S = Q K^T and O += P V on tcgen05 (fp16 operands, fp32 sums in tensor memory), an online softmax in between. Rows are (token, query head)
 // pairs, so all query heads of a KV head share a block's keys and values, which are turned from codes into operands once per block:
-//   dequantising warps   codes -> fp16 tiles in shared memory (a ring of slots of 128 keys x 128 dimensions), next slot's codes in flight in registers;
-//   softmax warps        one thread per query row: reads its row of S from tensor memory, writes P (fp16) over it;
+//   dequantising warps   codes -> fp16 tiles in shared memory (a ring of slots of 128 keys x 128 dimensions), the next slots' codes in flight in registers;
+//   softmax warps        eight: one thread per query row with two tiles, two threads (half of the keys, half of the values) with one. They read S
+//                        from tensor memory and write P (fp16) over it;
 //   MMA warp             one thread issues every product. With two tiles the products of one run while the softmax of the other does;
-//                        with one tile S has two buffers and the next block's scores run during this block's softmax;
+//                        with one tile S has two buffers and the next block's scores run during this block's softmax. Two threads per row took
+//                        ragged chunks at D = 256 from 487 to 453 us (the lone softmax warp of a scheduler waited for itself);
 //   info warps           blocks ahead: a block's pages, and how large its keys and values can be.
 // Every link is an mbarrier; every wait is bounded and sets the device error word.
 //
@@ -63,7 +65,8 @@ struct PcGeom {
   // registers a thread: the launch's 96, dealt out anew among the warpgroups
   static constexpr int R_ALL = 96, R_SOFT = 136, R_DEQ = 72, R_LAST = 64;
   static_assert(SOFT * R_SOFT + DEQ * R_DEQ + 4 * R_LAST <= WARPS * R_ALL, "registers of the launch");
-  // items of codes under way: what the registers hold, and a divisor of a block's items less one
+  // items of codes under way: a divisor of a block's items less one. More would cost the softmax warps their registers (453 us
+  // of ragged chunks at D = 256 become 480 with 120 registers there, 720 with 104)
   static constexpr int AHEAD = 1;
   static constexpr int O_COL = 256;                     // O behind two S buffers of 128 columns
   static_assert(NQ == 1 || D <= 128, "two tiles need room for two O");
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     };
     // The warp's query rows into shared memory, in the codes' unpacked order, each row scaled by a power of two; returns what undoes this thread's
     // row's scale, times the softmax scale. With one tile a row is read by lanes side by side; with two tiles (D <= 128) a thread reads its own
-    // row, which is slower by itself, but the other form costs the softmax loop registers there (ragged chunks at D = 256: 574 against 624 us for
+    // row, which is slower by itself, but the other form costs the softmax loop registers there (ragged chunks at D = 256: 575 against 622 us for
     // the first form; chunk over 32768 keys at D = 128: 869 us with the second, 887 with the first).
     auto load_q = [&](const PcTile& t) {
       float mul = 0.f;

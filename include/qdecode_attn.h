@@ -316,7 +316,7 @@ int qdecode_paged_append(const void* k, const void* v, long long k_tstride, long
  * gives zeros. Keys that a token does not see, rows of pages behind kv_len[b] among them, reach nothing, whatever they
  * hold. Rows of out at and behind q_start[B] stay as they are. max_q (>= 1) is the host's bound on the L_b and only
  * chooses the kernel: results are right for any value. Calls of up to 32 rows per KV head (max_q * H / Hkv; 16 at D =
- * 256, 48 at D = 512) take a kernel that reads the codes into matrix instructions as they are, with scores right to
+ * 256, 24 at D = 512) take a kernel that reads the codes into matrix instructions as they are, with scores right to
  * fp32 and weights rounded to 11 significant bits; larger ones a kernel that turns the codes into fp16 operands (keys,
  * values and weights rounded to 11 significant bits). All sums and the softmax are fp32 in both. Scales and biases are
  * meant to be finite and below 2^64 in magnitude: a token that sees a key with others may become infinite or NaN (in
