@@ -33,7 +33,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const QdaPagedParams& p, int start
   s.first = q0;
   s.rows = (q1 - q0) * p.nrep;
   s.tiles = (s.rows + MT - 1) / MT;
-  s.n_all = (int)min((long long)n, (long long)p.max_pages << p.page_shift);
+  s.n_all = (int)min(min((long long)n, (long long)p.max_pages << p.page_shift), 0x7ffffe00LL);   // sums with a block's keys stay in range
   s.base = p.causal ? n - (q1 - q0) : s.n_all;
   return s;
 }
@@ -52,9 +52,9 @@ __device__ __forceinline__ long long paged_prefix(const QdaPagedParams& p, const
   return p.causal ? flat + (long long)MT * ((long long)i * (i + 1) / 2) : flat;
 }
 
-// a / b for a >= 0, b > 0; 64-bit division only where it is needed.
-__device__ __forceinline__ long long paged_div(long long a, long long b) {
-  if (((unsigned long long)a | (unsigned long long)b) >> 32) return a / b;
+// a / b for b > 0; 64-bit division only where it is needed.
+__device__ __forceinline__ long long paged_div(unsigned long long a, unsigned long long b) {
+  if ((a | b) >> 32) return (long long)(a / b);
   return (uint32_t)a / (uint32_t)b;
 }
 
@@ -175,7 +175,7 @@ __device__ __forceinline__ int paged_tile_keys(const QdaPagedParams& p, const Pa
 __device__ __forceinline__ int paged_block_at(const PagedTile& t, int nblk, long long x) {
   if (x <= t.lo) return 0;
   if (x >= t.hi) return nblk;
-  return (int)paged_div((x - t.lo) * nblk, t.hi - t.lo);
+  return (int)paged_div((unsigned long long)(x - t.lo) * nblk, t.hi - t.lo);   // below 2^31 * 2^6 * 2^27
 }
 
 // Behind CTA k's part [j0, j1) of tile t (one thread): what the merge has to know of the tile, if it starts in piece k and goes on behind it, and

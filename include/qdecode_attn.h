@@ -324,9 +324,9 @@ int qdecode_paged_append(const void* k, const void* v, long long k_tstride, long
  * shares a power of two, and so do all values up to a block: rows 2^10 times smaller than the largest there keep their
  * 11 bits, smaller ones lose a bit with every further factor of two. q has strides q_tstride, q_hstride in elements;
  * out is contiguous [total_q, H, D] in q's dtype. dtype is the input dtype alone (q, scales, biases and out).
- * Supported: the bits, GS and D of qdecode_attn, H / Hkv <= QDA_MAX_NREP, B <= QDA_MAX_B. Uses the workspace as
- * qdecode_attn does, of
- * qdecode_paged_attn_workspace_bytes() bytes.
+ * Supported: the bits, GS and D of qdecode_attn, H / Hkv <= QDA_MAX_NREP, B <= QDA_MAX_B, total_q * H / Hkv below
+ * 2^31 - 256, kv_len below 2^31 - 512 (keys behind that are not seen). Uses the workspace as qdecode_attn does, of
+ * qdecode_paged_attn_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
  */
 int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                        const void* k_scales, const void* k_biases, const uint32_t* v_packed, const void* v_scales,

@@ -144,3 +144,9 @@ def test_packed_calls(L):
         x = list(args)
         x[i] = v
         assert call(op, P(*x)) == status, (op, i, v)
+
+
+@pytest.mark.parametrize("total_q,H,Hkv", [((1 << 31) - 1, 8, 2), (1 << 25, 64, 1), ((1 << 31) - 200, 1, 1)])
+def test_attn_refuses_query_rows_beyond_32_bits(L, total_q, H, Hkv):
+    # rows are (token, query head of the KV head) pairs, counted in 32 bits by the kernels
+    assert attn(L, total_q=total_q, H=H, Hkv=Hkv) == UNSUPPORTED
