@@ -491,3 +491,25 @@ def test_two_graphs_share_the_workspace():
         torch.cuda.synchronize()
         for o, r in zip(outs, ref):
             assert torch.equal(o, r)
+
+
+@pytest.mark.parametrize("D,GS,bits,dtype", [(64, 32, 8, "bf16"), (128, 64, 4, "fp16"), (256, 32, 8, "bf16"), (512, 128, 4, "bf16")])
+def test_pages_outside_the_pool_where_a_tile_has_two_threads_per_row(D, GS, bits, dtype):
+    # 60 and 100 query rows per KV head: absent pages in both halves of a block of keys, and a whole absent block
+    c = Case([30, 50], [300, 420], 4, 2, D, bits, GS, dtype, 32, seed=21)
+    absent = {0: [1, 2], 1: [4, 5, 6, 7, 11]}
+    for b, cols in absent.items():
+        for i, col in enumerate(cols):
+            c.table[b, col] = -1 - i
+    got = c.run(False)
+    torch.cuda.synchronize()
+    assert qda.qdecode_attn_device_status() == 8
+    c.check(got, False, hidden=[(b, n) for b, cols in absent.items() for col in cols for n in range(32 * col, 32 * col + 32)])
+
+
+@pytest.mark.parametrize("D,GS,bits", [(64, 32, 8), (128, 64, 4), (256, 64, 4), (256, 32, 8), (512, 64, 4)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_strong_scores_where_a_tile_has_two_threads_per_row(D, GS, bits, causal):
+    # a row's reference rises again and again, from either half of a block of keys
+    c = Case([15, 9, 21], [900, 2000, 131], 8, 2, D, bits, GS, "bf16", 16, seed=22, q_scale=4.0)
+    c.check(c.run(causal), causal)
