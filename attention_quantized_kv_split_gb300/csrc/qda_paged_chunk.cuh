@@ -13,8 +13,8 @@
 // Every link is an mbarrier; every wait is bounded and sets the device error word.
 //
 // Measured: 2048 tokens over 32768 keys (32 heads, 8 KV heads, D 128, 4-bit) 863 us, 1.24 PFLOP/s, 65 % of a large bf16 product's rate: the softmax of
-// 256 rows and the dequantising share the issue slots. Ragged chunks at D 256, 8-bit, 453 us (0.54 PFLOP/s): one tile per CTA, so a block is dequantised
-// for 128 rows only. Cross attention at D 64 66 us, 250 tokens over 4097 keys at D 512 99 us: start, first blocks and merge.
+// 256 rows and the dequantising share the issue slots. Ragged chunks at D 256, 8-bit, 427 us (0.57 PFLOP/s): one tile per CTA, so a block is dequantised
+// for 128 rows only. Cross attention at D 64 64 us, 250 tokens over 4097 keys at D 512 99 us: start, first blocks and merge.
 //
 // Operands are fp16 for both input types (11 significant bits; for bf16 caches the operands then add almost nothing to the one
 // rounding of the result, where bf16 operands would double it), and ranges are taken care of by powers of two: a query row is scaled so that its largest value

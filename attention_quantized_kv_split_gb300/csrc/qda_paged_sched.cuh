@@ -16,9 +16,9 @@
 namespace qda {
 
 // A tile's fixed work (its query rows, its results), in keys. Chunk kernel (tiles of 128 rows or more): ragged chunks of 1 to 1023 tokens at
-// D = 256 take 528 us with 64, 501 with 256, 494 with 448, cross attention at D = 64 69.0, 65.8 and 66.2 us. Split kernel: one token of
-// each of 64 sequences 100.2 us with 64, 96.9 with 160, 96.6 with 250.
-__device__ __forceinline__ constexpr int paged_tile_cost(int MT) { return MT >= 128 ? 448 : 250; }
+// D = 256 take 470 us with 300, 451 with 448, 427 with 700, 432 with 900, 437 with 1600, cross attention at D = 64 65.6, 65.5, 64.1, 66.1 and
+// 65.8 us. Split kernel: one token of each of 64 sequences 100.2 us with 64, 96.9 with 160, 96.6 with 250.
+__device__ __forceinline__ constexpr int paged_tile_cost(int MT) { return MT >= 128 ? 700 : 250; }
 
 struct PagedSeq {
   int rows, tiles, n_all, first;   // query rows and tiles, keys, first token's row in q
