@@ -449,7 +449,9 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         wait(&sh.info_full[g % kPcInfo], g / kPcInfo);
         wait(&sh.s_full[sb], NQ == 2 ? g : g >> 1);
         tc_fence_after();
-        const float mult = qmul * f.kmul;
+        // never 0 (a row and keys of zeros or next to it): hidden scores of -inf are multiplied by it. The products
+        // that the smallest normal number stands in for leave scores below 2^-109 either way
+        const float mult = fmaxf(qmul * f.kmul, 1.17549435e-38f);
         const int kv_new = j == 0 ? f.kv : max(kv, f.kv);
         const uint32_t flags = f.flags;
         const int left = seen - (t->j0 + j) * kPcKeys;   // keys of the block that the row sees

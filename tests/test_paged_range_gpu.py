@@ -1,0 +1,85 @@
+"""The paged attention's arithmetic at the ends of its range, against the plain 64-bit implementation (paged_ref): queries
+and keys of zero, scales far apart, scores far apart, and what keys that a token does not see may leave in its output."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attention_quantized_kv_split_gb300 as qda
+from attention_quantized_kv_split_gb300 import build
+
+from paged_ref import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    qda.lib()
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    torch.cuda.synchronize()
+    qda.qdecode_attn_device_status()
+    yield
+
+
+KP, KS, KB, VP, VS, VB = range(6)
+
+
+def put(c, array, b, keys, value):
+    """Scales or biases of sequence b's keys (every head and group)."""
+    keys = torch.as_tensor(list(keys), device="cuda")
+    c.arrays[array][c.table[b, keys // c.page].long(), :, keys % c.page] = value
+
+
+def reload(c):
+    """The 64-bit keys and values anew, from what the device's arrays hold."""
+    table = c.table.cpu().numpy()
+    c.K, c.V, c.A = [], [], []
+    for b, n in enumerate(c.kv_lens):
+        out = []
+        for p, s, z in (c.arrays[:3], c.arrays[3:]):
+            pages = torch.as_tensor(table[b, : -(-n // c.page)], device="cuda").long()
+            rows = lambda a: a[pages].transpose(1, 2).flatten(0, 1)[:n].transpose(0, 1)  # noqa: E731
+            w = rows(p).cpu().numpy().view(np.uint32).astype(np.int64)
+            code = np.stack([(w >> (c.bits * j)) & (2 ** c.bits - 1) for j in range(32 // c.bits)], -1).reshape(*w.shape[:2], -1)
+            sc, bi = (np.repeat(rows(a).double().cpu().numpy(), c.GS, axis=-1) for a in (s, z))
+            out.append((code * sc + bi, sc * (2 ** c.bits - 1) / 2))
+        c.K.append(out[0][0])
+        c.V.append(out[1][0])
+        c.A.append(np.maximum(np.abs(out[1][0]), np.abs(out[1][1])))
+
+
+def steer(c, scores, b=0):
+    """Queries of ones and constant keys: key n of sequence b gets the score scores[n] in log2 units, rounded to the type."""
+    c.q.fill_(1.0)
+    c.q64[...] = 1.0
+    c.arrays[KS].zero_()
+    vals = torch.as_tensor(np.asarray(scores), dtype=torch.float64, device="cuda") * (math.log(2) / math.sqrt(c.D))
+    keys = torch.arange(len(scores), device="cuda")
+    c.arrays[KB][c.table[b, keys // c.page].long(), :, keys % c.page] = vals.to(c.q.dtype)[:, None, None]
+
+
+KINDS = [(64, 32, 8, "bf16"), (128, 64, 4, "bf16"), (128, 128, 8, "fp16"), (256, 32, 8, "bf16"), (256, 64, 4, "fp16"),
+         (512, 128, 4, "bf16")]
+FEW, MANY = [1, 3], [64, 130]   # new tokens: the split kernel's calls, the chunk kernel's
+
+
+@pytest.mark.parametrize("D,GS,bits,dtype", KINDS)
+@pytest.mark.parametrize("q_lens", [FEW, MANY])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_size,k_size", [(0.0, 0.0), (0.0, 2.0 ** -22), (2.0 ** -23, 0.0)])
+def test_queries_and_keys_of_zero(D, GS, bits, dtype, q_lens, causal, q_size, k_size):
+    # a server's warm-up: nothing but zeros (or next to it) in the queries and in the pool's keys; lengths end inside a block
+    c = Case(q_lens, [77, 300], 4, 2, D, bits, GS, dtype, 32, seed=41)
+    c.q.fill_(q_size)
+    c.q64[...] = q_size
+    for a in (KS, KB):
+        c.arrays[a].fill_(k_size)
+    reload(c)
+    c.check(c.run(causal), causal)
+    assert qda.qdecode_attn_device_status() == 0
