@@ -138,6 +138,13 @@ __device__ __forceinline__ float ps_half(const uint32_t* w, int g) {
   }
 }
 
+// Largest 16-bit pattern of a scale below 2^k (fp16's subnormal ones count in steps of 2^-24, not in exponents)
+template <bool F16>
+__device__ __forceinline__ uint32_t ps_below(int k) {
+  if constexpr (F16) return k > 15 ? 0x7BFFu : k > -15 ? ((uint32_t)(k + 15) << 10) - 1 : k > -25 ? (1u << (k + 24)) - 1 : 0u;
+  else return k > 127 ? 0x7F7Fu : ((uint32_t)(k + 127) << 7) - 1;   // k stays far above the subnormal ones
+}
+
 // NW words of codes (NW = 0: half a word) from shared memory
 template <int NW>
 __device__ __forceinline__ void ps_words(uint32_t addr, uint32_t* w) {
@@ -503,16 +510,16 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           }
           if (__any_sync(0xffffffffu, rise)) {
             // the weights' unit: the largest finite scale to [2^2, 2^3), good for scales up to 16 times that (w stays below 2^15)
-            constexpr uint32_t INF = F16 ? 0x7C00u : 0x7F80u, SHIFT = F16 ? 10 : 7;
+            constexpr uint32_t INF = F16 ? 0x7C00u : 0x7F80u;
             big = __reduce_max_sync(0xffffffffu, big < INF ? big : 0u);
             float fo = 1.f;
             if (big > most) {
-              most = min(big + (4u << SHIFT), INF - 1);
               const uint32_t w = big;
               const int e = (int)(__float_as_uint(ps_half<F16>(&w, 0)) >> 23) - 127;
-              const float ve = (float)max(-60, min(2 - e, 60));
-              fo = ps_ex2(ve - vexp);
-              vexp = ve;
+              const int ve = max(-60, min(2 - e, 60));
+              most = ps_below<F16>(7 - ve);
+              fo = ps_ex2((float)ve - vexp);
+              vexp = (float)ve;
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {

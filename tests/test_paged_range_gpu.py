@@ -83,3 +83,19 @@ def test_queries_and_keys_of_zero(D, GS, bits, dtype, q_lens, causal, q_size, k_
     reload(c)
     c.check(c.run(causal), causal)
     assert qda.qdecode_attn_device_status() == 0
+
+
+@pytest.mark.parametrize("D,GS,bits", [(64, 64, 4), (128, 64, 4), (128, 32, 8), (256, 64, 8), (512, 128, 4)])
+@pytest.mark.parametrize("small", [2.0 ** -24, 2.0 ** -22, 3 * 2.0 ** -20])
+@pytest.mark.parametrize("rise", [3.0, 5.0, 7.5])
+@pytest.mark.parametrize("q_lens", [[1], [70]])
+def test_value_scales_below_the_normal_ones(D, GS, bits, small, rise, q_lens):
+    # fp16: almost constant groups of values first, larger ones behind them with scores a few log2 units higher
+    n = 600
+    c = Case(q_lens, [n], 2, 1, D, bits, GS, "fp16", 32, seed=42)
+    put(c, VS, 0, range(n), 2.0 ** -11)
+    put(c, VS, 0, range(300), small)
+    put(c, VB, 0, range(n), 0.0)
+    steer(c, np.where(np.arange(n) < 300, 0.0, rise))
+    reload(c)
+    c.check(c.run(False), False)
