@@ -391,8 +391,12 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
         m[nt][0] = m[nt][1] = -INFINITY;
       }
 
-      uint32_t most = 0;        // 16-bit pattern of the largest value scale that the weights' unit allows
-      float vexp = 0.f;         // everything that is summed is taken times 2^vexp, an integer
+      // each row's unit: everything that is summed for it is taken times 2^vexp, an integer that follows the value scales
+      // that the row sees. most: 16-bit pattern of the largest scale that the units of this lane's rows all allow
+      float vexp[NT][2];
+      uint32_t most = 0, known = 0;   // known: bit 2 nt + j: the row has met a scale other than 0
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) vexp[nt][0] = vexp[nt][1] = 0.f;
 
       int st = 0, first = (j0 + warp) * KPS;   // the block's stage and first key
       for (int k = 0; k < mine_n; ++k) {
@@ -511,16 +515,17 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           if (__any_sync(0xffffffffu, rise)) {
             // the weights' unit: the largest finite scale to [2^2, 2^3), good for scales up to 16 times that (w stays below 2^15)
             constexpr uint32_t INF = F16 ? 0x7C00u : 0x7F80u;
-            big = __reduce_max_sync(0xffffffffu, big < INF ? big : 0u);
-            float fo = 1.f;
-            if (big > most) {
-              const uint32_t w = big;
-              const int e = (int)(__float_as_uint(ps_half<F16>(&w, 0)) >> 23) - 127;
-              const int ve = max(-60, min(2 - e, 60));
-              most = ps_below<F16>(7 - ve);
-              fo = ps_ex2((float)ve - vexp);
-              vexp = (float)ve;
+            // the largest scale of either key of this lane, anew (rare: not worth a register elsewhere)
+            uint32_t mine2[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t y = sw[x][0] & 0x7fff7fffu;
+#pragma unroll
+              for (int i = 1; i < (NG + 1) / 2; ++i) y = __vmaxu2(y, sw[x][i] & 0x7fff7fffu);
+              y = max(y & 0xffffu, y >> 16);
+              mine2[x] = y < INF ? y : 0u;
             }
+            most = INF - 1;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -530,7 +535,23 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                 const float mn = fmaxf(m[nt][j], x);
-                const float f = m[nt][j] == -INFINITY ? 0.f : ps_ex2(m[nt][j] - mn) * fo;   // no key was visible before: sums are 0
+                // the largest scale that the row sees here
+                uint32_t top = max((hidden >> (4 * nt + j)) & 1u ? 0u : mine2[0], (hidden >> (4 * nt + j + 2)) & 1u ? 0u : mine2[1]);
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                float fo = 1.f;
+                const bool none = m[nt][j] == -INFINITY;   // no key was visible before: sums are 0
+                if (top > ((known >> (2 * nt + j)) & 1u ? ps_below<F16>(7 - (int)vexp[nt][j]) : 0u)) {
+                  const uint32_t w = top;
+                  const int e = (int)(__float_as_uint(ps_half<F16>(&w, 0)) >> 23) - 127;
+                  const float ve = (float)max(-60, min(2 - e, 60));
+                  fo = ps_ex2(ve - vexp[nt][j]);
+                  vexp[nt][j] = ve;
+                  known |= 1u << (2 * nt + j);
+                }
+                if (mn != -INFINITY) most = min(most, (known >> (2 * nt + j)) & 1u ? ps_below<F16>(7 - (int)vexp[nt][j]) : 0u);
+                const float f = none ? 0.f : ps_ex2(m[nt][j] - mn) * fo;
                 m[nt][j] = mn;
                 l[nt][j] *= f;
 #pragma unroll
@@ -551,7 +572,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const float m0 = (m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - vexp, m1 = (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - vexp;
+            const float m0 = (m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - vexp[nt][0];
+            const float m1 = (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - vexp[nt][1];
             s[nt][0] = ps_ex2(s[nt][0] - m0);
             s[nt][1] = ps_ex2(s[nt][1] - m1);
             s[nt][2] = ps_ex2(s[nt][2] - m0);
@@ -649,7 +671,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           for (int sh = 4; sh <= 16; sh <<= 1) l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], sh);
           if (r8 == 0) {
             s_ml[nt][warp][0][2 * c4 + j] = m[nt][j];
-            s_ml[nt][warp][1][2 * c4 + j] = l[nt][j] * ps_ex2(-vexp);
+            s_ml[nt][warp][1][2 * c4 + j] = l[nt][j] * ps_ex2(-vexp[nt][j]);
           }
         }
         __syncthreads();   // also: every warp is through with its ring (or with the last 8 rows)
@@ -659,7 +681,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           float M = -INFINITY;
 #pragma unroll
           for (int w = 0; w < kPsWarps; ++w) M = fmaxf(M, s_ml[nt][w][0][2 * c4 + j]);
-          f[j] = m[nt][j] == -INFINITY ? 0.f : ps_ex2(m[nt][j] - M - vexp);
+          f[j] = m[nt][j] == -INFINITY ? 0.f : ps_ex2(m[nt][j] - M - vexp[nt][j]);
         }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {

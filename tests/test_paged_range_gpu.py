@@ -99,3 +99,25 @@ def test_value_scales_below_the_normal_ones(D, GS, bits, small, rise, q_lens):
     steer(c, np.where(np.arange(n) < 300, 0.0, rise))
     reload(c)
     c.check(c.run(False), False)
+
+
+@pytest.mark.parametrize("D,GS,bits,dtype", KINDS)
+@pytest.mark.parametrize("q_lens", [[2], [8], [3, 5]])
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 20, 2.0 ** 40, 2.0 ** 60])
+@pytest.mark.parametrize("what", ["v", "vb", "k"])
+def test_large_keys_that_some_tokens_do_not_see(D, GS, bits, dtype, q_lens, size, what):
+    # the last tokens' own keys or values are large (and finite): the tokens before them do not see those
+    c = Case(q_lens, [90 + 111 * b for b in range(len(q_lens))], 4, 2, D, bits, GS, dtype, 32, seed=43)
+    size = min(size, 2.0 ** 13) if dtype == "fp16" else size
+    for b, n in enumerate(c.kv_lens):
+        put(c, {"v": VS, "vb": VB, "k": KS}[what], b, [n - 1], size)
+    reload(c)
+    ref, tol = c.reference()
+    got = c.run().double().cpu().numpy()
+    # 2^13 * 255 is beyond fp16: the token that sees it may have a result that its type does not hold
+    fits = np.abs(ref) < torch.finfo(c.q.dtype).max
+    if what == "k":   # its scores may be off by the rounding of the largest
+        fits[c.start[1:] - 1] = False
+    assert (np.abs(got - ref) <= tol)[fits].all()
+    others = np.delete(np.arange(c.total), c.start[1:] - 1)
+    assert fits[others].all() and np.isfinite(got[others]).all()
