@@ -42,6 +42,11 @@ constexpr int kPcInfoWarps = 3;  // info warps, taking blocks in turn (they fill
 
 constexpr uint32_t kPcNoRow = 0xffffffffu;
 
+// Most powers of two that a query row, and a block's keys, are scaled up by. What undoes both, times the softmax scale
+// (2^-4 and above), stays a normal number: hidden scores of -inf are multiplied by it, and zeros (a row, a block) would
+// ask for any power. Values that these leave small make scores next to 0 with all that the other side may hold.
+constexpr int kPcQUp = 63, kPcKUp = 57;
+
 struct PcInfo {
   uint32_t row[8];        // pool row of each 16 keys (kPcNoRow: behind the sequence or on an absent page)
   float kmul;             // what undoes the keys' scale
@@ -357,8 +362,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         *reinterpret_cast<uint4*>(q_s + tq * 128 * D * 2 + (piece >> 3) * 16384 + row * 128 + (((piece & 7) ^ (row & 7)) << 4)) =
             make_uint4(w[0], w[1], w[2], w[3]);
       };
-      // exponent field of the power of two that brings `top` to [2^8, 2^9)
-      auto scale_of = [](float top) { return min(262 - (int)((__float_as_uint(top) >> 23) & 255u), 253); };
+      // exponent field of the power of two that brings `top` to [2^8, 2^9), as far as kPcQUp
+      auto scale_of = [](float top) { return min(262 - (int)((__float_as_uint(top) >> 23) & 255u), 127 + kPcQUp); };
       auto row_at = [&](int r) {
         const int tok = r / p.nrep;
         return reinterpret_cast<const uint4*>(p.q + (long long)(t.s.first + tok) * p.q_tstride +
@@ -449,9 +454,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         wait(&sh.info_full[g % kPcInfo], g / kPcInfo);
         wait(&sh.s_full[sb], NQ == 2 ? g : g >> 1);
         tc_fence_after();
-        // never 0 (a row and keys of zeros or next to it): hidden scores of -inf are multiplied by it. The products
-        // that the smallest normal number stands in for leave scores below 2^-109 either way
-        const float mult = fmaxf(qmul * f.kmul, 1.17549435e-38f);
+        const float mult = qmul * f.kmul;
         const int kv_new = j == 0 ? f.kv : max(kv, f.kv);
         const uint32_t flags = f.flags;
         const int left = seen - (t->j0 + j) * kPcKeys;   // keys of the block that the row sees
@@ -1026,7 +1029,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         constexpr int T = BITS == 4 ? -6 : -3;
         const uint32_t tk = __float_as_uint(fmaf(pc_half(top[0], p.f16), QMAX, pc_half(top[1], p.f16)));
         const uint32_t tv = __float_as_uint(fmaf(pc_half(top[2], p.f16), QMAX, pc_half(top[3], p.f16)));
-        const int fk = max(1, min(254 + T - (int)(tk >> 23), 253)), fv = max(1, min(254 + T - (int)(tv >> 23), 253));
+        const int fk = max(1, min(254 + T - (int)(tk >> 23), 127 + kPcKUp)), fv = max(1, min(254 + T - (int)(tv >> 23), 253));
         wait(&sh.info_empty[g % kPcInfo], g / kPcInfo + 1);
         if (lane < 8)
           f.row[lane] = pg < 0 ? kPcNoRow : (uint32_t)qda_pool_row(pg, kvh, (key0 + 16 * lane) & pmask, Hkv, p.page_shift);
