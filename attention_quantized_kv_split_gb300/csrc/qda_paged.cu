@@ -6,8 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "qda_paged.h"
-#include "qda_ptx.cuh"
+#include "qda_paged_sched.cuh"
 
 namespace qda {
 
@@ -337,6 +336,7 @@ __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_const
   __shared__ float2 s_o[WPR > 1 ? 8 : 1][D / 2];
   __shared__ float2 s_ml[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
+  if constexpr (WPR == 1) pdl_launch_dependents();   // behind the chunk kernel another kernel may follow
   pdl_wait();
   const QdaPagedSplitTile t = p.split[c];
   if (!t.go || (int)blockIdx.y * (8 / WPR) >= t.rows) return;
@@ -416,6 +416,271 @@ cudaError_t launch_merge(const QdaPagedParams& p, int rows, cudaStream_t s) {
   cfg.numAttrs = 1;
   return few ? cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 8>, p, rows)
              : cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 1>, p, rows);
+}
+
+// ----------------------------------------------------------------------------- rows beside keys that they do not see
+
+// In the chunk kernel a block of 128 keys shares one power of two, chosen from the largest of them. Its fp16 operands are
+// off by at most half a step of the subnormal numbers, 2^-19 of the largest with 4-bit codes and 2^-22 with 8-bit ones:
+// next to nothing for a row that sees the largest, but a token in the middle of a causal chunk does not see the keys
+// behind it, whatever they hold. This kernel, behind the merge of a causal call, looks for tokens whose own part of their
+// last block holds nothing within FAR of the block's largest key, or value (so that the operands' error passes 2^-13 of
+// what they see themselves), and does their rows anew in fp32: a CTA per row, a thread per key for the scores and a thread
+// per dimension for the values. On ordinary inputs it finds none: a warp per KV head and block of new tokens reads their
+// scales and biases. What it costs then: chunk over 32768 keys 858 -> 861 us, ragged chunks at D = 256 424 -> 430 us, 250
+// tokens at D = 512 99 -> 100 us (the same done by the chunk kernel's own warps costs it registers: 858 -> 915 us).
+constexpr int kFarThreads = 256, kFarWarps = kFarThreads / 32;
+
+struct FarShared {
+  int first[QDA_MAX_B + 1];     // units (KV head, block of new tokens) before each sequence
+  uint32_t found[kFarWarps][4]; // a bit per key of a warp's unit: the token there is done anew
+  float q[512], w[kFarThreads], o[kFarThreads], red[kFarWarps];
+};
+
+__device__ __forceinline__ int far_tokens(const QdaPagedParams& p, const PagedSeq& s) { return s.rows / p.nrep; }
+
+// The blocks that hold a sequence's new tokens: *first and how many.
+__device__ __forceinline__ int far_blocks(const QdaPagedParams& p, const PagedSeq& s, int* first) {
+  const int end = min(s.n_all, s.base + far_tokens(p, s));   // keys that the last token sees
+  *first = max(s.base, 0) / 128;
+  return s.rows == 0 || end <= max(s.base, 0) ? 0 : (end - 1) / 128 - *first + 1;
+}
+
+// The largest that each of four keys (or values) from pool row `row` on can be; -1 for one that is not finite.
+template <int BITS, int NG>
+__device__ __forceinline__ void far_sizes(const uint16_t* scales, const uint16_t* biases, long long row, bool f16, float (&x)[4]) {
+  constexpr float QMAX = (float)((1 << BITS) - 1);
+  uint2 s[NG], b[NG];   // four rows of NG values, all on their way before the first is looked at
+#pragma unroll
+  for (int i = 0; i < NG; ++i) {
+    s[i] = __ldg(reinterpret_cast<const uint2*>(scales + row * NG) + i);
+    b[i] = __ldg(reinterpret_cast<const uint2*>(biases + row * NG) + i);
+  }
+  const uint32_t limit = f16 ? 0x7C00u : 0x7680u;   // the chunk kernel's: fp16 infinity; 2^110 in bf16
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t ts = 0, tb = 0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const int at = k * NG + g;
+      auto half = [&](const uint2& w) { return (((at & 2) ? w.y : w.x) >> (16 * (at & 1))) & 0x7fffu; };
+      ts = max(ts, half(s[at >> 2]));
+      tb = max(tb, half(b[at >> 2]));
+    }
+    x[k] = max(ts, tb) < limit ? fmaf(half_bits_to_float_rt(ts, f16), QMAX, half_bits_to_float_rt(tb, f16)) : -1.f;
+  }
+}
+
+// A warp: which keys of block j belong to tokens whose rows are to be done anew.
+template <int BITS, int NG>
+__device__ __forceinline__ void far_find(const QdaPagedParams& p, const PagedSeq& s, int b, int kvh, int j,
+                                         uint32_t (&found)[4]) {
+  constexpr float FAR = BITS == 4 ? 64.f : 512.f;
+  const int lane = threadIdx.x & 31, pmask = (1 << p.page_shift) - 1;
+  const int end = min((j + 1) * 128, min(s.n_all, s.base + far_tokens(p, s))), key0 = j * 128 + 4 * lane;
+  const int pg = key0 < end ? __ldg(p.table + (size_t)b * p.max_pages + (key0 >> p.page_shift)) : -1;
+  const bool have = (unsigned)pg < (unsigned)p.num_pages;   // four keys from a multiple of four on lie on one page
+  const long long row = qda_pool_row(have ? pg : 0, kvh, key0 & pmask, p.Hkv, p.page_shift);
+  float k[4], v[4];   // of this lane's four keys; then of all keys up to there
+  far_sizes<BITS, NG>(p.ks, p.kb, row, p.f16, k);
+  far_sizes<BITS, NG>(p.vs, p.vb, row, p.f16, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // a key counts if both parts of it are finite: else it is zero in the operands
+    const bool counts = have && key0 + i < end && k[i] >= 0.f && v[i] >= 0.f;
+    k[i] = counts ? k[i] : 0.f;
+    v[i] = counts ? v[i] : 0.f;
+    if (i > 0) {
+      k[i] = fmaxf(k[i], k[i - 1]);
+      v[i] = fmaxf(v[i], v[i - 1]);
+    }
+  }
+  float kup = k[3], vup = v[3];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    kup = fmaxf(kup, __shfl_up_sync(0xffffffffu, kup, o));   // (lanes below o get their own)
+    vup = fmaxf(vup, __shfl_up_sync(0xffffffffu, vup, o));
+  }
+  const float kall = __shfl_sync(0xffffffffu, kup, 31), vall = __shfl_sync(0xffffffffu, vup, 31);
+  kup = __shfl_up_sync(0xffffffffu, kup, 1);
+  vup = __shfl_up_sync(0xffffffffu, vup, 1);
+  if (lane == 0) kup = vup = 0.f;
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (key0 + i >= s.base && key0 + i < end && (kall > FAR * fmaxf(k[i], kup) || vall > FAR * fmaxf(v[i], vup))) mine |= 1u << i;
+  // key 4 lane + i of the block is bit 4 lane + i of 128
+#pragma unroll
+  for (int y = 0; y < 4; ++y) found[y] = __reduce_or_sync(0xffffffffu, lane >> 3 == y ? mine << (4 * (lane & 7)) : 0u);
+}
+
+// A CTA: f(the threads' x) over all of them, for every thread.
+template <typename F>
+__device__ __forceinline__ float far_reduce(FarShared& sh, float x, F f) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, o));
+  __syncthreads();   // the last one's results are read
+  if ((threadIdx.x & 31) == 0) sh.red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = sh.red[0];
+#pragma unroll
+  for (int w = 1; w < kFarWarps; ++w) x = f(x, sh.red[w]);
+  return x;
+}
+
+// A CTA: one output row, query head h of the token in row t of q, over its keys n < seen.
+template <int BITS>
+__device__ void far_row(const QdaPagedParams& p, FarShared& sh, int b, int kvh, int t, int h, int seen) {
+  constexpr int PER = 32 / BITS;
+  constexpr uint32_t MASK = (1u << BITS) - 1;
+  const int tid = threadIdx.x, pmask = (1 << p.page_shift) - 1;
+  const uint16_t* q = p.q + (long long)t * p.q_tstride + (long long)h * p.q_hstride;
+  const int* tab = p.table + (size_t)b * p.max_pages;
+  __syncthreads();   // the last row's queries and sums are read
+  for (int d = tid; d < p.D; d += kFarThreads) sh.q[d] = half_bits_to_float_rt(q[d], p.f16);
+  // values: a thread per dimension (two at D = 512) and key in turn
+  const int part = p.D < kFarThreads ? tid / p.D : 0, parts = p.D < kFarThreads ? kFarThreads / p.D : 1, d0 = tid & (p.D - 1);
+  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
+  for (int n0 = 0; n0 < seen; n0 += kFarThreads) {
+    const int n = n0 + tid;
+    int pg = n < seen ? __ldg(tab + (n >> p.page_shift)) : -1;
+    const bool sees = (unsigned)pg < (unsigned)p.num_pages;
+    const long long row = qda_pool_row(sees ? pg : 0, kvh, n & pmask, p.Hkv, p.page_shift);
+    __syncthreads();   // queries, and the last weights are read
+    float x = -INFINITY;
+    if (sees) {
+      x = 0.f;
+      for (int g = 0; g < p.NG; ++g) {
+        const float s = half_bits_to_float_rt(__ldg(p.ks + row * p.NG + g), p.f16);
+        const float z = half_bits_to_float_rt(__ldg(p.kb + row * p.NG + g), p.f16);
+        for (int i = 0; i < p.GS / PER; ++i) {
+          const uint32_t w = __ldg(p.kp + row * p.W + g * (p.GS / PER) + i);
+#pragma unroll
+          for (int e = 0; e < PER; ++e)
+            x = fmaf(sh.q[g * p.GS + i * PER + e], fmaf(s, (float)((w >> (BITS * e)) & MASK), z), x);
+        }
+      }
+      x *= p.qscale;
+    }
+    const float mn = fmaxf(m, far_reduce(sh, x, [](float a, float c) { return fmaxf(a, c); }));
+    const float a = m == -INFINITY ? 0.f : exp2f(m - mn), w = !sees ? 0.f : exp2f(x - (mn == -INFINITY ? 0.f : mn));
+    m = mn;
+    l = l * a + w;
+    o[0] *= a;
+    o[1] *= a;
+    sh.w[tid] = w;
+    __syncthreads();
+    const int many = min(kFarThreads, seen - n0);
+    for (int i = part; i < many; i += parts) {
+      const float wi = sh.w[i];
+      if (wi == 0.f) continue;   // (no key there, or none that counts: what it holds stays out)
+      const long long r = qda_pool_row(__ldg(tab + ((n0 + i) >> p.page_shift)), kvh, (n0 + i) & pmask, p.Hkv, p.page_shift);
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int d = d0 + y * kFarThreads;
+        if (d >= p.D) break;
+        const float s = half_bits_to_float_rt(__ldg(p.vs + r * p.NG + d / p.GS), p.f16);
+        const float z = half_bits_to_float_rt(__ldg(p.vb + r * p.NG + d / p.GS), p.f16);
+        const uint32_t c = (__ldg(p.vp + r * p.W + d / PER) >> (BITS * (d % PER))) & MASK;
+        o[y] = fmaf(wi, fmaf(s, (float)c, z), o[y]);
+      }
+    }
+  }
+  l = far_reduce(sh, l, [](float x, float y) { return x + y; });
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  sh.o[tid] = o[0];
+  __syncthreads();
+  if (part == 0) {
+    for (int i = 1; i < parts; ++i) o[0] += sh.o[tid + i * p.D];
+    uint16_t* out = p.out + ((long long)t * p.H + h) * p.D;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      if (d0 + y * kFarThreads < p.D)
+        out[d0 + y * kFarThreads] = (uint16_t)(p.f16 ? to_bits16<true>(o[y] * inv) : to_bits16<false>(o[y] * inv));
+  }
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kFarThreads) qda_paged_far_kernel(const __grid_constant__ QdaPagedParams p) {
+  __shared__ FarShared sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // units before each sequence: a warp scans the batch
+  if (warp == 0) {
+    int carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      int n = 0, first;
+      if (b < p.B) n = p.Hkv * far_blocks(p, paged_seq(p, b, 128), &first);
+      int up = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += x;
+      }
+      if (b < p.B) sh.first[b] = carry + up - n;
+      carry += __shfl_sync(0xffffffffu, up, 31);
+    }
+    if (lane == 0) sh.first[p.B] = carry;
+  }
+  __syncthreads();
+  const int units = sh.first[p.B];
+  bool waited = false;
+  for (int u0 = blockIdx.x; u0 < units; u0 += gridDim.x * kFarWarps) {   // units u0, u0 + gridDim.x, ...: a warp each
+    auto unit = [&](int u, int* b, int* kvh, int* j) {
+      *b = seq_of(sh.first, p.B, u);
+      const PagedSeq s = paged_seq(p, *b, 128);
+      const int blocks = far_blocks(p, s, j), i = u - sh.first[*b];
+      *kvh = i / blocks;
+      *j += i - *kvh * blocks;
+      return s;
+    };
+    uint32_t found[4] = {0u, 0u, 0u, 0u};
+    const int mine = u0 + warp * gridDim.x;
+    if (mine < units) {
+      int b, kvh, j;
+      const PagedSeq s = unit(mine, &b, &kvh, &j);
+      switch (p.NG) {
+        case 1: far_find<BITS, 1>(p, s, b, kvh, j, found); break;
+        case 2: far_find<BITS, 2>(p, s, b, kvh, j, found); break;
+        case 4: far_find<BITS, 4>(p, s, b, kvh, j, found); break;
+        case 8: far_find<BITS, 8>(p, s, b, kvh, j, found); break;
+        default: far_find<BITS, 16>(p, s, b, kvh, j, found); break;
+      }
+    }
+    if (!__syncthreads_or(found[0] | found[1] | found[2] | found[3])) continue;
+    // rare from here on
+    if (lane == 0) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) sh.found[warp][y] = found[y];
+    }
+    __syncthreads();
+    if (!waited) pdl_wait();   // the merge has written its rows
+    waited = true;
+    for (int w = 0; w < kFarWarps && u0 + w * (int)gridDim.x < units; ++w) {
+      int b, kvh, j;
+      const PagedSeq s = unit(u0 + w * gridDim.x, &b, &kvh, &j);
+      for (int key = 0; key < 128; ++key) {
+        if (!((sh.found[w][key >> 5] >> (key & 31)) & 1u)) continue;
+        const int pos = j * 128 + key;
+        for (int r = 0; r < p.nrep; ++r) far_row<BITS>(p, sh, b, kvh, s.first + pos - s.base, kvh * p.nrep + r, pos + 1);
+      }
+    }
+    __syncthreads();
+  }
+  if (!waited) pdl_wait();   // what follows this kernel follows the merge
+}
+
+cudaError_t launch_far(const QdaPagedParams& p, int bits, int sms, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(kFarThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return bits == 4 ? cudaLaunchKernelEx(&cfg, qda_paged_far_kernel<4>, p) : cudaLaunchKernelEx(&cfg, qda_paged_far_kernel<8>, p);
 }
 
 bool good_page(int page) { return page >= QDA_PAGE_MIN && page <= QDA_PAGE_MAX && (page & (page - 1)) == 0; }
@@ -699,6 +964,7 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   cudaError_t e = plan.chunk ? chunk_run(&p, D, bits, plan.rows, false, s)
                              : split_fn(bits, p.f16 != 0)(&p, D, GS, plan.rows, nullptr, s);
   if (e == cudaSuccess) e = qda_launch_paged_merge(p, plan.rows, s);
+  if (e == cudaSuccess && plan.chunk && p.causal) e = launch_far(p, bits, sms, s);
   return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
 }
 
