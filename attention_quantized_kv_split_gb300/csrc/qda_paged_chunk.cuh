@@ -542,7 +542,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           if (rise) top = both(top, [](float x, float y) { return fmaxf(x, y); });
         }
         if (rise) rescale(top);
-        const float mm = m == -INFINITY ? 0.f : -m;
+        // weights times 2^7: up to 2^15, so that those far below the reference keep their bits longer (the sum has the same factor)
+        const float mm = m == -INFINITY ? 0.f : 7.f - m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         auto weigh = [&](const float (&x)[32], int c) {
           uint32_t w[16];

@@ -17,7 +17,7 @@
 //
 // Memory: each warp fills its own ring of shared-memory stages with 16-byte asynchronous copies (no warp waits for another), the 16-byte
 // pieces of a row XORed over the banks so that both operand reads are free of conflicts. The online softmax keeps a
-// reference per query row that moves only when a score passes it by more than 8 (log2 units): one vote per 16 keys.
+// reference per query row that moves only when a score passes it by more than 4 (log2 units): one vote per 16 keys.
 // Measured: one token of 64 sequences of 700 to 8200 keys (32 heads, 8 KV heads, D 128, 4-bit) 97 us, 3.4 TB/s of cache, half of a copy's rate: 427 instructions per
 // 16 keys keep the schedulers busy, and of the four CTAs of an SM the one launched last runs a third longer (pieces weighted against that: 96 us
 // here, but 59 instead of 54 for one long sequence; not kept). One sequence of 131072 keys (16 heads, 4 KV heads, D 256) 54 us, 3.1 TB/s; 512 keys 14.4 us, latency.
@@ -510,10 +510,11 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
                   hidden |= 1u << (4 * nt + j);
                 }
             }
-            rise = rise || fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + 8.f || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + 8.f;
+            rise = rise || fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + 4.f || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + 4.f;
           }
           if (__any_sync(0xffffffffu, rise)) {
-            // the weights' unit: the largest finite scale to [2^2, 2^3), good for scales up to 16 times that (w stays below 2^15)
+            // a row's unit: the largest finite scale that it sees to [2^8, 2^9), good for scales up to 4 times that and weights up to 2^4 (w
+            // stays below 2^15): as high as fp16 goes, so that small weights keep their bits
             constexpr uint32_t INF = F16 ? 0x7C00u : 0x7F80u;
             // the largest scale of either key of this lane, anew (rare: not worth a register elsewhere)
             uint32_t mine2[2];
@@ -542,15 +543,15 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
                 float fo = 1.f;
                 const bool none = m[nt][j] == -INFINITY;   // no key was visible before: sums are 0
-                if (top > ((known >> (2 * nt + j)) & 1u ? ps_below<F16>(7 - (int)vexp[nt][j]) : 0u)) {
+                if (top > ((known >> (2 * nt + j)) & 1u ? ps_below<F16>(11 - (int)vexp[nt][j]) : 0u)) {
                   const uint32_t w = top;
                   const int e = (int)(__float_as_uint(ps_half<F16>(&w, 0)) >> 23) - 127;
-                  const float ve = (float)max(-60, min(2 - e, 60));
+                  const float ve = (float)max(-60, min(8 - e, 60));
                   fo = ps_ex2(ve - vexp[nt][j]);
                   vexp[nt][j] = ve;
                   known |= 1u << (2 * nt + j);
                 }
-                if (mn != -INFINITY) most = min(most, (known >> (2 * nt + j)) & 1u ? ps_below<F16>(7 - (int)vexp[nt][j]) : 0u);
+                if (mn != -INFINITY) most = min(most, (known >> (2 * nt + j)) & 1u ? ps_below<F16>(11 - (int)vexp[nt][j]) : 0u);
                 const float f = none ? 0.f : ps_ex2(m[nt][j] - mn) * fo;
                 m[nt][j] = mn;
                 l[nt][j] *= f;

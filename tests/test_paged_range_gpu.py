@@ -170,3 +170,35 @@ def test_keys_that_grow_along_a_chunk(D, GS, bits, dtype, zeros):
     tame = tol < 0.2 * np.maximum(np.abs(ref).max(axis=-1, keepdims=True), 1e-3)   # scores small enough for a bound
     assert tame[: zeros + 24].all()
     assert (np.abs(got - ref) <= tol)[tame].all()
+
+
+@pytest.mark.parametrize("D,GS,bits,dtype,far", [
+    (64, 32, 8, "bf16", 22.3), (128, 64, 4, "bf16", 22.3), (128, 128, 8, "fp16", 20.3), (256, 32, 8, "bf16", 20.3),
+    (256, 64, 4, "fp16", 20.3), (512, 128, 4, "bf16", 22.3)])
+@pytest.mark.parametrize("q_lens", [FEW, MANY])
+def test_weights_far_below_the_largest(D, GS, bits, dtype, far, q_lens):
+    # a first key that draws nearly all of the attention and has a value of zeros: the result is what the others leave (some 2^-22
+    # of the weight), and it keeps its bits. Weights are taken up by 2^7 (chunks) or 2^8 and more (few tokens), so that 2^-far
+    # becomes 2^-13.3 to 2^-16.3 in fp16, off by at most 2^-25 absolute: 2^-8.7 of the weight or less, of which 7 / 15 or less
+    # reaches the result (few tokens), or 2^-9.7 (chunks). Values of one sign, so that an error that all weights share shows;
+    # the keys' few bits are exact in the operands, so scores are off by fp32's sums alone: D 2^-24 of far log2 units
+    far += 2.0 * (q_lens is FEW)
+    n = 16 if q_lens is FEW else 1500   # (a warp of the first kind has a reference of its own: all keys are one warp's)
+    c = Case(q_lens, [n, n], 4, 2, D, bits, GS, dtype, 32, seed=46)
+    c.arrays[VP].fill_(-1)   # the largest codes: as far from the middle of the range as they get
+    for b in range(2):
+        put(c, VS, b, range(n), 1.0)
+        put(c, VB, b, range(n), 0.0)
+        put(c, VS, b, [0], 0.0)
+        steer(c, np.where(np.arange(n) == 0, far, 0.0), b)
+    reload(c)
+    got = c.run().double().cpu().numpy()
+    u = torch.finfo(c.q.dtype).eps / 2
+    for b, L in enumerate(q_lens):
+        s = c.K[b][0, 0, 0] * math.sqrt(D) / math.log(2)   # the first key's score as the type holds it
+        for i in range(L):
+            seen = n - L + i + 1
+            p = 2.0 ** -s / (1 + (seen - 1) * 2.0 ** -s)
+            ref = np.repeat(p * c.V[b][:, 1:seen].sum(1), 2, axis=0)
+            err = np.abs(got[c.start[b] + i] - ref).max() / ref.max()
+            assert err <= 2 * u + 2.0 ** -11 + 2.0 ** -17 + math.expm1(D * 2.0 ** -24 * far * math.log(2))
