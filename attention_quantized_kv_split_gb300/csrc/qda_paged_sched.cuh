@@ -46,9 +46,10 @@ __device__ __forceinline__ int paged_seen(const QdaPagedParams& p, const PagedSe
   return p.causal ? max(0, min(s.n_all, s.base + r / p.nrep + 1)) : s.n_all;
 }
 
-// Length of the sequence's first i tiles (of one unit) on the line, in keys times nrep: no division.
+// Length of the sequence's first i tiles (of one unit) on the line, in keys times nrep: no division. Keys and a tile's fixed work are
+// added without a sign: lengths up to INT_MAX (which may lie) keep the line ascending.
 __device__ __forceinline__ long long paged_prefix(const QdaPagedParams& p, const PagedSeq& s, int MT, int i) {
-  const long long flat = (long long)i * ((paged_tile_cost(MT) + max(s.base, 0)) * (long long)p.nrep);
+  const long long flat = (long long)i * (((uint32_t)paged_tile_cost(MT) + (uint32_t)max(s.base, 0)) * (long long)p.nrep);
   return p.causal ? flat + (long long)MT * ((long long)i * (i + 1) / 2) : flat;
 }
 

@@ -202,3 +202,17 @@ def test_weights_far_below_the_largest(D, GS, bits, dtype, far, q_lens):
             ref = np.repeat(p * c.V[b][:, 1:seen].sum(1), 2, axis=0)
             err = np.abs(got[c.start[b] + i] - ref).max() / ref.max()
             assert err <= 2 * u + 2.0 ** -11 + 2.0 ** -17 + math.expm1(D * 2.0 ** -24 * far * math.log(2))
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2, 1], [40, 70, 9], [200, 130, 1]])
+@pytest.mark.parametrize("kv_len", [2 ** 31 - 1, 2 ** 31 - 513, 2 ** 31 - 800, 1 << 30])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_length_beyond_the_table(q_lens, kv_len, causal):
+    # a length far beyond what the sequence's row of the table reaches: its tokens see all keys that the row has pages for, and
+    # the other sequences of the batch are as they were
+    c = Case(q_lens, [250, 320, 33], 8, 2, 128, 4, 64, "bf16", 32, seed=47)
+    c.kv_len[1] = kv_len
+    got = c.run(causal).double().cpu().numpy()
+    for rows, (ref, tol) in ((slice(0, c.start[1]), c.reference(causal)), (slice(c.start[1], c.start[2]), c.reference(False)),
+                             (slice(c.start[2], c.start[3]), c.reference(causal))):
+        assert (np.abs(got - ref) <= tol)[rows].all()
