@@ -337,6 +337,14 @@ __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_const
   __shared__ float2 s_ml[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x;
   if constexpr (WPR == 1) pdl_launch_dependents();   // behind the chunk kernel another kernel may follow
+  if (blockIdx.x == 0 && blockIdx.y == 0) {          // what the call was given, looked over once
+    bool bad = threadIdx.x == 0 && (p.q_start[0] < 0 || p.q_start[p.B] > p.total_q);
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+      const int rows = p.q_start[b + 1] - max(p.q_start[b], 0), n = p.kv_len[b];
+      bad = bad || rows < 0 || (rows > 0 && (n < 0 || n > (long long)p.max_pages << p.page_shift));
+    }
+    if (bad) atomicOr(p.err, QDA_ERR_BIT_PAGED);
+  }
   pdl_wait();
   const QdaPagedSplitTile t = p.split[c];
   if (!t.go || (int)blockIdx.y * (8 / WPR) >= t.rows) return;

@@ -270,7 +270,8 @@ int qdecode_cache_append(const uint32_t* k_packed, const void* k_scales, const v
  * arrays, read by the kernels only: a step can be captured once in a CUDA graph and replayed as they change.
  * page is a power of two from 16 to 256; num_pages * page < 2^31, num_pages * page * Hkv < 2^32 - 1. What the host
  * cannot check is checked on the device: an entry of the table or of slots outside the pool is skipped and sets bit 8
- * of qdecode_attn_device_status().
+ * of qdecode_attn_device_status(). So does, in qdecode_paged_attn, a length that is negative or beyond the sequence's row
+ * of the table (of a sequence with new tokens), a falling q_start and one outside 0 .. total_q.
  */
 #define QDA_PAGE_MIN 16
 #define QDA_PAGE_MAX 256

@@ -216,3 +216,40 @@ def test_a_length_beyond_the_table(q_lens, kv_len, causal):
     for rows, (ref, tol) in ((slice(0, c.start[1]), c.reference(causal)), (slice(c.start[1], c.start[2]), c.reference(False)),
                              (slice(c.start[2], c.start[3]), c.reference(causal))):
         assert (np.abs(got - ref) <= tol)[rows].all()
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2, 1], [40, 70, 9]])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("what", ["negative", "beyond the table", "falling starts", "starts beyond q", "negative start", "idle"])
+def test_bad_lengths_show_in_the_status(q_lens, causal, what):
+    c = Case(q_lens, [250, 320, 64], 8, 2, 128, 4, 64, "bf16", 32, seed=48, extra_cols=0)
+    checked, status = [0, 1, 2], 8
+    if what == "negative":
+        c.kv_len[2], checked = -5, [0, 1]
+    elif what == "beyond the table":
+        c.kv_len[1], checked = 321, [0, 2]
+    elif what == "falling starts":
+        c.q_start[3], checked = c.start[2] - 1, [0, 1]
+    elif what == "starts beyond q":
+        c.q_start[3] += 7
+    elif what == "negative start":   # counts as 0
+        c.q_start[0] = -3
+    else:   # a sequence without new tokens: its length is not looked at
+        c.q_start[3] = c.q_start[2]
+        c.kv_len[2], checked, status = 1 << 30, [0, 1], 0
+    got = c.run(causal).double().cpu().numpy()
+    ref, tol = c.reference(causal)
+    for b in checked:
+        assert (np.abs(got - ref) <= tol)[c.start[b]: c.start[b + 1]].all()
+    if what == "negative":
+        assert not got[c.start[2]:].any()
+    assert qda.qdecode_attn_device_status() == status
+
+
+def test_good_lengths_leave_the_status_clean():
+    for kv in ([250, 320, 64], [0, 1, 500]):
+        for q_lens in ([1, 0, 3], [60, 70, 0]):
+            c = Case(q_lens, kv, 8, 2, 128, 4, 64, "bf16", 32, seed=49, extra_cols=0, pad_rows=4)
+            c.run(True)
+            c.run(False)
+            assert qda.qdecode_attn_device_status() == 0
