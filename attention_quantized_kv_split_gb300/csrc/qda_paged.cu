@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kMapThreads)
   __shared__ int s_start[QDA_MAX_B + 1], s_take[QDA_MAX_B + 1], s_old[QDA_MAX_B];
   const int tid = threadIdx.x;
   const int pmask = (1 << page_shift) - 1;
+  const unsigned top_page = 0x7fffffffu >> page_shift;   // the pool's size is not known here: no id whose slots pass 32 bits
   int o = 0, n = 0;
   bool bad = false;
   if (tid < B) {
@@ -103,9 +104,10 @@ __global__ void __launch_bounds__(kMapThreads)
       bad = true;
       continue;
     }
-    const bool have = i < n_free;
+    const int pg = i < n_free ? free_pages[i] : -1;
+    const bool have = (unsigned)pg <= top_page;
     bad = bad || !have;
-    table[(size_t)b * max_pages + col] = have ? free_pages[i] : -1;
+    table[(size_t)b * max_pages + col] = have ? pg : -1;
   }
   const int total = s_start[B];
   for (long long t = first; t < max_tokens; t += step) {
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(kMapThreads)
         if (col < old_cols) pg = table[(size_t)b * max_pages + col];
         else if (nth < n_free) pg = free_pages[nth];
       }
-      if (pg >= 0) slot = (pg << page_shift) | ((int)at & pmask);
+      if ((unsigned)pg <= top_page) slot = (pg << page_shift) | ((int)at & pmask);
       else bad = true;
     }
     slots[t] = slot;

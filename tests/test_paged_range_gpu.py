@@ -253,3 +253,24 @@ def test_good_lengths_leave_the_status_clean():
             c.run(True)
             c.run(False)
             assert qda.qdecode_attn_device_status() == 0
+
+
+@pytest.mark.parametrize("page", [16, 256])
+@pytest.mark.parametrize("where", ["free list", "table"])
+def test_map_refuses_pages_whose_slots_pass_32_bits(page, where):
+    # a broken free list or table: an id so large that id * page + row would come out as another page's slot
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    last = (2 ** 31 - 1) // page            # the largest page whose slots are int32 numbers
+    for pid, good in ((last, True), (last + 1, False), (2 * (last + 1) - 1, False), (2 ** 31 - 1, False), (-9, False)):
+        table = i32([[pid if where == "table" else -1, -1], [-1, -1]])
+        free = i32([5, 6] if where == "table" else [pid, 6])
+        old = [1, 0] if where == "table" else [0, 0]
+        new = [2, 1]
+        outs = dict(q_start=i32([0] * 3), kv_len=i32([0] * 2), slots=i32([7] * 4), positions=i32([7] * 4), used=i32([7]))
+        qda.qdecode_paged_map(i32(old), i32(new), table, free, page, **outs)
+        slots = [pid * page + old[0], pid * page + old[0] + 1] if good else [-1, -1]
+        assert outs["slots"].tolist() == slots + [(5 if where == "table" else 6) * page, -1]
+        if where == "free list":
+            assert table[0].tolist() == [pid if good else -1, -1]
+        assert outs["positions"].tolist() == [old[0], old[0] + 1, 0, -1]
+        assert qda.qdecode_attn_device_status() == (0 if good else 8)
