@@ -5,6 +5,7 @@ only marshals torch tensors (device memory and streams) into that ABI, under the
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import struct
 from typing import Optional, Sequence
@@ -33,6 +34,17 @@ def _stream(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _on(stream, device):
+    """Context in which torch allocates (and copies) on ``stream``: memory that a call on another stream than torch's
+    current one writes must come from that stream's share of torch's allocator, which may otherwise hand out a block that
+    work on the current stream still uses, or give this one away while the call is under way."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):   # a handle; 0 and 1 name the default stream
+        stream = torch.cuda.default_stream(device) if int(stream) in (0, 1) else torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 def qdecode_attn(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.Tensor, k_biases: torch.Tensor,
@@ -375,10 +387,11 @@ class QuantizedKV:
         """The cache with T new tokens per sequence (``K_new``, ``V_new`` fp32 ``[B, Hkv, T, D]``): every KV head's
         old rows, then the new rows quantized (qdecode_cache_append). Writes ``out`` (allocated when None)."""
         B, Hkv, T, D = K_new.shape
-        kn, vn = K_new.contiguous(), V_new.contiguous()
-        if out is None:
-            out = QuantizedKV.empty([n + T for n in self.N], self.Hkv, self.D, self.GS, self.bits, self.dtype,
-                                    device=K_new.device)
+        with _on(stream, K_new.device):
+            kn, vn = K_new.contiguous(), V_new.contiguous()
+            if out is None:
+                out = QuantizedKV.empty([n + T for n in self.N], self.Hkv, self.D, self.GS, self.bits, self.dtype,
+                                        device=K_new.device)
         st = lib().qdecode_cache_append(
             _ptr(self.kp), _ptr(self.ks), _ptr(self.kb), _ptr(self.vp), _ptr(self.vs), _ptr(self.vb),
             _ptr(kn), _ptr(vn), _ptr(out.kp), _ptr(out.ks), _ptr(out.kb),
@@ -398,7 +411,8 @@ def decode_attention(q: torch.Tensor, cache: QuantizedKV, out_dtype: Optional[to
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Allocating wrapper of qdecode_attn over a QuantizedKV."""
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+        with _on(stream, q.device):
+            out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
     return qdecode_attn(q, cache.kp, cache.ks, cache.kb, cache.vp, cache.vs, cache.vb, out, cache.N, cache.Hkv,
                         cache.GS, cache.bits, stream)
 
@@ -425,7 +439,8 @@ class PagedKV:
         """q_start, kv_len, slots, positions and used of a step (qdecode_paged_map; block_table is extended in place)."""
         B = block_table.shape[0]
         mk = lambda n: torch.empty(n, dtype=torch.int32, device=block_table.device)  # noqa: E731
-        t = {"q_start": mk(B + 1), "kv_len": mk(B), "slots": mk(max_tokens), "positions": mk(max_tokens), "used": mk(1)}
+        with _on(stream, block_table.device):
+            t = {"q_start": mk(B + 1), "kv_len": mk(B), "slots": mk(max_tokens), "positions": mk(max_tokens), "used": mk(1)}
         qdecode_paged_map(old_len, new_len, block_table, free_pages, self.page, **t, stream=stream)
         return t
 
@@ -435,6 +450,7 @@ class PagedKV:
     def attend(self, q, q_start, kv_len, block_table, max_q, causal=True, out=None, stream=None) -> torch.Tensor:
         """Allocating wrapper of qdecode_paged_attn (rows of q behind q_start[B] leave theirs unwritten)."""
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            with _on(stream, q.device):
+                out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         return qdecode_paged_attn(q, *self.arrays(), out, q_start, kv_len, block_table, max_q, self.GS, self.bits, causal,
                                   stream)

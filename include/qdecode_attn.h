@@ -285,9 +285,10 @@ int qdecode_cache_append(const uint32_t* k_packed, const void* k_scales, const v
  *                      free_pages[n_free], sequences in order; every other entry stays as it is
  *     used[1]          pages needed in all; above n_free, the pool is exhausted
  *     slots, positions [max_tokens]: slot and position in its sequence of every new token; -1 behind the last one
- * A token or a table entry that has no page (free list exhausted, row too short, an id that is negative or whose slots pass
- * 2^31) gets -1 and sets bit 8 of the device status; so does a negative length (taken as 0) and a step of more than max_tokens tokens. kv_len must not be old_len
- * or new_len. positions may be NULL; slots may be NULL if max_tokens is 0. Asynchronous on stream, no workspace.
+ * A token or a table entry that has no page (free list exhausted, row too short, an id that is negative or whose slots
+ * pass 2^31) gets -1 and sets bit 8 of the device status; so does a negative length (taken as 0) and a step of more than
+ * max_tokens tokens. kv_len must not be old_len or new_len. positions may be NULL; slots may be NULL if max_tokens is 0.
+ * Asynchronous on stream, no workspace.
  */
 int qdecode_paged_map(const int32_t* old_len, const int32_t* new_len, int32_t* block_table, const int32_t* free_pages,
                       int32_t* q_start, int32_t* kv_len, int32_t* slots, int32_t* positions, int32_t* used, int B,
