@@ -841,6 +841,8 @@ extern "C" int qdecode_paged_append(const void* k, const void* v, long long k_ts
   for (const void* p : ptrs)
     if (off16(p)) return QDA_ERR_ALIGN;
   if (off4(slots) || k_tstride % unit || k_hstride % unit || v_tstride % unit || v_hstride % unit) return QDA_ERR_ALIGN;
+  // rows are counted in 32 bits (strides of 0 make more of them addressable), CTAs of 256 threads in 31
+  if ((long long)T * Hkv > 0xffffff00LL || (long long)T * Hkv * (D / 8) > 0x7fffffffLL * 256) return QDA_ERR_UNSUPPORTED;
   if (T == 0) return QDA_OK;
   AppendParams p;
   std::memset(&p, 0, sizeof(p));
@@ -862,7 +864,6 @@ extern "C" int qdecode_paged_append(const void* k, const void* v, long long k_ts
   p.vb = static_cast<uint16_t*>(v_biases);
   p.k_held = static_cast<uint16_t*>(k_held);
   p.v_held = static_cast<uint16_t*>(v_held);
-  if ((long long)T * Hkv * (D / 8) > 0x7fffffffLL * 256) return QDA_ERR_UNSUPPORTED;   // more than any GPU holds
   p.rows = (uint32_t)((long long)T * Hkv);
   p.Hkv = Hkv;
   p.pool_slots = num_pages * page;

@@ -300,7 +300,8 @@ int qdecode_paged_map(const int32_t* old_len, const int32_t* new_len, int32_t* b
  * read with strides (in elements: k_tstride from token to token, k_hstride from head to head; rows themselves are
  * contiguous), so views of a fused projection need no copy. k_held, v_held (contiguous [T, Hkv, D] in the cache dtype, or
  * both NULL) receive scale * code + bias, the values that the cache holds from then on. dtype: the cache dtype in the low byte, the
- * dtype of k and v (bf16, fp16 or fp32; 0 = the cache dtype) in the next. T = 0 does nothing. Data pointers 16-byte
+ * dtype of k and v (bf16, fp16 or fp32; 0 = the cache dtype) in the next. T = 0 does nothing; T * Hkv is at most
+ * 2^32 - 256. Data pointers 16-byte
  * aligned, strides multiples of 16 bytes. Asynchronous on stream, no workspace.
  */
 int qdecode_paged_append(const void* k, const void* v, long long k_tstride, long long k_hstride, long long v_tstride,
