@@ -36,7 +36,8 @@ __device__ __forceinline__ longlong2 block_scan2(longlong2 v, longlong2* tot) {
 }
 
 // Largest b < n with first[b] <= x (first ascending, first[0] <= x).
-__device__ __forceinline__ int seq_of(const int* first, int n, int x) {
+template <typename T>
+__device__ __forceinline__ int seq_of(const T* first, int n, T x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -442,8 +443,8 @@ cudaError_t launch_merge(const QdaPagedParams& p, int rows, cudaStream_t s) {
 constexpr int kFarThreads = 256, kFarWarps = kFarThreads / 32;
 
 struct FarShared {
-  int first[QDA_MAX_B + 1];     // units (KV head, block of new tokens) before each sequence
-  uint32_t found[kFarWarps][4]; // a bit per key of a warp's unit: the token there is done anew
+  long long first[QDA_MAX_B + 1];   // units (KV head, block of new tokens) before each sequence
+  uint32_t found[kFarWarps][4];     // a bit per key of a warp's unit: the token there is done anew
   float q[512], w[kFarThreads], o[kFarThreads], red[kFarWarps];
 };
 
@@ -616,15 +617,15 @@ __global__ void __launch_bounds__(kFarThreads) qda_paged_far_kernel(const __grid
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // units before each sequence: a warp scans the batch
   if (warp == 0) {
-    int carry = 0;
+    long long carry = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
       const int b = b0 + lane;
-      int n = 0, first;
-      if (b < p.B) n = p.Hkv * far_blocks(p, paged_seq(p, b, 128), &first);
-      int up = n;
+      int first;
+      const long long n = b < p.B ? (long long)p.Hkv * far_blocks(p, paged_seq(p, b, 128), &first) : 0;
+      long long up = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, up, o);
+        const long long x = __shfl_up_sync(0xffffffffu, up, o);
         if (lane >= o) up += x;
       }
       if (b < p.B) sh.first[b] = carry + up - n;
@@ -633,19 +634,20 @@ __global__ void __launch_bounds__(kFarThreads) qda_paged_far_kernel(const __grid
     if (lane == 0) sh.first[p.B] = carry;
   }
   __syncthreads();
-  const int units = sh.first[p.B];
+  const long long units = sh.first[p.B];
   bool waited = false;
-  for (int u0 = blockIdx.x; u0 < units; u0 += gridDim.x * kFarWarps) {   // units u0, u0 + gridDim.x, ...: a warp each
-    auto unit = [&](int u, int* b, int* kvh, int* j) {
+  for (long long u0 = blockIdx.x; u0 < units; u0 += (long long)gridDim.x * kFarWarps) {   // units u0, u0 + gridDim.x, ...: a warp each
+    auto unit = [&](long long u, int* b, int* kvh, int* j) {
       *b = seq_of(sh.first, p.B, u);
       const PagedSeq s = paged_seq(p, *b, 128);
-      const int blocks = far_blocks(p, s, j), i = u - sh.first[*b];
-      *kvh = i / blocks;
-      *j += i - *kvh * blocks;
+      const int blocks = far_blocks(p, s, j);
+      const long long i = u - sh.first[*b];
+      *kvh = (int)(i / blocks);
+      *j += (int)(i - (long long)*kvh * blocks);
       return s;
     };
     uint32_t found[4] = {0u, 0u, 0u, 0u};
-    const int mine = u0 + warp * gridDim.x;
+    const long long mine = u0 + (long long)warp * gridDim.x;
     if (mine < units) {
       int b, kvh, j;
       const PagedSeq s = unit(mine, &b, &kvh, &j);
@@ -666,9 +668,9 @@ __global__ void __launch_bounds__(kFarThreads) qda_paged_far_kernel(const __grid
     __syncthreads();
     if (!waited) pdl_wait();   // the merge has written its rows
     waited = true;
-    for (int w = 0; w < kFarWarps && u0 + w * (int)gridDim.x < units; ++w) {
+    for (int w = 0; w < kFarWarps && u0 + (long long)w * gridDim.x < units; ++w) {
       int b, kvh, j;
-      const PagedSeq s = unit(u0 + w * gridDim.x, &b, &kvh, &j);
+      const PagedSeq s = unit(u0 + (long long)w * gridDim.x, &b, &kvh, &j);
       for (int key = 0; key < 128; ++key) {
         if (!((sh.found[w][key >> 5] >> (key & 31)) & 1u)) continue;
         const int pos = j * 128 + key;
