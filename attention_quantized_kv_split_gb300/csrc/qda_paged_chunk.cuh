@@ -1056,7 +1056,9 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == W_MMA) {
-    if (lane == 0) {   // no product is under way when the tensor memory goes back (after a wait that gave up some may be)
+    // no product is under way when the tensor memory goes back (after a wait that gave up some may be): a commit speaks for
+    // the products of its own thread, so it is the same elected lane's
+    if (pc_elect()) {
       volatile int none = 0;
       mma_commit(&sh.drain);
       mbar_wait_bounded(&sh.drain, 0, &none, p.err, 2u);
