@@ -212,6 +212,9 @@ int qda_cuda_fail(cudaError_t e);
 int qda_device(int* num_sms, unsigned int** err);
 int qda_workspace(size_t need, void** ws);
 
+// The chunk that qdecode_attn_debug_stall_chunk holds back (-1: none).
+int qda_stall_chunk();
+
 // slices: CTAs per (b, l, h), each combining D / slices values of the head dimension; num_sms: the device's SMs (a
 // merge of few CTAs takes 1024 threads per CTA).
 cudaError_t qda_launch_merge(const QdaParams& p, void* out, int out_dtype, bool pdl, int slices, int num_sms,

@@ -973,6 +973,9 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   p.parts = plan.parts;
   p.units = Hkv * plan.parts;
   p.min_keys = plan.min_keys;
+#ifdef QDA_BOUNDS_CHECK
+  p.stall_block = qda_stall_chunk();
+#endif
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = plan.chunk ? chunk_run(&p, D, bits, plan.rows, false, s)
                              : split_fn(bits, p.f16 != 0)(&p, D, GS, plan.rows, nullptr, s);

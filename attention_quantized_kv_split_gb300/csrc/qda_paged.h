@@ -36,6 +36,9 @@ struct QdaPagedParams {
   QdaPagedSplitTile* split;   // [ctas]
   float* part_o;              // [2 * ctas, MT, D / parts] unnormalised partial outputs of split tiles
   float2* part_ml;            // [2 * ctas, MT] (reference in log2 units, sum of weights)
+#ifdef QDA_BOUNDS_CHECK
+  int stall_block;            // testing aid: the chunk kernel's first CTA gets no pages for this block of its own (-1: for all)
+#endif
 };
 
 // Row of the pool arrays that holds row `r` of page `pg` of KV head `kvh`.

@@ -278,6 +278,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     sh.abort = 0;
     fence_barrier_init();
   }
+  // rows that a role may look up after a wait that gave up
+  for (int i = tid; i < kPcInfo * 8; i += G::WARPS * 32) sh.info[i >> 3].row[i & 7] = kPcNoRow;
   PagedLine& line = *reinterpret_cast<PagedLine*>(ring);   // before the first slot is filled
   paged_line(p, MT, line);
   const int cta = blockIdx.x;
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
   const int pmask = (1 << p.page_shift) - 1, Hkv = p.units / G::PARTS;
   // blocks, slots and tiles with blocks so far: every role counts them for itself
   uint32_t bc = 0, ic = 0, tc = 0;
-  auto wait = [&](uint64_t* bar, uint32_t phase) { mbar_wait_bounded(bar, phase & 1u, abort, p.err, 1u); };
+  auto wait = [&](uint64_t* bar, uint32_t phase) { return mbar_wait_bounded(bar, phase & 1u, abort, p.err, 1u); };
   // tile k of this CTA's piece (null behind the last); every warp hands it back with tile_done
   auto tile_at = [&](int k) -> const PcTile* {
     wait(&sh.tile_full[k % kPcTiles], k / kPcTiles);
@@ -901,7 +903,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     for (int k = 0;; ++k) {
       if (first == 0) {
         // the next tile with work for this CTA
-        wait(&sh.tile_empty[k % kPcTiles], k / kPcTiles + 1);
+        // (a role that gave up may still be at the tile before: it stays as it is, and every role ends)
+        if (!wait(&sh.tile_empty[k % kPcTiles], k / kPcTiles + 1)) break;
         PcTile& e = sh.tile[k % kPcTiles];
         int n = -1;
         while (more && n < 0) {
@@ -959,6 +962,9 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         const int key0 = (j0 + j) * kPcKeys;
         int pg = next;
         next = page_of(j + kPcInfoWarps);
+#ifdef QDA_BOUNDS_CHECK
+        if (cta == 0 && (int)g == p.stall_block) continue;   // testing aid: the waits for this block must run out
+#endif
         const bool asked = lane < 8 && key0 + 16 * lane < keys;
         const bool gone = asked && (unsigned)pg >= (unsigned)p.num_pages;
         if (gone) pg = -1;

@@ -469,6 +469,8 @@ int run_call(const void* q, const uint32_t* k_packed, const void* k_scales, cons
 
 int qda_cuda_fail(cudaError_t e) { return cuda_fail(e); }
 
+int qda_stall_chunk() { return g_stall_chunk.load(); }
+
 int qda_device(int* num_sms, unsigned int** err) {
   int dev;
   DeviceState* d = device_state(&dev);

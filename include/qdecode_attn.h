@@ -207,7 +207,8 @@ int qdecode_attn_debug_force_splits(int num_ctas);
  * Testing aid for failure detection: with chunk >= 0, the producer of the first CTA of later calls (from every
  * thread) stops before its chunk number `chunk`, so that CTA's consumers wait for data that never comes. Their
  * bounded wait gives up after its time limit (about one second), the call's output is invalid and
- * qdecode_attn_device_status() reports bit 1; the context stays usable. chunk < 0 switches it off.
+ * qdecode_attn_device_status() reports bit 1; the context stays usable. chunk < 0 switches it off. In a library built with
+ * QDA_BOUNDS_CHECK it also holds back that block of 128 keys of the first CTA in the paged calls' chunk kernel.
  */
 int qdecode_attn_debug_stall_chunk(int chunk);
 
