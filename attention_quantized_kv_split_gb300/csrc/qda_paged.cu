@@ -388,9 +388,9 @@ __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_const
     if (part != 0 || !live) return;
     for (int w = 1; w < WPR; ++w) {
       const float2 ml = s_ml[warp + w];
-      if (ml.x == -INFINITY) continue;
       const float mn = fmaxf(m, ml.x);
-      const float a = m == -INFINITY ? 0.f : exp2f(m - mn), x = exp2f(ml.x - mn);
+      // (a part without a reference is zeros, or NaN that has to stay: of a query that is not a number)
+      const float a = m == -INFINITY ? 0.f : exp2f(m - mn), x = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mn);
       m = mn;
       l = fmaf(l, a, ml.y * x);
 #pragma unroll

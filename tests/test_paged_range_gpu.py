@@ -274,3 +274,17 @@ def test_map_refuses_pages_whose_slots_pass_32_bits(page, where):
             assert table[0].tolist() == [pid if good else -1, -1]
         assert outs["positions"].tolist() == [old[0], old[0] + 1, 0, -1]
         assert qda.qdecode_attn_device_status() == (0 if good else 8)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 1], [40, 50]])
+@pytest.mark.parametrize("D", [64, 256])
+def test_a_query_that_is_not_a_number(q_lens, D):
+    # NaN in one query row: that row's output is NaN wherever the borders between the CTAs fall, and no other's
+    for kv0 in range(1000, 1360, 12):
+        c = Case(q_lens, [kv0, 700], 2, 2, D, 8, 32, "bf16", 32, seed=50)
+        q = c.q.clone()
+        q[q_lens[0], 1, 5] = float("nan")
+        got = c.run(q=q)
+        assert torch.isnan(got[q_lens[0], 1]).all(), kv0
+        got[q_lens[0], 1] = c.run()[q_lens[0], 1]
+        assert torch.isfinite(got).all()
