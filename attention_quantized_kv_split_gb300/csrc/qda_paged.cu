@@ -47,9 +47,10 @@ __device__ __forceinline__ int seq_of(const T* first, int n, T x) {
 }
 
 // Every CTA scans the B lengths for itself (at most QDA_MAX_B values, all in L2) and then writes its share of the
-// tokens' slots and of the new pages: one launch, no CTA waits for another. A token on a new page takes its page id from the free
-// list and not from the table, which another CTA may be writing. Bound by the latency of two dependent loads and the scan:
-// 2.7 us for 64 sequences' tokens, 4.2 us for 512 sequences of 1 to 129 tokens (33000 slots, pages of 16), 7.3 and 8.2 us with the host's part of a call.
+// tokens' slots and of the new pages: one launch, no CTA waits for another. A token on a new page takes its page id from
+// the free list and not from the table, which another CTA may be writing. Bound by the latency of two dependent loads and
+// the scan: 2.7 us for 64 sequences' tokens, 4.2 us for 512 sequences of 1 to 129 tokens (33000 slots, pages of 16), 7.1
+// and 8.1 us with the host's part of a call.
 __global__ void __launch_bounds__(kMapThreads)
     qda_paged_map_kernel(const int* __restrict__ old_len, const int* __restrict__ new_len, int* __restrict__ table,
                          const int* __restrict__ free_pages, int* __restrict__ q_start, int* __restrict__ kv_len,
@@ -169,12 +170,15 @@ struct AppendParams {
   unsigned int* err;
 };
 
-// A row of D values takes D / E lanes of E = 8 consecutive values (two warps at D = 512; 16 values a lane measured 5 % slower there: fewer warps
-// fit): 16 bytes or more per load and whole words of codes per lane. A group spans GS / E lanes of one warp (minimum and maximum by shuffles). The arithmetic is the quantizer's,
-// in IEEE fp32; a code is the nearest integer to a multiplication by 1 / s wherever the distance to a middle between two codes is beyond that
-// product's error, and the division only there (17722 prompt tokens 143 us with divisions, 95 without). K and V of a row go to the same lanes, both
-// loads in flight together. Bound by HBM and, with 8-bit codes, by issue: 17722 tokens of 8 heads of 256 values, bf16 -> 8-bit, 95 us (3.9 TB/s
-// read and written, floor 55); 3500 tokens of 8 heads of 512 values, fp32 -> 4-bit, 35 us (4.6 TB/s, floor 23.5); one token of 64 sequences 3.9.
+// A row of D values takes D / E lanes of E = 8 consecutive values: 16 bytes or more per load and whole words of codes per
+// lane (two warps at D = 512; 16 values a lane take 36.3 us there for the rows below, 8 take 34.9). A group spans GS / E
+// lanes of one warp (minimum and maximum by shuffles). The arithmetic is the quantizer's, in IEEE fp32; a code is the
+// nearest integer to a multiplication by 1 / s wherever the distance to a middle between two codes is beyond that product's
+// error; next to a middle the remainder decides, and only scales and biases of extreme size are divided (17722 prompt
+// tokens 143 us with a division per value, 95 so; 3500 tokens in fp32 at D = 512 34.9 either way). K and V of a row go to
+// the same lanes, both loads in flight together. Bound by issue (39 instructions per value) and then by HBM: 17722 tokens
+// of 8 heads of 256 values, bf16 -> 8-bit, 95 us (3.9 TB/s read and written, floor 55); 3500 tokens of 8 heads of 512
+// values, fp32 -> 4-bit, 35 us (4.6 TB/s, floor 23.5); one token of 64 sequences 3.9.
 template <int BITS, int E, int LANES, bool F16, int SRC>
 __global__ void __launch_bounds__(256) qda_paged_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int D = LANES * E, PER = 32 / BITS, W = D / PER, WL = E / PER;
@@ -232,11 +236,11 @@ __global__ void __launch_bounds__(256) qda_paged_append_kernel(const __grid_cons
     }
     const uint32_t sb = to_bits16<F16>(__fdiv_rn(__fsub_rn(hi, lo), QMAX)), bb = to_bits16<F16>(lo);
     const float s = half_bits_to_float<F16>(sb), b = half_bits_to_float<F16>(bb);
-    // code = clamp(rint(RN((x - b) / s))), without the division: the product with 1 / s is off by less than 2^-14 in the codes' range
-    // (q 2^-23 and the quotient's own rounding, q < 258). Adding 1.5 * 2^23 rounds to the nearest integer, ties to even, and leaves it in the
-    // low bits. A value within 2^-14 of the middle m between two codes (common: the inputs are coarse) is decided by the remainder d - m s, whose
-    // sign a fused multiply-add gives exactly: |d - m s| up to s times half a step of m means that the quotient rounds to m itself
-    // (it never lies halfway between two floats), a tie.
+    // code = clamp(rint(RN((x - b) / s))), without the division: the product with 1 / s is off by less than 2^-14 in the
+    // codes' range (q 2^-23 and the quotient's own rounding, q < 258). Adding 1.5 * 2^23 rounds to the nearest integer,
+    // ties to even, and leaves it in the low bits. A value within 2^-14 of the middle m between two codes (common: the
+    // inputs are coarse) is decided by the remainder d - m s, whose sign a fused multiply-add gives exactly: |d - m s| up to
+    // s times half a step of m means that the quotient rounds to m itself (it never lies halfway between two floats), a tie.
     constexpr float ROUND = 12582912.f, NEAR = 0.5f - 6.2e-5f;
     const bool plain = s >= 1e-30f && s <= 1e30f && fabsf(b) <= 1e30f;
     const float inv = plain ? __frcp_rn(s) : 0.f;
@@ -328,11 +332,12 @@ cudaError_t launch_append_types(const AppendParams& p, int D, bool f16, int src,
 
 // ------------------------------------------------------------------------------------------- merge of split tiles
 
-// out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M) over the CTAs c that share a tile, in CTA order. CTA (x, y) takes the tile that starts in
-// piece x and goes on behind it (most CTAs find none and end), and 8 / WPR of its rows, WPR warps to a row: each folds every WPR-th part, then
-// the warps' sums meet in shared memory. Launched with programmatic dependent launch, ahead of the end of the kernel before it.
-// Bound by latency: a record, then its parts. The kernels before it leave the records; when the merge found the shared tiles by scanning the lengths itself, it
-// took 45 us more behind 64 sequences' tokens.
+// out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M) over the CTAs c that share a tile, in CTA order. CTA (x, y) takes the
+// tile that starts in piece x and goes on behind it (most CTAs find none and end), and 8 / WPR of its rows, WPR warps to a
+// row: each folds every WPR-th part, then the warps' sums meet in shared memory. Launched with programmatic dependent
+// launch, ahead of the end of the kernel before it. Bound by latency: a record, then its parts (behind the 64 sequences'
+// tokens 6 us, behind 131072 keys 11, behind the long chunk 14). The kernels before it leave the records; when the merge
+// found the shared tiles by scanning the lengths itself, it took 45 us more behind 64 sequences' tokens.
 template <int D, int WPR>
 __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_constant__ QdaPagedParams p, int MT) {
   constexpr int E = D / 64;   // pairs of values per lane
@@ -439,7 +444,8 @@ cudaError_t launch_merge(const QdaPagedParams& p, int rows, cudaStream_t s) {
 // what they see themselves), and does their rows anew in fp32: a CTA per row, a thread per key for the scores and a thread
 // per dimension for the values. On ordinary inputs it finds none: a warp per KV head and block of new tokens reads their
 // scales and biases. What it costs then: chunk over 32768 keys 858 -> 861 us, ragged chunks at D = 256 424 -> 430 us, 250
-// tokens at D = 512 99 -> 100 us (the same done by the chunk kernel's own warps costs it registers: 858 -> 915 us).
+// tokens at D = 512 99 -> 100 us (the same done by the chunk kernel's own warps costs it registers: 858 -> 915 us). Rows
+// that are done anew take some 100 us and more each at 32768 keys.
 constexpr int kFarThreads = 256, kFarWarps = kFarThreads / 32;
 
 struct FarShared {
@@ -459,7 +465,8 @@ __device__ __forceinline__ int far_blocks(const QdaPagedParams& p, const PagedSe
 
 // The largest that each of four keys (or values) from pool row `row` on can be; -1 for one that is not finite.
 template <int BITS, int NG>
-__device__ __forceinline__ void far_sizes(const uint16_t* scales, const uint16_t* biases, long long row, bool f16, float (&x)[4]) {
+__device__ __forceinline__ void far_sizes(const uint16_t* scales, const uint16_t* biases, long long row, bool f16,
+                                          float (&x)[4]) {
   constexpr float QMAX = (float)((1 << BITS) - 1);
   uint2 s[NG], b[NG];   // four rows of NG values, all on their way before the first is looked at
 #pragma unroll
@@ -519,7 +526,8 @@ __device__ __forceinline__ void far_find(const QdaPagedParams& p, const PagedSeq
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (key0 + i >= s.base && key0 + i < end && (kall > FAR * fmaxf(k[i], kup) || vall > FAR * fmaxf(v[i], vup))) mine |= 1u << i;
+    if (key0 + i >= s.base && key0 + i < end && (kall > FAR * fmaxf(k[i], kup) || vall > FAR * fmaxf(v[i], vup)))
+      mine |= 1u << i;
   // key 4 lane + i of the block is bit 4 lane + i of 128
 #pragma unroll
   for (int y = 0; y < 4; ++y) found[y] = __reduce_or_sync(0xffffffffu, lane >> 3 == y ? mine << (4 * (lane & 7)) : 0u);
@@ -636,7 +644,8 @@ __global__ void __launch_bounds__(kFarThreads) qda_paged_far_kernel(const __grid
   __syncthreads();
   const long long units = sh.first[p.B];
   bool waited = false;
-  for (long long u0 = blockIdx.x; u0 < units; u0 += (long long)gridDim.x * kFarWarps) {   // units u0, u0 + gridDim.x, ...: a warp each
+  // units u0, u0 + gridDim.x, ...: a warp each
+  for (long long u0 = blockIdx.x; u0 < units; u0 += (long long)gridDim.x * kFarWarps) {
     auto unit = [&](long long u, int* b, int* kvh, int* j) {
       *b = seq_of(sh.first, p.B, u);
       const PagedSeq s = paged_seq(p, *b, 128);
@@ -692,7 +701,8 @@ cudaError_t launch_far(const QdaPagedParams& p, int bits, int sms, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return bits == 4 ? cudaLaunchKernelEx(&cfg, qda_paged_far_kernel<4>, p) : cudaLaunchKernelEx(&cfg, qda_paged_far_kernel<8>, p);
+  return bits == 4 ? cudaLaunchKernelEx(&cfg, qda_paged_far_kernel<4>, p)
+                   : cudaLaunchKernelEx(&cfg, qda_paged_far_kernel<8>, p);
 }
 
 bool good_page(int page) { return page >= QDA_PAGE_MIN && page <= QDA_PAGE_MAX && (page & (page - 1)) == 0; }
@@ -732,10 +742,13 @@ SplitFn split_fn(int bits, bool f16) {
                    : (f16 ? qda_paged_split_b8_f1 : qda_paged_split_b8_f0);
 }
 
-// Rows (new tokens times query heads of a KV head) up to which the split kernel takes a call. Its time grows with every 16 rows (8 at
-// D = 512), the chunk kernel's stays the same up to 128. Split against chunk kernel, 8 KV heads and about 90000 keys in all: D 64, 8-bit, 32 rows
-// 84 / 85 us (64 rows 100 / 97), D 128, 4-bit, 16 rows 65 / 99, 32 rows 107 / 100 (one sequence alone 82 / 86), D 256, 4-bit, 16 rows
-// 98 / 130 (32 rows of 4 sequences' tokens 91 / 67), D 512, 4-bit, 16 rows 240 / 339, 32 rows 455 / 338 (of one short sequence 80 / 95).
+// Rows (new tokens times query heads of a KV head) up to which the split kernel takes a call. Its time grows with every 16
+// rows (8 at D = 512), the chunk kernel's stays the same up to 128. Split against chunk kernel, 8 KV heads and about 90000
+// keys in all: D 64, 8-bit, 32 rows 84 / 85 us (64 rows 100 / 97), D 128, 4-bit, 16 rows 65 / 99, 32 rows 107 / 100 (one
+// sequence alone 82 / 86), D 256, 4-bit, 16 rows 98 / 130 (32 rows of 4 sequences' tokens 91 / 67), D 512, 4-bit, 16 rows
+// 240 / 339, 32 rows 455 / 338 (of one short sequence 80 / 95). The rule knows neither lengths nor batch, which the device
+// alone has, and takes one kernel for the whole call: 63 single tokens (98 us by themselves) and a chunk of 512 over 8000
+// keys (93 us) take 375 us in one call with max_q = 512, where every token walks its keys as a tile of 256 rows.
 constexpr long long split_rows(int D) { return D == 512 ? 24 : D == 256 ? 16 : 32; }
 
 cudaError_t chunk_run(const QdaPagedParams* p, int D, int bits, int rows, bool prepare, cudaStream_t s) {

@@ -5,8 +5,8 @@
 
 #define QDA_ERR_BIT_PAGED 8u   // device status: a page, slot or length outside its pool or table
 
-// What a CTA of the attention kernels leaves for the merge: the tile that starts in its piece of the work and goes on behind it, and which of its
-// two slots (a tile that started before its piece, and one that starts in it) hold a part.
+// What a CTA of the attention kernels leaves for the merge: the tile that starts in its piece of the work and goes on
+// behind it, and which of its two slots (a tile that started before its piece, and one that starts in it) hold a part.
 struct QdaPagedSplitTile {
   int go, last;                     // there is such a tile; the last CTA that shares it
   int row0, rows, token0, unit;     // its query rows, the sequence's first token, the unit

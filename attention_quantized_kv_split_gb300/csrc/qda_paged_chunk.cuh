@@ -1,29 +1,41 @@
-// Paged attention for many query rows per KV head (sm_103a): chunks of prompts, cross attention. Bound by the tensor cores.
+// Paged attention for many query rows per KV head (sm_103a): chunks of prompts, cross attention.
 //
-// One CTA per SM takes a tile of 128 query rows of a KV head, or two of them side by side (D <= 128), and walks the tile's keys in blocks
-// of 128: S = Q K^T and O += P V on tcgen05 (fp16 operands, fp32 sums in tensor memory), an online softmax in between. Rows are (token, query head)
-// pairs, so all query heads of a KV head share a block's keys and values, which are turned from codes into operands once per block:
-//   dequantising warps   codes -> fp16 tiles in shared memory (a ring of slots of 128 keys x 128 dimensions), the next slots' codes in flight in registers;
-//   softmax warps        eight: one thread per query row with two tiles, two threads (half of the keys, half of the values) with one. They read S
-//                        from tensor memory and write P (fp16) over it;
-//   MMA warp             one thread issues every product. With two tiles the products of one run while the softmax of the other does;
-//                        with one tile S has two buffers and the next block's scores run during this block's softmax. Two threads per row took
-//                        ragged chunks at D = 256 from 487 to 453 us (the lone softmax warp of a scheduler waited for itself);
+// One CTA per SM takes a tile of 128 query rows of a KV head, or two of them side by side (D <= 128), and walks the tile's
+// keys in blocks of 128: S = Q K^T and O += P V on tcgen05 (fp16 operands, fp32 sums in tensor memory), an online softmax in
+// between. Rows are (token, query head) pairs, so all query heads of a KV head share a block's keys and values, which are
+// turned from codes into operands once per block:
+//   dequantising warps   codes -> fp16 tiles in shared memory (a ring of slots of 128 keys x 128 dimensions), the next
+//                        slot's codes in flight in registers;
+//   softmax warps        eight: one thread per query row with two tiles, two threads (half of the keys, half of the values)
+//                        with one. They read S from tensor memory and write P (fp16) over it;
+//   MMA warp             one thread issues every product. With two tiles the products of one run while the softmax of the
+//                        other does; with one tile S has two buffers and the next block's scores run during this block's
+//                        softmax. Two threads per row took ragged chunks at D = 256 from 487 to 453 us (the lone softmax
+//                        warp of a scheduler waited for itself);
 //   info warps           blocks ahead: a block's pages, and how large its keys and values can be.
-// Every link is an mbarrier; every wait is bounded and sets the device error word.
+// Every link is an mbarrier; every wait is bounded and sets the device error word, and after one that gave up every role
+// ends without an access that the call's arrays do not hold.
 //
-// Measured: 2048 tokens over 32768 keys (32 heads, 8 KV heads, D 128, 4-bit) 863 us, 1.24 PFLOP/s, 65 % of a large bf16 product's rate: the softmax of
-// 256 rows and the dequantising share the issue slots. Ragged chunks at D 256, 8-bit, 427 us (0.57 PFLOP/s): one tile per CTA, so a block is dequantised
-// for 128 rows only. Cross attention at D 64 64 us, 250 tokens over 4097 keys at D 512 99 us: start, first blocks and merge.
+// Measured: 2048 tokens over 32768 keys (32 heads, 8 KV heads, D 128, 4-bit) 873 us, 1.23 PFLOP/s, 64 % of a large bf16
+// product's rate. The tensor pipe and the issue slots are each busy half of the time there (52 and 54 %) and the warps wait
+// for loads most (long_scoreboard 4.3 per issue): for scores from tensor memory and for codes, one item ahead. Ragged chunks
+// at D 256, 8-bit, 431 us (0.56 PFLOP/s, tensor pipe 27 %, the same wait 5.6): one tile per CTA, so a block is dequantised for
+// 128 rows only, and the cache is read from DRAM four times over. Cross attention at D 64 65 us (12 %, 6.9), 250 tokens over
+// 4097 keys at D 512 100 us (21 %, 5.9).
 //
-// Operands are fp16 for both input types (11 significant bits; for bf16 caches the operands then add almost nothing to the one
-// rounding of the result, where bf16 operands would double it), and ranges are taken care of by powers of two: a query row is scaled so that its largest value
-// lies in [2^8, 2^9), a block's keys and values so that none passes 2^-4 (2^-1 for 8-bit codes), from the block's scales and biases. The scale of the keys is undone with
-// the softmax scale; that of the values only ever grows in a tile's walk and O is rescaled when it does. Small scale leaves no rounding behind: the
-// codes enter the multiply-add as fp16 subnormals c 2^-24 (the code's bits as they are, one AND for two of them), so that one fused multiply-add with s 2^24 makes
-// two operand values. The unpacked order of the dimensions is kept: q is stored in the same order and O read back in it.
-// Hidden keys: beyond a row's sight -inf; behind the sequence, on an absent page, or not finite they are zero in the operands, so they reach nothing
-// else, and a row that sees a key that is not finite becomes NaN.
+// Operands are fp16 for both input types (11 significant bits; for bf16 caches the operands then add almost nothing to the
+// one rounding of the result, where bf16 operands would double it), and ranges are taken care of by powers of two: a query
+// row is scaled so that its largest value lies in [2^8, 2^9), a block's keys and values so that the largest that its scales
+// and biases allow, scale * (2^bits - 1) + |bias|, lies in [2^-6, 2^-5) (4-bit codes) or [2^-3, 2^-2) (8-bit). Values down
+// to 2^-8 (2^-11) of that keep their 11 bits, smaller ones lose a bit with every factor of two. The scale of the keys is
+// undone with the softmax scale; that of the values only ever grows in a tile's walk and O is rescaled when it does. A small
+// scale leaves no rounding behind: the codes enter the multiply-add as fp16 subnormals c 2^-24 (the code's bits as they are,
+// one AND for two of them), so that one fused multiply-add with s 2^24 makes two operand values. The unpacked order of the
+// dimensions is kept: q is stored in the same order and O read back in it.
+// Hidden keys: beyond a row's sight -inf; behind the sequence, on an absent page, or not finite they are zero in the
+// operands, so they reach nothing else, and a row that sees a key that is not finite becomes NaN. A finite key does choose
+// the block's power of two for rows that do not see it: where that would cost them bits, the far kernel (qda_paged.cu) does
+// those rows anew.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -84,7 +96,7 @@ struct PcGeom {
 
 // A tile of this CTA's piece, and its part of the tile's key blocks.
 struct PcTile {
-  int n, j0;              // blocks j0 .. j0 + n - 1 (n = 0: a tile without keys, whose rows are zeros; -1: behind the last tile)
+  int n, j0;              // blocks j0 .. j0 + n - 1 (n = 0: a tile without keys, whose rows are zeros; -1: no more tiles)
   int keys;               // keys that the tile walks
   int whole, mine;        // all of the tile's blocks; the tile starts in this CTA's piece
   int row0, kvh, part, b;
@@ -119,15 +131,15 @@ __device__ __forceinline__ float pc_ex2(float x) {
   return y;
 }
 
-// Shared-memory descriptor of a 128-byte swizzled operand (rows of 128 bytes, 8-row groups 1024 bytes apart); lbo: bytes between 64-element blocks of
-// an operand whose rows run along K (values), unused for one whose rows hold K (keys, queries).
+// Shared-memory descriptor of a 128-byte swizzled operand (rows of 128 bytes, 8-row groups 1024 bytes apart); lbo: bytes
+// between 64-element blocks of an operand whose rows run along K (values), unused for one whose rows hold K (keys, queries).
 __device__ __forceinline__ uint64_t pc_desc(uint32_t saddr, uint32_t lbo) {
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024u >> 4) << 32) |
          (1ull << 46) | (2ull << 61);
 }
 
-// One lane of the warp, the same one every time. The products below are issued by that lane while the whole warp walks through the code: addresses and
-// descriptors then stay in uniform registers, where the instruction wants them.
+// One lane of the warp, the same one every time. The products below are issued by that lane while the whole warp walks
+// through the code: addresses and descriptors then stay in uniform registers, where the instruction wants them.
 __device__ __forceinline__ uint32_t pc_elect() {
   uint32_t e;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
@@ -142,7 +154,8 @@ __device__ __forceinline__ void pc_mma_ss(uint32_t one, uint32_t d_tmem, uint64_
       : "memory");
 }
 // D (tensor memory) (+)= A (tensor memory) * B (shared memory)
-__device__ __forceinline__ void pc_mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void pc_mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                          uint32_t acc) {
   asm volatile(
       "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
@@ -338,10 +351,11 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
       pair_sync();
       return half == 0 ? sh.row[rt] : x;
     };
-    // The warp's query rows into shared memory, in the codes' unpacked order, each row scaled by a power of two; returns what undoes this thread's
-    // row's scale, times the softmax scale. With one tile a row is read by lanes side by side; with two tiles (D <= 128) a thread reads its own
-    // row, which is slower by itself, but the other form costs the softmax loop registers there (ragged chunks at D = 256: 575 against 622 us for
-    // the first form; chunk over 32768 keys at D = 128: 869 us with the second, 887 with the first).
+    // The warp's query rows into shared memory, in the codes' unpacked order, each row scaled by a power of two; returns what
+    // undoes this thread's row's scale, times the softmax scale. With one tile a row is read by lanes side by side; with two
+    // tiles (D <= 128) a thread reads its own row, which is slower by itself, but the other form costs the softmax loop
+    // registers there (ragged chunks at D = 256: 575 against 622 us for the first form; chunk over 32768 keys at D = 128: 869
+    // us with the second, 887 with the first).
     auto load_q = [&](const PcTile& t) {
       float mul = 0.f;
       // 8 values: their largest magnitude; and with `up` 16 bytes of operand
@@ -496,9 +510,9 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           }
           kv = kv_new;
         };
-        // Two tiles: the row's 128 scores do not fit the registers next to everything else: the second half is read for its maximum, the
-        // first is read and kept, and the second read again as the first's registers come free. Weights lie over the
-        // first half's scores.
+        // Two tiles: the row's 128 scores do not fit the registers next to everything else: the second half is read for its
+        // maximum, the first is read and kept, and the second read again as the first's registers come free. Weights lie
+        // over the first half's scores.
         float u[2][32];
         auto get = [&](float (&x)[32], int c) { pc_ld32(s_t + 64 * half + 32 * c, x); };
         auto hide = [&](float (&x)[32], int c) {
@@ -535,7 +549,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         if (j == 0) kv = kv_new;
         bool rise = __any_sync(0xffffffffu, top > m + 8.f || kv_new != kv);
         if constexpr (NQ == 1) {
-          // does the other half of any row rise? Behind this both halves hold their scores in registers and weights may lie over them
+          // does the other half of any row rise? Behind this both halves hold their scores in registers and weights may lie
+          // over them
           tc_fence_before();
           if (lane == 0) sh.rise[g & 1][warp] = rise;
           pair_sync();
@@ -544,7 +559,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
           if (rise) top = both(top, [](float x, float y) { return fmaxf(x, y); });
         }
         if (rise) rescale(top);
-        // weights times 2^7: up to 2^15, so that those far below the reference keep their bits longer (the sum has the same factor)
+        // weights times 2^7: up to 2^15, so that those far below the reference keep their bits longer, 11 of them down to
+        // 2^-21 (the sum has the same factor)
         const float mm = m == -INFINITY ? 0.f : 7.f - m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         auto weigh = [&](const float (&x)[32], int c) {
@@ -835,7 +851,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         auto pv = [&](int sl, uint32_t it, uint32_t pt, uint32_t d, bool acc) {
           const uint64_t b = pc_desc(ring_a + (it % SLOTS) * G::SLOT, 16384);
 #pragma unroll
-          for (int x = 0; x < kPcKeys / 16; ++x) pc_mma_ts(one, d + sl * SD, pt + 8 * x, b + x * (2048 >> 4), ID_PV, acc || x > 0);
+          for (int x = 0; x < kPcKeys / 16; ++x)
+            pc_mma_ts(one, d + sl * SD, pt + 8 * x, b + x * (2048 >> 4), ID_PV, acc || x > 0);
         };
         wait(&sh.q_full, tc);
         tc_fence_after();
@@ -983,8 +1000,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
               const long long row = qda_pool_row(pv, kvh, (key0 + 16 * g16) & pmask, Hkv, p.page_shift);
               const int piece = v - g16 * 2 * p.NG;
               const long long at = row * p.NG / 8 + piece;
-              const uint4 a[4] = {__ldg(reinterpret_cast<const uint4*>(p.ks) + at), __ldg(reinterpret_cast<const uint4*>(p.kb) + at),
-                                  __ldg(reinterpret_cast<const uint4*>(p.vs) + at), __ldg(reinterpret_cast<const uint4*>(p.vb) + at)};
+              auto piece_of = [&](const uint16_t* array) { return __ldg(reinterpret_cast<const uint4*>(array) + at); };
+              const uint4 a[4] = {piece_of(p.ks), piece_of(p.kb), piece_of(p.vs), piece_of(p.vb)};
               each(a, 16 * g16, piece);
             }
           }

@@ -1,13 +1,13 @@
 // How a paged attention call is shared among its CTAs (sm_103a), from lengths that only the device knows.
 //
 // The rows of a sequence under one KV head, r = i * nrep + j for new token i and the head's query head j, are cut into
-// tiles of MT rows; a tile walks the keys that its last row sees. All (sequence, unit, tile) triples in that order (a unit is a KV head, or
-// for a kernel that cannot hold a head's values at once, a KV head and a part of its values)
-// form one line, each with a length in keys: exact for cross attention, linear in the tile's index for causal attention (plus a constant for a
-// tile's fixed work). CTA c takes the c-th of `ctas` equal pieces of the line, so ragged lengths, chunks and single
-// tokens are balanced alike, whatever they are. A piece border inside a tile falls on the border of a key block in proportion; the tile's partial
-// results are merged in CTA order, so results do not depend on timing. Every CTA (and the merge) finds its piece by itself: a scan
-// over the B lengths, then closed forms.
+// tiles of MT rows; a tile walks the keys that its last row sees. All (sequence, unit, tile) triples in that order (a unit
+// is a KV head, or for a kernel that cannot hold a head's values at once, a KV head and a part of its values) form one
+// line, each with a length in keys: exact for cross attention, linear in the tile's index for causal attention (plus a
+// constant for a tile's fixed work). CTA c takes the c-th of `ctas` equal pieces of the line, so ragged lengths, chunks and
+// single tokens are balanced alike, whatever they are. A piece border inside a tile falls on the border of a key block in
+// proportion; the tile's partial results are merged in CTA order, so results do not depend on timing. Every CTA finds its
+// piece by itself: a scan over the B lengths, then closed forms.
 #pragma once
 
 #include "qda_paged.h"
@@ -15,9 +15,13 @@
 
 namespace qda {
 
-// A tile's fixed work (its query rows, its results), in keys. Chunk kernel (tiles of 128 rows or more): ragged chunks of 1 to 1023 tokens at
-// D = 256 take 470 us with 300, 451 with 448, 427 with 700, 432 with 900, 437 with 1600, cross attention at D = 64 65.6, 65.5, 64.1, 66.1 and
-// 65.8 us. Split kernel: one token of each of 64 sequences 100.2 us with 64, 96.9 with 160, 96.6 with 250.
+// A tile's fixed work (its query rows, its results), in keys. Chunk kernel (tiles of 128 rows or more): ragged chunks of 1
+// to 1023 tokens at D = 256 take 470 us with 300, 451 with 448, 427 with 700, 432 with 900, 437 with 1600, cross attention
+// at D = 64 65.6, 65.5, 64.1, 66.1 and 65.8 us: anything from 700 to 1200 will do. Split kernel: one token of each of 64
+// sequences 100.2 us with 64, 96.9 with 160, 96.6 with 250; one sequence of 131072 keys 58 us with 240 or 256 and 54 with
+// 250, which is that length's luck and no reason: the cost is spread over a tile's blocks, so a border just behind a
+// tile's start hands one or two blocks to a CTA that pays the whole cost for them, and at that length no border falls so
+// (now 55.7 us there, and at 21 lengths from there to 133000 a median of 59.9, 61.5 at most).
 __device__ __forceinline__ constexpr int paged_tile_cost(int MT) { return MT >= 128 ? 700 : 250; }
 
 struct PagedSeq {
@@ -33,7 +37,8 @@ __device__ __forceinline__ PagedSeq paged_seq(const QdaPagedParams& p, int start
   s.first = q0;
   s.rows = (q1 - q0) * p.nrep;
   s.tiles = (s.rows + MT - 1) / MT;
-  s.n_all = (int)min(min((long long)n, (long long)p.max_pages << p.page_shift), 0x7ffffe00LL);   // sums with a block's keys stay in range
+  // (sums with a block's keys stay in range)
+  s.n_all = (int)min(min((long long)n, (long long)p.max_pages << p.page_shift), 0x7ffffe00LL);
   s.base = p.causal ? n - (q1 - q0) : s.n_all;
   return s;
 }
@@ -46,8 +51,8 @@ __device__ __forceinline__ int paged_seen(const QdaPagedParams& p, const PagedSe
   return p.causal ? max(0, min(s.n_all, s.base + r / p.nrep + 1)) : s.n_all;
 }
 
-// Length of the sequence's first i tiles (of one unit) on the line, in keys times nrep: no division. Keys and a tile's fixed work are
-// added without a sign: lengths up to INT_MAX (which may lie) keep the line ascending.
+// Length of the sequence's first i tiles (of one unit) on the line, in keys times nrep: no division. Keys and a tile's
+// fixed work are added without a sign: lengths up to INT_MAX (which may lie) keep the line ascending.
 __device__ __forceinline__ long long paged_prefix(const QdaPagedParams& p, const PagedSeq& s, int MT, int i) {
   const long long flat = (long long)i * (((uint32_t)paged_tile_cost(MT) + (uint32_t)max(s.base, 0)) * (long long)p.nrep);
   return p.causal ? flat + (long long)MT * ((long long)i * (i + 1) / 2) : flat;
@@ -179,8 +184,8 @@ __device__ __forceinline__ int paged_block_at(const PagedTile& t, int nblk, long
   return (int)paged_div((unsigned long long)(x - t.lo) * nblk, t.hi - t.lo);   // below 2^31 * 2^6 * 2^27
 }
 
-// Behind CTA k's part [j0, j1) of tile t (one thread): what the merge has to know of the tile, if it starts in piece k and goes on behind it, and
-// which of the CTA's two slots it has filled.
+// Behind CTA k's part [j0, j1) of tile t (one thread): what the merge has to know of the tile, if it starts in piece k and
+// goes on behind it, and which of the CTA's two slots it has filled.
 __device__ __forceinline__ void paged_record(const QdaPagedParams& p, const PagedPieces& c, const PagedTile& t, int MT,
                                              int nblk, int j0, int j1, int k) {
   QdaPagedSplitTile& r = p.split[k];

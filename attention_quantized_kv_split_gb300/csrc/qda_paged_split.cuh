@@ -1,28 +1,34 @@
 // Paged attention for few query rows per KV head (sm_103a): single tokens, a few tokens per sequence, and every shape the
 // chunk kernel does not take. Bound by HBM (the cache is read once per tile of 8 or 16 rows) and next to it by issue slots.
 //
-// Matrix instructions work on the codes themselves. A warp takes 16 keys at a time; the codes, straight from shared memory, become the 16-bit
-// A operand of m16n8k16 products with fp32 sums (a few query rows are far too thin for the 128-row tiles of tcgen05, and its operands would have to be written back
-// to shared or tensor memory first; here they never leave the registers):
-//   scores   rows = keys, k = head dimension, columns = query rows. A code's bits as they are, masked out of the packed word, are the fp16
-//            subnormal c 2^-24 (16 c 2^-24 where a nibble is left unshifted, with q / 16 on the other side): one AND makes two
-//            operand values, exact. q goes in as fp16 after an exact scaling of each row by a power of two (bf16 has fewer significant
-//            bits and a wider range). Per group, s_g sum(c q) + b_g sum(q) is formed in fp32: the scores are right to fp32.
+// Matrix instructions work on the codes themselves. A warp takes 16 keys at a time; the codes, straight from shared memory,
+// become the 16-bit A operand of m16n8k16 products with fp32 sums (a few query rows are far too thin for the 128-row tiles
+// of tcgen05, and its operands would have to be written back to shared or tensor memory first; here they never leave the
+// registers):
+//   scores   rows = keys, k = head dimension, columns = query rows. A code's bits as they are, masked out of the packed
+//            word, are the fp16 subnormal c 2^-24 (16 c 2^-24 where a nibble is left unshifted, with q / 16 on the other
+//            side): one AND makes two operand values, exact. q goes in as fp16 after an exact scaling of each row by a
+//            power of two (bf16 has fewer significant bits and a wider range). Per group, s_g sum(c q) + b_g sum(q) is
+//            formed in fp32: the scores are right to fp32.
 //   values   rows = head dimension, k = keys, columns = query rows: the weight w = p s_g of each group is the B operand,
-//            rounded to fp16 (11 significant bits: next to nothing beside a bf16 result, as much as the one rounding of an fp16 one); all sums
-//            are taken in a unit 2^-vexp that follows the largest scale met and keeps w in range. To centre the codes on the middle of their range (so that the rounding of w meets
-//            values no larger than half a group's range), sum(w) of a group comes from one more product with A = the middle, or with
-//            many groups the middle is taken off the codes; the rest, sum(p (b_g + mid s_g)), stays in fp32.
+//            rounded to fp16 (11 significant bits: next to nothing beside a bf16 result, as much as the one rounding of an
+//            fp16 one; w 2^-22 of the largest and less lose a bit with every factor of two); all sums of a query row are
+//            taken in a unit 2^-vexp that follows the largest scale of the keys that the row sees and keeps w in range. To
+//            centre the codes on the middle of their range (so that the rounding of w meets values no larger than half a
+//            group's range), sum(w) of a group comes from one more product with A = the middle, or with many groups the
+//            middle is taken off the codes; the rest, sum(p (b_g + mid s_g)), stays in fp32.
 // Keys and query rows change places between the two products: one movmatrix per 8 x 8 weights.
 //
-// Memory: each warp fills its own ring of shared-memory stages with 16-byte asynchronous copies (no warp waits for another), the 16-byte
-// pieces of a row XORed over the banks so that both operand reads are free of conflicts. The online softmax keeps a
-// reference per query row that moves only when a score passes it by more than 4 (log2 units): one vote per 16 keys.
-// Measured: one token of 64 sequences of 700 to 8200 keys (32 heads, 8 KV heads, D 128, 4-bit) 97 us, 3.4 TB/s of cache, half of a copy's rate: 427 instructions per
-// 16 keys keep the schedulers busy, and of the four CTAs of an SM the one launched last runs a third longer (pieces weighted against that: 96 us
-// here, but 59 instead of 54 for one long sequence; not kept). One sequence of 131072 keys (16 heads, 4 KV heads, D 256) 54 us, 3.1 TB/s; 512 keys 14.4 us, latency.
-// Hidden keys (behind the sequence, in a token's future, on a page outside the pool) get the weight 0 by selection, so that what
-// their rows hold, NaN included, reaches nothing.
+// Memory: each warp fills its own ring of shared-memory stages with 16-byte asynchronous copies (no warp waits for
+// another), the 16-byte pieces of a row XORed over the banks so that both operand reads are free of conflicts. The online
+// softmax keeps a reference per query row that moves only when a score passes it by more than 4 (log2 units): one vote per
+// 16 keys. Measured: one token of 64 sequences of 700 to 8200 keys (32 heads, 8 KV heads, D 128, 4-bit) 97 us, 3.4 TB/s of
+// cache, half of a copy's rate: some 430 instructions per 16 keys keep the schedulers busy, and of the four CTAs of an SM
+// the one launched last runs a third longer (pieces weighted against that: 96 us here, but 59 instead of 54 for one long
+// sequence; not kept). One sequence of 131072 keys (16 heads, 4 KV heads, D 256) 55 us, 3.0 TB/s (lengths near it up to
+// 61.5); 512 keys 14.4 us, latency.
+// Hidden keys (behind the sequence, in a token's future, on a page outside the pool) get the weight 0 by selection and do
+// not count for a row's unit, so that what their rows hold, NaN and large scales included, reaches nothing.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -55,7 +61,8 @@ struct PsGeom {
   static constexpr int SMEM = ROWS + (RING > COMB ? RING : COMB);
   static_assert(SMEM - ROWS >= (int)sizeof(PagedLine), "the line lies in the ring");
   static constexpr int OREGS = D / 4 * NT;
-  static constexpr int MINB = OREGS <= 32 ? (NG * NT > 2 ? 3 : 4) : 2;   // spills else
+  // resident CTAs: as many as leave most instances without spills (the one of the batch above spills a few registers at 4)
+  static constexpr int MINB = OREGS <= 32 ? (NG * NT > 2 ? 3 : 4) : 2;
 };
 
 __device__ __forceinline__ void ps_cp16(uint32_t dst, const void* src) {
@@ -102,8 +109,8 @@ __device__ __forceinline__ uint32_t ps_sub2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// What a key row's bytes are XORed with within a stage's codes: 32-byte pieces move over the banks so that the operand reads (8 rows at
-// one column, and 4 rows two apart at neighbouring columns) fall on distinct ones.
+// What a key row's bytes are XORed with within a stage's codes: 32-byte pieces move over the banks so that the operand
+// reads (8 rows at one column, and 4 rows two apart at neighbouring columns) fall on distinct ones.
 template <int RB>
 __host__ __device__ constexpr uint32_t ps_turn(int row) {
   return (RB < 128 ? ((row * RB) >> 7) & 3 : (row & 3) ^ ((row >> 2) & 1)) << 5;
@@ -323,7 +330,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
           top = fmaxf(top, fmaxf(fabsf(ps_half<F16>(&raw[i], 0)), fabsf(ps_half<F16>(&raw[i], 1))));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // largest value of the row to [2^8, 2^9): every product stays far inside fp32, values down to 2^-22 of it are normal in fp16
+        // largest value of the row to [2^8, 2^9): every product stays far inside fp32, values down to 2^-22 of it are normal
+        // in fp16
         const int fe = min(262 - (int)((__float_as_uint(top) >> 23) & 255u), 253);
         const float up = __uint_as_float((uint32_t)fe << 23), down = __uint_as_float((uint32_t)(254 - fe) << 23);
 #pragma unroll
@@ -513,8 +521,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             rise = rise || fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + 4.f || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + 4.f;
           }
           if (__any_sync(0xffffffffu, rise)) {
-            // a row's unit: the largest finite scale that it sees to [2^8, 2^9), good for scales up to 4 times that and weights up to 2^4 (w
-            // stays below 2^15): as high as fp16 goes, so that small weights keep their bits
+            // a row's unit: the largest finite scale that it sees to [2^8, 2^9), good for scales up to 4 times that and
+            // weights up to 2^4 (w stays below 2^15): as high as fp16 goes, so that small weights keep their bits
             constexpr uint32_t INF = F16 ? 0x7C00u : 0x7F80u;
             // the largest scale of either key of this lane, anew (rare: not worth a register elsewhere)
             uint32_t mine2[2];
@@ -537,7 +545,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
                 const float mn = fmaxf(m[nt][j], x);
                 // the largest scale that the row sees here
-                uint32_t top = max((hidden >> (4 * nt + j)) & 1u ? 0u : mine2[0], (hidden >> (4 * nt + j + 2)) & 1u ? 0u : mine2[1]);
+                uint32_t top = max((hidden >> (4 * nt + j)) & 1u ? 0u : mine2[0],
+                                   (hidden >> (4 * nt + j + 2)) & 1u ? 0u : mine2[1]);
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 8));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 16));
