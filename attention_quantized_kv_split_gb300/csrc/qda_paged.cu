@@ -940,6 +940,14 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
     if (off16(p)) return QDA_ERR_ALIGN;
   if (off4(q_start) || off4(kv_len) || off4(block_table) || q_tstride % 8 || q_hstride % 8) return QDA_ERR_ALIGN;
   if (total_q == 0) return QDA_OK;
+  // a row of q may be read after its output is written: by the other part of its values (D = 512), or to be done anew
+  long long lo = 0, hi = D;
+  for (const long long span : {(total_q - 1) * q_tstride, (H - 1) * q_hstride}) {
+    lo += std::min(span, 0LL);
+    hi += std::max(span, 0LL);
+  }
+  const char *qc = static_cast<const char*>(q), *oc = static_cast<const char*>(out);
+  if (qc + 2 * lo < oc + 2LL * total_q * H * D && oc < qc + 2 * hi) return QDA_ERR_INVALID;
   QdaPagedParams p;
   std::memset(&p, 0, sizeof(p));
   int sms;

@@ -317,7 +317,7 @@ int qdecode_paged_append(const void* k, const void* v, long long k_tstride, long
  *     out[t, h, :] = sum_n softmax_n( q[t, h, :] . k_hat[n] / sqrt(D) ) v_hat[n]
  * causal = 0 is cross attention to states of another length (an encoder's, appended once). A token that sees no key
  * gives zeros. Keys that a token does not see, rows of pages behind kv_len[b] among them, reach nothing, whatever they
- * hold. Rows of out at and behind q_start[B] stay as they are; out must not overlap q. max_q (>= 1) is the host's bound on
+ * hold. Rows of out at and behind q_start[B] stay as they are; out must not overlap q (refused). max_q (>= 1) is the host's bound on
  * the L_b and only chooses the kernel: results are right for any value (a step of many single tokens and a long chunk takes
  * one kernel for both, so it is faster as two calls where the host knows them apart).
  *

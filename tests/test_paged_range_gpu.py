@@ -288,3 +288,18 @@ def test_a_query_that_is_not_a_number(q_lens, D):
         assert torch.isnan(got[q_lens[0], 1]).all(), kv0
         got[q_lens[0], 1] = c.run()[q_lens[0], 1]
         assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2], [40, 90]])
+def test_outputs_next_to_the_queries(q_lens):
+    # queries and outputs back to back in one buffer, either way round, and one query row expanded over all tokens and heads
+    c = Case(q_lens, [200, 333], 4, 2, 512, 4, 64, "bf16", 32, seed=51)
+    ref = c.run()
+    both = torch.zeros(2 * c.total, c.H, c.D, dtype=c.q.dtype, device="cuda")
+    for q, out in ((both[: c.total], both[c.total:]), (both[c.total:], both[: c.total])):
+        q.copy_(c.q)
+        assert torch.equal(c.run(q=q, out=out), ref)
+    with pytest.raises(qda.QdaError):
+        c.run(q=both[: c.total], out=both[1: c.total + 1])
+    one = c.q[:1, :1].expand(c.total, c.H, c.D)
+    assert torch.equal(c.run(q=one, out=torch.empty_like(ref)), c.run(q=one.contiguous()))
