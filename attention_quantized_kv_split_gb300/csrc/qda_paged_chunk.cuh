@@ -16,10 +16,10 @@
 // Every link is an mbarrier; every wait is bounded and sets the device error word, and after one that gave up every role
 // ends without an access that the call's arrays do not hold.
 //
-// Measured: 2048 tokens over 32768 keys (32 heads, 8 KV heads, D 128, 4-bit) 873 us, 1.23 PFLOP/s, 64 % of a large bf16
+// Measured: 2048 tokens over 32768 keys (32 heads, 8 KV heads, D 128, 4-bit) 875 us, 1.22 PFLOP/s, 64 % of a large bf16
 // product's rate. The tensor pipe and the issue slots are each busy half of the time there (52 and 54 %) and the warps wait
 // for loads most (long_scoreboard 4.3 per issue): for scores from tensor memory and for codes, one item ahead. Ragged chunks
-// at D 256, 8-bit, 431 us (0.56 PFLOP/s, tensor pipe 27 %, the same wait 5.6): one tile per CTA, so a block is dequantised for
+// at D 256, 8-bit, 432 us (0.56 PFLOP/s, tensor pipe 27 %, the same wait 5.6): one tile per CTA, so a block is dequantised for
 // 128 rows only, and the cache is read from DRAM four times over. Cross attention at D 64 65 us (12 %, 6.9), 250 tokens over
 // 4097 keys at D 512 100 us (21 %, 5.9).
 //
