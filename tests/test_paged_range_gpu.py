@@ -303,3 +303,75 @@ def test_outputs_next_to_the_queries(q_lens):
         c.run(q=both[: c.total], out=both[1: c.total + 1])
     one = c.q[:1, :1].expand(c.total, c.H, c.D)
     assert torch.equal(c.run(q=one, out=torch.empty_like(ref)), c.run(q=one.contiguous()))
+
+
+@pytest.mark.parametrize("H,Hkv,D,GS,bits,page", [(5, 1, 128, 64, 4, 16), (12, 4, 64, 32, 8, 256), (64, 1, 64, 64, 4, 32),
+                                                  (6, 2, 512, 32, 8, 16), (3, 3, 256, 128, 4, 64)])
+def test_rows_done_anew_in_a_ragged_batch(H, Hkv, D, GS, bits, page):
+    # forty sequences of any lengths (some idle, some with more tokens than keys), strided queries, absent pages, large keys
+    # among the last third of a sequence's new tokens: eager, on another stream and from a captured graph
+    rng = np.random.default_rng(D + H)
+    q_lens = [int(x) for x in rng.integers(0, 60, 40)]
+    q_lens[3], q_lens[7] = 200, 0
+    kv_lens = [max(1, L + int(x)) for L, x in zip(q_lens, rng.integers(-10, 200, 40))]
+    c = Case(q_lens, kv_lens, H, Hkv, D, bits, GS, "bf16", page, seed=52)
+    quiet = np.zeros(c.total, bool)   # tokens that see none of the large keys
+    for b, (L, n) in enumerate(zip(q_lens, kv_lens)):
+        loud = sorted(int(k) for k in rng.integers(max(n - L // 3 - 1, 0), n, 3))
+        for k in loud:
+            put(c, int(rng.choice([KB, VS, VB])), b, [k], 2.0 ** int(rng.integers(8, 24)))
+        quiet[c.start[b]: c.start[b + 1]] = n - L + np.arange(L) < loud[0]
+    assert quiet.sum() > c.total / 3
+    hidden = []
+    for b in (3, 20, 30):
+        col = int(rng.integers(0, -(-kv_lens[b] // page)))
+        hidden += [(b, k) for k in range(col * page, min((col + 1) * page, kv_lens[b]))]
+        gone = (b, col)
+        c.table[gone] = c.arrays[0].shape[0] + b
+    table = c.table.clone()
+    c.table = torch.where((table >= c.arrays[0].shape[0]) | (table < 0), torch.zeros_like(table), table)
+    reload(c)
+    c.table = table
+    for b, k in hidden:   # (what an absent page would hold is nothing, not page 0's rest)
+        c.K[b][:, k] = c.V[b][:, k] = c.A[b][:, k] = 0
+    wide = torch.zeros(c.total, H + 3, D + 8, dtype=c.q.dtype, device="cuda")
+    wide[:, 2: H + 2, :D] = c.q
+    q = wide[:, 2: H + 2, :D]
+    ref, tol = c.reference(True, hidden)
+    # Beside the tolerance of ordinary inputs: operands are off by 2^-13 of the largest key or value that the token sees (bounds of
+    # what a scale and bias allow), that is what "done anew" is measured by
+    for b, (L, n) in enumerate(zip(q_lens, kv_lens)):
+        keys = torch.arange(n, device="cuda")
+        pages = c.table[b, keys // page].long().clamp(0, c.arrays[0].shape[0] - 1)
+        there = torch.tensor([(b, k) not in hidden for k in range(n)], device="cuda")[:, None, None]
+        sizes = lambda x: torch.where(there, c.arrays[x][pages, :, keys % page].double().abs(), 0)  # noqa: E731
+        top = [(sizes(x) * (2 ** bits - 1) + sizes(x + 1)).amax(-1).cummax(0).values.cpu().numpy() for x in (KS, VS)]
+        for i in range(L):
+            last = n - L + i
+            r = int(c.start[b]) + i
+            if last < 0 or not quiet[r]:
+                continue
+            seen = [k for k in range(last + 1) if (b, k) not in hidden]
+            for h in range(H):
+                g = h // (H // Hkv)
+                ds = 2.0 ** -13 * top[0][last, g] * np.abs(c.q64[r, h]).sum() / math.sqrt(D)
+                x = c.K[b][g, seen] @ c.q64[r, h] / math.sqrt(D)
+                w = np.exp(x - x.max()) if len(seen) else np.zeros(0)
+                with np.errstate(over="ignore"):
+                    tol[r, h] += 2.0 ** -13 * top[1][last, g] + (np.expm1(2 * ds) * (w @ c.A[b][g, seen]) / w.sum() if len(seen) else 0)
+    got = c.run(q=q)
+    err = np.abs(got.double().cpu().numpy() - ref)
+    assert np.isfinite(got.double().cpu().numpy()).all()
+    assert (err <= tol)[quiet].all(), (err / tol)[quiet].max()
+    out, s, graph = torch.zeros_like(got), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    c.run(q=q, out=out, stream=s)
+    s.synchronize()
+    assert torch.equal(out, got)
+    with torch.cuda.graph(graph):
+        c.run(q=q, out=out)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, got)
