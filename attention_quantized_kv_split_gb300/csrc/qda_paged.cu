@@ -440,7 +440,7 @@ cudaError_t launch_merge(const QdaPagedParams& p, int rows, cudaStream_t s) {
 // off by at most half a step of the subnormal numbers, 2^-19 of the largest with 4-bit codes and 2^-22 with 8-bit ones:
 // next to nothing for a row that sees the largest, but a token in the middle of a causal chunk does not see the keys
 // behind it, whatever they hold. This kernel, behind the merge of a causal call, looks for tokens whose own part of their
-// last block holds nothing within FAR of the block's largest key, or value (so that the operands' error passes 2^-13 of
+// last block holds less than 1 / FAR of the block's largest key, or value (so that the operands' error passes 2^-13 of
 // what they see themselves), and does their rows anew in fp32: a CTA per row, a thread per key for the scores and a thread
 // per dimension for the values. On ordinary inputs it finds none: a warp per KV head and block of new tokens reads their
 // scales and biases. What it costs then: chunk over 32768 keys 858 -> 861 us, ragged chunks at D = 256 424 -> 430 us, 250
@@ -523,11 +523,12 @@ __device__ __forceinline__ void far_find(const QdaPagedParams& p, const PagedSeq
   kup = __shfl_up_sync(0xffffffffu, kup, 1);
   vup = __shfl_up_sync(0xffffffffu, vup, 1);
   if (lane == 0) kup = vup = 0.f;
+  // (zeros are exact in any unit: a token that sees nothing else of the block, padding for instance, is left as it is)
+  auto far = [](float all, float own) { return own > 0.f && all > FAR * own; };
   uint32_t mine = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (key0 + i >= s.base && key0 + i < end && (kall > FAR * fmaxf(k[i], kup) || vall > FAR * fmaxf(v[i], vup)))
-      mine |= 1u << i;
+    if (key0 + i >= s.base && key0 + i < end && (far(kall, fmaxf(k[i], kup)) || far(vall, fmaxf(v[i], vup)))) mine |= 1u << i;
   // key 4 lane + i of the block is bit 4 lane + i of 128
 #pragma unroll
   for (int y = 0; y < 4; ++y) found[y] = __reduce_or_sync(0xffffffffu, lane >> 3 == y ? mine << (4 * (lane & 7)) : 0u);
