@@ -441,17 +441,22 @@ cudaError_t launch_merge(const QdaPagedParams& p, int rows, cudaStream_t s) {
 // next to nothing for a row that sees the largest, but a token in the middle of a causal chunk does not see the keys
 // behind it, whatever they hold. This kernel, behind the merge of a causal call, looks for tokens whose own part of their
 // last block holds less than 1 / FAR of the block's largest key, or value (so that the operands' error passes 2^-13 of
-// what they see themselves), and does their rows anew in fp32: a CTA per row, a thread per key for the scores and a thread
-// per dimension for the values. On ordinary inputs it finds none: a warp per KV head and block of new tokens reads their
-// scales and biases. What it costs then: chunk over 32768 keys 858 -> 861 us, ragged chunks at D = 256 424 -> 430 us, 250
-// tokens at D = 512 99 -> 100 us (the same done by the chunk kernel's own warps costs it registers: 858 -> 915 us). Rows
-// that are done anew take some 100 us and more each at 32768 keys.
+// what they see themselves), and does their rows anew in fp32: a CTA takes eight rows of a KV head at a time, a thread per
+// key for the scores and a thread per dimension for the values, so that a key is read once for all eight. On ordinary
+// inputs it finds none: a warp per KV head and block of new tokens reads their scales and biases. What it costs then: chunk
+// over 32768 keys 858 -> 861 us, ragged chunks at D = 256 424 -> 430 us, 250 tokens at D = 512 99 -> 100 us (the same done
+// by the chunk kernel's own warps costs it registers: 858 -> 915 us). 32 tokens of 8 heads done anew: 0.1 ms over 1024
+// keys, 2.7 over 32768 (D 128, 4-bit; a row at a time it took 193), 7.8 at D 256, 8-bit.
 constexpr int kFarThreads = 256, kFarWarps = kFarThreads / 32;
+constexpr int kFarRows = 8;    // rows that are done at a time
+constexpr int kFarParts = 16;  // CTAs at most that share a unit's rows
 
 struct FarShared {
   long long first[QDA_MAX_B + 1];   // units (KV head, block of new tokens) before each sequence
   uint32_t found[kFarWarps][4];     // a bit per key of a warp's unit: the token there is done anew
-  float q[512], w[kFarThreads], o[kFarThreads], red[kFarWarps];
+  uint32_t row[kFarThreads];        // pool rows of the keys at hand (all ones: absent)
+  float4 q[512][kFarRows / 4], w[kFarThreads][kFarRows / 4];   // queries by dimension, weights by key
+  float red[kFarWarps][kFarRows], o[kFarThreads];
 };
 
 __device__ __forceinline__ int far_tokens(const QdaPagedParams& p, const PagedSeq& s) { return s.rows / p.nrep; }
@@ -534,89 +539,170 @@ __device__ __forceinline__ void far_find(const QdaPagedParams& p, const PagedSeq
   for (int y = 0; y < 4; ++y) found[y] = __reduce_or_sync(0xffffffffu, lane >> 3 == y ? mine << (4 * (lane & 7)) : 0u);
 }
 
-// A CTA: f(the threads' x) over all of them, for every thread.
+// A CTA: f(the threads' x) over all of them, for every thread and row.
 template <typename F>
-__device__ __forceinline__ float far_reduce(FarShared& sh, float x, F f) {
+__device__ __forceinline__ void far_reduce(FarShared& sh, float (&x)[kFarRows], F f) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) x = f(x, __shfl_xor_sync(0xffffffffu, x, o));
+  for (int r = 0; r < kFarRows; ++r) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) x[r] = f(x[r], __shfl_xor_sync(0xffffffffu, x[r], o));
+  }
   __syncthreads();   // the last one's results are read
-  if ((threadIdx.x & 31) == 0) sh.red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  x = sh.red[0];
+  if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-  for (int w = 1; w < kFarWarps; ++w) x = f(x, sh.red[w]);
-  return x;
+    for (int r = 0; r < kFarRows; ++r) sh.red[threadIdx.x >> 5][r] = x[r];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kFarRows; ++r) {
+    x[r] = sh.red[0][r];
+#pragma unroll
+    for (int w = 1; w < kFarWarps; ++w) x[r] = f(x[r], sh.red[w][r]);
+  }
 }
 
-// A CTA: one output row, query head h of the token in row t of q, over its keys n < seen.
+__device__ __forceinline__ void far_unpack(const float4 (&a)[kFarRows / 4], float (&x)[kFarRows]) {
+#pragma unroll
+  for (int i = 0; i < kFarRows / 4; ++i) {
+    x[4 * i] = a[i].x;
+    x[4 * i + 1] = a[i].y;
+    x[4 * i + 2] = a[i].z;
+    x[4 * i + 3] = a[i].w;
+  }
+}
+
+// A CTA: output rows of up to kFarRows (token, query head) pairs of KV head kvh: heads[r] of the token in row tokens[r] of q
+// over its keys n < seen[r] (0: no such row).
 template <int BITS>
-__device__ void far_row(const QdaPagedParams& p, FarShared& sh, int b, int kvh, int t, int h, int seen) {
+__device__ void far_rows(const QdaPagedParams& p, FarShared& sh, int b, int kvh, const int (&tokens)[kFarRows],
+                         const int (&heads)[kFarRows], const int (&seen)[kFarRows]) {
   constexpr int PER = 32 / BITS;
   constexpr uint32_t MASK = (1u << BITS) - 1;
   const int tid = threadIdx.x, pmask = (1 << p.page_shift) - 1;
-  const uint16_t* q = p.q + (long long)t * p.q_tstride + (long long)h * p.q_hstride;
   const int* tab = p.table + (size_t)b * p.max_pages;
-  __syncthreads();   // the last row's queries and sums are read
-  for (int d = tid; d < p.D; d += kFarThreads) sh.q[d] = half_bits_to_float_rt(q[d], p.f16);
-  // values: a thread per dimension (two at D = 512) and key in turn
-  const int part = p.D < kFarThreads ? tid / p.D : 0, parts = p.D < kFarThreads ? kFarThreads / p.D : 1, d0 = tid & (p.D - 1);
-  float m = -INFINITY, l = 0.f, o[2] = {0.f, 0.f};
-  for (int n0 = 0; n0 < seen; n0 += kFarThreads) {
-    const int n = n0 + tid;
-    int pg = n < seen ? __ldg(tab + (n >> p.page_shift)) : -1;
-    const bool sees = (unsigned)pg < (unsigned)p.num_pages;
-    const long long row = qda_pool_row(sees ? pg : 0, kvh, n & pmask, p.Hkv, p.page_shift);
-    __syncthreads();   // queries, and the last weights are read
-    float x = -INFINITY;
-    if (sees) {
-      x = 0.f;
-      for (int g = 0; g < p.NG; ++g) {
-        const float s = half_bits_to_float_rt(__ldg(p.ks + row * p.NG + g), p.f16);
-        const float z = half_bits_to_float_rt(__ldg(p.kb + row * p.NG + g), p.f16);
-        for (int i = 0; i < p.GS / PER; ++i) {
-          const uint32_t w = __ldg(p.kp + row * p.W + g * (p.GS / PER) + i);
+  __syncthreads();   // the last rows' queries and sums are read
 #pragma unroll
-          for (int e = 0; e < PER; ++e)
-            x = fmaf(sh.q[g * p.GS + i * PER + e], fmaf(s, (float)((w >> (BITS * e)) & MASK), z), x);
+  for (int r = 0; r < kFarRows; ++r) {
+    const uint16_t* q = p.q + (long long)tokens[r] * p.q_tstride + (long long)heads[r] * p.q_hstride;
+    for (int d = tid; d < p.D; d += kFarThreads)
+      reinterpret_cast<float*>(&sh.q[d])[r] = seen[r] ? half_bits_to_float_rt(q[d], p.f16) : 0.f;
+  }
+  // values: a thread per dimension (two at D = 512) and key in turn
+  const int part = p.D < kFarThreads ? tid / p.D : 0, parts = p.D < kFarThreads ? kFarThreads / p.D : 1;
+  const int d0 = tid & (p.D - 1);
+  int most = 0;
+  float m[kFarRows], l[kFarRows], o[2][kFarRows];
+#pragma unroll
+  for (int r = 0; r < kFarRows; ++r) {
+    m[r] = -INFINITY;
+    l[r] = o[0][r] = o[1][r] = 0.f;
+    most = max(most, seen[r]);
+  }
+  for (int n0 = 0; n0 < most; n0 += kFarThreads) {
+    const int n = n0 + tid;
+    const int pg = n < most ? __ldg(tab + (n >> p.page_shift)) : -1;
+    const bool there = (unsigned)pg < (unsigned)p.num_pages;
+    const uint32_t row = there ? (uint32_t)qda_pool_row(pg, kvh, n & pmask, p.Hkv, p.page_shift) : 0xffffffffu;
+    __syncthreads();   // queries are there, the last weights and rows read
+    sh.row[tid] = row;
+    float x[kFarRows], top[kFarRows];
+#pragma unroll
+    for (int r = 0; r < kFarRows; ++r) x[r] = 0.f;
+    if (there) {
+      const uint4* codes = reinterpret_cast<const uint4*>(p.kp + (uint64_t)row * p.W);
+      for (int d = 0; d < p.D; d += 4 * PER) {   // 16 bytes of codes, of one group
+        const uint4 a = __ldg(codes + d / (4 * PER));
+        const uint64_t g = (uint64_t)row * p.NG + d / p.GS;
+        const float s = half_bits_to_float_rt(__ldg(p.ks + g), p.f16), z = half_bits_to_float_rt(__ldg(p.kb + g), p.f16);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+          for (int e = 0; e < PER; ++e) {
+            const float v = fmaf(s, (float)((w[i] >> (BITS * e)) & MASK), z);
+            float q[kFarRows];
+            far_unpack(sh.q[d + i * PER + e], q);
+#pragma unroll
+            for (int r = 0; r < kFarRows; ++r) x[r] = fmaf(q[r], v, x[r]);
+          }
         }
       }
-      x *= p.qscale;
     }
-    const float mn = fmaxf(m, far_reduce(sh, x, [](float a, float c) { return fmaxf(a, c); }));
-    const float a = m == -INFINITY ? 0.f : exp2f(m - mn), w = !sees ? 0.f : exp2f(x - (mn == -INFINITY ? 0.f : mn));
-    m = mn;
-    l = l * a + w;
-    o[0] *= a;
-    o[1] *= a;
-    sh.w[tid] = w;
-    __syncthreads();
-    const int many = min(kFarThreads, seen - n0);
-    for (int i = part; i < many; i += parts) {
-      const float wi = sh.w[i];
-      if (wi == 0.f) continue;   // (no key there, or none that counts: what it holds stays out)
-      const long long r = qda_pool_row(__ldg(tab + ((n0 + i) >> p.page_shift)), kvh, (n0 + i) & pmask, p.Hkv, p.page_shift);
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int d = d0 + y * kFarThreads;
-        if (d >= p.D) break;
-        const float s = half_bits_to_float_rt(__ldg(p.vs + r * p.NG + d / p.GS), p.f16);
-        const float z = half_bits_to_float_rt(__ldg(p.vb + r * p.NG + d / p.GS), p.f16);
-        const uint32_t c = (__ldg(p.vp + r * p.W + d / PER) >> (BITS * (d % PER))) & MASK;
-        o[y] = fmaf(wi, fmaf(s, (float)c, z), o[y]);
+    for (int r = 0; r < kFarRows; ++r) top[r] = x[r] = there && n < seen[r] ? x[r] * p.qscale : -INFINITY;
+    far_reduce(sh, top, [](float a, float c) { return fmaxf(a, c); });
+    float w[kFarRows];
+#pragma unroll
+    for (int r = 0; r < kFarRows; ++r) {
+      const float mn = fmaxf(m[r], top[r]);
+      const float a = m[r] == -INFINITY ? 0.f : exp2f(m[r] - mn);
+      w[r] = there && n < seen[r] ? exp2f(x[r] - (mn == -INFINITY ? 0.f : mn)) : 0.f;
+      m[r] = mn;
+      l[r] = l[r] * a + w[r];
+      o[0][r] *= a;
+      o[1][r] *= a;
+    }
+#pragma unroll
+    for (int i = 0; i < kFarRows / 4; ++i) sh.w[tid][i] = make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    __syncthreads();
+    const int many = min(kFarThreads, most - n0);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int d = d0 + y * kFarThreads;
+      if (d >= p.D) break;
+      const int at = d / PER, sh_bits = BITS * (d % PER), g = d / p.GS;
+#pragma unroll 1
+      for (int i0 = part; i0 < many; i0 += 4 * parts) {
+        uint32_t c[4], rw[4], us[4], uz[4];   // four keys' loads on their way together
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = i0 + j * parts;
+          rw[j] = i < many ? sh.row[i] : 0xffffffffu;
+          const uint64_t ok = rw[j] == 0xffffffffu ? 0 : rw[j];
+          c[j] = __ldg(p.vp + ok * p.W + at);
+          us[j] = __ldg(p.vs + ok * p.NG + g);
+          uz[j] = __ldg(p.vb + ok * p.NG + g);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (rw[j] == 0xffffffffu) continue;
+          const float s = half_bits_to_float_rt(us[j], p.f16), z = half_bits_to_float_rt(uz[j], p.f16);
+          const float v = fmaf(s, (float)((c[j] >> sh_bits) & MASK), z);
+          float wt[kFarRows];
+          far_unpack(sh.w[i0 + j * parts], wt);
+#pragma unroll
+          for (int r = 0; r < kFarRows; ++r)   // what a row does not see stays out, whatever it holds
+            o[y][r] = wt[r] == 0.f ? o[y][r] : fmaf(wt[r], v, o[y][r]);
+        }
       }
     }
   }
-  l = far_reduce(sh, l, [](float x, float y) { return x + y; });
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  sh.o[tid] = o[0];
-  __syncthreads();
-  if (part == 0) {
-    for (int i = 1; i < parts; ++i) o[0] += sh.o[tid + i * p.D];
+  far_reduce(sh, l, [](float x, float y) { return x + y; });
+#pragma unroll 1
+  for (int r = 0; r < kFarRows; ++r) {
+    float mine[2] = {0.f, 0.f}, sum = 0.f;
+    int t = 0, h = 0, see = 0;
+#pragma unroll
+    for (int k = 0; k < kFarRows; ++k)   // (registers have no index)
+      if (k == r) {
+        mine[0] = o[0][k];
+        mine[1] = o[1][k];
+        sum = l[k];
+        t = tokens[k];
+        h = heads[k];
+        see = seen[k];
+      }
+    __syncthreads();
+    sh.o[tid] = mine[0];
+    __syncthreads();
+    if (part != 0 || see == 0) continue;
+    for (int i = 1; i < parts; ++i) mine[0] += sh.o[tid + i * p.D];
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint16_t* out = p.out + ((long long)t * p.H + h) * p.D;
 #pragma unroll
     for (int y = 0; y < 2; ++y)
       if (d0 + y * kFarThreads < p.D)
-        out[d0 + y * kFarThreads] = (uint16_t)(p.f16 ? to_bits16<true>(o[y] * inv) : to_bits16<false>(o[y] * inv));
+        out[d0 + y * kFarThreads] = (uint16_t)(p.f16 ? to_bits16<true>(mine[y] * inv) : to_bits16<false>(mine[y] * inv));
   }
 }
 
@@ -644,10 +730,14 @@ __global__ void __launch_bounds__(kFarThreads) qda_paged_far_kernel(const __grid
   }
   __syncthreads();
   const long long units = sh.first[p.B];
+  // few units: several warps, of different CTAs, find the same one's rows and share them
+  const int share = units == 0 ? 1 : (int)max(1LL, min((long long)kFarParts, (long long)gridDim.x * kFarWarps / units));
+  const long long items = units * share;
   bool waited = false;
-  // units u0, u0 + gridDim.x, ...: a warp each
-  for (long long u0 = blockIdx.x; u0 < units; u0 += (long long)gridDim.x * kFarWarps) {
-    auto unit = [&](long long u, int* b, int* kvh, int* j) {
+  // items i0, i0 + gridDim.x, ...: a warp each; item i is unit i % units and part i / units of its rows
+  for (long long i0 = blockIdx.x; i0 < items; i0 += (long long)gridDim.x * kFarWarps) {
+    auto unit = [&](long long item, int* b, int* kvh, int* j) {
+      const long long u = item % units;
       *b = seq_of(sh.first, p.B, u);
       const PagedSeq s = paged_seq(p, *b, 128);
       const int blocks = far_blocks(p, s, j);
@@ -657,8 +747,8 @@ __global__ void __launch_bounds__(kFarThreads) qda_paged_far_kernel(const __grid
       return s;
     };
     uint32_t found[4] = {0u, 0u, 0u, 0u};
-    const long long mine = u0 + (long long)warp * gridDim.x;
-    if (mine < units) {
+    const long long mine = i0 + (long long)warp * gridDim.x;
+    if (mine < items) {
       int b, kvh, j;
       const PagedSeq s = unit(mine, &b, &kvh, &j);
       switch (p.NG) {
@@ -678,14 +768,29 @@ __global__ void __launch_bounds__(kFarThreads) qda_paged_far_kernel(const __grid
     __syncthreads();
     if (!waited) pdl_wait();   // the merge has written its rows
     waited = true;
-    for (int w = 0; w < kFarWarps && u0 + (long long)w * gridDim.x < units; ++w) {
+    for (int w = 0; w < kFarWarps && i0 + (long long)w * gridDim.x < items; ++w) {
       int b, kvh, j;
-      const PagedSeq s = unit(u0 + (long long)w * gridDim.x, &b, &kvh, &j);
+      const long long item = i0 + (long long)w * gridDim.x;
+      const PagedSeq s = unit(item, &b, &kvh, &j);
+      const int part = (int)(item / units);
+      int tokens[kFarRows], heads[kFarRows], seen[kFarRows], at = 0, group = 0;   // the rows of the next group, as they are met
+      auto flush = [&]() {
+        for (int r = at; r < kFarRows; ++r) tokens[r] = heads[r] = seen[r] = 0;
+        if (at > 0 && group % share == part) far_rows<BITS>(p, sh, b, kvh, tokens, heads, seen);
+        at = 0;
+        ++group;
+      };
       for (int key = 0; key < 128; ++key) {
         if (!((sh.found[w][key >> 5] >> (key & 31)) & 1u)) continue;
         const int pos = j * 128 + key;
-        for (int r = 0; r < p.nrep; ++r) far_row<BITS>(p, sh, b, kvh, s.first + pos - s.base, kvh * p.nrep + r, pos + 1);
+        for (int r = 0; r < p.nrep; ++r) {
+          tokens[at] = s.first + pos - s.base;
+          heads[at] = kvh * p.nrep + r;
+          seen[at] = pos + 1;
+          if (++at == kFarRows) flush();
+        }
       }
+      if (at > 0) flush();
     }
     __syncthreads();
   }

@@ -323,7 +323,7 @@ int qdecode_paged_append(const void* k, const void* v, long long k_tstride, long
  *
  * Calls of up to 32 rows per KV head (max_q * H / Hkv; 16 at D = 256, 24 at D = 512) take a kernel that reads the codes into
  * matrix instructions as they are, larger ones a kernel that turns the codes into fp16 operands; a causal call of the
- * second kind ends with a third kernel, which does rows anew (in fp32, slowly: a few microseconds per row and thousand
+ * second kind ends with a third kernel, which does rows anew (in fp32, slowly: some 3 us per token and thousand
  * keys) whose operands a far larger key of a later token would have cost their bits. All sums and the softmax are fp32. What is rounded to 11 significant bits:
  *   - the first kernel: the weight times the scale of a value's group. Products 2^-22 and more of a row's largest weight
  *     times the largest scale that the row sees keep their 11 bits. Scores are right to fp32.
