@@ -317,28 +317,28 @@ int qdecode_paged_append(const void* k, const void* v, long long k_tstride, long
  *     out[t, h, :] = sum_n softmax_n( q[t, h, :] . k_hat[n] / sqrt(D) ) v_hat[n]
  * causal = 0 is cross attention to states of another length (an encoder's, appended once). A token that sees no key
  * gives zeros. Keys that a token does not see, rows of pages behind kv_len[b] among them, reach nothing, whatever they
- * hold. Rows of out at and behind q_start[B] stay as they are; out must not overlap q (refused). max_q (>= 1) is the host's bound on
- * the L_b and only chooses the kernel: results are right for any value (a step of many single tokens and a long chunk takes
- * one kernel for both, so it is faster as two calls where the host knows them apart).
+ * hold. Rows of out at and behind q_start[B] stay as they are; out must not overlap q (refused). max_q (>= 1) is the
+ * host's bound on the L_b and only chooses the kernel: results are right for any value (a step of many single tokens and
+ * a long chunk takes one kernel for both, so it is faster as two calls where the host knows them apart).
  *
- * Calls of up to 32 rows per KV head (max_q * H / Hkv; 16 at D = 256, 24 at D = 512) take a kernel that reads the codes into
- * matrix instructions as they are, larger ones a kernel that turns the codes into fp16 operands; a causal call of the
- * second kind ends with a third kernel, which does rows anew (in fp32, slowly: some 3 us per token and thousand
- * keys) whose operands a far larger key of a later token would have cost their bits. All sums and the softmax are fp32. What is rounded to 11 significant bits:
+ * Calls of up to 32 rows per KV head (max_q * H / Hkv; 16 at D = 256, 24 at D = 512) take a kernel that reads the codes
+ * into matrix instructions as they are, larger ones a kernel that turns the codes into fp16 operands; a causal call of
+ * the second kind ends with a third kernel, which does rows anew (in fp32, slowly: some 3 us per token and thousand keys)
+ * whose operands a far larger key of a later token would have cost their bits. All sums and the softmax are fp32. What is
+ * rounded to 11 significant bits:
  *   - the first kernel: the weight times the scale of a value's group. Products 2^-22 and more of a row's largest weight
  *     times the largest scale that the row sees keep their 11 bits. Scores are right to fp32.
  *   - the second: keys, values and weights. Keys and values down to 2^-8 (4-bit codes) or 2^-11 (8-bit) of the largest that
  *     their block of 128 keys can hold, |scale| * (2^bits - 1) + |bias|, keep their 11 bits, values measured by the largest
  *     of the blocks before as well; weights down to 2^-21 of a row's largest.
  * Smaller ones lose a bit with every further factor of two. Scales and biases are meant to be finite and below 2^64 in
- * magnitude: a token that sees a key with others may become infinite or NaN (in the second kernel NaN from 2^110 on), tokens
- * that do not see it do not.
+ * magnitude: a token that sees a key with others may become infinite or NaN (in the second kernel NaN from 2^110 on),
+ * tokens that do not see it do not.
  *
  * q has strides q_tstride, q_hstride in elements; out is contiguous [total_q, H, D] in q's dtype. dtype is the input dtype
  * alone (q, scales, biases and out). Supported: the bits, GS and D of qdecode_attn, H / Hkv <= QDA_MAX_NREP, B <= QDA_MAX_B,
  * total_q * H / Hkv below 2^31 - 256, kv_len below 2^31 - 512 (keys behind that are not seen). Uses the workspace as
- * qdecode_attn does, of
- * qdecode_paged_attn_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
+ * qdecode_attn does, of qdecode_paged_attn_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
  */
 int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                        const void* k_scales, const void* k_biases, const uint32_t* v_packed, const void* v_scales,

@@ -25,6 +25,8 @@ def _clean_status():
     torch.cuda.synchronize()
     qda.qdecode_attn_device_status()
     yield
+    torch.cuda.synchronize()   # absent pages leave their bit to nobody else
+    qda.qdecode_attn_device_status()
 
 
 KP, KS, KB, VP, VS, VB = range(6)
