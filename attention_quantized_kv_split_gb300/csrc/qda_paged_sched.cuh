@@ -17,11 +17,12 @@ namespace qda {
 
 // A tile's fixed work (its query rows, its results), in keys. Chunk kernel (tiles of 128 rows or more): ragged chunks of 1
 // to 1023 tokens at D = 256 take 470 us with 300, 451 with 448, 427 with 700, 432 with 900, 437 with 1600, cross attention
-// at D = 64 65.6, 65.5, 64.1, 66.1 and 65.8 us: anything from 700 to 1200 will do. Split kernel: one token of each of 64
-// sequences 100.2 us with 64, 96.9 with 160, 96.6 with 250; one sequence of 131072 keys 58 us with 240 or 256 and 54 with
-// 250, which is that length's luck and no reason: the cost is spread over a tile's blocks, so a border just behind a
-// tile's start hands one or two blocks to a CTA that pays the whole cost for them, and at that length no border falls so
-// (now 55.7 us there, and at 21 lengths from there to 133000 a median of 59.9, 61.5 at most).
+// at D = 64 65.6, 65.5, 64.1, 66.1 and 65.8 us: anything from 700 to 1200 will do. Split kernel: over fourteen sets of
+// lengths each (medians, us, with 100, 160, 250, 400, 700) one token of each of 64 sequences at D = 128 takes 99.4, 98.2,
+// 96.9, 96.9 and 98.6, one to four tokens of 24 short sequences 37.4, 35.6, 33.6, 33.4 and 33.3, one sequence of about 130000
+// keys at D = 256 60.0 with all, other shapes within 1 %: anything from 250 to 400 will do. Single lengths differ by luck
+// (131072 keys: 55 with 250 or 350, 58 with 240, 256, 300 or 400): the cost is spread over a tile's blocks, so a border just
+// behind a tile's start hands one or two blocks to a CTA that pays the whole cost for them.
 __device__ __forceinline__ constexpr int paged_tile_cost(int MT) { return MT >= 128 ? 700 : 250; }
 
 struct PagedSeq {

@@ -25,8 +25,8 @@
 // 16 keys. Measured: one token of 64 sequences of 700 to 8200 keys (32 heads, 8 KV heads, D 128, 4-bit) 97 us, 3.4 TB/s of
 // cache, half of a copy's rate: some 430 instructions per 16 keys keep the schedulers busy, and of the four CTAs of an SM
 // the one launched last runs a third longer (pieces weighted against that: 96 us here, but 59 instead of 54 for one long
-// sequence; not kept). One sequence of 131072 keys (16 heads, 4 KV heads, D 256) 55 us, 3.0 TB/s (lengths near it up to
-// 61.5); 512 keys 14.4 us, latency.
+// sequence; not kept). One sequence of 131072 keys (16 heads, 4 KV heads, D 256) 55 us, 3.0 TB/s (lengths near it
+// 60); 512 keys 14.4 us, latency.
 // Hidden keys (behind the sequence, in a token's future, on a page outside the pool) get the weight 0 by selection and do
 // not count for a row's unit, so that what their rows hold, NaN and large scales included, reaches nothing.
 #pragma once
