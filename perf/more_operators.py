@@ -405,8 +405,8 @@ def run(state):
     st["side"].copy_(st["before"])
     if own:
         qda.qdecode_paged_evict(st["kp"], st["ks"], st["kb"], st["vp"], st["vs"], st["vb"], st["mass"], st["token"], st["kv_len"],
-                                st["new_len"], st["table"], st["freed"], st["n_freed"], c["budget"], limit=c["limit"],
-                                sinks=c["sinks"], recent=c["recent"], shift=st["shift"])
+                                st["new_len"], st["table"], st["freed"], st["n_freed"], c["GS"], c["bits"], c["budget"],
+                                limit=c["limit"], sinks=c["sinks"], recent=c["recent"], shift=st["shift"])
     else:
         _plain_evict(st)
     return {k: st[k] for k in ("kp", "ks", "kb", "vp", "vs", "vb", "mass", "token", "new_len", "shift", "table", "freed", "n_freed")}
