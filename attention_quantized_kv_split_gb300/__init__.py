@@ -231,6 +231,17 @@ def _ints(dev: int, names: str, *tensors) -> None:
                              f"strides {t.stride()}")
 
 
+def _floats(dev: int, name: str, t: torch.Tensor, shape) -> None:
+    if not (t.dtype is torch.float32 and t.shape == shape and t.is_contiguous() and t.get_device() == dev):
+        raise ValueError(f"{name}: expected contiguous float32 {tuple(shape)} on device {dev}, got {t.dtype} {tuple(t.shape)} on "
+                         f"{t.device}, strides {t.stride()}")
+
+
+def _keys(dev, kp, ks, kb, D, GS, bits):
+    """num_pages, Hkv, page and dtype of a pool's three arrays of keys."""
+    return _pool(dev, kp, ks, kb, kp, ks, kb, D, GS, bits)
+
+
 def _pool(dev, kp, ks, kb, vp, vs, vb, D, GS, bits):
     """num_pages, Hkv, page and dtype of a pool's six arrays: shapes, dtypes, device and contiguity checked."""
     shape, groups, dt = kp.shape, ks.shape, ks.dtype
@@ -248,7 +259,8 @@ def _pool(dev, kp, ks, kb, vp, vs, vb, D, GS, bits):
     return pages, Hkv, page, dt
 
 
-_PACK_MAP, _PACK_APPEND, _PACK_ATTN = (struct.Struct(f"={n}q").pack for n in (15, 24, 27))
+_PACK_MAP, _PACK_APPEND, _PACK_ATTN, _PACK_LSE, _PACK_ROPE, _PACK_WEIGHTS, _PACK_EVICT = (
+    struct.Struct(f"={f}").pack for f in ("15q", "24q", "27q", "28q", "25qdq", "26qdq", "28q"))
 
 
 def qdecode_paged_map(old_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
@@ -302,10 +314,11 @@ def qdecode_paged_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, 
 def qdecode_paged_attn(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.Tensor, k_biases: torch.Tensor,
                        v_packed: torch.Tensor, v_scales: torch.Tensor, v_biases: torch.Tensor, out: torch.Tensor,
                        q_start: torch.Tensor, kv_len: torch.Tensor, block_table: torch.Tensor, max_q: int, GS: int,
-                       bits: int, causal: bool = True, stream=None) -> torch.Tensor:
+                       bits: int, causal: bool = True, stream=None, lse: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention of every sequence's new tokens over its pages: q ``[total_q, H, D]`` (rows contiguous), out the same
     shape, contiguous; ``q_start [B + 1]``, ``kv_len [B]``, ``block_table [B, max_pages]`` int32 on the GPU. ``max_q``
-    bounds the new tokens of a sequence (it only chooses the kernel). ``causal=False`` is cross attention."""
+    bounds the new tokens of a sequence (it only chooses the kernel). ``causal=False`` is cross attention. ``lse
+    [total_q, H]`` (fp32) receives the logarithm of every row's sum of exponentials."""
     shape, dev = q.shape, q.get_device()
     T, H, D = shape
     pages, Hkv, page, dt = _pool(dev, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits)
@@ -318,11 +331,15 @@ def qdecode_paged_attn(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.
     if T and qd != 1:
         raise ValueError("rows of q must be contiguous")
     _ints(dev, "q_start kv_len block_table", q_start, kv_len, block_table)
-    _paged_call(2, "qdecode_paged_attn", _PACK_ATTN, dev, stream,
-                (q.data_ptr(), qt, qh, k_packed.data_ptr(), k_scales.data_ptr(), k_biases.data_ptr(), v_packed.data_ptr(),
-                 v_scales.data_ptr(), v_biases.data_ptr(), out.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
-                 block_table.data_ptr(), T, max_q, B, H, Hkv, pages, page, max_pages, 1 if causal else 0, D, GS, bits,
-                 _DT_CODE[dt]))
+    arrays = (q.data_ptr(), qt, qh, k_packed.data_ptr(), k_scales.data_ptr(), k_biases.data_ptr(), v_packed.data_ptr(),
+              v_scales.data_ptr(), v_biases.data_ptr(), out.data_ptr())
+    rest = (q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), T, max_q, B, H, Hkv, pages, page, max_pages,
+            1 if causal else 0, D, GS, bits, _DT_CODE[dt])
+    if lse is None:
+        _paged_call(2, "qdecode_paged_attn", _PACK_ATTN, dev, stream, arrays + rest)
+    else:
+        _floats(dev, "lse", lse, (T, H))
+        _paged_call(4, "qdecode_paged_attn_lse", _PACK_LSE, dev, stream, (*arrays, lse.data_ptr(), *rest))
     return out
 
 
@@ -330,6 +347,126 @@ def qdecode_paged_attn_workspace_bytes(B: int, H: int, Hkv: int, max_q: int, D: 
     out = ctypes.c_size_t()
     st = lib().qdecode_paged_attn_workspace_bytes(B, H, Hkv, max_q, D, GS, bits, ctypes.byref(out))
     _lib.check(st, "qdecode_paged_attn_workspace_bytes")
+    return out.value
+
+
+def qdecode_rope_freqs(rot: int, base: float = 10000.0, factor: float = 1.0, context: float = 0.0, slow: float = 1.0,
+                       fast: float = 4.0, device=None) -> torch.Tensor:
+    """Radians per position of the ``rot / 2`` pairs of qdecode_rope (float64): ``base ** (-2i / rot)``, stretched by
+    ``factor``: all of them (``context`` 0), or with ``context`` the length that the model was made for, those that turn
+    ``slow`` times or less over it, none that turn ``fast`` times or more, and a blend between."""
+    out = (ctypes.c_double * max(rot // 2, 1))()
+    _lib.check(lib().qdecode_rope_freqs(rot, base, factor, context, slow, fast, out), "qdecode_rope_freqs")
+    return torch.tensor(list(out), dtype=torch.float64, device=device)
+
+
+def qdecode_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor, freqs: torch.Tensor,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 scale: float = 1.0, inverse: bool = False, q_start: Optional[torch.Tensor] = None,
+                 shift: Optional[torch.Tensor] = None, stream=None):
+    """Rotary positions: the first ``2 * freqs.numel()`` dimensions of ``q [T, H, D]`` and ``k [T, Hkv, D]`` (bf16, fp16 or
+    fp32; last dimension contiguous, other strides free; either may be None) are turned by ``positions [T]`` (int32;
+    negative: row not written) times ``freqs`` (float64, qdecode_rope_freqs) and by ``scale``, pairs half and half or
+    ``interleaved``; the rest is copied. ``q_out``, ``k_out``: where to (any strides; None: in place). ``inverse`` turns
+    back, as gradients need it. With ``q_start [B + 1]`` and ``shift [B]`` a row's position grows by its sequence's shift.
+    Returns (q_out, k_out)."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("qdecode_rope takes q, k or both")
+    dev, T, D, dt = x.get_device(), x.shape[0], x.shape[2], x.dtype
+    if dt not in _DT_CODE:
+        raise ValueError(f"q and k must be bf16, fp16 or fp32, got {dt}")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+    q_out, k_out = q if q_out is None else q_out, k if k_out is None else k_out
+    rows = []
+    for name, a, like in (("q", q, q), ("k", k, k), ("q_out", q_out, q), ("k_out", k_out, k)):
+        if a is None:
+            rows += [0, 0, 0]
+            continue
+        if not (a.dim() == 3 and a.shape[0] == T and a.shape[2] == D and a.shape == like.shape and a.dtype is dt
+                and a.get_device() == dev):
+            raise ValueError(f"{name}: expected {dt} [{T}, heads, {D}] on device {dev}, got {a.dtype} {tuple(a.shape)} on {a.device}")
+        t, h, d = a.stride()
+        if T and d != 1:
+            raise ValueError(f"rows of {name} must be contiguous")
+        rows += [a.data_ptr(), t, h]
+    if not (freqs.dtype is torch.float64 and freqs.dim() == 1 and freqs.is_contiguous() and freqs.get_device() == dev):
+        raise ValueError(f"freqs: expected contiguous float64 on device {dev}, got {freqs.dtype} on {freqs.device}")
+    if (q_start is None) != (shift is None):
+        raise ValueError("q_start and shift go together")
+    _ints(dev, "positions q_start shift", positions, q_start, shift)
+    B = 0 if shift is None else shift.numel()
+    if positions.numel() != T or (shift is not None and q_start.numel() != B + 1):
+        raise ValueError(f"{positions.numel()} positions for {T} tokens, or q_start and shift of different batches")
+    _paged_call(5, "qdecode_rope", _PACK_ROPE, dev, stream,
+                (*rows, positions.data_ptr(), freqs.data_ptr(), 0 if q_start is None else q_start.data_ptr(),
+                 0 if shift is None else shift.data_ptr(), T, B, 0 if q is None else q.shape[1], 0 if k is None else k.shape[1], D,
+                 2 * freqs.numel(), 1 if interleaved else 0, 1 if inverse else 0, _DT_CODE[dt], scale))
+    return q_out, k_out
+
+
+def qdecode_paged_weights(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.Tensor, k_biases: torch.Tensor,
+                          lse: torch.Tensor, mass: torch.Tensor, token: torch.Tensor, q_start: torch.Tensor,
+                          kv_len: torch.Tensor, block_table: torch.Tensor, max_q: int, GS: int, bits: int, window: int = 0,
+                          decay: float = 1.0, shift: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention weight drawn by every key from this step's new tokens, added to ``mass [num_pages, Hkv, page]`` (fp32) times
+    ``decay``; ``lse [total_q, H]`` (fp32) as qdecode_paged_attn left it, the other arguments as given there (causal).
+    Only the last ``window`` new tokens of a sequence count (0: all). Rows of the new tokens start from 0, and their
+    position (row of the sequence plus ``shift [B]``) goes to ``token [num_pages, Hkv, page]`` (int32)."""
+    dev = q.get_device()
+    T, H, D = q.shape
+    pages, Hkv, page, dt = _keys(dev, k_packed, k_scales, k_biases, D, GS, bits)
+    B, max_pages = block_table.shape
+    if not (q.dtype is dt and kv_len.numel() == B and q_start.numel() == B + 1 and (shift is None or shift.numel() == B)):
+        raise ValueError(f"q {tuple(q.shape)} {q.dtype}, {kv_len.numel()} lengths and {q_start.numel()} starts do not fit a {dt} "
+                         f"cache of {B} sequences")
+    qt, qh, qd = q.stride()
+    if T and qd != 1:
+        raise ValueError("rows of q must be contiguous")
+    _floats(dev, "lse", lse, (T, H))
+    _floats(dev, "mass", mass, (pages, Hkv, page))
+    _ints(dev, "token q_start kv_len block_table shift", token, q_start, kv_len, block_table, shift)
+    if token.shape != mass.shape:
+        raise ValueError(f"token: expected {tuple(mass.shape)}, got {tuple(token.shape)}")
+    _paged_call(6, "qdecode_paged_weights", _PACK_WEIGHTS, dev, stream,
+                (q.data_ptr(), qt, qh, k_packed.data_ptr(), k_scales.data_ptr(), k_biases.data_ptr(), lse.data_ptr(),
+                 mass.data_ptr(), token.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+                 0 if shift is None else shift.data_ptr(), T, max_q, window, B, H, Hkv, pages, page, max_pages, D, GS, bits,
+                 _DT_CODE[dt], decay))
+    return mass
+
+
+def qdecode_paged_evict(k_packed: torch.Tensor, k_scales: torch.Tensor, k_biases: torch.Tensor, v_packed: torch.Tensor,
+                        v_scales: torch.Tensor, v_biases: torch.Tensor, mass: torch.Tensor, token: torch.Tensor,
+                        kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, freed: torch.Tensor,
+                        n_freed: torch.Tensor, GS: int, bits: int, budget: int, limit: Optional[int] = None,
+                        sinks: int = 0, recent: int = 0, shift: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Cuts every sequence of more than ``limit`` rows (None: ``budget``) to ``budget``, each KV head by itself: rows of the
+    first ``sinks`` tokens and of the ``recent`` newest stay, then those of the largest ``mass``; the pool's rows, ``mass``
+    and ``token`` are closed up in place. Writes ``new_len [B]``, adds to ``shift [B]``, moves the pages that are no longer
+    needed from ``block_table`` to ``freed`` and their number to ``n_freed [1]`` (all int32)."""
+    dev = mass.get_device()
+    D = k_packed.shape[-1] * 32 // max(bits, 1)
+    pages, Hkv, page, _ = _pool(dev, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, D, GS, bits)
+    _floats(dev, "mass", mass, (pages, Hkv, page))
+    _ints(dev, "token kv_len new_len block_table freed n_freed shift", token, kv_len, new_len, block_table, freed, n_freed, shift)
+    B, max_pages = block_table.shape
+    if not (token.shape == mass.shape and kv_len.numel() == new_len.numel() == B and n_freed.numel() >= 1
+            and (shift is None or shift.numel() == B)):
+        raise ValueError(f"token {tuple(token.shape)}, mass {tuple(mass.shape)}, {kv_len.numel()} and {new_len.numel()} lengths do "
+                         f"not fit a table of {B} sequences")
+    _paged_call(7, "qdecode_paged_evict", _PACK_EVICT, dev, stream,
+                (k_packed.data_ptr(), k_scales.data_ptr(), k_biases.data_ptr(), v_packed.data_ptr(), v_scales.data_ptr(),
+                 v_biases.data_ptr(), mass.data_ptr(), token.data_ptr(), kv_len.data_ptr(), new_len.data_ptr(),
+                 block_table.data_ptr(), freed.data_ptr(), n_freed.data_ptr(), 0 if shift is None else shift.data_ptr(), B, Hkv,
+                 pages, page, max_pages, freed.numel(), budget, budget if limit is None else limit, sinks, recent, D, GS, bits))
+
+
+def qdecode_paged_evict_workspace_bytes(B: int, Hkv: int, page: int, max_pages: int, budget: int) -> int:
+    out = ctypes.c_size_t()
+    _lib.check(lib().qdecode_paged_evict_workspace_bytes(B, Hkv, page, max_pages, budget, ctypes.byref(out)),
+               "qdecode_paged_evict_workspace_bytes")
     return out.value
 
 
@@ -419,14 +556,18 @@ def decode_attention(q: torch.Tensor, cache: QuantizedKV, out_dtype: Optional[to
 
 class PagedKV:
     """A pool of pages in the library's layout, and the paged calls on it. Tables, lengths and the free list are the
-    caller's (int32 tensors on the GPU); ``step_tables`` allocates one step's and fills them with qdecode_paged_map."""
+    caller's (int32 tensors on the GPU); ``step_tables`` allocates one step's and fills them with qdecode_paged_map. With
+    ``track`` the pool also holds every row's drawn attention weight and token (``mass``, ``token``), for ``weigh`` and
+    ``evict``."""
 
-    def __init__(self, num_pages, Hkv, page, D, GS, bits, dtype, device="cuda"):
+    def __init__(self, num_pages, Hkv, page, D, GS, bits, dtype, device="cuda", track=False):
         self.num_pages, self.Hkv, self.page, self.D, self.GS, self.bits = num_pages, Hkv, page, D, GS, bits
         mk = lambda last, dt: torch.zeros((num_pages, Hkv, page, last), dtype=dt, device=device)  # noqa: E731
         W, NG = D * bits // 32, D // GS
         self.kp, self.ks, self.kb = mk(W, torch.int32), mk(NG, dtype), mk(NG, dtype)
         self.vp, self.vs, self.vb = mk(W, torch.int32), mk(NG, dtype), mk(NG, dtype)
+        self.mass = torch.zeros((num_pages, Hkv, page), dtype=torch.float32, device=device) if track else None
+        self.token = torch.zeros((num_pages, Hkv, page), dtype=torch.int32, device=device) if track else None
 
     @property
     def dtype(self):
@@ -447,10 +588,31 @@ class PagedKV:
     def append(self, k, v, slots, k_held=None, v_held=None, stream=None) -> None:
         qdecode_paged_append(k, v, slots, *self.arrays(), self.GS, self.bits, k_held, v_held, stream)
 
-    def attend(self, q, q_start, kv_len, block_table, max_q, causal=True, out=None, stream=None) -> torch.Tensor:
+    def attend(self, q, q_start, kv_len, block_table, max_q, causal=True, out=None, stream=None, lse=None) -> torch.Tensor:
         """Allocating wrapper of qdecode_paged_attn (rows of q behind q_start[B] leave theirs unwritten)."""
         if out is None:
             with _on(stream, q.device):
                 out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         return qdecode_paged_attn(q, *self.arrays(), out, q_start, kv_len, block_table, max_q, self.GS, self.bits, causal,
-                                  stream)
+                                  stream, lse)
+
+    def _tracked(self):
+        if self.mass is None:
+            raise ValueError("this PagedKV was made without track=True: it holds no weights and tokens")
+
+    def weigh(self, q, lse, q_start, kv_len, block_table, max_q, window=0, decay=1.0, shift=None, stream=None) -> torch.Tensor:
+        """qdecode_paged_weights on this pool: behind ``attend``, with the ``lse`` that it left."""
+        self._tracked()
+        return qdecode_paged_weights(q, self.kp, self.ks, self.kb, lse, self.mass, self.token, q_start, kv_len, block_table,
+                                     max_q, self.GS, self.bits, window, decay, shift, stream)
+
+    def evict(self, kv_len, block_table, budget, limit=None, sinks=0, recent=0, shift=None, stream=None) -> dict:
+        """new_len, freed and n_freed of an eviction (qdecode_paged_evict; block_table and shift are changed in place, entries
+        of freed behind n_freed are unset)."""
+        self._tracked()
+        mk = lambda n: torch.empty(n, dtype=torch.int32, device=block_table.device)  # noqa: E731
+        with _on(stream, block_table.device):
+            t = {"new_len": mk(block_table.shape[0]), "freed": mk(block_table.numel()), "n_freed": mk(1)}
+        qdecode_paged_evict(*self.arrays(), self.mass, self.token, kv_len, t["new_len"], block_table, t["freed"], t["n_freed"],
+                            self.GS, self.bits, budget, limit, sinks, recent, shift, stream)
+        return t

@@ -22,6 +22,8 @@ QDA_MAX_NREP = 64
 QDA_MAX_L = 8
 QDA_QGEMV_MAX_T = 4
 QDA_PAGE_MIN, QDA_PAGE_MAX = 16, 256
+QDA_ROPE_MAX_HEADS = 4096
+QDA_EVICT_MAX_HEADS = 64
 
 
 class QdaPlan(ctypes.Structure):
@@ -43,7 +45,7 @@ class QdaPlan(ctypes.Structure):
         return {k: getattr(self, k) for k, _ in self._fields_}
 
 
-_I, _P, _LL, _SZ = ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_size_t
+_I, _P, _LL, _SZ, _F64 = ctypes.c_int, ctypes.c_void_p, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_double
 _PI32 = ctypes.POINTER(ctypes.c_int32)
 
 SIGNATURES = {
@@ -65,6 +67,12 @@ SIGNATURES = {
     "qdecode_paged_map": (_I, [_P] * 9 + [_I] * 5 + [_P]),
     "qdecode_paged_append": (_I, [_P, _P, _LL, _LL, _LL, _LL] + [_P] * 9 + [_I] * 8 + [_P]),
     "qdecode_paged_attn": (_I, [_P, _LL, _LL] + [_P] * 10 + [_I] * 13 + [_P]),
+    "qdecode_paged_attn_lse": (_I, [_P, _LL, _LL] + [_P] * 11 + [_I] * 13 + [_P]),
+    "qdecode_rope": (_I, [_P, _LL, _LL] * 4 + [_P] * 4 + [_I] * 9 + [_F64, _P]),
+    "qdecode_rope_freqs": (_I, [_I] + [_F64] * 5 + [ctypes.POINTER(_F64)]),
+    "qdecode_paged_weights": (_I, [_P, _LL, _LL] + [_P] * 10 + [_I] * 13 + [_F64, _P]),
+    "qdecode_paged_evict": (_I, [_P] * 14 + [_I] * 13 + [_P]),
+    "qdecode_paged_evict_workspace_bytes": (_I, [_I] * 5 + [ctypes.POINTER(_SZ)]),
     "qdecode_paged_packed": (_I, [_I, ctypes.c_char_p]),
     "qdecode_paged_attn_workspace_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_SZ)]),
     "qdecode_attn_strerror": (ctypes.c_char_p, [_I]),

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "qda_paged_check.h"
 #include "qda_paged_sched.cuh"
 
 namespace qda {
@@ -33,17 +34,6 @@ __device__ __forceinline__ longlong2 block_scan2(longlong2 v, longlong2* tot) {
     v.y += tot[w].y;
   }
   return v;
-}
-
-// Largest b < n with first[b] <= x (first ascending, first[0] <= x).
-template <typename T>
-__device__ __forceinline__ int seq_of(const T* first, int n, T x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= x) lo = mid; else hi = mid;
-  }
-  return lo;
 }
 
 // Every CTA scans the B lengths for itself (at most QDA_MAX_B values, all in L2) and then writes its share of the
@@ -100,7 +90,7 @@ __global__ void __launch_bounds__(kMapThreads)
   // the new pages, in the order of sequences and columns
   const int pages = s_take[B];
   for (long long i = first; i < pages; i += step) {
-    const int b = seq_of(s_take, B, (int)i);
+    const int b = qda_seq_of(s_take, B, (int)i);
     const long long col = (((long long)s_old[b] + pmask) >> page_shift) + (i - s_take[b]);
     if (col >= max_pages) {
       bad = true;
@@ -115,7 +105,7 @@ __global__ void __launch_bounds__(kMapThreads)
   for (long long t = first; t < max_tokens; t += step) {
     int slot = -1, pos = -1;
     if (t < total) {
-      const int b = seq_of(s_start, B, (int)t);
+      const int b = qda_seq_of(s_start, B, (int)t);
       const int ob = s_old[b];
       const long long at = (long long)ob + (t - s_start[b]);
       const long long col = at >> page_shift, old_cols = ((long long)ob + pmask) >> page_shift;
@@ -415,6 +405,8 @@ __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_const
 #pragma unroll
   for (int e = 0; e < E; ++e)
     dst[e * 32 + lane] = p.f16 ? to_bits16x2<true>(o[e].x * inv, o[e].y * inv) : to_bits16x2<false>(o[e].x * inv, o[e].y * inv);
+  if (lane == 0 && t.unit % p.parts == 0 && p.lse != nullptr)
+    qda_put_lse(p, t.token0 + tok, (t.unit / p.parts) * p.nrep + (row - tok * p.nrep), m, l, p.lse_unit);
 }
 
 template <int D>
@@ -680,7 +672,7 @@ __device__ void far_rows(const QdaPagedParams& p, FarShared& sh, int b, int kvh,
   far_reduce(sh, l, [](float x, float y) { return x + y; });
 #pragma unroll 1
   for (int r = 0; r < kFarRows; ++r) {
-    float mine[2] = {0.f, 0.f}, sum = 0.f;
+    float mine[2] = {0.f, 0.f}, sum = 0.f, ref = 0.f;
     int t = 0, h = 0, see = 0;
 #pragma unroll
     for (int k = 0; k < kFarRows; ++k)   // (registers have no index)
@@ -688,6 +680,7 @@ __device__ void far_rows(const QdaPagedParams& p, FarShared& sh, int b, int kvh,
         mine[0] = o[0][k];
         mine[1] = o[1][k];
         sum = l[k];
+        ref = m[k];
         t = tokens[k];
         h = heads[k];
         see = seen[k];
@@ -697,6 +690,7 @@ __device__ void far_rows(const QdaPagedParams& p, FarShared& sh, int b, int kvh,
     __syncthreads();
     if (part != 0 || see == 0) continue;
     for (int i = 1; i < parts; ++i) mine[0] += sh.o[tid + i * p.D];
+    if (tid == 0 && p.lse != nullptr) qda_put_lse(p, t, h, ref, sum, 0.f);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     uint16_t* out = p.out + ((long long)t * p.H + h) * p.D;
 #pragma unroll
@@ -738,7 +732,7 @@ __global__ void __launch_bounds__(kFarThreads) qda_paged_far_kernel(const __grid
   for (long long i0 = blockIdx.x; i0 < items; i0 += (long long)gridDim.x * kFarWarps) {
     auto unit = [&](long long item, int* b, int* kvh, int* j) {
       const long long u = item % units;
-      *b = seq_of(sh.first, p.B, u);
+      *b = qda_seq_of(sh.first, p.B, u);
       const PagedSeq s = paged_seq(p, *b, 128);
       const int blocks = far_blocks(p, s, j);
       const long long i = u - sh.first[*b];
@@ -811,30 +805,6 @@ cudaError_t launch_far(const QdaPagedParams& p, int bits, int sms, cudaStream_t 
                    : cudaLaunchKernelEx(&cfg, qda_paged_far_kernel<8>, p);
 }
 
-bool good_page(int page) { return page >= QDA_PAGE_MIN && page <= QDA_PAGE_MAX && (page & (page - 1)) == 0; }
-
-int page_shift_of(int page) {
-  int s = 0;
-  while ((1 << s) < page) ++s;
-  return s;
-}
-
-// bits, GS and D of every paged call: the quantizer's
-int check_codec(int D, int GS, int bits) {
-  if (D < 1 || GS < 1) return QDA_ERR_INVALID;
-  if (bits != 4 && bits != 8) return QDA_ERR_UNSUPPORTED;
-  if (GS != 32 && GS != 64 && GS != 128) return QDA_ERR_UNSUPPORTED;
-  if (D != 64 && D != 128 && D != 256 && D != 512) return QDA_ERR_UNSUPPORTED;
-  if (D % GS != 0) return QDA_ERR_UNSUPPORTED;
-  return QDA_OK;
-}
-
-int check_pool(int num_pages, int page) {
-  if (num_pages < 1 || page < 1) return QDA_ERR_INVALID;
-  if (!good_page(page) || (long long)num_pages * page > 0x7fffffffLL) return QDA_ERR_UNSUPPORTED;
-  return QDA_OK;
-}
-
 // The kernel a call takes, from what the host knows: the shape and the bound on a sequence's new tokens.
 struct PagedPlan {
   bool chunk;              // the chunk kernel (else the split kernel)
@@ -901,9 +871,6 @@ int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int
   plan->bytes = plan->o_bytes + plan->ml_bytes + plan->ctas * sizeof(QdaPagedSplitTile);
   return QDA_OK;
 }
-
-bool off16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-bool off4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 }  // namespace qda
 
@@ -1022,13 +989,14 @@ extern "C" int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max
   return QDA_OK;
 }
 
-extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
-                                  const void* k_scales, const void* k_biases, const uint32_t* v_packed,
-                                  const void* v_scales, const void* v_biases, void* out, const int32_t* q_start,
-                                  const int32_t* kv_len, const int32_t* block_table, int total_q, int max_q, int B,
-                                  int H, int Hkv, int num_pages, int page, int max_pages, int causal, int D, int GS,
-                                  int bits, int dtype, void* stream) {
-  using namespace qda;
+namespace qda {
+
+// Both attention calls; lse == nullptr: not asked for.
+static int paged_attn(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
+                      const void* k_scales, const void* k_biases, const uint32_t* v_packed, const void* v_scales,
+                      const void* v_biases, void* out, float* lse, const int32_t* q_start, const int32_t* kv_len,
+                      const int32_t* block_table, int total_q, int max_q, int B, int H, int Hkv, int num_pages, int page,
+                      int max_pages, int causal, int D, int GS, int bits, int dtype, void* stream) {
   if (!k_packed || !k_scales || !k_biases || !v_packed || !v_scales || !v_biases || !q_start || !kv_len ||
       !block_table)
     return QDA_ERR_INVALID;
@@ -1044,7 +1012,7 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   const void* ptrs[8] = {q, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, out};
   for (const void* p : ptrs)
     if (off16(p)) return QDA_ERR_ALIGN;
-  if (off4(q_start) || off4(kv_len) || off4(block_table) || q_tstride % 8 || q_hstride % 8) return QDA_ERR_ALIGN;
+  if (off4(lse) || off4(q_start) || off4(kv_len) || off4(block_table) || q_tstride % 8 || q_hstride % 8) return QDA_ERR_ALIGN;
   if (total_q == 0) return QDA_OK;
   // a row of q may be read after its output is written: by the other part of its values (D = 512), or to be done anew
   long long lo = 0, hi = D;
@@ -1067,6 +1035,7 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   p.vs = static_cast<const uint16_t*>(v_scales);
   p.vb = static_cast<const uint16_t*>(v_biases);
   p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
   p.q_start = q_start;
   p.kv_len = kv_len;
   p.table = block_table;
@@ -1096,6 +1065,7 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + plan.o_bytes);
   p.split = reinterpret_cast<QdaPagedSplitTile*>(static_cast<char*>(ws) + plan.o_bytes + plan.ml_bytes);
+  p.lse_unit = plan.chunk ? kPcWeightBits : 0.f;
   p.ctas = plan.ctas;
   p.parts = plan.parts;
   p.units = Hkv * plan.parts;
@@ -1111,23 +1081,72 @@ extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long 
   return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
 }
 
+}  // namespace qda
+
+extern "C" int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
+                                  const void* k_scales, const void* k_biases, const uint32_t* v_packed,
+                                  const void* v_scales, const void* v_biases, void* out, const int32_t* q_start,
+                                  const int32_t* kv_len, const int32_t* block_table, int total_q, int max_q, int B,
+                                  int H, int Hkv, int num_pages, int page, int max_pages, int causal, int D, int GS,
+                                  int bits, int dtype, void* stream) {
+  return qda::paged_attn(q, q_tstride, q_hstride, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, out, nullptr,
+                         q_start, kv_len, block_table, total_q, max_q, B, H, Hkv, num_pages, page, max_pages, causal, D, GS,
+                         bits, dtype, stream);
+}
+
+extern "C" int qdecode_paged_attn_lse(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
+                                      const void* k_scales, const void* k_biases, const uint32_t* v_packed,
+                                      const void* v_scales, const void* v_biases, void* out, float* lse,
+                                      const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table,
+                                      int total_q, int max_q, int B, int H, int Hkv, int num_pages, int page,
+                                      int max_pages, int causal, int D, int GS, int bits, int dtype, void* stream) {
+  if (total_q > 0 && lse == nullptr) return QDA_ERR_INVALID;
+  return qda::paged_attn(q, q_tstride, q_hstride, k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, out, lse,
+                         q_start, kv_len, block_table, total_q, max_q, B, H, Hkv, num_pages, page, max_pages, causal, D, GS,
+                         bits, dtype, stream);
+}
+
 extern "C" int qdecode_paged_packed(int op, const int64_t* args) {
-  static const int counts[3] = {15, 24, 27}, first_int[3] = {9, 15, 13};   // arguments; the first of the 32-bit ones
-  if (args == nullptr || op < 0 || op > 2) return QDA_ERR_INVALID;
-  int64_t a[27];
+  // per op: arguments; the first of the 32-bit ones; those behind them (a double, the stream)
+  static const int counts[8] = {15, 24, 27, 0, 28, 27, 28, 28}, first_int[8] = {9, 15, 13, 0, 14, 16, 13, 14};
+  static const int behind[8] = {1, 1, 1, 0, 1, 2, 2, 1};
+  if (args == nullptr || op < 0 || op > 7 || counts[op] == 0) return QDA_ERR_INVALID;
+  int64_t a[28];
   std::memcpy(a, args, sizeof(int64_t) * counts[op]);   // args may have any alignment
-  for (int i = first_int[op]; i < counts[op] - 1; ++i)
+  for (int i = first_int[op]; i < counts[op] - behind[op]; ++i)
     if (a[i] < INT32_MIN || a[i] > INT32_MAX) return QDA_ERR_INVALID;
   auto ptr = [&](int i) { return reinterpret_cast<void*>(static_cast<intptr_t>(a[i])); };
   auto i32 = [&](int i) { return static_cast<int32_t*>(ptr(i)); };
   auto u32 = [&](int i) { return static_cast<uint32_t*>(ptr(i)); };
+  auto f32 = [&](int i) { return static_cast<float*>(ptr(i)); };
   auto n = [&](int i) { return static_cast<int>(a[i]); };
+  auto real = [&](int i) {
+    double x;
+    std::memcpy(&x, &a[i], sizeof(x));
+    return x;
+  };
   if (op == 0)
     return qdecode_paged_map(i32(0), i32(1), i32(2), i32(3), i32(4), i32(5), i32(6), i32(7), i32(8), n(9), n(10), n(11),
                              n(12), n(13), ptr(14));
   if (op == 1)
     return qdecode_paged_append(ptr(0), ptr(1), a[2], a[3], a[4], a[5], i32(6), u32(7), ptr(8), ptr(9), u32(10), ptr(11),
                                 ptr(12), ptr(13), ptr(14), n(15), n(16), n(17), n(18), n(19), n(20), n(21), n(22), ptr(23));
+  if (op == 4)
+    return qdecode_paged_attn_lse(ptr(0), a[1], a[2], u32(3), ptr(4), ptr(5), u32(6), ptr(7), ptr(8), ptr(9), f32(10), i32(11),
+                                  i32(12), i32(13), n(14), n(15), n(16), n(17), n(18), n(19), n(20), n(21), n(22), n(23),
+                                  n(24), n(25), n(26), ptr(27));
+  if (op == 5)
+    return qdecode_rope(ptr(0), a[1], a[2], ptr(3), a[4], a[5], ptr(6), a[7], a[8], ptr(9), a[10], a[11], i32(12),
+                        static_cast<const double*>(ptr(13)), i32(14), i32(15), n(16), n(17), n(18), n(19), n(20), n(21),
+                        n(22), n(23), n(24), real(25), ptr(26));
+  if (op == 6)
+    return qdecode_paged_weights(ptr(0), a[1], a[2], u32(3), ptr(4), ptr(5), f32(6), f32(7), i32(8), i32(9), i32(10), i32(11),
+                                 i32(12), n(13), n(14), n(15), n(16), n(17), n(18), n(19), n(20), n(21), n(22), n(23), n(24),
+                                 n(25), real(26), ptr(27));
+  if (op == 7)
+    return qdecode_paged_evict(u32(0), ptr(1), ptr(2), u32(3), ptr(4), ptr(5), f32(6), i32(7), i32(8), i32(9), i32(10), i32(11),
+                               i32(12), i32(13), n(14), n(15), n(16), n(17), n(18), n(19), n(20), n(21), n(22), n(23), n(24),
+                               n(25), n(26), ptr(27));
   return qdecode_paged_attn(ptr(0), a[1], a[2], u32(3), ptr(4), ptr(5), u32(6), ptr(7), ptr(8), ptr(9), i32(10), i32(11),
                             i32(12), n(13), n(14), n(15), n(16), n(17), n(18), n(19), n(20), n(21), n(22), n(23), n(24),
                             n(25), ptr(26));

@@ -13,6 +13,9 @@ struct QdaPagedSplitTile {
   int first_filled, last_filled;
 };
 
+// log2 of the factor on the chunk kernel's weights, and so on their sums.
+constexpr float kPcWeightBits = 7.f;
+
 // Launch parameters of the paged attention kernels (passed by value as a __grid_constant__).
 struct QdaPagedParams {
   const uint16_t* q;          // row t, head h at t * q_tstride + h * q_hstride
@@ -23,6 +26,8 @@ struct QdaPagedParams {
   const uint16_t* vs;
   const uint16_t* vb;
   uint16_t* out;              // [total_q, H, D]
+  float* lse;                 // [total_q, H] log of the sum of a row's exponentials, or nullptr
+  float lse_unit;             // log2 of the factor that the sums of weights of split tiles carry
   const int* q_start;         // [B + 1]
   const int* kv_len;          // [B]
   const int* table;           // [B, max_pages]
@@ -40,6 +45,24 @@ struct QdaPagedParams {
   int stall_block;            // testing aid: the chunk kernel's first CTA gets no pages for this block of its own (-1: for all)
 #endif
 };
+
+// Log of the sum of exponentials of a row, from its reference (log2 units) and its sum of weights, which carries the factor
+// 2^unit. A row that sees no key: -inf.
+__device__ __forceinline__ void qda_put_lse(const QdaPagedParams& p, int token, int head, float m, float l,
+                                            float unit) {
+  p.lse[(long long)token * p.H + head] = l == 0.f ? -INFINITY : (m - unit + log2f(l)) * 0.693147180559945309f;
+}
+
+// Largest b < n with first[b] <= x (first ascending, first[0] <= x).
+template <typename T>
+__device__ __forceinline__ int qda_seq_of(const T* first, int n, T x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
 
 // Row of the pool arrays that holds row `r` of page `pg` of KV head `kvh`.
 __host__ __device__ inline long long qda_pool_row(int pg, int kvh, int r, int Hkv, int page_shift) {

@@ -561,7 +561,7 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         if (rise) rescale(top);
         // weights times 2^7: up to 2^15, so that those far below the reference keep their bits longer, 11 of them down to
         // 2^-21 (the sum has the same factor)
-        const float mm = m == -INFINITY ? 0.f : 7.f - m;
+        const float mm = m == -INFINITY ? 0.f : kPcWeightBits - m;
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         auto weigh = [&](const float (&x)[32], int c) {
           uint32_t w[16];
@@ -650,6 +650,8 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         }
       }
       if (real && !whole && half == 0) p.part_ml[slot] = make_float2(m, l);
+      if (real && whole && half == 0 && t->part == 0 && p.lse != nullptr)
+        qda_put_lse(p, t->s.first + tok, t->kvh * p.nrep + (r - tok * p.nrep), m, l, kPcWeightBits);
       tc_fence_before();
       bc += n;
       tc += n > 0;

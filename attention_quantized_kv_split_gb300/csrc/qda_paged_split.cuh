@@ -743,6 +743,8 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             else *reinterpret_cast<float2*>(po + d + 2 * lane) = v;
           }
           if (!whole && lane == 0) p.part_ml[(size_t)slot * MT + r] = make_float2(M, L);
+          if (whole && lane == 0 && p.lse != nullptr)
+            qda_put_lse(p, t.s.first + tok, t.unit * p.nrep + (row0 + r - tok * p.nrep), M, L, 0.f);
         }
       }
       if (saw_absent && lane == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);

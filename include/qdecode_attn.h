@@ -350,10 +350,107 @@ int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, 
 int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max_q, int D, int GS, int bits, size_t* bytes);
 
 /*
+ * qdecode_paged_attn_lse: qdecode_paged_attn that also leaves lse [total_q, H] (fp32, contiguous), the natural logarithm of
+ * sum_n exp(q[t, h, :] . k_hat[n] / sqrt(D)) over the keys that the token sees, with the roundings of the kernel that the
+ * call takes; -inf where it sees none. Rows at and behind q_start[B] stay as they are. out is the same, bit for bit. Same
+ * workspace, errors and limits; lse must not overlap q or out.
+ */
+int qdecode_paged_attn_lse(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
+                           const void* k_scales, const void* k_biases, const uint32_t* v_packed, const void* v_scales,
+                           const void* v_biases, void* out, float* lse, const int32_t* q_start, const int32_t* kv_len,
+                           const int32_t* block_table, int total_q, int max_q, int B, int H, int Hkv, int num_pages,
+                           int page, int max_pages, int causal, int D, int GS, int bits, int dtype, void* stream);
+
+/*
+ * A cache that forgets. Each row of the paged cache, under each KV head for itself, carries the attention weight that its
+ * key has drawn and the position of its token:
+ *     mass   [num_pages, Hkv, page]  fp32
+ *     token  [num_pages, Hkv, page]  int32
+ * A step is qdecode_paged_map, qdecode_rope, qdecode_paged_append, qdecode_paged_attn_lse, qdecode_paged_weights and, when
+ * sequences have grown too long, qdecode_paged_evict, whose new_len is the next step's old_len. Since rows leave, a
+ * sequence's next token no longer stands at the position kv_len: shift [B] (int32) holds the rows that it has lost so far,
+ * evict adds to it, and rope and weights add it to positions. No page may belong to two sequences.
+ */
+
+/*
+ * qdecode_rope: rotary positions. The first rot of D dimensions of every row of q [T, H, D] and k [T, Hkv, D] are turned by
+ * the token's position n = positions[t] (plus shift[b] of the sequence b that holds row t by q_start [B + 1]; both or
+ * neither may be NULL): pair i, which is (x[i], x[i + rot / 2]), with interleaved != 0 (x[2i], x[2i + 1]), becomes
+ *     scale * (a cos(n f_i) - b sin(n f_i),  b cos(n f_i) + a sin(n f_i)),   f_i = freqs[i] radians per position
+ * (freqs [rot / 2], double, device). With inverse != 0 it turns the other way: the gradient of the inputs from that of the
+ * outputs. The dimensions from rot on are copied. Rows whose position is negative (qdecode_paged_map's behind the last
+ * token) are not written. Angles are right to 2^-24 of a turn at every position; the arithmetic is fp32, rounded once.
+ *
+ * Rows are contiguous, the other strides (in elements) free; an output is its input (same pointer and strides, done in
+ * place) or apart from it, and apart from the other tensor's rows, else QDA_ERR_INVALID. Views of one buffer that holds a
+ * token after the other (a fused projection) count row by row. Heads and tokens of an output stand D or more elements apart.
+ * H or Hkv may be 0 (that tensor's pointers are then not used). dtype: bf16, fp16 or fp32, of inputs and outputs. D as for
+ * qdecode_attn, rot even and at most D, H + Hkv <= QDA_ROPE_MAX_HEADS, T <= 2^31 - 4096. Data pointers 16-byte aligned,
+ * strides multiples of 16 bytes. Asynchronous on stream, no workspace.
+ */
+#define QDA_ROPE_MAX_HEADS 4096
+int qdecode_rope(const void* q, long long q_tstride, long long q_hstride, const void* k, long long k_tstride,
+                 long long k_hstride, void* q_out, long long qo_tstride, long long qo_hstride, void* k_out,
+                 long long ko_tstride, long long ko_hstride, const int32_t* positions, const double* freqs,
+                 const int32_t* q_start, const int32_t* shift, int T, int B, int H, int Hkv, int D, int rot,
+                 int interleaved, int inverse, int dtype, double scale, void* stream);
+
+/*
+ * qdecode_rope_freqs (host only): freqs[i] = f_i = base^(-2i / rot), i < rot / 2, for a context stretched by `factor`: with
+ * context == 0 every f_i is divided by it; with context > 0, the context length that the model was made for, pairs that turn
+ * `fast` times or more over it stay, those that turn `slow` times or less are divided, and those between are blended
+ * linearly in their number of turns. factor = 1 is no stretching. Needs 0 <= slow < fast where context > 0.
+ */
+int qdecode_rope_freqs(int rot, double base, double factor, double context, double slow, double fast, double* freqs);
+
+/*
+ * qdecode_paged_weights: adds the attention weight that each key draws from this step's new tokens (q, q_start, kv_len,
+ * block_table as for qdecode_paged_attn, causal), given the row sums lse [total_q, H] of qdecode_paged_attn_lse:
+ *     mass[j, kvh] = decay * mass[j, kvh] + sum_t sum_h exp(q[t, h, :] . k_hat[j] / sqrt(D) - lse[t, h])
+ * over the sequence's last `window` new tokens (0: all of them) that see key j and the query heads h of KV head kvh. Keys of
+ * the new tokens themselves start from 0, whatever mass holds there, and their token becomes their position, j + shift[b]
+ * (shift may be NULL: 0). Sequences without new tokens, and rows behind kv_len, stay as they are. max_q bounds the new
+ * tokens of a sequence and only chooses the kernel. Scores are right to fp32 (queries below 2^-39 of their row's largest
+ * aside); sums are fp32 in a fixed order: the same bits on every run. Scales and biases as for the attention: a key that is
+ * not finite gives its own mass alone. Same types, limits and checks as qdecode_paged_attn; no workspace.
+ */
+int qdecode_paged_weights(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
+                          const void* k_scales, const void* k_biases, const float* lse, float* mass, int32_t* token,
+                          const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, const int32_t* shift,
+                          int total_q, int max_q, int window, int B, int H, int Hkv, int num_pages, int page,
+                          int max_pages, int D, int GS, int bits, int dtype, double decay, void* stream);
+
+/*
+ * qdecode_paged_evict: cuts every sequence of more than `limit` rows to `budget` rows (1 <= budget <= limit), each KV head
+ * by itself. What stays: rows whose token is below `sinks` or one of the `recent` newest positions (those from
+ * kv_len[b] + shift[b] - recent on), then those of the largest mass; of equal ones the lowest rows. (A mass that is no number ranks below
+ * all.) Needs sinks + recent <= budget. Rows that stay and lie at budget or behind move to the places of rows that go, both
+ * in ascending order; the others stay where they are, so a step that cuts one row moves at most one row per head. Order in
+ * the cache means nothing to the attention; mass and token move along. Codes, scales and biases move bit for bit.
+ *
+ * Writes new_len[b] = budget, or kv_len[b] where nothing is cut (new_len must not be kv_len), adds what was cut to shift[b]
+ * (may be NULL: then it reads as 0), and takes the pages behind the budget out of block_table (-1) into freed[max_freed],
+ * sequences in order; n_freed[0] counts them all, above max_freed some found no place (status bit 8). A length that is
+ * negative or beyond the table leaves its sequence as it is and sets bit 8; so does a page outside the pool, of which no row
+ * is read or written. Contents of rows from budget on are unspecified. D, GS, bits, pages and B as for the other paged
+ * calls, Hkv <= QDA_EVICT_MAX_HEADS, max_pages * page below 2^31 - 512. Uses the workspace as qdecode_attn does, of
+ * qdecode_paged_evict_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
+ */
+#define QDA_EVICT_MAX_HEADS 64
+int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_biases, uint32_t* v_packed, void* v_scales,
+                        void* v_biases, float* mass, int32_t* token, const int32_t* kv_len, int32_t* new_len,
+                        int32_t* block_table, int32_t* freed, int32_t* n_freed, int32_t* shift, int B, int Hkv,
+                        int num_pages, int page, int max_pages, int max_freed, int budget, int limit, int sinks,
+                        int recent, int D, int GS, int bits, void* stream);
+
+/* Workspace in bytes that qdecode_paged_evict needs for these arguments, whatever the lengths. */
+int qdecode_paged_evict_workspace_bytes(int B, int Hkv, int page, int max_pages, int budget, size_t* bytes);
+
+/*
  * qdecode_paged_packed: the calls above for bindings whose foreign calls cost by the argument: op 0 = qdecode_paged_map, 1 =
- * qdecode_paged_append, 2 = qdecode_paged_attn; args holds that call's arguments in order, each widened to 64 bits
- * (pointers as integers, the stream last). QDA_ERR_INVALID for another op, null args or a value beyond its parameter's
- * range.
+ * qdecode_paged_append, 2 = qdecode_paged_attn, 4 = qdecode_paged_attn_lse, 5 = qdecode_rope, 6 = qdecode_paged_weights, 7 =
+ * qdecode_paged_evict; args holds that call's arguments in order, each widened to 64 bits (pointers as integers, doubles as
+ * they are, the stream last). QDA_ERR_INVALID for another op, null args or a value beyond its parameter's range.
  */
 int qdecode_paged_packed(int op, const int64_t* args);
 

@@ -1,0 +1,193 @@
+"""Accumulated attention weight, and the row sums that it needs, against the definition in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attention_quantized_kv_split_gb300 as qda
+
+import forget_ref as R
+from paged_ref import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def clean_status():
+    qda.qdecode_attn_device_status()
+    yield
+    assert qda.qdecode_attn_device_status() == 0
+
+
+def side(c, seed=0):
+    """mass and token as an earlier owner of the pages left them, NaN where no row of these sequences is."""
+    rng = np.random.default_rng(seed)
+    shape = tuple(c.arrays[1].shape[:3])
+    mass = np.full(shape, np.nan, dtype=np.float32)
+    table = c.table.cpu().numpy()
+    for b, (L, n) in enumerate(zip(c.q_lens, c.kv_lens)):
+        key = np.arange(n - L if n > L else 0)
+        mass[table[b][key // c.page], :, key % c.page] = rng.random((len(key), c.Hkv))
+    return mass, rng.integers(-5, 5, shape).astype(np.int32)
+
+
+def run(c, lse, mass, token, window=0, decay=1.0, shift=None, max_q=None, q=None, stream=None):
+    m, t = torch.from_numpy(mass).cuda(), torch.from_numpy(token).cuda()
+    sh = None if shift is None else torch.tensor(shift, dtype=torch.int32, device="cuda")
+    qda.qdecode_paged_weights(c.q if q is None else q, *c.arrays[:3], lse, m, t, c.q_start, c.kv_len, c.table,
+                              max_q or max(max(c.q_lens), 1), c.GS, c.bits, window, decay, sh, stream)
+    torch.cuda.synchronize()
+    return m.cpu().numpy(), t.cpu().numpy()
+
+
+def log_sums(c):
+    return torch.from_numpy(R.log_sums(c).astype(np.float32)).cuda()
+
+
+def check(c, window=0, decay=1.0, shift=None, max_q=None, seed=0):
+    lse, (mass, token) = log_sums(c), side(c, seed)
+    got, tok = run(c, lse, mass, token, window, decay, shift, max_q)
+    ref, want, tol = R.weights(c, lse.cpu().numpy(), mass, token, window, decay, shift)
+    np.testing.assert_array_equal(tok, want)
+    np.testing.assert_array_equal(np.isnan(got), np.isnan(ref))   # rows of nobody are left as they were
+    ok = ~np.isnan(ref)
+    err = np.abs(got[ok] - ref[ok])
+    assert (err <= tol[ok]).all(), f"worst {np.max(err / np.maximum(tol[ok], 1e-300))} of the tolerance"
+
+
+@pytest.mark.parametrize("q_lens,kv_lens", [([1], [1]), ([1, 1, 1], [33, 1, 300]), ([3], [40]), ([17, 1, 0, 5], [64, 2, 9, 129]),
+                                            ([70, 33], [70, 500])])
+@pytest.mark.parametrize("D,bits,GS,dtype,page", [
+    (64, 4, 32, "bf16", 16), (64, 8, 64, "fp16", 32), (128, 4, 64, "bf16", 64), (128, 8, 128, "fp16", 16), (128, 4, 32, "fp16", 256),
+    (256, 8, 32, "bf16", 16), (256, 4, 128, "bf16", 32), (512, 4, 128, "fp16", 32), (512, 8, 32, "bf16", 64),
+])
+def test_against_the_definition(q_lens, kv_lens, D, bits, GS, dtype, page):
+    check(Case(q_lens, kv_lens, 6, 2, D, bits, GS, dtype, page, seed=D + bits), decay=0.75, shift=list(range(len(q_lens))))
+
+
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (2, 1), (16, 2), (5, 5), (64, 1)])
+@pytest.mark.parametrize("L", [1, 2, 9])
+def test_heads(H, Hkv, L):
+    check(Case([L, 2 * L], [100, 77], H, Hkv, 128, 4, 64, "bf16", 16, seed=H + L))
+
+
+@pytest.mark.parametrize("window", [1, 3, 64, 1000])
+def test_window(window):
+    check(Case([100, 2, 1], [333, 2, 50], 4, 2, 64, 8, 32, "fp16", 16, seed=window), window, 0.5)
+
+
+@pytest.mark.parametrize("max_q", [1, 100])
+def test_the_bound_only_chooses_the_kernel(max_q):
+    check(Case([1, 13], [90, 200], 4, 2, 128, 4, 32, "bf16", 32, seed=3), max_q=max_q)
+
+
+def test_long_sequence_among_short_ones():
+    check(Case([1, 4, 1, 0, 200], [9000, 5, 1, 40, 5000], 8, 2, 128, 4, 64, "bf16", 64, seed=11), window=9)
+
+
+def test_more_new_tokens_than_keys_sees_nothing():
+    """Lengths that lie (more new tokens than keys): the tokens before the first key see nothing and count nothing."""
+    check(Case([5], [3], 2, 1, 64, 4, 32, "bf16", 16, seed=1))
+
+
+def test_keys_that_are_not_seen_reach_nothing():
+    """NaN scales in rows behind the sequence, and in keys that come after a counted token: only such a key's own later
+    weights are NaN."""
+    c = Case([4], [37], 4, 2, 128, 4, 64, "bf16", 16, seed=6)   # rows behind 37 hold NaN scales
+    lse, (mass, token) = log_sums(c), side(c)
+    want, _ = run(c, lse, mass, token)
+    pg = int(c.table[0, 36 // 16])
+    c.arrays[1][pg, :, 36 % 16] = float("nan")                  # the last token's key
+    got, _ = run(c, lse, mass, token)
+    assert np.isnan(got[pg, :, 36 % 16]).all()
+    got[pg, :, 36 % 16] = want[pg, :, 36 % 16]
+    np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("power", [20, -60, None])
+def test_ranges_of_queries(power):
+    """Queries beyond fp16's range and far below it, with keys that bring the scores back; and zeros."""
+    c = Case([3], [50], 2, 1, 128, 8, 64, "bf16", 16, seed=2)
+    f = 0.0 if power is None else 2.0 ** power
+    c.q = (c.q.double() * f).to(torch.bfloat16)
+    c.q64 = c.q.double().cpu().numpy()
+    if power is not None:
+        c.arrays[1] /= f
+        c.arrays[2] /= f
+        c.K = [k / f for k in c.K]
+    check(c)
+
+
+def test_strides_streams_graphs_and_repeats():
+    c = Case([2, 1, 7], [130, 65, 300], 8, 2, 128, 4, 64, "bf16", 32, seed=8)
+    lse, (mass, token) = log_sums(c), side(c)
+    want, tok = run(c, lse, mass, token, 4, 0.5)
+    wide = torch.zeros(c.total, 20, 128, dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:18:2] = c.q
+    again, _ = run(c, lse, mass, token, 4, 0.5, q=wide[:, 2:18:2])
+    np.testing.assert_array_equal(again, want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other, _ = run(c, lse, mass, token, 4, 0.5, stream=s)
+    np.testing.assert_array_equal(other, want)
+    m, t = torch.from_numpy(mass).cuda(), torch.from_numpy(token).cuda()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qda.qdecode_paged_weights(c.q, *c.arrays[:3], lse, m, t, c.q_start, c.kv_len, c.table, 7, 64, 4, 4, 0.5)
+    m.copy_(torch.from_numpy(mass))
+    g.replay()
+    np.testing.assert_array_equal(m.cpu().numpy(), want)
+    np.testing.assert_array_equal(t.cpu().numpy(), tok)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 1], [700, 3]), ([4, 1, 0], [300, 1, 5]), ([200, 33], [1300, 33]), ([300], [300])])
+@pytest.mark.parametrize("H,Hkv,D,bits,GS,dtype", [(8, 2, 128, 4, 64, "bf16"), (4, 4, 64, 8, 32, "fp16"), (4, 2, 256, 8, 64, "bf16"),
+                                                   (16, 2, 512, 4, 128, "fp16")])
+def test_log_sums_of_the_attention(H, Hkv, D, bits, GS, dtype, q_lens, kv_lens, causal):
+    """lse against 64 bits: a score moves by ds (keys of 11 significant bits, as for the attention itself), queries are exact,
+    the sum and its logarithm add 2^-17 and 2^-22 of the logarithm; the outputs are those of the call without lse."""
+    c = Case(q_lens, kv_lens, H, Hkv, D, bits, GS, dtype, 16, seed=D, pad_rows=3)
+    lse = torch.full((c.total + 3, H), 7.0, device="cuda")
+    out = torch.full(c.q.shape, 7.0, dtype=c.q.dtype, device="cuda")
+    qda.qdecode_paged_attn(c.q, *c.arrays, out, c.q_start, c.kv_len, c.table, max(q_lens), GS, bits, causal, lse=lse)
+    assert torch.equal(out, c.run(causal))
+    got = lse.cpu().numpy().astype(np.float64)
+    assert (got[c.total:] == 7).all()
+    for b, (L, n) in enumerate(zip(q_lens, kv_lens)):
+        for h in range(H if L else 0):
+            s, _, seen = R.scores(c, b, h)
+            if not causal:
+                seen = np.ones_like(seen)
+            s = np.where(seen, s, -np.inf)
+            ref = s.max(1) + np.log(np.exp(s - s.max(1, keepdims=True)).sum(1))
+            q, K = c.q64[c.start[b]: c.start[b] + L, h], c.K[b][h // (H // Hkv)]
+            ds = 2.0 ** -11 * (np.abs(q) @ np.abs(K).T).max(1) / math.sqrt(D)
+            err = np.abs(got[c.start[b]: c.start[b] + L, h] - ref)
+            assert (err <= ds + 2.0 ** -17 + 2.0 ** -22 * np.abs(ref)).all(), (b, h, (err / ds).max())
+
+
+def test_log_sums_where_nothing_is_seen():
+    c = Case([4, 2], [2, 0], 2, 1, 64, 4, 32, "bf16", 16, seed=4)
+    lse = torch.full((c.total, 2), 7.0, device="cuda")
+    out = torch.empty_like(c.q)
+    qda.qdecode_paged_attn(c.q, *c.arrays, out, c.q_start, c.kv_len, c.table, 4, 32, 4, lse=lse)
+    got = lse.cpu().numpy()
+    np.testing.assert_array_equal(np.isneginf(got), np.isneginf(R.log_sums(c)))
+    assert np.isneginf(got[:2]).all() and np.isneginf(got[4:]).all() and np.isfinite(got[2:4]).all()
+
+
+def test_log_sums_of_rows_done_anew():
+    """A later token's key is far larger than what the others see: their rows are done anew in fp32, sums and all."""
+    q_lens, kv_lens = [40], [200]
+    c = Case(q_lens, kv_lens, 8, 2, 128, 4, 64, "bf16", 16, seed=5)
+    pg = int(c.table[0, 199 // 16])
+    c.arrays[1][pg, :, 199 % 16] *= 2.0 ** 20
+    c.arrays[2][pg, :, 199 % 16] *= 2.0 ** 20
+    c.K[0][:, 199] *= 2.0 ** 20
+    lse = torch.zeros(40, 8, device="cuda")
+    qda.qdecode_paged_attn(c.q, *c.arrays, torch.empty_like(c.q), c.q_start, c.kv_len, c.table, 40, 64, 4, lse=lse)
+    ref = R.log_sums(c)[:39]
+    err = np.abs(lse.cpu().numpy()[:39] - ref)
+    assert (err <= 2.0 ** -11 * 30 + 2.0 ** -17).all(), err.max()   # (sum |q k| / sqrt(D) stays below 30 here)
