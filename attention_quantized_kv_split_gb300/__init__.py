@@ -437,6 +437,13 @@ def qdecode_paged_weights(q: torch.Tensor, k_packed: torch.Tensor, k_scales: tor
     return mass
 
 
+def qdecode_paged_weights_workspace_bytes(B: int, H: int, Hkv: int, total_q: int, max_q: int, window: int, D: int) -> int:
+    out = ctypes.c_size_t()
+    _lib.check(lib().qdecode_paged_weights_workspace_bytes(B, H, Hkv, total_q, max_q, window, D, ctypes.byref(out)),
+               "qdecode_paged_weights_workspace_bytes")
+    return out.value
+
+
 def qdecode_paged_evict(k_packed: torch.Tensor, k_scales: torch.Tensor, k_biases: torch.Tensor, v_packed: torch.Tensor,
                         v_scales: torch.Tensor, v_biases: torch.Tensor, mass: torch.Tensor, token: torch.Tensor,
                         kv_len: torch.Tensor, new_len: torch.Tensor, block_table: torch.Tensor, freed: torch.Tensor,

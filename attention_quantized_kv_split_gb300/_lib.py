@@ -71,6 +71,7 @@ SIGNATURES = {
     "qdecode_rope": (_I, [_P, _LL, _LL] * 4 + [_P] * 4 + [_I] * 9 + [_F64, _P]),
     "qdecode_rope_freqs": (_I, [_I] + [_F64] * 5 + [ctypes.POINTER(_F64)]),
     "qdecode_paged_weights": (_I, [_P, _LL, _LL] + [_P] * 10 + [_I] * 13 + [_F64, _P]),
+    "qdecode_paged_weights_workspace_bytes": (_I, [_I] * 7 + [ctypes.POINTER(_SZ)]),
     "qdecode_paged_evict": (_I, [_P] * 14 + [_I] * 13 + [_P]),
     "qdecode_paged_evict_workspace_bytes": (_I, [_I] * 5 + [ctypes.POINTER(_SZ)]),
     "qdecode_paged_packed": (_I, [_I, ctypes.c_char_p]),

@@ -44,6 +44,7 @@
 #include <type_traits>
 
 #include "qda_paged_sched.cuh"
+#include "qda_paged_tc.cuh"
 
 namespace qda {
 
@@ -125,74 +126,6 @@ constexpr int pc_smem() {
   return 1024 + G::QB + G::SLOTS * G::SLOT + (int)sizeof(PcShared);
 }
 
-__device__ __forceinline__ float pc_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Shared-memory descriptor of a 128-byte swizzled operand (rows of 128 bytes, 8-row groups 1024 bytes apart); lbo: bytes
-// between 64-element blocks of an operand whose rows run along K (values), unused for one whose rows hold K (keys, queries).
-__device__ __forceinline__ uint64_t pc_desc(uint32_t saddr, uint32_t lbo) {
-  return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) | ((uint64_t)(1024u >> 4) << 32) |
-         (1ull << 46) | (2ull << 61);
-}
-
-// One lane of the warp, the same one every time. The products below are issued by that lane while the whole warp walks
-// through the code: addresses and descriptors then stay in uniform registers, where the instruction wants them.
-__device__ __forceinline__ uint32_t pc_elect() {
-  uint32_t e;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-  return e;
-}
-// D (tensor memory) (+)= A (shared memory) * B (shared memory)
-__device__ __forceinline__ void pc_mma_ss(uint32_t one, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(one)
-      : "memory");
-}
-// D (tensor memory) (+)= A (tensor memory) * B (shared memory)
-__device__ __forceinline__ void pc_mma_ts(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                          uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(one)
-      : "memory");
-}
-__device__ __forceinline__ void pc_commit(uint32_t one, uint64_t* bar) {
-  if (one) mma_commit(bar);
-}
-
-__device__ __forceinline__ void pc_ld32(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void pc_ld16(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // 8 columns of this thread's lane times x (rare; few registers, since the scores are being held)
 __device__ __forceinline__ void pc_scale8(uint32_t taddr, float x) {
   uint32_t r[8];
@@ -214,10 +147,6 @@ __device__ __forceinline__ float pc_max3(float a, float b, float c) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t pc_h2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t pc_fma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
   asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -230,13 +159,6 @@ __device__ __forceinline__ float pc_half(uint32_t u16, bool f16) { return half_b
 template <int BITS>
 __host__ __device__ constexpr int pc_dim(int i) {
   return BITS == 4 ? (i >> 1) + 4 * (i & 1) : (i & 4) + ((i & 3) >> 1) + 2 * (i & 1);
-}
-
-// Register count of the calling warpgroup from here on (the sums over the warpgroups stay within the launch's).
-template <int N, int LAUNCH>
-__device__ __forceinline__ void pc_regs() {
-  if constexpr (N > LAUNCH) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-  if constexpr (N < LAUNCH) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // f(integral_constant<0>), ..., f(integral_constant<N - 1>)
@@ -612,6 +534,10 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
       const bool whole = t->whole;
       const bool none = m == -INFINITY && l == l;   // the row saw no key
       const int tok = r / p.nrep;
+      // (the logarithm here by the approximate instruction: fewer registers beside the softmax's)
+      if (p.lse != nullptr && real && whole && half == 0 && t->part == 0)
+        p.lse[(long long)(t->s.first + tok) * p.H + t->kvh * p.nrep + (r - tok * p.nrep)] =
+            l == 0.f ? -INFINITY : (m - kPcWeightBits + pc_lg2(l)) * 0.693147180559945309f;
       const size_t slot = (size_t)(2 * cta + t->mine) * MT + rt;
       uint4* out = reinterpret_cast<uint4*>(
           p.out + ((long long)(t->s.first + tok) * p.H + t->kvh * p.nrep + (r - tok * p.nrep)) * D + t->part * DV);
@@ -650,8 +576,6 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
         }
       }
       if (real && !whole && half == 0) p.part_ml[slot] = make_float2(m, l);
-      if (real && whole && half == 0 && t->part == 0 && p.lse != nullptr)
-        qda_put_lse(p, t->s.first + tok, t->kvh * p.nrep + (r - tok * p.nrep), m, l, kPcWeightBits);
       tc_fence_before();
       bc += n;
       tc += n > 0;

@@ -1,11 +1,141 @@
-// Accumulated attention weight over the paged cache: host side.
+// Accumulated attention weight over the paged cache (sm_103a): the layout of query rows for the kernel for many, host side.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstring>
 
 #include "qda_paged_check.h"
-#include "qda_paged_weights.h"
+#include "qda_paged_weights_tc.cuh"
+
+namespace qda {
+
+constexpr int kPlThreads = 256;
+
+// A CTA lays out one chunk of counted query rows of a sequence under a KV head: each row to fp16 times a power of two that
+// brings its largest value to [2^14, 2^15), in the swizzled form that the products read, and its scalars; rows behind the
+// sequence's last are zeros that weigh nothing. 2048 tokens of 32 heads of 128 values: 17 MB read, 18 written, all in L2.
+template <int D>
+__global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const __grid_constant__ QdaWeightsParams p) {
+  using G = PvGeom<D>;
+  __shared__ int s_chunk[QDA_MAX_B + 1], s_tot[kPlThreads / 32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_launch_dependents();
+  int carry = 0;
+  if (tid == 0) s_chunk[0] = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlThreads) {
+    const int b = b0 + tid;
+    int c = b < p.B ? pv_chunks(p, pw_seq(p, b)) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, c, o);
+      if (lane >= o) c += z;
+    }
+    if (lane == 31) s_tot[warp] = c;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < kPlThreads / 32; ++w) {
+      if (w < warp) before += s_tot[w];
+      carry += s_tot[w];
+    }
+    if (b < p.B) s_chunk[b + 1] = before + c;
+    __syncthreads();
+  }
+  if (carry > p.max_chunks) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);
+    return;
+  }
+  const int kvh = blockIdx.y;
+  for (int ci = blockIdx.x; ci < carry; ci += gridDim.x) {
+    const int b = qda_seq_of(s_chunk, p.B, ci);
+    const PwSeq s = pw_seq(p, b);
+    const int row0 = (s.len - s.count) * p.nrep + (ci - s_chunk[b]) * kPvRows, row_end = s.len * p.nrep;
+    char* dst = p.chunks + ((size_t)ci * p.Hkv + kvh) * G::CHUNK;
+    PvScalars* scal = reinterpret_cast<PvScalars*>(dst + G::SLICES * G::SLICE);
+    // a row takes D / 8 lanes of 8 values
+    constexpr int LPR = D / 8 < 32 ? D / 8 : 32, RPW = 32 / LPR;
+    for (int i0 = warp * RPW; i0 < kPvRows; i0 += kPlThreads / 32 * RPW) {
+      const int i = i0 + lane / LPR, piece = lane % LPR;
+      const int row = row0 + i, tok = row / p.nrep, h = kvh * p.nrep + row - tok * p.nrep;
+      const bool real = row < row_end;
+      uint4 a = make_uint4(0, 0, 0, 0);
+      if (real)
+        a = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(s.first + tok) * p.q_tstride + (long long)h * p.q_hstride) + piece);
+      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+      float2 f[4];
+      float top = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[k] = half2_bits_to_float2_rt(u[k], p.f16);
+        top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+      }
+#pragma unroll
+      for (int o = LPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = top > 0.f && top < INFINITY ? max(-100, min(14 - ilogbf(top), 100)) : 0;
+      const float up = exp2f((float)e);
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = pc_h2(f[k].x * up, f[k].y * up);
+      // slices of SD dimensions; in them blocks of 64, rows of 128 bytes, 16-byte pieces swizzled
+      const int sl = piece / (G::SD / 8), in = piece % (G::SD / 8);
+      *reinterpret_cast<uint4*>(dst + sl * G::SLICE + (in >> 3) * 16384 + i * 128 + (((in & 7) ^ (i & 7)) << 4)) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+      if (piece == 0) {
+        float* ml = reinterpret_cast<float*>(&scal->ml[i >> 1]);
+        ml[i & 1] = real ? p.qscale * exp2f((float)-e) : 0.f;
+        ml[2 + (i & 1)] = real ? p.lse[(long long)(s.first + tok) * p.H + h] * -1.4426950408889634f : -INFINITY;
+        reinterpret_cast<int*>(&scal->last[i >> 1])[i & 1] = real ? s.base + tok : -1;
+      }
+    }
+  }
+}
+
+// Rows (counted new tokens times query heads of a KV head) up to which the kernel on matrix instructions takes a call.
+constexpr int kPwMostRows = 32;
+
+struct WeightsPlan {
+  bool tc;
+  int rows, chunks;
+  size_t bytes;
+};
+
+static WeightsPlan weights_plan(int B, int nrep, int Hkv, int total_q, int max_q, int window, int D) {
+  WeightsPlan w;
+  const long long count = window > 0 ? std::min(window, max_q) : max_q;
+  w.rows = (int)std::min(count * nrep, 1LL << 20);
+  w.tc = w.rows > kPwMostRows && D <= 256;
+  w.chunks = 0;
+  w.bytes = 0;
+  if (w.tc) {
+    long long tokens = total_q;
+    if (window > 0) tokens = std::min(tokens, (long long)window * B);
+    w.chunks = (int)std::min(tokens * nrep / kPvRows + std::min((long long)B, tokens), 0x7fffffffLL);
+    const size_t chunk = D == 64 ? PvGeom<64>::CHUNK : D == 128 ? PvGeom<128>::CHUNK : PvGeom<256>::CHUNK;
+    w.bytes = (size_t)w.chunks * Hkv * chunk;
+  }
+  return w;
+}
+
+}  // namespace qda
+
+cudaError_t qda_paged_weights_lay(const QdaWeightsParams& p, cudaStream_t s) {
+  const dim3 grid((unsigned)std::min(p.max_chunks, 65535), (unsigned)p.Hkv);
+  switch (p.D) {
+    case 64: qda::qda_paged_weights_lay_kernel<64><<<grid, qda::kPlThreads, 0, s>>>(p); break;
+    case 128: qda::qda_paged_weights_lay_kernel<128><<<grid, qda::kPlThreads, 0, s>>>(p); break;
+    default: qda::qda_paged_weights_lay_kernel<256><<<grid, qda::kPlThreads, 0, s>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+extern "C" int qdecode_paged_weights_workspace_bytes(int B, int H, int Hkv, int total_q, int max_q, int window, int D,
+                                                     size_t* bytes) {
+  using namespace qda;
+  if (bytes == nullptr || B < 1 || H < 1 || Hkv < 1 || total_q < 0 || max_q < 1 || window < 0 || H % Hkv != 0) return QDA_ERR_INVALID;
+  if (D != 64 && D != 128 && D != 256 && D != 512) return QDA_ERR_UNSUPPORTED;
+  if (B > QDA_MAX_B || H / Hkv > QDA_MAX_NREP || (long long)total_q * (H / Hkv) > 0x7fffff00LL) return QDA_ERR_UNSUPPORTED;
+  *bytes = weights_plan(B, H / Hkv, Hkv, total_q, max_q, window, D).bytes;
+  return QDA_OK;
+}
 
 extern "C" int qdecode_paged_weights(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                                      const void* k_scales, const void* k_biases, const float* lse, float* mass,
@@ -63,12 +193,37 @@ extern "C" int qdecode_paged_weights(const void* q, long long q_tstride, long lo
   p.f16 = dtype == QDA_FP16;
   p.qscale = 1.4426950408889634f / sqrtf((float)D);
   p.decay = (float)decay;
-  // the instance, and its resident CTAs per SM (0: not asked yet)
-  const long long count = window > 0 ? std::min(window, max_q) : max_q;
-  const int rows = (int)std::min(count * nrep, 1LL << 20);
+  p.D = D;
+  p.GS = GS;
+  p.NG = D / GS;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const WeightsPlan plan = weights_plan(B, nrep, Hkv, total_q, max_q, window, D);
+  const int rows = plan.rows;
   int dev = 0;
   const cudaError_t de = cudaGetDevice(&dev);
   if (de != cudaSuccess || dev < 0 || dev >= 64) return qda_cuda_fail(de == cudaSuccess ? cudaErrorInvalidDevice : de);
+  if (plan.tc) {
+    const auto run = bits == 4 ? qda_paged_weights_tc_b4 : qda_paged_weights_tc_b8;
+    static std::atomic<bool> ready[64][2][3] = {};
+    std::atomic<bool>& r = ready[dev][bits == 8][D / 128];
+    if (!r.load()) {
+      const cudaError_t e = run(nullptr, D, true, nullptr);
+      if (e != cudaSuccess) return qda_cuda_fail(e);
+      r.store(true);
+    }
+    void* ws = nullptr;
+    st = qda_workspace(plan.bytes, &ws);
+    if (st != QDA_OK) return st;
+    p.chunks = static_cast<char*>(ws);
+    p.max_chunks = plan.chunks;
+    p.ctas = sms;
+#ifdef QDA_BOUNDS_CHECK
+    p.stall = qda_stall_chunk();
+#endif
+    cudaError_t e = qda_paged_weights_lay(p, s);
+    if (e == cudaSuccess) e = run(&p, D, false, s);
+    return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
+  }
   const int di = D == 64 ? 0 : D == 128 ? 1 : D == 256 ? 2 : 3, gi = GS == 32 ? 0 : GS == 64 ? 1 : 2;
   static std::atomic<int> cache[64][2][4][3][2] = {};
   std::atomic<int>& slot = cache[dev][bits == 8][di][gi][rows > 8];
@@ -81,6 +236,6 @@ extern "C" int qdecode_paged_weights(const void* q, long long q_tstride, long lo
     slot.store(occ);
   }
   p.ctas = sms * occ;
-  const cudaError_t e = launch(&p, D, GS, rows, nullptr, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch(&p, D, GS, rows, nullptr, s);
   return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
 }

@@ -20,9 +20,82 @@ struct QdaWeightsParams {
   int total_q, window, B, H, Hkv, nrep, num_pages, page_shift, max_pages, ctas, f16;
   float qscale;               // log2(e) / sqrt(D)
   float decay;
+  // the kernel for many rows
+  int D, GS, NG;
+  char* chunks;               // [chunks of all sequences, Hkv] query rows as operands (qda_paged_weights_tc.cuh)
+  int max_chunks;             // chunks that there is room for
+  int stall;                  // testing aid of the checked build: the first CTA does not get this operand slice (-1: gets all)
 };
+
+#ifdef __CUDACC__
+namespace qda {
+
+// A sequence as these kernels see it.
+struct PwSeq {
+  int first, len;      // its first token's row in q, its new tokens
+  int n, base;         // keys; keys before the first new token (negative where the lengths lie)
+  int count;           // new tokens that count: the last ones
+};
+
+__device__ __forceinline__ PwSeq pw_seq(const QdaWeightsParams& p, int start, int end, int n) {
+  PwSeq s;
+  const int q0 = min(max(start, 0), p.total_q), q1 = min(max(end, q0), p.total_q);
+  s.first = q0;
+  s.len = q1 - q0;
+  // (sums with a block's keys stay in range)
+  s.n = (int)min((long long)max(n, 0), min((long long)min(p.max_pages, p.num_pages) << p.page_shift, 0x7ffffe00LL));
+  s.base = n - s.len;
+  s.count = p.window > 0 ? min(p.window, s.len) : s.len;
+  return s;
+}
+__device__ __forceinline__ PwSeq pw_seq(const QdaWeightsParams& p, int b) {
+  return pw_seq(p, p.q_start[b], p.q_start[b + 1], p.kv_len[b]);
+}
+
+// Whether a sequence's starts or length are not what they have to be.
+__device__ __forceinline__ bool pw_bad(const QdaWeightsParams& p, int start, int end, int n, const PwSeq& s) {
+  return start < 0 || end < start || end > p.total_q || (end > start && (n < 0 || n > s.n));
+}
+
+// Blocks of KEYS keys (none without new tokens).
+template <int KEYS>
+__device__ __forceinline__ int pw_blocks(const PwSeq& s) {
+  return s.len > 0 ? (int)(((long long)s.n + KEYS - 1) / KEYS) : 0;
+}
+
+// Work of the first i key blocks under one KV head, in query rows (COST: a block's work beside them). A block's rows are those
+// of the counted tokens that see its first key: min(count, n - i KEYS), all of them until the causal edge.
+template <int KEYS, int COST>
+__device__ __forceinline__ long long pw_prefix(const QdaWeightsParams& p, const PwSeq& s, int i) {
+  long long flat = s.n >= s.count ? ((long long)s.n - s.count) / KEYS + 1 : 0;
+  flat = min(flat, (long long)i);
+  const long long rest = i - flat;
+  const long long rows = flat * s.count + rest * s.n - KEYS * (((long long)i * (i - 1) - flat * (flat - 1)) / 2);
+  return (long long)i * COST + rows * p.nrep;
+}
+
+// First block under the KV head at place `at` of the line that starts at or behind x.
+template <int KEYS, int COST>
+__device__ __forceinline__ int pw_block_at(const QdaWeightsParams& p, const PwSeq& s, int blocks, long long at, long long x) {
+  int lo = 0, hi = blocks;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (at + pw_prefix<KEYS, COST>(p, s, mid) >= x) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+}  // namespace qda
+#endif
 
 // Translation units per code width. With ctas_per_sm the instance's resident CTAs per SM are stored there and nothing is
 // launched; else p.ctas CTAs are. rows: the bound on a KV head's query rows that choose the instance.
 cudaError_t qda_paged_weights_b4(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 cudaError_t qda_paged_weights_b8(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+
+// The kernel for many rows (D <= 256), and the one ahead of it that lays out the query rows. prepare sets the shared memory
+// limit on the current device and launches nothing.
+constexpr int kPvRows = 128;   // query rows of a chunk
+cudaError_t qda_paged_weights_tc_b4(const QdaWeightsParams* p, int D, bool prepare, cudaStream_t s);
+cudaError_t qda_paged_weights_tc_b8(const QdaWeightsParams* p, int D, bool prepare, cudaStream_t s);
+cudaError_t qda_paged_weights_lay(const QdaWeightsParams& p, cudaStream_t s);

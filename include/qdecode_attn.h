@@ -411,14 +411,19 @@ int qdecode_rope_freqs(int rot, double base, double factor, double context, doub
  * the new tokens themselves start from 0, whatever mass holds there, and their token becomes their position, j + shift[b]
  * (shift may be NULL: 0). Sequences without new tokens, and rows behind kv_len, stay as they are. max_q bounds the new
  * tokens of a sequence and only chooses the kernel. Scores are right to fp32 (queries below 2^-39 of their row's largest
- * aside); sums are fp32 in a fixed order: the same bits on every run. Scales and biases as for the attention: a key that is
- * not finite gives its own mass alone. Same types, limits and checks as qdecode_paged_attn; no workspace.
+ * and keys' values below 2^-39 of what their key can hold aside); sums are fp32 in a fixed order: the same bits on every run.
+ * Scales and biases as for the attention: a key that is not finite spoils its own mass alone. Same types, limits and checks
+ * as qdecode_paged_attn. Uses the workspace as qdecode_attn does, of qdecode_paged_weights_workspace_bytes() bytes; calls that
+ * share one must not overlap on the GPU.
  */
 int qdecode_paged_weights(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                           const void* k_scales, const void* k_biases, const float* lse, float* mass, int32_t* token,
                           const int32_t* q_start, const int32_t* kv_len, const int32_t* block_table, const int32_t* shift,
                           int total_q, int max_q, int window, int B, int H, int Hkv, int num_pages, int page,
                           int max_pages, int D, int GS, int bits, int dtype, double decay, void* stream);
+
+/* Workspace in bytes that qdecode_paged_weights needs for these arguments, whatever the lengths. */
+int qdecode_paged_weights_workspace_bytes(int B, int H, int Hkv, int total_q, int max_q, int window, int D, size_t* bytes);
 
 /*
  * qdecode_paged_evict: cuts every sequence of more than `limit` rows to `budget` rows (1 <= budget <= limit), each KV head
