@@ -11,7 +11,7 @@ namespace qda {
 
 constexpr int kPlThreads = 256;
 
-// A CTA lays out one chunk of counted query rows of a sequence under a KV head: each row to fp16 times a power of two that
+// Each warp lays out the counted query rows of a sequence under a KV head, a CTA's warps sixteen to sixty-four: each row to fp16 times a power of two that
 // brings its largest value to [2^14, 2^15), in the swizzled form that the products read, and its scalars; rows behind the
 // sequence's last are zeros that weigh nothing. 2048 tokens of 32 heads of 128 values: 17 MB read, 18 written, all in L2.
 template <int D>
@@ -45,16 +45,17 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
     return;
   }
   const int kvh = blockIdx.y;
-  for (int ci = blockIdx.x; ci < carry; ci += gridDim.x) {
+  constexpr int LPR = D / 8 < 32 ? D / 8 : 32, RPW = 32 / LPR;   // a row takes D / 8 lanes of 8 values
+  constexpr int ROWS = kPlThreads / 32 * RPW, PARTS = kPvRows / ROWS;
+  for (long long x = blockIdx.x; x < (long long)carry * PARTS; x += gridDim.x) {
+    const int ci = (int)(x / PARTS);
     const int b = qda_seq_of(s_chunk, p.B, ci);
     const PwSeq s = pw_seq(p, b);
     const int row0 = (s.len - s.count) * p.nrep + (ci - s_chunk[b]) * kPvRows, row_end = s.len * p.nrep;
     char* dst = p.chunks + ((size_t)ci * p.Hkv + kvh) * G::CHUNK;
     PvScalars* scal = reinterpret_cast<PvScalars*>(dst + G::SLICES * G::SLICE);
-    // a row takes D / 8 lanes of 8 values
-    constexpr int LPR = D / 8 < 32 ? D / 8 : 32, RPW = 32 / LPR;
-    for (int i0 = warp * RPW; i0 < kPvRows; i0 += kPlThreads / 32 * RPW) {
-      const int i = i0 + lane / LPR, piece = lane % LPR;
+    {
+      const int i = (int)(x % PARTS) * ROWS + warp * RPW + lane / LPR, piece = lane % LPR;
       const int row = row0 + i, tok = row / p.nrep, h = kvh * p.nrep + row - tok * p.nrep;
       const bool real = row < row_end;
       uint4 a = make_uint4(0, 0, 0, 0);
@@ -70,8 +71,8 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
       }
 #pragma unroll
       for (int o = LPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = top > 0.f && top < INFINITY ? max(-100, min(14 - ilogbf(top), 100)) : 0;
-      const float up = exp2f((float)e);
+      const int e = pv_up(top);
+      const float up = pv_pow2(e);
       uint32_t w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = pc_h2(f[k].x * up, f[k].y * up);
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
           make_uint4(w[0], w[1], w[2], w[3]);
       if (piece == 0) {
         float* ml = reinterpret_cast<float*>(&scal->ml[i >> 1]);
-        ml[i & 1] = real ? p.qscale * exp2f((float)-e) : 0.f;
+        ml[i & 1] = real ? p.qscale * pv_pow2(-e) : 0.f;
         ml[2 + (i & 1)] = real ? p.lse[(long long)(s.first + tok) * p.H + h] * -1.4426950408889634f : -INFINITY;
         reinterpret_cast<int*>(&scal->last[i >> 1])[i & 1] = real ? s.base + tok : -1;
       }
@@ -118,7 +119,7 @@ static WeightsPlan weights_plan(int B, int nrep, int Hkv, int total_q, int max_q
 }  // namespace qda
 
 cudaError_t qda_paged_weights_lay(const QdaWeightsParams& p, cudaStream_t s) {
-  const dim3 grid((unsigned)std::min(p.max_chunks, 65535), (unsigned)p.Hkv);
+  const dim3 grid((unsigned)std::min(p.max_chunks * 16LL, 1LL << 20), (unsigned)p.Hkv);
   switch (p.D) {
     case 64: qda::qda_paged_weights_lay_kernel<64><<<grid, qda::kPlThreads, 0, s>>>(p); break;
     case 128: qda::qda_paged_weights_lay_kernel<128><<<grid, qda::kPlThreads, 0, s>>>(p); break;

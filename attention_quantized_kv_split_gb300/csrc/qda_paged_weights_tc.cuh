@@ -7,9 +7,11 @@
 // Masses are fp32, so scores must be: a key is two fp16 operands, its value to 11 bits and what those leave (22 bits, or 2^-39
 // of the key's largest possible value), each key scaled by its own power of two, and a query row is exact in fp16 scaled by
 // its own (what is 2^-39 of the row's largest and less loses bits). Both products go to the same fp32 accumulator.
-//   dequantising warps   eight: two threads per key, codes -> the two operands in shared memory (two blocks ahead of each
-//                        other where they fit), and what undoes the key's scale;
-//   producer             one lane: a chunk's operands and scalars, laid out by the kernel ahead, by bulk copies into a ring;
+//   key loader           eight lanes, sixteen keys each: a block's codes, scales and biases by bulk copies into a ring;
+//   dequantising warps   eight: two threads per key, codes -> the two operands in tensor memory (where products read them
+//                        without a share of the shared memory's bandwidth; two blocks of them at D <= 128), and what undoes
+//                        the key's scale;
+//   row loader           one lane: a chunk's operands and scalars, laid out by the kernel ahead, by bulk copies into a ring;
 //   MMA warp             one lane issues every product; two accumulators of 128 columns take turns;
 //   exponential warps    eight: a thread per key and half of a chunk's columns.
 // Every link is an mbarrier; every wait is bounded and sets the device error word, and after one that gave up every role ends.
@@ -22,7 +24,7 @@ namespace qda {
 
 constexpr int kPvKeys = 128;
 constexpr int kPvCost = 48;    // work of a block beside its query rows, in query rows
-constexpr int kPvExp = 8, kPvDeq = 8, kPvWarps = kPvExp + kPvDeq + 2;
+constexpr int kPvExp = 8, kPvDeq = 8, kPvWarps = kPvExp + kPvDeq + 3;
 constexpr int kPvScalars = 3;  // chunks' scalars in flight
 
 // A chunk's scalars: pairs of rows side by side.
@@ -31,15 +33,73 @@ struct PvScalars {
   int2 last[kPvRows / 2];      // last key that the row sees; -1: no row
 };
 
+constexpr int kPvRaw = 3;      // blocks' codes in flight
+
 template <int D>
 struct PvGeom {
-  static constexpr int SD = D < 128 ? D : 128;           // dimensions of an operand slice
+  static constexpr int SD = 64;                          // dimensions of an operand slice
   static constexpr int SLICES = D / SD, SLICE = kPvRows * SD * 2;
   static constexpr int CHUNK = SLICES * SLICE + (int)sizeof(PvScalars);   // bytes in memory
-  static constexpr int A = 2 * kPvKeys * D * 2;          // a block's two operands
-  static constexpr int AS = D <= 128 ? 2 : 1;            // blocks in shared memory
-  static constexpr int BS = D == 64 ? 4 : 2;             // operand slices in flight
+  static constexpr int AS = D <= 128 ? 2 : 1;            // blocks in tensor memory, D columns each (two values a column, two operands)
+  static constexpr int A_COL = 256;                      // they stand behind two accumulators
+  static constexpr int BS = D == 256 ? 5 : 6;            // operand slices in flight
 };
+
+template <int BITS, int D>
+struct PvKeys {
+  static constexpr int RB = D * BITS / 8;                // a row of codes
+  static constexpr int SC = kPvKeys * (D / 32) * 2;      // room for the scales of the smallest groups
+  static constexpr int RAW = kPvKeys * RB + 2 * SC;
+};
+
+// Chunks of a sequence under a KV head.
+__device__ __forceinline__ int pv_chunks(const QdaWeightsParams& p, const PwSeq& s) {
+  return s.n > 0 ? (int)(((long long)s.count * p.nrep + kPvRows - 1) / kPvRows) : 0;
+}
+
+// Where a CTA stands on its piece of the line: at a block of keys. Every role walks for itself.
+struct PvWalk {
+  int b, kvh, x, blocks;
+  long long pos;               // the block's place
+  PwSeq s;
+
+  __device__ __forceinline__ void start(const QdaWeightsParams& p, const long long* line, long long from) {
+    b = qda_seq_of(line, p.B, from);
+    s = pw_seq(p, b);
+    blocks = pw_blocks<kPvKeys>(s);
+    const long long head = pw_prefix<kPvKeys, kPvCost>(p, s, blocks);
+    kvh = (int)((from - line[b]) / head);
+    const long long at = line[b] + kvh * head;
+    x = pw_block_at<kPvKeys, kPvCost>(p, s, blocks, at, from);
+    pos = at + pw_prefix<kPvKeys, kPvCost>(p, s, x);
+  }
+  // The block at hand, or the next one that there is; false behind the piece.
+  __device__ __forceinline__ bool here(const QdaWeightsParams& p, long long to) {
+    if (pos >= to) return false;
+    if (x >= blocks) {
+      x = 0;
+      if (++kvh >= p.Hkv) {
+        kvh = 0;
+        do {
+          if (++b >= p.B) return false;
+          s = pw_seq(p, b);
+          blocks = pw_blocks<kPvKeys>(s);
+        } while (blocks == 0);
+      }
+    }
+    return true;
+  }
+  __device__ __forceinline__ void step(const QdaWeightsParams& p) {
+    pos += kPvCost + (long long)p.nrep * min(s.count, s.n - x * kPvKeys);   // as pw_prefix has it
+    ++x;
+  }
+  // The chunks whose rows see the block's first key: from this one to the sequence's last.
+  __device__ __forceinline__ int first_chunk(const QdaWeightsParams& p) const {
+    const int before = max(0, x * kPvKeys - s.base - (s.len - s.count));   // counted tokens that do not
+    return (int)(((long long)before * p.nrep) >> 7);
+  }
+};
+static_assert(kPvRows == 128, "first_chunk");
 
 struct PvShared {
   PvScalars scal[kPvScalars];
@@ -47,76 +107,40 @@ struct PvShared {
   float part[2][kPvKeys];      // the second half's sums, by a block's parity
   long long at[QDA_MAX_B + 1]; // sequences on the line of work
   int chunk[QDA_MAX_B + 1];    // chunks before each sequence
+  PvWalk walk;
+  long long row[8][8];         // pool rows of a block's sixteens of keys (-1: none), eight blocks
   long long tot[kPvWarps];
   int ctot[kPvWarps];
-  uint64_t a_full[2], a_empty[2], b_full[4], b_empty[4], c_full[kPvScalars], c_empty[kPvScalars], d_full[2], d_empty[2],
-      p_full[2], p_empty[2], drain;
+  uint64_t r_full[kPvRaw], r_empty[kPvRaw], a_full[2], a_empty[2], b_full[8], b_empty[8], c_full[kPvScalars], c_empty[kPvScalars],
+      d_full[2], d_empty[2], p_full[2], p_empty[2], drain;
   uint32_t tmem;
   int abort;
 };
 
-template <int D>
+template <int BITS, int D>
 constexpr int pv_smem() {
   using G = PvGeom<D>;
-  return 1024 + G::AS * G::A + G::BS * G::SLICE + (int)sizeof(PvShared);
+  return 1024 + G::BS * G::SLICE + kPvRaw * PvKeys<BITS, D>::RAW + (int)sizeof(PvShared);
 }
 
-// Chunks of a sequence under a KV head.
-__device__ __forceinline__ int pv_chunks(const QdaWeightsParams& p, const PwSeq& s) {
-  return s.n > 0 ? (int)(((long long)s.count * p.nrep + kPvRows - 1) / kPvRows) : 0;
+// 2^e, and e that brings x to [2^14, 2^15) (0 for what is no positive number, or infinite).
+__device__ __forceinline__ float pv_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ int pv_up(float x) {
+  return x > 0.f && x < INFINITY ? max(-100, min(141 - (int)(__float_as_uint(x) >> 23), 100)) : 0;
 }
-
-// Where a CTA stands on its piece of the line.
-struct PvWalk {
-  int b, kvh, x, blocks;
-  long long head, at;
-  PwSeq s;
-
-  __device__ __forceinline__ void enter(const QdaWeightsParams& p) {
-    s = pw_seq(p, b);
-    blocks = pw_blocks<kPvKeys>(s);
-    head = pw_prefix<kPvKeys, kPvCost>(p, s, blocks);
-  }
-  __device__ __forceinline__ void start(const QdaWeightsParams& p, const long long* line, long long from) {
-    b = qda_seq_of(line, p.B, from);
-    enter(p);
-    kvh = (int)((from - line[b]) / head);
-    at = line[b] + kvh * head;
-    x = pw_block_at<kPvKeys, kPvCost>(p, s, blocks, at, from);
-  }
-  // The block at hand, or the next one that there is; false behind the piece.
-  __device__ __forceinline__ bool here(const QdaWeightsParams& p, long long to) {
-    if (x >= blocks) {
-      x = 0;
-      at += head;
-      if (++kvh >= p.Hkv) {
-        kvh = 0;
-        do {
-          if (++b >= p.B) return false;
-          enter(p);
-        } while (blocks == 0);
-      }
-    }
-    return at + pw_prefix<kPvKeys, kPvCost>(p, s, x) < to;
-  }
-  // The chunks whose rows see the block's first key: from this one to the sequence's last.
-  __device__ __forceinline__ int first_chunk(const QdaWeightsParams& p) const {
-    const int before = max(0, x * kPvKeys - s.base - (s.len - s.count));   // counted tokens that do not
-    return (int)((long long)before * p.nrep / kPvRows);
-  }
-};
 
 template <int BITS, int D>
 __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(const __grid_constant__ QdaWeightsParams p) {
   using G = PvGeom<D>;
-  constexpr int W = D * BITS / 32, SD = G::SD;
+  using K = PvKeys<BITS, D>;
+  constexpr int SD = G::SD;
   extern __shared__ __align__(1024) unsigned char pv_smem_raw[];
   unsigned char* base = pv_smem_raw + ((1024u - (smem_addr(pv_smem_raw) & 1023u)) & 1023u);
-  unsigned char* a_s = base;
-  unsigned char* b_s = base + G::AS * G::A;
-  PvShared& sh = *reinterpret_cast<PvShared*>(b_s + G::BS * G::SLICE);
+  unsigned char* b_s = base;
+  unsigned char* raw_s = base + G::BS * G::SLICE;
+  PvShared& sh = *reinterpret_cast<PvShared*>(raw_s + kPvRaw * K::RAW);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int W_MMA = kPvExp + kPvDeq;   // behind the exponential and the dequantising warps; the producer behind it
+  constexpr int W_MMA = kPvExp + kPvDeq, W_KEYS = W_MMA + 1;   // behind the exponential and the dequantising warps
   volatile int* abort = &sh.abort;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -127,9 +151,13 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       mbar_init(&sh.p_full[i], kPvExp / 2);
       mbar_init(&sh.p_empty[i], kPvExp / 2);
     }
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.b_full[i], 1);
       mbar_init(&sh.b_empty[i], 1);
+    }
+    for (int i = 0; i < kPvRaw; ++i) {
+      mbar_init(&sh.r_full[i], 8);
+      mbar_init(&sh.r_empty[i], kPvDeq);
     }
     for (int i = 0; i < kPvScalars; ++i) {
       mbar_init(&sh.c_full[i], 1);
@@ -191,7 +219,8 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
     pdl_wait();
     return;
   }
-  if (warp == W_MMA) tmem_alloc(&sh.tmem, 256);
+  if (warp == W_MMA) tmem_alloc(&sh.tmem, 512);
+  if (tid == 0) sh.walk.start(p, sh.at, from);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -199,73 +228,68 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
   auto wait = [&](uint64_t* bar, uint32_t phase) { return mbar_wait_bounded(bar, phase & 1u, abort, p.err, 1u); };
   // a warp's wait, for which it ends as one
   auto wait_all = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
-  const int pmask = (1 << p.page_shift) - 1;
-  PvWalk w;
-  w.start(p, sh.at, from);
+  PvWalk w = sh.walk;
   // blocks, chunks and slices so far: every role counts them for itself
   uint32_t bc = 0, cc = 0, sc = 0;
-  auto key_row = [&](int key, bool* there) -> long long {
-    const int pg = key < w.s.n ? __ldg(p.table + (size_t)w.b * p.max_pages + (key >> p.page_shift)) : -1;
-    *there = (unsigned)pg < (unsigned)p.num_pages;
-    return *there ? qda_pool_row(pg, w.kvh, key & pmask, p.Hkv, p.page_shift) : 0;
-  };
-
   if (warp < kPvExp) {
     // ============================================================================ exponentials: two threads per key
     const int half = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t d_t = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 64 * half;
-    for (; w.here(p, to); ++w.x, ++bc) {
+    for (; w.here(p, to); w.step(p), ++bc) {
       const int key = w.x * kPvKeys + r;
-      bool there;
-      const long long row = key_row(key, &there);
-      const bool keep = there && key < w.s.base;
-      float old = 0.f;
-      if (half == 0 && keep) old = p.mass[row];
       const int first_tok = w.s.len - w.s.count;
       const int chunks = sh.chunk[w.b + 1] - sh.chunk[w.b];
       if (!wait_all(&sh.a_full[bc % G::AS], bc / G::AS)) break;
       const float km = sh.kmul[bc % G::AS][r];
+      const long long row0 = sh.row[bc & 7][r >> 4], row = row0 + (r & 15);
+      const bool there = row0 >= 0 && key < w.s.n, keep = there && key < w.s.base;
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.a_empty[bc % G::AS]);
+      float old = 0.f;
+      if (half == 0 && keep) old = p.mass[row];
+      const float2 km2 = make_float2(km, km);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool ok = true;
+#pragma unroll 1
       for (int c = w.first_chunk(p); c < chunks; ++c, ++cc) {
         const int buf = cc & 1, ps = cc % kPvScalars;
         ok = wait_all(&sh.c_full[ps], cc / kPvScalars) && wait_all(&sh.d_full[buf], cc >> 1);
         if (!ok) break;
         tc_fence_after();
-        const PvScalars& f = sh.scal[ps];
-        const float2 km2 = make_float2(km, km);
-        // all of the chunk's rows see all of the block's keys
-        const bool open = w.x * kPvKeys + kPvKeys - 1 <= w.s.base + first_tok + (int)((long long)c * kPvRows / p.nrep);
-        // sixteen columns at a time, the next ones on their way
-        float v[2][16];
-        auto weigh = [&](const float (&u)[16], int q, bool masked) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 ml = f.ml[32 * half + 8 * q + i];
-            const float2 s2 = __fmul2_rn(make_float2(u[2 * i], u[2 * i + 1]), km2);
-            const float2 e = __ffma2_rn(s2, make_float2(ml.x, ml.y), make_float2(ml.z, ml.w));
-            float2 y = make_float2(pc_ex2(e.x), pc_ex2(e.y));
-            if (masked) {
-              const int2 last = f.last[32 * half + 8 * q + i];
-              y = make_float2(key <= last.x ? y.x : 0.f, key <= last.y ? y.y : 0.f);
-            }
-            sum[i & 1] = __fadd2_rn(sum[i & 1], y);
-          }
-        };
-        pc_ld16(d_t + 128 * buf, v[0]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        const float4* ml = sh.scal[ps].ml + 32 * half;
+        const int2* last = sh.scal[ps].last + 32 * half;
+        // all of the chunk's rows see all of the block's keys: the last key against the first row's token
+        const bool open = (long long)(w.x * kPvKeys + kPvKeys - 1 - w.s.base - first_tok) * p.nrep <= (long long)c * kPvRows;
+        // 32 columns at a time, in loops that stay small: with everything unrolled the warps' roles pushed each other out of
+        // the instruction cache
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          float v[32];
+          pc_ld32(d_t + 128 * buf + 32 * q, v);
           tmem_wait_ld();
-          if (q < 3) pc_ld16(d_t + 128 * buf + 16 * (q + 1), v[(q + 1) & 1]);
-          if (q == 3) {
+          if (q == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
           }
-          if (open) weigh(v[q & 1], q, false);
-          else weigh(v[q & 1], q, true);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float4 m = ml[16 * q + i];
+            const float2 s2 = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), km2);
+            const float2 e = __ffma2_rn(s2, make_float2(m.x, m.y), make_float2(m.z, m.w));
+            v[2 * i] = pc_ex2(e.x);
+            v[2 * i + 1] = pc_ex2(e.y);
+          }
+          if (!open) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int2 t = last[16 * q + i];
+              if (key > t.x) v[2 * i] = 0.f;
+              if (key > t.y) v[2 * i + 1] = 0.f;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sum[i & 1] = __fadd2_rn(sum[i & 1], make_float2(v[2 * i], v[2 * i + 1]));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.c_empty[ps]);
@@ -283,86 +307,106 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       add += sh.part[bc & 1][r];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_empty[bc & 1]);
-      if (there && key < w.s.n) {
-        if (keep) {
-          p.mass[row] = fmaf(p.decay, old, add);
-        } else {
-          p.mass[row] = add;
-          p.token[row] = key + (p.shift != nullptr ? p.shift[w.b] : 0);
-        }
+      if (keep) {
+        p.mass[row] = fmaf(p.decay, old, add);
+      } else if (there) {
+        p.mass[row] = add;
+        p.token[row] = key + (p.shift != nullptr ? p.shift[w.b] : 0);
       }
     }
   } else if (warp < W_MMA) {
     // ============================================================================ codes -> operands: two threads per key
     const int r = (tid - kPvExp * 32) & 127, half = (tid - kPvExp * 32) >> 7;
     constexpr float QMAX = (float)((1 << BITS) - 1);
-    for (; w.here(p, to); ++w.x, ++bc) {
-      const int key = w.x * kPvKeys + r;
-      bool there;
-      const long long row = key_row(key, &there);
-      if (!there && key < w.s.n) atomicOr(p.err, QDA_ERR_BIT_PAGED);
-      // what the key can hold at most, to [2^14, 2^15)
-      float top = 0.f;
+    const uint32_t a_t = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::A_COL;
+    for (; w.here(p, to); w.step(p), ++bc) {
+      const int st = bc % kPvRaw;
+      if (!wait_all(&sh.r_full[st], bc / kPvRaw)) break;
+      const unsigned char* raw = raw_s + st * K::RAW;
+      const bool there = sh.row[bc & 7][r >> 4] >= 0;
+      // all of the key's scales and biases (pairs of 16 bits)
+      uint32_t sw[4] = {0, 0, 0, 0}, bw[4] = {0, 0, 0, 0};
       if (there) {
-        for (int g = 0; g < p.NG; ++g) {
-          const float s = half_bits_to_float_rt(__ldg(p.ks + row * p.NG + g), p.f16), z = half_bits_to_float_rt(__ldg(p.kb + row * p.NG + g), p.f16);
-          top = fmaxf(top, fmaf(fabsf(s), QMAX, fabsf(z)));
+        const unsigned char *ks = raw + kPvKeys * K::RB + r * p.NG * 2, *kb = ks + kPvKeys * p.NG * 2;
+        if (p.NG == 8) {
+          const uint4 x = *reinterpret_cast<const uint4*>(ks), y = *reinterpret_cast<const uint4*>(kb);
+          sw[0] = x.x, sw[1] = x.y, sw[2] = x.z, sw[3] = x.w;
+          bw[0] = y.x, bw[1] = y.y, bw[2] = y.z, bw[3] = y.w;
+        } else if (p.NG == 4) {
+          const uint2 x = *reinterpret_cast<const uint2*>(ks), y = *reinterpret_cast<const uint2*>(kb);
+          sw[0] = x.x, sw[1] = x.y;
+          bw[0] = y.x, bw[1] = y.y;
+        } else if (p.NG == 2) {
+          sw[0] = *reinterpret_cast<const uint32_t*>(ks);
+          bw[0] = *reinterpret_cast<const uint32_t*>(kb);
+        } else {
+          sw[0] = *reinterpret_cast<const uint16_t*>(ks);
+          bw[0] = *reinterpret_cast<const uint16_t*>(kb);
         }
       }
-      const int e = top > 0.f && top < INFINITY ? max(-100, min(14 - ilogbf(top), 100)) : 0;
-      const float up = exp2f((float)e);
+      // what the key can hold at most, to [2^14, 2^15)
+      float top = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = half2_bits_to_float2_rt(sw[i], p.f16), z = half2_bits_to_float2_rt(bw[i], p.f16);
+        top = fmaxf(top, fmaxf(fmaf(fabsf(a.x), QMAX, fabsf(z.x)), fmaf(fabsf(a.y), QMAX, fabsf(z.y))));
+      }
+      const int e = pv_up(top);
+      const float up = pv_pow2(e);
       if (!wait_all(&sh.a_empty[bc % G::AS], bc / G::AS + 1)) break;
-      unsigned char* hi = a_s + (bc % G::AS) * G::A;
-      unsigned char* lo = hi + kPvKeys * D * 2;
-      if (half == 0) sh.kmul[bc % G::AS][r] = exp2f((float)-e);
-      // 32 values at a time: D / 64 of them for each thread
-      for (int i = 0; i < D / 64; ++i) {
-        const int u = half * (D / 64) + i;
+      tc_fence_after();
+      const uint32_t hi_t = a_t + (bc % G::AS) * D, lo_t = hi_t + D / 2;
+      if (half == 0) sh.kmul[bc % G::AS][r] = pv_pow2(-e);
+#pragma unroll 1
+      for (int i = 0; i < D / 64; ++i) {   // 32 values: 16 columns of either operand
+        const int u = half * (D / 64) + i, g = u * 32 / p.GS;
         uint32_t code[BITS];
 #pragma unroll
         for (int k = 0; k < BITS / 4; ++k) {
-          const uint4 q = there ? __ldg(reinterpret_cast<const uint4*>(p.kp + row * W + u * BITS) + k) : make_uint4(0, 0, 0, 0);
+          const uint4 q = *reinterpret_cast<const uint4*>(raw + r * K::RB + u * BITS * 4 + 16 * k);
           code[4 * k] = q.x;
           code[4 * k + 1] = q.y;
           code[4 * k + 2] = q.z;
           code[4 * k + 3] = q.w;
         }
-        const int g = u * 32 / p.GS;
-        const float s = there ? half_bits_to_float_rt(__ldg(p.ks + row * p.NG + g), p.f16) * up : 0.f;
-        const float z = there ? half_bits_to_float_rt(__ldg(p.kb + row * p.NG + g), p.f16) * up : 0.f;
+        const uint32_t s2 = g < 4 ? (g < 2 ? sw[0] : sw[1]) : (g < 6 ? sw[2] : sw[3]);
+        const uint32_t z2 = g < 4 ? (g < 2 ? bw[0] : bw[1]) : (g < 6 ? bw[2] : bw[3]);
+        // (a key that is not there has scale and bias 0)
+        const float s = half_bits_to_float_rt((s2 >> (16 * (g & 1))) & 0xffffu, p.f16) * up;
+        const float z = half_bits_to_float_rt((z2 >> (16 * (g & 1))) & 0xffffu, p.f16) * up;
+        uint32_t h[16], l[16];
 #pragma unroll
-        for (int o = 0; o < 4; ++o) {   // 8 values: 16 bytes of either operand
-          uint32_t h[4], l[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float v[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int at = 8 * o + 2 * k + j;
-              const uint32_t c = (code[at * BITS / 32] >> (at * BITS % 32)) & ((1u << BITS) - 1);
-              v[j] = fmaf(s, __uint_as_float(0x4B000000u | c) - 8388608.f, z);
-            }
-            h[k] = pc_h2(v[0], v[1]);
-            const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
-            l[k] = pc_h2(v[0] - b.x, v[1] - b.y);
-          }
-          const int piece = u * 4 + o;   // 16 bytes of the row; blocks of 64 values, rows of 128 bytes, swizzled
-          const int to16 = (piece >> 3) * 16384 + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(hi + to16) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(lo + to16) = make_uint4(l[0], l[1], l[2], l[3]);
+        for (int k = 0; k < 16; ++k) {
+          // codes 2k and 2k + 1 as 2^23 + c
+          const uint32_t w0 = BITS == 4 ? code[k >> 2] & 0x0F0F0F0Fu : code[k >> 1];
+          const uint32_t w1 = BITS == 4 ? (code[k >> 2] >> 4) & 0x0F0F0F0Fu : code[k >> 1];
+          const uint32_t c0 = __byte_perm(w0, 0x4B000000u, BITS == 4 ? 0x7440 + (k & 3) : 0x7440 + 2 * (k & 1));
+          const uint32_t c1 = __byte_perm(w1, 0x4B000000u, BITS == 4 ? 0x7440 + (k & 3) : 0x7441 + 2 * (k & 1));
+          const float2 c = __fadd2_rn(make_float2(__uint_as_float(c0), __uint_as_float(c1)), make_float2(-8388608.f, -8388608.f));
+          const float2 v = __ffma2_rn(make_float2(s, s), c, make_float2(z, z));
+          h[k] = pc_h2(v.x, v.y);
+          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+          const float2 d = __fadd2_rn(v, make_float2(-b.x, -b.y));
+          l[k] = pc_h2(d.x, d.y);
         }
+        tmem_st16(hi_t + 16 * u, h);
+        tmem_st16(lo_t + 16 * u, l);
       }
-      fence_proxy_async();
+      tmem_wait_st();
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.a_full[bc % G::AS]);
+      if (lane == 0) {
+        mbar_arrive(&sh.a_full[bc % G::AS]);
+        mbar_arrive(&sh.r_empty[st]);
+      }
     }
   } else if (warp == W_MMA) {
     // ============================================================================ one lane issues the products
     constexpr uint32_t ID = (1u << 4) | ((uint32_t)(kPvRows >> 3) << 17) | (8u << 24);   // M 128, N 128, fp16, fp32 sums
     const uint32_t one = pc_elect();
-    const uint32_t a_a = smem_addr(a_s), b_a = smem_addr(b_s);
+    const uint32_t b_a = smem_addr(b_s);
     bool ok = true;
-    for (; ok && w.here(p, to); ++w.x, ++bc) {
+    for (; ok && w.here(p, to); w.step(p), ++bc) {
       const int chunks = sh.chunk[w.b + 1] - sh.chunk[w.b];
       ok = wait_all(&sh.a_full[bc % G::AS], bc / G::AS);
       for (int c = w.first_chunk(p); ok && c < chunks; ++c, ++cc) {
@@ -375,12 +419,10 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
           const uint64_t b = pc_desc(b_a + (sc % G::BS) * G::SLICE, 16);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint64_t a = pc_desc(a_a + (bc % G::AS) * G::A + y * kPvKeys * D * 2 + sl * (SD / 64) * 16384, 16);
+            const uint32_t a = tmem + G::A_COL + (bc % G::AS) * D + y * (D / 2) + sl * (SD / 2);
 #pragma unroll
-            for (int x = 0; x < SD / 16; ++x) {
-              const uint32_t off = ((x >> 2) * 16384 + (x & 3) * 32) >> 4;
-              pc_mma_ss(one, tmem + 128 * buf, a + off, b + off, ID, sl > 0 || y > 0 || x > 0);
-            }
+            for (int x = 0; x < SD / 16; ++x)
+              pc_mma_ts(one, tmem + 128 * buf, a + 8 * x, b + (x * 32 >> 4), ID, sl > 0 || y > 0 || x > 0);
           }
           pc_commit(one, &sh.b_empty[sc % G::BS]);
         }
@@ -388,6 +430,38 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       }
       if (ok) pc_commit(one, &sh.a_empty[bc % G::AS]);
       __syncwarp();
+    }
+  } else if (warp == W_KEYS) {
+    // ============================================================================ codes, scales and biases: sixteen keys a lane
+    const uint64_t policy = policy_evict_first();
+    bool ok = true;
+    for (; ok && lane < 8 && w.here(p, to); w.step(p), ++bc) {
+      const int st = bc % kPvRaw, key = w.x * kPvKeys + 16 * lane;
+      const int pg = key < w.s.n ? __ldg(p.table + (size_t)w.b * p.max_pages + (key >> p.page_shift)) : -1;
+      const bool there = (unsigned)pg < (unsigned)p.num_pages;
+      const long long row = there ? qda_pool_row(pg, w.kvh, key & ((1 << p.page_shift) - 1), p.Hkv, p.page_shift) : -1;
+      if (!there && key < w.s.n) atomicOr(p.err, QDA_ERR_BIT_PAGED);
+      ok = wait(&sh.r_empty[st], bc / kPvRaw + 1);
+      if (!ok) break;
+      sh.row[bc & 7][lane] = row;   // (the exponential warps are at most six blocks behind)
+      unsigned char* dst = raw_s + st * K::RAW;
+      const uint32_t sb = 16 * p.NG * 2;
+      if (there) {
+        mbar_arrive_expect_tx(&sh.r_full[st], 16 * K::RB + 2 * sb);
+        bulk_g2s(dst + lane * 16 * K::RB, p.kp + row * (K::RB / 4), 16 * K::RB, &sh.r_full[st], policy);
+        bulk_g2s(dst + kPvKeys * K::RB + lane * sb, p.ks + row * p.NG, sb, &sh.r_full[st], policy);
+        bulk_g2s(dst + kPvKeys * K::RB + 8 * sb + lane * sb, p.kb + row * p.NG, sb, &sh.r_full[st], policy);
+      } else {
+        mbar_arrive(&sh.r_full[st]);
+      }
+    }
+    if (lane < 8 && (!ok || *abort)) {
+      // a wait gave up: copies under way land before the CTA's shared memory goes (one lane may wait for what another never
+      // began, until the limit)
+      for (uint32_t i = bc < (uint32_t)kPvRaw ? 0 : bc - kPvRaw; i < bc; ++i) {
+        volatile int none = 0;
+        mbar_wait_bounded(&sh.r_full[i % kPvRaw], (i / kPvRaw) & 1u, &none, p.err, 2u);
+      }
     }
   } else if (lane == 0) {
     // ============================================================================ operands and scalars of the chunks
@@ -399,7 +473,7 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       return x;
     }();
     bool ok = true;
-    for (; ok && w.here(p, to); ++w.x) {
+    for (; ok && w.here(p, to); w.step(p)) {
       const int c0 = sh.chunk[w.b], chunks = sh.chunk[w.b + 1] - c0;
       for (int c = w.first_chunk(p); ok && c < chunks; ++c, ++cc) {
         const char* src = p.chunks + ((size_t)(c0 + c) * p.Hkv + w.kvh) * G::CHUNK;
@@ -441,14 +515,14 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       mbar_wait_bounded(&sh.drain, 0, &none, p.err, 2u);
     }
     __syncwarp();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
 }
 
 template <int BITS, int D>
 cudaError_t pv_run(const QdaWeightsParams* p, bool prepare, cudaStream_t s) {
   auto kern = qda_paged_weights_tc_kernel<BITS, D>;
-  constexpr int smem = pv_smem<D>();
+  constexpr int smem = pv_smem<BITS, D>();
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   if (prepare) return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   cudaLaunchConfig_t cfg = {};
