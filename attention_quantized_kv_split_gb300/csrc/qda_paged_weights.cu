@@ -9,11 +9,11 @@
 
 namespace qda {
 
-constexpr int kPlThreads = 256;
+constexpr int kPlThreads = 512;
 
-// Each warp lays out the counted query rows of a sequence under a KV head, a CTA's warps sixteen to sixty-four: each row to fp16 times a power of two that
-// brings its largest value to [2^14, 2^15), in the swizzled form that the products read, and its scalars; rows behind the
-// sequence's last are zeros that weigh nothing. 2048 tokens of 32 heads of 128 values: 17 MB read, 18 written, all in L2.
+// A CTA lays out a chunk of counted query rows of a sequence under a KV head in the swizzled form that the products read, and
+// its scalars: the rows in fp16 times a power of two that brings the largest value of all of them to [2^14, 2^15), or of each
+// of them where they differ too much; rows behind the sequence's last are zeros that weigh nothing.
 template <int D>
 __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const __grid_constant__ QdaWeightsParams p) {
   using G = PvGeom<D>;
@@ -45,46 +45,75 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
     return;
   }
   const int kvh = blockIdx.y;
+  __shared__ int s_top[2];   // largest and smallest exponent of a row's largest value
   constexpr int LPR = D / 8 < 32 ? D / 8 : 32, RPW = 32 / LPR;   // a row takes D / 8 lanes of 8 values
-  constexpr int ROWS = kPlThreads / 32 * RPW, PARTS = kPvRows / ROWS;
-  for (long long x = blockIdx.x; x < (long long)carry * PARTS; x += gridDim.x) {
-    const int ci = (int)(x / PARTS);
+  constexpr int N = kPvRows / (kPlThreads / 32 * RPW);           // rows of a thread
+  for (int ci = blockIdx.x; ci < carry; ci += gridDim.x) {
     const int b = qda_seq_of(s_chunk, p.B, ci);
     const PwSeq s = pw_seq(p, b);
     const int row0 = (s.len - s.count) * p.nrep + (ci - s_chunk[b]) * kPvRows, row_end = s.len * p.nrep;
     char* dst = p.chunks + ((size_t)ci * p.Hkv + kvh) * G::CHUNK;
     PvScalars* scal = reinterpret_cast<PvScalars*>(dst + G::SLICES * G::SLICE);
-    {
-      const int i = (int)(x % PARTS) * ROWS + warp * RPW + lane / LPR, piece = lane % LPR;
-      const int row = row0 + i, tok = row / p.nrep, h = kvh * p.nrep + row - tok * p.nrep;
-      const bool real = row < row_end;
-      uint4 a = make_uint4(0, 0, 0, 0);
-      if (real)
-        a = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(s.first + tok) * p.q_tstride + (long long)h * p.q_hstride) + piece);
-      const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-      float2 f[4];
-      float top = 0.f;
+    if (tid == 0) {
+      s_top[0] = -1000;
+      s_top[1] = 1000;
+    }
+    __syncthreads();
+    const int piece = lane % LPR;
+    uint4 a[N];
+    float top[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int row = row0 + (j * (kPlThreads / 32) + warp) * RPW + lane / LPR, tok = row / p.nrep;
+      const int h = kvh * p.nrep + row - tok * p.nrep;
+      a[j] = make_uint4(0, 0, 0, 0);
+      if (row < row_end)
+        a[j] = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(s.first + tok) * p.q_tstride + (long long)h * p.q_hstride) + piece);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t u[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+      top[j] = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        f[k] = half2_bits_to_float2_rt(u[k], p.f16);
-        top = fmaxf(top, fmaxf(fabsf(f[k].x), fabsf(f[k].y)));
+        const float2 f = half2_bits_to_float2_rt(u[k], p.f16);
+        top[j] = fmaxf(top[j], fmaxf(fabsf(f.x), fabsf(f.y)));
       }
 #pragma unroll
-      for (int o = LPR / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = pv_up(top);
+      for (int o = LPR / 2; o >= 1; o >>= 1) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+      if (piece == 0 && top[j] > 0.f) {   // (zeros take any scale)
+        const int e = (int)(__float_as_uint(top[j]) >> 23);
+        atomicMax(&s_top[0], e);
+        atomicMin(&s_top[1], e);
+      }
+    }
+    __syncthreads();
+    // (an infinite value has the exponent 255: its row alone)
+    const bool near = s_top[0] < 255 && s_top[0] - s_top[1] <= kPvNear;
+    const int shared_up = near ? pv_up(__uint_as_float((uint32_t)max(s_top[0], 0) << 23)) : 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int i = (j * (kPlThreads / 32) + warp) * RPW + lane / LPR, row = row0 + i, tok = row / p.nrep;
+      const int h = kvh * p.nrep + row - tok * p.nrep;
+      const bool real = row < row_end;
+      const int e = near ? shared_up : pv_up(top[j]);
       const float up = pv_pow2(e);
+      const uint32_t u[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
       uint32_t w[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = pc_h2(f[k].x * up, f[k].y * up);
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = half2_bits_to_float2_rt(u[k], p.f16);
+        w[k] = pc_h2(f.x * up, f.y * up);
+      }
       // slices of SD dimensions; in them blocks of 64, rows of 128 bytes, 16-byte pieces swizzled
       const int sl = piece / (G::SD / 8), in = piece % (G::SD / 8);
       *reinterpret_cast<uint4*>(dst + sl * G::SLICE + (in >> 3) * 16384 + i * 128 + (((in & 7) ^ (i & 7)) << 4)) =
           make_uint4(w[0], w[1], w[2], w[3]);
       if (piece == 0) {
-        float* ml = reinterpret_cast<float*>(&scal->ml[i >> 1]);
-        ml[i & 1] = real ? p.qscale * pv_pow2(-e) : 0.f;
-        ml[2 + (i & 1)] = real ? p.lse[(long long)(s.first + tok) * p.H + h] * -1.4426950408889634f : -INFINITY;
-        reinterpret_cast<int*>(&scal->last[i >> 1])[i & 1] = real ? s.base + tok : -1;
+        scal->lse[i] = real ? p.lse[(long long)(s.first + tok) * p.H + h] * -1.4426950408889634f : -INFINITY;
+        scal->muls[i] = p.qscale * pv_pow2(-e);
+        scal->last[i] = real ? s.base + tok : -1;
+        if (i == 0) scal->mul = near ? p.qscale * pv_pow2(-e) : 0.f;
       }
     }
   }
@@ -119,7 +148,7 @@ static WeightsPlan weights_plan(int B, int nrep, int Hkv, int total_q, int max_q
 }  // namespace qda
 
 cudaError_t qda_paged_weights_lay(const QdaWeightsParams& p, cudaStream_t s) {
-  const dim3 grid((unsigned)std::min(p.max_chunks * 16LL, 1LL << 20), (unsigned)p.Hkv);
+  const dim3 grid((unsigned)std::min(p.max_chunks, 1 << 20), (unsigned)p.Hkv);
   switch (p.D) {
     case 64: qda::qda_paged_weights_lay_kernel<64><<<grid, qda::kPlThreads, 0, s>>>(p); break;
     case 128: qda::qda_paged_weights_lay_kernel<128><<<grid, qda::kPlThreads, 0, s>>>(p); break;

@@ -190,6 +190,9 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
   uint4* const ops = reinterpret_cast<uint4*>(smem + G::RING);
 
   // ---- the line of work: every CTA scans the lengths for itself
+  auto work = [&](const PwSeq& s, int i) {
+    return pw_prefix<kPwKeys>(p, s, i, kPwCost + (long long)s.count * p.nrep, kPwCost);
+  };
   long long carry = 0;
   if (tid == 0) s_at[0] = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPwWarps * 32) {
@@ -198,7 +201,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
     if (b < p.B) {
       const int start = p.q_start[b], end = p.q_start[b + 1], n = p.kv_len[b];
       const PwSeq s = pw_seq(p, start, end, n);
-      v = p.Hkv * pw_prefix<kPwKeys, kPwCost>(p, s, pw_blocks<kPwKeys>(s));
+      v = p.Hkv * work(s, pw_blocks<kPwKeys>(s));
       if (blockIdx.x == 0 && pw_bad(p, start, end, n, s)) atomicOr(p.err, QDA_ERR_BIT_PAGED);
     }
 #pragma unroll
@@ -225,13 +228,14 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
   int b = qda_seq_of(s_at, p.B, from);
   PwSeq s = pw_seq(p, b);
   int blocks = pw_blocks<kPwKeys>(s);
-  long long head = pw_prefix<kPwKeys, kPwCost>(p, s, blocks);
+  long long head = work(s, blocks);
   int kvh = (int)((from - s_at[b]) / head);
   long long at = s_at[b] + kvh * head;   // the KV head's place on the line
+  auto block_at = [&](long long x) { return pw_block_at(blocks, x, [&](int i) { return at + work(s, i); }); };
   const int pmask = (1 << p.page_shift) - 1;
-  int x0 = pw_block_at<kPwKeys, kPwCost>(p, s, blocks, at, from);
+  int x0 = block_at(from);
   while (true) {
-    const int x1 = at + head <= to ? blocks : pw_block_at<kPwKeys, kPwCost>(p, s, blocks, at, to);
+    const int x1 = at + head <= to ? blocks : block_at(to);
     if (x0 < x1) {
       const int* tab = p.table + (size_t)b * p.max_pages;
       const int t1 = min(x1 * kPwWarps, (s.n + 15) >> 4);
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
         s = pw_seq(p, b);
         blocks = pw_blocks<kPwKeys>(s);
       } while (blocks == 0);
-      head = pw_prefix<kPwKeys, kPwCost>(p, s, blocks);
+      head = work(s, blocks);
     }
     if (at >= to) return;
   }

@@ -63,24 +63,26 @@ __device__ __forceinline__ int pw_blocks(const PwSeq& s) {
   return s.len > 0 ? (int)(((long long)s.n + KEYS - 1) / KEYS) : 0;
 }
 
-// Work of the first i key blocks under one KV head, in query rows (COST: a block's work beside them). A block's rows are those
-// of the counted tokens that see its first key: min(count, n - i KEYS), all of them until the causal edge.
-template <int KEYS, int COST>
-__device__ __forceinline__ long long pw_prefix(const QdaWeightsParams& p, const PwSeq& s, int i) {
-  long long flat = s.n >= s.count ? ((long long)s.n - s.count) / KEYS + 1 : 0;
-  flat = min(flat, (long long)i);
-  const long long rest = i - flat;
-  const long long rows = flat * s.count + rest * s.n - KEYS * (((long long)i * (i - 1) - flat * (flat - 1)) / 2);
-  return (long long)i * COST + rows * p.nrep;
+// Work of the first i blocks of KEYS keys under one KV head, in query rows: a block whose first key every counted token sees
+// takes `whole`, one behind the causal edge `edge` and the rows of the tokens that see its first key (n - x KEYS of them).
+template <int KEYS>
+__device__ __forceinline__ int pw_flat(const PwSeq& s) {   // blocks of the first kind
+  return s.n >= s.count ? (s.n - s.count) / KEYS + 1 : 0;
+}
+template <int KEYS>
+__device__ __forceinline__ long long pw_prefix(const QdaWeightsParams& p, const PwSeq& s, int i, long long whole, int edge) {
+  const long long flat = min(pw_flat<KEYS>(s), i), rest = i - flat;
+  return flat * whole + rest * edge +
+         p.nrep * (rest * s.n - KEYS * (((long long)i * (i - 1) - flat * (flat - 1)) / 2));
 }
 
-// First block under the KV head at place `at` of the line that starts at or behind x.
-template <int KEYS, int COST>
-__device__ __forceinline__ int pw_block_at(const QdaWeightsParams& p, const PwSeq& s, int blocks, long long at, long long x) {
+// First of `blocks` blocks that starts at or behind x, where prefix(i) is the place of block i.
+template <typename F>
+__device__ __forceinline__ int pw_block_at(int blocks, long long x, F&& prefix) {
   int lo = 0, hi = blocks;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (at + pw_prefix<KEYS, COST>(p, s, mid) >= x) hi = mid; else lo = mid + 1;
+    if (prefix(mid) >= x) hi = mid; else lo = mid + 1;
   }
   return lo;
 }

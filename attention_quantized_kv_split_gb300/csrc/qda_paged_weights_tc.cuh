@@ -13,7 +13,7 @@
 //                        the key's scale;
 //   row loader           one lane: a chunk's operands and scalars, laid out by the kernel ahead, by bulk copies into a ring;
 //   MMA warp             one lane issues every product; two accumulators of 128 columns take turns;
-//   exponential warps    eight: a thread per key and half of a chunk's columns.
+//   exponential warps    sixteen: four threads per key, a quarter of a chunk's columns each.
 // Every link is an mbarrier; every wait is bounded and sets the device error word, and after one that gave up every role ends.
 #pragma once
 
@@ -23,14 +23,22 @@
 namespace qda {
 
 constexpr int kPvKeys = 128;
-constexpr int kPvCost = 48;    // work of a block beside its query rows, in query rows
-constexpr int kPvExp = 8, kPvDeq = 8, kPvWarps = kPvExp + kPvDeq + 3;
+// Work of a block beside its query rows, in query rows. Ragged chunks at D 256 take 260 us with 64, 237 with 128, 221 with 200,
+// 223 with 300, 225 with 450.
+constexpr int kPvCost = 240;
+constexpr int kPvExp = 16, kPvDeq = 8, kPvWarps = kPvExp + kPvDeq + 3;
+constexpr int kPvParts = kPvExp / 4, kPvCols = kPvRows / kPvParts;   // threads of a key, columns of each
 constexpr int kPvScalars = 3;  // chunks' scalars in flight
 
-// A chunk's scalars: pairs of rows side by side.
+// A chunk's scalars. Rows of a chunk share a power of two where the largest values of all of them lie within 2^kPvNear (they
+// then lose no more than that of the 39 bits' room below): what undoes it and the softmax scale is `mul`; else mul is 0 and
+// every row has its own.
+constexpr int kPvNear = 12;
 struct PvScalars {
-  float4 ml[kPvRows / 2];      // what undoes a row's scale times the softmax scale, twice; minus its lse in log2 units, twice
-  int2 last[kPvRows / 2];      // last key that the row sees; -1: no row
+  float lse[kPvRows];          // minus a row's lse in log2 units; -inf: no row
+  float muls[kPvRows];         // what undoes a row's scale, times the softmax scale
+  int last[kPvRows];           // last key that the row sees; -1: no row
+  float mul, pad[3];
 };
 
 constexpr int kPvRaw = 3;      // blocks' codes in flight
@@ -57,6 +65,11 @@ __device__ __forceinline__ int pv_chunks(const QdaWeightsParams& p, const PwSeq&
   return s.n > 0 ? (int)(((long long)s.count * p.nrep + kPvRows - 1) / kPvRows) : 0;
 }
 
+// Work of the first i blocks of a sequence under one KV head: the rows of a block's chunks, the last one as if it were full.
+__device__ __forceinline__ long long pv_prefix(const QdaWeightsParams& p, const PwSeq& s, int i) {
+  return pw_prefix<kPvKeys>(p, s, i, kPvCost + (long long)pv_chunks(p, s) * kPvRows, kPvCost + kPvRows);
+}
+
 // Where a CTA stands on its piece of the line: at a block of keys. Every role walks for itself.
 struct PvWalk {
   int b, kvh, x, blocks;
@@ -67,11 +80,11 @@ struct PvWalk {
     b = qda_seq_of(line, p.B, from);
     s = pw_seq(p, b);
     blocks = pw_blocks<kPvKeys>(s);
-    const long long head = pw_prefix<kPvKeys, kPvCost>(p, s, blocks);
+    const long long head = pv_prefix(p, s, blocks);
     kvh = (int)((from - line[b]) / head);
     const long long at = line[b] + kvh * head;
-    x = pw_block_at<kPvKeys, kPvCost>(p, s, blocks, at, from);
-    pos = at + pw_prefix<kPvKeys, kPvCost>(p, s, x);
+    x = pw_block_at(blocks, from, [&](int i) { return at + pv_prefix(p, s, i); });
+    pos = at + pv_prefix(p, s, x);
   }
   // The block at hand, or the next one that there is; false behind the piece.
   __device__ __forceinline__ bool here(const QdaWeightsParams& p, long long to) {
@@ -90,7 +103,8 @@ struct PvWalk {
     return true;
   }
   __device__ __forceinline__ void step(const QdaWeightsParams& p) {
-    pos += kPvCost + (long long)p.nrep * min(s.count, s.n - x * kPvKeys);   // as pw_prefix has it
+    pos += kPvCost + (x < pw_flat<kPvKeys>(s) ? (long long)pv_chunks(p, s) * kPvRows   // as pv_prefix has it
+                                              : kPvRows + (long long)p.nrep * (s.n - x * kPvKeys));
     ++x;
   }
   // The chunks whose rows see the block's first key: from this one to the sequence's last.
@@ -99,12 +113,12 @@ struct PvWalk {
     return (int)(((long long)before * p.nrep) >> 7);
   }
 };
-static_assert(kPvRows == 128, "first_chunk");
+static_assert(kPvRows == 128 && kPvCols == 32, "first_chunk; columns of a load");
 
 struct PvShared {
   PvScalars scal[kPvScalars];
   float kmul[2][kPvKeys];
-  float part[2][kPvKeys];      // the second half's sums, by a block's parity
+  float part[2][kPvParts - 1][kPvKeys];   // sums of a key's other threads, by a block's parity
   long long at[QDA_MAX_B + 1]; // sequences on the line of work
   int chunk[QDA_MAX_B + 1];    // chunks before each sequence
   PvWalk walk;
@@ -148,8 +162,8 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       mbar_init(&sh.a_empty[i], 1 + kPvExp);
       mbar_init(&sh.d_full[i], 1);
       mbar_init(&sh.d_empty[i], kPvExp);
-      mbar_init(&sh.p_full[i], kPvExp / 2);
-      mbar_init(&sh.p_empty[i], kPvExp / 2);
+      mbar_init(&sh.p_full[i], kPvExp - 4);
+      mbar_init(&sh.p_empty[i], 4);
     }
     for (int i = 0; i < 8; ++i) {
       mbar_init(&sh.b_full[i], 1);
@@ -179,7 +193,7 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
     if (b < p.B) {
       const int start = p.q_start[b], end = p.q_start[b + 1], n = p.kv_len[b];
       const PwSeq s = pw_seq(p, start, end, n);
-      v = p.Hkv * pw_prefix<kPvKeys, kPvCost>(p, s, pw_blocks<kPvKeys>(s));
+      v = p.Hkv * pv_prefix(p, s, pw_blocks<kPvKeys>(s));
       c = pv_chunks(p, s);
       if (blockIdx.x == 0 && pw_bad(p, start, end, n, s)) atomicOr(p.err, QDA_ERR_BIT_PAGED);
     }
@@ -232,9 +246,9 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
   // blocks, chunks and slices so far: every role counts them for itself
   uint32_t bc = 0, cc = 0, sc = 0;
   if (warp < kPvExp) {
-    // ============================================================================ exponentials: two threads per key
-    const int half = warp >> 2, r = 32 * (warp & 3) + lane;
-    const uint32_t d_t = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 64 * half;
+    // ============================================================================ exponentials: some threads per key
+    const int part = warp >> 2, r = 32 * (warp & 3) + lane;
+    const uint32_t d_t = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kPvCols * part;
     for (; w.here(p, to); w.step(p), ++bc) {
       const int key = w.x * kPvKeys + r;
       const int first_tok = w.s.len - w.s.count;
@@ -246,8 +260,7 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.a_empty[bc % G::AS]);
       float old = 0.f;
-      if (half == 0 && keep) old = p.mass[row];
-      const float2 km2 = make_float2(km, km);
+      if (part == 0 && keep) old = p.mass[row];
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool ok = true;
 #pragma unroll 1
@@ -256,55 +269,48 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
         ok = wait_all(&sh.c_full[ps], cc / kPvScalars) && wait_all(&sh.d_full[buf], cc >> 1);
         if (!ok) break;
         tc_fence_after();
-        const float4* ml = sh.scal[ps].ml + 32 * half;
-        const int2* last = sh.scal[ps].last + 32 * half;
+        const PvScalars& f = sh.scal[ps];
         // all of the chunk's rows see all of the block's keys: the last key against the first row's token
         const bool open = (long long)(w.x * kPvKeys + kPvKeys - 1 - w.s.base - first_tok) * p.nrep <= (long long)c * kPvRows;
-        // 32 columns at a time, in loops that stay small: with everything unrolled the warps' roles pushed each other out of
-        // the instruction cache
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          float v[32];
-          pc_ld32(d_t + 128 * buf + 32 * q, v);
-          tmem_wait_ld();
-          if (q == 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
-          }
+        float v[kPvCols];
+        pc_ld32(d_t + 128 * buf, v);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
+        float one = km * f.mul;
+        if (f.mul == 0.f) {   // rare: rows with scales of their own
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float4 m = ml[16 * q + i];
-            const float2 s2 = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), km2);
-            const float2 e = __ffma2_rn(s2, make_float2(m.x, m.y), make_float2(m.z, m.w));
-            v[2 * i] = pc_ex2(e.x);
-            v[2 * i + 1] = pc_ex2(e.y);
-          }
-          if (!open) {
+          for (int i = 0; i < kPvCols; ++i) v[i] *= km * f.muls[kPvCols * part + i];
+          one = 1.f;
+        }
+        if (!open) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int2 t = last[16 * q + i];
-              if (key > t.x) v[2 * i] = 0.f;
-              if (key > t.y) v[2 * i + 1] = 0.f;
-            }
-          }
+          for (int i = 0; i < kPvCols; ++i) v[i] = key > f.last[kPvCols * part + i] ? -INFINITY : v[i];
+        }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) sum[i & 1] = __fadd2_rn(sum[i & 1], make_float2(v[2 * i], v[2 * i + 1]));
+        for (int i = 0; i < kPvCols / 4; ++i) {
+          const float4 m = *reinterpret_cast<const float4*>(f.lse + kPvCols * part + 4 * i);
+          const float2 e0 = __ffma2_rn(make_float2(v[4 * i], v[4 * i + 1]), make_float2(one, one), make_float2(m.x, m.y));
+          const float2 e1 = __ffma2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(one, one), make_float2(m.z, m.w));
+          sum[0] = __fadd2_rn(sum[0], make_float2(pc_ex2(e0.x), pc_ex2(e0.y)));
+          sum[1] = __fadd2_rn(sum[1], make_float2(pc_ex2(e1.x), pc_ex2(e1.y)));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.c_empty[ps]);
       }
       if (!ok) break;
       float add = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      if (half == 1) {   // the other half's threads take it from here
+      if (part > 0) {   // the key's first thread takes it from here
         if (!wait_all(&sh.p_empty[bc & 1], (bc >> 1) + 1)) break;
-        sh.part[bc & 1][r] = add;
+        sh.part[bc & 1][part - 1][r] = add;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_full[bc & 1]);
         continue;
       }
       if (!wait_all(&sh.p_full[bc & 1], bc >> 1)) break;
-      add += sh.part[bc & 1][r];
+#pragma unroll
+      for (int i = 0; i < kPvParts - 1; ++i) add += sh.part[bc & 1][i][r];
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.p_empty[bc & 1]);
       if (keep) {
@@ -372,18 +378,27 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
         const uint32_t s2 = g < 4 ? (g < 2 ? sw[0] : sw[1]) : (g < 6 ? sw[2] : sw[3]);
         const uint32_t z2 = g < 4 ? (g < 2 ? bw[0] : bw[1]) : (g < 6 ? bw[2] : bw[3]);
         // (a key that is not there has scale and bias 0)
-        const float s = half_bits_to_float_rt((s2 >> (16 * (g & 1))) & 0xffffu, p.f16) * up;
-        const float z = half_bits_to_float_rt((z2 >> (16 * (g & 1))) & 0xffffu, p.f16) * up;
+        float s = half_bits_to_float_rt((s2 >> (16 * (g & 1))) & 0xffffu, p.f16) * up;
+        float z = half_bits_to_float_rt((z2 >> (16 * (g & 1))) & 0xffffu, p.f16) * up;
+        if constexpr (BITS == 4) {
+          z = fmaf(s, -16.f, z);
+          s *= 16.f;
+        }
         uint32_t h[16], l[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          // codes 2k and 2k + 1 as 2^23 + c
-          const uint32_t w0 = BITS == 4 ? code[k >> 2] & 0x0F0F0F0Fu : code[k >> 1];
-          const uint32_t w1 = BITS == 4 ? (code[k >> 2] >> 4) & 0x0F0F0F0Fu : code[k >> 1];
-          const uint32_t c0 = __byte_perm(w0, 0x4B000000u, BITS == 4 ? 0x7440 + (k & 3) : 0x7440 + 2 * (k & 1));
-          const uint32_t c1 = __byte_perm(w1, 0x4B000000u, BITS == 4 ? 0x7440 + (k & 3) : 0x7441 + 2 * (k & 1));
-          const float2 c = __fadd2_rn(make_float2(__uint_as_float(c0), __uint_as_float(c1)), make_float2(-8388608.f, -8388608.f));
-          const float2 v = __ffma2_rn(make_float2(s, s), c, make_float2(z, z));
+          float2 v;
+          if constexpr (BITS == 4) {   // codes as 1 + c / 16: z - 16 s is rounded once, by no more than the value itself may be
+            const uint32_t w0 = ((code[k >> 2] << 3) & 0x78787878u) | 0x80808080u, w1 = ((code[k >> 2] >> 1) & 0x78787878u) | 0x80808080u;
+            const float2 c = make_float2(__uint_as_float(__byte_perm(w0, 0x3F000000u, 0x7044 + ((k & 3) << 8))),
+                                         __uint_as_float(__byte_perm(w1, 0x3F000000u, 0x7044 + ((k & 3) << 8))));
+            v = __ffma2_rn(make_float2(s, s), c, make_float2(z, z));
+          } else {                     // 2^23 + c, less 2^23
+            const float2 c = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(code[k >> 1], 0x4B000000u, 0x7440 + 2 * (k & 1))),
+                                                    __uint_as_float(__byte_perm(code[k >> 1], 0x4B000000u, 0x7441 + 2 * (k & 1)))),
+                                        make_float2(-8388608.f, -8388608.f));
+            v = __ffma2_rn(make_float2(s, s), c, make_float2(z, z));
+          }
           h[k] = pc_h2(v.x, v.y);
           const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
           const float2 d = __fadd2_rn(v, make_float2(-b.x, -b.y));
