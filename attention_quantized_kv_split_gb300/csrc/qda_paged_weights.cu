@@ -185,10 +185,10 @@ extern "C" int qdecode_paged_weights(const void* q, long long q_tstride, long lo
   if (B > QDA_MAX_B || nrep > QDA_MAX_NREP) return QDA_ERR_UNSUPPORTED;
   if ((long long)num_pages * page * Hkv >= 0xffffffffLL) return QDA_ERR_UNSUPPORTED;
   if ((long long)total_q * nrep > 0x7fffff00LL) return QDA_ERR_UNSUPPORTED;
-  const void* ptrs[4] = {q, k_packed, k_scales, k_biases};
+  const void* ptrs[5] = {q, k_packed, k_scales, k_biases, mass};
   for (const void* p : ptrs)
     if (off16(p)) return QDA_ERR_ALIGN;
-  const void* words[7] = {lse, mass, token, q_start, kv_len, block_table, shift};
+  const void* words[6] = {lse, token, q_start, kv_len, block_table, shift};
   for (const void* p : words)
     if (off4(p)) return QDA_ERR_ALIGN;
   if (q_tstride % 8 || q_hstride % 8) return QDA_ERR_ALIGN;
@@ -255,9 +255,10 @@ extern "C" int qdecode_paged_weights(const void* q, long long q_tstride, long lo
     return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
   }
   const int di = D == 64 ? 0 : D == 128 ? 1 : D == 256 ? 2 : 3, gi = GS == 32 ? 0 : GS == 64 ? 1 : 2;
-  static std::atomic<int> cache[64][2][4][3][2] = {};
-  std::atomic<int>& slot = cache[dev][bits == 8][di][gi][rows > 8];
-  const auto launch = bits == 4 ? qda_paged_weights_b4 : qda_paged_weights_b8;
+  static std::atomic<int> cache[64][2][2][4][3][2] = {};
+  std::atomic<int>& slot = cache[dev][bits == 8][p.f16][di][gi][rows > 8];
+  const auto launch = bits == 4 ? (p.f16 ? qda_paged_weights_b4_f1 : qda_paged_weights_b4_f0)
+                                : (p.f16 ? qda_paged_weights_b8_f1 : qda_paged_weights_b8_f0);
   int occ = slot.load();
   if (occ == 0) {
     const cudaError_t e = launch(nullptr, D, GS, rows, &occ, nullptr);

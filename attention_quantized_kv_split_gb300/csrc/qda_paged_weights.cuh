@@ -18,8 +18,7 @@
 namespace qda {
 
 constexpr int kPwWarps = 4;
-constexpr int kPwKeys = 16 * kPwWarps;   // keys of a block
-constexpr int kPwCost = 24;              // work of a block beside its query rows (codes, mass, tokens), in query rows
+constexpr int kPwCost = 24;    // work of 64 keys beside their query rows (codes, mass, tokens), in query rows
 
 template <int BITS, int D, int GS, int NT>
 struct PwGeom {
@@ -28,14 +27,17 @@ struct PwGeom {
   static constexpr int WPU = BITS / 4;           // words of such a unit
   static constexpr int UNITS = D / 32;           // units of a row per lane: two k-steps each
   static constexpr int ROWS = 8 * NT;
+  static constexpr int T = NT == 1 ? 2 : 1;      // sixteens of keys that a warp takes at a time
+  static constexpr int KEYS = 16 * T * kPwWarps; // keys of a block
   static constexpr int RB = W * 4, CPR = RB / 16;   // bytes and 16-byte chunks of a row of codes
-  // a warp's stage: sixteen keys' codes, scales, biases, masses
-  static constexpr int SC = 16 * NG * 2, STAGE = 16 * RB + 2 * SC + 64;
+  // a warp's stage: its keys' codes, scales, biases, masses, sixteen by sixteen
+  static constexpr int SC = 16 * NG * 2, SUB = 16 * RB + 2 * SC + 64, STAGE = T * SUB;
   static constexpr int STAGES = STAGE <= 3000 ? 4 : STAGE <= 6000 ? 3 : 2;
   static constexpr int RING = kPwWarps * STAGES * STAGE;
   static constexpr int OPS = NT * UNITS * 32 * 16;
   static constexpr int SMEM = RING + OPS;
-  static constexpr int MINB = D >= 512 ? 2 : NT == 1 ? (D == 256 ? 4 : 6) : 3;   // resident CTAs per SM
+  static constexpr int MINB = D >= 512 ? 2 : NT == 1 ? (D == 256 ? 4 : 5) : 3;   // resident CTAs per SM
+  static constexpr int COST = kPwCost * KEYS / 64;
 };
 
 // Where 16-byte chunk ch of row r of a tile's codes lies: chunks of a row are permuted by the row's bits in reverse, so that
@@ -81,18 +83,34 @@ __device__ __forceinline__ void pw_lds(const char* p, uint32_t (&v)[N]) {
   }
 }
 
+// Half word i of words of 16-bit values, as a float.
+template <bool F16, int N>
+__device__ __forceinline__ float pw_half(const uint32_t (&w)[N], int i) {
+  if constexpr (F16) {
+    const __half2 h = *reinterpret_cast<const __half2*>(&w[i >> 1]);
+    return i & 1 ? __high2float(h) : __low2float(h);
+  } else {
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+}
+
 __device__ __forceinline__ float pw_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
+// c (+)= a b; without `more` the sums start from 0
 __device__ __forceinline__ void pw_mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                       uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+                                       uint32_t b1, bool more) {
+  if (more)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 template <int NT, int NG>
@@ -103,7 +121,7 @@ struct PwRows {
 };
 
 // The CTA: operands and scalars of query rows row .. row + ROWS - 1 of sequence s under KV head kvh.
-template <int BITS, int D, int GS, int NT>
+template <int BITS, int D, int GS, int NT, bool F16>
 __device__ __forceinline__ void pw_rows(const QdaWeightsParams& p, const PwSeq& s, int kvh, int row, uint4* ops,
                                         PwRows<NT, D / GS>& sh) {
   using G = PwGeom<BITS, D, GS, NT>;
@@ -122,11 +140,9 @@ __device__ __forceinline__ void pw_rows(const QdaWeightsParams& p, const PwSeq& 
       if (real && o < OCT) w = __ldg(reinterpret_cast<const uint4*>(src) + o);
       const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = half2_bits_to_float2_rt(u[j], p.f16);
-        v[i][2 * j] = f.x;
-        v[i][2 * j + 1] = f.y;
-        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] = pw_half<F16>(u, j);
+        top = fmaxf(top, fabsf(v[i][j]));
       }
     }
 #pragma unroll
@@ -167,20 +183,20 @@ __device__ __forceinline__ void pw_rows(const QdaWeightsParams& p, const PwSeq& 
       const int nt = r >> 3, c = (r & 7) >> 1;
       reinterpret_cast<float*>(&sh.mul[nt][c])[r & 1] = p.qscale * exp2f((float)(24 - e));
       reinterpret_cast<float*>(&sh.lse[nt][c])[r & 1] =
-          real ? p.lse[(long long)(s.first + tok) * p.H + h] * 1.4426950408889634f : 0.f;
+          real ? p.lse[(long long)(s.first + tok) * p.H + h] * 1.4426950408889634f : INFINITY;   // (no row weighs nothing)
       reinterpret_cast<int*>(&sh.last[nt][c])[r & 1] = real ? s.base + tok : -1;
     }
   }
 }
 
-// Few query rows: every warp streams tiles of sixteen keys through a ring of its own in shared memory, asynchronous copies
-// three tiles ahead, and the query rows of the CTA's (sequence, KV head) stay in shared memory as operands. With more rows
-// than ROWS the CTA's warps take a block of tiles together and the rows pass by, ROWS at a time.
-template <int BITS, int D, int GS, int NT>
+// Few query rows: every warp streams tiles of 16 T keys through a ring of its own in shared memory, asynchronous copies tiles
+// ahead, and the query rows of the CTA's (sequence, KV head) stay in shared memory as operands. With more rows than ROWS the
+// CTA's warps take a block of tiles together and the rows pass by, ROWS at a time.
+template <int BITS, int D, int GS, int NT, bool F16>
 __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
     qda_paged_weights_kernel(const __grid_constant__ QdaWeightsParams p) {
   using G = PwGeom<BITS, D, GS, NT>;
-  constexpr int NG = G::NG, UPL = G::UPL, WPU = G::WPU, ROWS = G::ROWS, S = G::STAGES;
+  constexpr int NG = G::NG, UPL = G::UPL, WPU = G::WPU, ROWS = G::ROWS, S = G::STAGES, T = G::T, RB = G::RB;
   extern __shared__ __align__(16) char smem[];
   __shared__ long long s_at[QDA_MAX_B + 1];   // sequences on the line of work
   __shared__ long long s_tot[kPwWarps];
@@ -191,7 +207,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
 
   // ---- the line of work: every CTA scans the lengths for itself
   auto work = [&](const PwSeq& s, int i) {
-    return pw_prefix<kPwKeys>(p, s, i, kPwCost + (long long)s.count * p.nrep, kPwCost);
+    return pw_prefix<G::KEYS>(p, s, i, G::COST + (long long)s.count * p.nrep, G::COST);
   };
   long long carry = 0;
   if (tid == 0) s_at[0] = 0;
@@ -201,7 +217,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
     if (b < p.B) {
       const int start = p.q_start[b], end = p.q_start[b + 1], n = p.kv_len[b];
       const PwSeq s = pw_seq(p, start, end, n);
-      v = p.Hkv * work(s, pw_blocks<kPwKeys>(s));
+      v = p.Hkv * work(s, pw_blocks<G::KEYS>(s));
       if (blockIdx.x == 0 && pw_bad(p, start, end, n, s)) atomicOr(p.err, QDA_ERR_BIT_PAGED);
     }
 #pragma unroll
@@ -227,190 +243,221 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
   // ---- the CTA's piece, a (sequence, KV head) at a time: the blocks that start in it
   int b = qda_seq_of(s_at, p.B, from);
   PwSeq s = pw_seq(p, b);
-  int blocks = pw_blocks<kPwKeys>(s);
+  int blocks = pw_blocks<G::KEYS>(s);
   long long head = work(s, blocks);
   int kvh = (int)((from - s_at[b]) / head);
   long long at = s_at[b] + kvh * head;   // the KV head's place on the line
   auto block_at = [&](long long x) { return pw_block_at(blocks, x, [&](int i) { return at + work(s, i); }); };
   const int pmask = (1 << p.page_shift) - 1;
   int x0 = block_at(from);
+  constexpr int LPS = 32 / T;                 // lanes that fetch a sixteen of keys
+  const int fsub = lane / LPS, fl = lane % LPS;
   while (true) {
     const int x1 = at + head <= to ? blocks : block_at(to);
     if (x0 < x1) {
       const int* tab = p.table + (size_t)b * p.max_pages;
-      const int t1 = min(x1 * kPwWarps, (s.n + 15) >> 4);
+      // sixteen keys `t` of the sequence: their page (-1: behind the sequence or this piece)
+      const int t1 = min(x1 * (T * kPwWarps), (s.n + 15) >> 4);
       auto page_of = [&](int t) { return t < t1 ? __ldg(tab + (t * 16 >> p.page_shift)) : -1; };
       auto row_of = [&](int t, int pg) { return qda_pool_row(pg, kvh, (t * 16) & pmask, p.Hkv, p.page_shift); };
-      // sixteen keys on their way into a stage (a page outside the pool: nothing is read)
+      // a tile on its way into a stage (a page outside the pool: nothing is read); pg: the page of this lane's sixteen
       auto fetch = [&](int t, int pg, int st) {
-        if (t < t1 && (unsigned)pg < (unsigned)p.num_pages) {
-          const long long row = row_of(t, pg);
-          const uint32_t dst = smem_addr(ring + st * G::STAGE);
-          const char* src = reinterpret_cast<const char*>(p.kp + row * G::W);
+        if ((unsigned)pg < (unsigned)p.num_pages) {
+          const long long row = row_of(t + fsub, pg);
+          const uint32_t dst = smem_addr(ring + st * G::STAGE + fsub * G::SUB);
+          const char* src = reinterpret_cast<const char*>(p.kp + row * G::W) + 16 * fl;
 #pragma unroll
-          for (int i = 0; i < (16 * G::CPR + 31) / 32; ++i) {
-            const int c = i * 32 + lane;
-            if (16 * G::CPR >= 32 || c < 16 * G::CPR)
-              pw_copy16(dst + pw_chunk<G::RB>(c / G::CPR, c % G::CPR), src + 16 * c);
+          for (int i = 0; i < (16 * G::CPR + LPS - 1) / LPS; ++i) {
+            const int c = i * LPS + fl;
+            if (16 * G::CPR >= LPS || c < 16 * G::CPR)
+              pw_copy16(dst + pw_chunk<RB>(c / G::CPR, c % G::CPR), src + 16 * LPS * i);
           }
-          constexpr int CS = G::SC / 16;   // chunks of the scales, and of the biases
-          if (lane < 2 * CS)
-            pw_copy16(dst + 16 * G::RB + 16 * lane,
-                      reinterpret_cast<const char*>((lane < CS ? p.ks : p.kb) + row * NG) + 16 * (lane < CS ? lane : lane - CS));
-          if (2 * CS > 32 && lane + 32 < 2 * CS)
-            pw_copy16(dst + 16 * G::RB + 16 * (lane + 32), reinterpret_cast<const char*>(p.kb + row * NG) + 16 * (lane + 32 - CS));
-          if (lane < 16) pw_copy4(dst + 16 * G::RB + 2 * G::SC + 4 * lane, p.mass + row + lane);
+          constexpr int CS = G::SC / 16, REST = 2 * CS + 4;   // chunks of the scales, the biases, the masses
+#pragma unroll
+          for (int i = 0; i < (REST + LPS - 1) / LPS; ++i) {
+            const int c = i * LPS + fl;
+            const char* from = c < CS ? reinterpret_cast<const char*>(p.ks + row * NG) + 16 * c
+                               : c < 2 * CS ? reinterpret_cast<const char*>(p.kb + row * NG) + 16 * (c - CS)
+                                            : reinterpret_cast<const char*>(p.mass + row) + 16 * (c - 2 * CS);
+            if (c < REST) pw_copy16(dst + 16 * RB + 16 * c, from);
+          }
         }
         pw_commit();
       };
       const int first = (s.len - s.count) * p.nrep, r_hi = s.len * p.nrep;
-      int t = x0 * kPwWarps + warp;
-      int pages[S];   // of the tiles in flight, and the next one's
+      int t = x0 * (T * kPwWarps) + warp * T;
+      int pages[S];   // of this lane's sixteen of the tiles in flight, and of the next one
 #pragma unroll
-      for (int i = 0; i < S; ++i) pages[i] = page_of(t + i * kPwWarps);
+      for (int i = 0; i < S; ++i) pages[i] = page_of(t + i * (T * kPwWarps) + fsub);
 #pragma unroll
-      for (int i = 0; i < S - 1; ++i) fetch(t + i * kPwWarps, pages[i], i);
+      for (int i = 0; i < S - 1; ++i) fetch(t + i * (T * kPwWarps), pages[i], i);
       const bool many = r_hi - first > ROWS;
       if (!many) {
         __syncthreads();   // the operands of before are read
-        pw_rows<BITS, D, GS, NT>(p, s, kvh, first, ops, rows);
+        pw_rows<BITS, D, GS, NT, F16>(p, s, kvh, first, ops, rows);
         __syncthreads();
       }
+      // keys up to here are seen by every counted row
+      const int open = s.base + s.len - s.count;
       int st = 0;
-      for (int step = x0; step < x1; ++step, t += kPwWarps) {
-        {   // the stage before this one's is free again
-          const int far = t + (S - 1) * kPwWarps;
-          fetch(far, pages[S - 1], st == 0 ? S - 1 : st - 1);
-        }
+#pragma unroll 1
+      for (int step = x0; step < x1; ++step, t += T * kPwWarps) {
+        fetch(t + (S - 1) * (T * kPwWarps), pages[S - 1], st == 0 ? S - 1 : st - 1);   // into the stage that was read last
         pw_wait<S - 1>();
         __syncwarp();
         const int pg = pages[0];
-        const bool there = t < t1 && (unsigned)pg < (unsigned)p.num_pages;
-        if (t < t1 && !there && lane == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);
 #pragma unroll
         for (int i = 0; i < S - 1; ++i) pages[i] = pages[i + 1];
-        pages[S - 1] = page_of(t + S * kPwWarps);
+        pages[S - 1] = page_of(t + S * (T * kPwWarps) + fsub);
+        const bool mine = (unsigned)pg < (unsigned)p.num_pages;
+        if (!mine && t + fsub < t1) atomicOr(p.err, QDA_ERR_BIT_PAGED);
+        const bool any = __any_sync(0xffffffffu, mine);
         const char* const stage = ring + st * G::STAGE;
         st = st == S - 1 ? 0 : st + 1;
         const int key0 = t * 16;
-        float sum[2] = {0.f, 0.f};
+        float sum[2 * T];   // of keys r8 and r8 + 8 of each sixteen, this lane's columns
+#pragma unroll
+        for (int i = 0; i < 2 * T; ++i) sum[i] = 0.f;
         auto tile = [&]() {
-          float sc[NT][4];
+          float sc[NT][T][4];
+          uint32_t sw[T][2][(NG + 1) / 2], bw[T][2][(NG + 1) / 2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-          uint32_t sw[2][(NG + 1) / 2], bw[2][(NG + 1) / 2];
+          for (int z = 0; z < T; ++z) {
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            pw_lds<NG * 2>(stage + 16 * G::RB + (r8 + 8 * y) * NG * 2, sw[y]);
-            pw_lds<NG * 2>(stage + 16 * G::RB + G::SC + (r8 + 8 * y) * NG * 2, bw[y]);
+            for (int y = 0; y < 2; ++y) {
+              const char* q = stage + z * G::SUB + 16 * RB + (r8 + 8 * y) * NG * 2;
+              pw_lds<NG * 2>(q, sw[z][y]);
+              pw_lds<NG * 2>(q + G::SC, bw[z][y]);
+            }
           }
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
             constexpr int LB = UPL * WPU * 4;   // a lane's bytes of a group
-            uint32_t code[2][UPL * WPU];
+            uint32_t code[T][2][UPL * WPU];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              if constexpr (LB <= 16) {
-                const int off = g * 4 * LB + c4 * LB;
-                pw_lds<LB>(stage + pw_chunk<G::RB>(r8 + 8 * y, off >> 4) + (off & 15), code[y]);
-              } else {
+            for (int z = 0; z < T; ++z) {
 #pragma unroll
-                for (int i = 0; i < LB / 16; ++i) {
-                  const uint4 v = *reinterpret_cast<const uint4*>(
-                      stage + pw_chunk<G::RB>(r8 + 8 * y, (g * 4 * LB + c4 * LB) / 16 + i));
-                  code[y][4 * i] = v.x;
-                  code[y][4 * i + 1] = v.y;
-                  code[y][4 * i + 2] = v.z;
-                  code[y][4 * i + 3] = v.w;
+              for (int y = 0; y < 2; ++y) {
+                if constexpr (LB <= 16) {
+                  const int off = g * 4 * LB + c4 * LB;
+                  pw_lds<LB>(stage + z * G::SUB + pw_chunk<RB>(r8 + 8 * y, off >> 4) + (off & 15), code[z][y]);
+                } else {
+#pragma unroll
+                  for (int i = 0; i < LB / 16; ++i) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(
+                        stage + z * G::SUB + pw_chunk<RB>(r8 + 8 * y, (g * 4 * LB + c4 * LB) / 16 + i));
+                    code[z][y][4 * i] = v.x;
+                    code[z][y][4 * i + 1] = v.y;
+                    code[z][y][4 * i + 2] = v.z;
+                    code[z][y][4 * i + 3] = v.w;
+                  }
                 }
               }
             }
-            float acc[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+            float acc[NT][T][4];
 #pragma unroll
             for (int u = 0; u < UPL; ++u) {
-              uint32_t a[8];   // two k-steps
-              if constexpr (BITS == 4) {
+              uint32_t a[T][8];   // two k-steps
+#pragma unroll
+              for (int z = 0; z < T; ++z) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                  const uint32_t w = code[y][u], z = w >> 8;
-                  a[y] = w & 0x000F000Fu;
-                  a[2 + y] = w & 0x00F000F0u;
-                  a[4 + y] = z & 0x000F000Fu;
-                  a[6 + y] = z & 0x00F000F0u;
-                }
-              } else {
+                  if constexpr (BITS == 4) {
+                    const uint32_t w = code[z][y][u], v = w >> 8;
+                    a[z][y] = w & 0x000F000Fu;
+                    a[z][2 + y] = w & 0x00F000F0u;
+                    a[z][4 + y] = v & 0x000F000Fu;
+                    a[z][6 + y] = v & 0x00F000F0u;
+                  } else {
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-#pragma unroll
-                  for (int j = 0; j < 2; ++j) {
-                    const uint32_t w = code[y][2 * u + j];
-                    a[4 * j + y] = w & 0x00FF00FFu;
-                    a[4 * j + 2 + y] = (w >> 8) & 0x00FF00FFu;
+                    for (int j = 0; j < 2; ++j) {
+                      const uint32_t w = code[z][y][2 * u + j];
+                      a[z][4 * j + y] = w & 0x00FF00FFu;
+                      a[z][4 * j + 2 + y] = (w >> 8) & 0x00FF00FFu;
+                    }
                   }
                 }
               }
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 const uint4 bq = ops[(nt * G::UNITS + g * UPL + u) * 32 + lane];
-                pw_mma(acc[nt], a[0], a[1], a[2], a[3], bq.x, bq.y);
-                pw_mma(acc[nt], a[4], a[5], a[6], a[7], bq.z, bq.w);
+#pragma unroll
+                for (int z = 0; z < T; ++z) {
+                  pw_mma(acc[nt][z], a[z][0], a[z][1], a[z][2], a[z][3], bq.x, bq.y, u > 0);
+                  pw_mma(acc[nt][z], a[z][4], a[z][5], a[z][6], a[z][7], bq.z, bq.w, true);
+                }
               }
             }
-            const float s0 = half_bits_to_float_rt((sw[0][g / 2] >> (16 * (g & 1))) & 0xffffu, p.f16);
-            const float s1 = half_bits_to_float_rt((sw[1][g / 2] >> (16 * (g & 1))) & 0xffffu, p.f16);
-            const float b0 = half_bits_to_float_rt((bw[0][g / 2] >> (16 * (g & 1))) & 0xffffu, p.f16);
-            const float b1 = half_bits_to_float_rt((bw[1][g / 2] >> (16 * (g & 1))) & 0xffffu, p.f16);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float2 qs = rows.sum[nt][g][c4];
-              sc[nt][0] = fmaf(b0, qs.x, fmaf(s0, acc[nt][0], sc[nt][0]));
-              sc[nt][1] = fmaf(b0, qs.y, fmaf(s0, acc[nt][1], sc[nt][1]));
-              sc[nt][2] = fmaf(b1, qs.x, fmaf(s1, acc[nt][2], sc[nt][2]));
-              sc[nt][3] = fmaf(b1, qs.y, fmaf(s1, acc[nt][3], sc[nt][3]));
+            for (int z = 0; z < T; ++z) {
+              const float s0 = pw_half<F16>(sw[z][0], g), s1 = pw_half<F16>(sw[z][1], g);
+              const float b0 = pw_half<F16>(bw[z][0], g), b1 = pw_half<F16>(bw[z][1], g);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const float2 qs = rows.sum[nt][g][c4];
+                float (&x)[4] = sc[nt][z];
+                const float (&v)[4] = acc[nt][z];
+                x[0] = fmaf(b0, qs.x, g == 0 ? s0 * v[0] : fmaf(s0, v[0], x[0]));
+                x[1] = fmaf(b0, qs.y, g == 0 ? s0 * v[1] : fmaf(s0, v[1], x[1]));
+                x[2] = fmaf(b1, qs.x, g == 0 ? s1 * v[2] : fmaf(s1, v[2], x[2]));
+                x[3] = fmaf(b1, qs.y, g == 0 ? s1 * v[3] : fmaf(s1, v[3], x[3]));
+              }
             }
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float2 mul = rows.mul[nt][c4], ls = rows.lse[nt][c4];
-            const int2 last = rows.last[nt][c4];
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int key = key0 + r8 + 8 * y;
-              const float e0 = pw_ex2(fmaf(sc[nt][2 * y], mul.x, -ls.x)), e1 = pw_ex2(fmaf(sc[nt][2 * y + 1], mul.y, -ls.y));
-              sum[y] += key <= last.x ? e0 : 0.f;
-              sum[y] += key <= last.y ? e1 : 0.f;
+            for (int z = 0; z < T; ++z) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                sc[nt][z][j] = fmaf(sc[nt][z][j], j & 1 ? mul.y : mul.x, j & 1 ? -ls.y : -ls.x);
+              if (many || key0 + 16 * T - 1 > open) {   // some row does not see some key
+                const int2 last = rows.last[nt][c4];
+                const int key = key0 + 16 * z + r8;
+                if (key > last.x) sc[nt][z][0] = -INFINITY;
+                if (key > last.y) sc[nt][z][1] = -INFINITY;
+                if (key + 8 > last.x) sc[nt][z][2] = -INFINITY;
+                if (key + 8 > last.y) sc[nt][z][3] = -INFINITY;
+              }
+              sum[2 * z] += pw_ex2(sc[nt][z][0]);
+              sum[2 * z] += pw_ex2(sc[nt][z][1]);
+              sum[2 * z + 1] += pw_ex2(sc[nt][z][2]);
+              sum[2 * z + 1] += pw_ex2(sc[nt][z][3]);
             }
           }
         };
         // the counted tokens that see the block's first key
-        int row = many ? max(first, max(step * kPwKeys - s.base, 0) * p.nrep) : first;
+        int row = many ? max(first, max(step * G::KEYS - s.base, 0) * p.nrep) : first;
         do {
           if (many) {
             __syncthreads();   // the operands of before are read
-            pw_rows<BITS, D, GS, NT>(p, s, kvh, row, ops, rows);
+            pw_rows<BITS, D, GS, NT, F16>(p, s, kvh, row, ops, rows);
             __syncthreads();
           }
-          if (there) tile();
+          if (any) tile();
           row += ROWS;
         } while (row < r_hi);
-        // ---- a key's sum over the quad's columns, and its new mass
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], 1);
-          sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], 2);
+        // ---- a key's sum over the quad's columns: with two sixteens each lane ends with one key's, its new mass
+        float add;
+        if constexpr (T == 2) {
+          const float x = c4 & 2 ? sum[0] : sum[2], y = c4 & 2 ? sum[1] : sum[3];
+          const float u = (c4 & 2 ? sum[2] : sum[0]) + __shfl_xor_sync(0xffffffffu, x, 2);
+          const float v = (c4 & 2 ? sum[3] : sum[1]) + __shfl_xor_sync(0xffffffffu, y, 2);
+          add = (c4 & 1 ? v : u) + __shfl_xor_sync(0xffffffffu, c4 & 1 ? u : v, 1);
+        } else {
+          const float x = (c4 & 1 ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, c4 & 1 ? sum[0] : sum[1], 1);
+          add = x + __shfl_xor_sync(0xffffffffu, x, 2);
         }
-        const int key = key0 + r8 + 8 * c4;
-        if (there && c4 < 2 && key < s.n) {
-          const long long row = row_of(t, pg) + r8 + 8 * c4;
-          const float add = c4 == 0 ? sum[0] : sum[1];
+        const int z = T == 2 ? c4 >> 1 : 0, i = r8 + 8 * (c4 & 1), key = key0 + 16 * z + i;
+        const int kpg = T == 2 ? __shfl_sync(0xffffffffu, pg, z * LPS) : pg;   // the page of this lane's key
+        if ((T == 2 || c4 < 2) && key < s.n && (unsigned)kpg < (unsigned)p.num_pages) {
+          const long long at_row = row_of(t + z, kpg) + i;
           if (key < s.base) {
-            const float old = *reinterpret_cast<const float*>(stage + 16 * G::RB + 2 * G::SC + 4 * (r8 + 8 * c4));
-            p.mass[row] = fmaf(p.decay, old, add);
+            p.mass[at_row] = fmaf(p.decay, *reinterpret_cast<const float*>(stage + z * G::SUB + 16 * RB + 2 * G::SC + 4 * i), add);
           } else {
-            p.mass[row] = add;
-            p.token[row] = key + (p.shift != nullptr ? p.shift[b] : 0);
+            p.mass[at_row] = add;
+            p.token[at_row] = key + (p.shift != nullptr ? p.shift[b] : 0);
           }
         }
         __syncwarp();   // the stage is read
@@ -426,7 +473,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
       do {
         if (++b >= p.B) return;
         s = pw_seq(p, b);
-        blocks = pw_blocks<kPwKeys>(s);
+        blocks = pw_blocks<G::KEYS>(s);
       } while (blocks == 0);
       head = work(s, blocks);
     }
@@ -434,10 +481,10 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
   }
 }
 
-template <int BITS, int D, int GS, int NT>
+template <int BITS, int D, int GS, int NT, bool F16>
 cudaError_t pw_run(const QdaWeightsParams* p, int* ctas_per_sm, cudaStream_t s) {
   using G = PwGeom<BITS, D, GS, NT>;
-  auto kern = qda_paged_weights_kernel<BITS, D, GS, NT>;
+  auto kern = qda_paged_weights_kernel<BITS, D, GS, NT, F16>;
   if (ctas_per_sm != nullptr) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, kern, kPwWarps * 32, G::SMEM);
@@ -447,13 +494,11 @@ cudaError_t pw_run(const QdaWeightsParams* p, int* ctas_per_sm, cudaStream_t s) 
   return cudaGetLastError();
 }
 
-template <int BITS>
+template <int BITS, bool F16>
 cudaError_t pw_pick(const QdaWeightsParams* p, int D, int GS, int rows, int* occ, cudaStream_t s) {
-#define QDA_PW(d, gs)                                                          \
-  if (D == d && GS == gs) {                                                    \
-    if (rows > 8) return pw_run<BITS, d, gs, 4>(p, occ, s);                    \
-    return pw_run<BITS, d, gs, 1>(p, occ, s);                                  \
-  }
+#define QDA_PW(d, gs)                                                               \
+  if (D == d && GS == gs)                                                           \
+    return rows > 8 ? pw_run<BITS, d, gs, 4, F16>(p, occ, s) : pw_run<BITS, d, gs, 1, F16>(p, occ, s);
   QDA_PW(64, 32) QDA_PW(64, 64)
   QDA_PW(128, 32) QDA_PW(128, 64) QDA_PW(128, 128)
   QDA_PW(256, 32) QDA_PW(256, 64) QDA_PW(256, 128)

@@ -90,10 +90,12 @@ __device__ __forceinline__ int pw_block_at(int blocks, long long x, F&& prefix) 
 }  // namespace qda
 #endif
 
-// Translation units per code width. With ctas_per_sm the instance's resident CTAs per SM are stored there and nothing is
+// Translation units per code width and input type. With ctas_per_sm the instance's resident CTAs per SM are stored there and nothing is
 // launched; else p.ctas CTAs are. rows: the bound on a KV head's query rows that choose the instance.
-cudaError_t qda_paged_weights_b4(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
-cudaError_t qda_paged_weights_b8(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_weights_b4_f0(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_weights_b4_f1(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_weights_b8_f0(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_weights_b8_f1(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 
 // The kernel for many rows (D <= 256), and the one ahead of it that lays out the query rows. prepare sets the shared memory
 // limit on the current device and launches nothing.

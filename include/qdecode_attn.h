@@ -413,8 +413,8 @@ int qdecode_rope_freqs(int rot, double base, double factor, double context, doub
  * tokens of a sequence and only chooses the kernel. Scores are right to fp32 (queries below 2^-39 of their row's largest
  * and keys' values below 2^-39 of what their key can hold aside); sums are fp32 in a fixed order: the same bits on every run.
  * Scales and biases as for the attention: a key that is not finite spoils its own mass alone. Same types, limits and checks
- * as qdecode_paged_attn. Uses the workspace as qdecode_attn does, of qdecode_paged_weights_workspace_bytes() bytes; calls that
- * share one must not overlap on the GPU.
+ * as qdecode_paged_attn; mass 16-byte aligned. Uses the workspace as qdecode_attn does, of qdecode_paged_weights_workspace_bytes()
+ * bytes; calls that share one must not overlap on the GPU.
  */
 int qdecode_paged_weights(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                           const void* k_scales, const void* k_biases, const float* lse, float* mass, int32_t* token,
