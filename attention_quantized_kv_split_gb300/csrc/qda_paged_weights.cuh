@@ -113,6 +113,12 @@ __device__ __forceinline__ void pw_mma(float (&c)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// ceil(total / n): 64-bit division only where it is needed.
+__device__ __forceinline__ long long pw_share(long long total, int n) {
+  if (total <= 0x7fffffffLL - n) return ((uint32_t)total + (uint32_t)n - 1) / (uint32_t)n;
+  return (total + n - 1) / n;
+}
+
 template <int NT, int NG>
 struct PwRows {
   float2 sum[NT][NG][4];         // a query row's sums per group, columns of a lane side by side
@@ -236,22 +242,46 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
     if (b < p.B) s_at[b + 1] = before + v;
     __syncthreads();
   }
-  const long long total = carry, piece = (total + p.ctas - 1) / p.ctas;
+  const long long total = carry, piece = pw_share(total, p.ctas);
   const long long from = min(total, piece * blockIdx.x), to = min(total, from + piece);
   if (from >= to) return;
 
-  // ---- the CTA's piece, a (sequence, KV head) at a time: the blocks that start in it
-  int b = qda_seq_of(s_at, p.B, from);
+  // ---- the CTA's piece, a (sequence, KV head) at a time: the blocks that start in it. (One warp looks for the start: the
+  // others' instructions would cost the SM's other CTAs more than they wait.)
+  __shared__ int s_b, s_kvh, s_x0;
+  if (warp == 0) {
+    const int b = qda_seq_of(s_at, p.B, from);
+    const PwSeq s = pw_seq(p, b);
+    const int blocks = pw_blocks<G::KEYS>(s);
+    const long long head = work(s, blocks);
+    const int kvh = (int)((from - s_at[b]) / head);
+    const long long at = s_at[b] + kvh * head;
+    const int x0 = pw_block_at(blocks, from, [&](int i) { return at + work(s, i); });
+    if (lane == 0) {
+      s_b = b;
+      s_kvh = kvh;
+      s_x0 = x0;
+    }
+  }
+  __syncthreads();
+  int b = s_b, kvh = s_kvh;
   PwSeq s = pw_seq(p, b);
   int blocks = pw_blocks<G::KEYS>(s);
   long long head = work(s, blocks);
-  int kvh = (int)((from - s_at[b]) / head);
   long long at = s_at[b] + kvh * head;   // the KV head's place on the line
   auto block_at = [&](long long x) { return pw_block_at(blocks, x, [&](int i) { return at + work(s, i); }); };
   const int pmask = (1 << p.page_shift) - 1;
-  int x0 = block_at(from);
+  int x0 = s_x0;
   constexpr int LPS = 32 / T;                 // lanes that fetch a sixteen of keys
   const int fsub = lane / LPS, fl = lane % LPS;
+  // chunks of sixteen keys' scales, biases and masses, and where the first row's lie
+  constexpr int CS = G::SC / 16, REST = 2 * CS + 4;
+  auto rest_of = [&](int c) {
+    return c < CS ? reinterpret_cast<const char*>(p.ks) + 16 * c
+           : c < 2 * CS ? reinterpret_cast<const char*>(p.kb) + 16 * (c - CS) : reinterpret_cast<const char*>(p.mass) + 16 * (c - 2 * CS);
+  };
+  const char* const rest = rest_of(fl);
+  const uint32_t rest_size = fl < 2 * CS ? NG * 2 : 4;
   while (true) {
     const int x1 = at + head <= to ? blocks : block_at(to);
     if (x0 < x1) {
@@ -259,27 +289,30 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
       // sixteen keys `t` of the sequence: their page (-1: behind the sequence or this piece)
       const int t1 = min(x1 * (T * kPwWarps), (s.n + 15) >> 4);
       auto page_of = [&](int t) { return t < t1 ? __ldg(tab + (t * 16 >> p.page_shift)) : -1; };
-      auto row_of = [&](int t, int pg) { return qda_pool_row(pg, kvh, (t * 16) & pmask, p.Hkv, p.page_shift); };
+      // (pool rows are below 2^32 - 1)
+      auto row_of = [&](int t, int pg) {
+        return (((uint32_t)pg * (uint32_t)p.Hkv + (uint32_t)kvh) << p.page_shift) + (uint32_t)((t * 16) & pmask);
+      };
       // a tile on its way into a stage (a page outside the pool: nothing is read); pg: the page of this lane's sixteen
       auto fetch = [&](int t, int pg, int st) {
         if ((unsigned)pg < (unsigned)p.num_pages) {
-          const long long row = row_of(t + fsub, pg);
+          const uint32_t row = row_of(t + fsub, pg);
           const uint32_t dst = smem_addr(ring + st * G::STAGE + fsub * G::SUB);
-          const char* src = reinterpret_cast<const char*>(p.kp + row * G::W) + 16 * fl;
+          const char* src = reinterpret_cast<const char*>(p.kp) + (uint64_t)row * RB + 16 * fl;
 #pragma unroll
           for (int i = 0; i < (16 * G::CPR + LPS - 1) / LPS; ++i) {
             const int c = i * LPS + fl;
             if (16 * G::CPR >= LPS || c < 16 * G::CPR)
               pw_copy16(dst + pw_chunk<RB>(c / G::CPR, c % G::CPR), src + 16 * LPS * i);
           }
-          constexpr int CS = G::SC / 16, REST = 2 * CS + 4;   // chunks of the scales, the biases, the masses
+          if constexpr (REST <= LPS) {
+            if (fl < REST) pw_copy16(dst + 16 * RB + 16 * fl, rest + (uint64_t)row * rest_size);
+          } else {
 #pragma unroll
-          for (int i = 0; i < (REST + LPS - 1) / LPS; ++i) {
-            const int c = i * LPS + fl;
-            const char* from = c < CS ? reinterpret_cast<const char*>(p.ks + row * NG) + 16 * c
-                               : c < 2 * CS ? reinterpret_cast<const char*>(p.kb + row * NG) + 16 * (c - CS)
-                                            : reinterpret_cast<const char*>(p.mass + row) + 16 * (c - 2 * CS);
-            if (c < REST) pw_copy16(dst + 16 * RB + 16 * c, from);
+            for (int i = 0; i < (REST + LPS - 1) / LPS; ++i) {
+              const int c = i * LPS + fl;
+              if (c < REST) pw_copy16(dst + 16 * RB + 16 * c, rest_of(c) + (uint64_t)row * (c < 2 * CS ? NG * 2 : 4));
+            }
           }
         }
         pw_commit();
@@ -452,7 +485,7 @@ __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
         const int z = T == 2 ? c4 >> 1 : 0, i = r8 + 8 * (c4 & 1), key = key0 + 16 * z + i;
         const int kpg = T == 2 ? __shfl_sync(0xffffffffu, pg, z * LPS) : pg;   // the page of this lane's key
         if ((T == 2 || c4 < 2) && key < s.n && (unsigned)kpg < (unsigned)p.num_pages) {
-          const long long at_row = row_of(t + z, kpg) + i;
+          const uint32_t at_row = row_of(t + z, kpg) + i;
           if (key < s.base) {
             p.mass[at_row] = fmaf(p.decay, *reinterpret_cast<const float*>(stage + z * G::SUB + 16 * RB + 2 * G::SC + 4 * i), add);
           } else {
