@@ -12,10 +12,11 @@ namespace qda {
 
 namespace cg = cooperative_groups;
 
-constexpr int kEvThreads = 512;
+constexpr int kEvThreads = 256;
 constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvHeld = 16384;      // keys that a CTA holds in shared memory (64 KB); those behind them are read again
-constexpr int kEvBins = 2048;       // 11 bits of a key at a time
+constexpr int kEvBins = 2048;       // 11 bits of a rank at a time
+constexpr int kEvFew = 256;         // ranks that are compared one by one
 constexpr int kEvCluster = 8;
 
 struct EvictParams {
@@ -39,22 +40,40 @@ __device__ __forceinline__ uint32_t ev_rank(float m) {
   return m != m ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// A row's rank: its mass, and of equal ones the lower row first. 32 bits of either.
+__device__ __forceinline__ uint64_t ev_full(uint32_t key, int row) { return (uint64_t)key << 32 | (uint32_t)~row; }
+
 struct alignas(16) EvShared {
   int hist[kEvBins];
+  uint64_t few[kEvFew];       // this CTA's ranks that are left
+  uint64_t all[kEvFew];       // the cluster's
   int warp[kEvWarps][2];
   int tot[2];                 // this CTA's counts, for the cluster
-  int pick[2];                // bin, keys above it
+  int pick[3];                // bin, ranks above it, ranks in it
+  int n_few;
+  uint64_t edge;              // the budget-th rank
 };
 
-// One cluster per (sequence, KV head), a contiguous piece of its rows per CTA. The rank of the budget-th key is found by 11
-// bits at a time over histograms that the cluster adds up through distributed shared memory; then rows are counted in order
-// (ballots in a warp, warps and CTAs through prefix sums), so that ties fall to the lowest rows and the i-th hole meets the
-// i-th row that comes, whatever the timing. A row's mass and token are read once.
+// One cluster per (sequence, KV head), a contiguous piece of its rows per CTA (ONE: clusters of one CTA). The budget-th
+// largest rank is found by 11 bits at a time over histograms that the cluster adds up through distributed shared memory, and
+// once no more than kEvFew ranks are left, by comparing them all. Ranks are all different (a row's number is part of its
+// rank), so what stays is what is not below the edge. Then holes and rows that come are counted in order, a bit a row, and
+// listed: the i-th hole meets the i-th row that comes, whatever the timing. A row's mass and token are read once. Bound by
+// latency: loads two deep, then some ten barriers.
+template <bool ONE>
 __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t s_key[];
   __shared__ EvShared sh;
   cg::cluster_group cl = cg::this_cluster();
-  const int cs = cl.num_blocks(), me = cl.block_rank();
+  const int cs = ONE ? 1 : cl.num_blocks(), me = ONE ? 0 : cl.block_rank();
+  auto sync = [&]() {
+    if constexpr (ONE) __syncthreads();
+    else cl.sync();
+  };
+  auto of = [&](auto* x, int r) {
+    if constexpr (ONE) return x;
+    else return cl.map_shared_rank(x, r);
+  };
   const int unit = blockIdx.x / cs, b = unit / p.Hkv, kvh = unit - b * p.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
@@ -73,49 +92,90 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
   const int* tab = p.table + (size_t)b * p.max_pages;
   const int seen = n + (p.shift != nullptr ? p.shift[b] : 0);
   const int young = seen - p.recent;
-  auto row_of = [&](int i) -> long long {
-    const int pg = tab[i >> p.page_shift];
-    return (unsigned)pg < (unsigned)p.num_pages ? qda_pool_row(pg, kvh, i & pmask, p.Hkv, p.page_shift) : -1;
+  // (pool rows are below 2^32 - 1, which stands for a row that is not there)
+  auto row_of = [&](int i) -> uint32_t {
+    const int pg = __ldg(tab + (i >> p.page_shift));
+    return (unsigned)pg < (unsigned)p.num_pages
+               ? (((uint32_t)pg * (uint32_t)p.Hkv + (uint32_t)kvh) << p.page_shift) + (uint32_t)(i & pmask) : 0xffffffffu;
   };
   auto load_key = [&](int i) -> uint32_t {
-    const long long r = row_of(i);
-    if (r < 0) {
+    const uint32_t r = row_of(i);
+    if (r == 0xffffffffu) {
       atomicOr(p.err, QDA_ERR_BIT_PAGED);
       return 0u;
     }
-    const int t = p.token[r];
-    const uint32_t k = ev_rank(p.mass[r]);
+    const int t = __ldg(p.token + r);
+    const uint32_t k = ev_rank(__ldg(p.mass + r));
     return t < p.sinks || t >= young ? 0xffffffffu : k;
   };
-  for (int i = lo + tid; i < min(hi, lo + p.held); i += kEvThreads) s_key[i - lo] = load_key(i);
+  // four rows of a page at a time (pages hold sixteens of rows, masses and tokens are aligned), four such loads on their way
+  constexpr int LQ = 4;
+  for (int i0 = lo + 4 * tid; i0 < min(hi, lo + p.held); i0 += LQ * 4 * kEvThreads) {
+    uint32_t r[LQ];
+    float4 m[LQ];
+    int4 t[LQ];
+#pragma unroll
+    for (int u = 0; u < LQ; ++u) {
+      const int i = i0 + u * 4 * kEvThreads;
+      r[u] = i < min(hi, lo + p.held) ? row_of(i) : 0xfffffffeu;
+    }
+#pragma unroll
+    for (int u = 0; u < LQ; ++u) {
+      if (r[u] >= 0xfffffffeu) continue;
+      m[u] = __ldg(reinterpret_cast<const float4*>(p.mass + r[u]));
+      t[u] = __ldg(reinterpret_cast<const int4*>(p.token + r[u]));
+    }
+#pragma unroll
+    for (int u = 0; u < LQ; ++u) {
+      const int i = i0 + u * 4 * kEvThreads;
+      if (r[u] == 0xfffffffeu) continue;
+      uint4 k = make_uint4(0, 0, 0, 0);
+      if (r[u] == 0xffffffffu) {
+        atomicOr(p.err, QDA_ERR_BIT_PAGED);
+      } else {
+        auto rank = [&](float x, int y) { return y < p.sinks || y >= young ? 0xffffffffu : ev_rank(x); };
+        k = make_uint4(rank(m[u].x, t[u].x), rank(m[u].y, t[u].y), rank(m[u].z, t[u].z), rank(m[u].w, t[u].w));
+      }
+      *reinterpret_cast<uint4*>(s_key + i - lo) = k;   // (a piece's room is a multiple of 32 keys)
+    }
+  }
   auto key_at = [&](int i) { return i - lo < p.held ? s_key[i - lo] : load_key(i); };
 
-  // ---- the budget-th largest key
-  uint32_t prefix = 0;
-  int above = 0;              // keys above the prefix
-  int equal = 0;
-  constexpr int SHIFT[3] = {21, 10, 0}, WIDTH[3] = {11, 11, 10};
-#pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    for (int i = tid; i < kEvBins; i += kEvThreads) sh.hist[i] = 0;
+  // ---- the budget-th largest rank
+  uint64_t prefix = 0;        // the bits that are known, from the top
+  int known = 0;
+  int above = 0, left = n;    // ranks above the prefix, ranks that have it
+  while (left > kEvFew) {     // (64 known bits leave one)
+    const int width = min(11, 64 - known), shift = 64 - known - width;
+    for (int i = tid; i < kEvBins / 4; i += kEvThreads) reinterpret_cast<int4*>(sh.hist)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    const int up = SHIFT[pass] + WIDTH[pass];
     for (int i = lo + tid; i < hi; i += kEvThreads) {
-      const uint32_t k = key_at(i);
-      if (pass == 0 || (k >> (up & 31)) == prefix) atomicAdd(&sh.hist[(k >> SHIFT[pass]) & ((1 << WIDTH[pass]) - 1)], 1);
+      const uint64_t k = ev_full(key_at(i), i);
+      if (known == 0 || (k >> (shift + width)) == prefix) atomicAdd(&sh.hist[(k >> shift) & ((1u << width) - 1)], 1);
     }
-    cl.sync();
-    // the cluster's counts of four bins a thread, highest bins first
-    int c[4] = {0, 0, 0, 0};
-    const int bin0 = kEvBins - 4 - 4 * tid;
-    for (int r = 0; r < cs; ++r) {
-      const int4 v = *reinterpret_cast<const int4*>(cl.map_shared_rank(sh.hist, r) + bin0);
-      c[0] += v.w;
-      c[1] += v.z;
-      c[2] += v.y;
-      c[3] += v.x;
+    sync();
+    // the cluster's counts of eight bins a thread, highest bins first
+    int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int bin0 = kEvBins - 8 - 8 * tid;
+    constexpr int RU = ONE ? 1 : 4;   // CTAs whose bins are on their way
+    for (int r0 = 0; r0 < cs; r0 += RU) {
+      int4 u[RU], v[RU];
+#pragma unroll
+      for (int k = 0; k < RU; ++k) {
+        const int4* h = reinterpret_cast<const int4*>(of(sh.hist, ONE ? 0 : min(r0 + k, cs - 1)) + bin0);
+        u[k] = h[1];
+        v[k] = h[0];
+      }
+#pragma unroll
+      for (int k = 0; k < RU; ++k) {
+        if (r0 + k >= cs) continue;
+        c[0] += u[k].w, c[1] += u[k].z, c[2] += u[k].y, c[3] += u[k].x;
+        c[4] += v[k].w, c[5] += v[k].z, c[6] += v[k].y, c[7] += v[k].x;
+      }
     }
-    const int mine = c[0] + c[1] + c[2] + c[3];
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mine += c[j];
     int up_to = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -124,104 +184,140 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
     }
     if (lane == 31) sh.warp[warp][0] = up_to;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) up_to += sh.warp[w][0];
-    int before = above + up_to - mine;   // keys in higher bins
+#pragma unroll
+    for (int w = 0; w < kEvWarps; ++w) up_to += w < warp ? sh.warp[w][0] : 0;
+    int before = above + up_to - mine;   // ranks in higher bins
     if (before < p.budget && before + mine >= p.budget) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         if (before < p.budget && before + c[j] >= p.budget) {
-          sh.pick[0] = bin0 + 3 - j;
+          sh.pick[0] = bin0 + 7 - j;
           sh.pick[1] = before;
-          sh.tot[0] = c[j];
+          sh.pick[2] = c[j];
         }
         before += c[j];
       }
     }
-    __syncthreads();
-    prefix = pass == 0 ? (uint32_t)sh.pick[0] : (prefix << WIDTH[pass]) | (uint32_t)sh.pick[0];
+    sync();   // every CTA has read the histograms
+    prefix = prefix << width | (uint32_t)sh.pick[0];
+    known += width;
     above = sh.pick[1];
-    equal = sh.tot[0];
-    cl.sync();   // every CTA has read the histograms
+    left = sh.pick[2];
   }
-  const uint32_t edge = prefix;
-  const int ties = p.budget - above;   // rows of that rank that stay, lowest first
-
-  // ---- rows in order: a warp takes a contiguous part of the CTA's piece, 32 rows at a time
-  const int part = ((hi - lo + kEvWarps - 1) / kEvWarps + 31) & ~31;
-  const int w_lo = min(hi, lo + part * warp), w_hi = min(hi, w_lo + part);
-  // sums over the warps and CTAs before this one, of two counts of each warp
-  auto before_of = [&](int x, int y) {
-    if (lane == 0) {
-      sh.warp[warp][0] = x;
-      sh.warp[warp][1] = y;
+  // ---- the ranks that are left, all of them against each other
+  if (tid == 0) sh.n_few = 0;
+  __syncthreads();
+  for (int i = lo + tid; i < hi; i += kEvThreads) {
+    const uint64_t k = ev_full(key_at(i), i);
+    if (known == 0 || (k >> (64 - known)) == prefix) sh.few[atomicAdd(&sh.n_few, 1)] = k;   // (in any order; no more than kEvFew)
+  }
+  sync();
+  const uint64_t* all = sh.few;
+  if constexpr (!ONE) {   // every CTA takes all of them, and finds the edge for itself
+    int m[kEvCluster];
+    uint64_t k[kEvCluster];
+#pragma unroll
+    for (int r = 0; r < kEvCluster; ++r) m[r] = r < cs ? *cl.map_shared_rank(&sh.n_few, r) : 0;
+#pragma unroll
+    for (int r = 0; r < kEvCluster; ++r) k[r] = tid < m[r] ? cl.map_shared_rank(sh.few, r)[tid] : 0;
+    int at = tid;
+#pragma unroll
+    for (int r = 0; r < kEvCluster; ++r) {
+      if (tid < m[r]) sh.all[at] = k[r];
+      at += m[r];
     }
+    all = sh.all;
     __syncthreads();
-    int2 mine = make_int2(0, 0), all = make_int2(0, 0);
-    for (int w = 0; w < kEvWarps; ++w) {
-      const int2 v = make_int2(sh.warp[w][0], sh.warp[w][1]);
-      if (w < warp) {
-        mine.x += v.x;
-        mine.y += v.y;
-      }
-      all.x += v.x;
-      all.y += v.y;
-    }
+  }
+  if (tid < left) {
+    const uint64_t k = all[tid];
+    int higher = above;
+#pragma unroll 8
+    for (int i = 0; i < left; ++i) higher += all[i] > k;
+    if (higher == p.budget - 1) sh.edge = k;
+  }
+  __syncthreads();
+  const uint64_t edge = sh.edge;
+
+  // ---- rows in order, 32 at a time as the bits of a word: holes and rows that come before each
+  const int words = (hi - lo + 31) >> 5;
+  const uint32_t below = (1u << lane) - 1;
+  // rows of word w that lie before the budget
+  auto inside = [&](int w) {
+    const int c = p.budget - (lo + 32 * w);
+    return c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1;
+  };
+  auto real = [&](int w) {
+    const int c = hi - (lo + 32 * w);
+    return c >= 32 ? 0xffffffffu : (1u << c) - 1;
+  };
+  auto stays = [&](int w) {
+    const int i = lo + 32 * w + lane;
+    return __ballot_sync(0xffffffffu, i < hi && ev_full(key_at(i), i) >= edge);
+  };
+  int holes = 0, comes = 0;   // of this warp's words: contiguous, so that warps are in order
+  const int part = (words + kEvWarps - 1) / kEvWarps, w_lo = min(words, part * warp), w_hi = min(words, w_lo + part);
+#pragma unroll 2
+  for (int w = w_lo; w < w_hi; ++w) {
+    const uint32_t stay = stays(w);
+    holes += __popc(~stay & inside(w) & real(w));
+    comes += __popc(stay & ~inside(w));
+  }
+  if (lane == 0) {
+    sh.warp[warp][0] = holes;
+    sh.warp[warp][1] = comes;
+  }
+  __syncthreads();
+  int h_at = 0, c_at = 0, h_all = 0, c_all = 0;
+#pragma unroll
+  for (int w = 0; w < kEvWarps; ++w) {
+    const int x = sh.warp[w][0], y = sh.warp[w][1];
+    h_at += w < warp ? x : 0;
+    c_at += w < warp ? y : 0;
+    h_all += x;
+    c_all += y;
+  }
+  if constexpr (!ONE) {
     if (tid == 0) {
-      sh.tot[0] = all.x;
-      sh.tot[1] = all.y;
+      sh.tot[0] = h_all;
+      sh.tot[1] = c_all;
     }
     cl.sync();
     for (int r = 0; r < me; ++r) {
       const int* t = cl.map_shared_rank(sh.tot, r);
-      mine.x += t[0];
-      mine.y += t[1];
+      h_at += t[0];
+      c_at += t[1];
     }
-    cl.sync();
-    return mine;
-  };
-  int tied = 0;   // rows of the edge's rank before this warp's part
-  if (ties < equal) {
-    int c = 0;
-    for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
-      const int i = i0 + lane;
-      c += __popc(__ballot_sync(0xffffffffu, i < w_hi && key_at(i) == edge));
-    }
-    tied = before_of(c, 0).x;
+    cl.sync();   // (no CTA goes while another reads its counts)
   }
-  const uint32_t below = (1u << lane) - 1;
-  // f(row, stays) for the rows of a 32-wide step
-  auto walk = [&](auto&& f) {
-    int t = tied;
-    for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
-      const int i = i0 + lane;
-      const bool in = i < w_hi;
-      const uint32_t k = in ? key_at(i) : 0u;
-      bool stays = in && k > edge;
-      const uint32_t eq = __ballot_sync(0xffffffffu, in && k == edge);
-      if (in && k == edge) stays = ties >= equal || t + __popc(eq & below) < ties;
-      t += __popc(eq);
-      f(i, in && !stays && i < p.budget, stays && i >= p.budget);
-    }
-  };
-  int holes = 0, comes = 0;
-  walk([&](int, bool hole, bool come) {
-    holes += __popc(__ballot_sync(0xffffffffu, hole));
-    comes += __popc(__ballot_sync(0xffffffffu, come));
-  });
-  int2 at = before_of(holes, comes);
-  if (me == cs - 1 && warp == kEvWarps - 1 && lane == 0) p.moves[unit] = at.x + holes;
+  if (me == cs - 1 && tid == kEvThreads - 32) p.moves[unit] = h_at + holes;
   uint32_t* const hole_list = p.hole + (size_t)unit * p.most;
   uint32_t* const come_list = p.come + (size_t)unit * p.most;
-  walk([&](int i, bool hole, bool come) {
-    const uint32_t h = __ballot_sync(0xffffffffu, hole), c = __ballot_sync(0xffffffffu, come);
-    if (hole || come) {
-      const uint32_t r = (uint32_t)row_of(i);   // (-1: no such row; pool rows are below 2^32 - 1)
-      const int j = hole ? at.x + __popc(h & below) : at.y + __popc(c & below);
-      if (j < p.most) (hole ? hole_list : come_list)[j] = r;
+  constexpr int WU = 4;   // words whose pages are looked up together
+  for (int w0 = w_lo; w0 < w_hi; w0 += WU) {
+    uint32_t h[WU], c[WU], r[WU];
+#pragma unroll
+    for (int u = 0; u < WU; ++u) {
+      const int w = w0 + u;
+      h[u] = c[u] = 0;
+      if (w < w_hi) {   // (the whole warp)
+        const uint32_t stay = stays(w);
+        h[u] = ~stay & inside(w) & real(w);
+        c[u] = stay & ~inside(w);
+      }
+      r[u] = ((h[u] | c[u]) >> lane) & 1u ? row_of(lo + 32 * w + lane) : 0;
     }
-    at.x += __popc(h);
-    at.y += __popc(c);
-  });
+#pragma unroll
+    for (int u = 0; u < WU; ++u) {
+      if (((h[u] | c[u]) >> lane) & 1u) {
+        const bool hole = (h[u] >> lane) & 1u;
+        const int j = hole ? h_at + __popc(h[u] & below) : c_at + __popc(c[u] & below);
+        if (j < p.most) (hole ? hole_list : come_list)[j] = r[u];
+      }
+      h_at += __popc(h[u]);
+      c_at += __popc(c[u]);
+    }
+  }
 }
 
 // The rows that come are copied to the holes: a lane has one fixed piece of a row (16 bytes of codes, scales or biases, its
@@ -279,59 +375,69 @@ __global__ void __launch_bounds__(kEvMoveThreads) qda_paged_evict_move_kernel(co
   if (moves == 0) return;
   const uint32_t* hole = p.hole + (size_t)unit * p.most;
   const uint32_t* come = p.come + (size_t)unit * p.most;
-  // pieces of a row: K codes, V codes (16 bytes each), scales and biases (up to 16 bytes each), mass, token
+  // pieces of a row: K codes, V codes (16 bytes each), scales and biases (up to 16 bytes each), mass, token. Many codes go by
+  // themselves, a power of two of lanes to a row; the rest then takes 8 or 16 lanes.
   const int cq = p.W / 4, sb = p.NG * 2, sp = sb > 16 ? sb / 16 : 1;
-  const int pieces = 2 * cq + 4 * sp + 2;
-  const int lanes = pieces <= 8 ? 8 : pieces <= 16 ? 16 : 32;
-  const int sub = tid / lanes, per = kEvMoveThreads / lanes * gridDim.x;
-  for (int it = tid % lanes; it < pieces; it += lanes) {
-    char* base;
-    int stride, size, off;
-    if (it < 2 * cq) {
-      base = reinterpret_cast<char*>(it < cq ? p.kp : p.vp);
-      stride = p.W * 4;
-      size = 16;
-      off = (it < cq ? it : it - cq) * 16;
-    } else if (it < 2 * cq + 4 * sp) {
-      const int j = it - 2 * cq, a = j / sp;
-      base = reinterpret_cast<char*>(a == 0 ? p.ks : a == 1 ? p.kb : a == 2 ? p.vs : p.vb);
-      stride = sb;
-      size = min(sb, 16);
-      off = (j - a * sp) * 16;
-    } else {
-      base = it == pieces - 1 ? reinterpret_cast<char*>(p.token) : reinterpret_cast<char*>(p.mass);
-      stride = size = 4;
-      off = 0;
+  const int small = 4 * sp + 2, codes = 2 * cq;
+  auto copy = [&](int first, int pieces, int lanes) {
+    const int sub = tid / lanes, group = kEvMoveThreads / lanes, per = group * gridDim.x;
+    for (int it = first + tid % lanes; it < first + pieces; it += lanes) {
+      char* base;
+      int stride, size, off;
+      if (it < codes) {
+        base = reinterpret_cast<char*>(it < cq ? p.kp : p.vp);
+        stride = p.W * 4;
+        size = 16;
+        off = (it < cq ? it : it - cq) * 16;
+      } else if (it < codes + 4 * sp) {
+        const int j = it - codes, a = j / sp;
+        base = reinterpret_cast<char*>(a == 0 ? p.ks : a == 1 ? p.kb : a == 2 ? p.vs : p.vb);
+        stride = sb;
+        size = min(sb, 16);
+        off = (j - a * sp) * 16;
+      } else {
+        base = it == codes + small - 1 ? reinterpret_cast<char*>(p.token) : reinterpret_cast<char*>(p.mass);
+        stride = size = 4;
+        off = 0;
+      }
+      base += off;
+      constexpr int U = 4;
+      for (int i0 = blockIdx.x * group + sub; i0 < moves; i0 += U * per) {
+        uint32_t f[U], t[U];
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int i = i0 + u * per;
+          f[u] = i < moves ? come[i] : 0xffffffffu;
+          t[u] = i < moves ? hole[i] : 0xffffffffu;
+          if (t[u] == 0xffffffffu) f[u] = t[u];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (f[u] == 0xffffffffu) continue;
+          const char* src = base + (uint64_t)f[u] * stride;
+          if (size == 16) v[u] = *reinterpret_cast<const uint4*>(src);
+          else if (size == 8) *reinterpret_cast<uint2*>(&v[u]) = *reinterpret_cast<const uint2*>(src);
+          else if (size == 4) v[u].x = *reinterpret_cast<const uint32_t*>(src);
+          else v[u].x = *reinterpret_cast<const uint16_t*>(src);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (f[u] == 0xffffffffu) continue;
+          char* dst = base + (uint64_t)t[u] * stride;
+          if (size == 16) *reinterpret_cast<uint4*>(dst) = v[u];
+          else if (size == 8) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(&v[u]);
+          else if (size == 4) *reinterpret_cast<uint32_t*>(dst) = v[u].x;
+          else *reinterpret_cast<uint16_t*>(dst) = (uint16_t)v[u].x;
+        }
+      }
     }
-    constexpr int U = 4;
-    for (int i0 = blockIdx.x * (kEvMoveThreads / lanes) + sub; i0 < moves; i0 += U * per) {
-      const char* src[U];
-      char* dst[U];
-      uint4 v[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * per;
-        const uint32_t f = i < moves ? come[i] : 0xffffffffu, t = i < moves ? hole[i] : 0xffffffffu;
-        src[u] = f == 0xffffffffu || t == 0xffffffffu ? nullptr : base + (uint64_t)f * stride + off;
-        dst[u] = base + (uint64_t)t * stride + off;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (src[u] == nullptr) continue;
-        if (size == 16) v[u] = *reinterpret_cast<const uint4*>(src[u]);
-        else if (size == 8) *reinterpret_cast<uint2*>(&v[u]) = *reinterpret_cast<const uint2*>(src[u]);
-        else if (size == 4) v[u].x = *reinterpret_cast<const uint32_t*>(src[u]);
-        else v[u].x = *reinterpret_cast<const uint16_t*>(src[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (src[u] == nullptr) continue;
-        if (size == 16) *reinterpret_cast<uint4*>(dst[u]) = v[u];
-        else if (size == 8) *reinterpret_cast<uint2*>(dst[u]) = *reinterpret_cast<uint2*>(&v[u]);
-        else if (size == 4) *reinterpret_cast<uint32_t*>(dst[u]) = v[u].x;
-        else *reinterpret_cast<uint16_t*>(dst[u]) = (uint16_t)v[u].x;
-      }
-    }
+  };
+  if (codes + small <= 16) {
+    copy(0, codes + small, 16);
+  } else {
+    copy(0, codes, min(codes, 32));
+    copy(codes, small, small <= 8 ? 8 : 16);
   }
 }
 
@@ -382,10 +488,10 @@ extern "C" int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_b
   if (B > QDA_MAX_B || Hkv > QDA_EVICT_MAX_HEADS) return QDA_ERR_UNSUPPORTED;
   if ((long long)num_pages * page * Hkv >= 0xffffffffLL) return QDA_ERR_UNSUPPORTED;   // pool rows are 32-bit
   if ((long long)max_pages * page > 0x7ffffe00LL) return QDA_ERR_UNSUPPORTED;
-  const void* ptrs[6] = {k_packed, k_scales, k_biases, v_packed, v_scales, v_biases};
+  const void* ptrs[8] = {k_packed, k_scales, k_biases, v_packed, v_scales, v_biases, mass, token};
   for (const void* p : ptrs)
     if (off16(p)) return QDA_ERR_ALIGN;
-  const void* words[8] = {mass, token, kv_len, new_len, block_table, freed, n_freed, shift};
+  const void* words[6] = {kv_len, new_len, block_table, freed, n_freed, shift};
   for (const void* p : words)
     if (off4(p)) return QDA_ERR_ALIGN;
   EvictParams p;
@@ -434,7 +540,10 @@ extern "C" int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_b
   if (ce != cudaSuccess || dev < 0 || dev >= 64) return qda_cuda_fail(ce == cudaSuccess ? cudaErrorInvalidDevice : ce);
   static std::atomic<bool> ready[64] = {};
   if (!ready[dev].load()) {
-    ce = cudaFuncSetAttribute(qda_paged_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHeld * 4);
+    constexpr int most = kEvHeld * 4;
+    ce = cudaFuncSetAttribute(qda_paged_evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (ce == cudaSuccess)
+      ce = cudaFuncSetAttribute(qda_paged_evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (ce != cudaSuccess) return qda_cuda_fail(ce);
     ready[dev].store(true);
   }
@@ -449,7 +558,8 @@ extern "C" int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_b
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  ce = cudaLaunchKernelEx(&cfg, qda_paged_evict_select_kernel, p);
+  ce = e.cluster == 1 ? cudaLaunchKernelEx(&cfg, qda_paged_evict_select_kernel<true>, p)
+                      : cudaLaunchKernelEx(&cfg, qda_paged_evict_select_kernel<false>, p);
   if (ce != cudaSuccess) return qda_cuda_fail(ce);
   cfg.gridDim = dim3((unsigned)e.move_x, (unsigned)(B * Hkv));
   cfg.blockDim = dim3(kEvMoveThreads);

@@ -438,7 +438,7 @@ int qdecode_paged_weights_workspace_bytes(int B, int H, int Hkv, int total_q, in
  * sequences in order; n_freed[0] counts them all, above max_freed some found no place (status bit 8). A length that is
  * negative or beyond the table leaves its sequence as it is and sets bit 8; so does a page outside the pool, of which no row
  * is read or written. Contents of rows from budget on are unspecified. D, GS, bits, pages and B as for the other paged
- * calls, Hkv <= QDA_EVICT_MAX_HEADS, max_pages * page below 2^31 - 512. Uses the workspace as qdecode_attn does, of
+ * calls, Hkv <= QDA_EVICT_MAX_HEADS, max_pages * page below 2^31 - 512; mass and token 16-byte aligned. Uses the workspace as qdecode_attn does, of
  * qdecode_paged_evict_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
  */
 #define QDA_EVICT_MAX_HEADS 64
