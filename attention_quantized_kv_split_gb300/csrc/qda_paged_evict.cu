@@ -45,6 +45,7 @@ __device__ __forceinline__ uint64_t ev_full(uint32_t key, int row) { return (uin
 
 struct alignas(16) EvShared {
   int hist[kEvBins];
+  int coarse[kEvBins / 32];   // sums of 32 bins
   uint64_t few[kEvFew];       // this CTA's ranks that are left
   uint64_t all[kEvFew];       // the cluster's
   int warp[kEvWarps][2];
@@ -59,10 +60,11 @@ struct alignas(16) EvShared {
 // once no more than kEvFew ranks are left, by comparing them all. Ranks are all different (a row's number is part of its
 // rank), so what stays is what is not below the edge. Then holes and rows that come are counted in order, a bit a row, and
 // listed: the i-th hole meets the i-th row that comes, whatever the timing. A row's mass and token are read once. Bound by
-// latency: loads two deep, then some ten barriers.
+// latency: loads two deep, then some ten barriers; reading all of the other CTAs' bins took half of the time (distributed
+// shared memory is slow to read), so that sums of 32 bins come first and then the 32 that matter.
 template <bool ONE>
 __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ uint32_t s_key[];
+  extern __shared__ uint32_t s_key[];   // keys, and behind them the pool row of every sixteenth row (-1: none)
   __shared__ EvShared sh;
   cg::cluster_group cl = cg::this_cluster();
   const int cs = ONE ? 1 : cl.num_blocks(), me = ONE ? 0 : cl.block_rank();
@@ -108,6 +110,7 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
     const uint32_t k = ev_rank(__ldg(p.mass + r));
     return t < p.sinks || t >= young ? 0xffffffffu : k;
   };
+  uint32_t* const s_row = s_key + p.held;
   // four rows of a page at a time (pages hold sixteens of rows, masses and tokens are aligned), four such loads on their way
   constexpr int LQ = 4;
   for (int i0 = lo + 4 * tid; i0 < min(hi, lo + p.held); i0 += LQ * 4 * kEvThreads) {
@@ -137,9 +140,31 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
         k = make_uint4(rank(m[u].x, t[u].x), rank(m[u].y, t[u].y), rank(m[u].z, t[u].z), rank(m[u].w, t[u].w));
       }
       *reinterpret_cast<uint4*>(s_key + i - lo) = k;   // (a piece's room is a multiple of 32 keys)
+      if ((i & 15) == 0) s_row[(i - lo) >> 4] = r[u];
     }
   }
   auto key_at = [&](int i) { return i - lo < p.held ? s_key[i - lo] : load_key(i); };
+  auto row_at = [&](int i) {
+    if (i - lo >= p.held) return row_of(i);
+    const uint32_t r = s_row[(i - lo) >> 4];
+    return r == 0xffffffffu ? r : r + (i & 15);
+  };
+  // f(key, row) for the CTA's rows that have the known bits
+  auto each = [&](uint64_t prefix, int known, auto&& f) {
+    if (known <= 32) {
+      const uint32_t want = (uint32_t)prefix;
+      const int shift = 32 - known;
+      for (int i = lo + tid; i < hi; i += kEvThreads) {
+        const uint32_t k = key_at(i);
+        if (known == 0 || (k >> shift) == want) f(k, i);
+      }
+    } else {
+      for (int i = lo + tid; i < hi; i += kEvThreads) {
+        const uint32_t k = key_at(i);
+        if ((ev_full(k, i) >> (64 - known)) == prefix) f(k, i);
+      }
+    }
+  };
 
   // ---- the budget-th largest rank
   uint64_t prefix = 0;        // the bits that are known, from the top
@@ -149,53 +174,52 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
     const int width = min(11, 64 - known), shift = 64 - known - width;
     for (int i = tid; i < kEvBins / 4; i += kEvThreads) reinterpret_cast<int4*>(sh.hist)[i] = make_int4(0, 0, 0, 0);
     __syncthreads();
-    for (int i = lo + tid; i < hi; i += kEvThreads) {
-      const uint64_t k = ev_full(key_at(i), i);
-      if (known == 0 || (k >> (shift + width)) == prefix) atomicAdd(&sh.hist[(k >> shift) & ((1u << width) - 1)], 1);
+    if (shift >= 32) {
+      each(prefix, known, [&](uint32_t k, int) { atomicAdd(&sh.hist[(k >> (shift - 32)) & ((1u << width) - 1)], 1); });
+    } else {
+      each(prefix, known, [&](uint32_t k, int i) { atomicAdd(&sh.hist[(ev_full(k, i) >> shift) & ((1u << width) - 1)], 1); });
+    }
+    __syncthreads();
+    {   // eight bins a thread, four threads a sum
+      const int4 *h = reinterpret_cast<const int4*>(sh.hist + 8 * tid), u = h[0], v = h[1];
+      int x = (u.x + u.y) + (u.z + u.w) + (v.x + v.y) + (v.z + v.w);
+      x += __shfl_xor_sync(0xffffffffu, x, 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      if ((tid & 3) == 0) sh.coarse[tid >> 2] = x;
     }
     sync();
-    // the cluster's counts of eight bins a thread, highest bins first
-    int c[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const int bin0 = kEvBins - 8 - 8 * tid;
-    constexpr int RU = ONE ? 1 : 4;   // CTAs whose bins are on their way
-    for (int r0 = 0; r0 < cs; r0 += RU) {
-      int4 u[RU], v[RU];
+    if (warp == 0) {
+      // the cluster's sums, the highest bins first: two a lane, the bin of 32 that holds the budget-th rank, then its 32
+      auto gather = [&](const int* x) {
+        int v[ONE ? 1 : kEvCluster], sum = 0;
 #pragma unroll
-      for (int k = 0; k < RU; ++k) {
-        const int4* h = reinterpret_cast<const int4*>(of(sh.hist, ONE ? 0 : min(r0 + k, cs - 1)) + bin0);
-        u[k] = h[1];
-        v[k] = h[0];
-      }
+        for (int r = 0; r < (ONE ? 1 : kEvCluster); ++r) v[r] = r < cs ? *of(x, r) : 0;
 #pragma unroll
-      for (int k = 0; k < RU; ++k) {
-        if (r0 + k >= cs) continue;
-        c[0] += u[k].w, c[1] += u[k].z, c[2] += u[k].y, c[3] += u[k].x;
-        c[4] += v[k].w, c[5] += v[k].z, c[6] += v[k].y, c[7] += v[k].x;
-      }
-    }
-    int mine = 0;
+        for (int r = 0; r < (ONE ? 1 : kEvCluster); ++r) sum += v[r];
+        return sum;
+      };
+      auto scan = [&](int x) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mine += c[j];
-    int up_to = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, up_to, o);
-      if (lane >= o) up_to += v;
-    }
-    if (lane == 31) sh.warp[warp][0] = up_to;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kEvWarps; ++w) up_to += w < warp ? sh.warp[w][0] : 0;
-    int before = above + up_to - mine;   // ranks in higher bins
-    if (before < p.budget && before + mine >= p.budget) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (before < p.budget && before + c[j] >= p.budget) {
-          sh.pick[0] = bin0 + 7 - j;
-          sh.pick[1] = before;
-          sh.pick[2] = c[j];
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += v;
         }
-        before += c[j];
+        return x;
+      };
+      const int c0 = gather(sh.coarse + 63 - 2 * lane), c1 = gather(sh.coarse + 62 - 2 * lane);
+      int before = above + scan(c0 + c1) - c0 - c1;   // ranks in higher bins
+      const bool in0 = before < p.budget && before + c0 >= p.budget;
+      const bool in1 = before + c0 < p.budget && before + c0 + c1 >= p.budget;
+      const uint32_t who = __ballot_sync(0xffffffffu, in0 || in1);
+      const int src = __ffs(who) - 1;
+      const int group = __shfl_sync(0xffffffffu, in0 ? 63 - 2 * lane : 62 - 2 * lane, src);
+      before = __shfl_sync(0xffffffffu, in0 ? before : before + c0, src);
+      const int c = gather(sh.hist + 32 * group + 31 - lane);
+      before += scan(c) - c;
+      if (before < p.budget && before + c >= p.budget) {
+        sh.pick[0] = 32 * group + 31 - lane;
+        sh.pick[1] = before;
+        sh.pick[2] = c;
       }
     }
     sync();   // every CTA has read the histograms
@@ -207,10 +231,7 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
   // ---- the ranks that are left, all of them against each other
   if (tid == 0) sh.n_few = 0;
   __syncthreads();
-  for (int i = lo + tid; i < hi; i += kEvThreads) {
-    const uint64_t k = ev_full(key_at(i), i);
-    if (known == 0 || (k >> (64 - known)) == prefix) sh.few[atomicAdd(&sh.n_few, 1)] = k;   // (in any order; no more than kEvFew)
-  }
+  each(prefix, known, [&](uint32_t k, int i) { sh.few[atomicAdd(&sh.n_few, 1)] = ev_full(k, i); });   // (in any order; few)
   sync();
   const uint64_t* all = sh.few;
   if constexpr (!ONE) {   // every CTA takes all of them, and finds the edge for itself
@@ -237,7 +258,8 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
     if (higher == p.budget - 1) sh.edge = k;
   }
   __syncthreads();
-  const uint64_t edge = sh.edge;
+  const uint32_t edge_key = (uint32_t)(sh.edge >> 32);
+  const int edge_row = (int)~(uint32_t)sh.edge;
 
   // ---- rows in order, 32 at a time as the bits of a word: holes and rows that come before each
   const int words = (hi - lo + 31) >> 5;
@@ -253,13 +275,16 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
   };
   auto stays = [&](int w) {
     const int i = lo + 32 * w + lane;
-    return __ballot_sync(0xffffffffu, i < hi && ev_full(key_at(i), i) >= edge);
+    const uint32_t k = i < hi ? key_at(i) : 0u;
+    return __ballot_sync(0xffffffffu, i < hi && (k > edge_key || (k == edge_key && i <= edge_row)));
   };
   int holes = 0, comes = 0;   // of this warp's words: contiguous, so that warps are in order
   const int part = (words + kEvWarps - 1) / kEvWarps, w_lo = min(words, part * warp), w_hi = min(words, w_lo + part);
+  uint32_t kept = 0;          // lane l: the bits of the warp's word l, where it has no more than 32
 #pragma unroll 2
   for (int w = w_lo; w < w_hi; ++w) {
     const uint32_t stay = stays(w);
+    if (lane == ((w - w_lo) & 31)) kept = stay;
     holes += __popc(~stay & inside(w) & real(w));
     comes += __popc(stay & ~inside(w));
   }
@@ -293,30 +318,17 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
   if (me == cs - 1 && tid == kEvThreads - 32) p.moves[unit] = h_at + holes;
   uint32_t* const hole_list = p.hole + (size_t)unit * p.most;
   uint32_t* const come_list = p.come + (size_t)unit * p.most;
-  constexpr int WU = 4;   // words whose pages are looked up together
-  for (int w0 = w_lo; w0 < w_hi; w0 += WU) {
-    uint32_t h[WU], c[WU], r[WU];
-#pragma unroll
-    for (int u = 0; u < WU; ++u) {
-      const int w = w0 + u;
-      h[u] = c[u] = 0;
-      if (w < w_hi) {   // (the whole warp)
-        const uint32_t stay = stays(w);
-        h[u] = ~stay & inside(w) & real(w);
-        c[u] = stay & ~inside(w);
-      }
-      r[u] = ((h[u] | c[u]) >> lane) & 1u ? row_of(lo + 32 * w + lane) : 0;
+  for (int w = w_lo; w < w_hi; ++w) {
+    const uint32_t stay = part <= 32 ? __shfl_sync(0xffffffffu, kept, (w - w_lo) & 31) : stays(w);
+    const uint32_t h = ~stay & inside(w) & real(w), c = stay & ~inside(w);
+    if ((h | c) == 0) continue;   // (the whole warp)
+    if (((h | c) >> lane) & 1u) {
+      const bool hole = (h >> lane) & 1u;
+      const int j = hole ? h_at + __popc(h & below) : c_at + __popc(c & below);
+      if (j < p.most) (hole ? hole_list : come_list)[j] = row_at(lo + 32 * w + lane);
     }
-#pragma unroll
-    for (int u = 0; u < WU; ++u) {
-      if (((h[u] | c[u]) >> lane) & 1u) {
-        const bool hole = (h[u] >> lane) & 1u;
-        const int j = hole ? h_at + __popc(h[u] & below) : c_at + __popc(c[u] & below);
-        if (j < p.most) (hole ? hole_list : come_list)[j] = r[u];
-      }
-      h_at += __popc(h[u]);
-      c_at += __popc(c[u]);
-    }
+    h_at += __popc(h);
+    c_at += __popc(c);
   }
 }
 
@@ -540,7 +552,7 @@ extern "C" int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_b
   if (ce != cudaSuccess || dev < 0 || dev >= 64) return qda_cuda_fail(ce == cudaSuccess ? cudaErrorInvalidDevice : ce);
   static std::atomic<bool> ready[64] = {};
   if (!ready[dev].load()) {
-    constexpr int most = kEvHeld * 4;
+    constexpr int most = kEvHeld * 4 + kEvHeld / 4;
     ce = cudaFuncSetAttribute(qda_paged_evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (ce == cudaSuccess)
       ce = cudaFuncSetAttribute(qda_paged_evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
@@ -551,7 +563,7 @@ extern "C" int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_b
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * Hkv * e.cluster));
   cfg.blockDim = dim3(kEvThreads);
-  cfg.dynamicSmemBytes = (size_t)e.held * 4;
+  cfg.dynamicSmemBytes = (size_t)e.held * 4 + e.held / 4;
   cfg.stream = s;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)e.cluster;
