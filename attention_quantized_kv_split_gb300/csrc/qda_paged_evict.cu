@@ -464,7 +464,7 @@ static EvictPlan evict_plan(int B, int Hkv, long long rows, int budget, int sms)
   const int units = B * Hkv;
   // CTAs per head: enough to fill the SMs, none with less than 2048 rows
   e.cluster = kEvCluster;
-  while (e.cluster > 1 && ((long long)units * e.cluster > 2LL * sms || rows < 2048LL * e.cluster)) e.cluster /= 2;
+  while (e.cluster > 1 && ((long long)units * e.cluster > 4LL * sms || rows < 2048LL * e.cluster)) e.cluster /= 2;
   e.held = (int)std::min<long long>(kEvHeld, ((rows + e.cluster - 1) / e.cluster + 31) & ~31LL);
   e.most = std::max(1LL, std::min((long long)budget, rows - budget));
   e.list_bytes = ((size_t)units * e.most * 4 + 255) & ~(size_t)255;

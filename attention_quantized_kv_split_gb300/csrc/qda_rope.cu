@@ -12,7 +12,7 @@
 
 namespace qda {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256;   // at most
 constexpr int kRopeAngles = 2048;   // cosines and sines that a CTA holds: 16 KB
 
 struct RopeParams {
@@ -24,7 +24,7 @@ struct RopeParams {
   const int* q_start;       // [B + 1], or nullptr
   const int* shift;         // [B]
   int T, B, heads[2], rot, tokens, head_step, inverse;
-  int items;                // a row's pairs of vectors
+  int items, rows;          // a row's pairs of vectors; rows that the CTA's threads take at a time
   float scale;
 };
 
@@ -54,119 +54,154 @@ struct alignas(sizeof(T) * V) RopeVec {
 // 64-bit fraction, n * round(2^64 frac(f / 2 pi)) mod 2^64: whole turns drop out of the integer product exactly, so that a
 // position of 2^31 costs no more than 2^-24 of a turn and no argument reduction, where a product in fp32 would be off by
 // 0.06 radians at 2^20. A CTA takes a few tokens: their cosines and sines go to shared memory, one thread each, and are used
-// by every head. A thread turns V pairs: two 16-byte loads (the two halves' values, or 2 V values side by side when pairs are
-// interleaved), and four such items are in flight.
+// by every head. A thread has one place in a row, V pairs there (two 16-byte loads: the two halves' values, or 2 V values side
+// by side when pairs are interleaved), and walks rows, so that it reads its cosines once a token and divides nowhere; the next
+// two rows are on their way while two are turned, the first ones while the angles are computed.
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) qda_rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 cs[kRopeAngles];
+  __shared__ __align__(16) float2 cs[kRopeAngles];
   __shared__ int s_pos[kRopeAngles];
   __shared__ int s_start[QDA_MAX_B + 1];
   using Vec = RopeVec<T, V>;
   const int tid = threadIdx.x, half = p.rot >> 1;
   const int t0 = blockIdx.x * p.tokens, nt = min(p.tokens, p.T - t0);
+  const int x = tid % p.items, y = tid / p.items;
+  const int hq = p.heads[0], h0 = blockIdx.y * p.head_step, nh = min(p.head_step, hq + p.heads[1] - h0);
+  const int turned = half / V;   // places that turn; those behind them are copied
+  const bool turns = x < turned;
+  const int d0 = turns && !INTER ? x * V : 2 * x * V, d1 = d0 + (turns && !INTER ? half : V);
+  constexpr int U = 2;
+  struct Rows {
+    Vec a[U], b[U];
+    int t, h;                    // token of the CTA and first row of its heads
+  };
+  Rows now, next;
+  auto place = [&](int h, int* w, int* hh) {
+    *w = h0 + h >= hq;
+    *hh = h0 + h - (*w ? hq : 0);
+  };
+  auto load = [&](Rows& r, int t, int h) {
+    r.t = t;
+    r.h = h;
+    if (t >= nt) return;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = h + u * p.rows;
+      if (i >= nh) continue;
+      int w, hh;
+      place(i, &w, &hh);
+      const T* src = static_cast<const T*>(p.x[w]) + (long long)(t0 + t) * p.xt[w] + hh * p.xh[w];
+      r.a[u] = *reinterpret_cast<const Vec*>(src + d0);
+      r.b[u] = *reinterpret_cast<const Vec*>(src + d1);
+    }
+  };
+  const bool busy = y < p.rows;
+  if (busy) load(now, 0, y);
+  else now.t = nt;
   if (p.shift != nullptr) {
-    for (int i = tid; i <= p.B; i += kRopeThreads) s_start[i] = p.q_start[i];
+    for (int i = tid; i <= p.B; i += blockDim.x) s_start[i] = p.q_start[i];
     __syncthreads();
   }
-  for (int i = tid; i < nt; i += kRopeThreads) {
+  for (int i = tid; i < nt; i += blockDim.x) {
     int pos = p.positions[t0 + i];
     if (pos >= 0 && p.shift != nullptr && t0 + i >= s_start[0] && t0 + i < s_start[p.B])
       pos += p.shift[qda_seq_of(s_start, p.B, t0 + i)];
     s_pos[i] = pos;
   }
   __syncthreads();
-  for (int i = tid; i < nt * half; i += kRopeThreads) {
+  for (int i = tid; i < nt * half; i += blockDim.x) {
     const int t = i / half, j = i - t * half;
-    const double turns = p.freqs[j] * 0.15915494309189533577;
-    const unsigned long long step = (unsigned long long)__double2ll_rn((turns - rint(turns)) * 18446744073709551616.0);
+    const double f = p.freqs[j] * 0.15915494309189533577;
+    const unsigned long long step = (unsigned long long)__double2ll_rn((f - rint(f)) * 18446744073709551616.0);
     const int phase = (int)((step * (unsigned long long)(unsigned)s_pos[t]) >> 32);
     float s, c;
     sincospif((float)phase * 4.656612873077392578125e-10f, &s, &c);   // half turns: phase 2^-31
     cs[i] = make_float2(p.scale * c, p.inverse ? -p.scale * s : p.scale * s);
   }
   __syncthreads();
-  const int items = p.items, per = kRopeThreads / items;
-  const int x = tid % items, y = tid / items;
-  if (y >= per) return;
-  const int hq = p.heads[0], h0 = blockIdx.y * p.head_step, nh = min(p.head_step, hq + p.heads[1] - h0);
-  const int turned = half / V;   // items that turn; those behind them are copied
-  constexpr int U = 4;
-  for (int r0 = y; r0 < nt * nh; r0 += U * per) {
-    Vec a[U], b[U];
-    bool live[U];
-    T* dst[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * per;
-      live[u] = r < nt * nh;
-      if (!live[u]) continue;
-      const int t = r / nh, h = h0 + r - t * nh;
-      const int w = h >= hq, hh = w ? h - hq : h;
-      const long long at = (long long)(t0 + t) * p.xt[w] + hh * p.xh[w], to = (long long)(t0 + t) * p.yt[w] + hh * p.yh[w];
-      const T* src = static_cast<const T*>(p.x[w]) + at;
-      dst[u] = static_cast<T*>(p.y[w]) + to;
-      live[u] = s_pos[t] >= 0 && (x < turned || dst[u] != src);
-      if (!live[u]) continue;
-      const int d = x < turned && !INTER ? x * V : 2 * x * V;
-      a[u] = *reinterpret_cast<const Vec*>(src + d);
-      b[u] = *reinterpret_cast<const Vec*>(src + d + (x < turned && !INTER ? half : V));
+  float2 k[V];
+  int held = -1;                 // the token whose cosines are in k
+  while (now.t < nt) {
+    {
+      const int h = now.h + U * p.rows;
+      if (h < nh) load(next, now.t, h);
+      else load(next, now.t + 1, y);
     }
+    if (s_pos[now.t] >= 0) {
+      if (turns && held != now.t) {
+        held = now.t;
+        const float2* c = cs + now.t * half + x * V;
+        if constexpr (V >= 2) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (!live[u]) continue;
-      if (x < turned) {
-        const float2* c = cs + (r0 + u * per) / nh * half + x * V;
-        if constexpr (INTER) {
-          float v[2 * V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            v[i] = rope_get(a[u].v[i]);
-            v[V + i] = rope_get(b[u].v[i]);
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float2 k = c[i];
-            const float e = v[2 * i], o = v[2 * i + 1];
-            v[2 * i] = fmaf(e, k.x, -o * k.y);
-            v[2 * i + 1] = fmaf(o, k.x, e * k.y);
-          }
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            a[u].v[i] = rope_put<T>(v[i]);
-            b[u].v[i] = rope_put<T>(v[V + i]);
+          for (int i = 0; i < V; i += 2) {
+            const float4 f = *reinterpret_cast<const float4*>(c + i);   // (half is a multiple of V)
+            k[i] = make_float2(f.x, f.y);
+            k[i + 1] = make_float2(f.z, f.w);
           }
         } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float2 k = c[i];
-            const float e = rope_get(a[u].v[i]), o = rope_get(b[u].v[i]);
-            a[u].v[i] = rope_put<T>(fmaf(e, k.x, -o * k.y));
-            b[u].v[i] = rope_put<T>(fmaf(o, k.x, e * k.y));
-          }
+          k[0] = c[0];
         }
       }
-      const int d = x < turned && !INTER ? x * V : 2 * x * V;
-      *reinterpret_cast<Vec*>(dst[u] + d) = a[u];
-      *reinterpret_cast<Vec*>(dst[u] + d + (x < turned && !INTER ? half : V)) = b[u];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = now.h + u * p.rows;
+        if (h >= nh) continue;
+        int w, hh;
+        place(h, &w, &hh);
+        const long long at = (long long)(t0 + now.t) * p.yt[w] + hh * p.yh[w];
+        T* dst = static_cast<T*>(p.y[w]) + at;
+        if (!turns && p.x[w] == p.y[w]) continue;   // in place: the rest stands there already
+        if (turns) {
+          if constexpr (INTER) {
+            float v[2 * V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              v[i] = rope_get(now.a[u].v[i]);
+              v[V + i] = rope_get(now.b[u].v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float e = v[2 * i], o = v[2 * i + 1];
+              v[2 * i] = fmaf(e, k[i].x, -o * k[i].y);
+              v[2 * i + 1] = fmaf(o, k[i].x, e * k[i].y);
+            }
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              now.a[u].v[i] = rope_put<T>(v[i]);
+              now.b[u].v[i] = rope_put<T>(v[V + i]);
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float e = rope_get(now.a[u].v[i]), o = rope_get(now.b[u].v[i]);
+              now.a[u].v[i] = rope_put<T>(fmaf(e, k[i].x, -o * k[i].y));
+              now.b[u].v[i] = rope_put<T>(fmaf(o, k[i].x, e * k[i].y));
+            }
+          }
+        }
+        *reinterpret_cast<Vec*>(dst + d0) = now.a[u];
+        *reinterpret_cast<Vec*>(dst + d1) = now.b[u];
+      }
     }
+    now = next;
   }
 }
 
 template <typename T, int V>
-cudaError_t rope_run(const RopeParams& p, bool inter, dim3 grid, cudaStream_t s) {
-  if (inter) qda_rope_kernel<T, V, true><<<grid, kRopeThreads, 0, s>>>(p);
-  else qda_rope_kernel<T, V, false><<<grid, kRopeThreads, 0, s>>>(p);
+cudaError_t rope_run(const RopeParams& p, bool inter, dim3 grid, int threads, cudaStream_t s) {
+  if (inter) qda_rope_kernel<T, V, true><<<grid, threads, 0, s>>>(p);
+  else qda_rope_kernel<T, V, false><<<grid, threads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t rope_pick(const RopeParams& p, int V, bool inter, dim3 grid, cudaStream_t s) {
+cudaError_t rope_pick(const RopeParams& p, int V, bool inter, dim3 grid, int threads, cudaStream_t s) {
   if constexpr (sizeof(T) == 2) {
-    if (V == 8) return rope_run<T, 8>(p, inter, grid, s);
+    if (V == 8) return rope_run<T, 8>(p, inter, grid, threads, s);
   }
-  return V == 4 ? rope_run<T, 4>(p, inter, grid, s)
-         : V == 2 ? rope_run<T, 2>(p, inter, grid, s)
-                  : rope_run<T, 1>(p, inter, grid, s);
+  return V == 4 ? rope_run<T, 4>(p, inter, grid, threads, s)
+         : V == 2 ? rope_run<T, 2>(p, inter, grid, threads, s)
+                  : rope_run<T, 1>(p, inter, grid, threads, s);
 }
 
 // Whether T tokens' rows of `heads` heads and D values of e bytes at a and at b touch the same memory. Exact for rows of one
@@ -273,19 +308,21 @@ extern "C" int qdecode_rope(const void* q, long long q_tstride, long long q_hstr
   while ((rot / 2) % V != 0) V /= 2;
   p.items = D / (2 * V);
   const int all = H + Hkv;
-  // as many tokens to a CTA as give each thread eight items, or fewer where that leaves SMs idle; then heads are shared too
-  const long long per = kRopeThreads / p.items;
-  long long tokens = std::max(1LL, 8 * per / all);
-  tokens = std::min(tokens, std::max(1LL, (long long)T / (4LL * sms)));
+  // rows at a time: all heads in as few rounds as 256 threads allow, rounds of equal size
+  const int rounds = (int)(((long long)all * p.items + kRopeThreads - 1) / kRopeThreads);
+  p.rows = (all + rounds - 1) / rounds;
+  // tokens to a CTA: up to eight rounds, fewer where that leaves SMs without CTAs; with few tokens the rounds are shared
+  long long tokens = std::max(1LL, 8LL / rounds);
+  tokens = std::min(tokens, std::max(1LL, (long long)T / (6LL * sms)));
   tokens = std::min(tokens, (long long)(kRopeAngles / (rot / 2)));
-  long long splits = 1;
-  if (tokens == 1) splits = std::max(1LL, std::min((2LL * sms + T - 1) / T, (all + per - 1) / per));
+  const int splits = tokens == 1 ? (int)std::min<long long>(rounds, std::max(1LL, 4LL * sms / T)) : 1;
   p.tokens = (int)tokens;
-  p.head_step = (int)((all + splits - 1) / splits);
+  p.head_step = (rounds + splits - 1) / splits * p.rows;
   const dim3 grid((unsigned)((T + tokens - 1) / tokens), (unsigned)((all + p.head_step - 1) / p.head_step));
+  const int threads = (p.rows * p.items + 31) & ~31;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t ce = dtype == QDA_FP32   ? rope_pick<float>(p, V, interleaved != 0, grid, s)
-                         : dtype == QDA_FP16 ? rope_pick<__half>(p, V, interleaved != 0, grid, s)
-                                             : rope_pick<__nv_bfloat16>(p, V, interleaved != 0, grid, s);
+  const cudaError_t ce = dtype == QDA_FP32   ? rope_pick<float>(p, V, interleaved != 0, grid, threads, s)
+                         : dtype == QDA_FP16 ? rope_pick<__half>(p, V, interleaved != 0, grid, threads, s)
+                                             : rope_pick<__nv_bfloat16>(p, V, interleaved != 0, grid, threads, s);
   return ce == cudaSuccess ? QDA_OK : qda_cuda_fail(ce);
 }
