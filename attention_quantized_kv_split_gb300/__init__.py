@@ -331,15 +331,19 @@ def qdecode_paged_attn(q: torch.Tensor, k_packed: torch.Tensor, k_scales: torch.
     if T and qd != 1:
         raise ValueError("rows of q must be contiguous")
     _ints(dev, "q_start kv_len block_table", q_start, kv_len, block_table)
-    arrays = (q.data_ptr(), qt, qh, k_packed.data_ptr(), k_scales.data_ptr(), k_biases.data_ptr(), v_packed.data_ptr(),
-              v_scales.data_ptr(), v_biases.data_ptr(), out.data_ptr())
-    rest = (q_start.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(), T, max_q, B, H, Hkv, pages, page, max_pages,
-            1 if causal else 0, D, GS, bits, _DT_CODE[dt])
     if lse is None:
-        _paged_call(2, "qdecode_paged_attn", _PACK_ATTN, dev, stream, arrays + rest)
-    else:
-        _floats(dev, "lse", lse, (T, H))
-        _paged_call(4, "qdecode_paged_attn_lse", _PACK_LSE, dev, stream, (*arrays, lse.data_ptr(), *rest))
+        _paged_call(2, "qdecode_paged_attn", _PACK_ATTN, dev, stream,
+                    (q.data_ptr(), qt, qh, k_packed.data_ptr(), k_scales.data_ptr(), k_biases.data_ptr(), v_packed.data_ptr(),
+                     v_scales.data_ptr(), v_biases.data_ptr(), out.data_ptr(), q_start.data_ptr(), kv_len.data_ptr(),
+                     block_table.data_ptr(), T, max_q, B, H, Hkv, pages, page, max_pages, 1 if causal else 0, D, GS, bits,
+                     _DT_CODE[dt]))
+        return out
+    _floats(dev, "lse", lse, (T, H))
+    _paged_call(4, "qdecode_paged_attn_lse", _PACK_LSE, dev, stream,
+                (q.data_ptr(), qt, qh, k_packed.data_ptr(), k_scales.data_ptr(), k_biases.data_ptr(), v_packed.data_ptr(),
+                 v_scales.data_ptr(), v_biases.data_ptr(), out.data_ptr(), lse.data_ptr(), q_start.data_ptr(),
+                 kv_len.data_ptr(), block_table.data_ptr(), T, max_q, B, H, Hkv, pages, page, max_pages, 1 if causal else 0,
+                 D, GS, bits, _DT_CODE[dt]))
     return out
 
 

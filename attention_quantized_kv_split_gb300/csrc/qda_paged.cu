@@ -328,7 +328,7 @@ cudaError_t launch_append_types(const AppendParams& p, int D, bool f16, int src,
 // launch, ahead of the end of the kernel before it. Bound by latency: a record, then its parts (behind the 64 sequences'
 // tokens 6 us, behind 131072 keys 11, behind the long chunk 14). The kernels before it leave the records; when the merge
 // found the shared tiles by scanning the lengths itself, it took 45 us more behind 64 sequences' tokens.
-template <int D, int WPR>
+template <int D, int WPR, bool LSE>
 __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_constant__ QdaPagedParams p, int MT) {
   constexpr int E = D / 64;   // pairs of values per lane
   __shared__ float2 s_o[WPR > 1 ? 8 : 1][D / 2];
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(256) qda_paged_merge_kernel(const __grid_const
 #pragma unroll
   for (int e = 0; e < E; ++e)
     dst[e * 32 + lane] = p.f16 ? to_bits16x2<true>(o[e].x * inv, o[e].y * inv) : to_bits16x2<false>(o[e].x * inv, o[e].y * inv);
-  if (lane == 0 && t.unit % p.parts == 0 && p.lse != nullptr)
+  if (LSE && lane == 0 && t.unit % p.parts == 0)
     qda_put_lse(p, t.token0 + tok, (t.unit / p.parts) * p.nrep + (row - tok * p.nrep), m, l, p.lse_unit);
 }
 
@@ -422,8 +422,11 @@ cudaError_t launch_merge(const QdaPagedParams& p, int rows, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 8>, p, rows)
-             : cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 1>, p, rows);
+  if (p.lse != nullptr)
+    return few ? cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 8, true>, p, rows)
+               : cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 1, true>, p, rows);
+  return few ? cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 8, false>, p, rows)
+             : cudaLaunchKernelEx(&cfg, qda_paged_merge_kernel<D, 1, false>, p, rows);
 }
 
 // ----------------------------------------------------------------------------- rows beside keys that they do not see
@@ -813,7 +816,10 @@ struct PagedPlan {
 };
 
 using SplitFn = cudaError_t (*)(const QdaPagedParams*, int, int, int, int*, cudaStream_t);
-SplitFn split_fn(int bits, bool f16) {
+SplitFn split_fn(int bits, bool f16, bool lse) {
+  if (lse)
+    return bits == 4 ? (f16 ? qda_paged_split_b4_f1_lse : qda_paged_split_b4_f0_lse)
+                     : (f16 ? qda_paged_split_b8_f1_lse : qda_paged_split_b8_f0_lse);
   return bits == 4 ? (f16 ? qda_paged_split_b4_f1 : qda_paged_split_b4_f0)
                    : (f16 ? qda_paged_split_b8_f1 : qda_paged_split_b8_f0);
 }
@@ -827,11 +833,12 @@ SplitFn split_fn(int bits, bool f16) {
 // keys (93 us) take 375 us in one call with max_q = 512, where every token walks its keys as a tile of 256 rows.
 constexpr long long split_rows(int D) { return D == 512 ? 24 : D == 256 ? 16 : 32; }
 
-cudaError_t chunk_run(const QdaPagedParams* p, int D, int bits, int rows, bool prepare, cudaStream_t s) {
-  return bits == 4 ? qda_paged_chunk_b4(p, D, rows / 128, prepare, s) : qda_paged_chunk_b8(p, D, rows / 128, prepare, s);
+cudaError_t chunk_run(const QdaPagedParams* p, int D, int bits, int rows, bool lse, bool prepare, cudaStream_t s) {
+  const auto run = bits == 4 ? (lse ? qda_paged_chunk_b4_lse : qda_paged_chunk_b4) : (lse ? qda_paged_chunk_b8_lse : qda_paged_chunk_b8);
+  return run(p, D, rows / 128, prepare, s);
 }
 
-int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int sms, PagedPlan* plan) {
+int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, bool lse, int sms, PagedPlan* plan) {
   const long long rows = max_q * nrep;
   int dev = 0;
   const cudaError_t de = cudaGetDevice(&dev);
@@ -843,10 +850,10 @@ int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int
     plan->min_keys = 512;
     plan->parts = D == 512 ? 2 : 1;
     plan->ctas = sms;
-    static std::atomic<bool> ready[64][2][4][2] = {};
-    std::atomic<bool>& r = ready[dev][bits == 8][di][plan->rows == 256];
+    static std::atomic<bool> ready[64][2][2][4][2] = {};
+    std::atomic<bool>& r = ready[dev][lse][bits == 8][di][plan->rows == 256];
     if (!r.load()) {
-      const cudaError_t e = chunk_run(nullptr, D, bits, plan->rows, true, nullptr);
+      const cudaError_t e = chunk_run(nullptr, D, bits, plan->rows, lse, true, nullptr);
       if (e != cudaSuccess) return qda_cuda_fail(e);
       r.store(true);
     }
@@ -854,14 +861,20 @@ int paged_plan(int nrep, long long max_q, int D, int GS, int bits, bool f16, int
     plan->rows = rows > 8 && D <= 256 ? 16 : 8;
     plan->min_keys = 176;
     plan->parts = 1;
-    static std::atomic<int> cache[64][2][2][4][3][2] = {};   // resident CTAs per SM of an instance, 0 = not asked yet
-    std::atomic<int>& slot = cache[dev][bits == 8][f16][di][gi][plan->rows == 16];
-    int occ = slot.load();
-    if (occ == 0) {
-      const cudaError_t e = split_fn(bits, f16)(nullptr, D, GS, plan->rows, &occ, nullptr);
-      if (e != cudaSuccess) return qda_cuda_fail(e);
-      occ = std::max(occ, 1);
-      slot.store(occ);
+    // resident CTAs per SM of an instance, 0 = not asked yet. The grid is the one of the instance without the rows' sums for
+    // either, so that a call's outputs do not depend on whether it asks for them.
+    static std::atomic<int> cache[64][2][2][2][4][3][2] = {};
+    int occ = 0;
+    for (int with = 0; with <= (lse ? 1 : 0); ++with) {
+      std::atomic<int>& slot = cache[dev][with][bits == 8][f16][di][gi][plan->rows == 16];
+      int n = slot.load();
+      if (n == 0) {
+        const cudaError_t e = split_fn(bits, f16, with != 0)(nullptr, D, GS, plan->rows, &n, nullptr);
+        if (e != cudaSuccess) return qda_cuda_fail(e);
+        n = std::max(n, 1);
+        slot.store(n);
+      }
+      if (with == 0) occ = n;
     }
     plan->ctas = sms * occ;
   }
@@ -974,13 +987,13 @@ extern "C" int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max
   unsigned int* err;
   int got = qda_device(&sms, &err);
   if (got != QDA_OK) return got;
-  // a call may state a smaller max_q than this one, and either dtype
+  // a call may state a smaller max_q than this one, either dtype, and ask for the rows' sums or not
   size_t most = 0;
-  for (int f16 = 0; f16 < 2; ++f16) {
+  for (int kind = 0; kind < 4; ++kind) {
     for (long long m : {1LL, split_rows(D) / (H / Hkv), 128LL / (H / Hkv), (long long)max_q}) {
       m = std::max(1LL, std::min(m, (long long)max_q));
       PagedPlan plan;
-      got = paged_plan(H / Hkv, m, D, GS, bits, f16 != 0, sms, &plan);
+      got = paged_plan(H / Hkv, m, D, GS, bits, (kind & 1) != 0, (kind & 2) != 0, sms, &plan);
       if (got != QDA_OK) return got;
       most = std::max(most, plan.bytes);
     }
@@ -1057,7 +1070,7 @@ static int paged_attn(const void* q, long long q_tstride, long long q_hstride, c
   p.f16 = dtype == QDA_FP16;
   p.qscale = 1.4426950408889634f / sqrtf((float)D);
   PagedPlan plan;
-  st = paged_plan(p.nrep, max_q, D, GS, bits, p.f16 != 0, sms, &plan);
+  st = paged_plan(p.nrep, max_q, D, GS, bits, p.f16 != 0, lse != nullptr, sms, &plan);
   if (st != QDA_OK) return st;
   void* ws = nullptr;
   st = qda_workspace(plan.bytes, &ws);
@@ -1074,8 +1087,8 @@ static int paged_attn(const void* q, long long q_tstride, long long q_hstride, c
   p.stall_block = qda_stall_chunk();
 #endif
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = plan.chunk ? chunk_run(&p, D, bits, plan.rows, false, s)
-                             : split_fn(bits, p.f16 != 0)(&p, D, GS, plan.rows, nullptr, s);
+  cudaError_t e = plan.chunk ? chunk_run(&p, D, bits, plan.rows, lse != nullptr, false, s)
+                             : split_fn(bits, p.f16 != 0, lse != nullptr)(&p, D, GS, plan.rows, nullptr, s);
   if (e == cudaSuccess) e = qda_launch_paged_merge(p, plan.rows, s);
   if (e == cudaSuccess && plan.chunk && p.causal) e = launch_far(p, bits, sms, s);
   return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);

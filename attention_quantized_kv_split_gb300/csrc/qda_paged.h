@@ -69,17 +69,23 @@ __host__ __device__ inline long long qda_pool_row(int pg, int kvh, int r, int Hk
   return ((((long long)pg * Hkv) + kvh) << page_shift) + r;
 }
 
-// The split kernel (qda_paged_split.cuh), translation units per (bits, fp16): its instance for (D, GS, rows per tile).
+// The split kernel (qda_paged_split.cuh), translation units per (bits, fp16), with and without the rows' sums: its instance for (D, GS, rows per tile).
 // With ctas_per_sm the instance's resident CTAs per SM are stored there and nothing is launched; else p.ctas CTAs are.
 cudaError_t qda_paged_split_b4_f0(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_split_b4_f0_lse(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 cudaError_t qda_paged_split_b4_f1(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_split_b4_f1_lse(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 cudaError_t qda_paged_split_b8_f0(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_split_b8_f0_lse(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 cudaError_t qda_paged_split_b8_f1(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
+cudaError_t qda_paged_split_b8_f1_lse(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 
 // The chunk kernel (qda_paged_chunk.cuh): 128 * tiles query rows per tile (tiles 1 or 2; 1 for D > 128), one CTA per SM.
 // prepare sets the instance's shared memory limit on the current device and launches nothing.
 cudaError_t qda_paged_chunk_b4(const QdaPagedParams* p, int D, int tiles, bool prepare, cudaStream_t s);
+cudaError_t qda_paged_chunk_b4_lse(const QdaPagedParams* p, int D, int tiles, bool prepare, cudaStream_t s);
 cudaError_t qda_paged_chunk_b8(const QdaPagedParams* p, int D, int tiles, bool prepare, cudaStream_t s);
+cudaError_t qda_paged_chunk_b8_lse(const QdaPagedParams* p, int D, int tiles, bool prepare, cudaStream_t s);
 
 // Merge of the split tiles' partial results, behind a kernel of `rows` rows per tile.
 cudaError_t qda_launch_paged_merge(const QdaPagedParams& p, int rows, cudaStream_t s);

@@ -170,7 +170,7 @@ __device__ __forceinline__ void pc_each(F&& f) {
   }
 }
 
-template <int D, int BITS, int NQ>
+template <int D, int BITS, int NQ, bool LSE>
 __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
     qda_paged_chunk_kernel(const __grid_constant__ QdaPagedParams p) {
   using G = PcGeom<D, BITS, NQ>;
@@ -534,10 +534,13 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
       const bool whole = t->whole;
       const bool none = m == -INFINITY && l == l;   // the row saw no key
       const int tok = r / p.nrep;
-      // (the logarithm here by the approximate instruction: fewer registers beside the softmax's)
-      if (p.lse != nullptr && real && whole && half == 0 && t->part == 0)
-        p.lse[(long long)(t->s.first + tok) * p.H + t->kvh * p.nrep + (r - tok * p.nrep)] =
-            l == 0.f ? -INFINITY : (m - kPcWeightBits + pc_lg2(l)) * 0.693147180559945309f;
+      // (an instance of its own for calls that want it, and the approximate logarithm: in the one kernel for all calls the
+      // registers cost the softmax loop 3 to 5 % of the chunk over 32768 keys)
+      if constexpr (LSE) {
+        if (real && whole && half == 0 && t->part == 0)
+          p.lse[(long long)(t->s.first + tok) * p.H + t->kvh * p.nrep + (r - tok * p.nrep)] =
+              l == 0.f ? -INFINITY : (m - kPcWeightBits + pc_lg2(l)) * 0.693147180559945309f;
+      }
       const size_t slot = (size_t)(2 * cta + t->mine) * MT + rt;
       uint4* out = reinterpret_cast<uint4*>(
           p.out + ((long long)(t->s.first + tok) * p.H + t->kvh * p.nrep + (r - tok * p.nrep)) * D + t->part * DV);
@@ -1017,9 +1020,9 @@ __global__ void __launch_bounds__(PcGeom<D, BITS, NQ>::WARPS * 32, 1)
   }
 }
 
-template <int D, int BITS, int NQ>
+template <int D, int BITS, int NQ, bool LSE>
 cudaError_t pc_run(const QdaPagedParams* p, bool prepare, cudaStream_t s) {
-  auto kern = qda_paged_chunk_kernel<D, BITS, NQ>;
+  auto kern = qda_paged_chunk_kernel<D, BITS, NQ, LSE>;
   constexpr int smem = pc_smem<D, BITS, NQ>();
   static_assert(smem <= 227 * 1024, "shared memory of a CTA");
   if (prepare) return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1027,13 +1030,13 @@ cudaError_t pc_run(const QdaPagedParams* p, bool prepare, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int BITS>
+template <int BITS, bool LSE>
 cudaError_t pc_pick(const QdaPagedParams* p, int D, int tiles, bool prepare, cudaStream_t s) {
   switch (D) {
-    case 64: return tiles == 2 ? pc_run<64, BITS, 2>(p, prepare, s) : pc_run<64, BITS, 1>(p, prepare, s);
-    case 128: return tiles == 2 ? pc_run<128, BITS, 2>(p, prepare, s) : pc_run<128, BITS, 1>(p, prepare, s);
-    case 256: return pc_run<256, BITS, 1>(p, prepare, s);
-    case 512: return pc_run<512, BITS, 1>(p, prepare, s);
+    case 64: return tiles == 2 ? pc_run<64, BITS, 2, LSE>(p, prepare, s) : pc_run<64, BITS, 1, LSE>(p, prepare, s);
+    case 128: return tiles == 2 ? pc_run<128, BITS, 2, LSE>(p, prepare, s) : pc_run<128, BITS, 1, LSE>(p, prepare, s);
+    case 256: return pc_run<256, BITS, 1, LSE>(p, prepare, s);
+    case 512: return pc_run<512, BITS, 1, LSE>(p, prepare, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -183,7 +183,7 @@ __device__ __forceinline__ uint32_t ps_out2(float a, float b) {
   }
 }
 
-template <int BITS, int D, int GS, int NT, bool F16>
+template <int BITS, int D, int GS, int NT, bool F16, bool LSE>
 __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
     qda_paged_split_kernel(const __grid_constant__ QdaPagedParams p) {
   using G = PsGeom<BITS, D, GS, NT>;
@@ -743,7 +743,7 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
             else *reinterpret_cast<float2*>(po + d + 2 * lane) = v;
           }
           if (!whole && lane == 0) p.part_ml[(size_t)slot * MT + r] = make_float2(M, L);
-          if (whole && lane == 0 && p.lse != nullptr)
+          if (LSE && whole && lane == 0)
             qda_put_lse(p, t.s.first + tok, t.unit * p.nrep + (row0 + r - tok * p.nrep), M, L, 0.f);
         }
       }
@@ -757,10 +757,10 @@ __global__ void __launch_bounds__(kPsWarps * 32, PsGeom<BITS, D, GS, NT>::MINB)
   }
 }
 
-template <int BITS, int D, int GS, int NT, bool F16>
+template <int BITS, int D, int GS, int NT, bool F16, bool LSE>
 cudaError_t ps_run(const QdaPagedParams* p, int* ctas_per_sm, cudaStream_t s) {
   using G = PsGeom<BITS, D, GS, NT>;
-  auto kern = qda_paged_split_kernel<BITS, D, GS, NT, F16>;
+  auto kern = qda_paged_split_kernel<BITS, D, GS, NT, F16, LSE>;
   if (ctas_per_sm != nullptr) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(ctas_per_sm, kern, kPsWarps * 32, G::SMEM);
@@ -770,14 +770,14 @@ cudaError_t ps_run(const QdaPagedParams* p, int* ctas_per_sm, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-template <int BITS, bool F16>
+template <int BITS, bool F16, bool LSE>
 cudaError_t ps_pick(const QdaPagedParams* p, int D, int GS, int rows, int* occ, cudaStream_t s) {
 #define QDA_PS(d, gs)                                                                   \
   if (D == d && GS == gs) {                                                             \
     if constexpr (d <= 256) {                                                           \
-      if (rows > 8) return ps_run<BITS, d, gs, 2, F16>(p, occ, s);                      \
+      if (rows > 8) return ps_run<BITS, d, gs, 2, F16, LSE>(p, occ, s);                 \
     }                                                                                   \
-    return ps_run<BITS, d, gs, 1, F16>(p, occ, s);                                      \
+    return ps_run<BITS, d, gs, 1, F16, LSE>(p, occ, s);                                 \
   }
   QDA_PS(64, 32) QDA_PS(64, 64)
   QDA_PS(128, 32) QDA_PS(128, 64) QDA_PS(128, 128)
