@@ -11,9 +11,9 @@ namespace qda {
 
 constexpr int kPlThreads = 512;
 
-// A CTA lays out a chunk of counted query rows of a sequence under a KV head in the swizzled form that the products read, and
-// its scalars: the rows in fp16 times a power of two that brings the largest value of all of them to [2^14, 2^15), or of each
-// of them where they differ too much; rows behind the sequence's last are zeros that weigh nothing.
+// A CTA lays out a part of a chunk of counted query rows of a sequence under a KV head in the swizzled form that the products
+// read, and its scalars: the rows in fp16 times a power of two that brings the largest value of all of them to [2^14, 2^15),
+// or of each of them where they differ too much; rows behind the sequence's last are zeros that weigh nothing.
 template <int D>
 __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const __grid_constant__ QdaWeightsParams p) {
   using G = PvGeom<D>;
@@ -47,8 +47,10 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
   const int kvh = blockIdx.y;
   __shared__ int s_top[2];   // largest and smallest exponent of a row's largest value
   constexpr int LPR = D / 8 < 32 ? D / 8 : 32, RPW = 32 / LPR;   // a row takes D / 8 lanes of 8 values
-  constexpr int N = kPvRows / (kPlThreads / 32 * RPW);           // rows of a thread
-  for (int ci = blockIdx.x; ci < carry; ci += gridDim.x) {
+  constexpr int RPC = kPlThreads / 32 * RPW;                     // rows of the CTA at a time
+  constexpr int N = kPvCols / RPC < 1 ? 1 : kPvCols / RPC;       // rows of a thread
+  for (long long x = blockIdx.x; x < (long long)carry * kPvParts; x += gridDim.x) {
+    const int ci = (int)(x / kPvParts), part = (int)(x % kPvParts);
     const int b = qda_seq_of(s_chunk, p.B, ci);
     const PwSeq s = pw_seq(p, b);
     const int row0 = (s.len - s.count) * p.nrep + (ci - s_chunk[b]) * kPvRows, row_end = s.len * p.nrep;
@@ -64,10 +66,10 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
     float top[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int row = row0 + (j * (kPlThreads / 32) + warp) * RPW + lane / LPR, tok = row / p.nrep;
+      const int in = j * RPC + warp * RPW + lane / LPR, row = row0 + part * kPvCols + in, tok = row / p.nrep;
       const int h = kvh * p.nrep + row - tok * p.nrep;
       a[j] = make_uint4(0, 0, 0, 0);
-      if (row < row_end)
+      if (in < kPvCols && row < row_end)
         a[j] = __ldg(reinterpret_cast<const uint4*>(p.q + (long long)(s.first + tok) * p.q_tstride + (long long)h * p.q_hstride) + piece);
     }
 #pragma unroll
@@ -93,7 +95,8 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
     const int shared_up = near ? pv_up(__uint_as_float((uint32_t)max(s_top[0], 0) << 23)) : 0;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const int i = (j * (kPlThreads / 32) + warp) * RPW + lane / LPR, row = row0 + i, tok = row / p.nrep;
+      const int i = part * kPvCols + j * RPC + warp * RPW + lane / LPR, row = row0 + i, tok = row / p.nrep;
+      if (i >= (part + 1) * kPvCols) continue;
       const int h = kvh * p.nrep + row - tok * p.nrep;
       const bool real = row < row_end;
       const int e = near ? shared_up : pv_up(top[j]);
@@ -106,16 +109,17 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
         w[k] = pc_h2(f.x * up, f.y * up);
       }
       // slices of SD dimensions; in them blocks of 64, rows of 128 bytes, 16-byte pieces swizzled
-      const int sl = piece / (G::SD / 8), in = piece % (G::SD / 8);
-      *reinterpret_cast<uint4*>(dst + sl * G::SLICE + (in >> 3) * 16384 + i * 128 + (((in & 7) ^ (i & 7)) << 4)) =
+      const int sl = piece / (G::SD / 8), at = piece % (G::SD / 8);
+      *reinterpret_cast<uint4*>(dst + sl * G::SLICE + (at >> 3) * 16384 + i * 128 + (((at & 7) ^ (i & 7)) << 4)) =
           make_uint4(w[0], w[1], w[2], w[3]);
       if (piece == 0) {
         scal->lse[i] = real ? p.lse[(long long)(s.first + tok) * p.H + h] * -1.4426950408889634f : -INFINITY;
         scal->muls[i] = p.qscale * pv_pow2(-e);
         scal->last[i] = real ? s.base + tok : -1;
-        if (i == 0) scal->mul = near ? p.qscale * pv_pow2(-e) : 0.f;
+        if (i == part * kPvCols) scal->mul[part] = near ? p.qscale * pv_pow2(-e) : 0.f;
       }
     }
+    __syncthreads();   // s_top is read
   }
 }
 
@@ -148,7 +152,7 @@ static WeightsPlan weights_plan(int B, int nrep, int Hkv, int total_q, int max_q
 }  // namespace qda
 
 cudaError_t qda_paged_weights_lay(const QdaWeightsParams& p, cudaStream_t s) {
-  const dim3 grid((unsigned)std::min(p.max_chunks, 1 << 20), (unsigned)p.Hkv);
+  const dim3 grid((unsigned)std::min((long long)p.max_chunks * qda::kPvParts, 1LL << 20), (unsigned)p.Hkv);
   switch (p.D) {
     case 64: qda::qda_paged_weights_lay_kernel<64><<<grid, qda::kPlThreads, 0, s>>>(p); break;
     case 128: qda::qda_paged_weights_lay_kernel<128><<<grid, qda::kPlThreads, 0, s>>>(p); break;

@@ -12,7 +12,8 @@
 //                        without a share of the shared memory's bandwidth; two blocks of them at D <= 128), and what undoes
 //                        the key's scale;
 //   row loader           one lane: a chunk's operands and scalars, laid out by the kernel ahead, by bulk copies into a ring;
-//   MMA warp             one lane issues every product; two accumulators of 128 columns take turns;
+//   MMA warps            two, a lane of each issues the products of every other chunk into an accumulator of its own (one
+//                        lane alone took 106 cycles a product, whose arithmetic takes 64);
 //   exponential warps    sixteen: four threads per key, a quarter of a chunk's columns each.
 // Every link is an mbarrier; every wait is bounded and sets the device error word, and after one that gave up every role ends.
 #pragma once
@@ -26,22 +27,21 @@ constexpr int kPvKeys = 128;
 // Work of a block beside its query rows, in query rows. Ragged chunks at D 256 take 260 us with 64, 237 with 128, 221 with 200,
 // 223 with 300, 225 with 450.
 constexpr int kPvCost = 240;
-constexpr int kPvExp = 16, kPvDeq = 8, kPvWarps = kPvExp + kPvDeq + 3;
+constexpr int kPvExp = 16, kPvDeq = 8, kPvWarps = kPvExp + kPvDeq + 4;
 constexpr int kPvParts = kPvExp / 4, kPvCols = kPvRows / kPvParts;   // threads of a key, columns of each
 constexpr int kPvScalars = 3;  // chunks' scalars in flight
+constexpr int kPvSlices = 10;  // operand slices in flight, at most
 
-// A chunk's scalars. Rows of a chunk share a power of two where the largest values of all of them lie within 2^kPvNear (they
-// then lose no more than that of the 39 bits' room below): what undoes it and the softmax scale is `mul`; else mul is 0 and
-// every row has its own.
+// A chunk's scalars. The rows of a part (those of one exponential thread) share a power of two where the largest values of all
+// of them lie within 2^kPvNear (they then lose no more than that of the 39 bits' room below): what undoes it and the softmax
+// scale is the part's `mul`; else that is 0 and every row has its own.
 constexpr int kPvNear = 12;
 struct PvScalars {
   float lse[kPvRows];          // minus a row's lse in log2 units; -inf: no row
   float muls[kPvRows];         // what undoes a row's scale, times the softmax scale
   int last[kPvRows];           // last key that the row sees; -1: no row
-  float mul, pad[3];
+  float mul[kPvParts];
 };
-
-constexpr int kPvRaw = 3;      // blocks' codes in flight
 
 template <int D>
 struct PvGeom {
@@ -50,7 +50,6 @@ struct PvGeom {
   static constexpr int CHUNK = SLICES * SLICE + (int)sizeof(PvScalars);   // bytes in memory
   static constexpr int AS = D <= 128 ? 2 : 1;            // blocks in tensor memory, D columns each (two values a column, two operands)
   static constexpr int A_COL = 256;                      // they stand behind two accumulators
-  static constexpr int BS = D == 256 ? 5 : 6;            // operand slices in flight
 };
 
 template <int BITS, int D>
@@ -58,6 +57,12 @@ struct PvKeys {
   static constexpr int RB = D * BITS / 8;                // a row of codes
   static constexpr int SC = kPvKeys * (D / 32) * 2;      // room for the scales of the smallest groups
   static constexpr int RAW = kPvKeys * RB + 2 * SC;
+  static constexpr int RS = RAW > 24 * 1024 ? 2 : 3;     // blocks' codes in flight
+  static constexpr int BS0 = (210 * 1024 - RS * RAW) / PvGeom<D>::SLICE;
+  static constexpr int BS = BS0 > kPvSlices ? kPvSlices : BS0;   // operand slices in flight
+  // (A wait tells neighbouring phases of a slot apart only. Before a chunk's slices are waited for, the exponentials of the
+  // chunk two before are done, and with them all its slices: the phase before is over.)
+  static_assert(BS >= 2 * PvGeom<D>::SLICES, "slots of two chunks");
 };
 
 // Chunks of a sequence under a KV head.
@@ -125,7 +130,7 @@ struct PvShared {
   long long row[8][8];         // pool rows of a block's sixteens of keys (-1: none), eight blocks
   long long tot[kPvWarps];
   int ctot[kPvWarps];
-  uint64_t r_full[kPvRaw], r_empty[kPvRaw], a_full[2], a_empty[2], b_full[8], b_empty[8], c_full[kPvScalars], c_empty[kPvScalars],
+  uint64_t r_full[3], r_empty[3], a_full[2], a_empty[2], b_full[kPvSlices], b_empty[kPvSlices], c_full[kPvScalars], c_empty[kPvScalars],
       d_full[2], d_empty[2], p_full[2], p_empty[2], drain;
   uint32_t tmem;
   int abort;
@@ -134,7 +139,7 @@ struct PvShared {
 template <int BITS, int D>
 constexpr int pv_smem() {
   using G = PvGeom<D>;
-  return 1024 + G::BS * G::SLICE + kPvRaw * PvKeys<BITS, D>::RAW + (int)sizeof(PvShared);
+  return 1024 + PvKeys<BITS, D>::BS * G::SLICE + PvKeys<BITS, D>::RS * PvKeys<BITS, D>::RAW + (int)sizeof(PvShared);
 }
 
 // 2^e, and e that brings x to [2^14, 2^15) (0 for what is no positive number, or infinite).
@@ -151,25 +156,25 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
   extern __shared__ __align__(1024) unsigned char pv_smem_raw[];
   unsigned char* base = pv_smem_raw + ((1024u - (smem_addr(pv_smem_raw) & 1023u)) & 1023u);
   unsigned char* b_s = base;
-  unsigned char* raw_s = base + G::BS * G::SLICE;
-  PvShared& sh = *reinterpret_cast<PvShared*>(raw_s + kPvRaw * K::RAW);
+  unsigned char* raw_s = base + K::BS * G::SLICE;
+  PvShared& sh = *reinterpret_cast<PvShared*>(raw_s + K::RS * K::RAW);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int W_MMA = kPvExp + kPvDeq, W_KEYS = W_MMA + 1;   // behind the exponential and the dequantising warps
+  constexpr int W_MMA = kPvExp + kPvDeq, W_KEYS = W_MMA + 2;   // behind the exponential and the dequantising warps
   volatile int* abort = &sh.abort;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.a_full[i], kPvDeq);
-      mbar_init(&sh.a_empty[i], 1 + kPvExp);
+      mbar_init(&sh.a_empty[i], 2 + kPvExp);
       mbar_init(&sh.d_full[i], 1);
       mbar_init(&sh.d_empty[i], kPvExp);
       mbar_init(&sh.p_full[i], kPvExp - 4);
       mbar_init(&sh.p_empty[i], 4);
     }
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kPvSlices; ++i) {
       mbar_init(&sh.b_full[i], 1);
       mbar_init(&sh.b_empty[i], 1);
     }
-    for (int i = 0; i < kPvRaw; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(&sh.r_full[i], 8);
       mbar_init(&sh.r_empty[i], kPvDeq);
     }
@@ -177,7 +182,7 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       mbar_init(&sh.c_full[i], 1);
       mbar_init(&sh.c_empty[i], kPvExp);
     }
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain, 2);
     sh.abort = 0;
     sh.at[0] = 0;
     sh.chunk[0] = 0;
@@ -278,8 +283,8 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
-        float one = km * f.mul;
-        if (f.mul == 0.f) {   // rare: rows with scales of their own
+        float one = km * f.mul[part];
+        if (f.mul[part] == 0.f) {   // rare: rows with scales of their own
 #pragma unroll
           for (int i = 0; i < kPvCols; ++i) v[i] *= km * f.muls[kPvCols * part + i];
           one = 1.f;
@@ -326,8 +331,8 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
     constexpr float QMAX = (float)((1 << BITS) - 1);
     const uint32_t a_t = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::A_COL;
     for (; w.here(p, to); w.step(p), ++bc) {
-      const int st = bc % kPvRaw;
-      if (!wait_all(&sh.r_full[st], bc / kPvRaw)) break;
+      const int st = bc % K::RS;
+      if (!wait_all(&sh.r_full[st], bc / K::RS)) break;
       const unsigned char* raw = raw_s + st * K::RAW;
       const bool there = sh.row[bc & 7][r >> 4] >= 0;
       // all of the key's scales and biases (pairs of 16 bits)
@@ -415,8 +420,8 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
         mbar_arrive(&sh.r_empty[st]);
       }
     }
-  } else if (warp == W_MMA) {
-    // ============================================================================ one lane issues the products
+  } else if (warp < W_KEYS) {
+    // ============================================================================ a lane issues the products of its chunks
     constexpr uint32_t ID = (1u << 4) | ((uint32_t)(kPvRows >> 3) << 17) | (8u << 24);   // M 128, N 128, fp16, fp32 sums
     const uint32_t one = pc_elect();
     const uint32_t b_a = smem_addr(b_s);
@@ -426,12 +431,16 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       ok = wait_all(&sh.a_full[bc % G::AS], bc / G::AS);
       for (int c = w.first_chunk(p); ok && c < chunks; ++c, ++cc) {
         const int buf = cc & 1;
+        if (buf != warp - W_MMA) {   // the other warp's
+          sc += G::SLICES;
+          continue;
+        }
         ok = wait_all(&sh.d_empty[buf], (cc >> 1) + 1);
         for (int sl = 0; ok && sl < G::SLICES; ++sl, ++sc) {
-          ok = wait_all(&sh.b_full[sc % G::BS], sc / G::BS);
+          ok = wait_all(&sh.b_full[sc % K::BS], sc / K::BS);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t b = pc_desc(b_a + (sc % G::BS) * G::SLICE, 16);
+          const uint64_t b = pc_desc(b_a + (sc % K::BS) * G::SLICE, 16);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const uint32_t a = tmem + G::A_COL + (bc % G::AS) * D + y * (D / 2) + sl * (SD / 2);
@@ -439,7 +448,7 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
             for (int x = 0; x < SD / 16; ++x)
               pc_mma_ts(one, tmem + 128 * buf, a + 8 * x, b + (x * 32 >> 4), ID, sl > 0 || y > 0 || x > 0);
           }
-          pc_commit(one, &sh.b_empty[sc % G::BS]);
+          pc_commit(one, &sh.b_empty[sc % K::BS]);
         }
         if (ok) pc_commit(one, &sh.d_full[buf]);
       }
@@ -451,12 +460,12 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
     const uint64_t policy = policy_evict_first();
     bool ok = true;
     for (; ok && lane < 8 && w.here(p, to); w.step(p), ++bc) {
-      const int st = bc % kPvRaw, key = w.x * kPvKeys + 16 * lane;
+      const int st = bc % K::RS, key = w.x * kPvKeys + 16 * lane;
       const int pg = key < w.s.n ? __ldg(p.table + (size_t)w.b * p.max_pages + (key >> p.page_shift)) : -1;
       const bool there = (unsigned)pg < (unsigned)p.num_pages;
       const long long row = there ? qda_pool_row(pg, w.kvh, key & ((1 << p.page_shift) - 1), p.Hkv, p.page_shift) : -1;
       if (!there && key < w.s.n) atomicOr(p.err, QDA_ERR_BIT_PAGED);
-      ok = wait(&sh.r_empty[st], bc / kPvRaw + 1);
+      ok = wait(&sh.r_empty[st], bc / K::RS + 1);
       if (!ok) break;
       sh.row[bc & 7][lane] = row;   // (the exponential warps are at most six blocks behind)
       unsigned char* dst = raw_s + st * K::RAW;
@@ -473,9 +482,9 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
     if (lane < 8 && (!ok || *abort)) {
       // a wait gave up: copies under way land before the CTA's shared memory goes (one lane may wait for what another never
       // began, until the limit)
-      for (uint32_t i = bc < (uint32_t)kPvRaw ? 0 : bc - kPvRaw; i < bc; ++i) {
+      for (uint32_t i = bc < (uint32_t)K::RS ? 0 : bc - K::RS; i < bc; ++i) {
         volatile int none = 0;
-        mbar_wait_bounded(&sh.r_full[i % kPvRaw], (i / kPvRaw) & 1u, &none, p.err, 2u);
+        mbar_wait_bounded(&sh.r_full[i % K::RS], (i / K::RS) & 1u, &none, p.err, 2u);
       }
     }
   } else if (lane == 0) {
@@ -498,13 +507,13 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
         mbar_arrive_expect_tx(&sh.c_full[ps], sizeof(PvScalars));
         bulk_g2s(&sh.scal[ps], src + G::SLICES * G::SLICE, sizeof(PvScalars), &sh.c_full[ps], policy);
         for (int sl = 0; sl < G::SLICES; ++sl, ++sc) {
-          ok = wait(&sh.b_empty[sc % G::BS], sc / G::BS + 1);
+          ok = wait(&sh.b_empty[sc % K::BS], sc / K::BS + 1);
           if (!ok) break;
 #ifdef QDA_BOUNDS_CHECK
           if (blockIdx.x == 0 && (p.stall == (int)sc)) continue;   // testing aid: the waits for this slice must run out
 #endif
-          mbar_arrive_expect_tx(&sh.b_full[sc % G::BS], G::SLICE);
-          bulk_g2s(b_s + (sc % G::BS) * G::SLICE, src + sl * G::SLICE, G::SLICE, &sh.b_full[sc % G::BS], policy);
+          mbar_arrive_expect_tx(&sh.b_full[sc % K::BS], G::SLICE);
+          bulk_g2s(b_s + (sc % K::BS) * G::SLICE, src + sl * G::SLICE, G::SLICE, &sh.b_full[sc % K::BS], policy);
         }
       }
     }
@@ -512,8 +521,8 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       // a wait gave up: copies under way land before the CTA's shared memory goes (a phase that a copy never began is waited
       // for in vain, until the limit)
       volatile int none = 0;
-      for (uint32_t i = sc < (uint32_t)G::BS ? 0 : sc - G::BS; i < sc; ++i)
-        none = 0, mbar_wait_bounded(&sh.b_full[i % G::BS], (i / G::BS) & 1u, &none, p.err, 2u);
+      for (uint32_t i = sc < (uint32_t)K::BS ? 0 : sc - K::BS; i < sc; ++i)
+        none = 0, mbar_wait_bounded(&sh.b_full[i % K::BS], (i / K::BS) & 1u, &none, p.err, 2u);
       for (uint32_t i = cc < (uint32_t)kPvScalars ? 0 : cc - kPvScalars; i < cc; ++i)
         none = 0, mbar_wait_bounded(&sh.c_full[i % kPvScalars], (i / kPvScalars) & 1u, &none, p.err, 2u);
     }
@@ -522,11 +531,14 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // no product is under way when the tensor memory goes back: an elected lane's commit speaks for its own products
+  if (warp == W_MMA || warp == W_MMA + 1) {
+    if (pc_elect()) mma_commit(&sh.drain);
+    __syncwarp();
+  }
   if (warp == W_MMA) {
-    // no product is under way when the tensor memory goes back: the elected lane's commit speaks for its own products
-    if (pc_elect()) {
+    if (lane == 0) {
       volatile int none = 0;
-      mma_commit(&sh.drain);
       mbar_wait_bounded(&sh.drain, 0, &none, p.err, 2u);
     }
     __syncwarp();
