@@ -14,7 +14,8 @@
 //   row loader           one lane: a chunk's operands and scalars, laid out by the kernel ahead, by bulk copies into a ring;
 //   MMA warps            two, a lane of each issues the products of every other chunk into an accumulator of its own (one
 //                        lane alone took 106 cycles a product, whose arithmetic takes 64);
-//   exponential warps    sixteen: four threads per key, a quarter of a chunk's columns each.
+//   exponential warps    eight: two threads per key, half of a chunk's columns each (sixteen of 72 registers: ragged chunks
+//                        216 us instead of 206).
 // Every link is an mbarrier; every wait is bounded and sets the device error word, and after one that gave up every role ends.
 #pragma once
 
@@ -27,7 +28,7 @@ constexpr int kPvKeys = 128;
 // Work of a block beside its query rows, in query rows. Ragged chunks at D 256 take 260 us with 64, 237 with 128, 221 with 200,
 // 223 with 300, 225 with 450.
 constexpr int kPvCost = 240;
-constexpr int kPvExp = 16, kPvDeq = 8, kPvWarps = kPvExp + kPvDeq + 4;
+constexpr int kPvExp = 8, kPvDeq = 8, kPvWarps = kPvExp + kPvDeq + 4;
 constexpr int kPvParts = kPvExp / 4, kPvCols = kPvRows / kPvParts;   // threads of a key, columns of each
 constexpr int kPvScalars = 3;  // chunks' scalars in flight
 constexpr int kPvSlices = 10;  // operand slices in flight, at most
@@ -36,12 +37,13 @@ constexpr int kPvSlices = 10;  // operand slices in flight, at most
 // of them lie within 2^kPvNear (they then lose no more than that of the 39 bits' room below): what undoes it and the softmax
 // scale is the part's `mul`; else that is 0 and every row has its own.
 constexpr int kPvNear = 12;
-struct PvScalars {
+struct alignas(16) PvScalars {
   float lse[kPvRows];          // minus a row's lse in log2 units; -inf: no row
   float muls[kPvRows];         // what undoes a row's scale, times the softmax scale
   int last[kPvRows];           // last key that the row sees; -1: no row
   float mul[kPvParts];
 };
+static_assert(sizeof(PvScalars) % 16 == 0, "a bulk copy's size");
 
 template <int D>
 struct PvGeom {
@@ -118,7 +120,7 @@ struct PvWalk {
     return (int)(((long long)before * p.nrep) >> 7);
   }
 };
-static_assert(kPvRows == 128 && kPvCols == 32, "first_chunk; columns of a load");
+static_assert(kPvRows == 128 && kPvCols % 32 == 0, "first_chunk; columns of a load");
 
 struct PvShared {
   PvScalars scal[kPvScalars];
@@ -277,29 +279,35 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
         const PvScalars& f = sh.scal[ps];
         // all of the chunk's rows see all of the block's keys: the last key against the first row's token
         const bool open = (long long)(w.x * kPvKeys + kPvKeys - 1 - w.s.base - first_tok) * p.nrep <= (long long)c * kPvRows;
-        float v[kPvCols];
-        pc_ld32(d_t + 128 * buf, v);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
-        float one = km * f.mul[part];
-        if (f.mul[part] == 0.f) {   // rare: rows with scales of their own
+#pragma unroll 1
+        for (int q = 0; q < kPvCols / 32; ++q) {   // (a loop that stays small: the roles share the instruction cache)
+          const int col = kPvCols * part + 32 * q;
+          float v[32];
+          pc_ld32(d_t + 128 * buf + 32 * q, v);
+          tmem_wait_ld();
+          if (q == kPvCols / 32 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
+          }
+          float one = km * f.mul[part];
+          if (f.mul[part] == 0.f) {   // rare: rows with scales of their own
 #pragma unroll
-          for (int i = 0; i < kPvCols; ++i) v[i] *= km * f.muls[kPvCols * part + i];
-          one = 1.f;
-        }
-        if (!open) {
+            for (int i = 0; i < 32; ++i) v[i] *= km * f.muls[col + i];
+            one = 1.f;
+          }
+          if (!open) {
 #pragma unroll
-          for (int i = 0; i < kPvCols; ++i) v[i] = key > f.last[kPvCols * part + i] ? -INFINITY : v[i];
-        }
+            for (int i = 0; i < 32; ++i) v[i] = key > f.last[col + i] ? -INFINITY : v[i];
+          }
 #pragma unroll
-        for (int i = 0; i < kPvCols / 4; ++i) {
-          const float4 m = *reinterpret_cast<const float4*>(f.lse + kPvCols * part + 4 * i);
-          const float2 e0 = __ffma2_rn(make_float2(v[4 * i], v[4 * i + 1]), make_float2(one, one), make_float2(m.x, m.y));
-          const float2 e1 = __ffma2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(one, one), make_float2(m.z, m.w));
-          sum[0] = __fadd2_rn(sum[0], make_float2(pc_ex2(e0.x), pc_ex2(e0.y)));
-          sum[1] = __fadd2_rn(sum[1], make_float2(pc_ex2(e1.x), pc_ex2(e1.y)));
+          for (int i = 0; i < 8; ++i) {
+            const float4 m = *reinterpret_cast<const float4*>(f.lse + col + 4 * i);
+            const float2 e0 = __ffma2_rn(make_float2(v[4 * i], v[4 * i + 1]), make_float2(one, one), make_float2(m.x, m.y));
+            const float2 e1 = __ffma2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(one, one), make_float2(m.z, m.w));
+            sum[0] = __fadd2_rn(sum[0], make_float2(pc_ex2(e0.x), pc_ex2(e0.y)));
+            sum[1] = __fadd2_rn(sum[1], make_float2(pc_ex2(e1.x), pc_ex2(e1.y)));
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.c_empty[ps]);
