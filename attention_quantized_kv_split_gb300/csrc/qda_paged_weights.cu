@@ -228,7 +228,7 @@ extern "C" int qdecode_paged_weights(const void* q, long long q_tstride, long lo
   p.qscale = 1.4426950408889634f / sqrtf((float)D);
   p.decay = (float)decay;
   p.D = D;
-  p.GS = GS;
+  p.gs_shift = GS == 32 ? 5 : GS == 64 ? 6 : 7;
   p.NG = D / GS;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const WeightsPlan plan = weights_plan(B, nrep, Hkv, total_q, max_q, window, D);

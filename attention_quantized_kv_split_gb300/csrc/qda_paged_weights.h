@@ -21,7 +21,7 @@ struct QdaWeightsParams {
   float qscale;               // log2(e) / sqrt(D)
   float decay;
   // the kernel for many rows
-  int D, GS, NG;
+  int D, NG, gs_shift;        // gs_shift: log2 of the group size
   char* chunks;               // [chunks of all sequences, Hkv] query rows as operands (qda_paged_weights_tc.cuh)
   int max_chunks;             // chunks that there is room for
   int stall;                  // testing aid of the checked build: the first CTA does not get this operand slice (-1: gets all)

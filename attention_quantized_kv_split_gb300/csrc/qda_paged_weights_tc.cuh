@@ -77,16 +77,22 @@ __device__ __forceinline__ long long pv_prefix(const QdaWeightsParams& p, const 
   return pw_prefix<kPvKeys>(p, s, i, kPvCost + (long long)pv_chunks(p, s) * kPvRows, kPvCost + kPvRows);
 }
 
-// Where a CTA stands on its piece of the line: at a block of keys. Every role walks for itself.
+// Where a CTA stands on its piece of the line: at a block of keys. Every role walks for itself, with what a sequence has in
+// hand: at some twenty warps a block, what a step costs is what the block costs.
 struct PvWalk {
-  int b, kvh, x, blocks;
+  int b, kvh, x, blocks, flat, chunks;   // flat: blocks that all of the sequence's chunks see
   long long pos;               // the block's place
   PwSeq s;
 
-  __device__ __forceinline__ void start(const QdaWeightsParams& p, const long long* line, long long from) {
-    b = qda_seq_of(line, p.B, from);
+  __device__ __forceinline__ void enter(const QdaWeightsParams& p) {
     s = pw_seq(p, b);
     blocks = pw_blocks<kPvKeys>(s);
+    flat = pw_flat<kPvKeys>(s);
+    chunks = pv_chunks(p, s);
+  }
+  __device__ __forceinline__ void start(const QdaWeightsParams& p, const long long* line, long long from) {
+    b = qda_seq_of(line, p.B, from);
+    enter(p);
     const long long head = pv_prefix(p, s, blocks);
     kvh = (int)((from - line[b]) / head);
     const long long at = line[b] + kvh * head;
@@ -102,24 +108,56 @@ struct PvWalk {
         kvh = 0;
         do {
           if (++b >= p.B) return false;
-          s = pw_seq(p, b);
-          blocks = pw_blocks<kPvKeys>(s);
+          enter(p);
         } while (blocks == 0);
       }
     }
     return true;
   }
-  __device__ __forceinline__ void step(const QdaWeightsParams& p) {
-    pos += kPvCost + (x < pw_flat<kPvKeys>(s) ? (long long)pv_chunks(p, s) * kPvRows   // as pv_prefix has it
-                                              : kPvRows + (long long)p.nrep * (s.n - x * kPvKeys));
+  __device__ __forceinline__ void step(const QdaWeightsParams& p) {   // (as pv_prefix has it)
+    if (x < flat) pos += kPvCost + (long long)chunks * kPvRows;
+    else pos += kPvCost + kPvRows + (long long)p.nrep * (s.n - x * kPvKeys);
     ++x;
   }
   // The chunks whose rows see the block's first key: from this one to the sequence's last.
   __device__ __forceinline__ int first_chunk(const QdaWeightsParams& p) const {
+    if (x < flat) return 0;
     const int before = max(0, x * kPvKeys - s.base - (s.len - s.count));   // counted tokens that do not
     return (int)(((long long)before * p.nrep) >> 7);
   }
 };
+
+// A slot of a ring of N and the parity of its phase, counted on.
+template <int N>
+struct PvSlot {
+  uint32_t at = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// As mbar_wait_bounded, for many warps that wait much: the barrier's own try suspends the warp for a while, and clock and abort
+// flag are looked at every 64th time only (with both at every time, waiting took half of the instructions that the kernel
+// issued).
+__device__ __forceinline__ bool pv_wait(uint64_t* bar, uint32_t parity, volatile int* abort, unsigned int* err) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 1; !mbar_try_wait(bar, parity); ++n) {
+    if (n & 63u) continue;
+    if (*abort) return false;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > 1000000000ull) {
+      atomicOr(err, 1u);
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
+}
+
 static_assert(kPvRows == 128 && kPvCols % 32 == 0, "first_chunk; columns of a load");
 
 struct PvShared {
@@ -246,39 +284,43 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  auto wait = [&](uint64_t* bar, uint32_t phase) { return mbar_wait_bounded(bar, phase & 1u, abort, p.err, 1u); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return pv_wait(bar, parity, abort, p.err); };
   // a warp's wait, for which it ends as one
-  auto wait_all = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   PvWalk w = sh.walk;
-  // blocks, chunks and slices so far: every role counts them for itself
-  uint32_t bc = 0, cc = 0, sc = 0;
+  // where every role stands in the rings: operands and codes of blocks, chunks, their scalars, slices
+  PvSlot<G::AS> as;
+  PvSlot<K::RS> rs;
+  PvSlot<2> ds, ps2;
+  PvSlot<kPvScalars> cs;
+  PvSlot<K::BS> bs;
+  uint32_t bc = 0;             // blocks so far
   if (warp < kPvExp) {
     // ============================================================================ exponentials: some threads per key
     const int part = warp >> 2, r = 32 * (warp & 3) + lane;
     const uint32_t d_t = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kPvCols * part;
-    for (; w.here(p, to); w.step(p), ++bc) {
+    for (; w.here(p, to); w.step(p), ++bc, as.next(), ps2.next()) {
       const int key = w.x * kPvKeys + r;
-      const int first_tok = w.s.len - w.s.count;
-      const int chunks = sh.chunk[w.b + 1] - sh.chunk[w.b];
-      if (!wait_all(&sh.a_full[bc % G::AS], bc / G::AS)) break;
-      const float km = sh.kmul[bc % G::AS][r];
+      if (!wait_all(&sh.a_full[as.at], as.phase)) break;
+      const float km = sh.kmul[as.at][r];
       const long long row0 = sh.row[bc & 7][r >> 4], row = row0 + (r & 15);
       const bool there = row0 >= 0 && key < w.s.n, keep = there && key < w.s.base;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.a_empty[bc % G::AS]);
+      if (lane == 0) mbar_arrive(&sh.a_empty[as.at]);
       float old = 0.f;
       if (part == 0 && keep) old = p.mass[row];
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool ok = true;
 #pragma unroll 1
-      for (int c = w.first_chunk(p); c < chunks; ++c, ++cc) {
-        const int buf = cc & 1, ps = cc % kPvScalars;
-        ok = wait_all(&sh.c_full[ps], cc / kPvScalars) && wait_all(&sh.d_full[buf], cc >> 1);
+      for (int c = w.first_chunk(p); c < w.chunks; ++c, ds.next(), cs.next()) {
+        const int buf = ds.at, ps = cs.at;
+        ok = wait_all(&sh.c_full[ps], cs.phase) && wait_all(&sh.d_full[buf], ds.phase);
         if (!ok) break;
         tc_fence_after();
         const PvScalars& f = sh.scal[ps];
         // all of the chunk's rows see all of the block's keys: the last key against the first row's token
-        const bool open = (long long)(w.x * kPvKeys + kPvKeys - 1 - w.s.base - first_tok) * p.nrep <= (long long)c * kPvRows;
+        const bool open = w.x + 1 < w.flat ||
+                          (long long)(w.x * kPvKeys + kPvKeys - 1 - w.s.base - (w.s.len - w.s.count)) * p.nrep <= (long long)c * kPvRows;
 #pragma unroll 1
         for (int q = 0; q < kPvCols / 32; ++q) {   // (a loop that stays small: the roles share the instruction cache)
           const int col = kPvCols * part + 32 * q;
@@ -315,17 +357,17 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       if (!ok) break;
       float add = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       if (part > 0) {   // the key's first thread takes it from here
-        if (!wait_all(&sh.p_empty[bc & 1], (bc >> 1) + 1)) break;
-        sh.part[bc & 1][part - 1][r] = add;
+        if (!wait_all(&sh.p_empty[ps2.at], ps2.phase ^ 1u)) break;
+        sh.part[ps2.at][part - 1][r] = add;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_full[bc & 1]);
+        if (lane == 0) mbar_arrive(&sh.p_full[ps2.at]);
         continue;
       }
-      if (!wait_all(&sh.p_full[bc & 1], bc >> 1)) break;
+      if (!wait_all(&sh.p_full[ps2.at], ps2.phase)) break;
 #pragma unroll
-      for (int i = 0; i < kPvParts - 1; ++i) add += sh.part[bc & 1][i][r];
+      for (int i = 0; i < kPvParts - 1; ++i) add += sh.part[ps2.at][i][r];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_empty[bc & 1]);
+      if (lane == 0) mbar_arrive(&sh.p_empty[ps2.at]);
       if (keep) {
         p.mass[row] = fmaf(p.decay, old, add);
       } else if (there) {
@@ -338,9 +380,9 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
     const int r = (tid - kPvExp * 32) & 127, half = (tid - kPvExp * 32) >> 7;
     constexpr float QMAX = (float)((1 << BITS) - 1);
     const uint32_t a_t = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + G::A_COL;
-    for (; w.here(p, to); w.step(p), ++bc) {
-      const int st = bc % K::RS;
-      if (!wait_all(&sh.r_full[st], bc / K::RS)) break;
+    for (; w.here(p, to); w.step(p), ++bc, as.next(), rs.next()) {
+      const int st = rs.at;
+      if (!wait_all(&sh.r_full[st], rs.phase)) break;
       const unsigned char* raw = raw_s + st * K::RAW;
       const bool there = sh.row[bc & 7][r >> 4] >= 0;
       // all of the key's scales and biases (pairs of 16 bits)
@@ -372,13 +414,13 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       }
       const int e = pv_up(top);
       const float up = pv_pow2(e);
-      if (!wait_all(&sh.a_empty[bc % G::AS], bc / G::AS + 1)) break;
+      if (!wait_all(&sh.a_empty[as.at], as.phase ^ 1u)) break;
       tc_fence_after();
-      const uint32_t hi_t = a_t + (bc % G::AS) * D, lo_t = hi_t + D / 2;
-      if (half == 0) sh.kmul[bc % G::AS][r] = pv_pow2(-e);
+      const uint32_t hi_t = a_t + as.at * D, lo_t = hi_t + D / 2;
+      if (half == 0) sh.kmul[as.at][r] = pv_pow2(-e);
 #pragma unroll 1
       for (int i = 0; i < D / 64; ++i) {   // 32 values: 16 columns of either operand
-        const int u = half * (D / 64) + i, g = u * 32 / p.GS;
+        const int u = half * (D / 64) + i, g = (u * 32) >> p.gs_shift;
         uint32_t code[BITS];
 #pragma unroll
         for (int k = 0; k < BITS / 4; ++k) {
@@ -424,7 +466,7 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&sh.a_full[bc % G::AS]);
+        mbar_arrive(&sh.a_full[as.at]);
         mbar_arrive(&sh.r_empty[st]);
       }
     }
@@ -434,46 +476,46 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
     const uint32_t one = pc_elect();
     const uint32_t b_a = smem_addr(b_s);
     bool ok = true;
-    for (; ok && w.here(p, to); w.step(p), ++bc) {
-      const int chunks = sh.chunk[w.b + 1] - sh.chunk[w.b];
-      ok = wait_all(&sh.a_full[bc % G::AS], bc / G::AS);
-      for (int c = w.first_chunk(p); ok && c < chunks; ++c, ++cc) {
-        const int buf = cc & 1;
+    for (; ok && w.here(p, to); w.step(p), as.next()) {
+      ok = wait_all(&sh.a_full[as.at], as.phase);
+      for (int c = w.first_chunk(p); ok && c < w.chunks; ++c, ds.next()) {
+        const int buf = ds.at;
         if (buf != warp - W_MMA) {   // the other warp's
-          sc += G::SLICES;
+#pragma unroll
+          for (int sl = 0; sl < G::SLICES; ++sl) bs.next();
           continue;
         }
-        ok = wait_all(&sh.d_empty[buf], (cc >> 1) + 1);
-        for (int sl = 0; ok && sl < G::SLICES; ++sl, ++sc) {
-          ok = wait_all(&sh.b_full[sc % K::BS], sc / K::BS);
+        ok = wait_all(&sh.d_empty[buf], ds.phase ^ 1u);
+        for (int sl = 0; ok && sl < G::SLICES; ++sl, bs.next()) {
+          ok = wait_all(&sh.b_full[bs.at], bs.phase);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t b = pc_desc(b_a + (sc % K::BS) * G::SLICE, 16);
+          const uint64_t b = pc_desc(b_a + bs.at * G::SLICE, 16);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const uint32_t a = tmem + G::A_COL + (bc % G::AS) * D + y * (D / 2) + sl * (SD / 2);
+            const uint32_t a = tmem + G::A_COL + as.at * D + y * (D / 2) + sl * (SD / 2);
 #pragma unroll
             for (int x = 0; x < SD / 16; ++x)
               pc_mma_ts(one, tmem + 128 * buf, a + 8 * x, b + (x * 32 >> 4), ID, sl > 0 || y > 0 || x > 0);
           }
-          pc_commit(one, &sh.b_empty[sc % K::BS]);
+          pc_commit(one, &sh.b_empty[bs.at]);
         }
         if (ok) pc_commit(one, &sh.d_full[buf]);
       }
-      if (ok) pc_commit(one, &sh.a_empty[bc % G::AS]);
+      if (ok) pc_commit(one, &sh.a_empty[as.at]);
       __syncwarp();
     }
   } else if (warp == W_KEYS) {
     // ============================================================================ codes, scales and biases: sixteen keys a lane
     const uint64_t policy = policy_evict_first();
     bool ok = true;
-    for (; ok && lane < 8 && w.here(p, to); w.step(p), ++bc) {
-      const int st = bc % K::RS, key = w.x * kPvKeys + 16 * lane;
+    for (; ok && lane < 8 && w.here(p, to); w.step(p), ++bc, rs.next()) {
+      const int st = rs.at, key = w.x * kPvKeys + 16 * lane;
       const int pg = key < w.s.n ? __ldg(p.table + (size_t)w.b * p.max_pages + (key >> p.page_shift)) : -1;
       const bool there = (unsigned)pg < (unsigned)p.num_pages;
       const long long row = there ? qda_pool_row(pg, w.kvh, key & ((1 << p.page_shift) - 1), p.Hkv, p.page_shift) : -1;
       if (!there && key < w.s.n) atomicOr(p.err, QDA_ERR_BIT_PAGED);
-      ok = wait(&sh.r_empty[st], bc / K::RS + 1);
+      ok = wait(&sh.r_empty[st], rs.phase ^ 1u);
       if (!ok) break;
       sh.row[bc & 7][lane] = row;   // (the exponential warps are at most six blocks behind)
       unsigned char* dst = raw_s + st * K::RAW;
@@ -505,23 +547,23 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       return x;
     }();
     bool ok = true;
+    uint32_t sc = 0, cc = 0;   // slices and chunks so far
     for (; ok && w.here(p, to); w.step(p)) {
-      const int c0 = sh.chunk[w.b], chunks = sh.chunk[w.b + 1] - c0;
-      for (int c = w.first_chunk(p); ok && c < chunks; ++c, ++cc) {
+      const int c0 = sh.chunk[w.b];
+      for (int c = w.first_chunk(p); ok && c < w.chunks; ++c, ++cc, cs.next()) {
         const char* src = p.chunks + ((size_t)(c0 + c) * p.Hkv + w.kvh) * G::CHUNK;
-        const int ps = cc % kPvScalars;
-        ok = wait(&sh.c_empty[ps], cc / kPvScalars + 1);
+        ok = wait(&sh.c_empty[cs.at], cs.phase ^ 1u);
         if (!ok) break;
-        mbar_arrive_expect_tx(&sh.c_full[ps], sizeof(PvScalars));
-        bulk_g2s(&sh.scal[ps], src + G::SLICES * G::SLICE, sizeof(PvScalars), &sh.c_full[ps], policy);
-        for (int sl = 0; sl < G::SLICES; ++sl, ++sc) {
-          ok = wait(&sh.b_empty[sc % K::BS], sc / K::BS + 1);
+        mbar_arrive_expect_tx(&sh.c_full[cs.at], sizeof(PvScalars));
+        bulk_g2s(&sh.scal[cs.at], src + G::SLICES * G::SLICE, sizeof(PvScalars), &sh.c_full[cs.at], policy);
+        for (int sl = 0; sl < G::SLICES; ++sl, ++sc, bs.next()) {
+          ok = wait(&sh.b_empty[bs.at], bs.phase ^ 1u);
           if (!ok) break;
 #ifdef QDA_BOUNDS_CHECK
           if (blockIdx.x == 0 && (p.stall == (int)sc)) continue;   // testing aid: the waits for this slice must run out
 #endif
-          mbar_arrive_expect_tx(&sh.b_full[sc % K::BS], G::SLICE);
-          bulk_g2s(b_s + (sc % K::BS) * G::SLICE, src + sl * G::SLICE, G::SLICE, &sh.b_full[sc % K::BS], policy);
+          mbar_arrive_expect_tx(&sh.b_full[bs.at], G::SLICE);
+          bulk_g2s(b_s + bs.at * G::SLICE, src + sl * G::SLICE, G::SLICE, &sh.b_full[bs.at], policy);
         }
       }
     }
