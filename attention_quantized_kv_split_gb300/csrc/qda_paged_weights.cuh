@@ -40,26 +40,6 @@ struct PwGeom {
   static constexpr int COST = kPwCost * KEYS / 64;
 };
 
-// Where 16-byte chunk ch of row r of a tile's codes lies: chunks of a row are permuted by the row's bits in reverse, so that
-// the eight rows that a warp reads at once fall into different banks for loads of 4, 8 and 16 bytes.
-template <int RB>
-__device__ __forceinline__ int pw_chunk(int r, int ch) {
-  constexpr int CPR = RB / 16, N = CPR < 8 ? CPR : 8;
-  const int x = r / (8 / N);
-  const int f = N == 8 ? ((x & 1) << 2) | (x & 2) | ((x >> 2) & 1) : N == 4 ? ((x & 1) << 1) | ((x >> 1) & 1) : x & 1;
-  return r * RB + ((ch ^ f) << 4);
-}
-
-__device__ __forceinline__ void pw_copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void pw_copy4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void pw_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void pw_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // BYTES (a power of two, up to 32) from shared memory into words.
 template <int BYTES, int N>
 __device__ __forceinline__ void pw_lds(const char* p, uint32_t (&v)[N]) {

@@ -7,7 +7,9 @@
 // Masses are fp32, so scores must be: a key is two fp16 operands, its value to 11 bits and what those leave (22 bits, or 2^-39
 // of the key's largest possible value), each key scaled by its own power of two, and a query row is exact in fp16 scaled by
 // its own (what is 2^-39 of the row's largest and less loses bits). Both products go to the same fp32 accumulator.
-//   key loader           eight lanes, sixteen keys each: a block's codes, scales and biases by bulk copies into a ring;
+//   key loader           a warp: a block's codes, scales and biases by asynchronous copies of 16 bytes into a ring, codes at
+//                        places that eight threads' rows do not share banks at (bulk copies of sixteen keys each, one after
+//                        the other, took 4200 cycles a block, more than all that follows with up to 128 rows);
 //   dequantising warps   eight: two threads per key, codes -> the two operands in tensor memory (where products read them
 //                        without a share of the shared memory's bandwidth; two blocks of them at D <= 128), and what undoes
 //                        the key's scale;
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       mbar_init(&sh.b_empty[i], 1);
     }
     for (int i = 0; i < 3; ++i) {
-      mbar_init(&sh.r_full[i], 8);
+      mbar_init(&sh.r_full[i], 33);   // the lanes' copies, and the rows' numbers
       mbar_init(&sh.r_empty[i], kPvDeq);
     }
     for (int i = 0; i < kPvScalars; ++i) {
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
         uint32_t code[BITS];
 #pragma unroll
         for (int k = 0; k < BITS / 4; ++k) {
-          const uint4 q = *reinterpret_cast<const uint4*>(raw + r * K::RB + u * BITS * 4 + 16 * k);
+          const uint4 q = *reinterpret_cast<const uint4*>(raw + pw_chunk<K::RB>(r, u * (BITS / 4) + k));
           code[4 * k] = q.x;
           code[4 * k + 1] = q.y;
           code[4 * k + 2] = q.z;
@@ -506,37 +508,42 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       __syncwarp();
     }
   } else if (warp == W_KEYS) {
-    // ============================================================================ codes, scales and biases: sixteen keys a lane
-    const uint64_t policy = policy_evict_first();
-    bool ok = true;
-    for (; ok && lane < 8 && w.here(p, to); w.step(p), ++bc, rs.next()) {
-      const int st = rs.at, key = w.x * kPvKeys + 16 * lane;
+    // ============================================================================ codes, scales and biases of the blocks
+    // four lanes have sixteen keys: a row's chunks of 64 bytes, row after row, then chunks of the scales and of the biases
+    const int g = lane >> 2, l4 = lane & 3, ng2 = 2 * p.NG;   // 16-byte chunks of sixteen keys' scales
+    const char* const codes = reinterpret_cast<const char*>(p.kp) + 16 * l4;
+    constexpr int CPR = K::RB / 16;                           // 16-byte chunks of a row of codes
+    for (; w.here(p, to); w.step(p), ++bc, rs.next()) {
+      const int key = w.x * kPvKeys + 16 * g;
       const int pg = key < w.s.n ? __ldg(p.table + (size_t)w.b * p.max_pages + (key >> p.page_shift)) : -1;
       const bool there = (unsigned)pg < (unsigned)p.num_pages;
-      const long long row = there ? qda_pool_row(pg, w.kvh, key & ((1 << p.page_shift) - 1), p.Hkv, p.page_shift) : -1;
       if (!there && key < w.s.n) atomicOr(p.err, QDA_ERR_BIT_PAGED);
-      ok = wait(&sh.r_empty[st], rs.phase ^ 1u);
-      if (!ok) break;
-      sh.row[bc & 7][lane] = row;   // (the exponential warps are at most six blocks behind)
-      unsigned char* dst = raw_s + st * K::RAW;
-      const uint32_t sb = 16 * p.NG * 2;
+      // (pool rows are below 2^32 - 1)
+      const uint32_t row = (((uint32_t)pg * (uint32_t)p.Hkv + (uint32_t)w.kvh) << p.page_shift) +
+                           (uint32_t)(key & ((1 << p.page_shift) - 1));
+      if (!wait_all(&sh.r_empty[rs.at], rs.phase ^ 1u)) break;
+      if (l4 == 0) sh.row[bc & 7][g] = there ? (long long)row : -1;   // (the exponential warps are at most six blocks behind)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.r_full[rs.at]);
       if (there) {
-        mbar_arrive_expect_tx(&sh.r_full[st], 16 * K::RB + 2 * sb);
-        bulk_g2s(dst + lane * 16 * K::RB, p.kp + row * (K::RB / 4), 16 * K::RB, &sh.r_full[st], policy);
-        bulk_g2s(dst + kPvKeys * K::RB + lane * sb, p.ks + row * p.NG, sb, &sh.r_full[st], policy);
-        bulk_g2s(dst + kPvKeys * K::RB + 8 * sb + lane * sb, p.kb + row * p.NG, sb, &sh.r_full[st], policy);
-      } else {
-        mbar_arrive(&sh.r_full[st]);
+        const uint32_t raw = smem_addr(raw_s + rs.at * K::RAW), dst = raw + 16 * g * K::RB;
+        const char* src = codes + (uint64_t)row * K::RB;
+#pragma unroll 8
+        for (int i = 0; i < 4 * CPR; ++i) {
+          const int c = 4 * i + l4;
+          pw_copy16(dst + pw_chunk<K::RB>(c / CPR, c % CPR), src + 64 * i);
+        }
+        const uint32_t to_s = raw + kPvKeys * K::RB + g * ng2 * 16, to_z = to_s + 8 * ng2 * 16;
+        const char* ks = reinterpret_cast<const char*>(p.ks) + (uint64_t)row * ng2;
+        const char* kb = reinterpret_cast<const char*>(p.kb) + (uint64_t)row * ng2;
+        for (int c = 16 * l4; c < 16 * ng2; c += 64) {
+          pw_copy16(to_s + c, ks + c);
+          pw_copy16(to_z + c, kb + c);
+        }
       }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sh.r_full[rs.at])) : "memory");
     }
-    if (lane < 8 && (!ok || *abort)) {
-      // a wait gave up: copies under way land before the CTA's shared memory goes (one lane may wait for what another never
-      // began, until the limit)
-      for (uint32_t i = bc < (uint32_t)K::RS ? 0 : bc - K::RS; i < bc; ++i) {
-        volatile int none = 0;
-        mbar_wait_bounded(&sh.r_full[i % K::RS], (i / K::RS) & 1u, &none, p.err, 2u);
-      }
-    }
+    pw_wait<0>();   // no copy is under way when the CTA's shared memory goes
   } else if (lane == 0) {
     // ============================================================================ operands and scalars of the chunks
     pdl_wait();   // the kernel ahead has laid them out
