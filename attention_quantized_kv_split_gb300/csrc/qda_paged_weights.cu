@@ -123,20 +123,24 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
   }
 }
 
-// Rows (counted new tokens times query heads of a KV head) up to which the kernel on matrix instructions takes a call.
+// Rows (counted new tokens times query heads of a KV head) up to which the kernel on matrix instructions takes a call, in the
+// instance for 8, 16 or 32 of them. Against the kernel for many, 4 sequences of 8192 keys, 8 KV heads, D 128, 4-bit: 8 rows 13 /
+// 38 us, 16 rows 17 / 38, 32 rows 26 / 38, 64 rows 74 / 38 (D 256, 8-bit: 32 rows 38 / 58, 64 rows 136 / 59; D 64: 32 rows 24 /
+// 32, 64 rows 62 / 32). D 512 has no kernel for many: its two operands do not fit the tensor memory beside an accumulator.
 constexpr int kPwMostRows = 32;
 
 struct WeightsPlan {
   bool tc;
-  int rows, chunks;
+  int rows, chunks;   // rows: in eights
   size_t bytes;
 };
 
 static WeightsPlan weights_plan(int B, int nrep, int Hkv, int total_q, int max_q, int window, int D) {
   WeightsPlan w;
   const long long count = window > 0 ? std::min(window, max_q) : max_q;
-  w.rows = (int)std::min(count * nrep, 1LL << 20);
-  w.tc = w.rows > kPwMostRows && D <= 256;
+  const long long rows = count * nrep;
+  w.tc = rows > kPwMostRows && D <= 256;
+  w.rows = rows <= 8 ? 1 : rows <= 16 || rows > kPwMostRows ? 2 : 4;
   w.chunks = 0;
   w.bytes = 0;
   if (w.tc) {
@@ -259,8 +263,8 @@ extern "C" int qdecode_paged_weights(const void* q, long long q_tstride, long lo
     return e == cudaSuccess ? QDA_OK : qda_cuda_fail(e);
   }
   const int di = D == 64 ? 0 : D == 128 ? 1 : D == 256 ? 2 : 3, gi = GS == 32 ? 0 : GS == 64 ? 1 : 2;
-  static std::atomic<int> cache[64][2][2][4][3][2] = {};
-  std::atomic<int>& slot = cache[dev][bits == 8][p.f16][di][gi][rows > 8];
+  static std::atomic<int> cache[64][2][2][4][3][3] = {};
+  std::atomic<int>& slot = cache[dev][bits == 8][p.f16][di][gi][rows / 2];
   const auto launch = bits == 4 ? (p.f16 ? qda_paged_weights_b4_f1 : qda_paged_weights_b4_f0)
                                 : (p.f16 ? qda_paged_weights_b8_f1 : qda_paged_weights_b8_f0);
   int occ = slot.load();

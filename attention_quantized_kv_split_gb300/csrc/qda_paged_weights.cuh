@@ -27,7 +27,7 @@ struct PwGeom {
   static constexpr int WPU = BITS / 4;           // words of such a unit
   static constexpr int UNITS = D / 32;           // units of a row per lane: two k-steps each
   static constexpr int ROWS = 8 * NT;
-  static constexpr int T = NT == 1 ? 2 : 1;      // sixteens of keys that a warp takes at a time
+  static constexpr int T = NT <= 2 ? 2 : 1;      // sixteens of keys that a warp takes at a time
   static constexpr int KEYS = 16 * T * kPwWarps; // keys of a block
   static constexpr int RB = W * 4, CPR = RB / 16;   // bytes and 16-byte chunks of a row of codes
   // a warp's stage: its keys' codes, scales, biases, masses, sixteen by sixteen
@@ -36,7 +36,7 @@ struct PwGeom {
   static constexpr int RING = kPwWarps * STAGES * STAGE;
   static constexpr int OPS = NT * UNITS * 32 * 16;
   static constexpr int SMEM = RING + OPS;
-  static constexpr int MINB = D >= 512 ? 2 : NT == 1 ? (D == 256 ? 4 : 5) : 3;   // resident CTAs per SM
+  static constexpr int MINB = D >= 512 ? 2 : NT == 1 ? (D == 256 ? 4 : 5) : NT == 2 && D <= 128 ? 4 : 3;   // resident CTAs per SM
   static constexpr int COST = kPwCost * KEYS / 64;
 };
 
@@ -509,9 +509,10 @@ cudaError_t pw_run(const QdaWeightsParams* p, int* ctas_per_sm, cudaStream_t s) 
 
 template <int BITS, bool F16>
 cudaError_t pw_pick(const QdaWeightsParams* p, int D, int GS, int rows, int* occ, cudaStream_t s) {
-#define QDA_PW(d, gs)                                                               \
-  if (D == d && GS == gs)                                                           \
-    return rows > 8 ? pw_run<BITS, d, gs, 4, F16>(p, occ, s) : pw_run<BITS, d, gs, 1, F16>(p, occ, s);
+#define QDA_PW(d, gs)                                                                       \
+  if (D == d && GS == gs)                                                                   \
+    return rows == 1 ? pw_run<BITS, d, gs, 1, F16>(p, occ, s)                               \
+           : rows == 2 ? pw_run<BITS, d, gs, 2, F16>(p, occ, s) : pw_run<BITS, d, gs, 4, F16>(p, occ, s);
   QDA_PW(64, 32) QDA_PW(64, 64)
   QDA_PW(128, 32) QDA_PW(128, 64) QDA_PW(128, 128)
   QDA_PW(256, 32) QDA_PW(256, 64) QDA_PW(256, 128)

@@ -108,8 +108,8 @@ __device__ __forceinline__ int pw_block_at(int blocks, long long x, F&& prefix) 
 }  // namespace qda
 #endif
 
-// Translation units per code width and input type. With ctas_per_sm the instance's resident CTAs per SM are stored there and nothing is
-// launched; else p.ctas CTAs are. rows: the bound on a KV head's query rows that choose the instance.
+// Translation units per code width and input type. With ctas_per_sm the instance's resident CTAs per SM are stored there and
+// nothing is launched; else p.ctas CTAs are. rows: query rows that the instance holds, in eights (1, 2 or 4).
 cudaError_t qda_paged_weights_b4_f0(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 cudaError_t qda_paged_weights_b4_f1(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 cudaError_t qda_paged_weights_b8_f0(const QdaWeightsParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
