@@ -112,65 +112,78 @@ __device__ __forceinline__ void pw_rows(const QdaWeightsParams& p, const PwSeq& 
                                         PwRows<NT, D / GS>& sh) {
   using G = PwGeom<BITS, D, GS, NT>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < G::ROWS; r += kPwWarps) {
-    const int tok = (row + r) / p.nrep, h = kvh * p.nrep + row + r - tok * p.nrep;
-    const bool real = row + r < s.len * p.nrep;
-    const uint16_t* src = p.q + (long long)(s.first + tok) * p.q_tstride + (long long)h * p.q_hstride;
-    constexpr int OCT = D / 8, OPL = (OCT + 31) / 32;   // octets of values, a lane's share
-    float v[OPL][8];
-    float top = 0.f;
+  constexpr int OCT = D / 8, OPL = (OCT + 31) / 32;   // octets of values, a lane's share
+  constexpr int RW = G::ROWS / kPwWarps, AT_ONCE = NT == 1 ? 1 : RW < 4 ? RW : 4;   // a warp's rows; those on their way together
+#pragma unroll 1
+  for (int r0 = 0; r0 < RW; r0 += AT_ONCE) {
+    uint4 raw[AT_ONCE][OPL];
 #pragma unroll
-    for (int i = 0; i < OPL; ++i) {
-      const int o = i * 32 + lane;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (real && o < OCT) w = __ldg(reinterpret_cast<const uint4*>(src) + o);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const int at = row + warp + (r0 + k) * kPwWarps, tok = at / p.nrep, h = kvh * p.nrep + at - tok * p.nrep;
+      const uint16_t* src = p.q + (long long)(s.first + tok) * p.q_tstride + (long long)h * p.q_hstride;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] = pw_half<F16>(u, j);
-        top = fmaxf(top, fabsf(v[i][j]));
+      for (int i = 0; i < OPL; ++i) {
+        raw[k][i] = make_uint4(0, 0, 0, 0);
+        if (at < s.len * p.nrep && i * 32 + lane < OCT) raw[k][i] = __ldg(reinterpret_cast<const uint4*>(src) + i * 32 + lane);
       }
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // 2^e times the row lies in [2^14, 2^15); what is 2^-39 of its largest and less loses bits (next to nothing)
-    const int e = top > 0.f && top < INFINITY ? max(-100, min(14 - ilogbf(top), 100)) : 0;
-    const float f = exp2f((float)e);
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const int r = warp + (r0 + k) * kPwWarps;
+      const int tok = (row + r) / p.nrep, h = kvh * p.nrep + row + r - tok * p.nrep;
+      const bool real = row + r < s.len * p.nrep;
+      float v[OPL][8];
+      float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < OPL; ++i) {
-      const int o = i * 32 + lane;
-      float part = 0.f;
+      for (int i = 0; i < OPL; ++i) {
+        const uint32_t u[4] = {raw[k][i].x, raw[k][i].y, raw[k][i].z, raw[k][i].w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] *= f;
-        part += v[i][j];
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] = pw_half<F16>(u, j);
+          top = fmaxf(top, fabsf(v[i][j]));
+        }
       }
-      // a group's octets lie side by side in lanes
 #pragma unroll
-      for (int k = 1; k < GS / 8; k <<= 1) part += __shfl_xor_sync(0xffffffffu, part, k);
-      if (o >= OCT) continue;
-      const int g = o / (GS / 8), in = o % (GS / 8);
-      if (in == 0) reinterpret_cast<float*>(&sh.sum[r >> 3][g][(r & 7) >> 1])[r & 1] = part * 5.9604644775390625e-8f;
-      constexpr float HI = BITS == 4 ? 0.0625f : 1.f;   // (odd codes of a 4-bit word stand four bits higher)
-      auto h2 = [](float a, float c) {
-        const __half2 h = __floats2half2_rn(a, c);
-        return *reinterpret_cast<const uint32_t*>(&h);
-      };
-      uint4 w;
-      if constexpr (BITS == 4) {
-        w = make_uint4(h2(v[i][0], v[i][4]), h2(v[i][1] * HI, v[i][5] * HI), h2(v[i][2], v[i][6]),
-                       h2(v[i][3] * HI, v[i][7] * HI));
-      } else {
-        w = make_uint4(h2(v[i][0], v[i][2]), h2(v[i][1], v[i][3]), h2(v[i][4], v[i][6]), h2(v[i][5], v[i][7]));
+      for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // 2^e times the row lies in [2^14, 2^15); what is 2^-39 of its largest and less loses bits (next to nothing)
+      const int e = top > 0.f && top < INFINITY ? max(-100, min(14 - ilogbf(top), 100)) : 0;
+      const float f = exp2f((float)e);
+#pragma unroll
+      for (int i = 0; i < OPL; ++i) {
+        const int o = i * 32 + lane;
+        float part = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] *= f;
+          part += v[i][j];
+        }
+        // a group's octets lie side by side in lanes
+#pragma unroll
+        for (int k = 1; k < GS / 8; k <<= 1) part += __shfl_xor_sync(0xffffffffu, part, k);
+        if (o >= OCT) continue;
+        const int g = o / (GS / 8), in = o % (GS / 8);
+        if (in == 0) reinterpret_cast<float*>(&sh.sum[r >> 3][g][(r & 7) >> 1])[r & 1] = part * 5.9604644775390625e-8f;
+        constexpr float HI = BITS == 4 ? 0.0625f : 1.f;   // (odd codes of a 4-bit word stand four bits higher)
+        auto h2 = [](float a, float c) {
+          const __half2 h = __floats2half2_rn(a, c);
+          return *reinterpret_cast<const uint32_t*>(&h);
+        };
+        uint4 w;
+        if constexpr (BITS == 4) {
+          w = make_uint4(h2(v[i][0], v[i][4]), h2(v[i][1] * HI, v[i][5] * HI), h2(v[i][2], v[i][6]),
+                         h2(v[i][3] * HI, v[i][7] * HI));
+        } else {
+          w = make_uint4(h2(v[i][0], v[i][2]), h2(v[i][1], v[i][3]), h2(v[i][4], v[i][6]), h2(v[i][5], v[i][7]));
+        }
+        ops[((r >> 3) * G::UNITS + g * G::UPL + in % G::UPL) * 32 + (r & 7) * 4 + in / G::UPL] = w;
       }
-      ops[((r >> 3) * G::UNITS + g * G::UPL + in % G::UPL) * 32 + (r & 7) * 4 + in / G::UPL] = w;
-    }
-    if (lane == 0) {
-      const int nt = r >> 3, c = (r & 7) >> 1;
-      reinterpret_cast<float*>(&sh.mul[nt][c])[r & 1] = p.qscale * exp2f((float)(24 - e));
-      reinterpret_cast<float*>(&sh.lse[nt][c])[r & 1] =
-          real ? p.lse[(long long)(s.first + tok) * p.H + h] * 1.4426950408889634f : INFINITY;   // (no row weighs nothing)
-      reinterpret_cast<int*>(&sh.last[nt][c])[r & 1] = real ? s.base + tok : -1;
+      if (lane == 0) {
+        const int nt = r >> 3, c = (r & 7) >> 1;
+        reinterpret_cast<float*>(&sh.mul[nt][c])[r & 1] = p.qscale * exp2f((float)(24 - e));
+        reinterpret_cast<float*>(&sh.lse[nt][c])[r & 1] =
+            real ? p.lse[(long long)(s.first + tok) * p.H + h] * 1.4426950408889634f : INFINITY;   // (no row weighs nothing)
+        reinterpret_cast<int*>(&sh.last[nt][c])[r & 1] = real ? s.base + tok : -1;
+      }
     }
   }
 }
