@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const
           make_uint4(w[0], w[1], w[2], w[3]);
       if (piece == 0) {
         scal->lse[i] = real ? p.lse[(long long)(s.first + tok) * p.H + h] * -1.4426950408889634f : -INFINITY;
-        scal->muls[i] = p.qscale * pv_pow2(-e);
+        scal->muls[i] = pv_pow2(-e);
         scal->last[i] = real ? s.base + tok : -1;
         if (i == part * kPvCols) scal->mul[part] = near ? p.qscale * pv_pow2(-e) : 0.f;
       }
@@ -190,7 +190,7 @@ extern "C" int qdecode_paged_weights(const void* q, long long q_tstride, long lo
   if (st == QDA_OK) st = check_pool(num_pages, page);
   if (st != QDA_OK) return st;
   const int nrep = H / Hkv;
-  if (B > QDA_MAX_B || nrep > QDA_MAX_NREP) return QDA_ERR_UNSUPPORTED;
+  if (B > QDA_MAX_B || nrep > QDA_MAX_NREP || Hkv > 65535) return QDA_ERR_UNSUPPORTED;
   if ((long long)num_pages * page * Hkv >= 0xffffffffLL) return QDA_ERR_UNSUPPORTED;
   if ((long long)total_q * nrep > 0x7fffff00LL) return QDA_ERR_UNSUPPORTED;
   const void* ptrs[5] = {q, k_packed, k_scales, k_biases, mass};

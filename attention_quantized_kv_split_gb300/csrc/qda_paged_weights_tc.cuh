@@ -41,7 +41,7 @@ constexpr int kPvSlices = 10;  // operand slices in flight, at most
 constexpr int kPvNear = 12;
 struct alignas(16) PvScalars {
   float lse[kPvRows];          // minus a row's lse in log2 units; -inf: no row
-  float muls[kPvRows];         // what undoes a row's scale, times the softmax scale
+  float muls[kPvRows];         // what undoes a row's own scale
   int last[kPvRows];           // last key that the row sees; -1: no row
   float mul[kPvParts];
 };
@@ -337,20 +337,24 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
           float one = km * f.mul[part];
           if (f.mul[part] == 0.f) {   // rare: rows with scales of their own
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] *= km * f.muls[col + i];
-            one = 1.f;
+            for (int i = 0; i < 32; ++i) v[i] *= f.muls[col + i];   // (exact: the same bits as with one scale for all)
+            one = km * p.qscale;
           }
-          if (!open) {
+          if (open) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = key > f.last[col + i] ? -INFINITY : v[i];
-          }
+            for (int i = 0; i < 8; ++i) {
+              const float4 m = *reinterpret_cast<const float4*>(f.lse + col + 4 * i);
+              const float2 e0 = __ffma2_rn(make_float2(v[4 * i], v[4 * i + 1]), make_float2(one, one), make_float2(m.x, m.y));
+              const float2 e1 = __ffma2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(one, one), make_float2(m.z, m.w));
+              sum[0] = __fadd2_rn(sum[0], make_float2(pc_ex2(e0.x), pc_ex2(e0.y)));
+              sum[1] = __fadd2_rn(sum[1], make_float2(pc_ex2(e1.x), pc_ex2(e1.y)));
+            }
+          } else {   // what a row does not see stays out, whatever the row and its lse hold
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 m = *reinterpret_cast<const float4*>(f.lse + col + 4 * i);
-            const float2 e0 = __ffma2_rn(make_float2(v[4 * i], v[4 * i + 1]), make_float2(one, one), make_float2(m.x, m.y));
-            const float2 e1 = __ffma2_rn(make_float2(v[4 * i + 2], v[4 * i + 3]), make_float2(one, one), make_float2(m.z, m.w));
-            sum[0] = __fadd2_rn(sum[0], make_float2(pc_ex2(e0.x), pc_ex2(e0.y)));
-            sum[1] = __fadd2_rn(sum[1], make_float2(pc_ex2(e1.x), pc_ex2(e1.y)));
+            for (int i = 0; i < 32; ++i) {
+              const float y = pc_ex2(fmaf(v[i], one, f.lse[col + i]));
+              sum[i & 1].x += key > f.last[col + i] ? 0.f : y;
+            }
           }
         }
         __syncwarp();

@@ -180,6 +180,43 @@ def test_absent_pages_are_neither_read_nor_written():
     assert got[3][0] == 50
 
 
+@pytest.mark.parametrize("kv,Hkv,budget", [([300, 700], 2, 64), ([9000], 1, 4000)])
+def test_own_workspace_is_enough_and_nothing_else_is_touched(kv, Hkv, budget):
+    p = Pool(kv, Hkv=Hkv, seed=31)
+    need = qda.qdecode_paged_evict_workspace_bytes(len(kv), Hkv, 16, p.table.shape[1], budget)
+    buf = torch.full((need + 8192,), 0x5A, dtype=torch.uint8, device="cuda")
+    try:
+        qda.qdecode_attn_set_workspace(buf[4096: 4096 + need])
+        p.check(budget, None, 1, 3)
+        qda.qdecode_attn_set_workspace(buf[4096: 4096 + need - 16])
+        with pytest.raises(qda.QdaError, match="-5"):
+            p.call(budget, None, 1, 3)
+    finally:
+        qda.qdecode_attn_set_workspace(None)
+    assert bool((buf[:4096] == 0x5A).all()) and bool((buf[4096 + need:] == 0x5A).all())
+
+
+def test_masses_whose_leading_bits_agree():
+    """Rows that differ in the last bits of their masses alone, and many that do not differ at all: more of them than are
+    compared one by one, so that every pass over the bits, and then the rows' order, decides."""
+    p = Pool([1500, 1500, 1500], Hkv=1, seed=40, page=32)
+    rng = np.random.default_rng(8)
+    i = np.arange(1500)
+    for b, bits in enumerate((rng.integers(0, 4, 1500), rng.integers(0, 1500, 1500), np.where(rng.random(1500) < 0.8, 7, rng.integers(0, 14, 1500)))):
+        p.mass[p.table[b][i // 32], 0, i % 32] = (np.float32(1.0).view(np.int32) + bits.astype(np.int32)).view(np.float32)
+    p.check(700, None, 0, 0)
+
+
+def test_other_calls_between_do_not_matter():
+    """The lists in the workspace are a call's own: evictions of other pools and attention between two alike."""
+    a, b = Pool([400, 300], seed=50), Pool([5000], Hkv=4, seed=51, page=64)
+    first = a.run(100, None, 2, 9)
+    b.check(2500)
+    again = a.run(100, None, 2, 9)
+    for x, y in zip((*first[0], *first[1:6]), (*again[0], *again[1:6])):
+        np.testing.assert_array_equal(x, y)
+
+
 def test_graph_stream_and_growing_batches():
     """A captured call replayed on other weights, with a larger call (and workspace) between."""
     p = Pool([300, 120], seed=21)

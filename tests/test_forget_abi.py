@@ -143,6 +143,25 @@ def test_weights_alignment(L, i):
     assert weights(L, p) == ALIGN
 
 
+def test_weights_heads_beyond_a_grid(L):
+    assert weights(L, H=65536, Hkv=65536, num_pages=9) == UNSUPPORTED
+
+
+def test_weights_workspace(L):
+    n = ctypes.c_size_t()
+    call = lambda *a: L.qdecode_paged_weights_workspace_bytes(*a, ctypes.byref(n))  # noqa: E731
+    assert call(64, 32, 8, 64, 1, 0, 128) == 0 and n.value == 0          # few rows need none
+    assert call(1, 32, 8, 2048, 2048, 0, 128) == 0 and n.value >= 8 * 2048 * 4 * 128 * 2
+    whole = n.value
+    assert call(1, 32, 8, 2048, 2048, 64, 128) == 0 and 8 * 64 * 4 * 128 * 2 <= n.value < whole / 8
+    assert call(1, 32, 8, 2048, 2048, 0, 512) == 0 and n.value == 0
+    for bad in [(0, 32, 8, 1, 1, 0, 128), (1, 31, 8, 1, 1, 0, 128), (1, 32, 0, 1, 1, 0, 128), (1, 32, 8, -1, 1, 0, 128),
+                (1, 32, 8, 1, 0, 0, 128), (1, 32, 8, 1, 1, -1, 128)]:
+        assert call(*bad) == INVALID
+    assert call(513, 32, 8, 1, 1, 0, 128) == call(1, 65, 1, 1, 1, 0, 128) == call(1, 32, 8, 1, 1, 0, 96) == UNSUPPORTED
+    assert L.qdecode_paged_weights_workspace_bytes(1, 32, 8, 1, 1, 0, 128, None) == INVALID
+
+
 def attn_lse(L, p=None, total_q=5):
     p = p or ptrs(12)
     return L.qdecode_paged_attn_lse(p[0], 1024, 128, *p[1:], total_q, 2, 2, 8, 2, 9, 16, 4, 1, 128, 64, 4, 1, None)

@@ -86,9 +86,10 @@ def test_long_sequence_among_short_ones():
     check(Case([1, 4, 1, 0, 200], [9000, 5, 1, 40, 5000], 8, 2, 128, 4, 64, "bf16", 64, seed=11), window=9)
 
 
-def test_more_new_tokens_than_keys_sees_nothing():
+@pytest.mark.parametrize("L,n", [(5, 3), (60, 20), (200, 150)])
+def test_more_new_tokens_than_keys_sees_nothing(L, n):
     """Lengths that lie (more new tokens than keys): the tokens before the first key see nothing and count nothing."""
-    check(Case([5], [3], 2, 1, 64, 4, 32, "bf16", 16, seed=1))
+    check(Case([L], [n], 2, 1, 64, 4, 32, "bf16", 16, seed=1))
 
 
 def test_keys_that_are_not_seen_reach_nothing():
@@ -103,6 +104,59 @@ def test_keys_that_are_not_seen_reach_nothing():
     assert np.isnan(got[pg, :, 36 % 16]).all()
     got[pg, :, 36 % 16] = want[pg, :, 36 % 16]
     np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("L,D", [(4, 128), (70, 128), (70, 256), (70, 512)])
+def test_rows_that_are_no_numbers_reach_only_what_they_see(L, D):
+    """A token whose query, or whose lse, is NaN or infinite: keys that it does not see keep their masses bit for bit."""
+    c = Case([L], [L + 90], 4, 2, D, 4, 64, "bf16", 16, seed=6)
+    lse, (mass, token) = log_sums(c), side(c)
+    want, _ = run(c, lse, mass, token)
+    key = np.arange(L + 90)
+    pg, row = c.table.cpu().numpy()[0][key // 16], key % 16
+    first = 90 + L // 2   # the first key that is not seen by token L // 2 - 1, nor by those before it
+    for bad in (float("nan"), float("inf"), float("-inf")):
+        q, ls = c.q.clone(), lse.clone()
+        q[: L // 2, :, 3] = bad
+        ls[L // 4: L // 2] = bad
+        got, _ = run(c, ls, mass, token, q=q)
+        np.testing.assert_array_equal(got[pg, :, row][first:], want[pg, :, row][first:])
+        assert np.isfinite(got[pg, :, row][first:]).all()
+
+
+@pytest.mark.parametrize("L,D,bits", [(3, 128, 4), (70, 64, 8), (70, 128, 4), (70, 256, 8)])
+def test_rows_and_keys_of_very_different_size(L, D, bits):
+    """Query rows 2^-30 to 2^30 apart and keys 2^-20 to 2^20 apart, side by side: each keeps its own bits. Scores stay small by
+    pairing: a key's and a row's factors enter the score together, so rows are taken whose factor undoes their keys'."""
+    c = Case([L], [L + 200], 4, 2, D, bits, 32, "bf16", 16, seed=9)
+    rng = np.random.default_rng(1)
+    power = rng.integers(-20, 21, L + 200)
+    table = c.table.cpu().numpy()[0]
+    f = torch.from_numpy(2.0 ** power).float().cuda()
+    pg = torch.from_numpy(table[np.arange(L + 200) // 16].astype(np.int64)).cuda()
+    row = torch.arange(L + 200, device="cuda") % 16
+    for a in c.arrays[1:3]:
+        a[pg, :, row] = (a[pg, :, row].float() * f[:, None, None]).to(a.dtype)
+    c.K = [k * (2.0 ** power)[None, :, None] for k in c.K]
+    # every row sees scores of up to 2^20 times its own size: rows from 2^-30 to 2^-20 of a normal one
+    scale = 2.0 ** rng.integers(-30, -19, c.total)
+    c.q = (c.q.double().cpu() * torch.from_numpy(scale)[:, None, None]).to(torch.bfloat16).cuda()
+    c.q64 = c.q.double().cpu().numpy()
+    check(c)
+
+
+def test_query_rows_far_apart_in_a_chunk():
+    """One token's queries 2^40 times the others', over keys that are tiny: the others' scores come from their own bits."""
+    c = Case([80], [300], 4, 2, 128, 4, 64, "bf16", 16, seed=12)
+    c.arrays[1] *= 2.0 ** -40
+    c.arrays[2] *= 2.0 ** -40
+    c.K = [k * 2.0 ** -40 for k in c.K]
+    f = np.full(80, 2.0 ** 40)
+    f[::7] = 1.0
+    f[::5] = 2.0 ** 20
+    c.q = (c.q.double().cpu() * torch.from_numpy(f)[:, None, None]).to(torch.bfloat16).cuda()
+    c.q64 = c.q.double().cpu().numpy()
+    check(c)
 
 
 @pytest.mark.parametrize("power", [20, -60, None])
@@ -139,6 +193,36 @@ def test_strides_streams_graphs_and_repeats():
     g.replay()
     np.testing.assert_array_equal(m.cpu().numpy(), want)
     np.testing.assert_array_equal(t.cpu().numpy(), tok)
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,window", [([1] * 512, [1 + i % 90 for i in range(512)], 0), ([40, 0] * 60, [60, 9] * 60, 0),
+                                                   ([33] * 100, [40 + i for i in range(100)], 17)])
+def test_large_batches(q_lens, kv_lens, window):
+    check(Case(q_lens, kv_lens, 2, 1, 64, 4, 32, "bf16", 16, seed=len(q_lens)), window, 0.5)
+
+
+@pytest.mark.parametrize("L,D", [(2, 128), (64, 128), (64, 256), (64, 512)])
+def test_own_workspace_is_enough_and_nothing_else_is_touched(L, D):
+    """An installed workspace of exactly the bytes asked for, guard bytes around it and around masses and tokens."""
+    c = Case([L, 1], [200, 150], 8, 2, D, 4, 64, "fp16", 32, seed=D)
+    lse, (mass, token) = log_sums(c), side(c)
+    want, tok = run(c, lse, mass, token)
+    need = qda.qdecode_paged_weights_workspace_bytes(2, 8, 2, c.total, L, 0, D)
+    assert (need > 0) == (L * 4 > 32 and D <= 256)
+    buf = torch.full((need + 8192,), 0x5A, dtype=torch.uint8, device="cuda")
+    try:
+        if need:
+            qda.qdecode_attn_set_workspace(buf[4096: 4096 + need])
+        got, got_tok = run(c, lse, mass, token)
+        if need:
+            qda.qdecode_attn_set_workspace(buf[4096: 4096 + need - 256])
+            with pytest.raises(qda.QdaError, match="-5"):
+                run(c, lse, mass, token)
+    finally:
+        qda.qdecode_attn_set_workspace(None)
+    np.testing.assert_array_equal(got, want)
+    np.testing.assert_array_equal(got_tok, tok)
+    assert bool((buf[:4096] == 0x5A).all()) and bool((buf[4096 + need:] == 0x5A).all())
 
 
 @pytest.mark.parametrize("causal", [True, False])
