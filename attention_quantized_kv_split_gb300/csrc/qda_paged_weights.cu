@@ -15,31 +15,28 @@ constexpr int kPlThreads = 512;
 // read, and its scalars: the rows in fp16 times a power of two that brings the largest value of all of them to [2^14, 2^15),
 // or of each of them where they differ too much; rows behind the sequence's last are zeros that weigh nothing.
 template <int D>
-__global__ void __launch_bounds__(kPlThreads) qda_paged_weights_lay_kernel(const __grid_constant__ QdaWeightsParams p) {
+__global__ void __launch_bounds__(kPlThreads, 3) qda_paged_weights_lay_kernel(const __grid_constant__ QdaWeightsParams p) {
   using G = PvGeom<D>;
-  __shared__ int s_chunk[QDA_MAX_B + 1], s_tot[kPlThreads / 32];
+  __shared__ int s_chunk[QDA_MAX_B + 1];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_launch_dependents();
-  int carry = 0;
-  if (tid == 0) s_chunk[0] = 0;
-  for (int b0 = 0; b0 < p.B; b0 += kPlThreads) {
-    const int b = b0 + tid;
-    int c = b < p.B ? pv_chunks(p, pw_seq(p, b)) : 0;
+  if (warp == 0) {   // chunks before each sequence
+    int c0 = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      int c = b < p.B ? pv_chunks(p, pw_seq(p, b)) : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int z = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += z;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int z = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += z;
+      }
+      if (b < p.B) s_chunk[b + 1] = c0 + c;
+      c0 += __shfl_sync(0xffffffffu, c, 31);
     }
-    if (lane == 31) s_tot[warp] = c;
-    __syncthreads();
-    int before = carry;
-    for (int w = 0; w < kPlThreads / 32; ++w) {
-      if (w < warp) before += s_tot[w];
-      carry += s_tot[w];
-    }
-    if (b < p.B) s_chunk[b + 1] = before + c;
-    __syncthreads();
+    if (lane == 0) s_chunk[0] = 0;
   }
+  __syncthreads();
+  const int carry = s_chunk[p.B];
   if (carry > p.max_chunks) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) atomicOr(p.err, QDA_ERR_BIT_PAGED);
     return;
