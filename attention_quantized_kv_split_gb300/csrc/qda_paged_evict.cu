@@ -61,7 +61,10 @@ struct alignas(16) EvShared {
 // rank), so what stays is what is not below the edge. Then holes and rows that come are counted in order, a bit a row, and
 // listed: the i-th hole meets the i-th row that comes, whatever the timing. A row's mass and token are read once. Bound by
 // latency: loads two deep, then some ten barriers; reading all of the other CTAs' bins took half of the time (distributed
-// shared memory is slow to read), so that sums of 32 bins come first and then the 32 that matter.
+// shared memory is slow to read), so that sums of 32 bins come first and then the 32 that matter (32768 rows of eight heads: 43
+// to 31 us, both kernels). It takes 14.6 us for 512 heads of 2049 rows in CTAs of their own, 20 us for eight of 32768 in clusters
+// of eight, 23 us for 128 heads of 300 to 9001 rows in clusters of four. Comparing the last ranks instead of going on bit by bit:
+// 43 to 29 us for the first.
 template <bool ONE>
 __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ uint32_t s_key[];   // keys, and behind them the pool row of every sixteenth row (-1: none)
@@ -335,7 +338,8 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
 // The rows that come are copied to the holes: a lane has one fixed piece of a row (16 bytes of codes, scales or biases, its
 // mass, its token) and walks the rows, so that its addresses are a multiplication and an addition. Sources lie behind the
 // budget and holes before it: no order among CTAs matters. CTA (0, 0) also does the lengths and the table, which the
-// selection has read and this kernel's other CTAs do not.
+// selection has read and this kernel's other CTAs do not. Rows are read where they lie, 512 bytes and less at a place, so that
+// latency binds before HBM does: 25 us for 100 MB of rows (D 256, 8-bit; HBM at 50 %), 7 us for one row of each of 512 heads.
 constexpr int kEvMoveThreads = 256;
 
 __global__ void __launch_bounds__(kEvMoveThreads) qda_paged_evict_move_kernel(const __grid_constant__ EvictParams p) {

@@ -208,7 +208,8 @@ int qdecode_attn_debug_force_splits(int num_ctas);
  * thread) stops before its chunk number `chunk`, so that CTA's consumers wait for data that never comes. Their
  * bounded wait gives up after its time limit (about one second), the call's output is invalid and
  * qdecode_attn_device_status() reports bit 1; the context stays usable. chunk < 0 switches it off. In a library built with
- * QDA_BOUNDS_CHECK it also holds back that block of 128 keys of the first CTA in the paged calls' chunk kernel.
+ * QDA_BOUNDS_CHECK it also holds back that block of 128 keys of the first CTA in the paged calls' chunk kernel, and the
+ * slice of that number of 64 dimensions of query rows of the first CTA in qdecode_paged_weights' kernel for many rows.
  */
 int qdecode_attn_debug_stall_chunk(int chunk);
 
@@ -375,7 +376,7 @@ int qdecode_paged_attn_lse(const void* q, long long q_tstride, long long q_hstri
 /*
  * qdecode_rope: rotary positions. The first rot of D dimensions of every row of q [T, H, D] and k [T, Hkv, D] are turned by
  * the token's position n = positions[t] (plus shift[b] of the sequence b that holds row t by q_start [B + 1]; both or
- * neither may be NULL): pair i, which is (x[i], x[i + rot / 2]), with interleaved != 0 (x[2i], x[2i + 1]), becomes
+ * neither may be NULL; the sum must stay below 2^31): pair i, which is (x[i], x[i + rot / 2]), with interleaved != 0 (x[2i], x[2i + 1]), becomes
  *     scale * (a cos(n f_i) - b sin(n f_i),  b cos(n f_i) + a sin(n f_i)),   f_i = freqs[i] radians per position
  * (freqs [rot / 2], double, device). With inverse != 0 it turns the other way: the gradient of the inputs from that of the
  * outputs. The dimensions from rot on are copied. Rows whose position is negative (qdecode_paged_map's behind the last
@@ -409,12 +410,12 @@ int qdecode_rope_freqs(int rot, double base, double factor, double context, doub
  *     mass[j, kvh] = decay * mass[j, kvh] + sum_t sum_h exp(q[t, h, :] . k_hat[j] / sqrt(D) - lse[t, h])
  * over the sequence's last `window` new tokens (0: all of them) that see key j and the query heads h of KV head kvh. Keys of
  * the new tokens themselves start from 0, whatever mass holds there, and their token becomes their position, j + shift[b]
- * (shift may be NULL: 0). Sequences without new tokens, and rows behind kv_len, stay as they are. max_q bounds the new
+ * (shift may be NULL: 0; the sum must stay below 2^31). Sequences without new tokens, and rows behind kv_len, stay as they are. max_q bounds the new
  * tokens of a sequence and only chooses the kernel. Scores are right to fp32 (queries below 2^-39 of their row's largest
- * and keys' values below 2^-39 of what their key can hold aside); sums are fp32 in a fixed order: the same bits on every run.
- * Scales and biases as for the attention: a key that is not finite spoils its own mass alone. Same types, limits and checks
- * as qdecode_paged_attn; mass 16-byte aligned. Uses the workspace as qdecode_attn does, of qdecode_paged_weights_workspace_bytes()
- * bytes; calls that share one must not overlap on the GPU.
+ * and keys' values below 2^-39 of what their key can hold aside); sums are fp32 in a fixed order: the same bits on every
+ * run. Scales and biases as for the attention: a key that is not finite spoils its own mass alone. Same types, limits and
+ * checks as qdecode_paged_attn; mass 16-byte aligned. Uses the workspace as qdecode_attn does, of
+ * qdecode_paged_weights_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
  */
 int qdecode_paged_weights(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                           const void* k_scales, const void* k_biases, const float* lse, float* mass, int32_t* token,
@@ -428,9 +429,9 @@ int qdecode_paged_weights_workspace_bytes(int B, int H, int Hkv, int total_q, in
 /*
  * qdecode_paged_evict: cuts every sequence of more than `limit` rows to `budget` rows (1 <= budget <= limit), each KV head
  * by itself. What stays: rows whose token is below `sinks` or one of the `recent` newest positions (those from
- * kv_len[b] + shift[b] - recent on), then those of the largest mass; of equal ones the lowest rows. (A mass that is no number ranks below
- * all.) Needs sinks + recent <= budget. Rows that stay and lie at budget or behind move to the places of rows that go, both
- * in ascending order; the others stay where they are, so a step that cuts one row moves at most one row per head. Order in
+ * kv_len[b] + shift[b] - recent on), then those of the largest mass; of equal ones the lowest rows. (A mass that is no
+ * number ranks below all.) Needs sinks + recent <= budget. Rows that stay and lie at budget or behind move to the places of
+ * rows that go, both in ascending order; the others stay where they are, so a step that cuts one row moves at most one row per head. Order in
  * the cache means nothing to the attention; mass and token move along. Codes, scales and biases move bit for bit.
  *
  * Writes new_len[b] = budget, or kv_len[b] where nothing is cut (new_len must not be kv_len), adds what was cut to shift[b]
@@ -438,8 +439,8 @@ int qdecode_paged_weights_workspace_bytes(int B, int H, int Hkv, int total_q, in
  * sequences in order; n_freed[0] counts them all, above max_freed some found no place (status bit 8). A length that is
  * negative or beyond the table leaves its sequence as it is and sets bit 8; so does a page outside the pool, of which no row
  * is read or written. Contents of rows from budget on are unspecified. D, GS, bits, pages and B as for the other paged
- * calls, Hkv <= QDA_EVICT_MAX_HEADS, max_pages * page below 2^31 - 512; mass and token 16-byte aligned. Uses the workspace as qdecode_attn does, of
- * qdecode_paged_evict_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
+ * calls, Hkv <= QDA_EVICT_MAX_HEADS, max_pages * page below 2^31 - 512; mass and token 16-byte aligned. Uses the workspace
+ * as qdecode_attn does, of qdecode_paged_evict_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
  */
 #define QDA_EVICT_MAX_HEADS 64
 int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_biases, uint32_t* v_packed, void* v_scales,
@@ -467,8 +468,8 @@ int qdecode_attn_last_cuda_error(void);
 
 /*
  * Device-side status: copies (synchronously) and clears the current device's error word. Bits: 1 = a pipeline
- * wait in a split kernel or in the paged calls' chunk kernel gave up after its time limit (the output of that call is
- * invalid); 2 = waiting for the CTA's own copies or products to land before it exits gave up; 4 = an index check failed
+ * wait in a split kernel, in the paged calls' chunk kernel or in qdecode_paged_weights' kernel for many rows gave up after
+ * its time limit (the output of that call, or its masses, are invalid); 2 = waiting for the CTA's own copies or products to land before it exits gave up; 4 = an index check failed
  * (only a library built with QDA_BOUNDS_CHECK checks, and it skips the access); 8 = a paged call met a page, slot or
  * length outside its pool or table. 0 = clean.
  */
