@@ -30,10 +30,10 @@ __global__ void __launch_bounds__(kPlThreads, 3) qda_paged_weights_lay_kernel(co
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int z = __shfl_up_sync(0xffffffffu, c, o);
-        if (lane >= o) c += z;
+        if (lane >= o) c = pv_add(c, z);
       }
-      if (b < p.B) s_chunk[b + 1] = c0 + c;
-      c0 += __shfl_sync(0xffffffffu, c, 31);
+      if (b < p.B) s_chunk[b + 1] = pv_add(c0, c);
+      c0 = pv_add(c0, __shfl_sync(0xffffffffu, c, 31));
     }
     if (lane == 0) s_chunk[0] = 0;
   }

@@ -81,6 +81,10 @@ __device__ __forceinline__ int pv_chunks(const QdaWeightsParams& p, const PwSeq&
   return s.n > 0 ? (int)(((long long)s.count * p.nrep + kPvRows - 1) / kPvRows) : 0;
 }
 
+// Sums of chunks stay at kPvTop, more than there is ever room for: starts that fall may count a row many times.
+constexpr int kPvTop = 0x3fffffff;
+__device__ __forceinline__ int pv_add(int a, int b) { return min(a + b, kPvTop); }
+
 // Work of the first i blocks of a sequence under one KV head: the rows of a block's chunks, the last one as if it were full.
 __device__ __forceinline__ long long pv_prefix(const QdaWeightsParams& p, const PwSeq& s, int i) {
   return pw_prefix<kPvKeys>(p, s, i, kPvCost + (long long)pv_chunks(p, s) * kPvRows, kPvCost + kPvRows);
@@ -257,7 +261,7 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
       const int z = __shfl_up_sync(0xffffffffu, c, o);
       if (lane >= o) {
         v += y;
-        c += z;
+        c = pv_add(c, z);
       }
     }
     if (lane == 31) {
@@ -270,14 +274,14 @@ __global__ void __launch_bounds__(kPvWarps * 32, 1) qda_paged_weights_tc_kernel(
     for (int w = 0; w < kPvWarps; ++w) {
       if (w < warp) {
         before += sh.tot[w];
-        cbefore += sh.ctot[w];
+        cbefore = pv_add(cbefore, sh.ctot[w]);
       }
       carry += sh.tot[w];
-      ccarry += sh.ctot[w];
+      ccarry = pv_add(ccarry, sh.ctot[w]);
     }
     if (b < p.B) {
       sh.at[b + 1] = before + v;
-      sh.chunk[b + 1] = cbefore + c;
+      sh.chunk[b + 1] = pv_add(cbefore, c);
     }
     __syncthreads();
   }

@@ -275,3 +275,75 @@ def test_log_sums_of_rows_done_anew():
     ref = R.log_sums(c)[:39]
     err = np.abs(lse.cpu().numpy()[:39] - ref)
     assert (err <= 2.0 ** -11 * 30 + 2.0 ** -17).all(), err.max()   # (sum |q k| / sqrt(D) stays below 30 here)
+
+
+def call(c, lse, mass, token, table=None, q_start=None, kv_len=None):
+    """The status of a call with other tables; masses and tokens behind it."""
+    m, t = torch.from_numpy(mass).cuda(), torch.from_numpy(token).cuda()
+    i32 = lambda a, like: like if a is None else torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    qda.qdecode_paged_weights(c.q, *c.arrays[:3], lse, m, t, i32(q_start, c.q_start), i32(kv_len, c.kv_len), i32(table, c.table),
+                              max(c.q_lens), c.GS, c.bits, decay=0.5)
+    torch.cuda.synchronize()
+    return qda.qdecode_attn_device_status(), m.cpu().numpy(), t.cpu().numpy()
+
+
+@pytest.mark.parametrize("L,D", [(1, 128), (3, 256), (40, 64), (70, 256), (70, 512)])
+@pytest.mark.parametrize("page", [-1, 1 << 30])
+def test_absent_pages_are_neither_read_nor_written(L, D, page):
+    """A page outside the pool sets bit 8; keys of other pages come out as they would."""
+    c = Case([L, 1], [L + 150, 33], 4, 2, D, 4, 64, "bf16", 16, seed=5)
+    lse, (mass, token) = log_sums(c), side(c)
+    status, want, tok = call(c, lse, mass, token)
+    assert status == 0
+    table = c.table.cpu().numpy()
+    gone = table[0, [3, (L + 149) // 16]]
+    table[0, [3, (L + 149) // 16]] = page
+    status, got, tk = call(c, lse, mass, token, table=table)
+    assert status == 8
+    want[gone], tok[gone] = mass[gone], token[gone]
+    np.testing.assert_array_equal(got, want)
+    np.testing.assert_array_equal(tk, tok)
+
+
+@pytest.mark.parametrize("L", [2, 70])
+def test_lengths_and_starts_that_lie(L):
+    """A length beyond the table or negative, starts that fall or lie outside q: bit 8; the other sequence comes out right."""
+    c = Case([L, L], [L + 60, L + 45], 4, 2, 128, 4, 64, "bf16", 16, seed=4)
+    lse, (mass, token) = log_sums(c), side(c)
+    _, want, tok = call(c, lse, mass, token)
+    second = c.table.cpu().numpy()[1][: -(-(L + 45) // 16)]
+    for n in (-3, 1 << 20, (1 << 31) - 1):
+        status, got, tk = call(c, lse, mass, token, kv_len=[n, L + 45])
+        assert status == 8
+        np.testing.assert_array_equal(got[second], want[second])
+        np.testing.assert_array_equal(tk[second], tok[second])
+    for start in ([0, L, 3 * L], [-5, L, 2 * L], [L, 0, 2 * L], [0, 2 * L, L]):
+        assert call(c, lse, mass, token, q_start=start)[0] == 8
+
+
+def test_starts_that_count_rows_many_times():
+    """More chunks than the workspace has room for: nothing is written."""
+    B = 40
+    c = Case([70] * B, [80] * B, 4, 2, 128, 4, 64, "bf16", 16, seed=4)
+    lse, (mass, token) = log_sums(c), side(c)
+    status, got, tk = call(c, lse, mass, token, q_start=[0, 70 * B] * (B // 2) + [0])
+    assert status == 8
+    np.testing.assert_array_equal(got, mass)
+    np.testing.assert_array_equal(tk, token)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_many_rows_captured(D):
+    c = Case([70, 0, 33, 200], [170, 5, 33, 500], 4, 2, D, 8, 32, "fp16", 32, seed=8)
+    lse, (mass, token) = log_sums(c), side(c)
+    want, tok = run(c, lse, mass, token, 64, 0.5)
+    m, t = torch.from_numpy(mass).cuda(), torch.from_numpy(token).cuda()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qda.qdecode_paged_weights(c.q, *c.arrays[:3], lse, m, t, c.q_start, c.kv_len, c.table, 200, 32, 8, 64, 0.5)
+    for _ in range(3):
+        m.copy_(torch.from_numpy(mass))
+        g.replay()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(m.cpu().numpy(), want)
+        np.testing.assert_array_equal(t.cpu().numpy(), tok)
