@@ -69,7 +69,8 @@ __host__ __device__ inline long long qda_pool_row(int pg, int kvh, int r, int Hk
   return ((((long long)pg * Hkv) + kvh) << page_shift) + r;
 }
 
-// The split kernel (qda_paged_split.cuh), translation units per (bits, fp16), with and without the rows' sums: its instance for (D, GS, rows per tile).
+// The split kernel (qda_paged_split.cuh), translation units per (bits, fp16), with and without the rows' sums: its instance for
+// (D, GS, rows per tile).
 // With ctas_per_sm the instance's resident CTAs per SM are stored there and nothing is launched; else p.ctas CTAs are.
 cudaError_t qda_paged_split_b4_f0(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);
 cudaError_t qda_paged_split_b4_f0_lse(const QdaPagedParams* p, int D, int GS, int rows, int* ctas_per_sm, cudaStream_t s);

@@ -14,6 +14,7 @@ namespace qda {
 
 constexpr int kRopeThreads = 256;   // at most
 constexpr int kRopeAngles = 2048;   // cosines and sines that a CTA holds: 16 KB
+constexpr int kRopeTokens = 8;      // tokens of a CTA, at most
 
 struct RopeParams {
   const void* x[2];         // queries, keys
@@ -63,7 +64,7 @@ struct alignas(sizeof(T) * V) RopeVec {
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) qda_rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ __align__(16) float2 cs[kRopeAngles];
-  __shared__ int s_pos[kRopeAngles];
+  __shared__ int s_pos[kRopeTokens];
   __shared__ int s_start[QDA_MAX_B + 1];
   using Vec = RopeVec<T, V>;
   const int tid = threadIdx.x, half = p.rot >> 1;
@@ -315,7 +316,7 @@ extern "C" int qdecode_rope(const void* q, long long q_tstride, long long q_hstr
   const int rounds = (int)(((long long)all * p.items + kRopeThreads - 1) / kRopeThreads);
   p.rows = (all + rounds - 1) / rounds;
   // tokens to a CTA: up to eight rounds, fewer where that leaves SMs without CTAs; with few tokens the rounds are shared
-  long long tokens = std::max(1LL, 8LL / rounds);
+  long long tokens = std::max(1, kRopeTokens / rounds);
   tokens = std::min(tokens, std::max(1LL, (long long)T / (6LL * sms)));
   tokens = std::min(tokens, (long long)(kRopeAngles / (rot / 2)));
   const int splits = tokens == 1 ? (int)std::min<long long>(rounds, std::max(1LL, 4LL * sms / T)) : 1;
