@@ -34,9 +34,10 @@ struct EvictParams {
   unsigned int* err;
 };
 
-// A mass as an unsigned number that orders alike; no number ranks below all, and the highest pattern stays free.
+// A mass as an unsigned number that orders alike, zeros of either sign as one; no number ranks below all, and the highest pattern
+// stays free.
 __device__ __forceinline__ uint32_t ev_rank(float m) {
-  const uint32_t u = __float_as_uint(m);
+  const uint32_t u = __float_as_uint(m + 0.f);   // (-0 + 0 is 0; everything else stays as it is)
   return m != m ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 

@@ -242,3 +242,11 @@ def test_graph_stream_and_growing_batches():
         np.testing.assert_array_equal(a, b)
     for a, b in zip(got[1:], want[1:]):
         np.testing.assert_array_equal(a, b)
+
+
+def test_zeros_of_either_sign_are_alike():
+    """-0.0 and 0.0 are equal masses: of them the lowest rows stay."""
+    p = Pool([200, 3000], Hkv=2, seed=60, page=32)
+    p.mass[:] = np.random.default_rng(4).choice(np.array([-0.0, 0.0], dtype=np.float32), p.mass.shape)
+    p.mass[p.table[1, :9]] = np.float32(-1e-45)
+    p.check(70, None, 1, 3)
