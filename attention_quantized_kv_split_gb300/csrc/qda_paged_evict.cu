@@ -96,8 +96,9 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
   const int lo = (int)min((long long)n, (long long)piece * me), hi = (int)min((long long)n, (long long)lo + piece);
   const int pmask = (1 << p.page_shift) - 1;
   const int* tab = p.table + (size_t)b * p.max_pages;
-  const int seen = n + (p.shift != nullptr ? p.shift[b] : 0);
-  const int young = seen - p.recent;
+  // the newest position that `recent` does not protect (counted down from the newest of all, which is below 2^31; the one behind
+  // it need not be)
+  const int old = n - 1 + (p.shift != nullptr ? p.shift[b] : 0) - p.recent;
   // (pool rows are below 2^32 - 1, which stands for a row that is not there)
   auto row_of = [&](int i) -> uint32_t {
     const int pg = __ldg(tab + (i >> p.page_shift));
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
     }
     const int t = __ldg(p.token + r);
     const uint32_t k = ev_rank(__ldg(p.mass + r));
-    return t < p.sinks || t >= young ? 0xffffffffu : k;
+    return t < p.sinks || t > old ? 0xffffffffu : k;
   };
   uint32_t* const s_row = s_key + p.held;
   // four rows of a page at a time (pages hold sixteens of rows, masses and tokens are aligned), four such loads on their way
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kEvThreads) qda_paged_evict_select_kernel(cons
       if (r[u] == 0xffffffffu) {
         atomicOr(p.err, QDA_ERR_BIT_PAGED);
       } else {
-        auto rank = [&](float x, int y) { return y < p.sinks || y >= young ? 0xffffffffu : ev_rank(x); };
+        auto rank = [&](float x, int y) { return y < p.sinks || y > old ? 0xffffffffu : ev_rank(x); };
         k = make_uint4(rank(m[u].x, t[u].x), rank(m[u].y, t[u].y), rank(m[u].z, t[u].z), rank(m[u].w, t[u].w));
       }
       *reinterpret_cast<uint4*>(s_key + i - lo) = k;   // (a piece's room is a multiple of 32 keys)

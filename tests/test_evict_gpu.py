@@ -250,3 +250,17 @@ def test_zeros_of_either_sign_are_alike():
     p.mass[:] = np.random.default_rng(4).choice(np.array([-0.0, 0.0], dtype=np.float32), p.mass.shape)
     p.mass[p.table[1, :9]] = np.float32(-1e-45)
     p.check(70, None, 1, 3)
+
+
+@pytest.mark.parametrize("recent", [0, 1, 7])
+def test_newest_position_of_all(recent):
+    """Tokens up to position 2^31 - 1: those that are protected are the newest, none where none is asked for."""
+    p = Pool([200], seed=61)
+    p.shift[:] = (1 << 31) - 200   # (the newest token's position is 2^31 - 1)
+    i = np.arange(200)
+    for h in range(2):
+        p.token[p.table[0][i // 16], h, i % 16] = np.random.default_rng(h).permutation(200) + np.int64(p.shift[0])
+    got = p.run(64, None, 0, recent)
+    want = R.evict(p.arrays, p.mass, p.token, [200], p.table, np.full(p.table.size, -7), 16, 64, None, 0, recent, p.shift.astype(np.int64))
+    for a, b in zip((*got[0], *got[1:]), (*want[0], *want[1:])):
+        np.testing.assert_array_equal(a, b)
