@@ -346,10 +346,11 @@ constexpr int kEvMoveThreads = 256;
 
 __global__ void __launch_bounds__(kEvMoveThreads) qda_paged_evict_move_kernel(const __grid_constant__ EvictParams p) {
   __shared__ int s_first[QDA_MAX_B + 1];
+  __shared__ int s_count[kEvMoveThreads / 32];
   const int tid = threadIdx.x;
   pdl_wait();
   if (blockIdx.x == 0 && blockIdx.y == 0) {
-    // freed pages before each sequence, the first sequences' first
+    // table entries that go before each sequence's, the first sequences' first
     if (tid < 32) {
       int carry = 0;
       for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -374,19 +375,51 @@ __global__ void __launch_bounds__(kEvMoveThreads) qda_paged_evict_move_kernel(co
         if (b < p.B) s_first[b] = carry + up - pages;
         carry += __shfl_sync(0xffffffffu, up, 31);
       }
-      if (tid == 0) {
-        s_first[p.B] = carry;
-        p.n_freed[0] = carry;
-        if (carry > p.max_freed) atomicOr(p.err, QDA_ERR_BIT_PAGED);
-      }
+      if (tid == 0) s_first[p.B] = carry;
     }
     __syncthreads();
     const int keep = (int)(((long long)p.budget + (1 << p.page_shift) - 1) >> p.page_shift);
-    for (int i = tid; i < s_first[p.B]; i += kEvMoveThreads) {
+    const int total = s_first[p.B];
+    auto entry = [&](int i) {
       const int b = qda_seq_of(s_first, p.B, i);
-      int* e = p.table + (size_t)b * p.max_pages + keep + (i - s_first[b]);
-      if (i < p.max_freed) p.freed[i] = *e;
-      *e = -1;
+      return p.table + (size_t)b * p.max_pages + keep + (i - s_first[b]);
+    };
+    bool absent = false;   // entries outside the pool leave the table, but are no pages that could be given back
+#pragma unroll 4
+    for (int i = tid; i < total; i += kEvMoveThreads) absent |= (unsigned)*entry(i) >= (unsigned)p.num_pages;
+    int at = total;
+    if (!__syncthreads_or(absent)) {
+      for (int i = tid; i < total; i += kEvMoveThreads) {
+        int* e = entry(i);
+        if (i < p.max_freed) p.freed[i] = *e;
+        *e = -1;
+      }
+    } else {
+      const int lane = tid & 31, warp = tid >> 5;
+      at = 0;
+      for (int i0 = 0; i0 < total; i0 += kEvMoveThreads) {
+        int pg = -1;
+        if (i0 + tid < total) {
+          int* e = entry(i0 + tid);
+          pg = *e;
+          *e = -1;
+        }
+        const bool real = (unsigned)pg < (unsigned)p.num_pages;
+        const uint32_t some = __ballot_sync(0xffffffffu, real);
+        if (lane == 0) s_count[warp] = __popc(some);
+        __syncthreads();
+        int to = at + __popc(some & ((1u << lane) - 1));
+        for (int w = 0; w < kEvMoveThreads / 32; ++w) {
+          to += w < warp ? s_count[w] : 0;
+          at += s_count[w];
+        }
+        if (real && to < p.max_freed) p.freed[to] = pg;
+        __syncthreads();
+      }
+    }
+    if (tid == 0) {
+      p.n_freed[0] = at;
+      if (at > p.max_freed) atomicOr(p.err, QDA_ERR_BIT_PAGED);
     }
   }
   const int unit = blockIdx.y, moves = min(p.moves[unit], p.most);

@@ -264,3 +264,23 @@ def test_newest_position_of_all(recent):
     want = R.evict(p.arrays, p.mass, p.token, [200], p.table, np.full(p.table.size, -7), 16, 64, None, 0, recent, p.shift.astype(np.int64))
     for a, b in zip((*got[0], *got[1:]), (*want[0], *want[1:])):
         np.testing.assert_array_equal(a, b)
+
+
+@pytest.mark.parametrize("kv,gone", [([100, 100], [(0, 5), (1, 4), (1, 1)]), ([100, 6000, 40, 9000], [(b, c) for b in (1, 3) for c in range(5, 375, 3)]),
+                                     ([100], [(0, 4), (0, 5), (0, 6)])])
+@pytest.mark.parametrize("max_freed", [None, 2])
+def test_absent_pages_are_not_given_back(kv, gone, max_freed):
+    """Entries outside the pool leave the table, but they are no pages: neither in freed nor counted."""
+    p = Pool(kv, seed=62, spare=4)
+    for j, (b, c) in enumerate(gone):
+        p.table[b, c] = (-1, p.mass.shape[0], -(1 << 31))[j % 3]
+    got = p.run(50, max_freed=max_freed)
+    assert qda.qdecode_attn_device_status() == 8
+    behind = [p.table[b, 4: -(-n // 16)] for b, n in enumerate(kv) if n > 50]
+    pages = np.concatenate([x[(x >= 0) & (x < p.mass.shape[0])] for x in behind])
+    assert got[6] == len(pages)
+    room = p.table.size if max_freed is None else max_freed
+    np.testing.assert_array_equal(got[5], np.concatenate([pages, np.full(room, -7)])[:room])
+    for b, n in enumerate(kv):
+        if n > 50:
+            assert (got[4][b, 4:] == -1).all()
