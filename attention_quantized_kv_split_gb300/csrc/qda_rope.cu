@@ -231,6 +231,19 @@ static bool rope_touch(const void* a, long long at, long long ah, int aheads, co
   return off < ahi - alo || off + (bhi - blo) > step;
 }
 
+// Whether two of the rows that T tokens' `heads` heads have, D values at token * ts + head * hs, touch.
+static bool rope_collide(long long ts, int T, long long hs, int heads, int D) {
+  const __int128 t = ts < 0 ? -(__int128)ts : ts, h = hs < 0 ? -(__int128)hs : hs;
+  if ((T > 1 && t < D) || (heads > 1 && h < D)) return true;
+  if (T == 1 || heads == 1 || t >= (heads - 1) * h + D || h >= (T - 1) * t + D) return false;   // one lies within the other
+  // dh heads on, the nearest tokens (of either direction: rows differ by dt tokens and dh heads, dt of any sign)
+  for (int dh = 1; dh < heads; ++dh) {
+    const __int128 off = dh * h, dt = off / t;
+    if ((dt < T && off - dt * t < D) || (dt + 1 < T && (dt + 1) * t - off < D)) return true;
+  }
+  return false;
+}
+
 }  // namespace qda
 
 extern "C" int qdecode_rope_freqs(int rot, double base, double factor, double context, double slow, double fast,
@@ -270,11 +283,8 @@ extern "C" int qdecode_rope(const void* q, long long q_tstride, long long q_hstr
     if (off16(ptrs[i]) || (heads[i] > 0 && (strides[i][0] % (16 / e) || strides[i][1] % (16 / e)))) return QDA_ERR_ALIGN;
   if (off4(positions) || off4(q_start) || off4(shift) || (reinterpret_cast<uintptr_t>(freqs) & 7u)) return QDA_ERR_ALIGN;
   if (T == 0) return QDA_OK;
-  for (int i = 2; i < 4; ++i) {   // rows of an output stand apart
-    if (heads[i] == 0) continue;
-    if (heads[i] > 1 && std::llabs(strides[i][1]) < D) return QDA_ERR_INVALID;
-    if (T > 1 && std::llabs(strides[i][0]) < D) return QDA_ERR_INVALID;
-  }
+  for (int i = 2; i < 4; ++i)
+    if (heads[i] > 0 && rope_collide(strides[i][0], T, strides[i][1], heads[i], D)) return QDA_ERR_INVALID;
   auto touch = [&](int i, int j) {
     return heads[i] > 0 && heads[j] > 0 &&
            rope_touch(ptrs[i], strides[i][0], strides[i][1], heads[i], ptrs[j], strides[j][0], strides[j][1], heads[j], T, D, e);

@@ -302,3 +302,20 @@ def test_evict_allocates_in_the_streams_context(monkeypatch):
     monkeypatch.setattr(torch, "empty", lambda *a, **k: (seen.append(list(inside)), empty(*a, **k))[1])
     pool.evict(i32(1), i32(1, 2), 4, stream=77)
     assert len(seen) == 3 and all(s == [77] for s in seen)
+
+
+# ------------------------------------------------------------------- outputs upon each other, numbers beyond fp32
+
+
+@pytest.mark.parametrize("ts,hs", [(128, 128), (256, 128), (896, 128), (128, 256), (384, 256), (-128, 128), (256, -128)])
+def test_rope_rows_of_an_output_that_collide(L, ts, hs):
+    """Token and head strides of D or more each for itself, that bring two rows to one place or partly over each other (T = 3
+    tokens of 8 heads of 128 values)."""
+    assert rope(L, qo=(ts, hs)) == INVALID
+    p = [*ptrs(6), None, None]
+    assert rope(L, edit(p, 2, p[0]), qs=(ts, hs), qo=(ts, hs)) == INVALID
+
+
+def test_rope_rows_that_collide_in_part(L):
+    assert rope(L, qo=(128 * 9, 128 * 6 - 8)) == INVALID        # three tokens on, two heads back: 24 elements apart
+    assert rope(L, qo=(128 + 8, 128), H=2, T=2) == INVALID      # the next token begins in the second head

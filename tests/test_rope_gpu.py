@@ -146,3 +146,18 @@ def test_graph_and_stream():
     g.replay()
     want = qda.qdecode_rope(q, k, pos, freqs, torch.empty_like(q), torch.empty_like(k))
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_outputs_whose_tokens_and_heads_interleave():
+    """Rows that lie apart without a token's heads, or a head's tokens, lying together."""
+    T, H, D = 4, 3, 64
+    q, _ = data(T, H, 1, D, "bf16", 9)
+    pos, freqs = torch.arange(5, 5 + T, dtype=torch.int32, device="cuda"), qda.qdecode_rope_freqs(D)
+    for ts, hs in ((3 * D, 4 * D), (D, T * D), (H * D, D), (2 * D, 2 * D * T + 3 * D)):
+        buf = torch.full((40 * D,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = buf.as_strided((T, H, D), (ts, hs, 1))
+        qda.qdecode_rope(q.cuda(), None, pos, freqs.cuda(), out)
+        check(out, q, pos.cpu().numpy(), freqs, "bf16")
+        rest = torch.ones(40, dtype=torch.bool)
+        rest[[(t * ts + h * hs) // D for t in range(T) for h in range(H)]] = False
+        assert (buf.view(40, D)[rest.cuda()] == 7).all()
