@@ -290,7 +290,8 @@ extern "C" int qdecode_rope(const void* q, long long q_tstride, long long q_hstr
            rope_touch(ptrs[i], strides[i][0], strides[i][1], heads[i], ptrs[j], strides[j][0], strides[j][1], heads[j], T, D, e);
   };
   for (int i = 0; i < 2; ++i) {   // an output is its input, or apart from it; and apart from the other tensor
-    const bool same = ptrs[i] == ptrs[i + 2] && strides[i][0] == strides[i + 2][0] && strides[i][1] == strides[i + 2][1];
+    const bool same = ptrs[i] == ptrs[i + 2] && (T == 1 || strides[i][0] == strides[i + 2][0]) &&
+                      (heads[i] == 1 || strides[i][1] == strides[i + 2][1]);   // (one token's stride means nothing)
     if (!same && touch(i, i + 2)) return QDA_ERR_INVALID;
   }
   if (touch(2, 1) || touch(3, 0) || touch(2, 3)) return QDA_ERR_INVALID;

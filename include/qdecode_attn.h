@@ -382,10 +382,10 @@ int qdecode_paged_attn_lse(const void* q, long long q_tstride, long long q_hstri
  * outputs. The dimensions from rot on are copied. Rows whose position is negative (qdecode_paged_map's behind the last
  * token) are not written. Angles are right to 2^-24 of a turn at every position; the arithmetic is fp32, rounded once.
  *
- * Rows are contiguous, the other strides (in elements) free; an output is its input (same pointer and strides, done in
- * place) or apart from it, and apart from the other tensor's rows, else QDA_ERR_INVALID. Views of one buffer that holds a
- * token after the other (a fused projection) count row by row. No two rows of an output share an element, else
- * QDA_ERR_INVALID.
+ * Rows are contiguous, the other strides (in elements) free; an output is its input (same pointer and strides, where there
+ * is more than one token or head; done in place) or apart from it, and apart from the other tensor's rows, else
+ * QDA_ERR_INVALID. Views of one buffer that holds a token after the other (a fused projection) count row by row. No two rows
+ * of an output share an element, else QDA_ERR_INVALID.
  * H or Hkv may be 0 (that tensor's pointers are then not used). dtype: bf16, fp16 or fp32, of inputs and outputs. D as for
  * qdecode_attn, rot even and at most D, H + Hkv <= QDA_ROPE_MAX_HEADS, T <= 2^31 - 4096. Data pointers 16-byte aligned,
  * strides multiples of 16 bytes. Asynchronous on stream, no workspace.

@@ -161,3 +161,15 @@ def test_outputs_whose_tokens_and_heads_interleave():
         rest = torch.ones(40, dtype=torch.bool)
         rest[[(t * ts + h * hs) // D for t in range(T) for h in range(H)]] = False
         assert (buf.view(40, D)[rest.cuda()] == 7).all()
+
+
+def test_strides_of_a_single_token_or_head_mean_nothing():
+    """In place: one token whose output has another token stride, one head whose output has another head stride."""
+    for T, H, other in ((1, 8, (8192, 128, 1)), (5, 1, (1024, 4096, 1))):
+        q, _ = data(T, H, 1, 128, "bf16", T)
+        x = torch.zeros(T, 8, 128, dtype=torch.bfloat16, device="cuda")
+        x[:, :H] = q
+        pos, freqs = torch.arange(3, 3 + T, dtype=torch.int32, device="cuda"), qda.qdecode_rope_freqs(128)
+        qda.qdecode_rope(x[:, :H], None, pos, freqs.cuda(), x[:, :H].as_strided((T, H, 128), other))
+        check(x[:, :H], q, pos.cpu().numpy(), freqs, "bf16")
+        assert not x[:, H:].any()
