@@ -184,7 +184,7 @@ extern "C" int qdecode_paged_weights(const void* q, long long q_tstride, long lo
   if (!k_packed || !k_scales || !k_biases || !mass || !token || !q_start || !kv_len || !block_table) return QDA_ERR_INVALID;
   if (total_q < 0 || max_q < 1 || window < 0 || B < 1 || H < 1 || Hkv < 1 || max_pages < 1 || H % Hkv != 0) return QDA_ERR_INVALID;
   if (total_q > 0 && (!q || !lse)) return QDA_ERR_INVALID;
-  if ((dtype != QDA_BF16 && dtype != QDA_FP16) || !std::isfinite(decay)) return QDA_ERR_INVALID;
+  if ((dtype != QDA_BF16 && dtype != QDA_FP16) || !std::isfinite((float)decay)) return QDA_ERR_INVALID;
   int st = check_codec(D, GS, bits);
   if (st == QDA_OK) st = check_pool(num_pages, page);
   if (st != QDA_OK) return st;

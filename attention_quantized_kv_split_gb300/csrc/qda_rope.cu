@@ -269,7 +269,7 @@ extern "C" int qdecode_rope(const void* q, long long q_tstride, long long q_hstr
   using namespace qda;
   if (T < 0 || H < 0 || Hkv < 0 || H + (long long)Hkv < 1 || D < 1 || rot < 0) return QDA_ERR_INVALID;
   if (dtype != QDA_BF16 && dtype != QDA_FP16 && dtype != QDA_FP32) return QDA_ERR_INVALID;
-  if (rot % 2 != 0 || rot < 2 || rot > D || !std::isfinite(scale)) return QDA_ERR_INVALID;
+  if (rot % 2 != 0 || rot < 2 || rot > D || !std::isfinite((float)scale)) return QDA_ERR_INVALID;
   if ((q_start == nullptr) != (shift == nullptr) || (shift != nullptr && B < 1)) return QDA_ERR_INVALID;
   if (T > 0 && ((H > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out)) || !positions || !freqs)) return QDA_ERR_INVALID;
   if (D != 64 && D != 128 && D != 256 && D != 512) return QDA_ERR_UNSUPPORTED;

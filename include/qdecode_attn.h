@@ -379,8 +379,9 @@ int qdecode_paged_attn_lse(const void* q, long long q_tstride, long long q_hstri
  * neither may be NULL; the sum must stay below 2^31): pair i, which is (x[i], x[i + rot / 2]), with interleaved != 0 (x[2i], x[2i + 1]), becomes
  *     scale * (a cos(n f_i) - b sin(n f_i),  b cos(n f_i) + a sin(n f_i)),   f_i = freqs[i] radians per position
  * (freqs [rot / 2], double, device). With inverse != 0 it turns the other way: the gradient of the inputs from that of the
- * outputs. The dimensions from rot on are copied. Rows whose position is negative (qdecode_paged_map's behind the last
- * token) are not written. Angles are right to 2^-24 of a turn at every position; the arithmetic is fp32, rounded once.
+ * outputs. scale is finite in fp32. The dimensions from rot on are copied. Rows whose position is negative
+ * (qdecode_paged_map's behind the last token) are not written. Angles are right to 2^-24 of a turn at every position; the
+ * arithmetic is fp32, rounded once.
  *
  * Rows are contiguous, the other strides (in elements) free; an output is its input (same pointer and strides, where there
  * is more than one token or head; done in place) or apart from it, and apart from the other tensor's rows, else
@@ -411,12 +412,13 @@ int qdecode_rope_freqs(int rot, double base, double factor, double context, doub
  *     mass[j, kvh] = decay * mass[j, kvh] + sum_t sum_h exp(q[t, h, :] . k_hat[j] / sqrt(D) - lse[t, h])
  * over the sequence's last `window` new tokens (0: all of them) that see key j and the query heads h of KV head kvh. Keys of
  * the new tokens themselves start from 0, whatever mass holds there, and their token becomes their position, j + shift[b]
- * (shift may be NULL: 0; the sum must stay below 2^31). Sequences without new tokens, and rows behind kv_len, stay as they are. max_q bounds the new
- * tokens of a sequence and only chooses the kernel. Scores are right to fp32 (queries below 2^-39 of their row's largest
- * and keys' values below 2^-39 of what their key can hold aside); sums are fp32 in a fixed order: the same bits on every
- * run. Scales and biases as for the attention: a key that is not finite spoils its own mass alone. Same types, limits and
- * checks as qdecode_paged_attn; mass 16-byte aligned. Uses the workspace as qdecode_attn does, of
- * qdecode_paged_weights_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
+ * (shift may be NULL: 0; the sum must stay below 2^31). decay is any number that is finite in fp32. Sequences without new
+ * tokens, and rows behind kv_len, stay as they are. max_q bounds the new tokens of a sequence and only chooses the kernel.
+ * Scores are right to fp32 (queries below 2^-39 of their row's largest and keys' values below 2^-39 of what their key can
+ * hold aside); sums are fp32 in a fixed order: the same bits on every run. Scales and biases as for the attention: a key
+ * that is not finite spoils its own mass alone. Same types, limits and checks as qdecode_paged_attn; mass 16-byte aligned.
+ * Uses the workspace as qdecode_attn does, of qdecode_paged_weights_workspace_bytes() bytes; calls that share one must not
+ * overlap on the GPU.
  */
 int qdecode_paged_weights(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                           const void* k_scales, const void* k_biases, const float* lse, float* mass, int32_t* token,

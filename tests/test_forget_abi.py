@@ -319,3 +319,9 @@ def test_rope_rows_of_an_output_that_collide(L, ts, hs):
 def test_rope_rows_that_collide_in_part(L):
     assert rope(L, qo=(128 * 9, 128 * 6 - 8)) == INVALID        # three tokens on, two heads back: 24 elements apart
     assert rope(L, qo=(128 + 8, 128), H=2, T=2) == INVALID      # the next token begins in the second head
+
+
+def test_factors_beyond_fp32(L):
+    """Finite in 64 bits, infinite in the 32 that the kernels hold them in."""
+    for x in (1e39, -1e39, 3.5e38):
+        assert rope(L, scale=x) == weights(L, decay=x) == INVALID
