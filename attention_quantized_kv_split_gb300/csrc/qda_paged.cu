@@ -1034,7 +1034,11 @@ static int paged_attn(const void* q, long long q_tstride, long long q_hstride, c
     hi += std::max(span, 0LL);
   }
   const char *qc = static_cast<const char*>(q), *oc = static_cast<const char*>(out);
-  if (qc + 2 * lo < oc + 2LL * total_q * H * D && oc < qc + 2 * hi) return QDA_ERR_INVALID;
+  const char *qb = qc + 2 * lo, *qe = qc + 2 * hi, *oe = oc + 2LL * total_q * H * D;
+  if (qb < oe && oc < qe) return QDA_ERR_INVALID;
+  // (the rows' sums are written while other rows' queries are still read, and beside outputs)
+  const char *lc = reinterpret_cast<const char*>(lse), *le = lc + 4LL * total_q * H;
+  if (lse != nullptr && ((qb < le && lc < qe) || (oc < le && lc < oe))) return QDA_ERR_INVALID;
   QdaPagedParams p;
   std::memset(&p, 0, sizeof(p));
   int sms;

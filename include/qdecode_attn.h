@@ -354,7 +354,7 @@ int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max_q, int D, 
  * qdecode_paged_attn_lse: qdecode_paged_attn that also leaves lse [total_q, H] (fp32, contiguous), the natural logarithm of
  * sum_n exp(q[t, h, :] . k_hat[n] / sqrt(D)) over the keys that the token sees, with the roundings of the kernel that the
  * call takes; -inf where it sees none. Rows at and behind q_start[B] stay as they are. out is the same, bit for bit. Same
- * workspace, errors and limits; lse must not overlap q or out.
+ * workspace, errors and limits; lse must not overlap q or out (refused).
  */
 int qdecode_paged_attn_lse(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                            const void* k_scales, const void* k_biases, const uint32_t* v_packed, const void* v_scales,

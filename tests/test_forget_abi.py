@@ -325,3 +325,11 @@ def test_factors_beyond_fp32(L):
     """Finite in 64 bits, infinite in the 32 that the kernels hold them in."""
     for x in (1e39, -1e39, 3.5e38):
         assert rope(L, scale=x) == weights(L, decay=x) == INVALID
+
+
+@pytest.mark.parametrize("other", [0, 7])
+def test_attn_lse_over_queries_or_outputs(L, other):
+    """lse [5, 8] of fp32 over q or out [5, 8, 128] of 16 bits: at their starts, their ends and in front."""
+    p = ptrs(12)
+    for off in (0, 160, 5 * 8 * 128 * 2 - 4, -156):
+        assert attn_lse(L, edit(p, 8, p[other] + off)) == INVALID
