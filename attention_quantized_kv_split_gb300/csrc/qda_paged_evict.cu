@@ -531,7 +531,7 @@ extern "C" int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_b
   if (!k_packed || !k_scales || !k_biases || !v_packed || !v_scales || !v_biases || !mass || !token || !kv_len || !new_len ||
       !block_table || !n_freed)
     return QDA_ERR_INVALID;
-  if (B < 1 || Hkv < 1 || max_pages < 1 || max_freed < 0 || (max_freed > 0 && !freed) || new_len == kv_len) return QDA_ERR_INVALID;
+  if (B < 1 || Hkv < 1 || max_pages < 1 || max_freed < 0 || (max_freed > 0 && !freed)) return QDA_ERR_INVALID;
   if (budget < 1 || limit < budget || sinks < 0 || recent < 0 || (long long)sinks + recent > budget) return QDA_ERR_INVALID;
   int st = check_codec(D, GS, bits);
   if (st == QDA_OK) st = check_pool(num_pages, page);
@@ -545,6 +545,12 @@ extern "C" int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_b
   const void* words[6] = {kv_len, new_len, block_table, freed, n_freed, shift};
   for (const void* p : words)
     if (off4(p)) return QDA_ERR_ALIGN;
+  // lengths are read, and new ones and shifts written, a warp of sequences after the other
+  auto apart = [&](const int32_t* x, const int32_t* y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return x == nullptr || y == nullptr || (a < b ? b - a : a - b) >= 4 * (uintptr_t)B;
+  };
+  if (!apart(kv_len, new_len) || !apart(kv_len, shift) || !apart(new_len, shift)) return QDA_ERR_INVALID;
   EvictParams p;
   std::memset(&p, 0, sizeof(p));
   int sms;

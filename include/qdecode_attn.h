@@ -437,13 +437,15 @@ int qdecode_paged_weights_workspace_bytes(int B, int H, int Hkv, int total_q, in
  * rows that go, both in ascending order; the others stay where they are, so a step that cuts one row moves at most one row per head. Order in
  * the cache means nothing to the attention; mass and token move along. Codes, scales and biases move bit for bit.
  *
- * Writes new_len[b] = budget, or kv_len[b] where nothing is cut (new_len must not be kv_len), adds what was cut to shift[b]
- * (may be NULL: then it reads as 0), and takes the pages behind the budget out of block_table (-1) into freed[max_freed],
- * sequences in order; n_freed[0] counts them all, above max_freed some found no place (status bit 8). A length that is
- * negative or beyond the table leaves its sequence as it is and sets bit 8. A page outside the pool sets it too: no row of it
- * is read or written, and behind the budget it leaves the table without being given back or counted. Contents of rows from budget on are unspecified. D, GS, bits, pages and B as for the other paged
- * calls, Hkv <= QDA_EVICT_MAX_HEADS, max_pages * page below 2^31 - 512; mass and token 16-byte aligned. Uses the workspace
- * as qdecode_attn does, of qdecode_paged_evict_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
+ * Writes new_len[b] = budget, or kv_len[b] where nothing is cut (kv_len, new_len and shift must lie apart, else
+ * QDA_ERR_INVALID), adds what was cut to shift[b] (may be NULL: then it reads as 0), and takes the pages behind the
+ * budget out of block_table (-1) into freed[max_freed], sequences in order; n_freed[0] counts them all, above max_freed
+ * some found no place (status bit 8). A length that is negative or beyond the table leaves its sequence as it is and sets
+ * bit 8. A page outside the pool sets it too: no row of it is read or written, and behind the budget it leaves the table
+ * without being given back or counted. Contents of rows from budget on are unspecified. D, GS, bits, pages and B as for
+ * the other paged calls, Hkv <= QDA_EVICT_MAX_HEADS, max_pages * page below 2^31 - 512; mass and token 16-byte aligned.
+ * Uses the workspace as qdecode_attn does, of qdecode_paged_evict_workspace_bytes() bytes; calls that share one must not
+ * overlap on the GPU.
  */
 #define QDA_EVICT_MAX_HEADS 64
 int qdecode_paged_evict(uint32_t* k_packed, void* k_scales, void* k_biases, uint32_t* v_packed, void* v_scales,

@@ -333,3 +333,9 @@ def test_attn_lse_over_queries_or_outputs(L, other):
     p = ptrs(12)
     for off in (0, 160, 5 * 8 * 128 * 2 - 4, -156):
         assert attn_lse(L, edit(p, 8, p[other] + off)) == INVALID
+
+
+def test_evict_lengths_that_overlap(L):
+    p = ptrs(14)
+    assert evict(L, edit(p, 9, p[8] + 4)) == evict(L, edit(p, 9, p[8] - 4)) == INVALID
+    assert evict(L, edit(p, 9, p[13])) == evict(L, edit(p, 13, p[8])) == INVALID
