@@ -377,6 +377,8 @@ def qdecode_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions
     x = q if q is not None else k
     if x is None:
         raise ValueError("qdecode_rope takes q, k or both")
+    if x.dim() != 3:
+        raise ValueError(f"q and k must be [T, heads, D], got {tuple(x.shape)}")
     dev, T, D, dt = x.get_device(), x.shape[0], x.shape[2], x.dtype
     if dt not in _DT_CODE:
         raise ValueError(f"q and k must be bf16, fp16 or fp32, got {dt}")

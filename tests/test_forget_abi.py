@@ -339,3 +339,12 @@ def test_evict_lengths_that_overlap(L):
     p = ptrs(14)
     assert evict(L, edit(p, 9, p[8] + 4)) == evict(L, edit(p, 9, p[8] - 4)) == INVALID
     assert evict(L, edit(p, 9, p[13])) == evict(L, edit(p, 13, p[8])) == INVALID
+
+
+def test_rope_takes_three_dimensions():
+    _, i32, q = tensors()
+    f = torch.ones(32, dtype=torch.float64)
+    for x in (q[0], q[None], q[0, 0], q.reshape(-1)):
+        for kw in (dict(q=x, k=None), dict(q=None, k=x), dict(q=q, k=x), dict(q=q, k=None, q_out=x)):
+            with pytest.raises(ValueError):
+                qda.qdecode_rope(**kw, positions=i32(2), freqs=f)
