@@ -60,7 +60,7 @@ struct alignas(16) EvShared {
 // largest rank is found by 11 bits at a time over histograms that the cluster adds up through distributed shared memory, and
 // once no more than kEvFew ranks are left, by comparing them all. Ranks are all different (a row's number is part of its
 // rank), so what stays is what is not below the edge. Then holes and rows that come are counted in order, a bit a row, and
-// listed: the i-th hole meets the i-th row that comes, whatever the timing. A row's mass and token are read once. Bound by
+// listed: the i-th hole meets the i-th row that comes, whatever the timing. A row's mass and token are read once. Limited by
 // latency: loads two deep, then some ten barriers; reading all of the other CTAs' bins took half of the time (distributed
 // shared memory is slow to read), so that sums of 32 bins come first and then the 32 that matter (32768 rows of eight heads: 43
 // to 31 us, both kernels). It takes 14.6 us for 512 heads of 2049 rows in CTAs of their own, 20 us for eight of 32768 in clusters
@@ -501,7 +501,10 @@ struct EvictPlan {
 static EvictPlan evict_plan(int B, int Hkv, long long rows, int budget, int sms) {
   EvictPlan e;
   const int units = B * Hkv;
-  // CTAs per head: enough to fill the SMs, none with less than 2048 rows
+  // CTAs per head: enough to fill the SMs, none with room for less than 2048 rows. Room is the table's: lengths are not known here,
+  // and a short sequence of a wide table is cut as finely as a long one. Room in shared memory goes by the table too: one row
+  // each from 512 heads of 2049 takes 17.4 us with tables of 33 to 128 pages of 64, 21.5 with 256 and 22.5 with 512 and more, where
+  // CTAs of 82 KB leave an SM two.
   e.cluster = kEvCluster;
   while (e.cluster > 1 && ((long long)units * e.cluster > 4LL * sms || rows < 2048LL * e.cluster)) e.cluster /= 2;
   e.held = (int)std::min<long long>(kEvHeld, ((rows + e.cluster - 1) / e.cluster + 31) & ~31LL);

@@ -123,9 +123,11 @@ __global__ void __launch_bounds__(kPlThreads, 3) qda_paged_weights_lay_kernel(co
 }
 
 // Rows (counted new tokens times query heads of a KV head) up to which the kernel on matrix instructions takes a call, in the
-// instance for 8, 16 or 32 of them. Against the kernel for many, 4 sequences of 8192 keys, 8 KV heads, D 128, 4-bit: 8 rows 13 /
-// 38 us, 16 rows 17 / 38, 32 rows 26 / 38, 64 rows 74 / 38 (D 256, 8-bit: 32 rows 38 / 58, 64 rows 136 / 59; D 64: 32 rows 24 /
-// 32, 64 rows 62 / 32). D 512 has no kernel for many: its two operands do not fit the tensor memory beside an accumulator.
+// instance for 8, 16 or 32 of them. Against the kernel for many (a max_q that is not the true one chooses either), 4 sequences of
+// 8192 keys, 8 KV heads, 32 query heads, D 128, 4-bit, one call after the other: 8 rows 15 / 43 us, 16 rows 18 / 43, 32 rows 25 / 43,
+// 64 rows 68 / 43 (D 256, 8-bit: 32 rows 33 / 63, 64 rows 99 / 64; D 64, 4-bit: 32 rows 24 / 35, 64 rows 59 / 35). D 512 has no
+// kernel for many: both operands of a whole key would fill the tensor memory. (256 dimensions of them at a time would fit; it is
+// not built.) Its time goes with the rows: 4-bit 64 rows 125 us, 128 rows 239, 256 rows 462.
 constexpr int kPwMostRows = 32;
 
 struct WeightsPlan {

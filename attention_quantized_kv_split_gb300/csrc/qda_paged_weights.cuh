@@ -6,9 +6,10 @@
 // from the row sums that the attention call before it has left (lse), so that the keys are read once more and nothing is
 // joined across CTAs: the query rows of a key block all meet in one CTA, in a fixed order, and no atomics are needed.
 //
-// Scores are exact to fp32 as in the split kernel: the codes go into m16n8k16 matrix instructions as fp16 subnormals
+// Keys enter as they are, as in the split kernel: the codes go into m16n8k16 matrix instructions as fp16 subnormals
 // (c 2^-24, one AND for two codes), a query row as fp16 scaled by a power of two to [2^14, 2^15), one accumulator per group,
-// and S = sum_g s_g acc_g + b_g sum_g(q) in fp32. Keys are the instruction's 16 rows and query rows its 8 columns, so a
+// and S = sum_g s_g acc_g + b_g sum_g(q) in fp32. A query's value is off by 2^-39 of its row's largest at most, and by 2^-35 in the
+// odd dimensions of 4-bit keys, where it is held as a sixteenth. Keys are the instruction's 16 rows and query rows its 8 columns, so a
 // lane's scale and bias serve both of its columns and a key's sum stays in a quad of lanes.
 #pragma once
 
@@ -145,7 +146,7 @@ __device__ __forceinline__ void pw_rows(const QdaWeightsParams& p, const PwSeq& 
       }
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // 2^e times the row lies in [2^14, 2^15); what is 2^-39 of its largest and less loses bits (next to nothing)
+      // 2^e times the row lies in [2^14, 2^15): steps of 2^-24 below 2^-14
       const int e = top > 0.f && top < INFINITY ? max(-100, min(14 - ilogbf(top), 100)) : 0;
       const float f = exp2f((float)e);
 #pragma unroll
@@ -192,11 +193,12 @@ __device__ __forceinline__ void pw_rows(const QdaWeightsParams& p, const PwSeq& 
 // ahead, and the query rows of the CTA's (sequence, KV head) stay in shared memory as operands. With more rows than ROWS the
 // CTA's warps take a block of tiles together and the rows pass by, ROWS at a time.
 //
-// Bound by instruction issue (62 % of the slots at 20 warps per SM) ahead of HBM (44 %): one token of 64 sequences of 700 to 8200
-// keys, 4-bit, D 128, takes 51 us, 3.5 TB/s of codes, scales, biases and masses; 133 us with loads straight to registers, 72 with
-// the ring, 55 with two sixteens of keys at a time, so that what a tile costs beside its products is paid half as often. One
-// token over 131072 keys at D 256 takes 27 us (3.2 TB/s; starts and first loads are a third), over 512 keys 10.5 (latency).
-// Sixteen rows over four sequences of 8192 keys take 17 us with NT = 2 and 24 with NT = 4.
+// Neither unit is full: instruction issue 62 % of the slots at 20 warps per SM, HBM 44 %. One token of 64 sequences of 700 to
+// 8200 keys, 4-bit, D 128, takes 51 us, 3.5 TB/s of codes, scales, biases and masses; 133 us with loads straight to registers,
+// 72 with the ring, 55 with two sixteens of keys at a time, so that what a tile costs beside its products is paid half as
+// often. One token over 131072 keys at D 256 takes 27 us (3.2 TB/s; starts and first loads are a third), over 512 keys 10
+// (latency). Sixteen rows over four sequences of 8192 keys (8 KV heads, D 128, 4-bit) take 18.5 us with NT = 2 and 24.6 with NT
+// = 4.
 template <int BITS, int D, int GS, int NT, bool F16>
 __global__ void __launch_bounds__(kPwWarps * 32, PwGeom<BITS, D, GS, NT>::MINB)
     qda_paged_weights_kernel(const __grid_constant__ QdaWeightsParams p) {

@@ -4,9 +4,11 @@
 // by in chunks of 128: S^T = K Q^T with keys in tensor memory's lanes and query rows in its columns, so that a thread owns a
 // key: it reads its scores, takes exp(s - lse) and adds them up, and the sum over the rows needs no exchange at all.
 //
-// Masses are fp32, so scores must be: a key is two fp16 operands, its value to 11 bits and what those leave (22 bits, or 2^-39
-// of the key's largest possible value), each key scaled by its own power of two, and a query row is exact in fp16 scaled by
-// its own (what is 2^-39 of the row's largest and less loses bits). Both products go to the same fp32 accumulator.
+// Masses are fp32, so scores should come near it: a key is two fp16 operands, its value to 11 bits and what those leave (22
+// bits in all, 2^-24 of what a group of 4-bit codes can hold where they are put together, and 2^-39 of the most that the key
+// can), each key scaled by its own power of two. A query row is fp16 under a power of two that it shares with the rows of its
+// part where their largest values lie near (kPvNear: its values are then off by 2^-27 of its own largest at most), else under
+// its own (2^-39). Both products go to the same fp32 accumulator.
 //   key loader           a warp: a block's codes, scales and biases by asynchronous copies of 16 bytes into a ring, codes at
 //                        places that eight threads' rows do not share banks at (bulk copies of sixteen keys each, one after
 //                        the other, took 4200 cycles a block, more than all that follows with up to 128 rows);
@@ -20,12 +22,13 @@
 //                        216 us instead of 206).
 // Every link is an mbarrier; every wait is bounded and sets the device error word, and after one that gave up every role ends.
 //
-// Ragged chunks (8 sequences, 1 to 1023 tokens over 1024 to 9001 keys, 2 heads per KV head, D 256, 8-bit): 204 us with the kernel
-// ahead (18), 0.60 PFLOP/s of products counted once; the tensor pipe is busy 61 % of the time with twice those, and the exponentials
-// run beside it. The last 64 tokens over 32768 keys (256 rows, D 128, 4-bit): 49 us (layout 6), bound by the latency of the warps'
-// instructions (some ten cycles each at five warps per scheduler) and a block's hand-overs, some 4000 cycles that two chunks hide
-// little of. With both operands in shared memory the former took 390 us instead of 343 then: a product reads all of them
-// there. With a loop over the few rows' kernel they take 3025 and 478 us.
+// Ragged chunks (8 sequences, 1 to 1023 tokens over 1024 to 9001 keys, 2 heads per KV head, D 256, 8-bit): 204 us with the
+// kernel ahead (18), 0.60 PFLOP/s of products counted once; the tensor pipe is busy 61 % of the time with twice those: at D 256
+// the operands of one block fill their half of the tensor memory, so that no block is dequantised while the one before is
+// multiplied. The last 64 tokens over 32768 keys (256 rows, D 128, 4-bit): 49 us (layout 6): the latency of the warps'
+// instructions (some ten cycles each at five warps per scheduler), a block's hand-overs, some 4000 cycles that two chunks hide
+// little of, and query rows that come from L2 again for every block. With both operands in shared memory the former took 390 us
+// instead of 343 then: a product reads all of them there. With a loop over the few rows' kernel they take 3025 and 478 us.
 #pragma once
 
 #include "qda_paged_tc.cuh"
@@ -34,8 +37,8 @@
 namespace qda {
 
 constexpr int kPvKeys = 128;
-// Work of a block beside its query rows, in query rows. Ragged chunks at D 256 take 260 us with 64, 237 with 128, 221 with 200,
-// 223 with 300, 225 with 450.
+// Work of a block beside its query rows, in query rows. Ragged chunks at D 256 take 231 us with 64, 211 with 128, 204 with 200 and
+// with 240, 206 with 300, 208 with 450; the window of 64 tokens 49 with any.
 constexpr int kPvCost = 240;
 constexpr int kPvExp = 8, kPvDeq = 8, kPvWarps = kPvExp + kPvDeq + 4;
 constexpr int kPvParts = kPvExp / 4, kPvCols = kPvRows / kPvParts;   // threads of a key, columns of each

@@ -53,14 +53,14 @@ struct alignas(sizeof(T) * V) RopeVec {
 
 // Pair i of a token at position n turns by n f_i: (a, b) -> s (a cos - b sin, b cos + a sin). The angle is kept in turns as a
 // 64-bit fraction, n * round(2^64 frac(f / 2 pi)) mod 2^64: whole turns drop out of the integer product exactly, so that a
-// position of 2^31 costs no more than 2^-24 of a turn and no argument reduction, where a product in fp32 would be off by
-// 0.06 radians at 2^20. A CTA takes a few tokens: their cosines and sines go to shared memory, one thread each, and are used
-// by every head. A thread has one place in a row, V pairs there (two 16-byte loads: the two halves' values, or 2 V values side
-// by side when pairs are interleaved), and walks rows, so that it reads its cosines once a token and divides nowhere; the next
-// two rows are on their way while two are turned, the first ones while the angles are computed (finding a row's place by division
-// took 22.6 us where this takes 16.4). Bound by memory, in small calls by its latency: 2048 tokens of 40 rows of 128 bf16 take
-// 16.4 us where a plain copy of the same 42 MB takes 14.4; 1756 tokens of 24 rows of 512 fp32 30.7 us, 5.6 TB/s; 15934 of 24 rows of
-// 256 fp16 with 64 turned 84 us, 4.6 TB/s (loads awaited, HBM at 53 %); 64 tokens 9.9 us, of which the kernel is 5.1.
+// position of 2^31 costs no more than 2^-24 of a turn and no argument reduction, where a product in fp32 would be off by 0.06
+// radians at 2^20. A CTA takes a few tokens: their cosines and sines go to shared memory, one thread each, and are used by every
+// head. A thread has one place in a row, V pairs there (two 16-byte loads: the two halves' values, or 2 V values side by side
+// when pairs are interleaved), and walks rows, so that it reads its cosines once a token and divides nowhere; the next two rows
+// are on their way while two are turned, the first ones while the angles are computed (a row's place found by division, and loads
+// behind the angles, took 22.6 us when this took 18.4). Limited by the latency of memory: 2048 tokens of 40 rows of 128 bf16 take
+// 16.4 us where a plain copy of the same 42 MB takes 14.4; 1756 tokens of 24 rows of 512 fp32 30.7 us, 5.6 TB/s; 15934 of 24 rows
+// of 256 fp16 with 64 turned 84 us, 4.6 TB/s (loads awaited, HBM at 53 %); 64 tokens 9.6 us, of which the kernel is 5.1.
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads) qda_rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ __align__(16) float2 cs[kRopeAngles];

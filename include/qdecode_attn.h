@@ -351,10 +351,10 @@ int qdecode_paged_attn(const void* q, long long q_tstride, long long q_hstride, 
 int qdecode_paged_attn_workspace_bytes(int B, int H, int Hkv, int max_q, int D, int GS, int bits, size_t* bytes);
 
 /*
- * qdecode_paged_attn_lse: qdecode_paged_attn that also leaves lse [total_q, H] (fp32, contiguous), the natural logarithm of
- * sum_n exp(q[t, h, :] . k_hat[n] / sqrt(D)) over the keys that the token sees, with the roundings of the kernel that the
- * call takes; -inf where it sees none. Rows at and behind q_start[B] stay as they are. out is the same, bit for bit. Same
- * workspace, errors and limits; lse must not overlap q or out (refused).
+ * qdecode_paged_attn_lse: qdecode_paged_attn that also leaves lse [total_q, H] (fp32, contiguous), the natural logarithm
+ * of sum_n exp(q[t, h, :] . k_hat[n] / sqrt(D)) over the keys that the token sees, with the roundings of the kernel that
+ * the call takes (the one for many rows: keys of 11 bits); -inf where it sees none. Rows at and behind q_start[B] stay as
+ * they are. out is the same, bit for bit. Same workspace, errors and limits; lse must not overlap q or out (refused).
  */
 int qdecode_paged_attn_lse(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                            const void* k_scales, const void* k_biases, const uint32_t* v_packed, const void* v_scales,
@@ -376,7 +376,8 @@ int qdecode_paged_attn_lse(const void* q, long long q_tstride, long long q_hstri
 /*
  * qdecode_rope: rotary positions. The first rot of D dimensions of every row of q [T, H, D] and k [T, Hkv, D] are turned by
  * the token's position n = positions[t] (plus shift[b] of the sequence b that holds row t by q_start [B + 1]; both or
- * neither may be NULL; the sum must stay below 2^31): pair i, which is (x[i], x[i + rot / 2]), with interleaved != 0 (x[2i], x[2i + 1]), becomes
+ * neither may be NULL; the sum must stay below 2^31): pair i, which is (x[i], x[i + rot / 2]), with interleaved != 0
+ * (x[2i], x[2i + 1]), becomes
  *     scale * (a cos(n f_i) - b sin(n f_i),  b cos(n f_i) + a sin(n f_i)),   f_i = freqs[i] radians per position
  * (freqs [rot / 2], double, device). With inverse != 0 it turns the other way: the gradient of the inputs from that of the
  * outputs. scale is finite in fp32. The dimensions from rot on are copied. Rows whose position is negative
@@ -414,11 +415,18 @@ int qdecode_rope_freqs(int rot, double base, double factor, double context, doub
  * the new tokens themselves start from 0, whatever mass holds there, and their token becomes their position, j + shift[b]
  * (shift may be NULL: 0; the sum must stay below 2^31). decay is any number that is finite in fp32. Sequences without new
  * tokens, and rows behind kv_len, stay as they are. max_q bounds the new tokens of a sequence and only chooses the kernel.
- * Scores are right to fp32 (queries below 2^-39 of their row's largest and keys' values below 2^-39 of what their key can
- * hold aside); sums are fp32 in a fixed order: the same bits on every run. Scales and biases as for the attention: a key
- * that is not finite spoils its own mass alone. Same types, limits and checks as qdecode_paged_attn; mass 16-byte aligned.
- * Uses the workspace as qdecode_attn does, of qdecode_paged_weights_workspace_bytes() bytes; calls that share one must not
- * overlap on the GPU.
+ * Scales and biases as for the attention: a key that is not finite spoils its own mass alone. Same types, limits and checks
+ * as qdecode_paged_attn; mass 16-byte aligned. Uses the workspace as qdecode_attn does, of
+ * qdecode_paged_weights_workspace_bytes() bytes; calls that share one must not overlap on the GPU.
+ *
+ * Products, exponentials and sums are fp32 in a fixed order: the same bits on every run. What goes into them:
+ *   - calls of up to 32 query rows per KV head (the smaller of max_q and window, times H / Hkv), and all at D = 512: codes,
+ *     scales and biases as they are; a query's values to 2^-35 of their row's largest.
+ *   - larger calls: a key's values to 22 bits: 2^-22 of the value, 2^-24 of the most that its group can hold, |scale| * 2^bits +
+ *     |bias|, and 2^-39 of the most of all of the key's groups; a query's values to 2^-27 of their row's largest.
+ *   - lse as the caller has it. Where the attention call took the kernel for many rows, its keys had 11 bits: lse may be off by
+ *     2^-11 of the largest sum of |q k| / sqrt(D) of its row, and with it all weights of that row by one factor, so that they do
+ *     not add up to 1 to the last bits. Which of a row's keys weighs more does not depend on it.
  */
 int qdecode_paged_weights(const void* q, long long q_tstride, long long q_hstride, const uint32_t* k_packed,
                           const void* k_scales, const void* k_biases, const float* lse, float* mass, int32_t* token,
@@ -434,8 +442,9 @@ int qdecode_paged_weights_workspace_bytes(int B, int H, int Hkv, int total_q, in
  * by itself. What stays: rows whose token is below `sinks` or one of the `recent` newest positions (those from
  * kv_len[b] + shift[b] - recent on), then those of the largest mass; of equal ones the lowest rows. (A mass that is no
  * number ranks below all.) Needs sinks + recent <= budget. Rows that stay and lie at budget or behind move to the places of
- * rows that go, both in ascending order; the others stay where they are, so a step that cuts one row moves at most one row per head. Order in
- * the cache means nothing to the attention; mass and token move along. Codes, scales and biases move bit for bit.
+ * rows that go, both in ascending order; the others stay where they are, so a step that cuts one row moves at most one
+ * row per head. Order in the cache means nothing to the attention; mass and token move along. Codes, scales and biases
+ * move bit for bit.
  *
  * Writes new_len[b] = budget, or kv_len[b] where nothing is cut (kv_len, new_len and shift must lie apart, else
  * QDA_ERR_INVALID), adds what was cut to shift[b] (may be NULL: then it reads as 0), and takes the pages behind the
