@@ -423,7 +423,8 @@ int qdecode_rope_freqs(int rot, double base, double factor, double context, doub
  *   - calls of up to 32 query rows per KV head (the smaller of max_q and window, times H / Hkv), and all at D = 512: codes,
  *     scales and biases as they are; a query's values to 2^-35 of their row's largest.
  *   - larger calls: a key's values to 22 bits: 2^-22 of the value, 2^-24 of the most that its group can hold, |scale| * 2^bits +
- *     |bias|, and 2^-39 of the most of all of the key's groups; a query's values to 2^-27 of their row's largest.
+ *     |bias|, and 2^-39 of the most of all of the key's groups; a query's values to 2^-27 of their row's largest. A score is
+ *     the fp32 sum of D / 8 steps of sixteen products, each of which may cut off 2^-23 of the sum so far.
  *   - lse as the caller has it. Where the attention call took the kernel for many rows, its keys had 11 bits: lse may be off by
  *     2^-11 of the largest sum of |q k| / sqrt(D) of its row, and with it all weights of that row by one factor, so that they do
  *     not add up to 1 to the last bits. Which of a row's keys weighs more does not depend on it.
